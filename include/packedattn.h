@@ -55,9 +55,14 @@ typedef enum {
 #define PA_DEVICE_ERR_SMEM_ALIGN 6   /* dynamic shared memory not 1024-byte aligned (kernel skipped) */
 #define PA_DEVICE_ERR_SEGMENT 7      /* pa_cfg_combine: bad sequence index, image offset or
                                         mismatched positive/negative image spans */
+#define PA_DEVICE_ERR_PAGE 8         /* a page index outside [0, num_pages) in a page table */
 
 /* Largest batch (number of packed sequences) the attention kernels accept. */
 #define PA_MAX_BATCH 1024
+
+/* What a paged K/V cache holds: bf16 rows, or e4m3 rows with an exponent byte each. */
+#define PA_CACHE_BF16 0
+#define PA_CACHE_E4M3 1
 
 /* Query rows per work item of pa_varlen_attn_fwd (two 128-row tensor-core tiles). */
 #define PA_VARLEN_TILE_M 256
@@ -206,6 +211,134 @@ pa_status pa_rope_packed(void *q, void *k, const int32_t *cu_seqlens_q,
                          const int32_t *cu_seqlens_k, const int32_t *pos_offset,
                          int32_t batch, int32_t total_q, int32_t total_k, int32_t H,
                          int32_t D, float base, pa_stream_t stream);
+
+/*
+ * Paged K/V caches
+ * ----------------
+ * A program that answers token by token, or takes a long input in chunks,
+ * keeps K and V between calls.  The cache is a pool of pages that any
+ * sequence may hold, in any order:
+ *
+ *   k_cache, v_cache  [num_pages, page_size, Hkv, D], each page contiguous;
+ *                     page g starts page_stride elements after page g - 1
+ *                     (page_size * Hkv * D, or more where pages of K and V
+ *                     alternate in one buffer)
+ *   page_table        device int32 [batch, table_pages]: position p of
+ *                     sequence b is row p % page_size of page
+ *                     page_table[b, p / page_size].  Entries past a
+ *                     sequence's last position are never read.
+ *   format            PA_CACHE_BF16: bf16 rows; k_exp and v_exp are ignored.
+ *                     PA_CACHE_E4M3: 8-bit rows.  A row (one token and head)
+ *                     x[0..D) is held as e4m3 values y and one exponent e
+ *                     with x ~ y * 2^e: e is the smallest integer with
+ *                     max |x| * 2^-e <= 448, kept within [-100, 7], and
+ *                     y = x * 2^-e rounded to nearest even, saturating at
+ *                     +-448 (so magnitudes above 57344, infinities among
+ *                     them, read back as 57344).  e + 127 is the row's byte in
+ *   k_exp, v_exp      [num_pages, Hkv, page_size], contiguous.  Byte 255: the
+ *                     row held a NaN and reads back as NaN throughout.
+ *
+ * page_size a power of two in [16, 256], D in {64, 128}, Hkv in [1, 4096],
+ * num_pages and table_pages >= 1; page_stride * element size a multiple of 16
+ * bytes; k_cache, v_cache, k_exp, v_exp 16-byte aligned.  A page index
+ * outside [0, num_pages) records PA_DEVICE_ERR_PAGE: its tokens are not
+ * written, and read as zeros.
+ */
+
+/*
+ * pa_kv_cache_write -- packed new rows into a paged cache, quantised as they
+ * are written where the cache holds 8-bit rows.
+ *
+ * Row j of packed sequence b goes to position pos_offset[b] + j (NULL: j),
+ * the position pa_rope_packed rotated it by.  k, v: bf16 [total, Hkv, D] with
+ * k_stride / v_stride elements from one token to the next (>= Hkv * D,
+ * multiples of 8: the rows may be slices of a fused projection's output).
+ * cu_seqlens device int32 [batch + 1]; pos_offset device int32 [batch].
+ * batch in [1, 65535]; total >= cu_seqlens[batch], later rows are ignored
+ * (total = 0 does nothing, and k, v may then be NULL).
+ * Everything of the cache that no row goes to is left as it was.  Two rows of
+ * one call must not share a place: which of them is kept, or a mixture, is
+ * not defined.  k, v must not overlap the cache.  Bad boundaries record
+ * PA_DEVICE_ERR_CU_SEQLENS; a negative offset or a position beyond
+ * table_pages * page_size records PA_DEVICE_ERR_MAX_LEN; such a sequence is
+ * skipped.
+ */
+pa_status pa_kv_cache_write(const void *k, const void *v, void *k_cache, void *v_cache,
+                            uint8_t *k_exp, uint8_t *v_exp, const int32_t *cu_seqlens,
+                            const int32_t *pos_offset, const int32_t *page_table,
+                            int32_t batch, int32_t total, int64_t k_stride, int64_t v_stride,
+                            int32_t num_pages, int32_t page_size, int32_t table_pages,
+                            int64_t page_stride, int32_t Hkv, int32_t D, int32_t format,
+                            pa_stream_t stream);
+
+/*
+ * pa_kv_cache_read -- cached rows back as packed bf16 rows, the inverse
+ * gather: positions [pos_offset[b], pos_offset[b] + L_b) of sequence b, with
+ * L_b = cu_seqlens[b+1] - cu_seqlens[b], become rows [cu_seqlens[b],
+ * cu_seqlens[b+1]) of k and v, bf16 [total, Hkv, D] contiguous.  Rows of 8-bit
+ * caches come back as y * 2^e, which bf16 holds exactly.  Rows of k and v
+ * past cu_seqlens[batch] are left as they were.  The other rules are
+ * pa_kv_cache_write's.
+ */
+pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8_t *k_exp,
+                           const uint8_t *v_exp, void *k, void *v, const int32_t *cu_seqlens,
+                           const int32_t *pos_offset, const int32_t *page_table,
+                           int32_t batch, int32_t total, int32_t num_pages, int32_t page_size,
+                           int32_t table_pages, int64_t page_stride, int32_t Hkv, int32_t D,
+                           int32_t format, pa_stream_t stream);
+
+/*
+ * pa_paged_attn_fwd -- softmax attention of packed new tokens over a paged
+ * K/V cache: a step of single tokens, chunks of long inputs, both in one
+ * batch, or (causal = 0) tokens over cached states of another length.
+ *
+ * Sequence b has L_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] queries and
+ * seq_lens[b] cached keys.  With causal != 0 its queries are the last L_b of
+ * those positions (their own K and V written before the call): query i sees
+ * key j iff j <= seq_lens[b] - L_b + i; with causal = 0 it sees every key.
+ * Query head h reads K/V head h / (Hq / Hkv).
+ *   out[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], k[j,h',:]>) * v[j,h',:]
+ * A query that sees no key gets zeros.  8-bit rows enter the products as the
+ * bf16 values that pa_kv_cache_read returns.  Scores, maxima, sums and the
+ * output's accumulation are fp32; softmax weights are rounded to bf16 for
+ * the product with V, and the output once to bf16.
+ *
+ * q [total_q, Hq, D] bf16, q_stride elements from one token to the next
+ * (>= Hq * D, a multiple of 8); out [total_q, Hq, D] bf16 contiguous, written
+ * at the rows that belong to a sequence only, and not overlapping q or the
+ * cache.  cu_seqlens_q device int32 [batch + 1], seq_lens device int32
+ * [batch], batch in [1, PA_MAX_BATCH]; total_q >= cu_seqlens_q[batch]
+ * (total_q = 0 does nothing, and q, out may then be NULL); max_q / max_k bound every L_b and
+ * seq_lens[b]; Hq a multiple of Hkv, Hq / Hkv <= 128; scale finite.
+ * Rows of a page past a sequence's last position never reach a result,
+ * whatever their bits.
+ *
+ * workspace: device memory of at least pa_paged_attn_workspace_bytes() bytes,
+ * 16-byte aligned, for the partial results of keys that are split over
+ * several CTAs (NULL where that is 0).  Its contents need not be kept or
+ * cleared; two calls that may run at the same time need one each.
+ *
+ * A sequence with bad boundaries (PA_DEVICE_ERR_CU_SEQLENS), a negative
+ * seq_lens (PA_DEVICE_ERR_LENGTH), or a length beyond max_q, max_k or
+ * table_pages * page_size (PA_DEVICE_ERR_MAX_LEN) is skipped, its rows left
+ * untouched.  Deterministic, and independent of the batch around a sequence:
+ * how its keys are split depends on its own lengths alone.
+ */
+pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
+                            const uint8_t *k_exp, const uint8_t *v_exp, void *out,
+                            const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                            const int32_t *page_table, int32_t batch, int32_t total_q,
+                            int32_t max_q, int32_t max_k, int64_t q_stride,
+                            int32_t num_pages, int32_t page_size, int32_t table_pages,
+                            int64_t page_stride, int32_t Hq, int32_t Hkv, int32_t D,
+                            int32_t format, int32_t causal, float scale, void *workspace,
+                            int64_t workspace_bytes, pa_stream_t stream);
+
+/* Workspace of a pa_paged_attn_fwd call with these arguments, in bytes (host
+ * arithmetic alone: it grows with each argument, so one of the largest serves
+ * smaller calls); -1 where that call would be refused. */
+int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q, int32_t max_q,
+                                      int32_t max_k, int32_t Hq, int32_t Hkv, int32_t D);
 
 /*
  * pa_linear_bf16 -- batch-invariant packed-M linear layer.

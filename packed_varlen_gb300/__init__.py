@@ -25,7 +25,7 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED",
 DEVICE_ERRORS = {0: "PA_DEVICE_OK", 1: "PA_DEVICE_ERR_CU_SEQLENS", 2: "PA_DEVICE_ERR_MAX_LEN",
                  3: "PA_DEVICE_ERR_TIMEOUT", 4: "PA_DEVICE_ERR_LENGTH",
                  5: "PA_DEVICE_ERR_CAPACITY", 6: "PA_DEVICE_ERR_SMEM_ALIGN",
-                 7: "PA_DEVICE_ERR_SEGMENT"}
+                 7: "PA_DEVICE_ERR_SEGMENT", 8: "PA_DEVICE_ERR_PAGE"}
 MAX_BATCH = 1024
 VARLEN_TILE_M = 256
 
@@ -61,6 +61,13 @@ _SIGNATURES = {
     "pa_cfg_combine": ([_c_ptr] * 8 + [_c_i32] * 5 + [_c_ptr], _c_i32),
     "pa_rope_packed": ([_c_ptr] * 5 + [_c_i32] * 5 + [_c_f32, _c_ptr], _c_i32),
     "pa_linear_bf16": ([_c_ptr] * 4 + [_c_i32] * 3 + [_c_ptr], _c_i32),
+    "pa_kv_cache_write": ([_c_ptr] * 9 + [_c_i32] * 2 + [_c_i64] * 2 + [_c_i32] * 3 + [_c_i64] +
+                          [_c_i32] * 3 + [_c_ptr], _c_i32),
+    "pa_kv_cache_read": ([_c_ptr] * 9 + [_c_i32] * 5 + [_c_i64] + [_c_i32] * 3 + [_c_ptr],
+                         _c_i32),
+    "pa_paged_attn_fwd": ([_c_ptr] * 9 + [_c_i32] * 4 + [_c_i64] + [_c_i32] * 3 + [_c_i64] +
+                          [_c_i32] * 5 + [_c_f32, _c_ptr, _c_i64, _c_ptr], _c_i32),
+    "pa_paged_attn_workspace_bytes": ([_c_i32] * 7, _c_i64),
 }
 
 
@@ -386,4 +393,235 @@ def linear_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] =
                             bias.data_ptr() if bias is not None else None, out.data_ptr(),
                             M, N, K, _stream(stream))
     _check("pa_linear_bf16", st)
+    return out
+
+
+# ---------------------------------------------------------------- paged K/V cache
+_CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+def _need_rows(t: torch.Tensor, name: str, dev) -> int:
+    """A packed [T, H, D] bf16 tensor whose rows (one token) are contiguous;
+    returns the elements from one token to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the cache's device {dev}, not {t.device}")
+    T, H, D = t.shape
+    sT, sH, sD = t.stride()
+    if (D > 1 and sD != 1) or (H > 1 and sH != D):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return sT if T > 1 else H * D
+
+
+def _need_index(t: torch.Tensor, name: str, shape, dev):
+    _need(t, name, torch.int32, len(shape))
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the cache's device {dev}, not {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _need_cache(k_cache, v_cache, k_exp, v_exp, page_table, batch):
+    """Checks the cache's tensors against each other; returns (device, format,
+    num_pages, page_size, Hkv, D, page_stride, k_exp address, v_exp address)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if t.dtype not in _CACHE_FORMATS:
+            raise TypeError(f"{n} must be torch.bfloat16 or torch.float8_e4m3fn, got {t.dtype}")
+        if t.dim() != 4:
+            raise ValueError(f"{n} must be [num_pages, page_size, Hkv, D]")
+    dev = k_cache.device
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != dev:
+        raise ValueError("k_cache and v_cache must have the same shape, type and device")
+    P, page, H, D = k_cache.shape
+    strides = []
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        s = t.stride()
+        if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (page > 1 and s[1] != H * D):
+            raise ValueError(f"each page of {n} must be contiguous")
+        strides.append(s[0] if P > 1 else page * H * D)
+    if strides[0] != strides[1]:
+        raise ValueError("k_cache and v_cache must have the same page stride")
+    fmt = _CACHE_FORMATS[k_cache.dtype]
+    ke = ve = None
+    if fmt == 1:
+        if k_exp is None or v_exp is None:
+            raise ValueError("an 8-bit cache needs k_exp and v_exp")
+        for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            _need(t, n, torch.uint8, 3)
+            if tuple(t.shape) != (P, H, page) or t.device != dev:
+                raise ValueError(f"{n} must be [num_pages, Hkv, page_size] on the cache's device")
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("a bf16 cache has no k_exp and v_exp")
+    _need(page_table, "page_table", torch.int32, 2)
+    if page_table.device != dev or page_table.shape[0] != batch:
+        raise ValueError("page_table must be [batch, table_pages] on the cache's device")
+    return dev, fmt, P, page, H, D, strides[0], ke, ve
+
+
+class _On:
+    """Device and stream of a call on tensors of device `dev`: the call itself
+    runs with that device current, and what it allocates belongs to the stream
+    that uses it, so that the memory is not handed on while it is in use."""
+    __slots__ = ("dev", "raw", "given", "guard")
+
+    def __init__(self, dev, stream):
+        self.dev, self.given, self.guard = dev, stream is not None, None
+        if stream is None:
+            self.raw = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+            self.guard = None
+
+    def new(self, make, shape, dtype):
+        if not self.given:
+            return make(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.raw, device=self.dev)):
+            return make(shape, dtype=dtype, device=self.dev)
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, cu_seqlens: torch.Tensor, page_table: torch.Tensor,
+                   pos_offset: Optional[torch.Tensor] = None,
+                   k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Packed new rows k, v [T, Hkv, D] bf16 into a paged cache (pa_kv_cache_write):
+    row j of sequence b goes to position pos_offset[b] + j.  k_cache, v_cache
+    [num_pages, page_size, Hkv, D] bf16, or float8_e4m3fn with exponent bytes
+    k_exp, v_exp [num_pages, Hkv, page_size] uint8; k and v may be slices of a
+    wider tensor along its last dimensions.  Returns (k_cache, v_cache)."""
+    lib = load_library()
+    B = cu_seqlens.numel() - 1
+    dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
+                                                      page_table, B)
+    ks, vs = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
+    if k.shape != v.shape or tuple(k.shape[1:]) != (H, D):
+        raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
+    _need_index(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    if pos_offset is not None:
+        _need_index(pos_offset, "pos_offset", (B,), dev)
+    with _On(dev, stream) as raw:
+        st = lib.pa_kv_cache_write(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+                                   v_cache.data_ptr(), ke, ve, cu_seqlens.data_ptr(),
+                                   None if pos_offset is None else pos_offset.data_ptr(),
+                                   page_table.data_ptr(), B, k.shape[0], ks, vs, P, page,
+                                   page_table.shape[1], ps, H, D, fmt, raw)
+    _check("pa_kv_cache_write", st)
+    return k_cache, v_cache
+
+
+def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torch.Tensor,
+                  page_table: torch.Tensor, total: int,
+                  pos_offset: Optional[torch.Tensor] = None,
+                  k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
+                  k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Cached rows as packed bf16 rows (pa_kv_cache_read): positions
+    [pos_offset[b], pos_offset[b] + L_b) of each sequence, L_b from cu_seqlens, as
+    rows cu_seqlens[b].. of k_out and v_out [total, Hkv, D].  Rows past
+    cu_seqlens[B] are left as they are (fresh outputs are zero-filled).
+    Returns (k_out, v_out)."""
+    lib = load_library()
+    B = cu_seqlens.numel() - 1
+    dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
+                                                      page_table, B)
+    _need_index(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    if pos_offset is not None:
+        _need_index(pos_offset, "pos_offset", (B,), dev)
+    on = _On(dev, stream)
+    with on as raw:
+        if k_out is None:
+            k_out = on.new(torch.zeros, (int(total), H, D), torch.bfloat16)
+        if v_out is None:
+            v_out = on.new(torch.zeros, (int(total), H, D), torch.bfloat16)
+        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+            _need(t, n, torch.bfloat16, 3)
+            if tuple(t.shape) != (total, H, D) or t.device != dev:
+                raise ValueError(f"{n} must be [total, Hkv, D] on the cache's device")
+        st = lib.pa_kv_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
+                                  k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(),
+                                  None if pos_offset is None else pos_offset.data_ptr(),
+                                  page_table.data_ptr(), B, int(total), P, page,
+                                  page_table.shape[1], ps, H, D, fmt, raw)
+    _check("pa_kv_cache_read", st)
+    return k_out, v_out
+
+
+def paged_attn_workspace_bytes(batch: int, total_q: int, max_q: int, max_k: int, Hq: int,
+                               Hkv: int, D: int) -> int:
+    """Workspace of paged_attn_fwd, in bytes (pa_paged_attn_workspace_bytes)."""
+    n = load_library().pa_paged_attn_workspace_bytes(int(batch), int(total_q), int(max_q),
+                                                     int(max_k), int(Hq), int(Hkv), int(D))
+    if n < 0:
+        raise PackedAttnError("pa_paged_attn_workspace_bytes", 1)
+    return int(n)
+
+
+def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor,
+                   page_table: torch.Tensor, max_q: int, max_k: int,
+                   k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
+                   causal: bool = True, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of packed new tokens q [Tq, Hq, D] bf16 over a paged cache
+    (pa_paged_attn_fwd).  seq_lens int32 [B]: keys of each sequence, its new
+    tokens' own among them (causal) or not (causal=False).  q may be a slice of
+    a wider tensor along its last dimensions.  Rows of ``out`` beyond
+    cu_seqlens_q[B] are not written (a fresh ``out`` is zero-filled).
+    ``workspace`` (uint8, paged_attn_workspace_bytes) is allocated per call
+    unless given; calls that may overlap need one each."""
+    lib = load_library()
+    B = cu_seqlens_q.numel() - 1
+    dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
+                                                      page_table, B)
+    qs = _need_rows(q, "q", dev)
+    Tq, Hq = q.shape[0], q.shape[1]
+    if q.shape[2] != D or Hq < 1 or Hq % H:
+        raise ValueError("q must be [Tq, Hq, D] with the cache's D and Hq a multiple of its Hkv")
+    _need_index(cu_seqlens_q, "cu_seqlens_q", (B + 1,), dev)
+    _need_index(seq_lens, "seq_lens", (B,), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    need = lib.pa_paged_attn_workspace_bytes(B, Tq, int(max_q), int(max_k), Hq, H, D)
+    on = _On(dev, stream)
+    with on as raw:
+        if out is None:
+            out = on.new(torch.zeros, (Tq, Hq, D), torch.bfloat16)
+        if workspace is None and need > 0:
+            workspace = on.new(torch.empty, (need,), torch.uint8)
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape != q.shape or out.device != dev:
+            raise ValueError("out must have q's shape, on its device")
+        wp, wn = None, 0
+        if workspace is not None:
+            _need(workspace, "workspace", torch.uint8, 1)
+            if workspace.device != dev:
+                raise ValueError("workspace must be on the cache's device")
+            wp, wn = workspace.data_ptr(), workspace.numel()
+        st = lib.pa_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
+                                   out.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+                                   page_table.data_ptr(), B, Tq, int(max_q), int(max_k), qs, P,
+                                   page, page_table.shape[1], ps, Hq, H, D, fmt, int(bool(causal)),
+                                   float(scale), wp, wn, raw)
+    _check("pa_paged_attn_fwd", st)
     return out

@@ -29,6 +29,24 @@ struct BlockWindowArgs {
   int num_sms;
 };
 
+// A paged K/V cache as the C ABI receives it.
+struct PagedCacheArgs {
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+  const int32_t *table;
+  int32_t num_pages, page_size, table_pages;
+  int64_t page_stride;
+  int32_t Hkv, D, format;
+};
+struct PagedCache;   // paged.cuh
+
+// The checks every entry point over a paged cache makes; fills `c` on PA_OK.
+pa_status check_cache(const PagedCacheArgs &a, PagedCache &c);
+
+inline bool aligned_to(const void *p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
 // Raises a kernel's dynamic shared-memory limit once per device (the
 // attribute persists; setting it on every launch costs host time between
 // back-to-back launches).  `done` is the caller's per-kernel device bitmask.

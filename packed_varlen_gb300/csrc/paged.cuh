@@ -1,0 +1,107 @@
+// Paged K/V cache: what its kernels share -- the cache's layout, the checks
+// of one sequence's lengths against it, and the 8-bit rows' arithmetic.
+//
+// Pages are token-major like every other tensor: row (page g, row r, head h)
+// of D elements starts at g * page_stride + (r * Hkv + h) * D.  Position p of
+// sequence b is row p % page_size of page table[b, p / page_size].
+//
+// 8-bit rows.  A row x[0..D) of one token and head is stored as e4m3 values
+// y_i and one exponent e, x_i ~ y_i * 2^e, with 2^e the smallest power of two
+// that brings max |x_i| to 448 (e4m3's largest value) or less.  A power of two
+// leaves a floating format's relative step as it is, so against a scale of
+// max / 448 it gives up nothing but the lowest of e4m3's 18 binades; in
+// return x * 2^-e and y * 2^e are exact, the one rounding is that to e4m3,
+// and a stored value (4 significant bits) is exact in bf16: attention over
+// an 8-bit cache is attention over the bf16 rows that reading it back gives.
+// e is kept as a byte e + 127 in [num_pages, Hkv, page_size], so a head's
+// exponents of one page are one run of page_size bytes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "packedattn.h"
+#include "sched.cuh"
+
+namespace pa {
+
+constexpr int kExpMin = -100;   // rows below 448 * 2^-100 lose low bits, then values
+constexpr int kExpMax = 7;      // magnitudes above 448 * 2^7 = 57344 saturate
+constexpr int kExpBias = 127;
+constexpr int kExpNan = 255;    // a row that held a NaN: all of it reads as NaN
+
+// Everything that locates a cached row.
+struct PagedCache {
+  void *k, *v;             // pages, bf16 or e4m3
+  uint8_t *k_exp, *v_exp;  // exponent bytes (8-bit caches)
+  const int32_t *table;    // [batch, table_pages]
+  int64_t page_stride;     // elements from one page to the next
+  int32_t num_pages, page_shift, table_pages, Hkv, D;
+};
+
+__device__ __forceinline__ bool page_ok(const PagedCache &c, int32_t page) {
+  return static_cast<uint32_t>(page) < static_cast<uint32_t>(c.num_pages);
+}
+
+// Element offset of row (page, row in page, head) and of its exponent byte.
+__device__ __forceinline__ int64_t row_offset(const PagedCache &c, int32_t page, int row,
+                                              int head) {
+  return page * c.page_stride + static_cast<int64_t>(row * c.Hkv + head) * c.D;
+}
+__device__ __forceinline__ int64_t exp_offset(const PagedCache &c, int32_t page, int row,
+                                              int head) {
+  return ((static_cast<int64_t>(page) * c.Hkv + head) << c.page_shift) + row;
+}
+
+// 2^e as fp32, e in [-126, 127].
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// Exponent of a row whose largest magnitude is `a` (no NaN).
+__device__ __forceinline__ int row_exponent(float a) {
+  const int bits = __float_as_int(a);   // a = (1 + m) 2^n, n from the exponent field
+  const int n = (bits >> 23) - 127;
+  const int e = n - 8 + ((bits & 0x7fffff) > 0x600000);   // a 2^-e in (224, 448]
+  return min(max(e, kExpMin), kExpMax);
+}
+
+// Scale of a stored row: 2^e, or NaN for a row that held one.
+__device__ __forceinline__ float row_scale(int byte) {
+  return byte == kExpNan ? __int_as_float(0x7fffffff) : pow2f(byte - kExpBias);
+}
+
+// Four fp32 values -> four e4m3 bytes, rounded to nearest even, saturating.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Sequence b of a paged attention call: query rows [q0, q0 + lq), lk keys.
+// Read like seq_bounds: a sequence that breaks the rules is returned without
+// queries and `err` says why.
+struct PagedSeq {
+  int32_t q0, lq, lk;
+};
+__device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
+                                              const int32_t *__restrict__ seq_lens, int b,
+                                              int total_q, int max_q, int max_k,
+                                              int64_t capacity, int &err) {
+  const int q0 = __ldg(cu_q + b), q1 = __ldg(cu_q + b + 1), lk = __ldg(seq_lens + b);
+  PagedSeq s{0, 0, 0};
+  err = 0;
+  if (!(q0 >= 0 && q0 <= q1 && q1 <= total_q && (b > 0 || q0 == 0))) {
+    err = PA_DEVICE_ERR_CU_SEQLENS;
+  } else if (lk < 0) {
+    err = PA_DEVICE_ERR_LENGTH;
+  } else if (q1 - q0 > max_q || lk > max_k || lk > capacity) {
+    err = PA_DEVICE_ERR_MAX_LEN;
+  } else {
+    s.q0 = q0;
+    s.lq = q1 - q0;
+    s.lk = lk;
+  }
+  return s;
+}
+
+}  // namespace pa

@@ -1,0 +1,175 @@
+// Attention of packed new tokens over a paged K/V cache: the entry point.
+//
+// Simplest form: one warp per (token, query head), an online softmax over the
+// keys one at a time.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct PagedAttnParams {
+  PagedCache c;
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  const int32_t *cu_q, *seq_lens;
+  int64_t q_stride;
+  int total_q, max_q, max_k, Hq;
+  int causal;
+  float scale_log2;
+  int32_t *status;
+};
+
+template <bool kQuant, int D>
+__global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const PagedAttnParams p) {
+  constexpr int E = D / 32;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  int err;
+  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
+  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
+  if (err) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.status, err);
+    return;
+  }
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int i = static_cast<int>(item / p.Hq), h = static_cast<int>(item - static_cast<int64_t>(i) * p.Hq);
+  if (i >= s.lq) return;
+  const int hk = h / (p.Hq / p.c.Hkv);
+  const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.table_pages;
+  float q[E], o[E];
+  const __nv_bfloat16 *qr = p.q + (s.q0 + i) * p.q_stride + static_cast<int64_t>(h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    q[e] = __bfloat162float(qr[e]);
+    o[e] = 0.f;
+  }
+  const int n = p.causal ? min(s.lk, s.lk - s.lq + i + 1) : s.lk;
+  float m = -INFINITY, l = 0.f;
+  for (int j = 0; j < n; ++j) {
+    const int32_t page = __ldg(table + (j >> p.c.page_shift));
+    const int row = j & ((1 << p.c.page_shift) - 1);
+    const bool good = page_ok(p.c, page);
+    if (!good) record_error(p.status, PA_DEVICE_ERR_PAGE);
+    const int64_t at = row_offset(p.c, good ? page : 0, row, hk) + lane * E;
+    float k[E], v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
+    if (good) {
+      if constexpr (kQuant) {
+        const int64_t xo = exp_offset(p.c, page, row, hk);
+        const float ks = row_scale(p.c.k_exp[xo]), vs = row_scale(p.c.v_exp[xo]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          __half_raw kr = __nv_cvt_fp8_to_halfraw(static_cast<uint8_t *>(p.c.k)[at + e], __NV_E4M3);
+          __half_raw vr = __nv_cvt_fp8_to_halfraw(static_cast<uint8_t *>(p.c.v)[at + e], __NV_E4M3);
+          k[e] = __half2float(__half(kr)) * ks;
+          v[e] = __half2float(__half(vr)) * vs;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          k[e] = __bfloat162float(static_cast<__nv_bfloat16 *>(p.c.k)[at + e]);
+          v[e] = __bfloat162float(static_cast<__nv_bfloat16 *>(p.c.v)[at + e]);
+        }
+      }
+    }
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x += q[e] * k[e];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    x *= p.scale_log2;
+    const float mn = fmaxf(m, x);
+    const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
+    const float w = mn == -INFINITY ? 0.f : exp2f(x - mn);
+    m = mn;
+    l = l * a + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * v[e];
+  }
+  __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(s.q0 + i) * p.Hq + h) * D + lane * E;
+  const float inv = n > 0 ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(n > 0 ? o[e] * inv : 0.f);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q, int32_t max_q,
+                                                 int32_t max_k, int32_t Hq, int32_t Hkv,
+                                                 int32_t D) {
+  if (batch < 1 || batch > PA_MAX_BATCH || total_q < 0 || max_q < 0 || max_k < 0 || Hkv < 1 ||
+      Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128))
+    return -1;
+  return 0;
+}
+
+extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
+                                       const uint8_t *k_exp, const uint8_t *v_exp, void *out,
+                                       const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                                       const int32_t *page_table, int32_t batch,
+                                       int32_t total_q, int32_t max_q, int32_t max_k,
+                                       int64_t q_stride, int32_t num_pages, int32_t page_size,
+                                       int32_t table_pages, int64_t page_stride, int32_t Hq,
+                                       int32_t Hkv, int32_t D, int32_t format, int32_t causal,
+                                       float scale, void *workspace, int64_t workspace_bytes,
+                                       pa_stream_t stream) {
+  if (!cu_seqlens_q || !seq_lens) return PA_ERR_INVALID_ARG;
+  if (batch < 1 || total_q < 0 || max_q < 0 || max_k < 0 || Hq < 1) return PA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!q || !out)) return PA_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return PA_ERR_INVALID_ARG;
+  PagedAttnParams p;
+  const PagedCacheArgs a{const_cast<void *>(k_cache), const_cast<void *>(v_cache),
+                         const_cast<uint8_t *>(k_exp), const_cast<uint8_t *>(v_exp),
+                         page_table, num_pages, page_size, table_pages, page_stride, Hkv, D,
+                         format};
+  const pa_status st = check_cache(a, p.c);
+  if (st != PA_OK) return st;
+  if (Hq % Hkv != 0 || q_stride < static_cast<int64_t>(Hq) * D) return PA_ERR_INVALID_ARG;
+  if (batch > PA_MAX_BATCH || Hq / Hkv > 128 || q_stride > (int64_t{1} << 38))
+    return PA_ERR_UNSUPPORTED;
+  if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(cu_seqlens_q, 4) ||
+      !aligned_to(seq_lens, 4) || (q_stride & 7) != 0 || !aligned_to(workspace, 16))
+    return PA_ERR_MISALIGNED;
+  const int64_t need =
+      pa_paged_attn_workspace_bytes(batch, total_q, max_q, max_k, Hq, Hkv, D);
+  if (need < 0 || workspace_bytes < need || (need > 0 && !workspace)) return PA_ERR_INVALID_ARG;
+  if (total_q == 0 || max_q == 0) return PA_OK;
+  int sms;
+  cudaError_t e = device_context(&p.status, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.cu_q = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.q_stride = q_stride;
+  p.total_q = total_q;
+  p.max_q = max_q;
+  p.max_k = max_k;
+  p.Hq = Hq;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_q) * Hq + 7) / 8), batch);
+  auto s = reinterpret_cast<cudaStream_t>(stream);
+  if (format == PA_CACHE_E4M3) {
+    if (D == 128)
+      paged_attn_simple_kernel<true, 128><<<grid, kThreads, 0, s>>>(p);
+    else
+      paged_attn_simple_kernel<true, 64><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (D == 128)
+      paged_attn_simple_kernel<false, 128><<<grid, kThreads, 0, s>>>(p);
+    else
+      paged_attn_simple_kernel<false, 64><<<grid, kThreads, 0, s>>>(p);
+  }
+  return from_cuda(cudaGetLastError());
+}

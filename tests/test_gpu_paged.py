@@ -1,0 +1,676 @@
+"""The paged K/V cache operators on the GPU against the fp64 oracle."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ["bf16", "e4m3"]
+
+
+@pytest.fixture(scope="module")
+def pv():
+    import packed_varlen_gb300 as pv
+    pv.load_library()
+    pv.get_device_status()
+    return pv
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _cu(lengths):
+    return _i32(np.concatenate([[0], np.cumsum(lengths)]).tolist())
+
+
+class Cache:
+    """A pool of pages full of other sequences' old rows, and pages of it handed out at random."""
+
+    def __init__(self, held, page, H, D, fmt, seed=0, width=None, spare=3, interleaved=False,
+                 old=7.0):
+        rng = np.random.default_rng(seed)
+        counts = [-(-n // page) for n in held]
+        P = sum(counts) + spare
+        self.page, self.H, self.D, self.fmt, self.P = page, H, D, fmt, P
+        perm = rng.permutation(P)
+        self.table = np.full((len(held), width or max(counts + [1])), -1, dtype=np.int64)
+        n = 0
+        for b, c in enumerate(counts):
+            self.table[b, :c] = perm[n:n + c]
+            n += c
+        dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+        shape = (P, 2, page, H, D) if interleaved else (2, P, page, H, D)
+        kv = torch.full(shape, old, device="cuda").to(dt)
+        self.k, self.v = (kv[:, 0], kv[:, 1]) if interleaved else (kv[0], kv[1])
+        self.ke = self.ve = None
+        if fmt == "e4m3":
+            byte = 127 if math.isfinite(old) else 255
+            self.ke, self.ve = torch.full((2, P, H, page), byte, dtype=torch.uint8, device="cuda")
+        self.dev_table = _i32(self.table.tolist())
+
+    def exps(self):
+        return dict(k_exp=self.ke, v_exp=self.ve)
+
+    def values(self):
+        """What the cache holds, in float64 [P, page, H, D]."""
+        out = []
+        for x, e in ((self.k, self.ke), (self.v, self.ve)):
+            y = x.float().double().cpu().numpy()
+            if e is not None:
+                y = oracle.dequantise_rows(y, e.cpu().numpy().transpose(0, 2, 1))
+            out.append(y)
+        return out
+
+
+def _rows(T, H, D, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, D, generator=g) * torch.exp(spread * torch.randn(T, H, 1, generator=g))
+    return x.to(torch.bfloat16)
+
+
+def _fill(pv, c, lengths, seed, offsets=None, spread=0.3):
+    """Writes the first rows of every sequence through the library."""
+    T = sum(lengths)
+    k, v = _rows(T, c.H, c.D, seed, spread), _rows(T, c.H, c.D, seed + 1, spread)
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu(lengths), c.dev_table,
+                      pos_offset=None if offsets is None else _i32(offsets), **c.exps())
+    return k, v
+
+
+# ------------------------------------------------------------------ write and read
+
+WRITES = [
+    # lengths, offsets, page, H, D
+    ([1], None, 16, 1, 64),
+    ([1, 1, 1, 1, 1], [0, 15, 16, 31, 100], 16, 8, 128),
+    ([37, 0, 64, 1], [5, 3, 0, 77], 16, 2, 64),
+    ([300, 17, 129], [0, 250, 31], 32, 3, 128),
+    ([1000, 3], [1, 0], 64, 5, 128),
+    ([2, 513], [255, 256], 256, 20, 64),
+    ([700], [12], 128, 12, 128),
+]
+
+
+def _write_case(pv, lengths, offsets, page, H, D, fmt, interleaved, strided):
+    held = [n + (offsets[b] if offsets else 0) for b, n in enumerate(lengths)]
+    c = Cache(held, page, H, D, fmt, seed=page + H, interleaved=interleaved,
+              width=max(-(-n // page) for n in held) + 2)
+    T, extra = sum(lengths), 3
+    k, v = _rows(T + extra, H, D, 1), _rows(T + extra, H, D, 2)
+    if strided:
+        fused = torch.full((T + extra, 3 * H * D), 9.0, dtype=torch.bfloat16, device="cuda")
+        fused[:, H * D:2 * H * D] = k.view(-1, H * D).cuda()
+        fused[:, 2 * H * D:] = v.view(-1, H * D).cuda()
+        dk, dv = fused[:, H * D:2 * H * D].view(-1, H, D), fused[:, 2 * H * D:].view(-1, H, D)
+    else:
+        dk, dv = k.cuda(), v.cuda()
+    before = [x.view(torch.uint8).clone().cpu() for x in (c.k, c.v)]
+    exps_before = [e.clone().cpu() for e in (c.ke, c.ve)] if fmt == "e4m3" else None
+    off = None if offsets is None else _i32(offsets)
+    got = pv.kv_cache_write(dk, dv, c.k, c.v, _cu(lengths), c.dev_table, pos_offset=off,
+                            **c.exps())
+    assert got[0] is c.k and got[1] is c.v
+    assert pv.get_device_status() == 0
+    at = oracle.places(lengths, offsets, c.table, page)
+    for i, (x, cache, exp) in enumerate(((k, c.k, c.ke), (v, c.v, c.ve))):
+        raw = cache.view(torch.uint8).cpu()
+        want = before[i].clone()
+        if fmt == "bf16":
+            bits = x.view(torch.uint8)
+        else:
+            y, byte = oracle.quantise_rows(oracle.to_f64(x))
+            bits = torch.tensor(y, dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8)
+            want_exp = exps_before[i].clone()
+        for t, (g, r) in enumerate(at):
+            want[g, r] = bits[t].view(H, -1)
+            if fmt == "e4m3":
+                want_exp[g, :, r] = torch.tensor(byte[t])
+        # -0 and 0 are one value: compare 8-bit payloads as values, everything else as bits
+        if fmt == "bf16":
+            assert torch.equal(raw, want)
+        else:
+            assert torch.equal(raw.view(torch.float8_e4m3fn).float(),
+                               want.view(torch.float8_e4m3fn).float())
+            assert torch.equal(exp.cpu(), want_exp)
+    # and back
+    out = [torch.full((T + extra, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+           for _ in range(2)]
+    pv.kv_cache_read(c.k, c.v, _cu(lengths), c.dev_table, T + extra, pos_offset=off,
+                     k_out=out[0], v_out=out[1], **c.exps())
+    assert pv.get_device_status() == 0
+    for x, o in ((k, out[0]), (v, out[1])):
+        assert (o[T:].float() == 3.0).all()
+        if fmt == "bf16":
+            assert torch.equal(o[:T].cpu().view(torch.int16), x[:T].view(torch.int16))
+        else:
+            y, byte = oracle.quantise_rows(oracle.to_f64(x[:T]))
+            assert (oracle.to_f64(o[:T]) == oracle.dequantise_rows(y, byte)).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lengths,offsets,page,H,D", WRITES)
+def test_write_and_read(pv, lengths, offsets, page, H, D, fmt):
+    _write_case(pv, lengths, offsets, page, H, D, fmt, False, False)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_write_strided_rows_into_interleaved_pages(pv, fmt):
+    _write_case(pv, [37, 0, 200, 1], [5, 3, 0, 77], 32, 3, 128, fmt, True, True)
+
+
+def test_quantised_special_rows(pv):
+    """Zeros, borders of the scale, ties, saturation, infinities, NaN, the smallest values."""
+    D, rows = 64, []
+    base = torch.zeros(D)
+    for top in (0.0, 448.0, 450.0, 224.0, 225.0, 1.0, 0.875, 57344.0, 60000.0, 3.38e38, 1e-30,
+                9.2e-41, 2.0 ** -92, 2.0 ** -100, math.inf):
+        r = base.clone()
+        r[3], r[60] = -top, top / 3 if math.isfinite(top) else 5.0
+        r[5], r[6] = 1e-3, -17.0 if top > 20 else 0.0
+        rows.append(r)
+    ties = torch.arange(D).float() * 0.5 + 200.0     # steps of 16 above 128: ties at 8
+    rows += [ties, -ties, torch.full((D,), math.nan), torch.full((D,), -0.0)]
+    one_nan = torch.randn(D)
+    one_nan[63] = math.nan
+    rows.append(one_nan)
+    x = torch.stack(rows).to(torch.bfloat16)[:, None]          # [T, 1, D]
+    T = x.shape[0]
+    c = Cache([T], 16, 1, D, "e4m3")
+    pv.kv_cache_write(x.cuda(), x.flip(0).contiguous().cuda(), c.k, c.v, _cu([T]), c.dev_table,
+                      **c.exps())
+    k, v = pv.kv_cache_read(c.k, c.v, _cu([T]), c.dev_table, T, **c.exps())
+    assert pv.get_device_status() == 0
+    y, byte = oracle.quantise_rows(oracle.to_f64(x))
+    want = oracle.dequantise_rows(y, byte)
+    np.testing.assert_array_equal(oracle.to_f64(k), want)
+    np.testing.assert_array_equal(oracle.to_f64(v), want[::-1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_copy_refusals_on_the_device(pv, fmt):
+    """Bad boundaries, offsets, lengths and pages: recorded, that sequence or page left alone."""
+    H, D, page = 2, 64, 16
+    c = Cache([40, 40], page, H, D, fmt)
+    k = _rows(64, H, D, 5).cuda()
+    before = c.k.view(torch.uint8).clone()
+    for cu, off, code in [([0, 20, 10], [0, 0], 1), ([0, 30, 70], [0, 0], 1), ([3, 5, 6], [0, 0], 1),
+                          ([0, 0, 5], [0, -1], 2), ([0, 0, 9], [0, 40], 2),
+                          ([0, 0, 1], [0, 2147483647], 2)]:
+        pv.kv_cache_write(k, k, c.k, c.v, _i32(cu), c.dev_table, pos_offset=_i32(off), **c.exps())
+        assert pv.get_device_status() == code
+        pv.kv_cache_read(c.k, c.v, _i32(cu), c.dev_table, 64, pos_offset=_i32(off), **c.exps())
+        assert pv.get_device_status() == code
+    for bad in (-1, c.P, 2147483647, -2147483648):
+        c.k.view(torch.uint8).copy_(before)
+        table = c.dev_table.clone()
+        table[0, 1] = bad
+        pv.kv_cache_write(k, k, c.k, c.v, _cu([40]), table[:1].contiguous(), **c.exps())
+        assert pv.get_device_status() == 8
+        out, _ = pv.kv_cache_read(c.k, c.v, _cu([40]), table[:1].contiguous(), 64, **c.exps())
+        assert pv.get_device_status() == 8
+        assert (out[16:32] == 0).all() and (out[40:] == 0).all()
+        assert (out[:16] != 0).any() and (out[32:40] != 0).any()
+        own = set(c.table[0].tolist()) - {int(c.table[0, 1])}
+        for g in set(range(c.P)) - own:
+            assert torch.equal(c.k.view(torch.uint8)[g], before[g])
+
+
+# ------------------------------------------------------------------ attention
+
+def _tolerance(want, weight, reach, D):
+    """fp32 scores, sums and accumulation, weights and output rounded to bf16.
+    The weights' rounding (2^-8 of each) moves a result by at most 2^-8 of
+    sum w |v|, the output's by 2^-8 of itself.  A score's fp32 sum of D
+    products (each exact) is off by at most D 2^-23 of sum |q k| (additions
+    that may truncate), the exponent's arithmetic and exp2 by 2^-22 of the
+    largest score and of the weight; twice that for numerator and sum."""
+    scores = (D + 4) * 2.0 ** -23 * reach + 2.0 ** -20
+    return (2.0 ** -8 + 2 * scores) * weight + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7) + 1e-30
+
+
+def _check(got, c, q, lengths, seq_lens, causal, scale, heads=None):
+    kc, vc = c.values()
+    want, weight, reach = oracle.paged_attention(oracle.to_f64(q), kc, vc, lengths, seq_lens,
+                                                 c.table, causal, scale, heads)
+    T = sum(lengths)
+    got = oracle.to_f64(got)[:T]
+    if heads is not None:
+        got, want, weight, reach = (x[:, heads] for x in (got, want, weight, reach))
+    assert np.isfinite(got).all()
+    excess = np.abs(got - want) - _tolerance(want, weight, reach, q.shape[2])
+    assert excess.size == 0 or excess.max() <= 0, \
+        f"{(excess > 0).sum()} of {excess.size} beyond, worst {excess.max():.3e} at " \
+        f"{np.unravel_index(excess.argmax(), excess.shape)}"
+
+
+def _attend(pv, c, q, lengths, seq_lens, causal, scale=None, extra=2, **kw):
+    out = torch.full((sum(lengths) + extra, q.shape[1], q.shape[2]), 5.0, dtype=torch.bfloat16,
+                     device="cuda")
+    qd = torch.cat([q, q.new_zeros(extra, *q.shape[1:])]).cuda()
+    pv.paged_attn_fwd(qd, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table,
+                      max(lengths + [0]), max(seq_lens + [0]), causal=causal, scale=scale, out=out,
+                      **c.exps(), **kw)
+    assert pv.get_device_status() == 0
+    assert (out[sum(lengths):].float() == 5.0).all()
+    return out
+
+
+def _attention_case(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal, scale=None, old=7.0,
+                    seed=0, spread=0.3, heads=None):
+    c = Cache(seq_lens, page, H, D, fmt, seed=seed, old=old)
+    _fill(pv, c, seq_lens, seed + 10, spread=spread)
+    q = _rows(sum(lengths), Hq, D, seed + 20, 0.0)
+    out = _attend(pv, c, q, lengths, seq_lens, causal, scale)
+    _check(out, c, q, lengths, seq_lens, causal, 1 / math.sqrt(D) if scale is None else scale,
+           heads)
+    return out
+
+
+DECODE = [
+    # seq_lens of single-token steps, Hq, Hkv, D, page
+    ([1], 1, 1, 64, 16),
+    ([1, 15, 16, 17, 2], 8, 8, 128, 16),
+    ([127, 128, 129, 1, 300], 8, 2, 128, 16),
+    ([64, 65, 1000, 511, 512, 513], 12, 3, 64, 32),
+    ([700, 33], 16, 2, 128, 64),
+    ([257, 1, 90], 16, 1, 128, 256),
+    ([255, 256, 31], 7, 1, 128, 128),
+    ([2500, 5], 10, 2, 64, 16),
+    ([40, 41], 40, 2, 128, 32),          # 20 query heads to a K/V head
+    ([129, 600], 64, 1, 128, 64),
+    ([77], 128, 1, 64, 16),
+    ([4100, 2049, 1025], 4, 1, 128, 16),
+]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("seq_lens,Hq,H,D,page", DECODE)
+def test_single_token_steps(pv, seq_lens, Hq, H, D, page, fmt):
+    _attention_case(pv, [1] * len(seq_lens), seq_lens, Hq, H, D, page, fmt, True)
+
+
+CHUNKS = [
+    # lengths, seq_lens, Hq, Hkv, D, page
+    ([2, 3, 4, 5, 8], [2, 40, 129, 1000, 9], 8, 2, 128, 16),
+    ([16, 17, 33], [16, 300, 33], 4, 4, 64, 32),
+    ([128, 129, 127], [128, 129, 500], 2, 2, 128, 16),
+    ([255, 256, 257], [300, 256, 800], 1, 1, 64, 64),
+    ([64, 65, 63], [64, 65, 200], 8, 2, 128, 128),
+    ([37, 200], [37, 1111], 14, 2, 128, 32),       # 7 query heads to a K/V head
+    ([50, 1], [513, 77], 15, 5, 64, 16),           # 3
+    ([3, 9], [1300, 64], 128, 1, 128, 256),        # 128: one token fills a tile
+    ([5, 2], [700, 5], 100, 1, 64, 16),
+    ([700], [1500], 4, 1, 128, 64),
+    ([1, 300, 1, 1, 0, 40], [900, 300, 1, 250, 30, 41], 8, 2, 128, 16),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lengths,seq_lens,Hq,H,D,page", CHUNKS)
+def test_chunks(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal):
+    _attention_case(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_see_nothing(pv, D, fmt):
+    """No keys at all, fewer keys than queries in causal order, no queries: zeros, or nothing."""
+    out = _attention_case(pv, [3, 1, 0, 40, 300], [0, 0, 20, 7, 130], 4, 2, D, 16, fmt, True)
+    assert (out[:4] == 0).all() and (out[4:4 + 33] == 0).all() and (out[44:44 + 170] == 0).all()
+    out = _attention_case(pv, [3, 1, 2], [0, 0, 20], 4, 2, D, 16, fmt, False)
+    assert (out[:4] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lengths,seq_lens", [([1, 1, 1], [1, 30, 257]), ([40, 7], [70, 7]),
+                                              ([300], [333])])
+def test_rows_past_a_sequence_never_reach_it(pv, lengths, seq_lens, fmt):
+    """NaN and infinities in every place of the pool that no sequence holds."""
+    for old in (math.nan, math.inf, -math.inf):
+        if fmt == "e4m3" and not math.isnan(old):
+            continue
+        _attention_case(pv, lengths, seq_lens, 8, 2, 128, 32, fmt, True, old=old)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5, 1e-4])
+def test_scales(pv, scale, fmt):
+    _attention_case(pv, [1, 20, 1], [300, 130, 1], 8, 2, 128, 16, fmt, True, scale=scale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_growing_scores(pv, fmt):
+    """Keys that grow along the sequence, so that the running maximum moves at every tile."""
+    D, H, n = 128, 1, 1500
+    c = Cache([n, n], 16, H, D, fmt)
+    k = _rows(2 * n, H, D, 3, 0.0).float()
+    k *= torch.linspace(0.05, 6.0, n).repeat(2)[:, None, None]
+    v = _rows(2 * n, H, D, 4, 0.0)
+    pv.kv_cache_write(k.to(torch.bfloat16).cuda(), v.cuda(), c.k, c.v, _cu([n, n]), c.dev_table,
+                      **c.exps())
+    q = _rows(301, 4, D, 5, 0.0)
+    out = _attend(pv, c, q, [300, 1], [n, n], True)
+    _check(out, c, q, [300, 1], [n, n], True, 1 / math.sqrt(D))
+
+
+def test_rows_of_very_unlike_scale(pv):
+    """8-bit rows whose exponents lie far apart: a huge row among tiny ones, values and keys."""
+    D, H, n = 128, 2, 400
+    c = Cache([n, n], 16, H, D, "e4m3")
+    k, v = _rows(2 * n, H, D, 3, 2.0), _rows(2 * n, H, D, 4, 4.0)
+    v[5], v[n + 17] = v[5] * 2.0 ** 9, v[n + 17] * 2.0 ** -30
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n, n]), c.dev_table, **c.exps())
+    q = _rows(41, 4, D, 5, 0.0)
+    out = _attend(pv, c, q, [1, 40], [n, n], True)
+    _check(out, c, q, [1, 40], [n, n], True, 1 / math.sqrt(D))
+
+
+def test_nan_in_a_visible_row_is_seen(pv):
+    for fmt in FORMATS:
+        c = Cache([100, 100], 16, 1, 64, fmt)
+        k, v = _rows(200, 1, 64, 1), _rows(200, 1, 64, 2)
+        k[20, 0, 7] = math.nan
+        pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([100, 100]), c.dev_table, **c.exps())
+        q = _rows(60, 2, 64, 3, 0.0)
+        out = _attend(pv, c, q, [30, 30], [100, 100], True).float()
+        assert torch.isnan(out[:30]).all() and torch.isfinite(out[30:60]).all()
+        out = _attend(pv, c, q[:2], [1, 1], [100, 100], True).float()
+        assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_independent_of_the_batch(pv, fmt):
+    """A sequence alone, in a batch, and in another order: the same bits; twice: the same bits."""
+    lengths, seq_lens = [1, 200, 1, 3, 40, 1, 64], [3000, 900, 17, 1200, 40, 600, 5000]
+    Hq, H, D, page = 8, 2, 128, 16
+    c = Cache(seq_lens, page, H, D, fmt)
+    _fill(pv, c, seq_lens, 1)
+    q = _rows(sum(lengths), Hq, D, 2, 0.0).cuda()
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    ref = pv.paged_attn_fwd(q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, 200, 5000,
+                            **c.exps())
+    again = pv.paged_attn_fwd(q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, 200, 5000,
+                              **c.exps())
+    assert torch.equal(ref.view(torch.int16), again.view(torch.int16))
+    for b, (n, m) in enumerate(zip(lengths, seq_lens)):
+        one = pv.paged_attn_fwd(q[cu[b]:cu[b + 1]], c.k, c.v, _cu([n]), _i32([m]),
+                                c.dev_table[b:b + 1].contiguous(), n, m, **c.exps())
+        assert torch.equal(one.view(torch.int16), ref[cu[b]:cu[b + 1]].view(torch.int16)), b
+    order = [4, 0, 6, 2, 5, 1, 3]
+    qs = torch.cat([q[cu[b]:cu[b + 1]] for b in order])
+    got = pv.paged_attn_fwd(qs, c.k, c.v, _cu([lengths[b] for b in order]),
+                            _i32([seq_lens[b] for b in order]),
+                            c.dev_table[order].contiguous(), 500, 9000, **c.exps())
+    want = torch.cat([ref[cu[b]:cu[b + 1]] for b in order])
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert pv.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_strided_queries_and_interleaved_pages(pv, fmt):
+    Hq, H, D, page = 6, 2, 128, 32
+    lengths, seq_lens = [1, 70, 1, 9], [500, 70, 33, 1000]
+    c = Cache(seq_lens, page, H, D, fmt, interleaved=True, width=40)
+    _fill(pv, c, seq_lens, 3)
+    T = sum(lengths)
+    fused = torch.full((T, (Hq + 2 * H) * D), math.nan, dtype=torch.bfloat16, device="cuda")
+    q = _rows(T, Hq, D, 9, 0.0)
+    fused[:, :Hq * D] = q.view(T, -1).cuda()
+    out = pv.paged_attn_fwd(fused[:, :Hq * D].view(T, Hq, D), c.k, c.v, _cu(lengths),
+                            _i32(seq_lens), c.dev_table, 70, 1000, **c.exps())
+    assert pv.get_device_status() == 0
+    _check(out, c, q, lengths, seq_lens, True, 1 / math.sqrt(D))
+
+
+def test_shared_pages(pv):
+    """Two sequences that hold the same pages of a common prefix."""
+    Hq, H, D, page = 8, 2, 64, 16
+    c = Cache([100, 100], page, H, D, "bf16")
+    c.table[1, :4] = c.table[0, :4]
+    c.dev_table = _i32(c.table.tolist())
+    _fill(pv, c, [64, 0], 1)
+    _fill(pv, c, [36, 36], 2, offsets=[64, 64])
+    q = _rows(20, Hq, D, 3, 0.0)
+    out = _attend(pv, c, q, [1, 19], [100, 100], True)
+    _check(out, c, q, [1, 19], [100, 100], True, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lq", [1, 40])
+def test_attention_refusals_on_the_device(pv, lq, fmt):
+    """Bad lengths and boundaries: recorded, that sequence's rows untouched, the others computed."""
+    Hq, H, D, page = 4, 2, 64, 16
+    c = Cache([100, 100], page, H, D, fmt)
+    _fill(pv, c, [100, 100], 1)
+    q = _rows(2 * lq, Hq, D, 2, 0.0)
+    want = _attend(pv, c, q, [lq, lq], [100, 100], True, extra=0)
+    for cu, lens, mq, mk, code in [
+            ([0, lq, 2 * lq], [100, -1], lq, 100, 4), ([0, lq, 2 * lq], [100, 113], lq, 200, 2),
+            ([0, lq, 2 * lq], [100, 101], lq, 100, 2), ([0, lq, 2 * lq + 1], [100, 100], lq + 1, 100, 1),
+            ([0, lq, lq - 1], [100, 100], lq, 100, 1)]:
+        out = torch.full((2 * lq, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        pv.paged_attn_fwd(q.cuda(), c.k, c.v, _i32(cu), _i32(lens), c.dev_table, mq, mk, out=out,
+                          **c.exps())
+        assert pv.get_device_status() == code
+        assert torch.equal(out[:lq], want[:lq]) and (out[lq:].float() == 5.0).all()
+    for bad in (-1, c.P, 2147483647, -2147483648):
+        table = c.dev_table.clone()
+        table[1, 2] = bad
+        out = pv.paged_attn_fwd(q.cuda(), c.k, c.v, _cu([lq, lq]), _i32([100, 100]), table, lq, 100,
+                                **c.exps())
+        assert pv.get_device_status() == 8
+        assert torch.equal(out[:lq], want[:lq]) and torch.isfinite(out.float()).all()
+
+
+def test_binding_refusals(pv):
+    c = Cache([40], 16, 2, 64, "e4m3")
+    x = _rows(4, 2, 64, 1).cuda()
+    cu = _cu([4])
+    lens = _i32([40])
+
+    def attend(**kw):
+        a = dict(q=x, k_cache=c.k, v_cache=c.v, cu_seqlens_q=cu, seq_lens=lens,
+                 page_table=c.dev_table, max_q=4, max_k=40, k_exp=c.ke, v_exp=c.ve)
+        a.update(kw)
+        return pv.paged_attn_fwd(**a)
+
+    for kw in [dict(k_exp=None), dict(k_exp=c.ke.transpose(1, 2)), dict(v_cache=c.v[1:]),
+               dict(k_cache=c.k.transpose(1, 2)), dict(q=x[:, :1].expand(4, 3, 64)),
+               dict(q=x.transpose(0, 1)), dict(q=x[..., :32]), dict(seq_lens=_i32([1, 2])),
+               dict(page_table=c.dev_table[0]), dict(out=x[:2]), dict(out=torch.empty(4, 2, 64)),
+               dict(seq_lens=lens.cpu()), dict(page_table=c.dev_table.repeat(2, 1)),
+               dict(workspace=torch.empty(64, dtype=torch.uint8))]:
+        with pytest.raises(ValueError):
+            attend(**kw)
+    for kw in [dict(q=x.float()), dict(k_cache=c.k.view(torch.uint8)), dict(seq_lens=lens.long()),
+               dict(v_exp=c.ve.float())]:
+        with pytest.raises((TypeError, ValueError)):
+            attend(**kw)
+    for kw in [dict(scale=math.nan), dict(max_q=-1)]:
+        with pytest.raises(pv.PackedAttnError):
+            attend(**kw)
+    with pytest.raises(ValueError):
+        pv.kv_cache_write(x, x[:2], c.k, c.v, cu, c.dev_table, k_exp=c.ke, v_exp=c.ve)
+    with pytest.raises(ValueError):
+        pv.kv_cache_read(c.k, c.v, cu, c.dev_table, 4, k_exp=c.ke, v_exp=c.ve, k_out=x[:2])
+    with pytest.raises(pv.PackedAttnError):       # a page size that is no power of two
+        bad = torch.zeros(3, 24, 2, 64, dtype=torch.bfloat16, device="cuda")
+        pv.kv_cache_write(x, x, bad, bad, cu, c.dev_table)
+    assert pv.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_beyond_32_bit_offsets(pv, fmt):
+    """A pool of more than 2^32 elements: rows in its last pages."""
+    H, D, page = 16, 128, 256
+    per_page = page * H * D
+    P = (1 << 32) // per_page + 9
+    dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    kc, vc = (torch.empty(P, page, H, D, dtype=dt, device="cuda") for _ in range(2))
+    ex = {}
+    if fmt == "e4m3":
+        ex = dict(k_exp=torch.empty(P, H, page, dtype=torch.uint8, device="cuda"),
+                  v_exp=torch.empty(P, H, page, dtype=torch.uint8, device="cuda"))
+    table = _i32([[P - 1, 3], [P - 5, P - 2]])
+    n = [300, 290]
+    k, v = _rows(sum(n), H, D, 1, 0.3), _rows(sum(n), H, D, 2, 0.3)
+    pv.kv_cache_write(k.cuda(), v.cuda(), kc, vc, _cu(n), table, **ex)
+    rk, rv = pv.kv_cache_read(kc, vc, _cu(n), table, sum(n), **ex)
+    if fmt == "bf16":
+        assert torch.equal(rk.cpu(), k) and torch.equal(rv.cpu(), v)
+    q = _rows(41, H, D, 3, 0.0)
+    out = pv.paged_attn_fwd(q.cuda(), kc, vc, _cu([1, 40]), _i32(n), table, 40, 300, **ex)
+    assert pv.get_device_status() == 0
+    # the same rows in a small pool
+    small = Cache(n, page, H, D, fmt)
+    pv.kv_cache_write(k.cuda(), v.cuda(), small.k, small.v, _cu(n), small.dev_table,
+                      **small.exps())
+    want = pv.paged_attn_fwd(q.cuda(), small.k, small.v, _cu([1, 40]), _i32(n), small.dev_table,
+                             40, 300, **small.exps())
+    assert torch.equal(out, want)
+    _check(want, small, q, [1, 40], n, True, 1 / math.sqrt(D), heads=[0, 15])
+
+
+# ------------------------------------------------------------------ used together
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_serving_run(pv, D, fmt):
+    """Prompts taken in chunks beside sequences that answer token by token: rotary
+    embedding, write and attention of every step; at the end the cache is read back."""
+    Hq, H, page, B = 6, 2, 16, 4
+    steps = [[30, 0, 17, 1], [25, 40, 1, 1], [1, 33, 1, 0], [1, 1, 1, 1], [1, 1, 0, 1]]
+    total = np.sum(steps, axis=0)
+    c = Cache(total.tolist(), page, H, D, fmt, width=12)
+    done = np.zeros(B, dtype=np.int64)
+    kept = [[] for _ in range(B)]
+    for s, lengths in enumerate(steps):
+        T = sum(lengths)
+        q, k, v = (_rows(T, h, D, 100 * s + i, 0.0).cuda() for i, h in enumerate((Hq, H, H)))
+        cu, off = _cu(lengths), _i32(done.tolist())
+        pv.rope_packed(k, k.clone(), cu, cu, off)         # a call takes q and k of equal heads
+        pv.rope_packed(q, q.clone(), cu, cu, off)
+        pv.kv_cache_write(k, v, c.k, c.v, cu, c.dev_table, pos_offset=off, **c.exps())
+        lens = (done + np.array(lengths)).tolist()
+        out = pv.paged_attn_fwd(q, c.k, c.v, cu, _i32(lens), c.dev_table, max(lengths), max(lens),
+                                **c.exps())
+        assert pv.get_device_status() == 0
+        _check(out, c, q.cpu(), lengths, lens, True, 1 / math.sqrt(D))
+        t = 0
+        for b, n in enumerate(lengths):
+            kept[b].append(k[t:t + n].cpu())
+            t += n
+        done += np.array(lengths)
+    rk, _ = pv.kv_cache_read(c.k, c.v, _cu(total.tolist()), c.dev_table, int(total.sum()),
+                             **c.exps())
+    want = oracle.to_f64(torch.cat([torch.cat(x) for x in kept]))
+    if fmt == "e4m3":
+        want = oracle.dequantise_rows(*oracle.quantise_rows(want))
+    assert (oracle.to_f64(rk) == want).all()
+
+
+def test_attention_over_cache_matches_packed_attention(pv):
+    """Equal heads, no causal order: the packed kernel on the rows that the cache gives back."""
+    H, D, page = 4, 128, 64
+    lengths, seq_lens = [300, 5, 64], [300, 700, 129]
+    for fmt in FORMATS:
+        c = Cache(seq_lens, page, H, D, fmt)
+        _fill(pv, c, seq_lens, 1)
+        q = _rows(sum(lengths), H, D, 2, 0.0).cuda()
+        a = pv.paged_attn_fwd(q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, 300, 700,
+                              causal=False, **c.exps())
+        k, v = pv.kv_cache_read(c.k, c.v, _cu(seq_lens), c.dev_table, sum(seq_lens), **c.exps())
+        b = pv.varlen_attn_fwd(q, k, v, _cu(lengths), _cu(seq_lens), 300, 700)
+        assert pv.get_device_status() == 0
+        _check(a, c, q.cpu(), lengths, seq_lens, False, 1 / math.sqrt(D))
+        _check(b, c, q.cpu(), lengths, seq_lens, False, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_graph_replays_with_new_lengths(pv, fmt):
+    """One captured step, replayed as the sequences grow; two graphs with their own workspaces."""
+    Hq, H, D, page, B = 8, 2, 128, 16, 3
+    c = Cache([900, 40, 300], page, H, D, fmt, width=64)
+    lens0 = [850, 20, 270]
+    _fill(pv, c, lens0, 1)
+    cu, lens, off = _cu([1] * B), _i32(lens0), _i32(lens0)
+    q = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(B, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    outs = [torch.zeros_like(q), torch.zeros_like(q)]
+    side = torch.cuda.Stream()
+    graphs = []
+    torch.cuda.synchronize()
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            pv.kv_cache_write(k, v, c.k, c.v, cu, c.dev_table, pos_offset=off, **c.exps())
+            pv.paged_attn_fwd(q, c.k, c.v, cu, lens, c.dev_table, 1, 1024, out=o, **c.exps())
+        graphs.append(g)
+    for step in range(4):
+        now = [n + step for n in lens0]
+        off.copy_(_i32(now))
+        lens.copy_(_i32([n + 1 for n in now]))
+        for x, h, s in ((q, Hq, 0), (k, H, 1), (v, H, 2)):
+            x.copy_(_rows(B, h, D, 50 * step + s, 0.0).cuda())
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert pv.get_device_status() == 0
+        _check(outs[0], c, q.cpu(), [1] * B, [n + 1 for n in now], True, 1 / math.sqrt(D))
+        assert torch.equal(outs[0], outs[1])
+
+
+def test_calls_on_two_streams_at_once(pv):
+    """Calls that overlap, each with the workspace that the binding allocates on its stream."""
+    Hq, H, D, page = 8, 2, 128, 16
+    seq_lens = [3000, 1500, 40]
+    c = Cache(seq_lens, page, H, D, "bf16")
+    _fill(pv, c, seq_lens, 1)
+    qs = [_rows(3, Hq, D, 10 + i, 0.0).cuda() for i in range(2)] + \
+         [_rows(90, Hq, D, 20, 0.0).cuda()]
+    lens = [[1, 1, 1], [1, 1, 1], [30, 20, 40]]
+    args = [(_cu(n), _i32(seq_lens)) for n in lens]
+    want = [pv.paged_attn_fwd(q, c.k, c.v, *a, c.dev_table, max(n), 3000)
+            for q, a, n in zip(qs, args, lens)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        outs = [torch.zeros_like(q) for q in qs]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for q, a, n, s, o in zip(qs, args, lens, streams, outs):
+                pv.paged_attn_fwd(q, c.k, c.v, *a, c.dev_table, max(n), 3000, out=o, stream=s)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    assert pv.get_device_status() == 0
+
+
+def test_many_sequences(pv):
+    """The largest batch, lengths from nothing to a few pages."""
+    B, Hq, H, D, page = 1024, 4, 2, 64, 16
+    rng = np.random.default_rng(0)
+    seq_lens = rng.integers(0, 60, B).tolist()
+    lengths = rng.integers(0, 3, B).tolist()
+    _attention_case(pv, lengths, seq_lens, Hq, H, D, page, "bf16", True)
+    lengths[500], seq_lens[500] = 50, 400
+    _attention_case(pv, lengths, seq_lens, Hq, H, D, page, "e4m3", True)
+
+
+def test_random_sweep(pv):
+    rng = np.random.default_rng(77)
+    for n in range(40):
+        B, H, G = int(rng.integers(1, 7)), int(rng.integers(1, 4)), int(rng.integers(1, 12))
+        D, page = int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128, 256]))
+        top = int(rng.choice([1, 4, 40, 300]))
+        lengths = rng.integers(0, top + 1, B).tolist()
+        seq_lens = [int(a + rng.integers(0, rng.choice([2, 200, 2500]))) for a in lengths]
+        heads = sorted(set(rng.integers(0, H * G, 4).tolist()))
+        _attention_case(pv, lengths, seq_lens, H * G, H, D, page, FORMATS[n % 2],
+                        bool(rng.random() < 0.7), seed=n, heads=heads)
