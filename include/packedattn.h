@@ -311,7 +311,9 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  * (total_q = 0 does nothing, and q, out may then be NULL); max_q / max_k bound every L_b and
  * seq_lens[b]; Hq a multiple of Hkv, Hq / Hkv <= 128; scale finite.
  * Rows of a page past a sequence's last position never reach a result,
- * whatever their bits.
+ * whatever their bits.  A key that causal order hides from a query has weight
+ * zero there; a NaN or infinity in its V row can still reach that query as
+ * 0 * NaN (in its K row it cannot).
  *
  * workspace: device memory of at least pa_paged_attn_workspace_bytes() bytes,
  * 16-byte aligned, for the partial results of keys that are split over

@@ -104,4 +104,63 @@ __device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
   return s;
 }
 
+// ---------------------------------------------------------------- splits
+// Keys of one (sequence, K/V head) are split over CTAs, and the parts joined
+// by combine_kernel.  The rule looks at the sequence's own lengths and the
+// head counts only, never at the batch, so a sequence's bits are its own.
+
+// Sequences of at most this many (query, head of the group) rows take the
+// streaming kernel (paged_decode.cu), longer ones the tiled one.
+constexpr int kDecodeRows = 16;
+
+constexpr int kDecodeUnits = 456;   // parts of a lone sequence: three for each of 152 SMs
+
+// Smallest part: short contexts are bound by latency and want many small
+// parts, long ones by bytes and want few partial results.
+__host__ __device__ __forceinline__ int decode_min_part(int lk) {
+  return lk <= 1024 ? 128 : lk <= 4096 ? 256 : 512;
+}
+__host__ __device__ __forceinline__ int decode_most_parts(int Hkv) {
+  return Hkv >= kDecodeUnits ? 1 : kDecodeUnits / Hkv;
+}
+// Keys of each part (a multiple of 64) of a sequence of lk keys.
+__host__ __device__ __forceinline__ int decode_part(int lk, int Hkv) {
+  const int most = decode_most_parts(Hkv);
+  const int even = static_cast<int>((static_cast<int64_t>(lk) + most - 1) / most);
+  const int part = even > decode_min_part(lk) ? even : decode_min_part(lk);
+  return part > (1 << 30) ? part : (part + 63) & ~63;
+}
+__host__ __device__ __forceinline__ int decode_parts(int lk, int Hkv) {
+  if (lk <= 0) return 0;
+  const int part = decode_part(lk, Hkv);
+  return static_cast<int>((static_cast<int64_t>(lk) + part - 1) / part);
+}
+// The most parts that a sequence of at most max_k keys has.
+inline int decode_parts_bound(int max_k, int Hkv) {
+  if (max_k <= 0) return 1;
+  int64_t n = (static_cast<int64_t>(max_k) + decode_min_part(max_k) - 1) / decode_min_part(max_k);
+  if (max_k > 1024 && n < 8) n = 8;
+  if (max_k > 4096 && n < 16) n = 16;
+  const int most = decode_most_parts(Hkv);
+  return static_cast<int>(n < most ? n : most);
+}
+
+// A paged attention call as its kernels see it.
+struct PagedAttnParams {
+  PagedCache c;
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  const int32_t *cu_q, *seq_lens;
+  int64_t q_stride;
+  int batch, total_q, max_q, max_k, Hq, G;
+  int causal;
+  float scale_log2;
+  int32_t *status;
+  // partial results of the streaming kernel: part s of row (token i, head h)
+  // of sequence b at slot (b * dec_parts + s) * dec_rows + i * Hq + h
+  float *dec_o;        // [slot][D], not normalised
+  float2 *dec_ml;      // [slot] (maximum in log2 units, sum)
+  int dec_parts, dec_rows;
+};
+
 }  // namespace pa

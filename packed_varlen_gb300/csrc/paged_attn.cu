@@ -8,23 +8,12 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_launch.h"
 
 namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-
-struct PagedAttnParams {
-  PagedCache c;
-  const __nv_bfloat16 *q;
-  __nv_bfloat16 *out;
-  const int32_t *cu_q, *seq_lens;
-  int64_t q_stride;
-  int total_q, max_q, max_k, Hq;
-  int causal;
-  float scale_log2;
-  int32_t *status;
-};
 
 template <bool kQuant, int D>
 __global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const PagedAttnParams p) {
@@ -37,6 +26,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const Paged
     if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.status, err);
     return;
   }
+  if (s.lq <= kDecodeRows / p.G) return;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int i = static_cast<int>(item / p.Hq), h = static_cast<int>(item - static_cast<int64_t>(i) * p.Hq);
   if (i >= s.lq) return;
@@ -99,6 +89,28 @@ __global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const Paged
   for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(n > 0 ? o[e] * inv : 0.f);
 }
 
+// Where the partial results lie in the workspace.
+struct WorkspacePlan {
+  int dec_parts, dec_rows;
+  int64_t dec_o, dec_ml;   // byte offsets
+  int64_t bytes;
+};
+
+WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv,
+                             int D) {
+  WorkspacePlan w{};
+  const int G = Hq / Hkv;
+  int tokens = max_q < total_q ? max_q : total_q;   // of a sequence in the streaming kernel
+  if (tokens > kDecodeRows / G) tokens = kDecodeRows / G;
+  w.dec_parts = tokens > 0 ? decode_parts_bound(max_k, Hkv) : 1;
+  w.dec_rows = tokens * Hq;
+  const int64_t slots = w.dec_parts > 1 ? static_cast<int64_t>(batch) * w.dec_parts * w.dec_rows : 0;
+  w.dec_o = 0;
+  w.dec_ml = slots * D * 4;
+  w.bytes = (w.dec_ml + slots * 8 + 15) & ~int64_t{15};
+  return w;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -110,7 +122,8 @@ extern "C" int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q,
   if (batch < 1 || batch > PA_MAX_BATCH || total_q < 0 || max_q < 0 || max_k < 0 || Hkv < 1 ||
       Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128))
     return -1;
-  return 0;
+  const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D);
+  return w.bytes;
 }
 
 extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
@@ -158,9 +171,22 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.Hq = Hq;
   p.causal = causal;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_q) * Hq + 7) / 8), batch);
+  p.batch = batch;
+  p.G = Hq / Hkv;
+  const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D);
+  p.dec_parts = w.dec_parts;
+  p.dec_rows = w.dec_rows;
+  p.dec_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.dec_o);
+  p.dec_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + w.dec_ml);
   auto s = reinterpret_cast<cudaStream_t>(stream);
-  if (format == PA_CACHE_E4M3) {
+  const bool quant = format == PA_CACHE_E4M3;
+  if (p.G <= kDecodeRows) {
+    e = launch_paged_decode(p, quant, s);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  if (max_q <= kDecodeRows / p.G) return PA_OK;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_q) * Hq + 7) / 8), batch);
+  if (quant) {
     if (D == 128)
       paged_attn_simple_kernel<true, 128><<<grid, kThreads, 0, s>>>(p);
     else

@@ -1,0 +1,13 @@
+// Launchers of the paged attention kernels (paged_attn.cu calls them).
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace pa {
+
+struct PagedAttnParams;   // paged.cuh
+
+// Sequences of at most kDecodeRows rows: streaming kernel, and the join of its parts.
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, cudaStream_t stream);
+
+}  // namespace pa
