@@ -161,6 +161,13 @@ struct PagedAttnParams {
   float *dec_o;        // [slot][D], not normalised
   float2 *dec_ml;      // [slot] (maximum in log2 units, sum)
   int dec_parts, dec_rows;
+  // partial results of the tiled kernel
+  float *chunk_o;      // [chunk_rows][D], not normalised
+  float2 *chunk_ml;    // [chunk_rows]
+  int4 *chunk_join;    // two to a share: what to join at its end
+  int32_t *chunk_n_cuts;   // shares of the call
+  int64_t chunk_rows;
+  int chunk_cuts;      // bound on the shares of the call
 };
 
 }  // namespace pa

@@ -8,6 +8,7 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_chunk_work.cuh"
 #include "paged_launch.h"
 
 namespace pa {
@@ -92,7 +93,9 @@ __global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const Paged
 // Where the partial results lie in the workspace.
 struct WorkspacePlan {
   int dec_parts, dec_rows;
-  int64_t dec_o, dec_ml;   // byte offsets
+  int64_t chunk_rows;
+  int chunk_cuts;
+  int64_t dec_o, dec_ml, chunk_o, chunk_ml, chunk_join, chunk_n_cuts;   // byte offsets
   int64_t bytes;
 };
 
@@ -105,9 +108,39 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
   w.dec_parts = tokens > 0 ? decode_parts_bound(max_k, Hkv) : 1;
   w.dec_rows = tokens * Hq;
   const int64_t slots = w.dec_parts > 1 ? static_cast<int64_t>(batch) * w.dec_parts * w.dec_rows : 0;
-  w.dec_o = 0;
-  w.dec_ml = slots * D * 4;
-  w.bytes = (w.dec_ml + slots * 8 + 15) & ~int64_t{15};
+  // Sequences of the tiled kernel, and what their shares may leave: a share
+  // has at least kChunkMinShare key tiles, and two parts of at most an item's
+  // rows; none where no sequence can have enough keys to be cut.
+  const int item_tokens = 2 * (kChunkTile / G), few = kDecodeRows / G;
+  const int64_t tiles_k = (static_cast<int64_t>(max_k) + kChunkTile - 1) / kChunkTile;
+  int64_t seqs = 0, shares = 0;
+  if (max_q > few && tiles_k > kChunkMinShare) {
+    seqs = total_q / (few + 1);
+    if (seqs > batch) seqs = batch;
+    const int64_t items = (static_cast<int64_t>(max_q) + item_tokens - 1) / item_tokens;
+    // tiles of all items of a sequence's heads, kept from overflowing
+    const int64_t tiles = items * Hkv > kChunkShares * kChunkMinShare
+                              ? kChunkShares * kChunkMinShare : items * Hkv * tiles_k;
+    shares = (tiles + kChunkMinShare - 1) / kChunkMinShare;
+    if (shares > kChunkShares) shares = kChunkShares;
+  }
+  w.chunk_cuts = static_cast<int>(seqs * shares);
+  const int64_t rows_by_items = seqs * item_tokens * G, rows_by_tokens = static_cast<int64_t>(total_q) * G;
+  w.chunk_rows = 2 * shares * (seqs == 0 ? 0 : rows_by_items < rows_by_tokens ? rows_by_items
+                                                                              : rows_by_tokens);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 15) & ~int64_t{15};
+    return here;
+  };
+  w.dec_o = take(slots * D * 4);
+  w.dec_ml = take(slots * 8);
+  w.chunk_o = take(w.chunk_rows * D * 4);
+  w.chunk_ml = take(w.chunk_rows * 8);
+  w.chunk_join = take(static_cast<int64_t>(w.chunk_cuts) * 32);
+  w.chunk_n_cuts = take(w.chunk_cuts > 0 ? 16 : 0);
+  w.bytes = at;
   return w;
 }
 
@@ -176,8 +209,15 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D);
   p.dec_parts = w.dec_parts;
   p.dec_rows = w.dec_rows;
-  p.dec_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.dec_o);
-  p.dec_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + w.dec_ml);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.dec_o = reinterpret_cast<float *>(ws + w.dec_o);
+  p.dec_ml = reinterpret_cast<float2 *>(ws + w.dec_ml);
+  p.chunk_o = reinterpret_cast<float *>(ws + w.chunk_o);
+  p.chunk_ml = reinterpret_cast<float2 *>(ws + w.chunk_ml);
+  p.chunk_join = reinterpret_cast<int4 *>(ws + w.chunk_join);
+  p.chunk_n_cuts = reinterpret_cast<int32_t *>(ws + w.chunk_n_cuts);
+  p.chunk_rows = w.chunk_rows;
+  p.chunk_cuts = w.chunk_cuts;
   auto s = reinterpret_cast<cudaStream_t>(stream);
   const bool quant = format == PA_CACHE_E4M3;
   if (p.G <= kDecodeRows) {
@@ -185,6 +225,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
     if (e != cudaSuccess) return from_cuda(e);
   }
   if (max_q <= kDecodeRows / p.G) return PA_OK;
+  if (!quant) return from_cuda(launch_paged_chunk(p, quant, sms, s));
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_q) * Hq + 7) / 8), batch);
   if (quant) {
     if (D == 128)

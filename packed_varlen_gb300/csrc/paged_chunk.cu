@@ -1,0 +1,792 @@
+// Paged attention of sequences with many query rows, on the 5th-generation
+// tensor cores: chunks of long inputs over everything cached before them.
+//
+// Bound by the tensor pipe once a K/V head's rows fill its tiles.  Grouped
+// query heads share their K/V head's keys, so a 128-row tile holds the whole
+// group of 128 / G tokens (row = token * G + head of the group): each K/V
+// byte brought to shared memory serves G heads.  Otherwise the kernel is the
+// single-CTA packed attention kernel (attn_tc.cu) with its K/V tiles
+// assembled from pages: one persistent CTA per SM, two 128-row tiles that
+// share every K/V tile, S and O of both in TMEM, P over S.
+//   warp 0       TMA producer: Q once per item, then K0, V0, K1, V1, ..., each
+//                tile one copy per page (or per 128 rows of a larger page) and
+//                64 columns; pages past the sequence's last key are fetched
+//                from an out-of-range page, so they land as zeros.
+//   warps 1, 2   issue tile 0's and tile 1's tcgen05.mma in turn.
+//   warps 3..6   softmax of tile 0, a thread per row; warps 7..10 of tile 1.
+// A unit of work is whole items or a share of the sequence's key tiles
+// (paged_chunk_work.cuh); a part of an item leaves its unnormalised output,
+// maximum and sum in the workspace, and paged_chunk_join_kernel joins them.
+// Keys that a row does not see are masked to -inf; V rows past the sequence's
+// last key are cleared in shared memory before any product reads them (0 *
+// NaN would be NaN); rows of a tile beyond its tokens are computed from
+// whatever lies there and never stored.  Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "paged_chunk_work.cuh"
+#include "paged_launch.h"
+#include "tc_ptx.cuh"
+#include "tma_map.h"
+
+namespace pa {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = kChunkTile;
+constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
+constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
+constexpr float kRescaleThreshold = 8.0f;       // log2 units
+
+template <int D, bool kQuant>
+struct Cfg {
+  static constexpr int kSoftmaxWarp = 3;                    // first of eight
+  static constexpr int kThreads = (kSoftmaxWarp + 8) * 32;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kHalfBytes = kTile * 64 * 2;         // 128 rows x 128 B
+  static constexpr int kTileBytes = kTile * D * 2;          // one Q/K/V tile
+  static constexpr int kQOff = 0;                           // Q0, Q1
+  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  // barriers: per Q tile t an S-full, a P-ready and an O-full barrier
+  static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
+                       kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots;
+  static constexpr int kNumBars = 12 + 2 * kSlots;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag, counter
+  static constexpr int kSchedOff = (kMiscOff + 16 + 127) / 128 * 128;
+  // order, first part row, first cut unit and first unit of each sequence in the list
+  static constexpr int kSmemBytes = kSchedOff + (4 * PA_MAX_BATCH + 2) * 4;
+  static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
+  // TMEM columns: S_t at 128 t (P_t over its first 64), O_t at 256 + D t
+  static constexpr uint32_t kColS = 0;
+  static constexpr uint32_t kColO = 256;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile, false);
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D, true);
+  // V (MN-major): next 64-column half at LBO, next 8 keys at SBO = 1024.  With
+  // D = 64 the MMA spans a single half and LBO is never used.
+  static constexpr uint32_t kVLbo = D == 128 ? kHalfBytes : 1024;
+};
+
+// Whole warp: zero key rows [valid, 128) of a V tile in shared memory (its
+// column halves are 128 rows of 128 bytes; the swizzle permutes 16-byte chunks
+// inside a row only).  The fences order the stores after the bytes that
+// landed and before the tensor core's reads.
+template <int D>
+__device__ __forceinline__ void zero_v_tail(uint8_t *tile, int valid, int lane) {
+  fence_proxy_async();
+  const int per_half = (kTile - valid) * 8;   // 16-byte chunks per half
+  for (int c = lane; c < per_half * (D / 64); c += 32) {
+    const int hf = c / per_half, r = c - hf * per_half;
+    *reinterpret_cast<uint4 *>(tile + hf * (kTile * 128) + (valid + (r >> 3)) * 128 +
+                               (r & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
+// The sequences of the call that take this kernel, most keys first, with the
+// prefixes of their units, of those that may cut items (shares), and of the
+// workspace rows of their parts.  Built by every CTA; all threads call it and
+// it ends with __syncthreads().  first[n] = all units, cut0[n] = all shares.
+__device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32_t *first,
+                                 int32_t *cut0, int32_t *part0, int32_t *tmp_seq,
+                                 int32_t *tmp_lk, int32_t *count, bool report) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
+  for (int b = tid; b < p.batch; b += nt) {
+    int err;
+    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
+    if (err && report) record_error(p.status, err);
+    if (s.lq > kDecodeRows / p.G) {
+      const int at = atomicAdd(count, 1);   // any order: the ranks below are the list's
+      tmp_seq[at] = b;
+      tmp_lk[at] = s.lk;
+    }
+  }
+  __syncthreads();
+  const int n = *count;
+  for (int x = tid; x < n; x += nt) {
+    const int b = tmp_seq[x], lb = tmp_lk[x];
+    int rank = 0;
+    for (int y = 0; y < n; ++y) rank += (tmp_lk[y] > lb) || (tmp_lk[y] == lb && tmp_seq[y] < b);
+    order[rank] = b;
+  }
+  __syncthreads();
+  for (int x = tid; x < n; x += nt) {
+    int err;
+    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, order[x], p.total_q, p.max_q, p.max_k, cap, err);
+    const ChunkWork w = chunk_work(s.lq, s.lk, p.causal, p.G, p.c.Hkv);
+    tmp_seq[x] = w.units;
+    tmp_lk[x] = w.share ? chunk_part_rows(s.lq, p.G) : 0;   // rows of one part
+  }
+  __syncthreads();
+  if (tid < 32) {
+    int units = 0, cuts = 0, rows = 0;
+    for (int base = 0; base < n; base += 32) {
+      const int x = base + tid;
+      const int u = x < n ? tmp_seq[x] : 0, pr = x < n ? tmp_lk[x] : 0;
+      const int k = pr > 0 ? u : 0, r = 2 * u * pr;   // two parts at most to a share
+      int iu = u, ik = k, ir = r;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int yu = __shfl_up_sync(0xffffffffu, iu, off);
+        const int yk = __shfl_up_sync(0xffffffffu, ik, off);
+        const int yr = __shfl_up_sync(0xffffffffu, ir, off);
+        if (tid >= off) {
+          iu += yu;
+          ik += yk;
+          ir += yr;
+        }
+      }
+      if (x < n) {
+        first[x] = units + iu - u;
+        cut0[x] = cuts + ik - k;
+        part0[x] = rows + ir - r;
+      }
+      units += __shfl_sync(0xffffffffu, iu, 31);
+      cuts += __shfl_sync(0xffffffffu, ik, 31);
+      rows += __shfl_sync(0xffffffffu, ir, 31);
+    }
+    if (tid == 0) {
+      first[n] = units;
+      cut0[n] = cuts;
+    }
+  }
+  __syncthreads();
+  return n;
+}
+
+// A unit's sequence, and the walk over its pieces.
+struct Unit {
+  PagedSeq s;
+  int b, local;       // sequence, unit within it
+  int at;             // place of the sequence in the list
+  int part_rows;      // workspace rows of one part
+  int64_t part0;      // workspace row of the sequence's first part
+  ChunkWork w;
+  ChunkCursor cur;
+};
+__device__ __forceinline__ Unit open_unit(const PagedAttnParams &p, const int32_t *order,
+                                          const int32_t *first, const int32_t *part0, int n,
+                                          int u) {
+  int lo = 0, hi = n;   // largest x < n with first[x] <= u (every sequence has a unit)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= u) lo = mid; else hi = mid;
+  }
+  Unit x;
+  x.b = order[lo];
+  int err;
+  x.s = paged_seq(p.cu_q, p.seq_lens, x.b, p.total_q, p.max_q, p.max_k,
+                  static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
+  x.local = u - first[lo];
+  x.at = lo;
+  x.part0 = part0[lo];
+  x.part_rows = chunk_part_rows(x.s.lq, p.G);
+  x.w = chunk_work(x.s.lq, x.s.lk, p.causal, p.G, p.c.Hkv);
+  x.cur.start(x.w, x.local, p.c.Hkv);
+  return x;
+}
+
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
+  using C = Cfg<D, kQuant>;
+  extern __shared__ uint8_t smem_raw[];
+  // 128-byte swizzle atoms need a 1024-byte aligned base
+  const uint32_t base = smem_u32(smem_raw);
+  if (base & 1023u) {
+    if (threadIdx.x == 0) record_error(p.status, PA_DEVICE_ERR_SMEM_ALIGN);
+    return;
+  }
+  uint8_t *gbase = smem_raw;
+  const uint32_t sQ = base + C::kQOff;
+  const uint32_t sRing = base + C::kRingOff;
+  auto bar = [&](int idx) -> uint32_t { return base + C::kBarOff + 8u * idx; };
+  uint32_t *tmem_base_ptr = reinterpret_cast<uint32_t *>(gbase + C::kMiscOff);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(gbase + C::kMiscOff + 4);
+  int32_t *counter = reinterpret_cast<int32_t *>(gbase + C::kMiscOff + 8);
+  int32_t *order = reinterpret_cast<int32_t *>(gbase + C::kSchedOff);
+  int32_t *part0 = order + PA_MAX_BATCH;
+  int32_t *cut0 = part0 + PA_MAX_BATCH;
+  int32_t *first = cut0 + PA_MAX_BATCH + 1;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- set-up: barriers, TMEM, work list --------------------------------
+  if (tid == 0) {
+    mbar_init(bar(C::kQFull), 1);
+    mbar_init(bar(C::kQEmpty), 2);   // one arrival per MMA issuer
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(C::kSFull + t), 1);
+      mbar_init(bar(C::kPReady + t), 128);
+      mbar_init(bar(C::kOFull + t), 1);
+      mbar_init(bar(C::kFinal + t), 1);
+      mbar_init(bar(C::kTurn + t), 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(bar(C::kSlotFull + s), 1);
+      mbar_init(bar(C::kSlotEmpty + s), 2);   // one arrival per MMA issuer
+    }
+    *abort_flag = 0;
+    *counter = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(base + C::kMiscOff, C::kTmemCols);
+  __syncthreads();
+  // the ring is free until the first load: use it for the build's temporaries
+  int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
+  const int n_seqs = build_list(p, order, first, cut0, part0, tmp, tmp + PA_MAX_BATCH,
+                                counter, blockIdx.x == 0);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_base_ptr;
+  const int n_units = first[n_seqs];
+  const int tile_tokens = kTile / p.G, tile_rows = tile_tokens * p.G;
+  if (blockIdx.x == 0 && tid == 0 && p.chunk_cuts > 0) *p.chunk_n_cuts = cut0[n_seqs];
+
+  if (warp == 0) {
+    // ================= TMA producer =================
+    const bool lead = elect_one();
+    if (lead) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    uint32_t q_loads = 0, slot_loads = 0;
+    bool ok = true;
+    auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
+      const bool w = bounded_wait(b, parity, abort_flag, p.status, kWaitLimit);
+      return __all_sync(0xffffffffu, w);
+    };
+    const int box_rows = min(1 << p.c.page_shift, kTile), boxes = kTile / box_rows;
+    const int page_mask = (1 << p.c.page_shift) - 1;
+    // lane x < boxes: page of the x-th box of a key tile
+    auto load_pages = [&](const Unit &x, int j) -> int32_t {
+      const int64_t key = static_cast<int64_t>(j) * kTile + lane * box_rows;
+      if (lane >= boxes || key >= x.s.lk) return -1;
+      const int32_t page =
+          __ldg(p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages + (key >> p.c.page_shift));
+      if (!page_ok(p.c, page)) {
+        record_error(p.status, PA_DEVICE_ERR_PAGE);
+        return -1;
+      }
+      return page;
+    };
+    auto load_kv = [&](const CUtensorMap *tm, int32_t pages, int j, int head) -> bool {
+      const uint32_t s = slot_loads % C::kSlots;
+      const uint32_t use = slot_loads / C::kSlots;
+      if (!wait_all(bar(C::kSlotEmpty + s), (use & 1u) ^ 1u)) return false;
+      const uint32_t dst = sRing + s * C::kTileBytes;
+      if (lead) mbar_arrive_expect_tx(bar(C::kSlotFull + s), C::kTileBytes);
+      const int row = (j * kTile) & page_mask;   // not 0 only where a page spans several tiles
+      for (int x = 0; x < boxes; ++x) {
+        const int32_t page = __shfl_sync(0xffffffffu, pages, x);
+        if (lead) {
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_load_4d(dst + hf * C::kHalfBytes + x * box_rows * 128, tm, bar(C::kSlotFull + s),
+                        hf * 64, head, row, page);
+        }
+      }
+      ++slot_loads;
+      return true;
+    };
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      Unit x = open_unit(p, order, first, part0, n_seqs, u);
+      ChunkPiece pc;
+      while (ok && x.cur.next(x.w, pc)) {
+        int32_t pages = load_pages(x, pc.j0);
+        const int tok0 = pc.item * x.w.item_tokens;
+        const int ntq = x.s.lq - tok0 > tile_tokens ? 2 : 1;
+        if (!wait_all(bar(C::kQEmpty), (q_loads & 1u) ^ 1u)) {
+          ok = false;
+          break;
+        }
+        if (lead) {
+          mbar_arrive_expect_tx(bar(C::kQFull), ntq * (D / 64) * tile_rows * 128);
+          for (int t = 0; t < ntq; ++t) {
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              tma_load_4d(sQ + t * C::kTileBytes + hf * C::kHalfBytes, &tm_q, bar(C::kQFull),
+                          hf * 64, 0, pc.head, x.s.q0 + tok0 + t * tile_tokens);
+          }
+        }
+        ++q_loads;
+        for (int j = pc.j0; j < pc.j1 && ok; ++j) {
+          const int32_t next = j + 1 < pc.j1 ? load_pages(x, j + 1) : -1;
+          ok = load_kv(&tm_k, pages, j, pc.head);
+          if (ok) ok = load_kv(&tm_v, pages, j, pc.head);
+          pages = next;
+        }
+      }
+    }
+    if (!ok) {
+      // give the copies already issued a bounded chance to land
+      for (uint32_t s = 0; s < C::kSlots && s < slot_loads; ++s) {
+        const uint32_t n = (slot_loads - s + C::kSlots - 1) / C::kSlots;  // loads into s
+        drain_wait(bar(C::kSlotFull + s), (n - 1) & 1u, kDrainLimit);
+      }
+      if (q_loads) drain_wait(bar(C::kQFull), (q_loads - 1) & 1u, kDrainLimit);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ================= MMA issuers: warp 1 for tile 0, warp 2 for tile 1 ====
+    // Each issuer walks the same pieces and ring slots; it issues its own
+    // tile's MMAs in the order S_0 | PV_0 S_1 | PV_1 S_2 ... and frees a slot
+    // (or the Q buffer) with one arrival on a two-arrival barrier: a commit
+    // once its MMAs reading the slot are done, or a plain arrive when its tile
+    // is absent from the item.  The whole warp runs the issuer, so every
+    // operand of an MMA is warp-uniform, and one elected lane issues.
+    const int t = warp - 1;
+    const bool lead = elect_one();
+    uint32_t q_uses = 0, slot_uses = 0, issued = 0, p_waits = 0;
+    bool ok = true;
+    auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
+      const bool w = bounded_wait(b, parity, abort_flag, p.status, kWaitLimit);
+      return __all_sync(0xffffffffu, w);
+    };
+    // next ring slot in consumption order, once its load has landed
+    auto wait_slot = [&](uint32_t &s) -> bool {
+      s = slot_uses % C::kSlots;
+      return wait_all(bar(C::kSlotFull + s), (slot_uses / C::kSlots) & 1u);
+    };
+    // (descriptors advance by adding the byte offset >> 4 to the start
+    // address field; every operand lies below 256 KB, so nothing carries)
+    const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024) + ((t * C::kTileBytes) >> 4);
+    const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
+    const uint64_t vdesc0 = sdesc_sw128(sRing, C::kVLbo, 1024);
+    const uint32_t d_s = tmem + C::kColS + t * kTile, d_o = tmem + C::kColO + t * D;
+    // S_t = Q_t K^T (both K-major, SBO = 8 rows x 128 B)
+    auto issue_s = [&](uint32_t slot) {
+      const uint64_t b0 = kdesc0 + ((slot * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::kHalfBytes + (kk & 3) * 32) >> 4;
+        if (lead) mma_ss(d_s, qdesc0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
+      }
+    };
+    // O_t += P_t V (P_t is in the first 64 columns of the S buffer)
+    auto issue_pv = [&](uint32_t slot, bool fresh) {
+      const uint64_t b0 = vdesc0 + ((slot * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk) {
+        if (lead)
+          mma_ts(d_o, d_s + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescO,
+                 (fresh && kk == 0) ? 0u : 1u);
+      }
+    };
+    // The two issuers take turns group by group (S0_0, S1_0, [PV0_0 S0_1],
+    // [PV1_0 S1_1], ...); each finishes its waits before taking the turn and
+    // commits after passing it on.
+    uint32_t turns = 0;
+    auto take_turn = [&]() -> bool {
+      const uint32_t parity = t == 0 ? ((turns & 1u) ^ 1u) : (turns & 1u);
+      return wait_all(bar(C::kTurn + t), parity);
+    };
+    auto pass_turn = [&]() {
+      ++turns;
+      if (lead) mbar_arrive(bar(C::kTurn + (1 - t)));
+    };
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      Unit x = open_unit(p, order, first, part0, n_seqs, u);
+      ChunkPiece pc;
+      while (ok && x.cur.next(x.w, pc)) {
+        const bool mine = x.s.lq - pc.item * x.w.item_tokens > t * tile_tokens;
+        const int last_tile = x.s.lk > 0 ? (x.s.lk - 1) / kTile : 0;   // holds the last key
+        // release a slot / the Q buffer: after this tile's MMAs, or at once
+        auto release = [&](uint32_t b) {
+          if (!lead) return;
+          if (mine)
+            mma_commit(b);
+          else
+            mbar_arrive(b);
+        };
+        if (!wait_all(bar(C::kQFull), q_uses & 1u)) {
+          ok = false;
+          break;
+        }
+        ++q_uses;
+        // prologue: S of the first key tile
+        uint32_t sk;
+        if (!wait_slot(sk) || !take_turn()) {
+          ok = false;
+          break;
+        }
+        if (mine) {
+          issue_s(sk);
+          issued = 1;
+        }
+        pass_turn();
+        if (mine && lead) mma_commit(bar(C::kSFull + t));
+        release(bar(C::kSlotEmpty + sk));
+        ++slot_uses;
+        if (pc.j1 - pc.j0 == 1) release(bar(C::kQEmpty));
+        for (int j = pc.j0; j < pc.j1 && ok; ++j) {
+          const bool more = j + 1 < pc.j1;
+          uint32_t sv, sk2 = 0;
+          if (!wait_slot(sv)) {
+            ok = false;
+            break;
+          }
+          ++slot_uses;
+          // V rows past the sequence's last key: P is 0 there, but 0 * Inf and
+          // 0 * NaN are NaN.  Tile 0's issuer runs for every item and issues
+          // its PV before tile 1's (the turn order), so it alone clears them.
+          if (t == 0 && j == last_tile) {
+            const int valid = x.s.lk - j * kTile;
+            if (valid < kTile)
+              zero_v_tail<D>(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
+          }
+          if (more && !wait_slot(sk2)) {
+            ok = false;
+            break;
+          }
+          // the issue turn first (the order is fixed, so holding it early
+          // blocks nobody), then P_j written by this tile's softmax
+          if (!take_turn()) {
+            ok = false;
+            break;
+          }
+          if (mine) {
+            if (!wait_all(bar(C::kPReady + t), p_waits & 1u)) {
+              ok = false;
+              break;
+            }
+            ++p_waits;
+            fence_after_sync();
+            // PV_j, then S_{j+1} (after the PV that reads P from the S buffer)
+            issue_pv(sv, j == pc.j0);
+            if (more) issue_s(sk2);
+          }
+          pass_turn();
+          if (mine && lead) mma_commit(more ? bar(C::kSFull + t) : bar(C::kOFull + t));
+          release(bar(C::kSlotEmpty + sv));
+          if (more) {
+            release(bar(C::kSlotEmpty + sk2));
+            ++slot_uses;
+            if (j + 2 == pc.j1) release(bar(C::kQEmpty));
+          }
+        }
+      }
+    }
+    // every MMA this thread issued has finished before TMEM is released
+    if (issued) {
+      if (lead) mma_commit(bar(C::kFinal + t));
+      drain_wait(bar(C::kFinal + t), 0, kWaitLimit);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax / correction / epilogue =================
+    // four warps to a tile; TMEM lane quadrant = warp % 4
+    const int t = (warp - C::kSoftmaxWarp) >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const int row_token = row / p.G;             // token of the row within its tile
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t colS = C::kColS + t * kTile;
+    const uint32_t colO = C::kColO + t * D;
+    const float sl2 = p.scale_log2;
+    const bool pos_scale = sl2 > 0.f;
+    const float mul = pos_scale ? sl2 : 1.f;
+    uint32_t s_waits = 0, o_waits = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      Unit x = open_unit(p, order, first, part0, n_seqs, u);
+      int4 join_a = make_int4(0, 0, 0, 0), join_b = join_a;   // no item is cut at this unit's end
+      ChunkPiece pc;
+      while (ok && x.cur.next(x.w, pc)) {
+        const int tok0 = pc.item * x.w.item_tokens;
+        const int tokens = min(x.w.item_tokens, x.s.lq - tok0);
+        if (pc.j0 == 0 && pc.j1 < pc.nk) {
+          // this unit begins the item, later units go on with it: how many
+          const int64_t after = pc.nk - pc.j1;
+          const int more = static_cast<int>((after + x.w.share - 1) / x.w.share);
+          join_a = make_int4(1 + more, static_cast<int>(x.part0) + (2 * x.local + 1) * x.part_rows,
+                             static_cast<int>(x.part0) + (2 * x.local + 2) * x.part_rows,
+                             2 * x.part_rows);
+          join_b = make_int4(tokens * p.G, x.s.q0 + tok0, pc.head, 0);
+        }
+        if (tokens <= t * tile_tokens) continue;   // tile absent: nothing issued for it
+        const int token = t * tile_tokens + row_token;
+        const bool store = row < tile_rows && token < tokens;
+        // keys that this row sees
+        int lim = x.s.lk;
+        if (p.causal) lim = min(lim, x.s.lk - x.s.lq + tok0 + token + 1);
+        float m = -INFINITY, l = 0.f;
+        for (int j = pc.j0; j < pc.j1; ++j) {
+          ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kWaitLimit);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ++s_waits;
+          fence_after_sync();
+          // all four 32-column loads in flight, then one wait
+          uint32_t sr[kTile];
+#pragma unroll
+          for (int c = 0; c < kTile / 32; ++c)
+            tmem_ld32(lane_base + colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_wait_ld();
+          // raw scores as pairs; with a positive scale the scale is folded
+          // into the exponent's FFMA, otherwise the scores are scaled first
+          float2 sc[kTile / 2];
+#pragma unroll
+          for (int c = 0; c < kTile / 2; ++c)
+            sc[c] = make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
+          if (!pos_scale) {
+            const float2 s2 = make_float2(sl2, sl2);
+#pragma unroll
+            for (int c = 0; c < kTile / 2; ++c) sc[c] = __fmul2_rn(sc[c], s2);
+          }
+          const int seen = lim - j * kTile;
+          if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+            for (int c = 0; c < kTile / 2; ++c) {
+              if (2 * c >= seen) sc[c].x = -INFINITY;
+              if (2 * c + 1 >= seen) sc[c].y = -INFINITY;
+            }
+          }
+          // row maximum: eight chains of 3-input max, fixed combine
+          float mx8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(sc[e].x, sc[e].y);
+#pragma unroll
+          for (int c = 8; c < kTile / 2; ++c) mx8[c & 7] = fmax3(mx8[c & 7], sc[c].x, sc[c].y);
+          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                 fmaxf(mx8[6], mx8[7])) * mul;
+          float alpha = 1.f;
+          bool rescale = false;
+          if (mx > m + kRescaleThreshold) {   // from -inf: any finite score
+            alpha = ex2(m - mx);
+            m = mx;
+            rescale = j > pc.j0;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-ref, -ref);
+          float2 sum8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum8[e] = make_float2(0.f, 0.f);
+          uint32_t pk[kTile / 2];
+#pragma unroll
+          for (int c = 0; c < kTile / 2; ++c) {
+            const float2 tt = __ffma2_rn(sc[c], mul2, negm2);
+            const float2 pp = make_float2(ex2(tt.x), ex2(tt.y));
+            sum8[c & 7] = __fadd2_rn(sum8[c & 7], pp);
+            pk[c] = pack_bf16x2(pp.x, pp.y);
+          }
+          const float2 s01 = __fadd2_rn(__fadd2_rn(sum8[0], sum8[1]), __fadd2_rn(sum8[2], sum8[3]));
+          const float2 s45 = __fadd2_rn(__fadd2_rn(sum8[4], sum8[5]), __fadd2_rn(sum8[6], sum8[7]));
+          const float2 s8 = __fadd2_rn(s01, s45);
+          l = l * alpha + (s8.x + s8.y);
+          // S_j complete implies the PV issued before it is complete: O is
+          // current and can be rescaled in place
+          if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(lane_base + colO + c * 32, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st32(lane_base + colO + c * 32, r);
+            }
+          }
+          // P over the first 64 columns of this tile's S buffer
+          {
+            uint32_t r[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = pk[e];
+            tmem_st32(lane_base + colS, r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = pk[32 + e];
+            tmem_st32(lane_base + colS + 32, r);
+          }
+          tmem_wait_st();
+          fence_before_sync();
+          mbar_arrive(bar(C::kPReady + t));
+        }
+        if (!ok) break;
+        // epilogue: wait for this tile's last PV, then store the valid rows
+        ok = bounded_wait(bar(C::kOFull + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++o_waits;
+        fence_after_sync();
+        const bool whole = pc.j0 == 0 && pc.j1 == pc.nk;
+        if (whole) {
+          // a row that sees no key: O and l are 0 (or NaN, if a score was)
+          const float inv = m == -INFINITY ? 0.f : 1.f / l;
+          __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(x.s.q0 + tok0 + token) * p.Hq +
+                                        pc.head * p.G + (row - row_token * p.G)) * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(lane_base + colO + c * 32, r);
+            tmem_wait_ld();
+            if (store) {
+              uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * e]) * inv,
+                                     __uint_as_float(r[8 * v + 2 * e + 1]) * inv);
+                d4[v] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+        } else {
+          const int64_t slot = x.part0 + static_cast<int64_t>(2 * x.local + (pc.j0 == 0)) * x.part_rows +
+                               t * tile_rows + row;
+          float4 *dst = reinterpret_cast<float4 *>(p.chunk_o + slot * D);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(lane_base + colO + c * 32, r);
+            tmem_wait_ld();
+            if (store) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                dst[c * 8 + v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                             __uint_as_float(r[4 * v + 2]),
+                                             __uint_as_float(r[4 * v + 3]));
+            }
+          }
+          if (store) p.chunk_ml[slot] = make_float2(m, l);
+        }
+      }
+      if (warp == C::kSoftmaxWarp && lane == 0 && ok && x.w.share > 0) {
+        int4 *join = p.chunk_join + 2 * (static_cast<int64_t>(cut0[x.at]) + x.local);
+        join[0] = join_a;
+        join[1] = join_b;
+      }
+    }
+  }
+
+  // ---- teardown -------------------------------------------------------------
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// Joins the parts of the items that shares cut: CTA (x, y) takes rows of the
+// item that share x begins and does not finish, a warp per row.  What the
+// chunk kernel noted is checked against the call before it is used, so that
+// a call that gave up (a wait that ran out) reads nothing out of place.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_chunk_join_kernel(const PagedAttnParams p) {
+  constexpr int E = D / 32;
+  griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= *p.chunk_n_cuts) return;
+  const int4 a = p.chunk_join[2 * static_cast<int64_t>(blockIdx.x)];
+  const int4 c = p.chunk_join[2 * static_cast<int64_t>(blockIdx.x) + 1];
+  const int parts = a.x, rows = c.x;
+  if (parts < 2 || parts > kChunkShares + 1 || rows < 1 || rows > 2 * kTile || a.y < 0 || a.z < 0 ||
+      a.w < 0 || a.y + static_cast<int64_t>(rows) > p.chunk_rows ||
+      a.z + static_cast<int64_t>(parts - 2) * a.w + rows > p.chunk_rows || c.y < 0 ||
+      c.y + static_cast<int64_t>(rows) / p.G > p.total_q || c.z < 0 || c.z >= p.c.Hkv)
+    return;
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
+       r += gridDim.y * (kJoinThreads / 32)) {
+    auto slot = [&](int n) -> int64_t {
+      return (n == 0 ? a.y : a.z + static_cast<int64_t>(n - 1) * a.w) + r;
+    };
+    float top = -INFINITY;
+    for (int n = 0; n < parts; ++n) top = fmaxf(top, p.chunk_ml[slot(n)].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float acc[E], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int n = 0; n < parts; ++n) {
+      const float2 v = p.chunk_ml[slot(n)];
+      const float f = ex2(v.x - ref);
+      sum += f * v.y;
+      const float *src = p.chunk_o + slot(n) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += f * src[e];
+    }
+    const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+    const int tok = r / p.G;
+    __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(c.y + tok) * p.Hq + c.z * p.G + (r - tok * p.G)) * D +
+                         lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+// q as (D, G, Hkv, tokens): a box is 64 columns of the group's heads of the
+// tokens of one tile; rows of a page as (D, Hkv, row, page): a box is 64
+// columns of one head's rows.  128-byte swizzle.
+bool make_map(CUtensorMap *map, const void *ptr, const cuuint64_t (&dims)[4],
+              const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kQuant>
+cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D, kQuant>;
+  CUtensorMap mq, mk, mv;
+  const cuuint64_t G = p.G, H = p.c.Hkv, d = D;
+  const cuuint64_t qdims[4] = {d, G, H, static_cast<cuuint64_t>(p.total_q)};
+  const cuuint64_t qstr[3] = {d * 2, G * d * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+  const cuuint32_t qbox[4] = {64, static_cast<cuuint32_t>(G), 1,
+                              static_cast<cuuint32_t>(kTile / p.G)};
+  const cuuint64_t cdims[4] = {d, H, cuuint64_t{1} << p.c.page_shift,
+                               static_cast<cuuint64_t>(p.c.num_pages)};
+  const cuuint64_t cstr[3] = {d * 2, H * d * 2, static_cast<cuuint64_t>(p.c.page_stride) * 2};
+  const int page = 1 << p.c.page_shift;
+  const cuuint32_t cbox[4] = {64, 1, static_cast<cuuint32_t>(page < kTile ? page : kTile), 1};
+  if (!make_map(&mq, p.q, qdims, qstr, qbox) || !make_map(&mk, p.c.k, cdims, cstr, cbox) ||
+      !make_map(&mv, p.c.v, cdims, cstr, cbox))
+    return cudaErrorInvalidValue;
+  static unsigned long long configured = 0;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_chunk_kernel<D, kQuant>),
+                                C::kSmemBytes, configured);
+  if (e != cudaSuccess) return e;
+  paged_chunk_kernel<D, kQuant><<<num_sms, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.chunk_cuts == 0) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.chunk_cuts, 4);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_chunk_join_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
+                               cudaStream_t stream) {
+  if (quant) return cudaErrorNotSupported;
+  return p.c.D == 128 ? launch<128, false>(p, num_sms, stream)
+                      : launch<64, false>(p, num_sms, stream);
+}
+
+}  // namespace pa
