@@ -1,9 +1,9 @@
 // Attention of packed new tokens over a paged K/V cache: the entry point.
 //
-// Simplest form: one warp per (token, query head), an online softmax over the
-// keys one at a time.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+// Sequences of few query rows are bound by the cache's bytes and take the
+// streaming kernel (paged_decode.cu), longer ones by tensor operations and
+// take the tiled one (paged_chunk.cu); a mixed batch launches both, and each
+// skips the other's sequences.
 #include <math.h>
 
 #include "internal.h"
@@ -13,82 +13,6 @@
 
 namespace pa {
 namespace {
-
-constexpr int kThreads = 256;
-
-template <bool kQuant, int D>
-__global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const PagedAttnParams p) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  int err;
-  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
-  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
-  if (err) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.status, err);
-    return;
-  }
-  if (s.lq <= kDecodeRows / p.G) return;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int i = static_cast<int>(item / p.Hq), h = static_cast<int>(item - static_cast<int64_t>(i) * p.Hq);
-  if (i >= s.lq) return;
-  const int hk = h / (p.Hq / p.c.Hkv);
-  const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.table_pages;
-  float q[E], o[E];
-  const __nv_bfloat16 *qr = p.q + (s.q0 + i) * p.q_stride + static_cast<int64_t>(h) * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(qr[e]);
-    o[e] = 0.f;
-  }
-  const int n = p.causal ? min(s.lk, s.lk - s.lq + i + 1) : s.lk;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    const int32_t page = __ldg(table + (j >> p.c.page_shift));
-    const int row = j & ((1 << p.c.page_shift) - 1);
-    const bool good = page_ok(p.c, page);
-    if (!good) record_error(p.status, PA_DEVICE_ERR_PAGE);
-    const int64_t at = row_offset(p.c, good ? page : 0, row, hk) + lane * E;
-    float k[E], v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-    if (good) {
-      if constexpr (kQuant) {
-        const int64_t xo = exp_offset(p.c, page, row, hk);
-        const float ks = row_scale(p.c.k_exp[xo]), vs = row_scale(p.c.v_exp[xo]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          __half_raw kr = __nv_cvt_fp8_to_halfraw(static_cast<uint8_t *>(p.c.k)[at + e], __NV_E4M3);
-          __half_raw vr = __nv_cvt_fp8_to_halfraw(static_cast<uint8_t *>(p.c.v)[at + e], __NV_E4M3);
-          k[e] = __half2float(__half(kr)) * ks;
-          v[e] = __half2float(__half(vr)) * vs;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          k[e] = __bfloat162float(static_cast<__nv_bfloat16 *>(p.c.k)[at + e]);
-          v[e] = __bfloat162float(static_cast<__nv_bfloat16 *>(p.c.v)[at + e]);
-        }
-      }
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x += q[e] * k[e];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= p.scale_log2;
-    const float mn = fmaxf(m, x);
-    const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
-    const float w = mn == -INFINITY ? 0.f : exp2f(x - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * v[e];
-  }
-  __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(s.q0 + i) * p.Hq + h) * D + lane * E;
-  const float inv = n > 0 ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(n > 0 ? o[e] * inv : 0.f);
-}
 
 // Where the partial results lie in the workspace.
 struct WorkspacePlan {
@@ -225,18 +149,5 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
     if (e != cudaSuccess) return from_cuda(e);
   }
   if (max_q <= kDecodeRows / p.G) return PA_OK;
-  if (!quant) return from_cuda(launch_paged_chunk(p, quant, sms, s));
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_q) * Hq + 7) / 8), batch);
-  if (quant) {
-    if (D == 128)
-      paged_attn_simple_kernel<true, 128><<<grid, kThreads, 0, s>>>(p);
-    else
-      paged_attn_simple_kernel<true, 64><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (D == 128)
-      paged_attn_simple_kernel<false, 128><<<grid, kThreads, 0, s>>>(p);
-    else
-      paged_attn_simple_kernel<false, 64><<<grid, kThreads, 0, s>>>(p);
-  }
-  return from_cuda(cudaGetLastError());
+  return from_cuda(launch_paged_chunk(p, quant, sms, s));
 }

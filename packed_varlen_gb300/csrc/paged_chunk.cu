@@ -14,6 +14,8 @@
 //                from an out-of-range page, so they land as zeros.
 //   warps 1, 2   issue tile 0's and tile 1's tcgen05.mma in turn.
 //   warps 3..6   softmax of tile 0, a thread per row; warps 7..10 of tile 1.
+//   warps 11..18 (8-bit caches) widen the rows that the producer fetched into
+//                the bf16 tiles that the products read.
 // A unit of work is whole items or a share of the sequence's key tiles
 // (paged_chunk_work.cuh); a part of an item leaves its unnormalised output,
 // maximum and sum in the workspace, and paged_chunk_join_kernel joins them.
@@ -46,17 +48,26 @@ constexpr float kRescaleThreshold = 8.0f;       // log2 units
 template <int D, bool kQuant>
 struct Cfg {
   static constexpr int kSoftmaxWarp = 3;                    // first of eight
-  static constexpr int kThreads = (kSoftmaxWarp + 8) * 32;
-  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kWidenWarp = kSoftmaxWarp + 8;       // first of kWideners (8-bit caches)
+  static constexpr int kWideners = 8;
+  static constexpr int kThreads = (kWidenWarp + (kQuant ? kWideners : 0)) * 32;
+  // columns of S that a softmax thread holds at a time: what the registers of
+  // 352 or 608 threads allow
+  static constexpr int kCols = kQuant ? 32 : 64;
+  static constexpr int kSlots = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+  static constexpr int kRaws = kQuant ? kSlots : 0;         // 8-bit tiles as they arrive
+  static constexpr int kRawBytes = kTile * D;
   static constexpr int kHalfBytes = kTile * 64 * 2;         // 128 rows x 128 B
   static constexpr int kTileBytes = kTile * D * 2;          // one Q/K/V tile
   static constexpr int kQOff = 0;                           // Q0, Q1
   static constexpr int kRingOff = 2 * kTileBytes;
-  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
   // barriers: per Q tile t an S-full, a P-ready and an O-full barrier
   static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
-                       kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots;
-  static constexpr int kNumBars = 12 + 2 * kSlots;
+                       kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots,
+                       kRawFull = 12 + 2 * kSlots, kRawEmpty = kRawFull + kRaws;
+  static constexpr int kNumBars = 12 + 2 * kSlots + 2 * kRaws;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag, counter
   static constexpr int kSchedOff = (kMiscOff + 16 + 127) / 128 * 128;
   // order, first part row, first cut unit and first unit of each sequence in the list
@@ -88,6 +99,25 @@ __device__ __forceinline__ void zero_v_tail(uint8_t *tile, int valid, int lane) 
   }
   fence_proxy_async();
   __syncwarp();
+}
+
+// Loads that are issued where they are written, ahead of their use (a plain
+// __ldg may be moved down to it).
+__device__ __forceinline__ int32_t load_now(const int32_t *p) {
+  int32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int load_now(const uint8_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return static_cast<int>(v);
+}
+
+// Two e4m3 bytes of w, as `sel` puts them in bytes 1 and 3, to bf16 times
+// 2^-120, times the row's scale.
+__device__ __forceinline__ uint32_t widen_pair(uint32_t w, uint32_t scale, uint32_t sel) {
+  return mul_bf16x2(odd_bytes(__byte_perm(w, 0u, sel)), scale);
 }
 
 // The sequences of the call that take this kernel, most keys first, with the
@@ -172,15 +202,16 @@ struct Unit {
   ChunkWork w;
   ChunkCursor cur;
 };
-__device__ __forceinline__ Unit open_unit(const PagedAttnParams &p, const int32_t *order,
-                                          const int32_t *first, const int32_t *part0, int n,
-                                          int u) {
-  int lo = 0, hi = n;   // largest x < n with first[x] <= u (every sequence has a unit)
+// Not inlined: five roles would each fetch their own copy of code that runs
+// once a unit, and instruction fetch is what it costs.
+__device__ __noinline__ void open_unit(const PagedAttnParams &p, const int32_t *order,
+                                       const int32_t *first, const int32_t *part0, int n, int u,
+                                       Unit &x) {
+  int lo = 0, hi = n;   // largest i < n with first[i] <= u (every sequence has a unit)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= u) lo = mid; else hi = mid;
   }
-  Unit x;
   x.b = order[lo];
   int err;
   x.s = paged_seq(p.cu_q, p.seq_lens, x.b, p.total_q, p.max_q, p.max_k,
@@ -191,7 +222,6 @@ __device__ __forceinline__ Unit open_unit(const PagedAttnParams &p, const int32_
   x.part_rows = chunk_part_rows(x.s.lq, p.G);
   x.w = chunk_work(x.s.lq, x.s.lk, p.causal, p.G, p.c.Hkv);
   x.cur.start(x.w, x.local, p.c.Hkv);
-  return x;
 }
 
 template <int D, bool kQuant>
@@ -233,8 +263,12 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       mbar_init(bar(C::kTurn + t), 1);
     }
     for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(bar(C::kSlotFull + s), 1);
+      mbar_init(bar(C::kSlotFull + s), kQuant ? C::kWideners : 1);   // the widening warps, or the copy
       mbar_init(bar(C::kSlotEmpty + s), 2);   // one arrival per MMA issuer
+    }
+    for (int s = 0; s < C::kRaws; ++s) {
+      mbar_init(bar(C::kRawFull + s), 1);
+      mbar_init(bar(C::kRawEmpty + s), C::kWideners);
     }
     *abort_flag = 0;
     *counter = 0;
@@ -256,6 +290,12 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
 
   if (warp == 0) {
     // ================= TMA producer =================
+    // fills K/V slots, or (8-bit caches) the buffers that the widening warps read
+    constexpr int kBufs = kQuant ? C::kRaws : C::kSlots;
+    constexpr int kFull = kQuant ? C::kRawFull : C::kSlotFull;
+    constexpr int kEmpty = kQuant ? C::kRawEmpty : C::kSlotEmpty;
+    constexpr int kBufBytes = kQuant ? C::kRawBytes : C::kTileBytes;
+    const uint32_t sBuf = base + (kQuant ? C::kRawOff : C::kRingOff);
     const bool lead = elect_one();
     if (lead) {
       tma_prefetch_desc(&tm_q);
@@ -274,8 +314,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     auto load_pages = [&](const Unit &x, int j) -> int32_t {
       const int64_t key = static_cast<int64_t>(j) * kTile + lane * box_rows;
       if (lane >= boxes || key >= x.s.lk) return -1;
-      const int32_t page =
-          __ldg(p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages + (key >> p.c.page_shift));
+      const int32_t page = load_now(p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages +
+                                    (key >> p.c.page_shift));
       if (!page_ok(p.c, page)) {
         record_error(p.status, PA_DEVICE_ERR_PAGE);
         return -1;
@@ -283,26 +323,29 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       return page;
     };
     auto load_kv = [&](const CUtensorMap *tm, int32_t pages, int j, int head) -> bool {
-      const uint32_t s = slot_loads % C::kSlots;
-      const uint32_t use = slot_loads / C::kSlots;
-      if (!wait_all(bar(C::kSlotEmpty + s), (use & 1u) ^ 1u)) return false;
-      const uint32_t dst = sRing + s * C::kTileBytes;
-      if (lead) mbar_arrive_expect_tx(bar(C::kSlotFull + s), C::kTileBytes);
+      const uint32_t s = slot_loads % kBufs;
+      const uint32_t use = slot_loads / kBufs;
+      if (!wait_all(bar(kEmpty + s), (use & 1u) ^ 1u)) return false;
+      const uint32_t dst = sBuf + s * kBufBytes;
+      if (lead) mbar_arrive_expect_tx(bar(kFull + s), kBufBytes);
       const int row = (j * kTile) & page_mask;   // not 0 only where a page spans several tiles
       for (int x = 0; x < boxes; ++x) {
         const int32_t page = __shfl_sync(0xffffffffu, pages, x);
-        if (lead) {
+        if (kQuant) {
+          if (lead) tma_load_4d(dst + x * box_rows * D, tm, bar(kFull + s), 0, head, row, page);
+        } else if (lead) {
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_4d(dst + hf * C::kHalfBytes + x * box_rows * 128, tm, bar(C::kSlotFull + s),
-                        hf * 64, head, row, page);
+            tma_load_4d(dst + hf * C::kHalfBytes + x * box_rows * 128, tm, bar(kFull + s), hf * 64,
+                        head, row, page);
         }
       }
       ++slot_loads;
       return true;
     };
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      Unit x = open_unit(p, order, first, part0, n_seqs, u);
+      Unit x;
+      open_unit(p, order, first, part0, n_seqs, u, x);
       ChunkPiece pc;
       while (ok && x.cur.next(x.w, pc)) {
         int32_t pages = load_pages(x, pc.j0);
@@ -332,9 +375,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     }
     if (!ok) {
       // give the copies already issued a bounded chance to land
-      for (uint32_t s = 0; s < C::kSlots && s < slot_loads; ++s) {
-        const uint32_t n = (slot_loads - s + C::kSlots - 1) / C::kSlots;  // loads into s
-        drain_wait(bar(C::kSlotFull + s), (n - 1) & 1u, kDrainLimit);
+      for (uint32_t s = 0; s < kBufs && s < slot_loads; ++s) {
+        const uint32_t n = (slot_loads - s + kBufs - 1) / kBufs;  // loads into s
+        drain_wait(bar(kFull + s), (n - 1) & 1u, kDrainLimit);
       }
       if (q_loads) drain_wait(bar(C::kQFull), (q_loads - 1) & 1u, kDrainLimit);
     }
@@ -397,7 +440,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       if (lead) mbar_arrive(bar(C::kTurn + (1 - t)));
     };
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      Unit x = open_unit(p, order, first, part0, n_seqs, u);
+      Unit x;
+      open_unit(p, order, first, part0, n_seqs, u, x);
       ChunkPiece pc;
       while (ok && x.cur.next(x.w, pc)) {
         const bool mine = x.s.lq - pc.item * x.w.item_tokens > t * tile_tokens;
@@ -441,7 +485,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           // V rows past the sequence's last key: P is 0 there, but 0 * Inf and
           // 0 * NaN are NaN.  Tile 0's issuer runs for every item and issues
           // its PV before tile 1's (the turn order), so it alone clears them.
-          if (t == 0 && j == last_tile) {
+          // (Widened V tiles come with those rows as zeros.)
+          if (!kQuant && t == 0 && j == last_tile) {
             const int valid = x.s.lk - j * kTile;
             if (valid < kTile)
               zero_v_tail<D>(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
@@ -484,7 +529,100 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       drain_wait(bar(C::kFinal + t), 0, kWaitLimit);
     }
     __syncwarp();
-  } else {
+  } else if (kQuant && warp >= C::kWidenWarp) {
+    // ================= 8-bit rows to bf16 =================
+    // Eight warps, 16 rows of a tile each: a lane takes 16 bytes of a row at a
+    // time, widens them with the row's scale (lane x holds that of K's row x,
+    // lane 16 + x of V's) and stores two 16-byte chunks of the swizzled bf16 tile.  Lanes of the second
+    // column half store their odd chunk first, so the eight lanes of a row
+    // never meet in a bank.
+    if constexpr (kQuant) {
+      constexpr int kRowLanes = D / 16, kPass = 32 / kRowLanes;   // rows of a warp-wide load
+      constexpr int kRows = kTile / C::kWideners, kPasses = kRows / kPass;
+      static_assert(kRows == 16, "a lane holds one exponent");
+      const int w = warp - C::kWidenWarp;
+      const int sub = lane / kRowLanes, col = lane % kRowLanes;   // 16 columns from col * 16
+      const int hf = col >> 2, chunk = (col & 3) * 2;
+      uint32_t n = 0;
+      bool ok = true;
+      auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
+        const bool x = bounded_wait(b, parity, abort_flag, p.status, kWaitLimit);
+        return __all_sync(0xffffffffu, x);
+      };
+      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+        Unit x;
+      open_unit(p, order, first, part0, n_seqs, u, x);
+        const int32_t *table = p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages;
+        ChunkPiece pc;
+        while (ok && x.cur.next(x.w, pc)) {
+          // this lane's row of key tile j: its page, then its exponent byte
+          const int my_row = w * kRows + (lane & 15);
+          const uint8_t *exps = lane < 16 ? p.c.k_exp : p.c.v_exp;
+          auto load_page = [&](int j) -> int32_t {
+            const int64_t key = static_cast<int64_t>(j) * kTile + my_row;
+            return j < pc.j1 && key < x.s.lk ? load_now(table + (key >> p.c.page_shift)) : -1;
+          };
+          auto load_exp = [&](int j, int32_t page) -> int {
+            if (!page_ok(p.c, page)) return -1;   // no such row: scale 0
+            const int row = (j * kTile + my_row) & ((1 << p.c.page_shift) - 1);
+            return load_now(exps + exp_offset(p.c, page, row, pc.head));
+          };
+          int32_t page = load_page(pc.j0);
+          int byte = load_exp(pc.j0, page);
+          page = load_page(pc.j0 + 1);
+          for (int j = pc.j0; j < pc.j1 && ok; ++j) {
+            const int byte_next = load_exp(j + 1, page);
+            page = load_page(j + 2);
+            const uint32_t scale = byte < 0 ? 0u : widen_scale(byte) * 0x10001u;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+              const uint32_t r = n % C::kRaws, s = n % C::kSlots;
+              if (!wait_all(bar(C::kRawFull + r), (n / C::kRaws) & 1u)) {
+                ok = false;
+                break;
+              }
+              // all loads in flight before the first store
+              const uint8_t *raw = gbase + C::kRawOff + r * C::kRawBytes + w * kRows * D + lane * 16;
+              uint4 y[kPasses];
+              uint32_t sc[kPasses];
+#pragma unroll
+              for (int i = 0; i < kPasses; ++i) y[i] = *reinterpret_cast<const uint4 *>(raw + i * 512);
+#pragma unroll
+              for (int i = 0; i < kPasses; ++i)
+                sc[i] = __shfl_sync(0xffffffffu, scale, kv * 16 + i * kPass + sub);
+              if (!wait_all(bar(C::kSlotEmpty + s), ((n / C::kSlots) & 1u) ^ 1u)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) mbar_arrive(bar(C::kRawEmpty + r));   // every lane has its bytes
+              uint8_t *tile = gbase + C::kRingOff + s * C::kTileBytes + hf * C::kHalfBytes;
+#pragma unroll
+              for (int i = 0; i < kPasses; ++i) {
+                const int row = i * kPass + sub;
+                uint4 a, c;
+                a.x = widen_pair(y[i].x, sc[i], 0x1100);
+                a.y = widen_pair(y[i].x, sc[i], 0x3322);
+                a.z = widen_pair(y[i].y, sc[i], 0x1100);
+                a.w = widen_pair(y[i].y, sc[i], 0x3322);
+                c.x = widen_pair(y[i].z, sc[i], 0x1100);
+                c.y = widen_pair(y[i].z, sc[i], 0x3322);
+                c.z = widen_pair(y[i].w, sc[i], 0x1100);
+                c.w = widen_pair(y[i].w, sc[i], 0x3322);
+                uint8_t *dst = tile + (w * kRows + row) * 128;
+                const int even = ((chunk ^ (row & 7)) * 16), odd = (((chunk + 1) ^ (row & 7)) * 16);
+                *reinterpret_cast<uint4 *>(dst + (hf ? odd : even)) = hf ? c : a;
+                *reinterpret_cast<uint4 *>(dst + (hf ? even : odd)) = hf ? a : c;
+              }
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::kSlotFull + s));
+            }
+            byte = byte_next;
+          }
+        }
+      }
+    }
+  } else if (warp >= C::kSoftmaxWarp) {
     // ================= softmax / correction / epilogue =================
     // four warps to a tile; TMEM lane quadrant = warp % 4
     const int t = (warp - C::kSoftmaxWarp) >> 2;
@@ -500,16 +638,16 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     uint32_t s_waits = 0, o_waits = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      Unit x = open_unit(p, order, first, part0, n_seqs, u);
+      Unit x;
+      open_unit(p, order, first, part0, n_seqs, u, x);
       int4 join_a = make_int4(0, 0, 0, 0), join_b = join_a;   // no item is cut at this unit's end
       ChunkPiece pc;
       while (ok && x.cur.next(x.w, pc)) {
         const int tok0 = pc.item * x.w.item_tokens;
         const int tokens = min(x.w.item_tokens, x.s.lq - tok0);
         if (pc.j0 == 0 && pc.j1 < pc.nk) {
-          // this unit begins the item, later units go on with it: how many
-          const int64_t after = pc.nk - pc.j1;
-          const int more = static_cast<int>((after + x.w.share - 1) / x.w.share);
+          // this share begins the item, later ones go on with it: how many
+          const int more = x.w.shares_after(x.local, pc.head, pc.item);
           join_a = make_int4(1 + more, static_cast<int>(x.part0) + (2 * x.local + 1) * x.part_rows,
                              static_cast<int>(x.part0) + (2 * x.local + 2) * x.part_rows,
                              2 * x.part_rows);
@@ -530,39 +668,46 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
           ++s_waits;
           fence_after_sync();
-          // all four 32-column loads in flight, then one wait
-          uint32_t sr[kTile];
-#pragma unroll
-          for (int c = 0; c < kTile / 32; ++c)
-            tmem_ld32(lane_base + colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          tmem_wait_ld();
-          // raw scores as pairs; with a positive scale the scale is folded
-          // into the exponent's FFMA, otherwise the scores are scaled first
-          float2 sc[kTile / 2];
-#pragma unroll
-          for (int c = 0; c < kTile / 2; ++c)
-            sc[c] = make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
-          if (!pos_scale) {
-            const float2 s2 = make_float2(sl2, sl2);
-#pragma unroll
-            for (int c = 0; c < kTile / 2; ++c) sc[c] = __fmul2_rn(sc[c], s2);
-          }
+          // The row is read twice, kCols columns at a time: for its maximum,
+          // then for the weights.  Holding all of it would cost 128 registers.
           const int seen = lim - j * kTile;
-          if (__any_sync(0xffffffffu, seen < kTile)) {
+          const bool masked = __any_sync(0xffffffffu, seen < kTile);
+          constexpr int kPairs = C::kCols / 2;
+          float2 sc[kPairs];
+          auto read_part = [&](int h) {
+            uint32_t r[C::kCols];
 #pragma unroll
-            for (int c = 0; c < kTile / 2; ++c) {
-              if (2 * c >= seen) sc[c].x = -INFINITY;
-              if (2 * c + 1 >= seen) sc[c].y = -INFINITY;
+            for (int c = 0; c < C::kCols; c += 32)
+              tmem_ld32(lane_base + colS + h * C::kCols + c,
+                        *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kPairs; ++c)
+              sc[c] = make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+            // with a positive scale the scale is folded into the exponent's
+            // FFMA, otherwise the scores are scaled first
+            if (!pos_scale) {
+              const float2 s2 = make_float2(sl2, sl2);
+#pragma unroll
+              for (int c = 0; c < kPairs; ++c) sc[c] = __fmul2_rn(sc[c], s2);
             }
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < kPairs; ++c) {
+                if (h * C::kCols + 2 * c >= seen) sc[c].x = -INFINITY;
+                if (h * C::kCols + 2 * c + 1 >= seen) sc[c].y = -INFINITY;
+              }
+            }
+          };
+          // row maximum: four chains of 3-input max, fixed combine
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = 0; h < kTile / C::kCols; ++h) {
+            read_part(h);
+#pragma unroll
+            for (int c = 0; c < kPairs; ++c) mx4[c & 3] = fmax3(mx4[c & 3], sc[c].x, sc[c].y);
           }
-          // row maximum: eight chains of 3-input max, fixed combine
-          float mx8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(sc[e].x, sc[e].y);
-#pragma unroll
-          for (int c = 8; c < kTile / 2; ++c) mx8[c & 7] = fmax3(mx8[c & 7], sc[c].x, sc[c].y);
-          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                 fmaxf(mx8[6], mx8[7])) * mul;
+          const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * mul;
           float alpha = 1.f;
           bool rescale = false;
           if (mx > m + kRescaleThreshold) {   // from -inf: any finite score
@@ -572,21 +717,27 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-ref, -ref);
-          float2 sum8[8];
+          float2 sum4[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum8[e] = make_float2(0.f, 0.f);
-          uint32_t pk[kTile / 2];
+          for (int e = 0; e < 4; ++e) sum4[e] = make_float2(0.f, 0.f);
+          // P over the first 64 columns of the S buffer: a part's weights take
+          // columns that have been read already
+#pragma unroll 1
+          for (int h = 0; h < kTile / C::kCols; ++h) {
+            read_part(h);
+            uint32_t pk[kPairs];
 #pragma unroll
-          for (int c = 0; c < kTile / 2; ++c) {
-            const float2 tt = __ffma2_rn(sc[c], mul2, negm2);
-            const float2 pp = make_float2(ex2(tt.x), ex2(tt.y));
-            sum8[c & 7] = __fadd2_rn(sum8[c & 7], pp);
-            pk[c] = pack_bf16x2(pp.x, pp.y);
+            for (int c = 0; c < kPairs; ++c) {
+              const float2 tt = __ffma2_rn(sc[c], mul2, negm2);
+              const float2 pp = make_float2(ex2(tt.x), ex2(tt.y));
+              sum4[c & 3] = __fadd2_rn(sum4[c & 3], pp);
+              pk[c] = pack_bf16x2(pp.x, pp.y);
+            }
+#pragma unroll
+            for (int c = 0; c < kPairs; c += 16) tmem_st16(lane_base + colS + h * kPairs + c, pk + c);
           }
-          const float2 s01 = __fadd2_rn(__fadd2_rn(sum8[0], sum8[1]), __fadd2_rn(sum8[2], sum8[3]));
-          const float2 s45 = __fadd2_rn(__fadd2_rn(sum8[4], sum8[5]), __fadd2_rn(sum8[6], sum8[7]));
-          const float2 s8 = __fadd2_rn(s01, s45);
-          l = l * alpha + (s8.x + s8.y);
+          const float2 s4 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
+          l = l * alpha + (s4.x + s4.y);
           // S_j complete implies the PV issued before it is complete: O is
           // current and can be rescaled in place
           if (__any_sync(0xffffffffu, rescale)) {
@@ -599,16 +750,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
               for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
               tmem_st32(lane_base + colO + c * 32, r);
             }
-          }
-          // P over the first 64 columns of this tile's S buffer
-          {
-            uint32_t r[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = pk[e];
-            tmem_st32(lane_base + colS, r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = pk[32 + e];
-            tmem_st32(lane_base + colS + 32, r);
           }
           tmem_wait_st();
           fence_before_sync();
@@ -733,13 +874,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_chunk_join_kernel(const Pa
 // q as (D, G, Hkv, tokens): a box is 64 columns of the group's heads of the
 // tokens of one tile; rows of a page as (D, Hkv, row, page): a box is 64
 // columns of one head's rows.  128-byte swizzle.
-bool make_map(CUtensorMap *map, const void *ptr, const cuuint64_t (&dims)[4],
+// Rows of an 8-bit page come whole, unswizzled.
+bool make_map(CUtensorMap *map, bool bytes, const void *ptr, const cuuint64_t (&dims)[4],
               const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -755,11 +898,13 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
                               static_cast<cuuint32_t>(kTile / p.G)};
   const cuuint64_t cdims[4] = {d, H, cuuint64_t{1} << p.c.page_shift,
                                static_cast<cuuint64_t>(p.c.num_pages)};
-  const cuuint64_t cstr[3] = {d * 2, H * d * 2, static_cast<cuuint64_t>(p.c.page_stride) * 2};
+  const cuuint64_t es = kQuant ? 1 : 2;
+  const cuuint64_t cstr[3] = {d * es, H * d * es, static_cast<cuuint64_t>(p.c.page_stride) * es};
   const int page = 1 << p.c.page_shift;
-  const cuuint32_t cbox[4] = {64, 1, static_cast<cuuint32_t>(page < kTile ? page : kTile), 1};
-  if (!make_map(&mq, p.q, qdims, qstr, qbox) || !make_map(&mk, p.c.k, cdims, cstr, cbox) ||
-      !make_map(&mv, p.c.v, cdims, cstr, cbox))
+  const cuuint32_t cbox[4] = {kQuant ? D : 64, 1, static_cast<cuuint32_t>(page < kTile ? page : kTile), 1};
+  if (!make_map(&mq, false, p.q, qdims, qstr, qbox) ||
+      !make_map(&mk, kQuant, p.c.k, cdims, cstr, cbox) ||
+      !make_map(&mv, kQuant, p.c.v, cdims, cstr, cbox))
     return cudaErrorInvalidValue;
   static unsigned long long configured = 0;
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_chunk_kernel<D, kQuant>),
@@ -784,7 +929,9 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
                                cudaStream_t stream) {
-  if (quant) return cudaErrorNotSupported;
+  if (quant)
+    return p.c.D == 128 ? launch<128, true>(p, num_sms, stream)
+                        : launch<64, true>(p, num_sms, stream);
   return p.c.D == 128 ? launch<128, false>(p, num_sms, stream)
                       : launch<64, false>(p, num_sms, stream);
 }

@@ -7,14 +7,17 @@
 // one CTA takes at a time:
 //  - whole items, heaviest first, where a sequence has many of them or few
 //    keys;
-//  - else an equal share of the sequence's key tiles, items laid end to end
-//    (heads in order, then tiles): a share starts and ends in the middle of
-//    an item, at most two of its pieces are parts of items, and those go
-//    through the workspace.
+//  - else an equal share of the sequence's keys, items laid end to end (heads
+//    in order, then tiles): a share starts and ends in the middle of an item,
+//    at most two of its pieces are parts of items, and those go through the
+//    workspace.  Shares are cut in keys rather than in key tiles, which keeps
+//    the sum over the items before a place a quadratic, and rounded down to a
+//    tile where they meet an item (at most one tile in six or more).
 // The choice looks at the sequence alone, as if it had the GPU (152 CTAs) to
 // itself, so its bits do not depend on the batch.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 namespace pa {
@@ -24,60 +27,82 @@ constexpr int kChunkShares = 152;    // shares of a lone sequence
 constexpr int kChunkMinShare = 6;    // key tiles of the smallest share
 constexpr int kChunkManyItems = 6 * kChunkShares;
 
-// sum of floor((a i + b) / m) for i in [0, n), by the Euclidean descent on (a, m)
-__host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
-  while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t top = a * n + b;
-    if (top < m) break;
-    n = top / m;
-    b = top % m;
-    const int64_t x = m;
-    m = a;
-    a = x;
-  }
-  return sum;
+// x / y for x, y >= 0, in 32 bits where they fit.
+__host__ __device__ inline int64_t quotient(int64_t x, int64_t y) {
+  if (x < (int64_t{1} << 31) && y < (int64_t{1} << 31))
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
+
+// Key tile j of item `item` of head `head`: where a unit starts or ends.
+struct ChunkPlace {
+  int head, item, j;
+};
 
 struct ChunkWork {
   int lq, lk, causal, item_tokens, items_head;   // items of one K/V head
-  int nk_last;                                   // key tiles of the last (heaviest) item
-  int64_t head_tiles;                            // key tiles of all items of a head
-  int64_t share;                                 // key tiles of a share; 0: whole items
+  int few;             // leading items whose queries see at most one tile of keys
+  int64_t head_keys;   // keys of all items of a head
+  int64_t share;       // keys of a share; 0: whole items
   int units;
 
-  // Key tiles of item i: at least one, so that rows that see nothing are written too.
-  __host__ __device__ int tiles_of(int i) const {
+  // Keys that item i reads: at least a tile's, so that rows that see nothing are written too.
+  __host__ __device__ int keys_of(int i) const {
     int64_t keys = lk;
     if (causal) {
       const int64_t last = static_cast<int64_t>(lk) - lq + static_cast<int64_t>(i + 1) * item_tokens;
       keys = last < keys ? last : keys;
     }
-    return keys <= kChunkTile ? 1 : static_cast<int>((keys + kChunkTile - 1) / kChunkTile);
+    return keys < kChunkTile ? kChunkTile : static_cast<int>(keys);
   }
-  // Key tiles of items [0, i) of a head.
-  __host__ __device__ int64_t tiles_before(int i) const {
-    if (!causal) return static_cast<int64_t>(i) * nk_last;
-    if (i <= 0) return 0;
-    if (i >= items_head) return tiles_before(items_head - 1) + nk_last;
-    const int64_t first = static_cast<int64_t>(lk) - lq;     // keys before the chunk
-    int64_t blind = first < 0 ? -first / item_tokens : 0;    // items that see no key count one
-    if (blind > i) blind = i;
-    return blind + floor_sum(i - blind, kChunkTile, item_tokens,
-                             first + (blind + 1) * item_tokens + kChunkTile - 1);
+  __host__ __device__ int tiles_of(int i) const {
+    return (keys_of(i) - 1) / kChunkTile + 1;
   }
-  // Item that holds key tile `pos` of a head.
+  // Keys of items [0, i) of a head, i < items_head.
+  __host__ __device__ int64_t keys_before(int i) const {
+    if (!causal) return static_cast<int64_t>(i) * keys_of(0);
+    if (i <= few) return static_cast<int64_t>(i) * kChunkTile;
+    const int64_t n = i - few;   // items few .. i - 1: first, first + item_tokens, ...
+    const int64_t first = static_cast<int64_t>(lk) - lq + static_cast<int64_t>(few + 1) * item_tokens;
+    return static_cast<int64_t>(few) * kChunkTile + n * first + n * (n - 1) / 2 * item_tokens;
+  }
+  // Item that holds key `pos` of a head's items laid end to end.
   __host__ __device__ int item_at(int64_t pos) const {
-    if (!causal) return static_cast<int>(pos / nk_last);
-    int lo = 0, hi = items_head;
-    while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;
-      if (tiles_before(mid) <= pos) lo = mid; else hi = mid;
+    if (!causal) return static_cast<int>(quotient(pos, keys_of(0)));
+    int i;
+    const int64_t small = static_cast<int64_t>(few) * kChunkTile;
+    if (pos < small) {
+      i = static_cast<int>(pos / kChunkTile);
+    } else {
+      // n first + n^2 / 2 item_tokens (with first at the middle of a step) = pos - small
+      const float a = 0.5f * item_tokens, x = static_cast<float>(pos - small);
+      const float f = static_cast<float>(lk - lq) + (few + 0.5f) * item_tokens;
+      const float root = sqrtf(fmaxf(f * f + 4.f * a * x, 0.f));
+      const float n = f + root > 0.f ? 2.f * x / (f + root) : 0.f;
+      i = few + static_cast<int>(n < static_cast<float>(items_head) ? n : static_cast<float>(items_head));
     }
-    return lo;
+    if (i > items_head - 1) i = items_head - 1;
+    while (i > 0 && keys_before(i) > pos) --i;                        // the guess is at most
+    while (i + 1 < items_head && keys_before(i + 1) <= pos) ++i;      // a rounding away
+    return i;
+  }
+  // Where the share that starts at key `pos` of all heads' items starts.
+  __host__ __device__ ChunkPlace place_at(int64_t pos, int Hkv) const {
+    ChunkPlace x;
+    x.head = static_cast<int>(quotient(pos, head_keys));
+    if (x.head >= Hkv) {
+      x.item = x.j = 0;
+      return x;
+    }
+    const int64_t in_head = pos - x.head * head_keys;
+    x.item = item_at(in_head);
+    x.j = static_cast<int>(in_head - keys_before(x.item)) / kChunkTile;
+    return x;
+  }
+  // Shares after share u that go on with an item that it begins.
+  __host__ __device__ int shares_after(int u, int head, int item) const {
+    const int64_t end = head * head_keys + keys_before(item) + keys_of(item);
+    return static_cast<int>(quotient(end - 1, share)) - u;
   }
 };
 
@@ -87,19 +112,23 @@ __host__ __device__ inline ChunkWork chunk_work(int lq, int lk, int causal, int 
   w.lk = lk;
   w.causal = causal;
   w.item_tokens = 2 * (kChunkTile / G);
-  w.items_head = static_cast<int>((static_cast<int64_t>(lq) + w.item_tokens - 1) / w.item_tokens);
-  w.nk_last = w.tiles_of(w.items_head - 1);
-  w.head_tiles = w.tiles_before(w.items_head);
+  w.items_head =
+      static_cast<int>(quotient(static_cast<int64_t>(lq) + w.item_tokens - 1, w.item_tokens));
+  const int64_t room = kChunkTile - (static_cast<int64_t>(lk) - lq);
+  const int64_t few = causal && room > 0 ? quotient(room, w.item_tokens) : 0;
+  w.few = static_cast<int>(few < w.items_head ? few : w.items_head);
+  w.head_keys = w.keys_before(w.items_head - 1) + w.keys_of(w.items_head - 1);
   const int64_t items = static_cast<int64_t>(w.items_head) * Hkv;
-  const int64_t all = w.head_tiles * Hkv;
-  int64_t share = (all + kChunkShares - 1) / kChunkShares;
-  if (share < kChunkMinShare) share = kChunkMinShare;
-  if (items >= kChunkManyItems || w.nk_last <= kChunkMinShare + kChunkMinShare / 2) {
+  const int64_t all = w.head_keys * Hkv;
+  int64_t share = quotient(all + kChunkShares - 1, kChunkShares);
+  if (share < kChunkMinShare * kChunkTile) share = kChunkMinShare * kChunkTile;
+  if (items >= kChunkManyItems ||
+      w.keys_of(w.items_head - 1) <= (kChunkMinShare + kChunkMinShare / 2) * kChunkTile) {
     w.share = 0;
     w.units = static_cast<int>(items);
   } else {
     w.share = share;
-    w.units = static_cast<int>((all + share - 1) / share);
+    w.units = static_cast<int>(quotient(all + share - 1, share));
   }
   return w;
 }
@@ -117,37 +146,33 @@ struct ChunkPiece {
 
 // Walks the pieces of unit `u` of a sequence.
 struct ChunkCursor {
-  int64_t left;    // key tiles of the unit still to come
-  int head, item, j;
+  ChunkPlace at, end;
 
   __host__ __device__ void start(const ChunkWork &w, int u, int Hkv) {
     if (w.share == 0) {   // heaviest items first, the heads side by side
       const int i = u / Hkv;
-      head = u - i * Hkv;
-      item = w.items_head - 1 - i;
-      j = 0;
-      left = w.tiles_of(item);
+      at.head = u - i * Hkv;
+      at.item = w.items_head - 1 - i;
+      at.j = 0;
+      end = at;
+      end.j = w.tiles_of(at.item);
     } else {
-      const int64_t pos = u * w.share, all = w.head_tiles * Hkv;
-      left = all - pos < w.share ? all - pos : w.share;
-      head = static_cast<int>(pos / w.head_tiles);
-      const int64_t in_head = pos - head * w.head_tiles;
-      item = w.item_at(in_head);
-      j = static_cast<int>(in_head - w.tiles_before(item));
+      at = w.place_at(u * w.share, Hkv);
+      end = w.place_at((u + 1) * w.share, Hkv);
     }
   }
   __host__ __device__ bool next(const ChunkWork &w, ChunkPiece &p) {
-    if (left <= 0) return false;
-    p.head = head;
-    p.item = item;
-    p.nk = w.tiles_of(item);
-    p.j0 = j;
-    p.j1 = left < p.nk - j ? j + static_cast<int>(left) : p.nk;
-    left -= p.j1 - p.j0;
-    j = 0;
-    if (++item == w.items_head) {
-      item = 0;
-      ++head;
+    const bool last = at.head == end.head && at.item == end.item;
+    if (at.head > end.head || (last && at.j >= end.j)) return false;
+    p.head = at.head;
+    p.item = at.item;
+    p.nk = w.tiles_of(at.item);
+    p.j0 = at.j;
+    p.j1 = last ? end.j : p.nk;
+    at.j = last ? end.j : 0;
+    if (!last && ++at.item == w.items_head) {
+      at.item = 0;
+      ++at.head;
     }
     return true;
   }

@@ -20,9 +20,7 @@
 // from one 16-byte vector of each of its four keys, paired by byte permutes.
 // P^T's B operand is S^T's accumulator transposed in 8x8 blocks (movmatrix).
 //
-// 8-bit rows are widened in registers: e4m3's bits moved to bf16's place give
-// the value times 2^-120 (subnormals included), and one packed bf16 multiply
-// by 2^(120 + e) makes it the exact stored value.
+// 8-bit rows are widened in registers (paged.cuh).
 #include <math.h>
 
 #include "internal.h"
@@ -67,23 +65,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Bytes 1 and 3 (0 and 2) of w, e4m3, as two bf16 of 2^-120 their value.
-__device__ __forceinline__ uint32_t odd_bytes(uint32_t w) {
-  return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t even_bytes(uint32_t w) {
-  return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
-}
-// 2^(120 + e) in bf16 bits for an exponent byte e + 127; NaN for a NaN row.
-__device__ __forceinline__ uint32_t widen_scale(uint32_t byte) {
-  return byte == kExpNan ? 0x7fffu : (byte + 120u) << 7;
-}
-
 template <int D, bool kQuant, int NT>
 struct Cfg {
   static constexpr int kRowBytes = D * (kQuant ? 1 : 2);
