@@ -134,12 +134,12 @@ __device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
 // streaming kernel (paged_decode.cu), longer ones the tiled one.
 constexpr int kDecodeRows = 16;
 
-constexpr int kDecodeUnits = 456;   // parts of a lone sequence: three for each of 152 SMs
+constexpr int kDecodeUnits = 1824;   // parts of a lone sequence: twelve warps for each of 152 SMs
 
 // Smallest part: short contexts are bound by latency and want many small
 // parts, long ones by bytes and want few partial results.
 __host__ __device__ __forceinline__ int decode_min_part(int lk) {
-  return lk <= 1024 ? 128 : lk <= 4096 ? 256 : 512;
+  return lk <= 1024 ? 128 : lk <= 16384 ? 256 : 512;
 }
 __host__ __device__ __forceinline__ int decode_most_parts(int Hkv) {
   return Hkv >= kDecodeUnits ? 1 : kDecodeUnits / Hkv;
@@ -161,7 +161,7 @@ inline int decode_parts_bound(int max_k, int Hkv) {
   if (max_k <= 0) return 1;
   int64_t n = (static_cast<int64_t>(max_k) + decode_min_part(max_k) - 1) / decode_min_part(max_k);
   if (max_k > 1024 && n < 8) n = 8;
-  if (max_k > 4096 && n < 16) n = 16;
+  if (max_k > 16384 && n < 64) n = 64;
   const int most = decode_most_parts(Hkv);
   return static_cast<int>(n < most ? n : most);
 }

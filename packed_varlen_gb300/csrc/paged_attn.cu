@@ -145,7 +145,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   auto s = reinterpret_cast<cudaStream_t>(stream);
   const bool quant = format == PA_CACHE_E4M3;
   if (p.G <= kDecodeRows) {
-    e = launch_paged_decode(p, quant, s);
+    e = launch_paged_decode(p, quant, sms, s);
     if (e != cudaSuccess) return from_cuda(e);
   }
   if (max_q <= kDecodeRows / p.G) return PA_OK;

@@ -33,23 +33,15 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTileKeys = 16;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;\n" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 load_stream(const uint8_t *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -68,356 +60,445 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 template <int D, bool kQuant, int NT>
 struct Cfg {
   static constexpr int kRowBytes = D * (kQuant ? 1 : 2);
-  static constexpr int kKVecs = kRowBytes / 32;             // a lane's 16-byte K vectors of a tile
+  static constexpr int kKVecs = kRowBytes / 32;             // a lane's 16-byte K vectors of 16 keys
   static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8; // a lane's V vector
   static constexpr int kVSets = kRowBytes / (8 * kVBytes);  // vectors of one key
-  static constexpr int kTileBytes = 16 * kRowBytes;
-  static constexpr int kStageBytes = 2 * kTileBytes + (kQuant ? 128 : 0);
-  static constexpr int kStages = kQuant ? 4 : 3;
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kPitch = D + 4;                      // floats of a merged row
-  static constexpr int kMergeBytes = kWarps * kRows * (kPitch + 2) * 4;
-  static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+  static constexpr int kVWords = kVBytes / 4;
+  static constexpr int kHalves = kQuant ? 2 : 1;            // 16-key halves of a tile
+  static constexpr int kTileKeys = 16 * kHalves;
+  static constexpr int kCtas = (NT == 1 ? 4 : 3) - (D == 128 ? 1 : 0);   // CTAs that share an SM
 };
 
-template <int D, bool kQuant, int NT>
-__global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnParams p) {
-  using C = Cfg<D, kQuant, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.y, hk = blockIdx.x % p.c.Hkv, part = blockIdx.x / p.c.Hkv;
-  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
-  int err;
-  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
-  if (err && blockIdx.x == 0 && tid == 0) record_error(p.status, err);
-  const int R = s.lq * p.G;
-  if (s.lq == 0 || s.lq > kDecodeRows / p.G) return;
-  const int keys_part = decode_part(s.lk, p.c.Hkv);
-  const int parts = decode_parts(s.lk, p.c.Hkv);
-  if (part > 0 && part >= parts) return;   // part 0 of a sequence without keys writes its zeros
-  const int k0 = part * keys_part, k1 = k0 + min(s.lk - k0, keys_part);
+// Walks the units of the call, (sequence, part of its keys, K/V head), heads
+// running fastest: a warp holds 32 sequences at a time, one per lane, with the
+// units before each.  Units are asked for in rising order.
+struct Walk {
+  int group, base, total;       // 32 sequences from group * 32, their first unit, their units
+  int q0, lq, lk, first, units; // this lane's sequence
+  // the unit found
+  int b, part, hk, s_q0, s_lq, s_lk;
 
-  // ---- Q^T, the B operand of every S^T product
-  uint32_t qf[NT][D / 16][2];
+  __device__ __forceinline__ void load(const PagedAttnParams &p, bool report) {
+    const int lane = threadIdx.x & 31, x = group * 32 + lane;
+    q0 = lq = lk = units = 0;
+    if (x < p.batch) {
+      int err;
+      const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, x, p.total_q, p.max_q, p.max_k,
+                                   static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
+      if (err && report) record_error(p.status, err);
+      q0 = s.q0;
+      lq = s.lq;
+      lk = s.lk;
+      if (lq > 0 && lq <= kDecodeRows / p.G)
+        units = max(decode_parts(lk, p.c.Hkv), 1) * p.c.Hkv;   // no keys: one unit writes zeros
+    }
+    int incl = units;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    const bool live = r < R;
-    const int i = live ? r / p.G : 0, gg = live ? r - i * p.G : 0;
-    const __nv_bfloat16 *row =
-        p.q + (s.q0 + i) * p.q_stride + static_cast<int64_t>(hk * p.G + gg) * D;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint2 w = make_uint2(0u, 0u);
-      // four values: of vector t + 4 (ks / 2) (bf16) or t + 4 (ks / 4) (e4m3)
-      const int d = kQuant ? (t + 4 * (ks >> 2)) * 16 + (ks & 3) * 4
-                           : (t + 4 * (ks >> 1)) * 8 + (ks & 1) * 4;
-      if (live) w = __ldg(reinterpret_cast<const uint2 *>(row + d));
-      if (kQuant) {   // the widened bytes come as values 0, 2 and 1, 3
-        qf[nt][ks][0] = __byte_perm(w.x, w.y, 0x5410);
-        qf[nt][ks][1] = __byte_perm(w.x, w.y, 0x7632);
-      } else {
-        qf[nt][ks][0] = w.x;
-        qf[nt][ks][1] = w.y;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    first = incl - units;
+    total = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __device__ __forceinline__ void open(const PagedAttnParams &p, bool report) {
+    group = base = 0;
+    load(p, report);
+  }
+  __device__ __forceinline__ bool seek(const PagedAttnParams &p, int u, bool report) {
+    while (u >= base + total) {
+      base += total;
+      ++group;
+      if (group * 32 >= p.batch) {
+        total = 0;
+        --group;
+        return false;
       }
+      load(p, report);
     }
+    const int local = u - base;
+    const uint32_t at = __ballot_sync(0xffffffffu, units > 0 && first <= local);
+    const int src = 31 - __clz(at);
+    const int rest = local - __shfl_sync(0xffffffffu, first, src);
+    b = group * 32 + src;
+    part = rest / p.c.Hkv;
+    hk = rest - part * p.c.Hkv;
+    s_q0 = __shfl_sync(0xffffffffu, q0, src);
+    s_lq = __shfl_sync(0xffffffffu, lq, src);
+    s_lk = __shfl_sync(0xffffffffu, lk, src);
+    return true;
   }
-  // last key + 1 that each of this lane's columns (rows of q) sees
-  int lim[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * t + e;
-      lim[nt][e] = r >= R ? 0 : p.causal ? s.lk - s.lq + 1 + r / p.G : s.lk;
-    }
-  const int all_see = p.causal ? s.lk - s.lq + 1 : s.lk;   // keys before it need no mask
+};
 
-  float o[NT][D / 16][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
-
-  // ---- this warp's tiles: warp, warp + 4, ... of the part
-  const int part_tiles = k1 > k0 ? (k1 - k0 + kTileKeys - 1) / kTileKeys : 0;
-  const int n_tiles = part_tiles > warp ? (part_tiles - warp + kWarps - 1) / kWarps : 0;
-  const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.table_pages;
+// Every warp walks units of its own: its number, its number + all warps, ...
+template <int D, bool kQuant, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
+    paged_decode_kernel(const PagedAttnParams p) {
+  using C = Cfg<D, kQuant, NT>;
+  constexpr int kTile = C::kTileKeys;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int page_mask = (1 << p.c.page_shift) - 1;
   const int64_t row_stride = static_cast<int64_t>(p.c.Hkv) * C::kRowBytes;
-  const uint8_t *kbase = static_cast<const uint8_t *>(p.c.k) + hk * C::kRowBytes;
-  const uint8_t *vbase = static_cast<const uint8_t *>(p.c.v) + hk * C::kRowBytes;
-  uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
-  const uint32_t ring_u = tc::smem_u32(ring);
+  Walk w;
+  const bool report = blockIdx.x == 0 && warp == 0;
+  w.open(p, report);
+  for (int u = blockIdx.x * kWarps + warp; w.seek(p, u, report); u += gridDim.x * kWarps) {
+    const int lq = w.s_lq, lk = w.s_lk, hk = w.hk, R = lq * p.G;
+    const int keys_part = decode_part(lk, p.c.Hkv), parts = decode_parts(lk, p.c.Hkv);
+    const int k0 = w.part * keys_part, keys = min(lk - k0, keys_part);
+    const int n_tiles = (keys + kTile - 1) / kTile;
+    const int32_t *table = p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages;
 
-  // pages of 32 tiles at a time, one per lane (a tile lies inside one page)
-  auto tile_key = [&](int n) { return k0 + (n * kWarps + warp) * kTileKeys; };
-  auto load_pages = [&](int n0) -> int32_t {
-    const int n = n0 + lane;
-    return n < n_tiles ? __ldg(table + (tile_key(n) >> p.c.page_shift)) : 0;
-  };
-  int32_t pages = load_pages(0), pages_next = load_pages(32);
+    // pages of 32 runs of 16 keys at a time, one per lane (a run lies in one page)
+    const int runs = (keys + 15) / 16;
+    auto load_pages = [&](int n0) -> int32_t {
+      const int n = n0 + lane;
+      return n < runs ? __ldg(table + ((k0 + n * 16) >> p.c.page_shift)) : 0;
+    };
+    int32_t pages = load_pages(0), pages_next = load_pages(32);
 
-  auto issue = [&](int n) {
-    if (n < n_tiles) {
-      if (n > 0 && (n & 31) == 0) {
-        pages = pages_next;
-        pages_next = load_pages(n + 32);
-      }
-      int32_t page = __shfl_sync(0xffffffffu, pages, n & 31);
-      bool good = page_ok(p.c, page);
-      if (!good) {
-        if (lane == 0) record_error(p.status, PA_DEVICE_ERR_PAGE);
-        page = 0;
-      }
-      const int key = tile_key(n);
-      const int have = good ? s.lk - key : 0;   // rows of the tile that are the sequence's
-      const int row0 = key & page_mask;
-      const int64_t at = (page * p.c.page_stride) * (kQuant ? 1 : 2) + row0 * row_stride;
-      const uint32_t dst = ring_u + (n % C::kStages) * C::kStageBytes;
+    // ---- one tile's bytes, as the products take them
+    uint4 kreg[C::kHalves][C::kKVecs];
+    uint32_t vreg[C::kHalves][4 * C::kVSets][C::kVWords];
+    int kexp[C::kHalves][2], vexp[C::kHalves][2];   // of keys g and g + 8
+    int64_t at[C::kHalves];      // first byte of the run's rows of this head
+    bool good[C::kHalves];
+    auto locate = [&](int n) {   // tile n's runs
 #pragma unroll
-      for (int v = 0; v < C::kKVecs; ++v) {
-        const int row = (v & 1) * 8 + g, chunk = t + 4 * (v >> 1);
-        cp_async16(dst + v * 512 + lane * 16, kbase + at + row * row_stride + chunk * 16,
-                   row < have ? 16 : 0);
-      }
+      for (int h = 0; h < C::kHalves; ++h) {
+        const int run = n * C::kHalves + h;
+        int32_t page = __shfl_sync(0xffffffffu, pages, run & 31);
+        good[h] = run < runs && page_ok(p.c, page);
+        if (!good[h] && run < runs && lane == 0) record_error(p.status, PA_DEVICE_ERR_PAGE);
+        const int row0 = (k0 + run * 16) & page_mask;
+        if (!good[h]) page = 0;
+        at[h] = page * p.c.page_stride * (kQuant ? 1 : 2) + row0 * row_stride + hk * C::kRowBytes;
+        if (kQuant && good[h]) {
+          const int64_t ex = exp_offset(p.c, page, row0, hk);
 #pragma unroll
-      for (int v = 0; v < 4 * C::kVSets; ++v) {
-        const int row = 2 * t + (v & 1) + 8 * ((v >> 1) & 1), chunk = g + 8 * (v >> 2);
-        const uint8_t *src = vbase + at + row * row_stride + chunk * C::kVBytes;
-        const uint32_t to = dst + C::kTileBytes + v * (32 * C::kVBytes) + lane * C::kVBytes;
-        if (C::kVBytes == 16)
-          cp_async16(to, src, row < have ? 16 : 0);
-        else
-          cp_async8(to, src, row < have ? 8 : 0);
-      }
-      if (kQuant && lane < 2) {
-        const uint8_t *e = lane == 0 ? p.c.k_exp : p.c.v_exp;
-        cp_async16(dst + 2 * C::kTileBytes + lane * 16, e + exp_offset(p.c, page, row0, hk),
-                   good ? 16 : 0);
-      }
-    }
-    cp_async_commit();
-  };
-
-#pragma unroll
-  for (int n = 0; n < C::kStages - 1; ++n) issue(n);
-
-  for (int n = 0; n < n_tiles; ++n) {
-    cp_async_wait<C::kStages - 2>();
-    __syncwarp();                       // the exponents come from other lanes' copies
-    issue(n + C::kStages - 1);          // into the slots that tile n - 1 has left
-    const uint8_t *st = ring + (n % C::kStages) * C::kStageBytes;
-    const int key = tile_key(n);
-
-    // S^T = K Q^T
-    float sc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-    if constexpr (!kQuant) {
-#pragma unroll
-      for (int i = 0; i < C::kKVecs / 2; ++i) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(st + (2 * i) * 512 + lane * 16);
-        const uint4 c = *reinterpret_cast<const uint4 *>(st + (2 * i + 1) * 512 + lane * 16);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(sc[nt], a.x, c.x, a.y, c.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-          mma16816(sc[nt], a.z, c.z, a.w, c.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+          for (int e = 0; e < 2; ++e) {
+            const int row = min(g + 8 * e, max(lk - 1 - k0 - run * 16, 0));
+            kexp[h][e] = __ldg(p.c.k_exp + ex + row);
+            vexp[h][e] = __ldg(p.c.v_exp + ex + row);
+          }
         }
       }
-    } else {
-      const uint8_t *ex = st + 2 * C::kTileBytes;
-      const uint32_t s0 = widen_scale(ex[g]) * 0x10001u, s8 = widen_scale(ex[g + 8]) * 0x10001u;
+    };
+    // Rows past the sequence's last key are read as that key: their weights are
+    // zero, and what lies past it is never touched.
+    auto load_k = [&](int n) {
 #pragma unroll
-      for (int i = 0; i < C::kKVecs / 2; ++i) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(st + (2 * i) * 512 + lane * 16);
-        const uint4 c = *reinterpret_cast<const uint4 *>(st + (2 * i + 1) * 512 + lane * 16);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
+      for (int h = 0; h < C::kHalves; ++h) {
+        const int last = max(lk - 1 - k0 - (n * C::kHalves + h) * 16, 0);
+        const uint8_t *src = static_cast<const uint8_t *>(p.c.k) + at[h] + t * 16;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t a0 = mul_bf16x2(even_bytes(aw[w]), s0), a2 = mul_bf16x2(odd_bytes(aw[w]), s0);
-          const uint32_t a1 = mul_bf16x2(even_bytes(cw[w]), s8), a3 = mul_bf16x2(odd_bytes(cw[w]), s8);
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t *row = src + min(g + 8 * e, last) * row_stride;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(sc[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
+          for (int v = 0; v < C::kKVecs / 2; ++v)
+            kreg[h][2 * v + e] = good[h] ? load_stream(row + v * 64) : make_uint4(0u, 0u, 0u, 0u);
         }
       }
+    };
+    auto load_v = [&](int n) {
+#pragma unroll
+      for (int h = 0; h < C::kHalves; ++h) {
+        const int last = max(lk - 1 - k0 - (n * C::kHalves + h) * 16, 0);
+        const uint8_t *src = static_cast<const uint8_t *>(p.c.v) + at[h] + g * C::kVBytes;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint8_t *row = src + min(2 * t + (kk & 1) + 8 * (kk >> 1), last) * row_stride;
+#pragma unroll
+          for (int cs = 0; cs < C::kVSets; ++cs) {
+            uint32_t(&v)[C::kVWords] = vreg[h][cs * 4 + kk];
+            if constexpr (C::kVBytes == 16) {
+              const uint4 x = good[h] ? load_stream(row + cs * 128) : make_uint4(0u, 0u, 0u, 0u);
+              v[0] = x.x;
+              v[1] = x.y;
+              v[2] = x.z;
+              v[3] = x.w;
+            } else {
+              const uint2 x = good[h] ? __ldg(reinterpret_cast<const uint2 *>(row))
+                                      : make_uint2(0u, 0u);
+              v[0] = x.x;
+              v[1] = x.y;
+            }
+          }
+        }
+      }
+    };
+    if (n_tiles > 0) {
+      locate(0);
+      load_k(0);
+      load_v(0);
     }
 
-    // online softmax over the tile's keys, all lanes of a column in step
-    uint32_t pf[NT][2];
-    bool moved = false;
-    float alpha[NT][2];
+    // Q^T, the B operand of every S^T product.  Over an 8-bit cache the rows
+    // are scaled by a power of two, which the scores' factor takes back: the
+    // widened K bytes are 2^-120 of their values, and q * 2^119 would overflow.
+    uint32_t qf[NT][D / 16][2];
+    float factor[NT][2];   // of this lane's two columns (rows of q)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      const bool live = r < R;
+      const int i = live ? r / p.G : 0, gg = live ? r - i * p.G : 0;
+      const __nv_bfloat16 *row =
+          p.q + (w.s_q0 + i) * p.q_stride + static_cast<int64_t>(hk * p.G + gg) * D;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint2 x = make_uint2(0u, 0u);
+        // four values: of vector t + 4 (ks / 2) (bf16) or t + 4 (ks / 4) (e4m3)
+        const int d = kQuant ? (t + 4 * (ks >> 2)) * 16 + (ks & 3) * 4
+                             : (t + 4 * (ks >> 1)) * 8 + (ks & 1) * 4;
+        if (live) x = __ldg(reinterpret_cast<const uint2 *>(row + d));
+        if (kQuant) {   // the widened bytes come as values 0, 2 and 1, 3
+          qf[nt][ks][0] = __byte_perm(x.x, x.y, 0x5410);
+          qf[nt][ks][1] = __byte_perm(x.x, x.y, 0x7632);
+        } else {
+          qf[nt][ks][0] = x.x;
+          qf[nt][ks][1] = x.y;
+        }
+      }
+      float back = p.scale_log2;
+      if constexpr (kQuant) {
+        uint32_t top = 0;   // largest exponent field of the row, in place
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = qf[nt][ks][e] & 0x7f807f80u;
+            top = max(top, max(x & 0xffffu, x >> 16));
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // |q| < 2^(field - 126): times 2^up it stays below 2^121
+        const int up = min(max(245 - static_cast<int>(top >> 7), -7), 127);
+        const float f = pow2f(up);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qf[nt][ks][e] = tc::pack_bf16x2(__uint_as_float(qf[nt][ks][e] << 16) * f,
+                                            __uint_as_float(qf[nt][ks][e] & 0xffff0000u) * f);
+        back = p.scale_log2 * pow2f(120 - up);
+      }
+      factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
+    // last key + 1 that each of this lane's columns (rows of q) sees
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
+        lim[nt][e] = r >= R ? 0 : p.causal ? lk - lq + 1 + r / p.G : lk;
+      }
+    const int all_see = p.causal ? lk - lq + 1 : lk;   // keys before it need no mask
+
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] *= p.scale_log2;
-      if (key + kTileKeys > all_see) {
+      for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key + g + 8 * (e >> 1) >= lim[nt][e & 1]) sc[nt][e] = -INFINITY;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        alpha[nt][e] = 1.f;
-        if (mx > m[nt][e] + kRescaleThreshold) {   // from -inf: any finite score
-          alpha[nt][e] = tc::ex2(m[nt][e] - mx);
-          m[nt][e] = mx;
-          moved = true;
-        }
-        const float base = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-        const float p0 = tc::ex2(sc[nt][e] - base), p1 = tc::ex2(sc[nt][e + 2] - base);
-        l[nt][e] = l[nt][e] * alpha[nt][e] + (p0 + p1);
-        sc[nt][e] = p0;
-        sc[nt][e + 2] = p1;
-      }
-      pf[nt][0] = transpose8x8(tc::pack_bf16x2(sc[nt][0], sc[nt][1]));
-      pf[nt][1] = transpose8x8(tc::pack_bf16x2(sc[nt][2], sc[nt][3]));
-    }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[nt][e & 1];
+        for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // O^T += V^T P^T
-    const uint8_t *sv = st + C::kTileBytes;
-    if constexpr (!kQuant) {
+    for (int n = 0; n < n_tiles; ++n) {
+      const int key = k0 + n * kTile;
+      const bool more = n + 1 < n_tiles;
+
+      // S^T = K Q^T, in two chains
+      float sc[C::kHalves][NT][4];
+      float kf[C::kHalves][2], vf[C::kHalves][2];
 #pragma unroll
-      for (int cs = 0; cs < C::kVSets; ++cs) {
-        uint4 v[4];
+      for (int h = 0; h < C::kHalves; ++h) {
+        float s2[NT][4];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          v[kk] = *reinterpret_cast<const uint4 *>(sv + (cs * 4 + kk) * 512 + lane * 16);
-        const uint32_t va[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w},
-                                   {v[1].x, v[1].y, v[1].z, v[1].w},
-                                   {v[2].x, v[2].y, v[2].z, v[2].w},
-                                   {v[3].x, v[3].y, v[3].z, v[3].w}};
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t a0 = __byte_perm(va[0][w], va[1][w], 0x5410);
-          const uint32_t a1 = __byte_perm(va[0][w], va[1][w], 0x7632);
-          const uint32_t a2 = __byte_perm(va[2][w], va[3][w], 0x5410);
-          const uint32_t a3 = __byte_perm(va[2][w], va[3][w], 0x7632);
+          for (int e = 0; e < 4; ++e) sc[h][nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][cs * 4 + w], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        for (int i = 0; i < C::kKVecs / 2; ++i) {
+          const uint4 a = kreg[h][2 * i], c = kreg[h][2 * i + 1];
+          if constexpr (!kQuant) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(sc[h][nt], a.x, c.x, a.y, c.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+              mma16816(s2[nt], a.z, c.z, a.w, c.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+            }
+          } else {
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a0 = even_bytes(aw[x]), a2 = odd_bytes(aw[x]);
+              const uint32_t a1 = even_bytes(cw[x]), a3 = odd_bytes(cw[x]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(x & 1 ? s2[nt] : sc[h][nt], a0, a1, a2, a3, qf[nt][4 * i + x][0],
+                         qf[nt][4 * i + x][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[h][nt][e] += s2[nt][e];
+        if constexpr (kQuant) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // p * 2^(e + 112): p <= 2^8 and e <= 7, and a stored byte is 2^-120
+            // of its value, so the output accumulates in units of 2^8
+            kf[h][e] = good[h] ? row_scale(kexp[h][e]) : 0.f;
+            vf[h][e] = !good[h] ? 0.f
+                       : vexp[h][e] == kExpNan ? __int_as_float(0x7fffffff)
+                                               : pow2f(vexp[h][e] - kExpBias + 112);
+          }
         }
       }
-    } else {
-      const uint8_t *ex = st + 2 * C::kTileBytes + 16;
-      uint32_t sc4[4];
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const int row = 2 * t + (kk & 1) + 8 * (kk >> 1);
-        // a NaN byte of a row past the end must not meet its zeros
-        sc4[kk] = key + row < s.lk ? widen_scale(ex[row]) : 0u;
+      // the next tile's K, into the registers that this one has left
+      if (more) {
+        if (((n + 1) * C::kHalves & 31) == 0) {
+          pages = pages_next;
+          pages_next = load_pages((n + 1) * C::kHalves + 32);
+        }
+        locate(n + 1);
+        load_k(n + 1);
       }
-      const uint32_t s0 = sc4[0] | (sc4[1] << 16), s8 = sc4[2] | (sc4[3] << 16);
-      uint32_t va[4][C::kVBytes / 4];
+
+      // online softmax over the tile's keys, all lanes of a column in step
+      uint32_t pf[C::kHalves][NT][2];
+      bool moved = false;
+      float alpha[NT][2];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if constexpr (C::kVBytes == 16) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(sv + kk * 512 + lane * 16);
-          va[kk][0] = v.x;
-          va[kk][1] = v.y;
-          va[kk][2] = v.z;
-          va[kk][3] = v.w;
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (kQuant) sc[h][nt][e] *= kf[h][e >> 1];
+            sc[h][nt][e] *= factor[nt][e & 1];
+          }
+          if (key + kTile > all_see) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key + 16 * h + g + 8 * (e >> 1) >= lim[nt][e & 1]) sc[h][nt][e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+          for (int h = 1; h < C::kHalves; ++h) mx = tc::fmax3(mx, sc[h][nt][e], sc[h][nt][e + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          alpha[nt][e] = 1.f;
+          if (mx > m[nt][e] + kRescaleThreshold) {   // from -inf: any finite score
+            alpha[nt][e] = tc::ex2(m[nt][e] - mx);
+            m[nt][e] = mx;
+            moved = true;
+          }
+          const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+          l[nt][e] *= alpha[nt][e];
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h) {
+            const float p0 = tc::ex2(sc[h][nt][e] - ref), p1 = tc::ex2(sc[h][nt][e + 2] - ref);
+            l[nt][e] += p0 + p1;
+            sc[h][nt][e] = kQuant ? p0 * vf[h][0] : p0;
+            sc[h][nt][e + 2] = kQuant ? p1 * vf[h][1] : p1;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          pf[h][nt][0] = transpose8x8(tc::pack_bf16x2(sc[h][nt][0], sc[h][nt][1]));
+          pf[h][nt][1] = transpose8x8(tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
+        }
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[nt][e & 1];
+      }
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int h = 0; h < C::kHalves; ++h) {
+#pragma unroll
+        for (int cs = 0; cs < C::kVSets; ++cs) {
+          const uint32_t(*va)[C::kVWords] = &vreg[h][cs * 4];
+#pragma unroll
+          for (int x = 0; x < C::kVWords; ++x) {
+            // low and high halves of a word: of bf16 values 0 and 1, of e4m3 0, 1 and 2, 3
+            const uint32_t ab0 = __byte_perm(va[0][x], va[1][x], 0x5410);
+            const uint32_t ab1 = __byte_perm(va[0][x], va[1][x], 0x7632);
+            const uint32_t cd0 = __byte_perm(va[2][x], va[3][x], 0x5410);
+            const uint32_t cd1 = __byte_perm(va[2][x], va[3][x], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (!kQuant) {
+                mma16816(o[nt][cs * 4 + x], ab0, ab1, cd0, cd1, pf[h][nt][0], pf[h][nt][1]);
+              } else {
+                mma16816(o[nt][2 * x], even_bytes(ab0), odd_bytes(ab0), even_bytes(cd0),
+                         odd_bytes(cd0), pf[h][nt][0], pf[h][nt][1]);
+                mma16816(o[nt][2 * x + 1], even_bytes(ab1), odd_bytes(ab1), even_bytes(cd1),
+                         odd_bytes(cd1), pf[h][nt][0], pf[h][nt][1]);
+              }
+            }
+          }
+        }
+      }
+      if (more) load_v(n + 1);
+    }
+
+    // ---- this lane's columns: D / 8 dims each of rows 2 t and 2 t + 1, in runs
+    // of 2 KR consecutive ones
+    constexpr int KR = !kQuant && D == 128 ? 4 : D / 16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+        const int r = nt * 8 + 2 * t + e;
+        if (r >= R) continue;
+        const int i = r / p.G, h = hk * p.G + r - i * p.G;
+        const float unit = kQuant ? 256.f : 1.f;
+        if (parts <= 1) {
+          const float inv = m[nt][e] == -INFINITY ? 0.f : unit / l[nt][e];
+          __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D;
+#pragma unroll
+          for (int mt = 0; mt < D / 16; mt += 4) {
+            const int d = g * 2 * KR + 16 * KR * (mt / KR) + 2 * (mt % KR);
+            uint32_t x[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              x[y] = tc::pack_bf16x2(o[nt][mt + y][e] * inv, o[nt][mt + y][e + 2] * inv);
+            *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
         } else {
-          const uint2 v = *reinterpret_cast<const uint2 *>(sv + kk * 256 + lane * 8);
-          va[kk][0] = v.x;
-          va[kk][1] = v.y;
-        }
-      }
+          const int64_t slot = (static_cast<int64_t>(w.b) * p.dec_parts + w.part) * p.dec_rows +
+                               static_cast<int64_t>(i) * p.Hq + h;
 #pragma unroll
-      for (int w = 0; w < C::kVBytes / 4; ++w) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {   // values 0, 1, then 2, 3 of the word
-          const uint32_t ab = __byte_perm(va[0][w], va[1][w], half ? 0x7632 : 0x5410);
-          const uint32_t cd = __byte_perm(va[2][w], va[3][w], half ? 0x7632 : 0x5410);
-          const uint32_t a0 = mul_bf16x2(even_bytes(ab), s0), a1 = mul_bf16x2(odd_bytes(ab), s0);
-          const uint32_t a2 = mul_bf16x2(even_bytes(cd), s8), a3 = mul_bf16x2(odd_bytes(cd), s8);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][2 * w + half], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+          for (int mt = 0; mt < D / 16; mt += 2) {
+            const int d = g * 2 * KR + 16 * KR * (mt / KR) + 2 * (mt % KR);
+            *reinterpret_cast<float4 *>(p.dec_o + slot * D + d) =
+                make_float4(o[nt][mt][e] * unit, o[nt][mt][e + 2] * unit, o[nt][mt + 1][e] * unit,
+                            o[nt][mt + 1][e + 2] * unit);
+          }
+          if (g == 0) p.dec_ml[slot] = make_float2(m[nt][e], l[nt][e]);
         }
       }
     }
   }
   tc::griddep_launch_dependents();
-
-  // ---- join the four warps
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
-  cp_async_wait<0>();
-  __syncthreads();
-  float *mo = reinterpret_cast<float *>(smem);                       // [warp][row][pitch]
-  float2 *ml = reinterpret_cast<float2 *>(mo + kWarps * C::kRows * C::kPitch);   // [warp][row]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * t + e;
-      float *dst = mo + (warp * C::kRows + r) * C::kPitch;
-#pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        const int d = !kQuant && D == 128 ? g * 8 + 64 * (mt >> 2) + 2 * (mt & 3)
-                                          : g * (D / 8) + 2 * mt;
-        *reinterpret_cast<float2 *>(dst + d) = make_float2(o[nt][mt][e], o[nt][mt][e + 2]);
-      }
-      if (g == 0) ml[warp * C::kRows + r] = make_float2(m[nt][e], l[nt][e]);
-    }
-  }
-  __syncthreads();
-  for (int x = tid; x < R * (D / 4); x += kThreads) {
-    const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 v = ml[w * C::kRows + r];
-      const float f = tc::ex2(v.x - base);
-      const float4 a = *reinterpret_cast<const float4 *>(mo + (w * C::kRows + r) * C::kPitch + d);
-      sum += f * v.y;
-      acc.x += f * a.x;
-      acc.y += f * a.y;
-      acc.z += f * a.z;
-      acc.w += f * a.w;
-    }
-    const int i = r / p.G, h = hk * p.G + r - i * p.G;
-    if (parts <= 1) {
-      const float inv = top == -INFINITY ? 0.f : 1.f / sum;
-      const uint2 w = make_uint2(tc::pack_bf16x2(acc.x * inv, acc.y * inv),
-                                 tc::pack_bf16x2(acc.z * inv, acc.w * inv));
-      *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(s.q0 + i) * p.Hq + h) * D + d) = w;
-    } else {
-      const int64_t slot = (static_cast<int64_t>(b) * p.dec_parts + part) * p.dec_rows +
-                           static_cast<int64_t>(i) * p.Hq + h;
-      *reinterpret_cast<float4 *>(p.dec_o + slot * D + d) = acc;
-      if (d == 0) p.dec_ml[slot] = make_float2(top, sum);
-    }
-  }
 }
 
 // Joins the parts of every row that has more than one: a CTA per row, its four
@@ -469,15 +550,13 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttn
 }
 
 template <int D, bool kQuant, int NT>
-cudaError_t launch(const PagedAttnParams &p, cudaStream_t stream) {
-  constexpr int smem = Cfg<D, kQuant, NT>::kSmem;
-  static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_decode_kernel<D, kQuant, NT>),
-                                smem, configured);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.dec_parts) * p.c.Hkv, p.batch);
-  paged_decode_kernel<D, kQuant, NT><<<grid, kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
+cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
+  const int64_t most =
+      (static_cast<int64_t>(p.dec_parts) * p.c.Hkv * p.batch + kWarps - 1) / kWarps;
+  const int64_t ctas = static_cast<int64_t>(num_sms) * Cfg<D, kQuant, NT>::kCtas;
+  paged_decode_kernel<D, kQuant, NT>
+      <<<static_cast<unsigned>(most < ctas ? most : ctas), kThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.dec_parts == 1) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -493,17 +572,18 @@ cudaError_t launch(const PagedAttnParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, cudaStream_t stream) {
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
+                                cudaStream_t stream) {
   // 8 columns where no sequence of the call can have more rows: a column's
   // results do not depend on the others, so this changes no bits
   const int most = p.max_q < kDecodeRows / p.G ? p.max_q * p.G : kDecodeRows / p.G * p.G;
   const bool wide = most > 8;
   if (p.c.D == 128) {
-    if (quant) return wide ? launch<128, true, 2>(p, stream) : launch<128, true, 1>(p, stream);
-    return wide ? launch<128, false, 2>(p, stream) : launch<128, false, 1>(p, stream);
+    if (quant) return wide ? launch<128, true, 2>(p, num_sms, stream) : launch<128, true, 1>(p, num_sms, stream);
+    return wide ? launch<128, false, 2>(p, num_sms, stream) : launch<128, false, 1>(p, num_sms, stream);
   }
-  if (quant) return wide ? launch<64, true, 2>(p, stream) : launch<64, true, 1>(p, stream);
-  return wide ? launch<64, false, 2>(p, stream) : launch<64, false, 1>(p, stream);
+  if (quant) return wide ? launch<64, true, 2>(p, num_sms, stream) : launch<64, true, 1>(p, num_sms, stream);
+  return wide ? launch<64, false, 2>(p, num_sms, stream) : launch<64, false, 1>(p, num_sms, stream);
 }
 
 }  // namespace pa

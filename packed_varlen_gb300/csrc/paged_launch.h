@@ -8,7 +8,8 @@ namespace pa {
 struct PagedAttnParams;   // paged.cuh
 
 // Sequences of at most kDecodeRows rows: streaming kernel, and the join of its parts.
-cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, cudaStream_t stream);
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
+                                cudaStream_t stream);
 
 // Longer sequences: tiled kernel, and the join of the parts that its shares leave.
 cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
