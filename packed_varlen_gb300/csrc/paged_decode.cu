@@ -52,6 +52,26 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The low (high) two e4m3 bytes of w as f16, exactly.
+__device__ __forceinline__ uint32_t f16_low(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_high(uint32_t w) { return f16_low(w >> 16); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
@@ -138,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
   constexpr int kTile = C::kTileKeys;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int page_mask = (1 << p.c.page_shift) - 1;
-  const int64_t row_stride = static_cast<int64_t>(p.c.Hkv) * C::kRowBytes;
+  const int row_stride = p.c.Hkv * C::kRowBytes;   // at most 4096 heads of 256 bytes
   Walk w;
   const bool report = blockIdx.x == 0 && warp == 0;
   w.open(p, report);
@@ -233,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
       load_v(0);
     }
 
-    // Q^T, the B operand of every S^T product.  Over an 8-bit cache the rows
-    // are scaled by a power of two, which the scores' factor takes back: the
-    // widened K bytes are 2^-120 of their values, and q * 2^119 would overflow.
+    // Q^T, the B operand of every S^T product.  Over an 8-bit cache it is f16,
+    // each row scaled by a power of two to the top of f16's range (what that
+    // loses lies 2^-40 below the row's largest); the scores' factor takes it back.
     uint32_t qf[NT][D / 16][2];
     float factor[NT][2];   // of this lane's two columns (rows of q)
 #pragma unroll
@@ -252,13 +272,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
         const int d = kQuant ? (t + 4 * (ks >> 2)) * 16 + (ks & 3) * 4
                              : (t + 4 * (ks >> 1)) * 8 + (ks & 1) * 4;
         if (live) x = __ldg(reinterpret_cast<const uint2 *>(row + d));
-        if (kQuant) {   // the widened bytes come as values 0, 2 and 1, 3
-          qf[nt][ks][0] = __byte_perm(x.x, x.y, 0x5410);
-          qf[nt][ks][1] = __byte_perm(x.x, x.y, 0x7632);
-        } else {
-          qf[nt][ks][0] = x.x;
-          qf[nt][ks][1] = x.y;
-        }
+        qf[nt][ks][0] = x.x;
+        qf[nt][ks][1] = x.y;
       }
       float back = p.scale_log2;
       if constexpr (kQuant) {
@@ -272,16 +287,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // |q| < 2^(field - 126): times 2^up it stays below 2^121
-        const int up = min(max(245 - static_cast<int>(top >> 7), -7), 127);
+        // |q| < 2^(field - 126): times 2^up it stays below 2^15
+        const int up = min(141 - static_cast<int>(top >> 7), 126);
         const float f = pow2f(up);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            qf[nt][ks][e] = tc::pack_bf16x2(__uint_as_float(qf[nt][ks][e] << 16) * f,
-                                            __uint_as_float(qf[nt][ks][e] & 0xffff0000u) * f);
-        back = p.scale_log2 * pow2f(120 - up);
+            qf[nt][ks][e] = pack_f16x2(__uint_as_float(qf[nt][ks][e] << 16) * f,
+                                       __uint_as_float(qf[nt][ks][e] & 0xffff0000u) * f);
+        back = p.scale_log2 * pow2f(-up);
       }
       factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
       factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
@@ -308,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
       l[nt][0] = l[nt][1] = 0.f;
     }
 
+    int unit = 0;   // exponent byte that the output's units go by (8-bit caches)
     for (int n = 0; n < n_tiles; ++n) {
       const int key = k0 + n * kTile;
       const bool more = n + 1 < n_tiles;
@@ -335,12 +351,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
             const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t a0 = even_bytes(aw[x]), a2 = odd_bytes(aw[x]);
-              const uint32_t a1 = even_bytes(cw[x]), a3 = odd_bytes(cw[x]);
+              const uint32_t a0 = f16_low(aw[x]), a2 = f16_high(aw[x]);
+              const uint32_t a1 = f16_low(cw[x]), a3 = f16_high(cw[x]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma16816(x & 1 ? s2[nt] : sc[h][nt], a0, a1, a2, a3, qf[nt][4 * i + x][0],
-                         qf[nt][4 * i + x][1]);
+                mma16816_f16(x & 1 ? s2[nt] : sc[h][nt], a0, a1, a2, a3, qf[nt][4 * i + x][0],
+                             qf[nt][4 * i + x][1]);
             }
           }
         }
@@ -350,15 +366,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           for (int e = 0; e < 4; ++e) sc[h][nt][e] += s2[nt][e];
         if constexpr (kQuant) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // p * 2^(e + 112): p <= 2^8 and e <= 7, and a stored byte is 2^-120
-            // of its value, so the output accumulates in units of 2^8
-            kf[h][e] = good[h] ? row_scale(kexp[h][e]) : 0.f;
+          for (int e = 0; e < 2; ++e) kf[h][e] = good[h] ? row_scale(kexp[h][e]) : 0.f;
+        }
+      }
+      // V's scales go into the weights: w 2^(e - unit + 14) in f16, unit the
+      // largest exponent so far, so nothing exceeds 2^14, and full precision is
+      // kept down to 2^-28 of a weight of one on the largest rows.  The output
+      // accumulates in units of 2^(unit - 14).
+      float regrade = 1.f;
+      if constexpr (kQuant) {
+        int top = 0;
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (good[h] && vexp[h][e] != kExpNan) top = max(top, vexp[h][e]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (top > unit) {
+          regrade = pow2f(max(unit - top, -126));
+          unit = top;
+        }
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
             vf[h][e] = !good[h] ? 0.f
                        : vexp[h][e] == kExpNan ? __int_as_float(0x7fffffff)
-                                               : pow2f(vexp[h][e] - kExpBias + 112);
-          }
-        }
+                                               : pow2f(max(vexp[h][e] - unit, -126) + 14);
       }
       // the next tile's K, into the registers that this one has left
       if (more) {
@@ -398,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           alpha[nt][e] = 1.f;
-          if (mx > m[nt][e] + kRescaleThreshold) {   // from -inf: any finite score
+          // from -inf: any finite score.  f16 weights leave no room above one.
+          if (mx > m[nt][e] + (kQuant ? 0.f : kRescaleThreshold)) {
             alpha[nt][e] = tc::ex2(m[nt][e] - mx);
             m[nt][e] = mx;
             moved = true;
@@ -415,17 +450,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
         }
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
-          pf[h][nt][0] = transpose8x8(tc::pack_bf16x2(sc[h][nt][0], sc[h][nt][1]));
-          pf[h][nt][1] = transpose8x8(tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
+          pf[h][nt][0] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][0], sc[h][nt][1])
+                                             : tc::pack_bf16x2(sc[h][nt][0], sc[h][nt][1]));
+          pf[h][nt][1] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][2], sc[h][nt][3])
+                                             : tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
         }
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, moved) || (kQuant && regrade != 1.f)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const float a[2] = {alpha[nt][0] * regrade, alpha[nt][1] * regrade};
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[nt][e & 1];
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= a[e & 1];
+        }
       }
 
       // O^T += V^T P^T
@@ -436,20 +475,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           const uint32_t(*va)[C::kVWords] = &vreg[h][cs * 4];
 #pragma unroll
           for (int x = 0; x < C::kVWords; ++x) {
-            // low and high halves of a word: of bf16 values 0 and 1, of e4m3 0, 1 and 2, 3
-            const uint32_t ab0 = __byte_perm(va[0][x], va[1][x], 0x5410);
-            const uint32_t ab1 = __byte_perm(va[0][x], va[1][x], 0x7632);
-            const uint32_t cd0 = __byte_perm(va[2][x], va[3][x], 0x5410);
-            const uint32_t cd1 = __byte_perm(va[2][x], va[3][x], 0x7632);
+            // bf16: values 0 and 1 of the word, of two keys each; e4m3: 0, 1 and 2, 3
+            const uint32_t ab0 = __byte_perm(va[0][x], va[1][x], kQuant ? 0x5140 : 0x5410);
+            const uint32_t ab1 = __byte_perm(va[0][x], va[1][x], kQuant ? 0x7362 : 0x7632);
+            const uint32_t cd0 = __byte_perm(va[2][x], va[3][x], kQuant ? 0x5140 : 0x5410);
+            const uint32_t cd1 = __byte_perm(va[2][x], va[3][x], kQuant ? 0x7362 : 0x7632);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               if constexpr (!kQuant) {
                 mma16816(o[nt][cs * 4 + x], ab0, ab1, cd0, cd1, pf[h][nt][0], pf[h][nt][1]);
               } else {
-                mma16816(o[nt][2 * x], even_bytes(ab0), odd_bytes(ab0), even_bytes(cd0),
-                         odd_bytes(cd0), pf[h][nt][0], pf[h][nt][1]);
-                mma16816(o[nt][2 * x + 1], even_bytes(ab1), odd_bytes(ab1), even_bytes(cd1),
-                         odd_bytes(cd1), pf[h][nt][0], pf[h][nt][1]);
+                mma16816_f16(o[nt][2 * x], f16_low(ab0), f16_high(ab0), f16_low(cd0),
+                             f16_high(cd0), pf[h][nt][0], pf[h][nt][1]);
+                mma16816_f16(o[nt][2 * x + 1], f16_low(ab1), f16_high(ab1), f16_low(cd1),
+                             f16_high(cd1), pf[h][nt][0], pf[h][nt][1]);
               }
             }
           }
@@ -460,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
 
     // ---- this lane's columns: D / 8 dims each of rows 2 t and 2 t + 1, in runs
     // of 2 KR consecutive ones
+    const float grade = kQuant && unit > 0 ? pow2f(unit - kExpBias - 14) : 1.f;
     constexpr int KR = !kQuant && D == 128 ? 4 : D / 16;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -470,9 +510,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
         const int r = nt * 8 + 2 * t + e;
         if (r >= R) continue;
         const int i = r / p.G, h = hk * p.G + r - i * p.G;
-        const float unit = kQuant ? 256.f : 1.f;
         if (parts <= 1) {
-          const float inv = m[nt][e] == -INFINITY ? 0.f : unit / l[nt][e];
+          const float inv = m[nt][e] == -INFINITY ? 0.f : grade / l[nt][e];
           __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D;
 #pragma unroll
           for (int mt = 0; mt < D / 16; mt += 4) {
@@ -490,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           for (int mt = 0; mt < D / 16; mt += 2) {
             const int d = g * 2 * KR + 16 * KR * (mt / KR) + 2 * (mt % KR);
             *reinterpret_cast<float4 *>(p.dec_o + slot * D + d) =
-                make_float4(o[nt][mt][e] * unit, o[nt][mt][e + 2] * unit, o[nt][mt + 1][e] * unit,
-                            o[nt][mt + 1][e + 2] * unit);
+                make_float4(o[nt][mt][e] * grade, o[nt][mt][e + 2] * grade, o[nt][mt + 1][e] * grade,
+                            o[nt][mt + 1][e + 2] * grade);
           }
           if (g == 0) p.dec_ml[slot] = make_float2(m[nt][e], l[nt][e]);
         }
