@@ -2,31 +2,36 @@
 // steps of a few tokens (up to 16 rows of one K/V head's group).
 //
 // Bound by the cache's bytes: each is used for 2 to 16 rows only.  So the
-// kernel is built around a stream of loads that never waits for anything: a
-// unit is one (sequence, K/V head, part of the keys), its four warps take
-// 16-key tiles in turn, and every lane fetches, with 16-byte cp.async into
-// slots of its own, exactly the bytes that it later feeds to the tensor core
-// from registers.  Nothing in the loop waits for another warp, no
-// swizzle or transposing load is needed, and a tile needs no staging beyond
-// the slots, three to four tiles deep.
+// kernel is built around a stream of copies: a unit is one (sequence, K/V
+// head, part of the keys) and belongs to one warp, which fetches its tiles
+// with TMA into a ring of its own and waits for nobody else.  Twelve warps
+// share an SM; a tile is 8 KB of K and V, so some 100 KB are in flight per SM.
+// Against fetching into registers (16 loads a lane and their addresses for
+// every tile) the copies cost four instructions of one lane.
 //
 // The products run with the keys as the M side of m16n8k16 MMAs, so that 8
 // query rows fill a tile (N = 8) that 16 rows of padding would waste:
 //   S^T [16 keys, 8 rows] = K [16 keys, D] Q^T
 //   O^T [D, 8 rows]      += V^T [D, 16 keys] P^T [16 keys, 8 rows]
 // The sum over D may run in any order as long as K and Q agree, so a lane
-// takes its four (e4m3: four) values of a k-step from one 16-byte vector of a
-// row; V^T's rows may be numbered in any order too, so a lane's V values come
-// from one 16-byte vector of each of its four keys, paired by byte permutes.
-// P^T's B operand is S^T's accumulator transposed in 8x8 blocks (movmatrix).
+// takes its four values of a k-step from one 16-byte vector of a row; V^T's
+// rows may be numbered in any order too, so a lane's V values come from one
+// 16-byte vector of each of its four keys, paired by byte permutes.  P^T's B
+// operand is S^T's accumulator transposed in 8x8 blocks (movmatrix).  Keys of
+// a run may stand in any order as well: key_of() takes them in one in which
+// the lanes that read together (rows 2a and 2a + 1 of K, even or odd rows of
+// V) fall on different banks of the 128-byte swizzle.
 //
-// 8-bit rows are widened in registers (paged.cuh).
+// 8-bit rows become f16, which holds e4m3 exactly, one conversion for two
+// values; the rows' scales go to the scores (K) and into the weights (V).
+#include <cuda.h>
 #include <math.h>
 
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_launch.h"
 #include "tc_ptx.cuh"
+#include "tma_map.h"
 
 namespace pa {
 namespace {
@@ -35,14 +40,21 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 
-// 16 bytes that are read once.
-__device__ __forceinline__ uint4 load_stream(const uint8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (~2 s)
+constexpr long long kDrainLimit = 400000000LL;
+
+// 16 bytes (aligned) to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load16(uint32_t dst, const void *src, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];\n" ::"r"(
+          dst),
+      "l"(src), "r"(bar)
+      : "memory");
 }
+
+// Key of a run of 8 that stands in row x of an MMA (see the head of the file):
+// 0 4 3 7 5 1 6 2.
+__device__ __forceinline__ int key_of(int x) { return (0x26157340 >> (4 * x)) & 7; }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -84,9 +96,24 @@ struct Cfg {
   static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8; // a lane's V vector
   static constexpr int kVSets = kRowBytes / (8 * kVBytes);  // vectors of one key
   static constexpr int kVWords = kVBytes / 4;
-  static constexpr int kHalves = kQuant ? 2 : 1;            // 16-key halves of a tile
+  static constexpr int kHalves = kRowBytes == 256 ? 1 : 2;  // 16-key runs of a tile
   static constexpr int kTileKeys = 16 * kHalves;
-  static constexpr int kCtas = (NT == 1 ? 4 : 3) - (D == 128 ? 1 : 0);   // CTAs that share an SM
+  // A run in shared memory: 16 rows of 128 swizzled bytes, two such blocks for
+  // rows of 256 bytes; rows of 64 bytes as they are.
+  static constexpr int kBlocks = kRowBytes == 256 ? 2 : 1;
+  static constexpr int kLine = kRowBytes / kBlocks;
+  static constexpr int kRunBytes = 16 * kRowBytes;
+  // a stage: K runs, V runs, then (8-bit) 16 exponent bytes of each
+  static constexpr int kExpOff = 2 * kHalves * kRunBytes;
+  static constexpr int kStageBytes = kExpOff + (kQuant ? 1024 : 0);   // 1024: the swizzle's period
+  static constexpr int kStageTx = kExpOff + (kQuant ? 2 * kHalves * 16 : 0);
+  static constexpr int kCtas = NT == 1 || D == 64 ? 3 : 2;  // CTAs that share an SM
+  static constexpr int kRoom = 233472 / kCtas - 1024 - 1024;
+  static constexpr int kFit = kRoom / (kWarps * kStageBytes);
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kBarOff = kWarps * kStages * kStageBytes;
+  static constexpr int kSmem = kBarOff + kWarps * (kStages + 1) * 8;   // a flag's place for each warp
+  static_assert(kStages >= 2, "no ring");
 };
 
 // Walks the units of the call, (sequence, part of its keys, K/V head), heads
@@ -153,16 +180,39 @@ struct Walk {
 // Every warp walks units of its own: its number, its number + all warps, ...
 template <int D, bool kQuant, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
-    paged_decode_kernel(const PagedAttnParams p) {
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
   using C = Cfg<D, kQuant, NT>;
   constexpr int kTile = C::kTileKeys;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int page_mask = (1 << p.c.page_shift) - 1;
-  const int row_stride = p.c.Hkv * C::kRowBytes;   // at most 4096 heads of 256 bytes
+  if (tc::smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) record_error(p.status, PA_DEVICE_ERR_SMEM_ALIGN);
+    return;
+  }
+  uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
+  const uint32_t ring_u = tc::smem_u32(ring);
+  const uint32_t bars = tc::smem_u32(smem + C::kBarOff) + warp * (C::kStages + 1) * 8;
+  volatile int32_t *gave_up = reinterpret_cast<volatile int32_t *>(
+      smem + C::kBarOff + (warp * (C::kStages + 1) + C::kStages) * 8);
+  if (lane == 0) {
+    for (int x = 0; x < C::kStages; ++x) tc::mbar_init(bars + 8 * x, 1);
+    *gave_up = 0;
+    tc::fence_mbar_init();
+  }
+  __syncwarp();
+  const bool lead = tc::elect_one();
+  // this lane's places in a run: K rows g and g + 8, V rows of four keys
+  const int kkey = key_of(g);
+  const int vkey[2] = {key_of(2 * t), key_of(2 * t + 1)};
+  uint32_t issued = 0, used = 0;   // tiles of this warp so far
+  uint32_t bad = 0;                // bit (stage * halves + run): no such page, or past the part
+  bool ok = true;
   Walk w;
   const bool report = blockIdx.x == 0 && warp == 0;
   w.open(p, report);
-  for (int u = blockIdx.x * kWarps + warp; w.seek(p, u, report); u += gridDim.x * kWarps) {
+  for (int u = blockIdx.x * kWarps + warp; ok && w.seek(p, u, report); u += gridDim.x * kWarps) {
     const int lq = w.s_lq, lk = w.s_lk, hk = w.hk, R = lq * p.G;
     const int keys_part = decode_part(lk, p.c.Hkv), parts = decode_parts(lk, p.c.Hkv);
     const int k0 = w.part * keys_part, keys = min(lk - k0, keys_part);
@@ -177,81 +227,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
     };
     int32_t pages = load_pages(0), pages_next = load_pages(32);
 
-    // ---- one tile's bytes, as the products take them
-    uint4 kreg[C::kHalves][C::kKVecs];
-    uint32_t vreg[C::kHalves][4 * C::kVSets][C::kVWords];
-    int kexp[C::kHalves][2], vexp[C::kHalves][2];   // of keys g and g + 8
-    int64_t at[C::kHalves];      // first byte of the run's rows of this head
-    bool good[C::kHalves];
-    auto locate = [&](int n) {   // tile n's runs
+    // copies of tile n into the ring's next stage
+    auto issue = [&](int n) {
+      const uint32_t st = issued % C::kStages, dst = ring_u + st * C::kStageBytes;
+      const uint32_t bar = bars + 8 * st;
+      if (n > 0 && (n * C::kHalves & 31) == 0) {
+        pages = pages_next;
+        pages_next = load_pages(n * C::kHalves + 32);
+      }
+      if (lead) tc::mbar_arrive_expect_tx(bar, C::kStageTx);
 #pragma unroll
       for (int h = 0; h < C::kHalves; ++h) {
         const int run = n * C::kHalves + h;
         int32_t page = __shfl_sync(0xffffffffu, pages, run & 31);
-        good[h] = run < runs && page_ok(p.c, page);
-        if (!good[h] && run < runs && lane == 0) record_error(p.status, PA_DEVICE_ERR_PAGE);
+        const bool there = run < runs, good = there && page_ok(p.c, page);
+        const uint32_t bit = 1u << (st * C::kHalves + h);
+        bad = good ? bad & ~bit : bad | bit;
+        if (there && !good && lead) record_error(p.status, PA_DEVICE_ERR_PAGE);
+        if (!good) page = -1;   // lands as zeros
         const int row0 = (k0 + run * 16) & page_mask;
-        if (!good[h]) page = 0;
-        at[h] = page * p.c.page_stride * (kQuant ? 1 : 2) + row0 * row_stride + hk * C::kRowBytes;
-        if (kQuant && good[h]) {
-          const int64_t ex = exp_offset(p.c, page, row0, hk);
+        if (lead) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = min(g + 8 * e, max(lk - 1 - k0 - run * 16, 0));
-            kexp[h][e] = __ldg(p.c.k_exp + ex + row);
-            vexp[h][e] = __ldg(p.c.v_exp + ex + row);
+          for (int x = 0; x < C::kBlocks; ++x) {
+            tc::tma_load_4d(dst + h * C::kRunBytes + x * 2048, &tm_k, bar, x * 64, hk, row0, page);
+            tc::tma_load_4d(dst + (C::kHalves + h) * C::kRunBytes + x * 2048, &tm_v, bar, x * 64, hk,
+                            row0, page);
+          }
+          if (kQuant) {
+            const int64_t ex = exp_offset(p.c, good ? page : 0, row0, hk);
+            bulk_load16(dst + C::kExpOff + h * 16, p.c.k_exp + ex, bar);
+            bulk_load16(dst + C::kExpOff + (C::kHalves + h) * 16, p.c.v_exp + ex, bar);
           }
         }
       }
+      ++issued;
     };
-    // Rows past the sequence's last key are read as that key: their weights are
-    // zero, and what lies past it is never touched.
-    auto load_k = [&](int n) {
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) {
-        const int last = max(lk - 1 - k0 - (n * C::kHalves + h) * 16, 0);
-        const uint8_t *src = static_cast<const uint8_t *>(p.c.k) + at[h] + t * 16;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t *row = src + min(g + 8 * e, last) * row_stride;
-#pragma unroll
-          for (int v = 0; v < C::kKVecs / 2; ++v)
-            kreg[h][2 * v + e] = good[h] ? load_stream(row + v * 64) : make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-    };
-    auto load_v = [&](int n) {
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) {
-        const int last = max(lk - 1 - k0 - (n * C::kHalves + h) * 16, 0);
-        const uint8_t *src = static_cast<const uint8_t *>(p.c.v) + at[h] + g * C::kVBytes;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint8_t *row = src + min(2 * t + (kk & 1) + 8 * (kk >> 1), last) * row_stride;
-#pragma unroll
-          for (int cs = 0; cs < C::kVSets; ++cs) {
-            uint32_t(&v)[C::kVWords] = vreg[h][cs * 4 + kk];
-            if constexpr (C::kVBytes == 16) {
-              const uint4 x = good[h] ? load_stream(row + cs * 128) : make_uint4(0u, 0u, 0u, 0u);
-              v[0] = x.x;
-              v[1] = x.y;
-              v[2] = x.z;
-              v[3] = x.w;
-            } else {
-              const uint2 x = good[h] ? __ldg(reinterpret_cast<const uint2 *>(row))
-                                      : make_uint2(0u, 0u);
-              v[0] = x.x;
-              v[1] = x.y;
-            }
-          }
-        }
-      }
-    };
-    if (n_tiles > 0) {
-      locate(0);
-      load_k(0);
-      load_v(0);
-    }
+    for (int n = 0; n < C::kStages - 1 && n < n_tiles; ++n) issue(n);
 
     // Q^T, the B operand of every S^T product.  Over an 8-bit cache it is f16,
     // each row scaled by a power of two to the top of f16's range (what that
@@ -326,11 +337,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
     int unit = 0;   // exponent byte that the output's units go by (8-bit caches)
     for (int n = 0; n < n_tiles; ++n) {
       const int key = k0 + n * kTile;
-      const bool more = n + 1 < n_tiles;
+      // every lane has read the stage that is filled next (the tile before this one)
+      __syncwarp();
+      if (n + C::kStages - 1 < n_tiles) issue(n + C::kStages - 1);
+      const uint32_t stage = used % C::kStages;
+      ok = tc::bounded_wait(bars + 8 * stage, (used / C::kStages) & 1u, gave_up, p.status, kWaitLimit);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      ++used;
+      const uint8_t *st = ring + stage * C::kStageBytes;
+      const uint32_t bad_runs = bad >> (stage * C::kHalves);
+      // byte address of 16-byte vector `vec` of row `row` of a run
+      auto vector = [&](const uint8_t *run, int row, int vec) -> const uint8_t * {
+        if constexpr (C::kLine == 128)
+          return run + (vec >> 3) * 2048 + row * 128 + (((vec & 7) ^ (row & 7)) << 4);
+        else
+          return run + row * C::kLine + (vec << 4);
+      };
 
       // S^T = K Q^T, in two chains
       float sc[C::kHalves][NT][4];
       float kf[C::kHalves][2], vf[C::kHalves][2];
+      int vexp[C::kHalves][2];   // of keys key_of(g) and 8 later
 #pragma unroll
       for (int h = 0; h < C::kHalves; ++h) {
         float s2[NT][4];
@@ -340,7 +370,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           for (int e = 0; e < 4; ++e) sc[h][nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < C::kKVecs / 2; ++i) {
-          const uint4 a = kreg[h][2 * i], c = kreg[h][2 * i + 1];
+          const uint8_t *run = st + h * C::kRunBytes;
+          const uint4 a = *reinterpret_cast<const uint4 *>(vector(run, kkey, t + 4 * i));
+          const uint4 c = *reinterpret_cast<const uint4 *>(vector(run, kkey + 8, t + 4 * i));
           if constexpr (!kQuant) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -366,7 +398,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           for (int e = 0; e < 4; ++e) sc[h][nt][e] += s2[nt][e];
         if constexpr (kQuant) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) kf[h][e] = good[h] ? row_scale(kexp[h][e]) : 0.f;
+          for (int e = 0; e < 2; ++e) {
+            // bytes of rows that are not the sequence's may be anything
+            const bool mine = key + 16 * h + 8 * e + kkey < lk && !(bad_runs >> h & 1u);
+            const uint8_t *ex = st + C::kExpOff + h * 16 + 8 * e + kkey;
+            kf[h][e] = mine ? row_scale(ex[0]) : 0.f;
+            vexp[h][e] = mine ? ex[C::kHalves * 16] : 0;
+          }
         }
       }
       // V's scales go into the weights: w 2^(e - unit + 14) in f16, unit the
@@ -380,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
         for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (good[h] && vexp[h][e] != kExpNan) top = max(top, vexp[h][e]);
+            if (vexp[h][e] != kExpNan) top = max(top, vexp[h][e]);
         top = __reduce_max_sync(0xffffffffu, top);
         if (top > unit) {
           regrade = pow2f(max(unit - top, -126));
@@ -390,18 +428,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
         for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            vf[h][e] = !good[h] ? 0.f
+            vf[h][e] = vexp[h][e] == 0 ? 0.f
                        : vexp[h][e] == kExpNan ? __int_as_float(0x7fffffff)
                                                : pow2f(max(vexp[h][e] - unit, -126) + 14);
-      }
-      // the next tile's K, into the registers that this one has left
-      if (more) {
-        if (((n + 1) * C::kHalves & 31) == 0) {
-          pages = pages_next;
-          pages_next = load_pages((n + 1) * C::kHalves + 32);
-        }
-        locate(n + 1);
-        load_k(n + 1);
       }
 
       // online softmax over the tile's keys, all lanes of a column in step
@@ -420,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           if (key + kTile > all_see) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (key + 16 * h + g + 8 * (e >> 1) >= lim[nt][e & 1]) sc[h][nt][e] = -INFINITY;
+              if (key + 16 * h + kkey + 8 * (e >> 1) >= lim[nt][e & 1]) sc[h][nt][e] = -INFINITY;
           }
         }
 #pragma unroll
@@ -472,7 +501,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
       for (int h = 0; h < C::kHalves; ++h) {
 #pragma unroll
         for (int cs = 0; cs < C::kVSets; ++cs) {
-          const uint32_t(*va)[C::kVWords] = &vreg[h][cs * 4];
+          uint32_t va[4][C::kVWords];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int row = vkey[kk & 1] + 8 * (kk >> 1);
+            const uint8_t *run = st + (C::kHalves + h) * C::kRunBytes;
+            if constexpr (C::kVBytes == 16) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(vector(run, row, g + 8 * cs));
+              va[kk][0] = x.x;
+              va[kk][1] = x.y;
+              va[kk][2] = x.z;
+              va[kk][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2 *>(run + row * C::kLine + g * 8);
+              va[kk][0] = x.x;
+              va[kk][1] = x.y;
+            }
+          }
+          if (key + kTile > lk) {   // rows past the last key: weight 0, whatever they hold
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (key + 16 * h + vkey[kk & 1] + 8 * (kk >> 1) >= lk)
+#pragma unroll
+                for (int x = 0; x < C::kVWords; ++x) va[kk][x] = 0u;
+          }
 #pragma unroll
           for (int x = 0; x < C::kVWords; ++x) {
             // bf16: values 0 and 1 of the word, of two keys each; e4m3: 0, 1 and 2, 3
@@ -494,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
           }
         }
       }
-      if (more) load_v(n + 1);
     }
 
     // ---- this lane's columns: D / 8 dims each of rows 2 t and 2 t + 1, in runs
@@ -538,6 +589,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
     }
   }
   tc::griddep_launch_dependents();
+  if (!ok) {   // give the copies already issued a bounded chance to land
+    for (; used < issued; ++used)
+      tc::drain_wait(bars + 8 * (used % C::kStages), (used / C::kStages) & 1u, kDrainLimit);
+  }
 }
 
 // Joins the parts of every row that has more than one: a CTA per row, its four
@@ -588,14 +643,39 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttn
   }
 }
 
+// Rows of a page as (D, Hkv, row, page): a box is one head's rows of a run.
+bool make_map(CUtensorMap *map, const void *ptr, const PagedCache &c, bool quant) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t es = quant ? 1 : 2, D = c.D, H = c.Hkv;
+  const cuuint64_t dims[4] = {D, H, cuuint64_t{1} << c.page_shift,
+                              static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {D * es, H * D * es, static_cast<cuuint64_t>(c.page_stride) * es};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(quant ? D : 64), 1, 16, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             quant && D == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool kQuant, int NT>
 cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
+  constexpr int smem = Cfg<D, kQuant, NT>::kSmem;
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, p.c.k, p.c, kQuant) || !make_map(&mv, p.c.v, p.c, kQuant))
+    return cudaErrorInvalidValue;
+  static unsigned long long configured = 0;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_decode_kernel<D, kQuant, NT>),
+                                smem, configured);
+  if (e != cudaSuccess) return e;
   const int64_t most =
       (static_cast<int64_t>(p.dec_parts) * p.c.Hkv * p.batch + kWarps - 1) / kWarps;
   const int64_t ctas = static_cast<int64_t>(num_sms) * Cfg<D, kQuant, NT>::kCtas;
   paged_decode_kernel<D, kQuant, NT>
-      <<<static_cast<unsigned>(most < ctas ? most : ctas), kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+      <<<static_cast<unsigned>(most < ctas ? most : ctas), kThreads, smem, stream>>>(mk, mv, p);
+  e = cudaGetLastError();
   if (e != cudaSuccess || p.dec_parts == 1) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
