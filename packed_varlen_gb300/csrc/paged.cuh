@@ -137,9 +137,13 @@ constexpr int kDecodeRows = 16;
 constexpr int kDecodeUnits = 1824;   // parts of a lone sequence: twelve warps for each of 152 SMs
 
 // Smallest part: short contexts are bound by latency and want many small
-// parts, long ones by bytes and want few partial results.
+// parts, long ones by bytes and want few partial results, but enough parts for
+// an even load.  64 / 256 keys against others, GPU time: a step of four
+// contexts of 180-700 tokens 10.5 us (128: 11.7), one of 8000 17.8 us (512:
+// 25.0), 64 of 900-8000 185 us (512: 192), 96 8-bit ones of 2-12k 281 us (512:
+// 274, 1024: 267).
 __host__ __device__ __forceinline__ int decode_min_part(int lk) {
-  return lk <= 1024 ? 128 : lk <= 16384 ? 256 : 512;
+  return lk <= 1024 ? 64 : 256;
 }
 __host__ __device__ __forceinline__ int decode_most_parts(int Hkv) {
   return Hkv >= kDecodeUnits ? 1 : kDecodeUnits / Hkv;
@@ -160,8 +164,7 @@ __host__ __device__ __forceinline__ int decode_parts(int lk, int Hkv) {
 inline int decode_parts_bound(int max_k, int Hkv) {
   if (max_k <= 0) return 1;
   int64_t n = (static_cast<int64_t>(max_k) + decode_min_part(max_k) - 1) / decode_min_part(max_k);
-  if (max_k > 1024 && n < 8) n = 8;
-  if (max_k > 16384 && n < 64) n = 64;
+  if (max_k > 1024 && n < 16) n = 16;   // shorter sequences have smaller parts
   const int most = decode_most_parts(Hkv);
   return static_cast<int>(n < most ? n : most);
 }

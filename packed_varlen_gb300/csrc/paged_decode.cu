@@ -588,22 +588,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
       }
     }
   }
-  tc::griddep_launch_dependents();
   if (!ok) {   // give the copies already issued a bounded chance to land
     for (; used < issued; ++used)
       tc::drain_wait(bars + 8 * (used % C::kStages), (used / C::kStages) & 1u, kDrainLimit);
   }
 }
 
-// Joins the parts of every row that has more than one: a CTA per row, its four
-// warps over the parts, a lane over D / 32 dims.
-template <int D>
-__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttnParams p) {
+// Joins the parts of every row that has more than one, a lane over D / 32
+// dims.  The parts go to eight sums in turn, and these are added in order: by
+// eight warps that have a sum each (kWide: few rows with many parts, where
+// latency is all there is to it; one sequence with 228 parts and 32 rows takes
+// 92 us in all, 102 with four warps to a row), or by one warp that has them
+// all (many rows with few parts).  The same bits either way.
+constexpr int kSums = 8;
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kWide ? 256 : 128) paged_combine_kernel(const PagedAttnParams p) {
   constexpr int E = D / 32;
-  __shared__ float acc_s[kWarps][D];
-  __shared__ float sum_s[kWarps];
+  __shared__ float acc_s[kWide ? kSums : 1][D];
+  __shared__ float sum_s[kSums];
   tc::griddep_wait();
-  const int b = blockIdx.y, row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, row = kWide ? blockIdx.x : blockIdx.x * 4 + warp;
   const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
   int err;
   const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
@@ -611,36 +617,84 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttn
   const int parts = decode_parts(s.lk, p.c.Hkv);
   if (parts <= 1) return;
   const int64_t slot0 = static_cast<int64_t>(b) * p.dec_parts * p.dec_rows + row;
+  auto slot_of = [&](int n) { return slot0 + static_cast<int64_t>(n) * p.dec_rows; };
   float top = -INFINITY;
-  for (int n = lane; n < parts; n += 32)
-    top = fmaxf(top, p.dec_ml[slot0 + static_cast<int64_t>(n) * p.dec_rows].x);
+  for (int n = lane; n < parts; n += 32) top = fmaxf(top, p.dec_ml[slot_of(n)].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float base = top == -INFINITY ? 0.f : top;
-  float acc[E], sum = 0.f;
+  const float ref = top == -INFINITY ? 0.f : top;
+
+  // eight parts in flight: of this warp's sum, or one of each sum
+  constexpr int kOwn = kWide ? 1 : kSums;
+  float acc[kOwn][E], sum[kOwn];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int n = warp; n < parts; n += kWarps) {
-    const int64_t slot = slot0 + static_cast<int64_t>(n) * p.dec_rows;
-    const float2 v = p.dec_ml[slot];
-    const float f = tc::ex2(v.x - base);
-    sum += f * v.y;
-    const float *src = p.dec_o + slot * D + lane * E;
+  for (int y = 0; y < kOwn; ++y) {
+    sum[y] = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += f * src[e];
+    for (int e = 0; e < E; ++e) acc[y][e] = 0.f;
   }
+  constexpr int kStep = kWide ? kSums : 1;
+  for (int n0 = kWide ? warp : 0; n0 < parts; n0 += 8 * kStep) {
+    float2 v[8];
+    float o[8][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
-  if (lane == 0) sum_s[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x;
-    const float total = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
-    const float v = acc_s[0][d] + acc_s[1][d] + acc_s[2][d] + acc_s[3][d];
-    p.out[(static_cast<int64_t>(s.q0) * p.Hq + row) * D + d] =
-        __float2bfloat16(v * (top == -INFINITY ? 0.f : 1.f / total));   // NaN stays NaN
+    for (int x = 0; x < 8; ++x) {
+      const int n = n0 + x * kStep;
+      v[x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[x][e] = 0.f;
+      if (n < parts) {
+        v[x] = p.dec_ml[slot_of(n)];
+        const float *src = p.dec_o + slot_of(n) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(src);
+          o[x][0] = y.x;
+          o[x][1] = y.y;
+          o[x][2] = y.z;
+          o[x][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2 *>(src);
+          o[x][0] = y.x;
+          o[x][1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float f = tc::ex2(v[x].x - ref);
+      sum[x % kOwn] += f * v[x].y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[x % kOwn][e] += f * o[x][e];
+    }
   }
+  float total = 0.f, out[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = 0.f;
+  if constexpr (kWide) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[0][e];
+    if (lane == 0) sum_s[warp] = sum[0];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int y = 0; y < kSums; ++y) {
+      total += sum_s[y];
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[e] += acc_s[y][lane * E + e];
+    }
+  } else {
+#pragma unroll
+    for (int y = 0; y < kSums; ++y) {
+      total += sum[y];
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[e] += acc[y][e];
+    }
+  }
+  const float inv = top == -INFINITY ? 0.f : 1.f / total;   // NaN stays NaN
+  uint32_t *dst = reinterpret_cast<uint32_t *>(
+      p.out + (static_cast<int64_t>(s.q0) * p.Hq + row) * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = tc::pack_bf16x2(out[e] * inv, out[e + 1] * inv);
 }
 
 // Rows of a page as (D, Hkv, row, page): a box is one head's rows of a run.
@@ -681,12 +735,14 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.dec_rows, p.batch);
-  cfg.blockDim = dim3(kThreads);
+  const bool wide = p.dec_parts > 64;
+  cfg.gridDim = dim3(wide ? p.dec_rows : (p.dec_rows + 3) / 4, p.batch);
+  cfg.blockDim = dim3(wide ? 256 : 128);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p);
+  return wide ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, true>, p)
+              : cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, false>, p);
 }
 
 }  // namespace
