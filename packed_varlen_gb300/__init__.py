@@ -397,75 +397,100 @@ def linear_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] =
 
 
 # ---------------------------------------------------------------- paged K/V cache
+# A step of single tokens takes some ten microseconds on the GPU, so these calls
+# keep their checks short: each is one test on the good path, and the functions
+# that name what is wrong run only where it fails.
 _CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
 
-def _need_rows(t: torch.Tensor, name: str, dev) -> int:
-    """A packed [T, H, D] bf16 tensor whose rows (one token) are contiguous;
-    returns the elements from one token to the next."""
+def _rows_stride(t: torch.Tensor, name: str, dev: int) -> int:
+    """Elements from one token to the next of a packed [T, H, D] bf16 tensor
+    whose rows (one token) are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on the cache's device {dev}, not {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device, not {t.device}")
     T, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
     sT, sH, sD = t.stride()
     if (D > 1 and sD != 1) or (H > 1 and sH != D):
         raise ValueError(f"the rows of {name} must be contiguous")
     return sT if T > 1 else H * D
 
 
-def _need_index(t: torch.Tensor, name: str, shape, dev):
-    _need(t, name, torch.int32, len(shape))
-    if t.device != dev:
-        raise ValueError(f"{name} must be on the cache's device {dev}, not {t.device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _need_index(t: torch.Tensor, name: str, n: int, dev: int):
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and \
+            t.is_contiguous() and t.dim() == 1 and t.numel() == n:
+        return
+    _need(t, name, torch.int32, 1)
+    raise ValueError(f"{name} must be [{n}] on the cache's device, got {list(t.shape)} on {t.device}")
+
+
+def _need_out(t: torch.Tensor, name: str, shape, dev: int):
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and \
+            t.is_contiguous() and t.shape == shape:
+        return
+    _need(t, name, torch.bfloat16, len(shape))
+    raise ValueError(f"{name} must be {list(shape)} on the cache's device")
+
+
+def _page_stride(t: torch.Tensor, name: str) -> int:
+    P, page, H, D = t.shape
+    s = t.stride()
+    if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (page > 1 and s[1] != H * D):
+        raise ValueError(f"each page of {name} must be contiguous")
+    return s[0] if P > 1 else page * H * D
 
 
 def _need_cache(k_cache, v_cache, k_exp, v_exp, page_table, batch):
-    """Checks the cache's tensors against each other; returns (device, format,
-    num_pages, page_size, Hkv, D, page_stride, k_exp address, v_exp address)."""
+    """Checks the cache's tensors against each other; returns (device index,
+    format, num_pages, page_size, Hkv, D, page_stride, k_exp address, v_exp
+    address)."""
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError(f"{n} must be a CUDA tensor")
-        if t.dtype not in _CACHE_FORMATS:
-            raise TypeError(f"{n} must be torch.bfloat16 or torch.float8_e4m3fn, got {t.dtype}")
-        if t.dim() != 4:
-            raise ValueError(f"{n} must be [num_pages, page_size, Hkv, D]")
-    dev = k_cache.device
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != dev:
+    dev = k_cache.get_device()
+    dtype, shape = k_cache.dtype, k_cache.shape
+    fmt = _CACHE_FORMATS.get(dtype)
+    if fmt is None or v_cache.dtype not in _CACHE_FORMATS:
+        raise TypeError("k_cache and v_cache must be torch.bfloat16 or torch.float8_e4m3fn, "
+                        f"got {dtype} and {v_cache.dtype}")
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [num_pages, page_size, Hkv, D]")
+    if v_cache.shape != shape or v_cache.dtype is not dtype or v_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must have the same shape, type and device")
-    P, page, H, D = k_cache.shape
-    strides = []
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        s = t.stride()
-        if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (page > 1 and s[1] != H * D):
-            raise ValueError(f"each page of {n} must be contiguous")
-        strides.append(s[0] if P > 1 else page * H * D)
-    if strides[0] != strides[1]:
-        raise ValueError("k_cache and v_cache must have the same page stride")
-    fmt = _CACHE_FORMATS[k_cache.dtype]
+    P, page, H, D = shape
+    if k_cache.is_contiguous() and v_cache.is_contiguous():
+        stride = page * H * D
+    else:
+        stride = _page_stride(k_cache, "k_cache")
+        if _page_stride(v_cache, "v_cache") != stride:
+            raise ValueError("k_cache and v_cache must have the same page stride")
     ke = ve = None
     if fmt == 1:
         if k_exp is None or v_exp is None:
             raise ValueError("an 8-bit cache needs k_exp and v_exp")
         for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-            _need(t, n, torch.uint8, 3)
-            if tuple(t.shape) != (P, H, page) or t.device != dev:
+            if not (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and
+                    t.get_device() == dev and t.is_contiguous() and t.shape == (P, H, page)):
+                _need(t, n, torch.uint8, 3)
                 raise ValueError(f"{n} must be [num_pages, Hkv, page_size] on the cache's device")
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
         raise ValueError("a bf16 cache has no k_exp and v_exp")
-    _need(page_table, "page_table", torch.int32, 2)
-    if page_table.device != dev or page_table.shape[0] != batch:
+    if not (isinstance(page_table, torch.Tensor) and page_table.dtype is torch.int32 and
+            page_table.get_device() == dev and page_table.is_contiguous() and
+            page_table.dim() == 2 and page_table.shape[0] == batch):
+        _need(page_table, "page_table", torch.int32, 2)
         raise ValueError("page_table must be [batch, table_pages] on the cache's device")
-    return dev, fmt, P, page, H, D, strides[0], ke, ve
+    return dev, fmt, P, page, H, D, stride, ke, ve
 
 
 class _On:
@@ -477,12 +502,12 @@ class _On:
     def __init__(self, dev, stream):
         self.dev, self.given, self.guard = dev, stream is not None, None
         if stream is None:
-            self.raw = torch.cuda.current_stream(dev).cuda_stream
+            self.raw = torch._C._cuda_getCurrentRawStream(dev)
         else:
             self.raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
     def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
+        if torch._C._cuda_getDevice() != self.dev:
             self.guard = torch.cuda.device(self.dev)
             self.guard.__enter__()
         return self.raw
@@ -493,10 +518,11 @@ class _On:
             self.guard = None
 
     def new(self, make, shape, dtype):
+        dev = torch.device("cuda", self.dev)
         if not self.given:
-            return make(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(torch.cuda.ExternalStream(self.raw, device=self.dev)):
-            return make(shape, dtype=dtype, device=self.dev)
+            return make(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.raw, device=dev)):
+            return make(shape, dtype=dtype, device=dev)
 
 
 def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -509,16 +535,16 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     [num_pages, page_size, Hkv, D] bf16, or float8_e4m3fn with exponent bytes
     k_exp, v_exp [num_pages, Hkv, page_size] uint8; k and v may be slices of a
     wider tensor along its last dimensions.  Returns (k_cache, v_cache)."""
-    lib = load_library()
+    lib = _lib or load_library()
     B = cu_seqlens.numel() - 1
     dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
                                                       page_table, B)
-    ks, vs = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (H, D):
+    ks, vs = _rows_stride(k, "k", dev), _rows_stride(v, "v", dev)
+    if k.shape != v.shape or k.shape[1:] != (H, D):
         raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
-    _need_index(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    _need_index(cu_seqlens, "cu_seqlens", B + 1, dev)
     if pos_offset is not None:
-        _need_index(pos_offset, "pos_offset", (B,), dev)
+        _need_index(pos_offset, "pos_offset", B, dev)
     with _On(dev, stream) as raw:
         st = lib.pa_kv_cache_write(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
                                    v_cache.data_ptr(), ke, ve, cu_seqlens.data_ptr(),
@@ -540,23 +566,21 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torc
     rows cu_seqlens[b].. of k_out and v_out [total, Hkv, D].  Rows past
     cu_seqlens[B] are left as they are (fresh outputs are zero-filled).
     Returns (k_out, v_out)."""
-    lib = load_library()
+    lib = _lib or load_library()
     B = cu_seqlens.numel() - 1
     dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
                                                       page_table, B)
-    _need_index(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    _need_index(cu_seqlens, "cu_seqlens", B + 1, dev)
     if pos_offset is not None:
-        _need_index(pos_offset, "pos_offset", (B,), dev)
+        _need_index(pos_offset, "pos_offset", B, dev)
     on = _On(dev, stream)
     with on as raw:
         if k_out is None:
             k_out = on.new(torch.zeros, (int(total), H, D), torch.bfloat16)
         if v_out is None:
             v_out = on.new(torch.zeros, (int(total), H, D), torch.bfloat16)
-        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-            _need(t, n, torch.bfloat16, 3)
-            if tuple(t.shape) != (total, H, D) or t.device != dev:
-                raise ValueError(f"{n} must be [total, Hkv, D] on the cache's device")
+        _need_out(k_out, "k_out", (int(total), H, D), dev)
+        _need_out(v_out, "v_out", (int(total), H, D), dev)
         st = lib.pa_kv_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
                                   k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(),
                                   None if pos_offset is None else pos_offset.data_ptr(),
@@ -590,32 +614,32 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     cu_seqlens_q[B] are not written (a fresh ``out`` is zero-filled).
     ``workspace`` (uint8, paged_attn_workspace_bytes) is allocated per call
     unless given; calls that may overlap need one each."""
-    lib = load_library()
+    lib = _lib or load_library()
     B = cu_seqlens_q.numel() - 1
     dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
                                                       page_table, B)
-    qs = _need_rows(q, "q", dev)
-    Tq, Hq = q.shape[0], q.shape[1]
-    if q.shape[2] != D or Hq < 1 or Hq % H:
+    qs = _rows_stride(q, "q", dev)
+    Tq, Hq, Dq = q.shape
+    if Dq != D or Hq < 1 or Hq % H:
         raise ValueError("q must be [Tq, Hq, D] with the cache's D and Hq a multiple of its Hkv")
-    _need_index(cu_seqlens_q, "cu_seqlens_q", (B + 1,), dev)
-    _need_index(seq_lens, "seq_lens", (B,), dev)
+    _need_index(cu_seqlens_q, "cu_seqlens_q", B + 1, dev)
+    _need_index(seq_lens, "seq_lens", B, dev)
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
+        scale = D ** -0.5
     need = lib.pa_paged_attn_workspace_bytes(B, Tq, int(max_q), int(max_k), Hq, H, D)
     on = _On(dev, stream)
     with on as raw:
         if out is None:
             out = on.new(torch.zeros, (Tq, Hq, D), torch.bfloat16)
+        else:
+            _need_out(out, "out", (Tq, Hq, D), dev)
         if workspace is None and need > 0:
             workspace = on.new(torch.empty, (need,), torch.uint8)
-        _need(out, "out", torch.bfloat16, 3)
-        if out.shape != q.shape or out.device != dev:
-            raise ValueError("out must have q's shape, on its device")
         wp, wn = None, 0
         if workspace is not None:
-            _need(workspace, "workspace", torch.uint8, 1)
-            if workspace.device != dev:
+            if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or \
+                    not workspace.is_contiguous():
+                _need(workspace, "workspace", torch.uint8)
                 raise ValueError("workspace must be on the cache's device")
             wp, wn = workspace.data_ptr(), workspace.numel()
         st = lib.pa_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
