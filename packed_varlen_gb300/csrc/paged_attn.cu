@@ -31,6 +31,7 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
   if (tokens > kDecodeRows / G) tokens = kDecodeRows / G;
   w.dec_parts = tokens > 0 ? decode_parts_bound(max_k, Hkv) : 1;
   w.dec_rows = tokens * Hq;
+  if (paged_decode_is_local(batch, tokens, max_k, G, Hkv)) w.dec_parts = 1;
   const int64_t slots = w.dec_parts > 1 ? static_cast<int64_t>(batch) * w.dec_parts * w.dec_rows : 0;
   // Sequences of the tiled kernel, and what their shares may leave: a share
   // has at least kChunkMinShare key tiles, and two parts of at most an item's

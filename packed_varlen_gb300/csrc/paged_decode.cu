@@ -36,8 +36,12 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;         // of a CTA of the streaming kernel
+constexpr int kLocalWarps = 8;    // of a CTA that joins its parts itself
+constexpr int kSums = 8;          // sums that parts are joined in
+// (sequence, K/V head) pairs that a call may have for that: two for each of 152 SMs.
+constexpr int kLocalUnits = 304;
+constexpr int kLocalParts = 16;   // parts that it has room for: those of 1024 keys
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (~2 s)
@@ -89,8 +93,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
 }
-template <int D, bool kQuant, int NT>
+template <int D, bool kQuant, int NT, bool kLocal>
 struct Cfg {
+  static constexpr int kCtaWarps = kLocal ? kLocalWarps : kWarps;
   static constexpr int kRowBytes = D * (kQuant ? 1 : 2);
   static constexpr int kKVecs = kRowBytes / 32;             // a lane's 16-byte K vectors of 16 keys
   static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8; // a lane's V vector
@@ -107,12 +112,14 @@ struct Cfg {
   static constexpr int kExpOff = 2 * kHalves * kRunBytes;
   static constexpr int kStageBytes = kExpOff + (kQuant ? 1024 : 0);   // 1024: the swizzle's period
   static constexpr int kStageTx = kExpOff + (kQuant ? 2 * kHalves * 16 : 0);
-  static constexpr int kCtas = NT == 1 || D == 64 ? 3 : 2;  // CTAs that share an SM
-  static constexpr int kRoom = 233472 / kCtas - 1024 - 1024;
-  static constexpr int kFit = kRoom / (kWarps * kStageBytes);
+  static constexpr int kCtas = kLocal ? 1 : NT == 1 || D == 64 ? 3 : 2;   // CTAs that share an SM
+  static constexpr int kPartBytes = kLocal ? kLocalParts * 8 * NT * (D + 2) * 4 : 0;
+  static constexpr int kRoom = 233472 / kCtas - 1024 - 1024 - kPartBytes;
+  static constexpr int kFit = kRoom / (kCtaWarps * kStageBytes);
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static constexpr int kBarOff = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kBarOff + kWarps * (kStages + 1) * 8;   // a flag's place for each warp
+  static constexpr int kPartOff = kCtaWarps * kStages * kStageBytes;
+  static constexpr int kBarOff = kPartOff + kPartBytes;
+  static constexpr int kSmem = kBarOff + kCtaWarps * (kStages + 1) * 8;   // a flag's place for each warp
   static_assert(kStages >= 2, "no ring");
 };
 
@@ -178,11 +185,15 @@ struct Walk {
 };
 
 // Every warp walks units of its own: its number, its number + all warps, ...
-template <int D, bool kQuant, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
+// kLocal: a CTA has one (sequence, K/V head), its warps the parts in turn, and
+// joins them in shared memory: one launch and no workspace, for calls of few
+// short contexts, whose time is latency.
+template <int D, bool kQuant, int NT, bool kLocal>
+__global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
+                                  Cfg<D, kQuant, NT, kLocal>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
-  using C = Cfg<D, kQuant, NT>;
+  using C = Cfg<D, kQuant, NT, kLocal>;
   constexpr int kTile = C::kTileKeys;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -206,13 +217,40 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
   // this lane's places in a run: K rows g and g + 8, V rows of four keys
   const int kkey = key_of(g);
   const int vkey[2] = {key_of(2 * t), key_of(2 * t + 1)};
+  float *part_o = reinterpret_cast<float *>(smem + C::kPartOff);   // kLocal: [part][row][D]
+  float2 *part_ml = reinterpret_cast<float2 *>(part_o + kLocalParts * 8 * NT * D);
   uint32_t issued = 0, used = 0;   // tiles of this warp so far
   uint32_t bad = 0;                // bit (stage * halves + run): no such page, or past the part
   bool ok = true;
   Walk w;
   const bool report = blockIdx.x == 0 && warp == 0;
-  w.open(p, report);
-  for (int u = blockIdx.x * kWarps + warp; ok && w.seek(p, u, report); u += gridDim.x * kWarps) {
+  if constexpr (kLocal) {
+    w.b = blockIdx.x / p.c.Hkv;
+    w.hk = blockIdx.x - w.b * p.c.Hkv;
+    int err;
+    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, w.b, p.total_q, p.max_q, p.max_k,
+                                 static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
+    if (err && w.hk == 0 && threadIdx.x == 0) record_error(p.status, err);
+    if (s.lq == 0 || s.lq > kDecodeRows / p.G) return;
+    w.s_q0 = s.q0;
+    w.s_lq = s.lq;
+    w.s_lk = s.lk;
+    w.total = max(decode_parts(s.lk, p.c.Hkv), 1);
+  } else {
+    w.open(p, report);
+  }
+  // the next unit: for a warp of a local CTA the next part
+  auto more_units = [&](int u) -> bool {
+    if constexpr (kLocal) {
+      w.part = u;
+      return u < w.total;
+    } else {
+      return w.seek(p, u, report);
+    }
+  };
+  const int u_first = kLocal ? warp : blockIdx.x * kWarps + warp;
+  const int u_step = kLocal ? kLocalWarps : gridDim.x * kWarps;
+  for (int u = u_first; ok && more_units(u); u += u_step) {
     const int lq = w.s_lq, lk = w.s_lk, hk = w.hk, R = lq * p.G;
     const int keys_part = decode_part(lk, p.c.Hkv), parts = decode_parts(lk, p.c.Hkv);
     const int k0 = w.part * keys_part, keys = min(lk - k0, keys_part);
@@ -576,15 +614,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
         } else {
           const int64_t slot = (static_cast<int64_t>(w.b) * p.dec_parts + w.part) * p.dec_rows +
                                static_cast<int64_t>(i) * p.Hq + h;
+          float *dst = kLocal ? part_o + (w.part * 8 * NT + r) * D : p.dec_o + slot * D;
 #pragma unroll
           for (int mt = 0; mt < D / 16; mt += 2) {
             const int d = g * 2 * KR + 16 * KR * (mt / KR) + 2 * (mt % KR);
-            *reinterpret_cast<float4 *>(p.dec_o + slot * D + d) =
+            *reinterpret_cast<float4 *>(dst + d) =
                 make_float4(o[nt][mt][e] * grade, o[nt][mt][e + 2] * grade, o[nt][mt + 1][e] * grade,
                             o[nt][mt + 1][e + 2] * grade);
           }
-          if (g == 0) p.dec_ml[slot] = make_float2(m[nt][e], l[nt][e]);
+          float2 *ml = kLocal ? part_ml + w.part * 8 * NT + r : p.dec_ml + slot;
+          if (g == 0) *ml = make_float2(m[nt][e], l[nt][e]);
         }
+      }
+    }
+  }
+  if constexpr (kLocal) {
+    // the join of paged_combine_kernel, sum for sum
+    if (w.total > 1) {
+      __syncthreads();
+      const int R = w.s_lq * p.G;
+      for (int x = threadIdx.x; x < R * (D / 4); x += kLocalWarps * 32) {
+        const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
+        float top = -INFINITY;
+        for (int n = 0; n < w.total; ++n) top = fmaxf(top, part_ml[n * 8 * NT + r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float total = 0.f;
+        float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < kSums; ++y) {
+          float sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int n = y; n < w.total; n += kSums) {
+            const float2 v = part_ml[n * 8 * NT + r];
+            const float4 o = *reinterpret_cast<const float4 *>(part_o + (n * 8 * NT + r) * D + d);
+            const float f = tc::ex2(v.x - ref);
+            sum += f * v.y;
+            acc.x += f * o.x;
+            acc.y += f * o.y;
+            acc.z += f * o.z;
+            acc.w += f * o.w;
+          }
+          total += sum;
+          out.x += acc.x;
+          out.y += acc.y;
+          out.z += acc.z;
+          out.w += acc.w;
+        }
+        const float inv = top == -INFINITY ? 0.f : 1.f / total;   // NaN stays NaN
+        const int i = r / p.G, h = w.hk * p.G + r - i * p.G;
+        *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D + d) =
+            make_uint2(tc::pack_bf16x2(out.x * inv, out.y * inv),
+                       tc::pack_bf16x2(out.z * inv, out.w * inv));
       }
     }
   }
@@ -600,8 +679,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kQuant, NT>::kCtas)
 // latency is all there is to it; one sequence with 228 parts and 32 rows takes
 // 92 us in all, 102 with four warps to a row), or by one warp that has them
 // all (many rows with few parts).  The same bits either way.
-constexpr int kSums = 8;
-
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kWide ? 256 : 128) paged_combine_kernel(const PagedAttnParams p) {
   constexpr int E = D / 32;
@@ -714,23 +791,25 @@ bool make_map(CUtensorMap *map, const void *ptr, const PagedCache &c, bool quant
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kQuant, int NT>
+template <int D, bool kQuant, int NT, bool kLocal>
 cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
-  constexpr int smem = Cfg<D, kQuant, NT>::kSmem;
+  using C = Cfg<D, kQuant, NT, kLocal>;
   CUtensorMap mk, mv;
   if (!make_map(&mk, p.c.k, p.c, kQuant) || !make_map(&mv, p.c.v, p.c, kQuant))
     return cudaErrorInvalidValue;
   static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_decode_kernel<D, kQuant, NT>),
-                                smem, configured);
+  cudaError_t e =
+      set_smem_once(reinterpret_cast<const void *>(paged_decode_kernel<D, kQuant, NT, kLocal>),
+                    C::kSmem, configured);
   if (e != cudaSuccess) return e;
-  const int64_t most =
-      (static_cast<int64_t>(p.dec_parts) * p.c.Hkv * p.batch + kWarps - 1) / kWarps;
-  const int64_t ctas = static_cast<int64_t>(num_sms) * Cfg<D, kQuant, NT>::kCtas;
-  paged_decode_kernel<D, kQuant, NT>
-      <<<static_cast<unsigned>(most < ctas ? most : ctas), kThreads, smem, stream>>>(mk, mv, p);
+  const int64_t units = static_cast<int64_t>(p.batch) * p.c.Hkv * (kLocal ? 1 : p.dec_parts);
+  const int64_t most = kLocal ? units : (units + kWarps - 1) / kWarps;
+  const int64_t ctas = kLocal ? units : static_cast<int64_t>(num_sms) * C::kCtas;
+  paged_decode_kernel<D, kQuant, NT, kLocal>
+      <<<static_cast<unsigned>(most < ctas ? most : ctas), C::kCtaWarps * 32, C::kSmem, stream>>>(
+          mk, mv, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.dec_parts == 1) return e;
+  if (e != cudaSuccess || kLocal || p.dec_parts == 1) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -747,18 +826,27 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
-                                cudaStream_t stream) {
+bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv) {
+  return tokens * G <= 8 && max_k <= 1024 && static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
+}
+
+template <int D, bool kQuant>
+cudaError_t launch_for(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
   // 8 columns where no sequence of the call can have more rows: a column's
   // results do not depend on the others, so this changes no bits
-  const int most = p.max_q < kDecodeRows / p.G ? p.max_q * p.G : kDecodeRows / p.G * p.G;
-  const bool wide = most > 8;
-  if (p.c.D == 128) {
-    if (quant) return wide ? launch<128, true, 2>(p, num_sms, stream) : launch<128, true, 1>(p, num_sms, stream);
-    return wide ? launch<128, false, 2>(p, num_sms, stream) : launch<128, false, 1>(p, num_sms, stream);
-  }
-  if (quant) return wide ? launch<64, true, 2>(p, num_sms, stream) : launch<64, true, 1>(p, num_sms, stream);
-  return wide ? launch<64, false, 2>(p, num_sms, stream) : launch<64, false, 1>(p, num_sms, stream);
+  const int few = kDecodeRows / p.G, tokens = p.max_q < few ? p.max_q : few;
+  if (paged_decode_is_local(p.batch, tokens, p.max_k, p.G, p.c.Hkv))
+    return launch<D, kQuant, 1, true>(p, num_sms, stream);
+  return tokens * p.G > 8 ? launch<D, kQuant, 2, false>(p, num_sms, stream)
+                          : launch<D, kQuant, 1, false>(p, num_sms, stream);
+}
+
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
+                                cudaStream_t stream) {
+  if (p.c.D == 128)
+    return quant ? launch_for<128, true>(p, num_sms, stream)
+                 : launch_for<128, false>(p, num_sms, stream);
+  return quant ? launch_for<64, true>(p, num_sms, stream) : launch_for<64, false>(p, num_sms, stream);
 }
 
 }  // namespace pa

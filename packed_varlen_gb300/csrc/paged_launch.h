@@ -11,6 +11,9 @@ struct PagedAttnParams;   // paged.cuh
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
                                 cudaStream_t stream);
 
+// Whether that kernel joins its parts itself and needs no workspace.
+bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv);
+
 // Longer sequences: tiled kernel, and the join of the parts that its shares leave.
 cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
                                cudaStream_t stream);

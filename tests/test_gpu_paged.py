@@ -413,6 +413,52 @@ def test_independent_of_the_batch(pv, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lq", [1, 2])
+def test_same_bits_whatever_the_bounds(pv, lq, fmt):
+    """The bounds max_q and max_k, and a large batch, choose among kernels; never a result."""
+    Hq, H, D, page = 8, 2, 128, 16
+    seq_lens = [1000, 64, 65, 1024, 1, 300, 129, 0]
+    lengths = [lq] * len(seq_lens)
+    c = Cache(seq_lens, page, H, D, fmt, width=20000 // page)
+    _fill(pv, c, seq_lens, 1)
+    q = _rows(sum(lengths), Hq, D, 2, 0.0).cuda()
+
+    def attend(max_q, max_k, n=1):
+        out = pv.paged_attn_fwd(q.repeat(n, 1, 1), c.k, c.v, _cu(lengths * n), _i32(seq_lens * n),
+                                c.dev_table.repeat(n, 1), max_q, max_k, **c.exps())
+        assert pv.get_device_status() == 0
+        return out
+
+    want = attend(lq, 1024)
+    _check(want, c, q.cpu(), lengths, seq_lens, True, 1 / math.sqrt(D))
+    for max_q, max_k in ((lq, 5000), (lq, 20000), (3, 1024), (4, 1030), (40, 20000)):
+        assert torch.equal(attend(max_q, max_k).view(torch.int16), want.view(torch.int16))
+    many = attend(lq, 1024, 40)
+    assert torch.equal(many.view(torch.int16), want.repeat(40, 1, 1).view(torch.int16))
+
+
+@pytest.mark.parametrize("lq", [1, 33])
+def test_smallest_values_of_8bit_rows(pv, lq):
+    """Rows whose one large element the queries do not see (or that weighs nothing in the
+    output dims looked at): what is left are e4m3's subnormals, which must not be lost."""
+    D, H, n = 128, 1, 70
+    c = Cache([n, n], 16, H, D, "e4m3")
+    g = torch.Generator().manual_seed(5)
+    k = (torch.randint(-7, 8, (2 * n, H, D), generator=g) * 2.0 ** -9)   # subnormals of a 448 row
+    v = (torch.randint(-7, 8, (2 * n, H, D), generator=g) * 2.0 ** -9)
+    k[..., 0] = 448.0
+    v[..., 0] = 448.0
+    q = _rows(lq + 1, 1, D, 3, 0.0)
+    q[..., 0] = 0
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n, n]), c.dev_table, **c.exps())
+    kc, _ = c.values()
+    assert (oracle.cached_rows(kc, c.table[0], n) == oracle.to_f64(k[:n])).all()
+    out = _attend(pv, c, q, [lq, 1], [n, n], True, scale=3.0)
+    _check(out, c, q, [lq, 1], [n, n], True, 3.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_strided_queries_and_interleaved_pages(pv, fmt):
     Hq, H, D, page = 6, 2, 128, 32
     lengths, seq_lens = [1, 70, 1, 9], [500, 70, 33, 1000]
