@@ -136,35 +136,40 @@ constexpr int kDecodeRows = 16;
 
 constexpr int kDecodeUnits = 1824;   // parts of a lone sequence: twelve warps for each of 152 SMs
 
-// Smallest part: short contexts are bound by latency and want many small
-// parts, long ones by bytes and want few partial results, but enough parts for
-// an even load.  64 / 256 keys against others, GPU time: a step of four
-// contexts of 180-700 tokens 10.5 us (128: 11.7), one of 8000 17.8 us (512:
-// 25.0), 64 of 900-8000 185 us (512: 192), 96 8-bit ones of 2-12k 281 us (512:
-// 274, 1024: 267).
+// Smallest part: short contexts are bound by latency and want eight parts at
+// most, one for each warp of a CTA that joins them itself; long ones by bytes,
+// and want few partial results but enough parts for an even load.  256 keys
+// against others, GPU time: one context of 8000 tokens 17.8 us (512: 25.0), 64
+// of 900-8000 185 us (512: 192), 96 8-bit ones of 2-12k 281 us (512: 274,
+// 1024: 267).
 __host__ __device__ __forceinline__ int decode_min_part(int lk) {
-  return lk <= 1024 ? 64 : 256;
+  return lk <= 512 ? 64 : lk <= 1024 ? 128 : 256;
 }
 __host__ __device__ __forceinline__ int decode_most_parts(int Hkv) {
   return Hkv >= kDecodeUnits ? 1 : kDecodeUnits / Hkv;
 }
-// Keys of each part (a multiple of 64) of a sequence of lk keys.
-__host__ __device__ __forceinline__ int decode_part(int lk, int Hkv) {
-  const int most = decode_most_parts(Hkv);
-  const int even = static_cast<int>((static_cast<int64_t>(lk) + most - 1) / most);
-  const int part = even > decode_min_part(lk) ? even : decode_min_part(lk);
-  return part > (1 << 30) ? part : (part + 63) & ~63;
-}
-__host__ __device__ __forceinline__ int decode_parts(int lk, int Hkv) {
-  if (lk <= 0) return 0;
-  const int part = decode_part(lk, Hkv);
-  return static_cast<int>((static_cast<int64_t>(lk) + part - 1) / part);
+// Keys of each part (a multiple of 64) of a sequence of lk keys, and its parts.
+struct DecodeSplit {
+  int part, parts;
+};
+__host__ __device__ __forceinline__ DecodeSplit decode_split(int lk, int most) {
+  const int least = decode_min_part(lk);   // a power of two
+  DecodeSplit x{least, 0};
+  if (lk <= 0) return x;
+  if (static_cast<int64_t>(least) * most >= lk) {   // no division for most sequences
+    x.parts = (lk - 1) / (lk <= 512 ? 64 : lk <= 1024 ? 128 : 256) + 1;   // least, by shifts
+  } else {
+    const uint32_t even = (static_cast<uint32_t>(lk) + most - 1) / static_cast<uint32_t>(most);
+    x.part = even > (1u << 30) ? static_cast<int>(even) : static_cast<int>((even + 63u) & ~63u);
+    x.parts = static_cast<int>((static_cast<uint32_t>(lk) - 1) / static_cast<uint32_t>(x.part)) + 1;
+  }
+  return x;
 }
 // The most parts that a sequence of at most max_k keys has.
 inline int decode_parts_bound(int max_k, int Hkv) {
   if (max_k <= 0) return 1;
   int64_t n = (static_cast<int64_t>(max_k) + decode_min_part(max_k) - 1) / decode_min_part(max_k);
-  if (max_k > 1024 && n < 16) n = 16;   // shorter sequences have smaller parts
+  if (max_k > 512 && n < 8) n = 8;   // shorter sequences have smaller parts
   const int most = decode_most_parts(Hkv);
   return static_cast<int>(n < most ? n : most);
 }
@@ -185,6 +190,7 @@ struct PagedAttnParams {
   float *dec_o;        // [slot][D], not normalised
   float2 *dec_ml;      // [slot] (maximum in log2 units, sum)
   int dec_parts, dec_rows;
+  int dec_most;        // decode_most_parts(Hkv)
   // partial results of the tiled kernel
   float *chunk_o;      // [chunk_rows][D], not normalised
   float2 *chunk_ml;    // [chunk_rows]

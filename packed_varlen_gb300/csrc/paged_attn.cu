@@ -134,6 +134,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D);
   p.dec_parts = w.dec_parts;
   p.dec_rows = w.dec_rows;
+  p.dec_most = decode_most_parts(Hkv);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.dec_o = reinterpret_cast<float *>(ws + w.dec_o);
   p.dec_ml = reinterpret_cast<float2 *>(ws + w.dec_ml);

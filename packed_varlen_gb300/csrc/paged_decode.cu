@@ -41,7 +41,7 @@ constexpr int kLocalWarps = 8;    // of a CTA that joins its parts itself
 constexpr int kSums = 8;          // sums that parts are joined in
 // (sequence, K/V head) pairs that a call may have for that: two for each of 152 SMs.
 constexpr int kLocalUnits = 304;
-constexpr int kLocalParts = 16;   // parts that it has room for: those of 1024 keys
+constexpr int kLocalKeys = 1024;  // longest sequence that has at most a part for each warp
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (~2 s)
@@ -113,7 +113,7 @@ struct Cfg {
   static constexpr int kStageBytes = kExpOff + (kQuant ? 1024 : 0);   // 1024: the swizzle's period
   static constexpr int kStageTx = kExpOff + (kQuant ? 2 * kHalves * 16 : 0);
   static constexpr int kCtas = kLocal ? 1 : NT == 1 || D == 64 ? 3 : 2;   // CTAs that share an SM
-  static constexpr int kPartBytes = kLocal ? kLocalParts * 8 * NT * (D + 2) * 4 : 0;
+  static constexpr int kPartBytes = kLocal ? kLocalWarps * 8 * NT * (D + 2) * 4 : 0;
   static constexpr int kRoom = 233472 / kCtas - 1024 - 1024 - kPartBytes;
   static constexpr int kFit = kRoom / (kCtaWarps * kStageBytes);
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
@@ -144,7 +144,7 @@ struct Walk {
       lq = s.lq;
       lk = s.lk;
       if (lq > 0 && lq <= kDecodeRows / p.G)
-        units = max(decode_parts(lk, p.c.Hkv), 1) * p.c.Hkv;   // no keys: one unit writes zeros
+        units = max(decode_split(lk, p.dec_most).parts, 1) * p.c.Hkv;   // no keys: one unit writes zeros
     }
     int incl = units;
 #pragma unroll
@@ -185,7 +185,7 @@ struct Walk {
 };
 
 // Every warp walks units of its own: its number, its number + all warps, ...
-// kLocal: a CTA has one (sequence, K/V head), its warps the parts in turn, and
+// kLocal: a CTA has one (sequence, K/V head), each of its warps a part, and
 // joins them in shared memory: one launch and no workspace, for calls of few
 // short contexts, whose time is latency.
 template <int D, bool kQuant, int NT, bool kLocal>
@@ -214,19 +214,28 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
   }
   __syncwarp();
   const bool lead = tc::elect_one();
+  if (warp == 0 && lead) {
+    tc::tma_prefetch_desc(&tm_k);
+    tc::tma_prefetch_desc(&tm_v);
+  }
   // this lane's places in a run: K rows g and g + 8, V rows of four keys
   const int kkey = key_of(g);
   const int vkey[2] = {key_of(2 * t), key_of(2 * t + 1)};
   float *part_o = reinterpret_cast<float *>(smem + C::kPartOff);   // kLocal: [part][row][D]
-  float2 *part_ml = reinterpret_cast<float2 *>(part_o + kLocalParts * 8 * NT * D);
+  float2 *part_ml = reinterpret_cast<float2 *>(part_o + kLocalWarps * 8 * NT * D);
   uint32_t issued = 0, used = 0;   // tiles of this warp so far
   uint32_t bad = 0;                // bit (stage * halves + run): no such page, or past the part
   bool ok = true;
   Walk w;
   const bool report = blockIdx.x == 0 && warp == 0;
+  int32_t early = 0;   // kLocal: pages of this warp's part, read before its length is known
   if constexpr (kLocal) {
     w.b = blockIdx.x / p.c.Hkv;
     w.hk = blockIdx.x - w.b * p.c.Hkv;
+    // runs of parts of 64 keys in lanes 0 to 3, of 128 keys in lanes 8 to 15
+    const int entry = (lane < 4 ? warp * 64 + lane * 16 : warp * 128 + (lane & 7) * 16) >> p.c.page_shift;
+    if ((lane < 4 || (lane & 24) == 8) && entry < p.c.table_pages)
+      early = __ldg(p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages + entry);
     int err;
     const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, w.b, p.total_q, p.max_q, p.max_k,
                                  static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
@@ -235,11 +244,11 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     w.s_q0 = s.q0;
     w.s_lq = s.lq;
     w.s_lk = s.lk;
-    w.total = max(decode_parts(s.lk, p.c.Hkv), 1);
+    w.total = max(decode_split(s.lk, p.dec_most).parts, 1);
   } else {
     w.open(p, report);
   }
-  // the next unit: for a warp of a local CTA the next part
+  // the next unit; a warp of a local CTA has one part
   auto more_units = [&](int u) -> bool {
     if constexpr (kLocal) {
       w.part = u;
@@ -250,57 +259,76 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
   };
   const int u_first = kLocal ? warp : blockIdx.x * kWarps + warp;
   const int u_step = kLocal ? kLocalWarps : gridDim.x * kWarps;
-  for (int u = u_first; ok && more_units(u); u += u_step) {
-    const int lq = w.s_lq, lk = w.s_lk, hk = w.hk, R = lq * p.G;
-    const int keys_part = decode_part(lk, p.c.Hkv), parts = decode_parts(lk, p.c.Hkv);
-    const int k0 = w.part * keys_part, keys = min(lk - k0, keys_part);
-    const int n_tiles = (keys + kTile - 1) / kTile;
-    const int32_t *table = p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages;
-
-    // pages of 32 runs of 16 keys at a time, one per lane (a run lies in one page)
-    const int runs = (keys + 15) / 16;
-    auto load_pages = [&](int n0) -> int32_t {
-      const int n = n0 + lane;
-      return n < runs ? __ldg(table + ((k0 + n * 16) >> p.c.page_shift)) : 0;
-    };
-    int32_t pages = load_pages(0), pages_next = load_pages(32);
-
-    // copies of tile n into the ring's next stage
-    auto issue = [&](int n) {
-      const uint32_t st = issued % C::kStages, dst = ring_u + st * C::kStageBytes;
-      const uint32_t bar = bars + 8 * st;
-      if (n > 0 && (n * C::kHalves & 31) == 0) {
-        pages = pages_next;
-        pages_next = load_pages(n * C::kHalves + 32);
-      }
-      if (lead) tc::mbar_arrive_expect_tx(bar, C::kStageTx);
+  // ---- copies: the part that is being fetched and its next tile
+  const int32_t *table = p.c.table;
+  int src_k0 = 0, src_runs = 0, src_tiles = 0, src_n = 0;
+  // pages of 32 runs of 16 keys at a time, one per lane (a run lies in one page)
+  int32_t pages = 0, pages_next = 0;
+  auto load_pages = [&](int n0) -> int32_t {
+    const int n = n0 + lane;
+    return n < src_runs ? __ldg(table + ((src_k0 + n * 16) >> p.c.page_shift)) : 0;
+  };
+  auto open_source = [&](int part) {
+    const int keys_part = decode_split(w.s_lk, p.dec_most).part;
+    src_k0 = part * keys_part;
+    const int keys = min(w.s_lk - src_k0, keys_part);
+    src_runs = keys > 0 ? (keys + 15) / 16 : 0;
+    src_tiles = (src_runs + C::kHalves - 1) / C::kHalves;
+    src_n = 0;
+    if (kLocal && (keys_part == 64 || keys_part == 128)) {
+      pages = __shfl_sync(0xffffffffu, early, keys_part == 64 ? lane : 8 + (lane & 7));
+    } else {
+      pages = load_pages(0);
+      pages_next = load_pages(32);
+    }
+  };
+  // copies of the next tile, if there is one, into the ring's next stage
+  auto issue = [&]() {
+    if (src_n == src_tiles) return;
+    const int n = src_n++;
+    const uint32_t st = issued % C::kStages, dst = ring_u + st * C::kStageBytes;
+    const uint32_t bar = bars + 8 * st;
+    if (n > 0 && (n * C::kHalves & 31) == 0) {
+      pages = pages_next;
+      pages_next = load_pages(n * C::kHalves + 32);
+    }
+    if (lead) tc::mbar_arrive_expect_tx(bar, C::kStageTx);
 #pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) {
-        const int run = n * C::kHalves + h;
-        int32_t page = __shfl_sync(0xffffffffu, pages, run & 31);
-        const bool there = run < runs, good = there && page_ok(p.c, page);
-        const uint32_t bit = 1u << (st * C::kHalves + h);
-        bad = good ? bad & ~bit : bad | bit;
-        if (there && !good && lead) record_error(p.status, PA_DEVICE_ERR_PAGE);
-        if (!good) page = -1;   // lands as zeros
-        const int row0 = (k0 + run * 16) & page_mask;
-        if (lead) {
+    for (int h = 0; h < C::kHalves; ++h) {
+      const int run = n * C::kHalves + h;
+      int32_t page = __shfl_sync(0xffffffffu, pages, run & 31);
+      const bool there = run < src_runs, good = there && page_ok(p.c, page);
+      const uint32_t bit = 1u << (st * C::kHalves + h);
+      bad = good ? bad & ~bit : bad | bit;
+      if (there && !good && lead) record_error(p.status, PA_DEVICE_ERR_PAGE);
+      if (!good) page = -1;   // lands as zeros
+      const int row0 = (src_k0 + run * 16) & page_mask;
+      if (lead) {
 #pragma unroll
-          for (int x = 0; x < C::kBlocks; ++x) {
-            tc::tma_load_4d(dst + h * C::kRunBytes + x * 2048, &tm_k, bar, x * 64, hk, row0, page);
-            tc::tma_load_4d(dst + (C::kHalves + h) * C::kRunBytes + x * 2048, &tm_v, bar, x * 64, hk,
-                            row0, page);
-          }
-          if (kQuant) {
-            const int64_t ex = exp_offset(p.c, good ? page : 0, row0, hk);
-            bulk_load16(dst + C::kExpOff + h * 16, p.c.k_exp + ex, bar);
-            bulk_load16(dst + C::kExpOff + (C::kHalves + h) * 16, p.c.v_exp + ex, bar);
-          }
+        for (int x = 0; x < C::kBlocks; ++x) {
+          tc::tma_load_4d(dst + h * C::kRunBytes + x * 2048, &tm_k, bar, x * 64, w.hk, row0, page);
+          tc::tma_load_4d(dst + (C::kHalves + h) * C::kRunBytes + x * 2048, &tm_v, bar, x * 64, w.hk,
+                          row0, page);
+        }
+        if (kQuant) {
+          const int64_t ex = exp_offset(p.c, good ? page : 0, row0, w.hk);
+          bulk_load16(dst + C::kExpOff + h * 16, p.c.k_exp + ex, bar);
+          bulk_load16(dst + C::kExpOff + (C::kHalves + h) * 16, p.c.v_exp + ex, bar);
         }
       }
-      ++issued;
-    };
-    for (int n = 0; n < C::kStages - 1 && n < n_tiles; ++n) issue(n);
+    }
+    ++issued;
+  };
+
+  for (int u = u_first; ok && more_units(u); u += u_step) {
+    const int lq = w.s_lq, lk = w.s_lk, hk = w.hk, R = lq * p.G;
+    const DecodeSplit split = decode_split(lk, p.dec_most);
+    const int parts = split.parts, k0 = w.part * split.part, keys = min(lk - k0, split.part);
+    const int n_tiles = (keys + kTile - 1) / kTile;
+    table = p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages;
+    open_source(w.part);
+#pragma unroll
+    for (int n = 0; n < C::kStages - 1; ++n) issue();
 
     // Q^T, the B operand of every S^T product.  Over an 8-bit cache it is f16,
     // each row scaled by a power of two to the top of f16's range (what that
@@ -377,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
       const int key = k0 + n * kTile;
       // every lane has read the stage that is filled next (the tile before this one)
       __syncwarp();
-      if (n + C::kStages - 1 < n_tiles) issue(n + C::kStages - 1);
+      issue();
       const uint32_t stage = used % C::kStages;
       ok = tc::bounded_wait(bars + 8 * stage, (used / C::kStages) & 1u, gave_up, p.status, kWaitLimit);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -629,35 +657,38 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     }
   }
   if constexpr (kLocal) {
-    // the join of paged_combine_kernel, sum for sum
+    // the join of paged_combine_kernel, step for step: each of its eight sums has
+    // at most one part here
+    static_assert(kLocalWarps == kSums, "one part to a sum");
     if (w.total > 1) {
       __syncthreads();
       const int R = w.s_lq * p.G;
       for (int x = threadIdx.x; x < R * (D / 4); x += kLocalWarps * 32) {
         const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
+        float2 v[kSums];
+        float4 o[kSums];
         float top = -INFINITY;
-        for (int n = 0; n < w.total; ++n) top = fmaxf(top, part_ml[n * 8 * NT + r].x);
+#pragma unroll
+        for (int n = 0; n < kSums; ++n) {
+          v[n] = make_float2(-INFINITY, 0.f);
+          o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (n < w.total) {
+            v[n] = part_ml[n * 8 * NT + r];
+            o[n] = *reinterpret_cast<const float4 *>(part_o + (n * 8 * NT + r) * D + d);
+          }
+          top = fmaxf(top, v[n].x);
+        }
         const float ref = top == -INFINITY ? 0.f : top;
         float total = 0.f;
         float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y = 0; y < kSums; ++y) {
-          float sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int n = y; n < w.total; n += kSums) {
-            const float2 v = part_ml[n * 8 * NT + r];
-            const float4 o = *reinterpret_cast<const float4 *>(part_o + (n * 8 * NT + r) * D + d);
-            const float f = tc::ex2(v.x - ref);
-            sum += f * v.y;
-            acc.x += f * o.x;
-            acc.y += f * o.y;
-            acc.z += f * o.z;
-            acc.w += f * o.w;
-          }
-          total += sum;
-          out.x += acc.x;
-          out.y += acc.y;
-          out.z += acc.z;
-          out.w += acc.w;
+#pragma unroll
+        for (int n = 0; n < kSums; ++n) {
+          const float f = tc::ex2(v[n].x - ref);
+          total = __fadd_rn(total, __fmul_rn(f, v[n].y));
+          out.x = __fadd_rn(out.x, __fmul_rn(f, o[n].x));
+          out.y = __fadd_rn(out.y, __fmul_rn(f, o[n].y));
+          out.z = __fadd_rn(out.z, __fmul_rn(f, o[n].z));
+          out.w = __fadd_rn(out.w, __fmul_rn(f, o[n].w));
         }
         const float inv = top == -INFINITY ? 0.f : 1.f / total;   // NaN stays NaN
         const int i = r / p.G, h = w.hk * p.G + r - i * p.G;
@@ -691,7 +722,7 @@ __global__ void __launch_bounds__(kWide ? 256 : 128) paged_combine_kernel(const 
   int err;
   const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
   if (s.lq > kDecodeRows / p.G || row >= s.lq * p.Hq) return;
-  const int parts = decode_parts(s.lk, p.c.Hkv);
+  const int parts = decode_split(s.lk, p.dec_most).parts;
   if (parts <= 1) return;
   const int64_t slot0 = static_cast<int64_t>(b) * p.dec_parts * p.dec_rows + row;
   auto slot_of = [&](int n) { return slot0 + static_cast<int64_t>(n) * p.dec_rows; };
@@ -827,7 +858,7 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv) {
-  return tokens * G <= 8 && max_k <= 1024 && static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
+  return tokens * G <= 8 && max_k <= kLocalKeys && static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
 }
 
 template <int D, bool kQuant>
