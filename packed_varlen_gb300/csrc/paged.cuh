@@ -127,7 +127,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
 
 // ---------------------------------------------------------------- splits
 // Keys of one (sequence, K/V head) are split over CTAs, and the parts joined
-// by combine_kernel.  The rule looks at the sequence's own lengths and the
+// by paged_join_kernel (paged_join.cu).  The rule looks at the sequence's own lengths and the
 // head counts only, never at the batch, so a sequence's bits are its own.
 
 // Sequences of at most this many (query, head of the group) rows take the
@@ -173,6 +173,9 @@ inline int decode_parts_bound(int max_k, int Hkv) {
   const int most = decode_most_parts(Hkv);
   return static_cast<int>(n < most ? n : most);
 }
+
+// The parts of a row are added up in this many sums in turn, these in order.
+constexpr int kJoinSums = 8;
 
 // A paged attention call as its kernels see it.
 struct PagedAttnParams {

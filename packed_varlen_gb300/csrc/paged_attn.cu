@@ -146,10 +146,10 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.chunk_cuts = w.chunk_cuts;
   auto s = reinterpret_cast<cudaStream_t>(stream);
   const bool quant = format == PA_CACHE_E4M3;
-  if (p.G <= kDecodeRows) {
-    e = launch_paged_decode(p, quant, sms, s);
-    if (e != cudaSuccess) return from_cuda(e);
-  }
-  if (max_q <= kDecodeRows / p.G) return PA_OK;
-  return from_cuda(launch_paged_chunk(p, quant, sms, s));
+  // The long sequences first; the streaming kernel fills the SMs that they leave.
+  const bool chunk = max_q > kDecodeRows / p.G, few = p.G <= kDecodeRows;
+  if (chunk) e = launch_paged_chunk(p, quant, sms, s);
+  if (e == cudaSuccess && few) e = launch_paged_decode(p, quant, sms, chunk, s);
+  if (e == cudaSuccess && (p.dec_parts > 1 || p.chunk_cuts > 0)) e = launch_paged_join(p, sms, s);
+  return from_cuda(e);
 }

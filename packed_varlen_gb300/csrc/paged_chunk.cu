@@ -18,7 +18,7 @@
 //                the bf16 tiles that the products read.
 // A unit of work is whole items or a share of the sequence's key tiles
 // (paged_chunk_work.cuh); a part of an item leaves its unnormalised output,
-// maximum and sum in the workspace, and paged_chunk_join_kernel joins them.
+// maximum and sum in the workspace, and paged_join_kernel joins them.
 // Keys that a row does not see are masked to -inf; V rows past the sequence's
 // last key are cleared in shared memory before any product reads them (0 *
 // NaN would be NaN); rows of a tile beyond its tokens are computed from
@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   int32_t *first = cut0 + PA_MAX_BATCH + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();   // the streaming kernel may take the SMs that this one leaves
 
   // ---- set-up: barriers, TMEM, work list --------------------------------
   if (tid == 0) {
@@ -823,54 +824,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the parts of the items that shares cut: CTA (x, y) takes rows of the
-// item that share x begins and does not finish, a warp per row.  What the
-// chunk kernel noted is checked against the call before it is used, so that
-// a call that gave up (a wait that ran out) reads nothing out of place.
-constexpr int kJoinThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_chunk_join_kernel(const PagedAttnParams p) {
-  constexpr int E = D / 32;
-  griddep_wait();
-  if (static_cast<int>(blockIdx.x) >= *p.chunk_n_cuts) return;
-  const int4 a = p.chunk_join[2 * static_cast<int64_t>(blockIdx.x)];
-  const int4 c = p.chunk_join[2 * static_cast<int64_t>(blockIdx.x) + 1];
-  const int parts = a.x, rows = c.x;
-  if (parts < 2 || parts > kChunkShares + 1 || rows < 1 || rows > 2 * kTile || a.y < 0 || a.z < 0 ||
-      a.w < 0 || a.y + static_cast<int64_t>(rows) > p.chunk_rows ||
-      a.z + static_cast<int64_t>(parts - 2) * a.w + rows > p.chunk_rows || c.y < 0 ||
-      c.y + static_cast<int64_t>(rows) / p.G > p.total_q || c.z < 0 || c.z >= p.c.Hkv)
-    return;
-  const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
-       r += gridDim.y * (kJoinThreads / 32)) {
-    auto slot = [&](int n) -> int64_t {
-      return (n == 0 ? a.y : a.z + static_cast<int64_t>(n - 1) * a.w) + r;
-    };
-    float top = -INFINITY;
-    for (int n = 0; n < parts; ++n) top = fmaxf(top, p.chunk_ml[slot(n)].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float acc[E], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int n = 0; n < parts; ++n) {
-      const float2 v = p.chunk_ml[slot(n)];
-      const float f = ex2(v.x - ref);
-      sum += f * v.y;
-      const float *src = p.chunk_o + slot(n) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * src[e];
-    }
-    const float inv = top == -INFINITY ? 0.f : 1.f / sum;
-    const int tok = r / p.G;
-    __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(c.y + tok) * p.Hq + c.z * p.G + (r - tok * p.G)) * D +
-                         lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  }
-}
-
 // q as (D, G, Hkv, tokens): a box is 64 columns of the group's heads of the
 // tokens of one tile; rows of a page as (D, Hkv, row, page): a box is 64
 // columns of one head's rows.  128-byte swizzle.
@@ -911,18 +864,7 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
                                 C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   paged_chunk_kernel<D, kQuant><<<num_sms, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.chunk_cuts == 0) return e;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.chunk_cuts, 4);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_chunk_join_kernel<D>, p);
+  return cudaGetLastError();
 }
 
 }  // namespace

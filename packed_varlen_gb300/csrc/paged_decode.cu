@@ -38,7 +38,6 @@ namespace {
 
 constexpr int kWarps = 4;         // of a CTA of the streaming kernel
 constexpr int kLocalWarps = 8;    // of a CTA that joins its parts itself
-constexpr int kSums = 8;          // sums that parts are joined in
 // (sequence, K/V head) pairs that a call may have for that: two for each of 152 SMs.
 constexpr int kLocalUnits = 304;
 constexpr int kLocalKeys = 1024;  // longest sequence that has at most a part for each warp
@@ -200,6 +199,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
   const int page_mask = (1 << p.c.page_shift) - 1;
   if (tc::smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_error(p.status, PA_DEVICE_ERR_SMEM_ALIGN);
+    tc::griddep_wait();
     return;
   }
   uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
@@ -240,7 +240,10 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, w.b, p.total_q, p.max_q, p.max_k,
                                  static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
     if (err && w.hk == 0 && threadIdx.x == 0) record_error(p.status, err);
-    if (s.lq == 0 || s.lq > kDecodeRows / p.G) return;
+    if (s.lq == 0 || s.lq > kDecodeRows / p.G) {
+      tc::griddep_wait();
+      return;
+    }
     w.s_q0 = s.q0;
     w.s_lq = s.lq;
     w.s_lk = s.lk;
@@ -657,19 +660,19 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     }
   }
   if constexpr (kLocal) {
-    // the join of paged_combine_kernel, step for step: each of its eight sums has
+    // the join of paged_join_kernel, step for step: each of its eight sums has
     // at most one part here
-    static_assert(kLocalWarps == kSums, "one part to a sum");
+    static_assert(kLocalWarps == kJoinSums, "one part to a sum");
     if (w.total > 1) {
       __syncthreads();
       const int R = w.s_lq * p.G;
       for (int x = threadIdx.x; x < R * (D / 4); x += kLocalWarps * 32) {
         const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
-        float2 v[kSums];
-        float4 o[kSums];
+        float2 v[kJoinSums];
+        float4 o[kJoinSums];
         float top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < kSums; ++n) {
+        for (int n = 0; n < kJoinSums; ++n) {
           v[n] = make_float2(-INFINITY, 0.f);
           o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (n < w.total) {
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         float total = 0.f;
         float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int n = 0; n < kSums; ++n) {
+        for (int n = 0; n < kJoinSums; ++n) {
           const float f = tc::ex2(v[n].x - ref);
           total = __fadd_rn(total, __fmul_rn(f, v[n].y));
           out.x = __fadd_rn(out.x, __fmul_rn(f, o[n].x));
@@ -702,107 +705,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     for (; used < issued; ++used)
       tc::drain_wait(bars + 8 * (used % C::kStages), (used / C::kStages) & 1u, kDrainLimit);
   }
-}
-
-// Joins the parts of every row that has more than one, a lane over D / 32
-// dims.  The parts go to eight sums in turn, and these are added in order: by
-// eight warps that have a sum each (kWide: few rows with many parts, where
-// latency is all there is to it; one sequence with 228 parts and 32 rows takes
-// 92 us in all, 102 with four warps to a row), or by one warp that has them
-// all (many rows with few parts).  The same bits either way.
-template <int D, bool kWide>
-__global__ void __launch_bounds__(kWide ? 256 : 128) paged_combine_kernel(const PagedAttnParams p) {
-  constexpr int E = D / 32;
-  __shared__ float acc_s[kWide ? kSums : 1][D];
-  __shared__ float sum_s[kSums];
+  // every way out waits: this kernel's end is the end of the tiled one before it
   tc::griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.y, row = kWide ? blockIdx.x : blockIdx.x * 4 + warp;
-  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
-  int err;
-  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
-  if (s.lq > kDecodeRows / p.G || row >= s.lq * p.Hq) return;
-  const int parts = decode_split(s.lk, p.dec_most).parts;
-  if (parts <= 1) return;
-  const int64_t slot0 = static_cast<int64_t>(b) * p.dec_parts * p.dec_rows + row;
-  auto slot_of = [&](int n) { return slot0 + static_cast<int64_t>(n) * p.dec_rows; };
-  float top = -INFINITY;
-  for (int n = lane; n < parts; n += 32) top = fmaxf(top, p.dec_ml[slot_of(n)].x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float ref = top == -INFINITY ? 0.f : top;
-
-  // eight parts in flight: of this warp's sum, or one of each sum
-  constexpr int kOwn = kWide ? 1 : kSums;
-  float acc[kOwn][E], sum[kOwn];
-#pragma unroll
-  for (int y = 0; y < kOwn; ++y) {
-    sum[y] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[y][e] = 0.f;
-  }
-  constexpr int kStep = kWide ? kSums : 1;
-  for (int n0 = kWide ? warp : 0; n0 < parts; n0 += 8 * kStep) {
-    float2 v[8];
-    float o[8][E];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const int n = n0 + x * kStep;
-      v[x] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[x][e] = 0.f;
-      if (n < parts) {
-        v[x] = p.dec_ml[slot_of(n)];
-        const float *src = p.dec_o + slot_of(n) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4 *>(src);
-          o[x][0] = y.x;
-          o[x][1] = y.y;
-          o[x][2] = y.z;
-          o[x][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2 *>(src);
-          o[x][0] = y.x;
-          o[x][1] = y.y;
-        }
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float f = tc::ex2(v[x].x - ref);
-      sum[x % kOwn] += f * v[x].y;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[x % kOwn][e] += f * o[x][e];
-    }
-  }
-  float total = 0.f, out[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = 0.f;
-  if constexpr (kWide) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[0][e];
-    if (lane == 0) sum_s[warp] = sum[0];
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int y = 0; y < kSums; ++y) {
-      total += sum_s[y];
-#pragma unroll
-      for (int e = 0; e < E; ++e) out[e] += acc_s[y][lane * E + e];
-    }
-  } else {
-#pragma unroll
-    for (int y = 0; y < kSums; ++y) {
-      total += sum[y];
-#pragma unroll
-      for (int e = 0; e < E; ++e) out[e] += acc[y][e];
-    }
-  }
-  const float inv = top == -INFINITY ? 0.f : 1.f / total;   // NaN stays NaN
-  uint32_t *dst = reinterpret_cast<uint32_t *>(
-      p.out + (static_cast<int64_t>(s.q0) * p.Hq + row) * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = tc::pack_bf16x2(out[e] * inv, out[e + 1] * inv);
 }
 
 // Rows of a page as (D, Hkv, row, page): a box is one head's rows of a run.
@@ -823,7 +727,7 @@ bool make_map(CUtensorMap *map, const void *ptr, const PagedCache &c, bool quant
 }
 
 template <int D, bool kQuant, int NT, bool kLocal>
-cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const PagedAttnParams &p, int num_sms, bool after_chunk, cudaStream_t stream) {
   using C = Cfg<D, kQuant, NT, kLocal>;
   CUtensorMap mk, mv;
   if (!make_map(&mk, p.c.k, p.c, kQuant) || !make_map(&mv, p.c.v, p.c, kQuant))
@@ -836,23 +740,19 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(p.batch) * p.c.Hkv * (kLocal ? 1 : p.dec_parts);
   const int64_t most = kLocal ? units : (units + kWarps - 1) / kWarps;
   const int64_t ctas = kLocal ? units : static_cast<int64_t>(num_sms) * C::kCtas;
-  paged_decode_kernel<D, kQuant, NT, kLocal>
-      <<<static_cast<unsigned>(most < ctas ? most : ctas), C::kCtaWarps * 32, C::kSmem, stream>>>(
-          mk, mv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || kLocal || p.dec_parts == 1) return e;
+  // After the tiled kernel of the same call this one may start as that one's
+  // CTAs leave their SMs (it waits for its end at its own end).
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const bool wide = p.dec_parts > 64;
-  cfg.gridDim = dim3(wide ? p.dec_rows : (p.dec_rows + 3) / 4, p.batch);
-  cfg.blockDim = dim3(wide ? 256 : 128);
+  cfg.gridDim = dim3(static_cast<unsigned>(most < ctas ? most : ctas));
+  cfg.blockDim = dim3(C::kCtaWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, true>, p)
-              : cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, false>, p);
+  cfg.numAttrs = after_chunk ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, kQuant, NT, kLocal>, mk, mv, p);
 }
 
 }  // namespace
@@ -862,22 +762,24 @@ bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv) {
 }
 
 template <int D, bool kQuant>
-cudaError_t launch_for(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
+static cudaError_t launch_for(const PagedAttnParams &p, int num_sms, bool after_chunk,
+                       cudaStream_t stream) {
   // 8 columns where no sequence of the call can have more rows: a column's
   // results do not depend on the others, so this changes no bits
   const int few = kDecodeRows / p.G, tokens = p.max_q < few ? p.max_q : few;
   if (paged_decode_is_local(p.batch, tokens, p.max_k, p.G, p.c.Hkv))
-    return launch<D, kQuant, 1, true>(p, num_sms, stream);
-  return tokens * p.G > 8 ? launch<D, kQuant, 2, false>(p, num_sms, stream)
-                          : launch<D, kQuant, 1, false>(p, num_sms, stream);
+    return launch<D, kQuant, 1, true>(p, num_sms, after_chunk, stream);
+  return tokens * p.G > 8 ? launch<D, kQuant, 2, false>(p, num_sms, after_chunk, stream)
+                          : launch<D, kQuant, 1, false>(p, num_sms, after_chunk, stream);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
-                                cudaStream_t stream) {
+                                bool after_chunk, cudaStream_t stream) {
   if (p.c.D == 128)
-    return quant ? launch_for<128, true>(p, num_sms, stream)
-                 : launch_for<128, false>(p, num_sms, stream);
-  return quant ? launch_for<64, true>(p, num_sms, stream) : launch_for<64, false>(p, num_sms, stream);
+    return quant ? launch_for<128, true>(p, num_sms, after_chunk, stream)
+                 : launch_for<128, false>(p, num_sms, after_chunk, stream);
+  return quant ? launch_for<64, true>(p, num_sms, after_chunk, stream)
+               : launch_for<64, false>(p, num_sms, after_chunk, stream);
 }
 
 }  // namespace pa

@@ -7,15 +7,17 @@ namespace pa {
 
 struct PagedAttnParams;   // paged.cuh
 
-// Sequences of at most kDecodeRows rows: streaming kernel, and the join of its parts.
-cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
-                                cudaStream_t stream);
+// Sequences of more than kDecodeRows rows: tiled kernel.
+cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
+                               cudaStream_t stream);
 
+// The others: streaming kernel; after_chunk: launched behind the tiled one.
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
+                                bool after_chunk, cudaStream_t stream);
 // Whether that kernel joins its parts itself and needs no workspace.
 bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv);
 
-// Longer sequences: tiled kernel, and the join of the parts that its shares leave.
-cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
-                               cudaStream_t stream);
+// Join of the parts that both leave, behind whichever was launched last.
+cudaError_t launch_paged_join(const PagedAttnParams &p, int num_sms, cudaStream_t stream);
 
 }  // namespace pa
