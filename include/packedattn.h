@@ -300,8 +300,9 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  *   out[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], k[j,h',:]>) * v[j,h',:]
  * A query that sees no key gets zeros.  8-bit rows enter the products as the
  * bf16 values that pa_kv_cache_read returns.  Scores, maxima, sums and the
- * output's accumulation are fp32; softmax weights are rounded to bf16 for
- * the product with V, and the output once to bf16.
+ * output's accumulation are fp32; softmax weights are rounded to bf16 (f16 for
+ * few queries over an 8-bit cache) for the product with V, and the output once
+ * to bf16.
  *
  * q [total_q, Hq, D] bf16, q_stride elements from one token to the next
  * (>= Hq * D, a multiple of 8); out [total_q, Hq, D] bf16 contiguous, written
@@ -317,7 +318,8 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  *
  * workspace: device memory of at least pa_paged_attn_workspace_bytes() bytes,
  * 16-byte aligned, for the partial results of keys that are split over
- * several CTAs (NULL where that is 0).  Its contents need not be kept or
+ * several CTAs, and for the 8-bit rows of long sequences as bf16 where these
+ * take at most 1 GB (NULL where that is 0).  Its contents need not be kept or
  * cleared; two calls that may run at the same time need one each.
  *
  * A sequence with bad boundaries (PA_DEVICE_ERR_CU_SEQLENS), a negative
@@ -337,10 +339,11 @@ pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_ca
                             int64_t workspace_bytes, pa_stream_t stream);
 
 /* Workspace of a pa_paged_attn_fwd call with these arguments, in bytes (host
- * arithmetic alone: it grows with each argument, so one of the largest serves
- * smaller calls); -1 where that call would be refused. */
+ * arithmetic alone); -1 where that call would be refused.  A workspace serves
+ * every call that needs no more than it has. */
 int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q, int32_t max_q,
-                                      int32_t max_k, int32_t Hq, int32_t Hkv, int32_t D);
+                                      int32_t max_k, int32_t Hq, int32_t Hkv, int32_t D,
+                                      int32_t format);
 
 /*
  * pa_linear_bf16 -- batch-invariant packed-M linear layer.

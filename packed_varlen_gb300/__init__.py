@@ -67,7 +67,7 @@ _SIGNATURES = {
                          _c_i32),
     "pa_paged_attn_fwd": ([_c_ptr] * 9 + [_c_i32] * 4 + [_c_i64] + [_c_i32] * 3 + [_c_i64] +
                           [_c_i32] * 5 + [_c_f32, _c_ptr, _c_i64, _c_ptr], _c_i32),
-    "pa_paged_attn_workspace_bytes": ([_c_i32] * 7, _c_i64),
+    "pa_paged_attn_workspace_bytes": ([_c_i32] * 8, _c_i64),
 }
 
 
@@ -591,10 +591,12 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torc
 
 
 def paged_attn_workspace_bytes(batch: int, total_q: int, max_q: int, max_k: int, Hq: int,
-                               Hkv: int, D: int) -> int:
-    """Workspace of paged_attn_fwd, in bytes (pa_paged_attn_workspace_bytes)."""
+                               Hkv: int, D: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Workspace of paged_attn_fwd over a cache of `dtype`, in bytes
+    (pa_paged_attn_workspace_bytes)."""
     n = load_library().pa_paged_attn_workspace_bytes(int(batch), int(total_q), int(max_q),
-                                                     int(max_k), int(Hq), int(Hkv), int(D))
+                                                     int(max_k), int(Hq), int(Hkv), int(D),
+                                                     _CACHE_FORMATS.get(dtype, -1))
     if n < 0:
         raise PackedAttnError("pa_paged_attn_workspace_bytes", 1)
     return int(n)
@@ -626,7 +628,7 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     _need_index(seq_lens, "seq_lens", B, dev)
     if scale is None:
         scale = D ** -0.5
-    need = lib.pa_paged_attn_workspace_bytes(B, Tq, int(max_q), int(max_k), Hq, H, D)
+    need = lib.pa_paged_attn_workspace_bytes(B, Tq, int(max_q), int(max_k), Hq, H, D, fmt)
     on = _On(dev, stream)
     with on as raw:
         if out is None:

@@ -10,6 +10,9 @@
 // never leaves registers between its load and its store.
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_chunk_work.cuh"
+#include "paged_launch.h"
+#include "tc_ptx.cuh"
 
 namespace pa {
 namespace {
@@ -82,27 +85,14 @@ __device__ __forceinline__ uint2 dequantise4(uint32_t w, float scale) {
   return make_uint2(pack_bf16(f[0] * scale, f[1] * scale), pack_bf16(f[2] * scale, f[3] * scale));
 }
 
-// grid (tiles, batch, K or V): a CTA strides over its sequence's tiles of
-// tile_tokens tokens, a thread over a tile's cache vectors.
+// Positions [off, off + n) of sequence b, packed rows from row0 on: the CTAs of
+// blockIdx.x stride over tiles of tile_tokens tokens, a thread over a tile's
+// cache vectors.
 template <bool kWrite, bool kQuant, int D>
-__global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams p) {
+__device__ __forceinline__ void copy_rows(const CopyParams &p, int b, bool is_v, int64_t row0,
+                                          int64_t off, int n) {
   constexpr int kElems = kQuant ? 16 : 8;     // elements of a cache vector
   constexpr int kLanes = D / kElems;          // vectors (lanes) of a row
-  const int b = blockIdx.y;
-  const bool is_v = blockIdx.z == 1;
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-  const int64_t off = p.pos_offset ? __ldg(p.pos_offset + b) : 0;
-  const bool lead = blockIdx.x == 0 && threadIdx.x == 0 && !is_v;
-  if (c0 < 0 || c0 > c1 || c1 > p.total || (b == 0 && c0 != 0)) {
-    if (lead) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
-    return;
-  }
-  const int n = c1 - c0;
-  if (n == 0) return;
-  if (off < 0 || off + n > static_cast<int64_t>(p.c.table_pages) << p.c.page_shift) {
-    if (lead) record_error(p.status, PA_DEVICE_ERR_MAX_LEN);
-    return;
-  }
   const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.table_pages;
   uint8_t *rows = is_v ? p.v_rows : p.k_rows;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
@@ -122,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams p
       const int row = static_cast<int>(pos) & page_mask, head = vec / kLanes;
       const bool good = page_ok(p.c, page);
       if (on && !good) record_error(p.status, PA_DEVICE_ERR_PAGE);
-      uint8_t *packed = rows + (c0 + j) * stride + static_cast<int64_t>(vec) * kElems * 2;
+      uint8_t *packed = rows + (row0 + j) * stride + static_cast<int64_t>(vec) * kElems * 2;
       const int64_t at = page * p.c.page_stride + static_cast<int64_t>(row) * p.c.Hkv * D +
                          static_cast<int64_t>(vec) * kElems;
       const bool live = on && good;
@@ -166,6 +156,55 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams p
       }
     }
   }
+}
+
+// grid (CTAs of a sequence, batch, K or V)
+template <bool kWrite, bool kQuant, int D>
+__global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams p) {
+  const int b = blockIdx.y;
+  const bool is_v = blockIdx.z == 1;
+  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+  const int64_t off = p.pos_offset ? __ldg(p.pos_offset + b) : 0;
+  const bool lead = blockIdx.x == 0 && threadIdx.x == 0 && !is_v;
+  if (c0 < 0 || c0 > c1 || c1 > p.total || (b == 0 && c0 != 0)) {
+    if (lead) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
+    return;
+  }
+  const int n = c1 - c0;
+  if (n == 0) return;
+  if (off < 0 || off + n > static_cast<int64_t>(p.c.table_pages) << p.c.page_shift) {
+    if (lead) record_error(p.status, PA_DEVICE_ERR_MAX_LEN);
+    return;
+  }
+  copy_rows<kWrite, kQuant, D>(p, b, is_v, c0, off, n);
+}
+
+// The keys of the long sequences of an attention call over an 8-bit cache as
+// bf16 rows, a sequence from a multiple of 128 rows on (flat_page: which).
+template <int D>
+__global__ void __launch_bounds__(kThreads) widen_kernel(const PagedAttnParams a, const CopyParams p) {
+  __shared__ int32_t sums[kThreads / 32];
+  tc::griddep_launch_dependents();
+  const int b = blockIdx.y;
+  int err;
+  const PagedSeq s = paged_seq(a.cu_q, a.seq_lens, b, a.total_q, a.max_q, a.max_k, a.capacity, err);
+  if (s.lq <= kDecodeRows / a.G || !chunk_widens(s.lq, a.G)) return;
+  int before = 0;   // pages of the long sequences before this one
+  for (int x = threadIdx.x; x < b; x += kThreads) {
+    const PagedSeq o = paged_seq(a.cu_q, a.seq_lens, x, a.total_q, a.max_q, a.max_k, a.capacity, err);
+    if (o.lq > kDecodeRows / a.G && chunk_widens(o.lq, a.G))
+      before += (o.lk + kChunkTile - 1) / kChunkTile;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = before;
+  __syncthreads();
+  int page = 0;
+#pragma unroll
+  for (int x = 0; x < kThreads / 32; ++x) page += sums[x];
+  if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) a.flat_page[b] = page;
+  if (page + static_cast<int64_t>(s.lk + kChunkTile - 1) / kChunkTile > a.flat_pages) return;
+  copy_rows<false, true, D>(p, b, blockIdx.z == 1, static_cast<int64_t>(page) * kChunkTile, 0, s.lk);
 }
 
 template <bool kWrite>
@@ -220,6 +259,29 @@ pa_status cache_copy(void *k_rows, void *v_rows, const PagedCacheArgs &a, const 
 }
 
 }  // namespace
+
+cudaError_t launch_paged_widen(const PagedAttnParams &a, int num_sms, cudaStream_t stream) {
+  CopyParams p;
+  p.c = a.c;
+  p.k_rows = reinterpret_cast<uint8_t *>(a.flat_k);
+  p.v_rows = reinterpret_cast<uint8_t *>(a.flat_v);
+  p.k_stride = p.v_stride = static_cast<int64_t>(a.c.Hkv) * a.c.D * 2;
+  p.cu = nullptr;
+  p.pos_offset = nullptr;
+  p.total = 0;
+  p.row_vecs = a.c.Hkv * a.c.D / 16;
+  p.tile_tokens = p.row_vecs >= kTileVecs ? 1 : kTileVecs / p.row_vecs;
+  p.status = a.status;
+  int64_t per_seq = (static_cast<int64_t>(num_sms) * 8 + a.batch - 1) / a.batch;
+  const int64_t most = (static_cast<int64_t>(a.max_k) + p.tile_tokens - 1) / p.tile_tokens;
+  if (per_seq > most) per_seq = most;
+  const dim3 grid(static_cast<unsigned>(per_seq), a.batch, 2);
+  if (a.c.D == 128)
+    widen_kernel<128><<<grid, kThreads, 0, stream>>>(a, p);
+  else
+    widen_kernel<64><<<grid, kThreads, 0, stream>>>(a, p);
+  return cudaGetLastError();
+}
 
 pa_status check_cache(const PagedCacheArgs &a, PagedCache &c) {
   if (!a.k || !a.v || !a.table) return PA_ERR_INVALID_ARG;

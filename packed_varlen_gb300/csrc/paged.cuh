@@ -184,6 +184,7 @@ struct PagedAttnParams {
   __nv_bfloat16 *out;
   const int32_t *cu_q, *seq_lens;
   int64_t q_stride;
+  int64_t capacity;    // positions that the page table has room for
   int batch, total_q, max_q, max_k, Hq, G;
   int causal;
   float scale_log2;
@@ -201,6 +202,15 @@ struct PagedAttnParams {
   int32_t *chunk_n_cuts;   // shares of the call
   int64_t chunk_rows;
   int chunk_cuts;      // bound on the shares of the call
+  int64_t chunk_row0, chunk_row0_rest;   // where part rows and cuts of this launch, and
+  int chunk_cut0, chunk_cut0_rest;       // of the one for kSetRest, begin
+  // 8-bit rows of long sequences widened once (chunk_widens): bf16 rows in
+  // pages of 128, a sequence's pages in a row from flat_page[b] on
+  __nv_bfloat16 *flat_k, *flat_v;
+  int32_t *flat_page;
+  int flat_pages;      // room for so many; 0: the call widens nothing ahead
+  int chunk_set;       // the sequences that a launch of the tiled kernel takes
 };
+enum { kSetAll = 0, kSetFlat = 1, kSetRest = 2 };
 
 }  // namespace pa

@@ -14,45 +14,65 @@
 namespace pa {
 namespace {
 
+// Bytes of widened rows up to which a call over an 8-bit cache widens ahead.
+constexpr int64_t kWidenMost = int64_t{1} << 30;
+
 // Where the partial results lie in the workspace.
 struct WorkspacePlan {
   int dec_parts, dec_rows;
-  int64_t chunk_rows;
-  int chunk_cuts;
+  int64_t chunk_rows, chunk_row0_rest;
+  int chunk_cuts, chunk_cut0_rest;
+  int64_t flat_pages;
   int64_t dec_o, dec_ml, chunk_o, chunk_ml, chunk_join, chunk_n_cuts;   // byte offsets
+  int64_t flat_k, flat_v, flat_page;
   int64_t bytes;
 };
 
-WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv,
-                             int D) {
+WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv, int D,
+                             int format) {
   WorkspacePlan w{};
-  const int G = Hq / Hkv;
+  const int G = Hq / Hkv, few = kDecodeRows / G;
   int tokens = max_q < total_q ? max_q : total_q;   // of a sequence in the streaming kernel
-  if (tokens > kDecodeRows / G) tokens = kDecodeRows / G;
+  if (tokens > few) tokens = few;
   w.dec_parts = tokens > 0 ? decode_parts_bound(max_k, Hkv) : 1;
   w.dec_rows = tokens * Hq;
   if (paged_decode_is_local(batch, tokens, max_k, G, Hkv)) w.dec_parts = 1;
   const int64_t slots = w.dec_parts > 1 ? static_cast<int64_t>(batch) * w.dec_parts * w.dec_rows : 0;
-  // Sequences of the tiled kernel, and what their shares may leave: a share
-  // has at least kChunkMinShare key tiles, and two parts of at most an item's
-  // rows; none where no sequence can have enough keys to be cut.
-  const int item_tokens = 2 * (kChunkTile / G), few = kDecodeRows / G;
+
+  const int item_tokens = 2 * (kChunkTile / G);
   const int64_t tiles_k = (static_cast<int64_t>(max_k) + kChunkTile - 1) / kChunkTile;
-  int64_t seqs = 0, shares = 0;
-  if (max_q > few && tiles_k > kChunkMinShare) {
-    seqs = total_q / (few + 1);
-    if (seqs > batch) seqs = batch;
-    const int64_t items = (static_cast<int64_t>(max_q) + item_tokens - 1) / item_tokens;
-    // tiles of all items of a sequence's heads, kept from overflowing
-    const int64_t tiles = items * Hkv > kChunkShares * kChunkMinShare
-                              ? kChunkShares * kChunkMinShare : items * Hkv * tiles_k;
-    shares = (tiles + kChunkMinShare - 1) / kChunkMinShare;
+  auto most_seqs = [&](int least) -> int64_t {   // sequences of at least so many tokens
+    const int64_t n = max_q < least ? 0 : total_q / least;
+    return n < batch ? n : batch;
+  };
+  // Shares that sequences of the tiled kernel are cut into, and the rows that
+  // these may leave: a share has at least kChunkMinShare key tiles, and two
+  // parts of at most an item's rows; none where no sequence can have enough
+  // keys to be cut.
+  auto add_cuts = [&](int64_t seqs, int64_t items) {
+    if (tiles_k <= kChunkMinShare || seqs == 0) return;
+    // key tiles of a sequence's items, kept from overflowing
+    const int64_t all = items * Hkv > kChunkShares * kChunkMinShare ? kChunkShares * kChunkMinShare
+                                                                    : items * Hkv * tiles_k;
+    int64_t shares = (all + kChunkMinShare - 1) / kChunkMinShare;
     if (shares > kChunkShares) shares = kChunkShares;
+    const int64_t by_items = seqs * item_tokens * G, by_tokens = static_cast<int64_t>(total_q) * G;
+    w.chunk_cuts += static_cast<int>(seqs * shares);
+    w.chunk_rows += 2 * shares * (by_items < by_tokens ? by_items : by_tokens);
+  };
+  const int64_t items = (static_cast<int64_t>(max_q) + item_tokens - 1) / item_tokens;
+  if (format == PA_CACHE_E4M3) {
+    const int64_t seqs = most_seqs(2 * item_tokens + 1), pages = seqs * tiles_k;
+    if (pages * kChunkTile * Hkv * D * 4 <= kWidenMost && pages < (1 << 24)) w.flat_pages = pages;
   }
-  w.chunk_cuts = static_cast<int>(seqs * shares);
-  const int64_t rows_by_items = seqs * item_tokens * G, rows_by_tokens = static_cast<int64_t>(total_q) * G;
-  w.chunk_rows = 2 * shares * (seqs == 0 ? 0 : rows_by_items < rows_by_tokens ? rows_by_items
-                                                                              : rows_by_tokens);
+  if (w.flat_pages > 0) {
+    add_cuts(most_seqs(2 * item_tokens + 1), items);
+    w.chunk_row0_rest = w.chunk_rows;
+    w.chunk_cut0_rest = w.chunk_cuts;
+    add_cuts(most_seqs(few + 1), 2);
+  } else {
+    add_cuts(most_seqs(few + 1), items);
+  }
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -65,6 +85,9 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
   w.chunk_ml = take(w.chunk_rows * 8);
   w.chunk_join = take(static_cast<int64_t>(w.chunk_cuts) * 32);
   w.chunk_n_cuts = take(w.chunk_cuts > 0 ? 16 : 0);
+  w.flat_page = take(w.flat_pages > 0 ? static_cast<int64_t>(batch) * 4 : 0);
+  w.flat_k = take(w.flat_pages * kChunkTile * Hkv * D * 2);
+  w.flat_v = take(w.flat_pages * kChunkTile * Hkv * D * 2);
   w.bytes = at;
   return w;
 }
@@ -76,12 +99,12 @@ using namespace pa;
 
 extern "C" int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q, int32_t max_q,
                                                  int32_t max_k, int32_t Hq, int32_t Hkv,
-                                                 int32_t D) {
+                                                 int32_t D, int32_t format) {
   if (batch < 1 || batch > PA_MAX_BATCH || total_q < 0 || max_q < 0 || max_k < 0 || Hkv < 1 ||
-      Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128))
+      Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > kChunkTile || (D != 64 && D != 128) ||
+      (format != PA_CACHE_BF16 && format != PA_CACHE_E4M3))
     return -1;
-  const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D);
-  return w.bytes;
+  return workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format).bytes;
 }
 
 extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
@@ -112,7 +135,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
       !aligned_to(seq_lens, 4) || (q_stride & 7) != 0 || !aligned_to(workspace, 16))
     return PA_ERR_MISALIGNED;
   const int64_t need =
-      pa_paged_attn_workspace_bytes(batch, total_q, max_q, max_k, Hq, Hkv, D);
+      pa_paged_attn_workspace_bytes(batch, total_q, max_q, max_k, Hq, Hkv, D, format);
   if (need < 0 || workspace_bytes < need || (need > 0 && !workspace)) return PA_ERR_INVALID_ARG;
   if (total_q == 0 || max_q == 0) return PA_OK;
   int sms;
@@ -131,7 +154,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.scale_log2 = scale * 1.4426950408889634f;
   p.batch = batch;
   p.G = Hq / Hkv;
-  const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D);
+  const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format);
   p.dec_parts = w.dec_parts;
   p.dec_rows = w.dec_rows;
   p.dec_most = decode_most_parts(Hkv);
@@ -144,6 +167,15 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.chunk_n_cuts = reinterpret_cast<int32_t *>(ws + w.chunk_n_cuts);
   p.chunk_rows = w.chunk_rows;
   p.chunk_cuts = w.chunk_cuts;
+  p.chunk_row0 = p.chunk_cut0 = 0;
+  p.chunk_row0_rest = w.chunk_row0_rest;
+  p.chunk_cut0_rest = w.chunk_cut0_rest;
+  p.flat_k = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_k);
+  p.flat_v = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_v);
+  p.flat_page = reinterpret_cast<int32_t *>(ws + w.flat_page);
+  p.flat_pages = static_cast<int>(w.flat_pages);
+  p.chunk_set = kSetAll;
+  p.capacity = static_cast<int64_t>(table_pages) * page_size;
   auto s = reinterpret_cast<cudaStream_t>(stream);
   const bool quant = format == PA_CACHE_E4M3;
   // The long sequences first; the streaming kernel fills the SMs that they leave.

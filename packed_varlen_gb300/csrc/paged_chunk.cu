@@ -128,12 +128,12 @@ __device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32
                                  int32_t *cut0, int32_t *part0, int32_t *tmp_seq,
                                  int32_t *tmp_lk, int32_t *count, bool report) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
   for (int b = tid; b < p.batch; b += nt) {
     int err;
-    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
+    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
     if (err && report) record_error(p.status, err);
-    if (s.lq > kDecodeRows / p.G) {
+    if (s.lq > kDecodeRows / p.G &&
+        (p.chunk_set == kSetAll || chunk_widens(s.lq, p.G) == (p.chunk_set == kSetFlat))) {
       const int at = atomicAdd(count, 1);   // any order: the ranks below are the list's
       tmp_seq[at] = b;
       tmp_lk[at] = s.lk;
@@ -150,14 +150,14 @@ __device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32
   __syncthreads();
   for (int x = tid; x < n; x += nt) {
     int err;
-    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, order[x], p.total_q, p.max_q, p.max_k, cap, err);
+    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, order[x], p.total_q, p.max_q, p.max_k, p.capacity, err);
     const ChunkWork w = chunk_work(s.lq, s.lk, p.causal, p.G, p.c.Hkv);
     tmp_seq[x] = w.units;
     tmp_lk[x] = w.share ? chunk_part_rows(s.lq, p.G) : 0;   // rows of one part
   }
   __syncthreads();
   if (tid < 32) {
-    int units = 0, cuts = 0, rows = 0;
+    int units = 0, cuts = p.chunk_cut0, rows = static_cast<int>(p.chunk_row0);
     for (int base = 0; base < n; base += 32) {
       const int x = base + tid;
       const int u = x < n ? tmp_seq[x] : 0, pr = x < n ? tmp_lk[x] : 0;
@@ -198,6 +198,7 @@ struct Unit {
   int b, local;       // sequence, unit within it
   int at;             // place of the sequence in the list
   int part_rows;      // workspace rows of one part
+  int flat_page;      // first page of its widened rows (kSetFlat)
   int64_t part0;      // workspace row of the sequence's first part
   ChunkWork w;
   ChunkCursor cur;
@@ -215,11 +216,12 @@ __device__ __noinline__ void open_unit(const PagedAttnParams &p, const int32_t *
   x.b = order[lo];
   int err;
   x.s = paged_seq(p.cu_q, p.seq_lens, x.b, p.total_q, p.max_q, p.max_k,
-                  static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
+                  p.capacity, err);
   x.local = u - first[lo];
   x.at = lo;
   x.part0 = part0[lo];
   x.part_rows = chunk_part_rows(x.s.lq, p.G);
+  x.flat_page = p.chunk_set == kSetFlat ? p.flat_page[x.b] : 0;
   x.w = chunk_work(x.s.lq, x.s.lk, p.causal, p.G, p.c.Hkv);
   x.cur.start(x.w, x.local, p.c.Hkv);
 }
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   const uint32_t base = smem_u32(smem_raw);
   if (base & 1023u) {
     if (threadIdx.x == 0) record_error(p.status, PA_DEVICE_ERR_SMEM_ALIGN);
+    griddep_wait();
     return;
   }
   uint8_t *gbase = smem_raw;
@@ -281,13 +284,16 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
   const int n_seqs = build_list(p, order, first, cut0, part0, tmp, tmp + PA_MAX_BATCH,
                                 counter, blockIdx.x == 0);
+  // rows that the launch before this one widens
+  if (p.chunk_set == kSetFlat) griddep_wait();
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_base_ptr;
   const int n_units = first[n_seqs];
   const int tile_tokens = kTile / p.G, tile_rows = tile_tokens * p.G;
-  if (blockIdx.x == 0 && tid == 0 && p.chunk_cuts > 0) *p.chunk_n_cuts = cut0[n_seqs];
+  if (blockIdx.x == 0 && tid == 0 && p.chunk_cuts > 0)
+    p.chunk_n_cuts[p.chunk_set == kSetRest] = cut0[n_seqs];
 
   if (warp == 0) {
     // ================= TMA producer =================
@@ -315,6 +321,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     auto load_pages = [&](const Unit &x, int j) -> int32_t {
       const int64_t key = static_cast<int64_t>(j) * kTile + lane * box_rows;
       if (lane >= boxes || key >= x.s.lk) return -1;
+      if (p.chunk_set == kSetFlat) return x.flat_page + j < p.flat_pages ? x.flat_page + j : -1;
       const int32_t page = load_now(p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages +
                                     (key >> p.c.page_shift));
       if (!page_ok(p.c, page)) {
@@ -822,6 +829,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  // every way out waits: this kernel's end is the end of those launched before it
+  griddep_wait();
 }
 
 // q as (D, G, Hkv, tokens): a box is 64 columns of the group's heads of the
@@ -841,7 +850,7 @@ bool make_map(CUtensorMap *map, bool bytes, const void *ptr, const cuuint64_t (&
 }
 
 template <int D, bool kQuant>
-cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const PagedAttnParams &p, int num_sms, bool behind, cudaStream_t stream) {
   using C = Cfg<D, kQuant>;
   CUtensorMap mq, mk, mv;
   const cuuint64_t G = p.G, H = p.c.Hkv, d = D;
@@ -863,19 +872,48 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_chunk_kernel<D, kQuant>),
                                 C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  paged_chunk_kernel<D, kQuant><<<num_sms, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<D, kQuant>, mq, mk, mv, p);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
                                cudaStream_t stream) {
-  if (quant)
-    return p.c.D == 128 ? launch<128, true>(p, num_sms, stream)
-                        : launch<64, true>(p, num_sms, stream);
-  return p.c.D == 128 ? launch<128, false>(p, num_sms, stream)
-                      : launch<64, false>(p, num_sms, stream);
+  if (!quant)
+    return p.c.D == 128 ? launch<128, false>(p, num_sms, false, stream)
+                        : launch<64, false>(p, num_sms, false, stream);
+  PagedAttnParams rest = p;
+  if (p.flat_pages > 0) {
+    // long sequences over rows widened ahead, then the others, each in its own
+    // half of the cuts and behind the kernel before it
+    cudaError_t e = launch_paged_widen(p, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    PagedAttnParams flat = p;
+    flat.chunk_set = kSetFlat;
+    flat.c.k = p.flat_k;
+    flat.c.v = p.flat_v;
+    flat.c.page_shift = 7;
+    flat.c.page_stride = static_cast<int64_t>(kTile) * p.c.Hkv * p.c.D;
+    flat.c.num_pages = p.flat_pages;
+    e = p.c.D == 128 ? launch<128, false>(flat, num_sms, true, stream)
+                     : launch<64, false>(flat, num_sms, true, stream);
+    if (e != cudaSuccess) return e;
+    rest.chunk_set = kSetRest;
+    rest.chunk_row0 = p.chunk_row0_rest;
+    rest.chunk_cut0 = p.chunk_cut0_rest;
+  }
+  return p.c.D == 128 ? launch<128, true>(rest, num_sms, p.flat_pages > 0, stream)
+                      : launch<64, true>(rest, num_sms, p.flat_pages > 0, stream);
 }
 
 }  // namespace pa

@@ -137,7 +137,7 @@ struct Walk {
     if (x < p.batch) {
       int err;
       const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, x, p.total_q, p.max_q, p.max_k,
-                                   static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
+                                   p.capacity, err);
       if (err && report) record_error(p.status, err);
       q0 = s.q0;
       lq = s.lq;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
       early = __ldg(p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages + entry);
     int err;
     const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, w.b, p.total_q, p.max_q, p.max_k,
-                                 static_cast<int64_t>(p.c.table_pages) << p.c.page_shift, err);
+                                 p.capacity, err);
     if (err && w.hk == 0 && threadIdx.x == 0) record_error(p.status, err);
     if (s.lq == 0 || s.lq > kDecodeRows / p.G) {
       tc::griddep_wait();

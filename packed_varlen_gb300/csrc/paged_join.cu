@@ -53,9 +53,8 @@ __device__ __forceinline__ void join_row(const PagedAttnParams &p, int b, int ro
   __shared__ float acc_s[kWide ? kJoinSums : 1][D];
   __shared__ float sum_s[kJoinSums];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t cap = static_cast<int64_t>(p.c.table_pages) << p.c.page_shift;
   int err;
-  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, cap, err);
+  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
   if (s.lq > kDecodeRows / p.G || row >= s.lq * p.Hq) return;
   const int parts = decode_split(s.lk, p.dec_most).parts;
   if (parts <= 1) return;
@@ -194,10 +193,14 @@ __global__ void __launch_bounds__(kWarps<kWide> * 32)
     join_row<D, kWide>(p, b, kWide ? x : x * kWarps<kWide> + warp);
     return;
   }
-  const int n_cuts = min(*p.chunk_n_cuts, p.chunk_cuts);
-  for (int x = (blockIdx.x - dec_ctas) * kWarps<kWide> + warp; x < n_cuts * 2 * kChunkTile;
-       x += (gridDim.x - dec_ctas) * kWarps<kWide>)
-    join_item_row<D>(p, x / (2 * kChunkTile), x % (2 * kChunkTile));
+  // the cuts of one launch of the tiled kernel, or of two
+  const int sets = p.flat_pages > 0 ? 2 : 1;
+  for (int set = 0; set < sets; ++set) {
+    const int from = set ? p.chunk_cut0_rest : 0, to = min(p.chunk_n_cuts[set], p.chunk_cuts);
+    for (int x = (blockIdx.x - dec_ctas) * kWarps<kWide> + warp; x < (to - from) * 2 * kChunkTile;
+         x += (gridDim.x - dec_ctas) * kWarps<kWide>)
+      join_item_row<D>(p, from + x / (2 * kChunkTile), x % (2 * kChunkTile));
+  }
 }
 
 template <int D, bool kWide>

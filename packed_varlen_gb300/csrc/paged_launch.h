@@ -11,6 +11,9 @@ struct PagedAttnParams;   // paged.cuh
 cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
                                cudaStream_t stream);
 
+// 8-bit rows of the sequences that chunk_widens() names, as bf16 (kv_cache.cu).
+cudaError_t launch_paged_widen(const PagedAttnParams &p, int num_sms, cudaStream_t stream);
+
 // The others: streaming kernel; after_chunk: launched behind the tiled one.
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool quant, int num_sms,
                                 bool after_chunk, cudaStream_t stream);

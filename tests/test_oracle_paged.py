@@ -142,23 +142,22 @@ def test_empty_calls_touch_nothing(lib):
     assert lib.pa_kv_cache_write(*[a[n] for n in COPY], None) == 0
 
 
-def test_workspace_bytes(lib):
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_workspace_bytes(lib, fmt):
     f = lib.pa_paged_attn_workspace_bytes
-    assert f(0, 1, 1, 1, 8, 8, 128) == -1 and f(1, 1, 1, 1, 9, 8, 128) == -1
-    assert f(1, -1, 1, 1, 8, 8, 128) == -1 and f(1, 1, 1, 1, 8, 8, 96) == -1
-    assert f(2000, 1, 1, 1, 8, 8, 128) == -1
-    base = (4, 100, 30, 5000, 32, 8, 128)
-    n = f(*base)
-    assert n >= 0
-    for i, more in enumerate([9, 200, 60, 50000]):
-        bigger = list(base)
-        bigger[i] = more
-        assert f(*bigger) >= n
-    # a call that is given less is refused
-    if n > 0:
-        a = dict(ATTN, batch=4, total=100, max_q=30, max_k=5000, wn=n - 1)
+    assert f(0, 1, 1, 1, 8, 8, 128, fmt) == -1 and f(1, 1, 1, 1, 9, 8, 128, fmt) == -1
+    assert f(1, -1, 1, 1, 8, 8, 128, fmt) == -1 and f(1, 1, 1, 1, 8, 8, 96, fmt) == -1
+    assert f(2000, 1, 1, 1, 8, 8, 128, fmt) == -1 and f(1, 1, 1, 1, 8, 8, 128, 5) == -1
+    assert f(1, 1, 1, 1, 129, 1, 128, fmt) == -1
+    for batch, total, max_q, max_k in [(4, 100, 30, 5000), (4, 3000, 1000, 20000), (1, 7, 7, 90000),
+                                       (1024, 100000, 9000, 1 << 20), (1, 1, 1, 1 << 30),
+                                       (3, 1 << 20, 1 << 20, 1 << 20)]:
+        n = f(batch, total, max_q, max_k, 32, 8, 128, fmt)
+        assert 0 < n < 1 << 40
+        # a call that is given less is refused
+        a = dict(ATTN, batch=batch, total=total, max_q=max_q, max_k=max_k, fmt=fmt, wn=n - 1)
         assert lib.pa_paged_attn_fwd(*[a[k] for k in ATTN], None) == 1
-        a = dict(ATTN, batch=4, total=100, max_q=30, max_k=5000, ws=None)
+        a = dict(a, ws=None, wn=n)
         assert lib.pa_paged_attn_fwd(*[a[k] for k in ATTN], None) == 1
 
 
