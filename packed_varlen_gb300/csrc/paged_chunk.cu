@@ -57,6 +57,8 @@ struct Cfg {
   static constexpr int kSlots = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
   static constexpr int kRaws = kQuant ? kSlots : 0;         // 8-bit tiles as they arrive
   static constexpr int kRawBytes = kTile * D;
+  static constexpr int kPieces = 4;                         // told ahead by the producer
+  static constexpr int kReaders = 2 + 8 + (kQuant ? kWideners : 0);   // warps that read them
   static constexpr int kHalfBytes = kTile * 64 * 2;         // 128 rows x 128 B
   static constexpr int kTileBytes = kTile * D * 2;          // one Q/K/V tile
   static constexpr int kQOff = 0;                           // Q0, Q1
@@ -66,12 +68,14 @@ struct Cfg {
   // barriers: per Q tile t an S-full, a P-ready and an O-full barrier
   static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
                        kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots,
-                       kRawFull = 12 + 2 * kSlots, kRawEmpty = kRawFull + kRaws;
-  static constexpr int kNumBars = 12 + 2 * kSlots + 2 * kRaws;
+                       kRawFull = 12 + 2 * kSlots, kRawEmpty = kRawFull + kRaws,
+                       kPieceFull = kRawEmpty + kRaws, kPieceEmpty = kPieceFull + kPieces;
+  static constexpr int kNumBars = kPieceEmpty + kPieces;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag, counter
   static constexpr int kSchedOff = (kMiscOff + 16 + 127) / 128 * 128;
   // order, first part row, first cut unit and first unit of each sequence in the list
-  static constexpr int kSmemBytes = kSchedOff + (4 * PA_MAX_BATCH + 2) * 4;
+  static constexpr int kPieceOff = kSchedOff + ((4 * PA_MAX_BATCH + 2) * 4 + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kPieceOff + kPieces * 64;
   static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
   // TMEM columns: S_t at 128 t (P_t over its first 64), O_t at 256 + D t
   static constexpr uint32_t kColS = 0;
@@ -192,6 +196,20 @@ __device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32
   return n;
 }
 
+// A piece as the producer tells the other warps of it: finding a unit's place
+// takes some 10,000 cycles the first time (mostly instruction fetch), so one
+// warp does it, ahead of the others.
+struct Piece {
+  int32_t j0, j1;       // key tiles; j1 = 0: no more pieces
+  int32_t q0, tok0;     // the sequence's first row of q, the item's first token
+  int32_t tokens, head;
+  int32_t lk, before;   // the sequence's keys, and those before its first query
+  int32_t slot;         // workspace row of a part, or -1: the item is whole
+  int32_t b;            // the sequence
+  int32_t pad[6];
+};
+static_assert(sizeof(Piece) == 64, "four 16-byte reads");
+
 // A unit's sequence, and the walk over its pieces.
 struct Unit {
   PagedSeq s;
@@ -203,9 +221,7 @@ struct Unit {
   ChunkWork w;
   ChunkCursor cur;
 };
-// Not inlined: five roles would each fetch their own copy of code that runs
-// once a unit, and instruction fetch is what it costs.
-__device__ __noinline__ void open_unit(const PagedAttnParams &p, const int32_t *order,
+__device__ __forceinline__ void open_unit(const PagedAttnParams &p, const int32_t *order,
                                        const int32_t *first, const int32_t *part0, int n, int u,
                                        Unit &x) {
   int lo = 0, hi = n;   // largest i < n with first[i] <= u (every sequence has a unit)
@@ -274,6 +290,10 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       mbar_init(bar(C::kRawFull + s), 1);
       mbar_init(bar(C::kRawEmpty + s), C::kWideners);
     }
+    for (int s = 0; s < C::kPieces; ++s) {
+      mbar_init(bar(C::kPieceFull + s), 1);
+      mbar_init(bar(C::kPieceEmpty + s), C::kReaders);
+    }
     *abort_flag = 0;
     *counter = 0;
     fence_mbar_init();
@@ -294,6 +314,21 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   const int tile_tokens = kTile / p.G, tile_rows = tile_tokens * p.G;
   if (blockIdx.x == 0 && tid == 0 && p.chunk_cuts > 0)
     p.chunk_n_cuts[p.chunk_set == kSetRest] = cut0[n_seqs];
+
+  Piece *pieces = reinterpret_cast<Piece *>(gbase + C::kPieceOff);
+  uint32_t pieces_read = 0;
+  // the next piece, for each of the reading warps
+  auto next_piece = [&](Piece &x) -> bool {
+    const uint32_t at = pieces_read % C::kPieces;
+    const bool told = bounded_wait(bar(C::kPieceFull + at), (pieces_read / C::kPieces) & 1u,
+                                   abort_flag, p.status, kWaitLimit);
+    if (!__all_sync(0xffffffffu, told)) return false;
+    ++pieces_read;
+    x = pieces[at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::kPieceEmpty + at));
+    return x.j1 > 0;
+  };
 
   if (warp == 0) {
     // ================= TMA producer =================
@@ -318,6 +353,17 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     const int box_rows = min(1 << p.c.page_shift, kTile), boxes = kTile / box_rows;
     const int page_mask = (1 << p.c.page_shift) - 1;
     // lane x < boxes: page of the x-th box of a key tile
+    uint32_t told = 0;
+    auto tell = [&](const Piece &x) -> bool {
+      const uint32_t at = told % C::kPieces;
+      if (!wait_all(bar(C::kPieceEmpty + at), ((told / C::kPieces) & 1u) ^ 1u)) return false;
+      if (lead) {
+        pieces[at] = x;
+        mbar_arrive(bar(C::kPieceFull + at));
+      }
+      ++told;
+      return true;
+    };
     auto load_pages = [&](const Unit &x, int j) -> int32_t {
       const int64_t key = static_cast<int64_t>(j) * kTile + lane * box_rows;
       if (lane >= boxes || key >= x.s.lk) return -1;
@@ -354,11 +400,34 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
       Unit x;
       open_unit(p, order, first, part0, n_seqs, u, x);
+      int4 join_a = make_int4(0, 0, 0, 0), join_b = join_a;   // no item is cut at this unit's end
       ChunkPiece pc;
       while (ok && x.cur.next(x.w, pc)) {
         int32_t pages = load_pages(x, pc.j0);
         const int tok0 = pc.item * x.w.item_tokens;
-        const int ntq = x.s.lq - tok0 > tile_tokens ? 2 : 1;
+        Piece piece;
+        piece.j0 = pc.j0;
+        piece.j1 = pc.j1;
+        piece.q0 = x.s.q0;
+        piece.tok0 = tok0;
+        piece.tokens = min(x.w.item_tokens, x.s.lq - tok0);
+        piece.head = pc.head;
+        piece.lk = x.s.lk;
+        piece.before = x.s.lk - x.s.lq;
+        piece.b = x.b;
+        piece.slot = pc.j0 == 0 && pc.j1 == pc.nk
+                         ? -1 : static_cast<int>(x.part0) + (2 * x.local + (pc.j0 == 0)) * x.part_rows;
+        if (!tell(piece)) {
+          ok = false;
+          break;
+        }
+        if (pc.j0 == 0 && pc.j1 < pc.nk) {
+          // this share begins the item, later ones go on with it: how many
+          const int more = x.w.shares_after(x.local, pc.head, pc.item);
+          join_a = make_int4(1 + more, piece.slot, piece.slot + x.part_rows, 2 * x.part_rows);
+          join_b = make_int4(piece.tokens * p.G, x.s.q0 + tok0, pc.head, 0);
+        }
+        const int ntq = piece.tokens > tile_tokens ? 2 : 1;
         if (!wait_all(bar(C::kQEmpty), (q_loads & 1u) ^ 1u)) {
           ok = false;
           break;
@@ -380,6 +449,15 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           pages = next;
         }
       }
+      if (lead && ok && x.w.share > 0) {
+        int4 *join = p.chunk_join + 2 * (static_cast<int64_t>(cut0[x.at]) + x.local);
+        join[0] = join_a;
+        join[1] = join_b;
+      }
+    }
+    if (ok) {
+      Piece none = {};
+      ok = tell(none);
     }
     if (!ok) {
       // give the copies already issued a bounded chance to land
@@ -447,13 +525,11 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       ++turns;
       if (lead) mbar_arrive(bar(C::kTurn + (1 - t)));
     };
-    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      Unit x;
-      open_unit(p, order, first, part0, n_seqs, u, x);
-      ChunkPiece pc;
-      while (ok && x.cur.next(x.w, pc)) {
-        const bool mine = x.s.lq - pc.item * x.w.item_tokens > t * tile_tokens;
-        const int last_tile = x.s.lk > 0 ? (x.s.lk - 1) / kTile : 0;   // holds the last key
+    {
+      Piece pc;
+      while (ok && next_piece(pc)) {
+        const bool mine = pc.tokens > t * tile_tokens;
+        const int last_tile = pc.lk > 0 ? (pc.lk - 1) / kTile : 0;   // holds the last key
         // release a slot / the Q buffer: after this tile's MMAs, or at once
         auto release = [&](uint32_t b) {
           if (!lead) return;
@@ -495,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           // its PV before tile 1's (the turn order), so it alone clears them.
           // (Widened V tiles come with those rows as zeros.)
           if (!kQuant && t == 0 && j == last_tile) {
-            const int valid = x.s.lk - j * kTile;
+            const int valid = pc.lk - j * kTile;
             if (valid < kTile)
               zero_v_tail<D>(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
           }
@@ -557,18 +633,16 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         const bool x = bounded_wait(b, parity, abort_flag, p.status, kWaitLimit);
         return __all_sync(0xffffffffu, x);
       };
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-        Unit x;
-      open_unit(p, order, first, part0, n_seqs, u, x);
-        const int32_t *table = p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages;
-        ChunkPiece pc;
-        while (ok && x.cur.next(x.w, pc)) {
+      {
+        Piece pc;
+        while (ok && next_piece(pc)) {
+          const int32_t *table = p.c.table + static_cast<int64_t>(pc.b) * p.c.table_pages;
           // this lane's row of key tile j: its page, then its exponent byte
           const int my_row = w * kRows + (lane & 15);
           const uint8_t *exps = lane < 16 ? p.c.k_exp : p.c.v_exp;
           auto load_page = [&](int j) -> int32_t {
             const int64_t key = static_cast<int64_t>(j) * kTile + my_row;
-            return j < pc.j1 && key < x.s.lk ? load_now(table + (key >> p.c.page_shift)) : -1;
+            return j < pc.j1 && key < pc.lk ? load_now(table + (key >> p.c.page_shift)) : -1;
           };
           auto load_exp = [&](int j, int32_t page) -> int {
             if (!page_ok(p.c, page)) return -1;   // no such row: scale 0
@@ -645,28 +719,16 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     const float mul = pos_scale ? sl2 : 1.f;
     uint32_t s_waits = 0, o_waits = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      Unit x;
-      open_unit(p, order, first, part0, n_seqs, u, x);
-      int4 join_a = make_int4(0, 0, 0, 0), join_b = join_a;   // no item is cut at this unit's end
-      ChunkPiece pc;
-      while (ok && x.cur.next(x.w, pc)) {
-        const int tok0 = pc.item * x.w.item_tokens;
-        const int tokens = min(x.w.item_tokens, x.s.lq - tok0);
-        if (pc.j0 == 0 && pc.j1 < pc.nk) {
-          // this share begins the item, later ones go on with it: how many
-          const int more = x.w.shares_after(x.local, pc.head, pc.item);
-          join_a = make_int4(1 + more, static_cast<int>(x.part0) + (2 * x.local + 1) * x.part_rows,
-                             static_cast<int>(x.part0) + (2 * x.local + 2) * x.part_rows,
-                             2 * x.part_rows);
-          join_b = make_int4(tokens * p.G, x.s.q0 + tok0, pc.head, 0);
-        }
+    {
+      Piece pc;
+      while (ok && next_piece(pc)) {
+        const int tok0 = pc.tok0, tokens = pc.tokens;
         if (tokens <= t * tile_tokens) continue;   // tile absent: nothing issued for it
         const int token = t * tile_tokens + row_token;
         const bool store = row < tile_rows && token < tokens;
         // keys that this row sees
-        int lim = x.s.lk;
-        if (p.causal) lim = min(lim, x.s.lk - x.s.lq + tok0 + token + 1);
+        int lim = pc.lk;
+        if (p.causal) lim = min(lim, pc.before + tok0 + token + 1);
         float m = -INFINITY, l = 0.f;
         for (int j = pc.j0; j < pc.j1; ++j) {
           ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kWaitLimit);
@@ -772,11 +834,10 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         }
         ++o_waits;
         fence_after_sync();
-        const bool whole = pc.j0 == 0 && pc.j1 == pc.nk;
-        if (whole) {
+        if (pc.slot < 0) {
           // a row that sees no key: O and l are 0 (or NaN, if a score was)
           const float inv = m == -INFINITY ? 0.f : 1.f / l;
-          __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(x.s.q0 + tok0 + token) * p.Hq +
+          __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(pc.q0 + tok0 + token) * p.Hq +
                                         pc.head * p.G + (row - row_token * p.G)) * D;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -797,8 +858,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             }
           }
         } else {
-          const int64_t slot = x.part0 + static_cast<int64_t>(2 * x.local + (pc.j0 == 0)) * x.part_rows +
-                               t * tile_rows + row;
+          const int64_t slot = static_cast<int64_t>(pc.slot) + t * tile_rows + row;
           float4 *dst = reinterpret_cast<float4 *>(p.chunk_o + slot * D);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -815,11 +875,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
           if (store) p.chunk_ml[slot] = make_float2(m, l);
         }
-      }
-      if (warp == C::kSoftmaxWarp && lane == 0 && ok && x.w.share > 0) {
-        int4 *join = p.chunk_join + 2 * (static_cast<int64_t>(cut0[x.at]) + x.local);
-        join[0] = join_a;
-        join[1] = join_b;
       }
     }
   }

@@ -126,12 +126,14 @@ __device__ __forceinline__ void join_row(const PagedAttnParams &p, int b, int ro
                top == -INFINITY ? 0.f : 1.f / total);
 }
 
-// Row r of the item that cut `cut` begins.  What the tiled kernel noted is
-// checked against the call before it is used, so that a call that gave up (a
-// wait that ran out) reads nothing out of place.
+// Rows r .. r + 3 of the item that cut `cut` begins: four rows' loads in flight.
+// What the tiled kernel noted is checked against the call before it is used,
+// so that a call that gave up (a wait that ran out) reads nothing out of place.
+constexpr int kItemRows = 4;
+
 template <int D>
-__device__ __forceinline__ void join_item_row(const PagedAttnParams &p, int cut, int r) {
-  constexpr int E = D / 32, kBatch = 4;
+__device__ __forceinline__ void join_item_rows(const PagedAttnParams &p, int cut, int r) {
+  constexpr int E = D / 32, kBatch = 2;
   const int lane = threadIdx.x & 31;
   const int4 a = p.chunk_join[2 * static_cast<int64_t>(cut)];
   const int4 c = p.chunk_join[2 * static_cast<int64_t>(cut) + 1];
@@ -144,41 +146,59 @@ __device__ __forceinline__ void join_item_row(const PagedAttnParams &p, int cut,
   auto slot_of = [&](int n) -> int64_t {
     return (n == 0 ? a.y : a.z + static_cast<int64_t>(n - 1) * a.w) + r;
   };
-  float m = -INFINITY, sum = 0.f, acc[E];   // an online softmax over the parts, in order
+  float m[kItemRows], sum[kItemRows], acc[kItemRows][E];   // an online softmax over the parts, in order
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int y = 0; y < kItemRows; ++y) {
+    m[y] = -INFINITY;
+    sum[y] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[y][e] = 0.f;
+  }
   for (int n0 = 0; n0 < parts; n0 += kBatch) {
-    float2 v[kBatch];
-    float o[kBatch][E], top = m;
+    float2 v[kBatch][kItemRows];
+    float o[kBatch][kItemRows][E];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
-      v[x] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[x][e] = 0.f;
-      if (n0 + x < parts) {
-        v[x] = p.chunk_ml[slot_of(n0 + x)];
-        load_row<E>(o[x], p.chunk_o + slot_of(n0 + x) * D + lane * E);
+      for (int y = 0; y < kItemRows; ++y) {
+        v[x][y] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[x][y][e] = 0.f;
+        if (n0 + x < parts && r + y < rows) {
+          const int64_t slot = slot_of(n0 + x) + y;
+          v[x][y] = p.chunk_ml[slot];
+          load_row<E>(o[x][y], p.chunk_o + slot * D + lane * E);
+        }
       }
     }
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) top = fmaxf(top, v[x].x);
-    const float ref = top == -INFINITY ? 0.f : top, old = tc::ex2(m - ref);
-    m = top;
-    sum *= old;
+    for (int y = 0; y < kItemRows; ++y) {
+      float top = m[y];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= old;
+      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, v[x][y].x);
+      const float ref = top == -INFINITY ? 0.f : top, old = tc::ex2(m[y] - ref);
+      m[y] = top;
+      sum[y] *= old;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const float f = tc::ex2(v[x].x - ref);
-      sum += f * v[x].y;
+      for (int e = 0; e < E; ++e) acc[y][e] *= old;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * o[x][e];
+      for (int x = 0; x < kBatch; ++x) {
+        const float f = tc::ex2(v[x][y].x - ref);
+        sum[y] += f * v[x][y].y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[y][e] += f * o[x][y][e];
+      }
     }
   }
-  const int tok = r / p.G;
-  store_row<E>(p.out + (static_cast<int64_t>(c.y + tok) * p.Hq + c.z * p.G + (r - tok * p.G)) * D +
-                   lane * E,
-               acc, m == -INFINITY ? 0.f : 1.f / sum);
+#pragma unroll
+  for (int y = 0; y < kItemRows; ++y) {
+    if (r + y >= rows) break;
+    const int tok = (r + y) / p.G;
+    store_row<E>(p.out +
+                     (static_cast<int64_t>(c.y + tok) * p.Hq + c.z * p.G + (r + y - tok * p.G)) * D +
+                     lane * E,
+                 acc[y], m[y] == -INFINITY ? 0.f : 1.f / sum[y]);
+  }
 }
 
 // CTAs [0, dec_ctas) join rows of the streaming kernel, dec_per_seq of them to
@@ -197,9 +217,10 @@ __global__ void __launch_bounds__(kWarps<kWide> * 32)
   const int sets = p.flat_pages > 0 ? 2 : 1;
   for (int set = 0; set < sets; ++set) {
     const int from = set ? p.chunk_cut0_rest : 0, to = min(p.chunk_n_cuts[set], p.chunk_cuts);
-    for (int x = (blockIdx.x - dec_ctas) * kWarps<kWide> + warp; x < (to - from) * 2 * kChunkTile;
+    constexpr int kGroups = 2 * kChunkTile / kItemRows;   // of an item's rows
+    for (int x = (blockIdx.x - dec_ctas) * kWarps<kWide> + warp; x < (to - from) * kGroups;
          x += (gridDim.x - dec_ctas) * kWarps<kWide>)
-      join_item_row<D>(p, from + x / (2 * kChunkTile), x % (2 * kChunkTile));
+      join_item_rows<D>(p, from + x / kGroups, x % kGroups * kItemRows);
   }
 }
 
@@ -207,7 +228,7 @@ template <int D, bool kWide>
 cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
   const int per_seq = p.dec_parts <= 1 ? 0 : kWide ? p.dec_rows : (p.dec_rows + kWarps<kWide> - 1) / kWarps<kWide>;
   const int dec_ctas = per_seq * p.batch;
-  const int64_t cut_ctas = static_cast<int64_t>(p.chunk_cuts) * (2 * kChunkTile / kWarps<kWide>);
+  const int64_t cut_ctas = static_cast<int64_t>(p.chunk_cuts) * (2 * kChunkTile / kItemRows / kWarps<kWide>);
   const int most = num_sms * (kWide ? 6 : 12);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
