@@ -206,7 +206,8 @@ struct Piece {
   int32_t lk, before;   // the sequence's keys, and those before its first query
   int32_t slot;         // workspace row of a part, or -1: the item is whole
   int32_t b;            // the sequence
-  int32_t pad[6];
+  int32_t part_rows;    // rows of a part in the workspace
+  int32_t pad[5];
 };
 static_assert(sizeof(Piece) == 64, "four 16-byte reads");
 
@@ -415,6 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         piece.lk = x.s.lk;
         piece.before = x.s.lk - x.s.lq;
         piece.b = x.b;
+        piece.part_rows = x.part_rows;
         piece.slot = pc.j0 == 0 && pc.j1 == pc.nk
                          ? -1 : static_cast<int>(x.part0) + (2 * x.local + (pc.j0 == 0)) * x.part_rows;
         if (!tell(piece)) {
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         if (pc.j0 == 0 && pc.j1 < pc.nk) {
           // this share begins the item, later ones go on with it: how many
           const int more = x.w.shares_after(x.local, pc.head, pc.item);
-          join_a = make_int4(1 + more, piece.slot, piece.slot + x.part_rows, 2 * x.part_rows);
+          join_a = make_int4(1 + more, piece.slot, x.part_rows, 0);
           join_b = make_int4(piece.tokens * p.G, x.s.q0 + tok0, pc.head, 0);
         }
         const int ntq = piece.tokens > tile_tokens ? 2 : 1;
@@ -858,8 +860,11 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             }
           }
         } else {
+          // a part lies in the workspace column by column, four at a time, so
+          // that a warp's stores are runs of 512 bytes
           const int64_t slot = static_cast<int64_t>(pc.slot) + t * tile_rows + row;
-          float4 *dst = reinterpret_cast<float4 *>(p.chunk_o + slot * D);
+          float4 *dst = reinterpret_cast<float4 *>(p.chunk_o + static_cast<int64_t>(pc.slot) * D) +
+                        t * tile_rows + row;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
@@ -868,9 +873,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             if (store) {
 #pragma unroll
               for (int v = 0; v < 8; ++v)
-                dst[c * 8 + v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                             __uint_as_float(r[4 * v + 2]),
-                                             __uint_as_float(r[4 * v + 3]));
+                dst[static_cast<int64_t>(c * 8 + v) * pc.part_rows] =
+                    make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
             }
           }
           if (store) p.chunk_ml[slot] = make_float2(m, l);

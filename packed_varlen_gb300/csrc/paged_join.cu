@@ -126,79 +126,59 @@ __device__ __forceinline__ void join_row(const PagedAttnParams &p, int b, int ro
                top == -INFINITY ? 0.f : 1.f / total);
 }
 
-// Rows r .. r + 3 of the item that cut `cut` begins: four rows' loads in flight.
-// What the tiled kernel noted is checked against the call before it is used,
-// so that a call that gave up (a wait that ran out) reads nothing out of place.
-constexpr int kItemRows = 4;
-
+// 32 columns of 32 rows, a row to a lane, of the item that cut `cut` begins
+// (parts lie column by column there, four at a time).  What the tiled kernel
+// noted is checked against the call before it is used, so that a call that
+// gave up (a wait that ran out) reads nothing out of place.
 template <int D>
-__device__ __forceinline__ void join_item_rows(const PagedAttnParams &p, int cut, int r) {
-  constexpr int E = D / 32, kBatch = 2;
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void join_item_block(const PagedAttnParams &p, int cut, int block) {
+  constexpr int kCols = 8;   // of four
+  const int r = block / (D / 32) * 32 + (threadIdx.x & 31), c0 = block % (D / 32) * kCols;
   const int4 a = p.chunk_join[2 * static_cast<int64_t>(cut)];
   const int4 c = p.chunk_join[2 * static_cast<int64_t>(cut) + 1];
-  const int parts = a.x, rows = c.x;
-  if (parts < 2 || parts > kChunkShares + 1 || r >= rows || rows > 2 * kChunkTile || a.y < 0 ||
-      a.z < 0 || a.w < 0 || a.y + static_cast<int64_t>(rows) > p.chunk_rows ||
-      a.z + static_cast<int64_t>(parts - 2) * a.w + rows > p.chunk_rows || c.y < 0 ||
-      c.y + static_cast<int64_t>(rows) / p.G > p.total_q || c.z < 0 || c.z >= p.c.Hkv)
+  // part 0 at row a.y of the workspace, part 1 one part further, then every second
+  const int parts = a.x, rows = c.x, part_rows = a.z;
+  if (parts < 2 || parts > kChunkShares + 1 || rows < 1 || part_rows < rows ||
+      part_rows > 2 * kChunkTile || a.y < 0 ||
+      a.y + static_cast<int64_t>(2 * parts - 2) * part_rows > p.chunk_rows || c.y < 0 ||
+      c.y + static_cast<int64_t>(rows) / p.G > p.total_q || c.z < 0 || c.z >= p.c.Hkv || r >= rows)
     return;
-  auto slot_of = [&](int n) -> int64_t {
-    return (n == 0 ? a.y : a.z + static_cast<int64_t>(n - 1) * a.w) + r;
+  auto first_row = [&](int n) -> int64_t {
+    return a.y + static_cast<int64_t>(n == 0 ? 0 : 2 * n - 1) * part_rows;
   };
-  float m[kItemRows], sum[kItemRows], acc[kItemRows][E];   // an online softmax over the parts, in order
+  float top = -INFINITY;
+  for (int n = 0; n < parts; ++n) top = fmaxf(top, p.chunk_ml[first_row(n) + r].x);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  float4 acc[kCols];
 #pragma unroll
-  for (int y = 0; y < kItemRows; ++y) {
-    m[y] = -INFINITY;
-    sum[y] = 0.f;
+  for (int x = 0; x < kCols; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int n = 0; n < parts; ++n) {
+    const float2 v = p.chunk_ml[first_row(n) + r];
+    const float4 *src =
+        reinterpret_cast<const float4 *>(p.chunk_o + first_row(n) * D) + c0 * part_rows + r;
+    const float f = tc::ex2(v.x - ref);
+    sum += f * v.y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[y][e] = 0.f;
-  }
-  for (int n0 = 0; n0 < parts; n0 += kBatch) {
-    float2 v[kBatch][kItemRows];
-    float o[kBatch][kItemRows][E];
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-#pragma unroll
-      for (int y = 0; y < kItemRows; ++y) {
-        v[x][y] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[x][y][e] = 0.f;
-        if (n0 + x < parts && r + y < rows) {
-          const int64_t slot = slot_of(n0 + x) + y;
-          v[x][y] = p.chunk_ml[slot];
-          load_row<E>(o[x][y], p.chunk_o + slot * D + lane * E);
-        }
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < kItemRows; ++y) {
-      float top = m[y];
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, v[x][y].x);
-      const float ref = top == -INFINITY ? 0.f : top, old = tc::ex2(m[y] - ref);
-      m[y] = top;
-      sum[y] *= old;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[y][e] *= old;
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const float f = tc::ex2(v[x][y].x - ref);
-        sum[y] += f * v[x][y].y;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[y][e] += f * o[x][y][e];
-      }
+    for (int x = 0; x < kCols; ++x) {
+      const float4 o = src[x * part_rows];
+      acc[x].x += f * o.x;
+      acc[x].y += f * o.y;
+      acc[x].z += f * o.z;
+      acc[x].w += f * o.w;
     }
   }
+  const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+  const int tok = r / p.G;
+  uint4 *dst = reinterpret_cast<uint4 *>(
+      p.out + (static_cast<int64_t>(c.y + tok) * p.Hq + c.z * p.G + (r - tok * p.G)) * D + c0 * 4);
 #pragma unroll
-  for (int y = 0; y < kItemRows; ++y) {
-    if (r + y >= rows) break;
-    const int tok = (r + y) / p.G;
-    store_row<E>(p.out +
-                     (static_cast<int64_t>(c.y + tok) * p.Hq + c.z * p.G + (r + y - tok * p.G)) * D +
-                     lane * E,
-                 acc[y], m[y] == -INFINITY ? 0.f : 1.f / sum[y]);
-  }
+  for (int x = 0; x < kCols; x += 2)
+    dst[x / 2] = make_uint4(tc::pack_bf16x2(acc[x].x * inv, acc[x].y * inv),
+                            tc::pack_bf16x2(acc[x].z * inv, acc[x].w * inv),
+                            tc::pack_bf16x2(acc[x + 1].x * inv, acc[x + 1].y * inv),
+                            tc::pack_bf16x2(acc[x + 1].z * inv, acc[x + 1].w * inv));
 }
 
 // CTAs [0, dec_ctas) join rows of the streaming kernel, dec_per_seq of them to
@@ -217,10 +197,10 @@ __global__ void __launch_bounds__(kWarps<kWide> * 32)
   const int sets = p.flat_pages > 0 ? 2 : 1;
   for (int set = 0; set < sets; ++set) {
     const int from = set ? p.chunk_cut0_rest : 0, to = min(p.chunk_n_cuts[set], p.chunk_cuts);
-    constexpr int kGroups = 2 * kChunkTile / kItemRows;   // of an item's rows
-    for (int x = (blockIdx.x - dec_ctas) * kWarps<kWide> + warp; x < (to - from) * kGroups;
+    constexpr int kBlocks = 2 * kChunkTile / 32 * (D / 32);   // of an item
+    for (int x = (blockIdx.x - dec_ctas) * kWarps<kWide> + warp; x < (to - from) * kBlocks;
          x += (gridDim.x - dec_ctas) * kWarps<kWide>)
-      join_item_rows<D>(p, from + x / kGroups, x % kGroups * kItemRows);
+      join_item_block<D>(p, from + x / kBlocks, x % kBlocks);
   }
 }
 
@@ -228,7 +208,7 @@ template <int D, bool kWide>
 cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
   const int per_seq = p.dec_parts <= 1 ? 0 : kWide ? p.dec_rows : (p.dec_rows + kWarps<kWide> - 1) / kWarps<kWide>;
   const int dec_ctas = per_seq * p.batch;
-  const int64_t cut_ctas = static_cast<int64_t>(p.chunk_cuts) * (2 * kChunkTile / kItemRows / kWarps<kWide>);
+  const int64_t cut_ctas = static_cast<int64_t>(p.chunk_cuts) * (2 * kChunkTile / 32 * (D / 32) / kWarps<kWide>);
   const int most = num_sms * (kWide ? 6 : 12);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
