@@ -188,11 +188,11 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const PagedAttnParams a
   const int b = blockIdx.y;
   int err;
   const PagedSeq s = paged_seq(a.cu_q, a.seq_lens, b, a.total_q, a.max_q, a.max_k, a.capacity, err);
-  if (s.lq <= kDecodeRows / a.G || !chunk_widens(s.lq, a.G)) return;
+  if (decode_takes(s.lq, a.G) || !chunk_widens(s.lq, a.G)) return;
   int before = 0;   // pages of the long sequences before this one
   for (int x = threadIdx.x; x < b; x += kThreads) {
     const PagedSeq o = paged_seq(a.cu_q, a.seq_lens, x, a.total_q, a.max_q, a.max_k, a.capacity, err);
-    if (o.lq > kDecodeRows / a.G && chunk_widens(o.lq, a.G))
+    if (!decode_takes(o.lq, a.G) && chunk_widens(o.lq, a.G))
       before += (o.lk + kChunkTile - 1) / kChunkTile;
   }
 #pragma unroll

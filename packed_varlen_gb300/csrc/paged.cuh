@@ -130,9 +130,18 @@ __device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
 // by paged_join_kernel (paged_join.cu).  The rule looks at the sequence's own lengths and the
 // head counts only, never at the batch, so a sequence's bits are its own.
 
-// Sequences of at most this many (query, head of the group) rows take the
-// streaming kernel (paged_decode.cu), longer ones the tiled one.
-constexpr int kDecodeRows = 16;
+// Sequences of few (query, head of the group) rows take the streaming kernel
+// (paged_decode.cu), which reads the keys once for every 16 rows, the others
+// the tiled one (paged_chunk.cu), which has 256 rows for a key tile and a
+// pipeline to fill first.  32 rows, GPU time of the two: 32 sequences over
+// 10-12k keys 352 against 410 us, four 62 against 82, 16 over 700-1500 of D = 64
+// 44 against 56; 64 rows: 681 against 421, 62 against 62, 69 against 56.
+constexpr int kGroupRows = 16;
+constexpr int kFewRows = 32;
+__host__ __device__ __forceinline__ bool decode_takes(int lq, int G) { return lq <= kFewRows / G; }
+__host__ __device__ __forceinline__ int row_groups(int lq, int G) {   // lq <= kFewRows / G
+  return (lq * G + kGroupRows - 1) / kGroupRows;
+}
 
 constexpr int kDecodeUnits = 1824;   // parts of a lone sequence: twelve warps for each of 152 SMs
 
@@ -152,7 +161,8 @@ __host__ __device__ __forceinline__ int decode_most_parts(int Hkv) {
 struct DecodeSplit {
   int part, parts;
 };
-__host__ __device__ __forceinline__ DecodeSplit decode_split(int lk, int most) {
+__host__ __device__ __forceinline__ DecodeSplit decode_split(int lk, int groups, int most) {
+  if (groups > 1) most = most > groups ? most / groups : 1;   // more rows, fewer parts
   const int least = decode_min_part(lk);   // a power of two
   DecodeSplit x{least, 0};
   if (lk <= 0) return x;
@@ -165,12 +175,13 @@ __host__ __device__ __forceinline__ DecodeSplit decode_split(int lk, int most) {
   }
   return x;
 }
-// The most parts that a sequence of at most max_k keys has.
-inline int decode_parts_bound(int max_k, int Hkv) {
+// The most parts that a sequence of at most max_k keys and so many groups of rows has.
+inline int decode_parts_bound(int max_k, int groups, int Hkv) {
   if (max_k <= 0) return 1;
   int64_t n = (static_cast<int64_t>(max_k) + decode_min_part(max_k) - 1) / decode_min_part(max_k);
   if (max_k > 512 && n < 8) n = 8;   // shorter sequences have smaller parts
-  const int most = decode_most_parts(Hkv);
+  int most = decode_most_parts(Hkv);
+  if (groups > 1) most = most > groups ? most / groups : 1;
   return static_cast<int>(n < most ? n : most);
 }
 
@@ -190,10 +201,11 @@ struct PagedAttnParams {
   float scale_log2;
   int32_t *status;
   // partial results of the streaming kernel: part s of row (token i, head h)
-  // of sequence b at slot (b * dec_parts + s) * dec_rows + i * Hq + h
+  // of sequence b, of lq tokens, at slot b * dec_slots + (s * lq + i) * Hq + h
   float *dec_o;        // [slot][D], not normalised
   float2 *dec_ml;      // [slot] (maximum in log2 units, sum)
-  int dec_parts, dec_rows;
+  int64_t dec_slots;
+  int dec_parts, dec_rows;   // bounds of a sequence's parts and rows
   int dec_most;        // decode_most_parts(Hkv)
   // partial results of the tiled kernel
   float *chunk_o;      // [chunk_rows][D], not normalised

@@ -19,6 +19,7 @@ constexpr int64_t kWidenMost = int64_t{1} << 30;
 
 // Where the partial results lie in the workspace.
 struct WorkspacePlan {
+  int64_t dec_slots;
   int dec_parts, dec_rows;
   int64_t chunk_rows, chunk_row0_rest;
   int chunk_cuts, chunk_cut0_rest;
@@ -31,15 +32,24 @@ struct WorkspacePlan {
 WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv, int D,
                              int format) {
   WorkspacePlan w{};
-  const int G = Hq / Hkv, few = kDecodeRows / G;
+  const int G = Hq / Hkv;
   int tokens = max_q < total_q ? max_q : total_q;   // of a sequence in the streaming kernel
-  if (tokens > few) tokens = few;
-  w.dec_parts = tokens > 0 ? decode_parts_bound(max_k, Hkv) : 1;
+  if (tokens > kFewRows / G) tokens = kFewRows / G;
+  w.dec_parts = 1;
   w.dec_rows = tokens * Hq;
-  if (paged_decode_is_local(batch, tokens, max_k, G, Hkv)) w.dec_parts = 1;
-  const int64_t slots = w.dec_parts > 1 ? static_cast<int64_t>(batch) * w.dec_parts * w.dec_rows : 0;
+  if (tokens > 0 && !paged_decode_is_local(batch, tokens, max_k, G, Hkv)) {
+    for (int groups = 1; groups <= row_groups(tokens, G); ++groups) {
+      const int parts = decode_parts_bound(max_k, groups, Hkv);
+      const int rows = groups * kGroupRows < tokens * G ? groups * kGroupRows : tokens * G;
+      if (parts > w.dec_parts) w.dec_parts = parts;
+      if (parts > 1 && static_cast<int64_t>(rows) * Hkv * parts > w.dec_slots)
+        w.dec_slots = static_cast<int64_t>(rows) * Hkv * parts;
+    }
+  }
+  const int64_t slots = w.dec_slots * batch;
 
   const int item_tokens = 2 * (kChunkTile / G);
+  const int few = kFewRows / G;   // tokens up to which no sequence takes the tiled kernel
   const int64_t tiles_k = (static_cast<int64_t>(max_k) + kChunkTile - 1) / kChunkTile;
   auto most_seqs = [&](int least) -> int64_t {   // sequences of at least so many tokens
     const int64_t n = max_q < least ? 0 : total_q / least;
@@ -157,6 +167,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format);
   p.dec_parts = w.dec_parts;
   p.dec_rows = w.dec_rows;
+  p.dec_slots = w.dec_slots;
   p.dec_most = decode_most_parts(Hkv);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.dec_o = reinterpret_cast<float *>(ws + w.dec_o);
@@ -179,7 +190,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   auto s = reinterpret_cast<cudaStream_t>(stream);
   const bool quant = format == PA_CACHE_E4M3;
   // The long sequences first; the streaming kernel fills the SMs that they leave.
-  const bool chunk = max_q > kDecodeRows / p.G, few = p.G <= kDecodeRows;
+  const bool chunk = !decode_takes(max_q, p.G), few = p.G <= kFewRows;
   if (chunk) e = launch_paged_chunk(p, quant, sms, s);
   if (e == cudaSuccess && few) e = launch_paged_decode(p, quant, sms, chunk, s);
   if (e == cudaSuccess && (p.dec_parts > 1 || p.chunk_cuts > 0)) e = launch_paged_join(p, sms, s);

@@ -136,7 +136,7 @@ __device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32
     int err;
     const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
     if (err && report) record_error(p.status, err);
-    if (s.lq > kDecodeRows / p.G &&
+    if (!decode_takes(s.lq, p.G) &&
         (p.chunk_set == kSetAll || chunk_widens(s.lq, p.G) == (p.chunk_set == kSetFlat))) {
       const int at = atomicAdd(count, 1);   // any order: the ranks below are the list's
       tmp_seq[at] = b;

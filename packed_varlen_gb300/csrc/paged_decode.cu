@@ -122,14 +122,14 @@ struct Cfg {
   static_assert(kStages >= 2, "no ring");
 };
 
-// Walks the units of the call, (sequence, part of its keys, K/V head), heads
-// running fastest: a warp holds 32 sequences at a time, one per lane, with the
+// Walks the units of the call, (sequence, part of its keys, group of 16 rows,
+// K/V head), heads running fastest: a warp holds 32 sequences at a time, one per lane, with the
 // units before each.  Units are asked for in rising order.
 struct Walk {
   int group, base, total;       // 32 sequences from group * 32, their first unit, their units
   int q0, lq, lk, first, units; // this lane's sequence
   // the unit found
-  int b, part, hk, s_q0, s_lq, s_lk;
+  int b, part, rows0, hk, s_q0, s_lq, s_lk;
 
   __device__ __forceinline__ void load(const PagedAttnParams &p, bool report) {
     const int lane = threadIdx.x & 31, x = group * 32 + lane;
@@ -142,8 +142,10 @@ struct Walk {
       q0 = s.q0;
       lq = s.lq;
       lk = s.lk;
-      if (lq > 0 && lq <= kDecodeRows / p.G)
-        units = max(decode_split(lk, p.dec_most).parts, 1) * p.c.Hkv;   // no keys: one unit writes zeros
+      if (lq > 0 && decode_takes(lq, p.G)) {
+        const int groups = row_groups(lq, p.G);   // no keys: a unit writes zeros
+        units = max(decode_split(lk, groups, p.dec_most).parts, 1) * groups * p.c.Hkv;
+      }
     }
     int incl = units;
 #pragma unroll
@@ -174,10 +176,16 @@ struct Walk {
     const int src = 31 - __clz(at);
     const int rest = local - __shfl_sync(0xffffffffu, first, src);
     b = group * 32 + src;
-    part = rest / p.c.Hkv;
-    hk = rest - part * p.c.Hkv;
     s_q0 = __shfl_sync(0xffffffffu, q0, src);
     s_lq = __shfl_sync(0xffffffffu, lq, src);
+    part = rest / p.c.Hkv;
+    hk = rest - part * p.c.Hkv;
+    rows0 = 0;
+    const int groups = row_groups(s_lq, p.G);
+    if (groups > 1) {
+      rows0 = part % groups * kGroupRows;
+      part /= groups;
+    }
     s_lk = __shfl_sync(0xffffffffu, lk, src);
     return true;
   }
@@ -240,14 +248,15 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, w.b, p.total_q, p.max_q, p.max_k,
                                  p.capacity, err);
     if (err && w.hk == 0 && threadIdx.x == 0) record_error(p.status, err);
-    if (s.lq == 0 || s.lq > kDecodeRows / p.G) {
+    if (s.lq == 0 || !decode_takes(s.lq, p.G)) {
       tc::griddep_wait();
       return;
     }
     w.s_q0 = s.q0;
     w.s_lq = s.lq;
     w.s_lk = s.lk;
-    w.total = max(decode_split(s.lk, p.dec_most).parts, 1);
+    w.rows0 = 0;
+    w.total = max(decode_split(s.lk, 1, p.dec_most).parts, 1);
   } else {
     w.open(p, report);
   }
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     return n < src_runs ? __ldg(table + ((src_k0 + n * 16) >> p.c.page_shift)) : 0;
   };
   auto open_source = [&](int part) {
-    const int keys_part = decode_split(w.s_lk, p.dec_most).part;
+    const int keys_part = decode_split(w.s_lk, row_groups(w.s_lq, p.G), p.dec_most).part;
     src_k0 = part * keys_part;
     const int keys = min(w.s_lk - src_k0, keys_part);
     src_runs = keys > 0 ? (keys + 15) / 16 : 0;
@@ -324,8 +333,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
   };
 
   for (int u = u_first; ok && more_units(u); u += u_step) {
-    const int lq = w.s_lq, lk = w.s_lk, hk = w.hk, R = lq * p.G;
-    const DecodeSplit split = decode_split(lk, p.dec_most);
+    const int lq = w.s_lq, lk = w.s_lk, hk = w.hk;
+    const int r0 = w.rows0, R = min(lq * p.G - r0, kGroupRows);   // this unit's rows
+    const DecodeSplit split = decode_split(lk, row_groups(lq, p.G), p.dec_most);
     const int parts = split.parts, k0 = w.part * split.part, keys = min(lk - k0, split.part);
     const int n_tiles = (keys + kTile - 1) / kTile;
     table = p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages;
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
       const bool live = r < R;
-      const int i = live ? r / p.G : 0, gg = live ? r - i * p.G : 0;
+      const int i = live ? (r0 + r) / p.G : 0, gg = live ? r0 + r - i * p.G : 0;
       const __nv_bfloat16 *row =
           p.q + (w.s_q0 + i) * p.q_stride + static_cast<int64_t>(hk * p.G + gg) * D;
 #pragma unroll
@@ -388,9 +398,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * t + e;
-        lim[nt][e] = r >= R ? 0 : p.causal ? lk - lq + 1 + r / p.G : lk;
+        lim[nt][e] = r >= R ? 0 : p.causal ? lk - lq + 1 + (r0 + r) / p.G : lk;
       }
-    const int all_see = p.causal ? lk - lq + 1 : lk;   // keys before it need no mask
+    const int all_see = p.causal ? lk - lq + 1 + r0 / p.G : lk;   // keys before it need no mask
 
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -629,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
         const int r = nt * 8 + 2 * t + e;
         if (r >= R) continue;
-        const int i = r / p.G, h = hk * p.G + r - i * p.G;
+        const int i = (r0 + r) / p.G, h = hk * p.G + r0 + r - i * p.G;
         if (parts <= 1) {
           const float inv = m[nt][e] == -INFINITY ? 0.f : grade / l[nt][e];
           __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D;
@@ -643,8 +653,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
             *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         } else {
-          const int64_t slot = (static_cast<int64_t>(w.b) * p.dec_parts + w.part) * p.dec_rows +
-                               static_cast<int64_t>(i) * p.Hq + h;
+          const int64_t slot =
+              w.b * p.dec_slots + static_cast<int64_t>(w.part * lq + i) * p.Hq + h;
           float *dst = kLocal ? part_o + (w.part * 8 * NT + r) * D : p.dec_o + slot * D;
 #pragma unroll
           for (int mt = 0; mt < D / 16; mt += 2) {
@@ -737,7 +747,8 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, bool after_chunk, cuda
       set_smem_once(reinterpret_cast<const void *>(paged_decode_kernel<D, kQuant, NT, kLocal>),
                     C::kSmem, configured);
   if (e != cudaSuccess) return e;
-  const int64_t units = static_cast<int64_t>(p.batch) * p.c.Hkv * (kLocal ? 1 : p.dec_parts);
+  const int64_t units = static_cast<int64_t>(p.batch) * p.c.Hkv *
+                        (kLocal ? 1 : p.dec_parts * (p.dec_rows / p.Hq * p.G + 15) / 16);
   const int64_t most = kLocal ? units : (units + kWarps - 1) / kWarps;
   const int64_t ctas = kLocal ? units : static_cast<int64_t>(num_sms) * C::kCtas;
   // After the tiled kernel of the same call this one may start as that one's
@@ -758,7 +769,7 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, bool after_chunk, cuda
 }  // namespace
 
 bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv) {
-  return tokens * G <= 8 && max_k <= kLocalKeys && static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
+  return tokens > 0 && tokens * G <= 8 && max_k <= kLocalKeys && static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
 }
 
 template <int D, bool kQuant>
@@ -766,7 +777,7 @@ static cudaError_t launch_for(const PagedAttnParams &p, int num_sms, bool after_
                        cudaStream_t stream) {
   // 8 columns where no sequence of the call can have more rows: a column's
   // results do not depend on the others, so this changes no bits
-  const int few = kDecodeRows / p.G, tokens = p.max_q < few ? p.max_q : few;
+  const int few = kFewRows / p.G, tokens = p.max_q < few ? p.max_q : few;
   if (paged_decode_is_local(p.batch, tokens, p.max_k, p.G, p.c.Hkv))
     return launch<D, kQuant, 1, true>(p, num_sms, after_chunk, stream);
   return tokens * p.G > 8 ? launch<D, kQuant, 2, false>(p, num_sms, after_chunk, stream)

@@ -55,11 +55,11 @@ __device__ __forceinline__ void join_row(const PagedAttnParams &p, int b, int ro
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int err;
   const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
-  if (s.lq > kDecodeRows / p.G || row >= s.lq * p.Hq) return;
-  const int parts = decode_split(s.lk, p.dec_most).parts;
+  if (!decode_takes(s.lq, p.G) || row >= s.lq * p.Hq) return;
+  const int parts = decode_split(s.lk, row_groups(s.lq, p.G), p.dec_most).parts;
   if (parts <= 1) return;
-  const int64_t slot0 = static_cast<int64_t>(b) * p.dec_parts * p.dec_rows + row;
-  auto slot_of = [&](int n) { return slot0 + static_cast<int64_t>(n) * p.dec_rows; };
+  const int64_t slot0 = b * p.dec_slots + row;
+  auto slot_of = [&](int n) { return slot0 + static_cast<int64_t>(n) * (s.lq * p.Hq); };
   float top = -INFINITY;
   for (int n = lane; n < parts; n += 32) top = fmaxf(top, p.dec_ml[slot_of(n)].x);
 #pragma unroll

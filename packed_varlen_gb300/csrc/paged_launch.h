@@ -7,7 +7,7 @@ namespace pa {
 
 struct PagedAttnParams;   // paged.cuh
 
-// Sequences of more than kDecodeRows rows: tiled kernel.
+// Sequences of more than kFewRows rows: tiled kernel.
 cudaError_t launch_paged_chunk(const PagedAttnParams &p, bool quant, int num_sms,
                                cudaStream_t stream);
 
