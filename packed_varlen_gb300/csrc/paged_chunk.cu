@@ -12,7 +12,9 @@
 //                tile one copy per page (or per 128 rows of a larger page) and
 //                64 columns; pages past the sequence's last key are fetched
 //                from an out-of-range page, so they land as zeros.
-//   warps 1, 2   issue tile 0's and tile 1's tcgen05.mma in turn.
+//   warps 1, 2   issue tile 0's and tile 1's tcgen05.mma in turn.  Where an item
+//                has rows for one tile only, the two take its even and its odd
+//                key tiles, and the epilogue adds the two outputs up.
 //   warps 3..6   softmax of tile 0, a thread per row; warps 7..10 of tile 1.
 //   warps 11..18 (8-bit caches) widen the rows that the producer fetched into
 //                the bf16 tiles that the products read.
@@ -69,13 +71,15 @@ struct Cfg {
   static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
                        kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots,
                        kRawFull = 12 + 2 * kSlots, kRawEmpty = kRawFull + kRaws,
-                       kPieceFull = kRawEmpty + kRaws, kPieceEmpty = kPieceFull + kPieces;
-  static constexpr int kNumBars = kPieceEmpty + kPieces;
+                       kPieceFull = kRawEmpty + kRaws, kPieceEmpty = kPieceFull + kPieces,
+                       kBothDone = kPieceEmpty + kPieces, kBothRead = kBothDone + 1;
+  static constexpr int kNumBars = kBothRead + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag, counter
   static constexpr int kSchedOff = (kMiscOff + 16 + 127) / 128 * 128;
   // order, first part row, first cut unit and first unit of each sequence in the list
   static constexpr int kPieceOff = kSchedOff + ((4 * PA_MAX_BATCH + 2) * 4 + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kPieceOff + kPieces * 64;
+  static constexpr int kStatOff = kPieceOff + kPieces * 64;   // (maximum, sum) of [tile][row]
+  static constexpr int kSmemBytes = kStatOff + 2 * kTile * 8;
   static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
   // TMEM columns: S_t at 128 t (P_t over its first 64), O_t at 256 + D t
   static constexpr uint32_t kColS = 0;
@@ -291,6 +295,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       mbar_init(bar(C::kRawFull + s), 1);
       mbar_init(bar(C::kRawEmpty + s), C::kWideners);
     }
+    mbar_init(bar(C::kBothDone), 8);
+    mbar_init(bar(C::kBothRead), 8);
     for (int s = 0; s < C::kPieces; ++s) {
       mbar_init(bar(C::kPieceFull + s), 1);
       mbar_init(bar(C::kPieceEmpty + s), C::kReaders);
@@ -353,7 +359,10 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     };
     const int box_rows = min(1 << p.c.page_shift, kTile), boxes = kTile / box_rows;
     const int page_mask = (1 << p.c.page_shift) - 1;
-    // lane x < boxes: page of the x-th box of a key tile
+    // A tile's copies are one to a lane: box x of its rows and column half y
+    // belong to lane x * kHalves + y, which also holds the box's page.
+    constexpr int kHalves = kQuant ? 1 : D / 64;
+    const int box = lane / kHalves, half = lane % kHalves;
     uint32_t told = 0;
     auto tell = [&](const Piece &x) -> bool {
       const uint32_t at = told % C::kPieces;
@@ -366,8 +375,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       return true;
     };
     auto load_pages = [&](const Unit &x, int j) -> int32_t {
-      const int64_t key = static_cast<int64_t>(j) * kTile + lane * box_rows;
-      if (lane >= boxes || key >= x.s.lk) return -1;
+      const int64_t key = static_cast<int64_t>(j) * kTile + box * box_rows;
+      if (box >= boxes || key >= x.s.lk) return -1;
       if (p.chunk_set == kSetFlat) return x.flat_page + j < p.flat_pages ? x.flat_page + j : -1;
       const int32_t page = load_now(p.c.table + static_cast<int64_t>(x.b) * p.c.table_pages +
                                     (key >> p.c.page_shift));
@@ -377,24 +386,17 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       }
       return page;
     };
-    auto load_kv = [&](const CUtensorMap *tm, int32_t pages, int j, int head) -> bool {
+    auto load_kv = [&](const CUtensorMap *tm, int32_t page, int j, int head) -> bool {
       const uint32_t s = slot_loads % kBufs;
       const uint32_t use = slot_loads / kBufs;
       if (!wait_all(bar(kEmpty + s), (use & 1u) ^ 1u)) return false;
       const uint32_t dst = sBuf + s * kBufBytes;
       if (lead) mbar_arrive_expect_tx(bar(kFull + s), kBufBytes);
       const int row = (j * kTile) & page_mask;   // not 0 only where a page spans several tiles
-      for (int x = 0; x < boxes; ++x) {
-        const int32_t page = __shfl_sync(0xffffffffu, pages, x);
-        if (kQuant) {
-          if (lead) tma_load_4d(dst + x * box_rows * D, tm, bar(kFull + s), 0, head, row, page);
-        } else if (lead) {
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_4d(dst + hf * C::kHalfBytes + x * box_rows * 128, tm, bar(kFull + s), hf * 64,
-                        head, row, page);
-        }
-      }
+      __syncwarp();   // no byte of a copy is counted before all are announced
+      if (box < boxes)
+        tma_load_4d(dst + box * box_rows * (kQuant ? D : 128) + half * C::kHalfBytes, tm,
+                    bar(kFull + s), half * 64, head, row, page);
       ++slot_loads;
       return true;
     };
@@ -474,9 +476,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     // Each issuer walks the same pieces and ring slots; it issues its own
     // tile's MMAs in the order S_0 | PV_0 S_1 | PV_1 S_2 ... and frees a slot
     // (or the Q buffer) with one arrival on a two-arrival barrier: a commit
-    // once its MMAs reading the slot are done, or a plain arrive when its tile
-    // is absent from the item.  The whole warp runs the issuer, so every
-    // operand of an MMA is warp-uniform, and one elected lane issues.
+    // once its MMAs reading the slot are done, or a plain arrive where it reads
+    // none.  The whole warp runs the issuer, so every operand of an MMA is
+    // warp-uniform, and one elected lane issues.
     const int t = warp - 1;
     const bool lead = elect_one();
     uint32_t q_uses = 0, slot_uses = 0, issued = 0, p_waits = 0;
@@ -492,17 +494,18 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     };
     // (descriptors advance by adding the byte offset >> 4 to the start
     // address field; every operand lies below 256 KB, so nothing carries)
-    const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024) + ((t * C::kTileBytes) >> 4);
+    const uint64_t qdesc_one = sdesc_sw128(sQ, 16, 1024);
+    const uint64_t qdesc0 = qdesc_one + ((t * C::kTileBytes) >> 4);
     const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
     const uint64_t vdesc0 = sdesc_sw128(sRing, C::kVLbo, 1024);
     const uint32_t d_s = tmem + C::kColS + t * kTile, d_o = tmem + C::kColO + t * D;
     // S_t = Q_t K^T (both K-major, SBO = 8 rows x 128 B)
-    auto issue_s = [&](uint32_t slot) {
+    auto issue_s = [&](uint32_t slot, uint64_t qdesc) {
       const uint64_t b0 = kdesc0 + ((slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * C::kHalfBytes + (kk & 3) * 32) >> 4;
-        if (lead) mma_ss(d_s, qdesc0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
+        if (lead) mma_ss(d_s, qdesc + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
       }
     };
     // O_t += P_t V (P_t is in the first 64 columns of the S buffer)
@@ -530,33 +533,80 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     {
       Piece pc;
       while (ok && next_piece(pc)) {
-        const bool mine = pc.tokens > t * tile_tokens;
         const int last_tile = pc.lk > 0 ? (pc.lk - 1) / kTile : 0;   // holds the last key
-        // release a slot / the Q buffer: after this tile's MMAs, or at once
-        auto release = [&](uint32_t b) {
-          if (!lead) return;
-          if (mine)
-            mma_commit(b);
-          else
-            mbar_arrive(b);
-        };
         if (!wait_all(bar(C::kQFull), q_uses & 1u)) {
           ok = false;
           break;
         }
         ++q_uses;
+        if (pc.tokens <= tile_tokens) {
+          // One tile of rows: the issuers share its key tiles, tile t of S and O
+          // has every second one from t on.  An issuer's PV waits until it has
+          // let go of the other's next slots, and comes before its own next S.
+          const int n = pc.j1 - pc.j0, mine = (n - t + 1) / 2;
+          int done = 0, held = -1;   // S issued; key tile whose PV is still to come
+          uint32_t sv = 0;
+          auto flush = [&]() -> bool {
+            if (held < 0) return true;
+            if (!kQuant && held == last_tile) {
+              const int valid = pc.lk - held * kTile;
+              if (valid < kTile) zero_v_tail<D>(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
+            }
+            if (!wait_all(bar(C::kPReady + t), p_waits & 1u)) return false;
+            ++p_waits;
+            fence_after_sync();
+            issue_pv(sv, held == pc.j0 + t);
+            if (lead) {
+              mma_commit(bar(C::kSlotEmpty + sv));
+              if (done == mine) mma_commit(bar(C::kOFull + t));
+            }
+            held = -1;
+            return true;
+          };
+          if (mine == 0 && lead) mbar_arrive(bar(C::kQEmpty));
+          for (int i = 0; i < n && ok; ++i) {
+            uint32_t sk;
+            ok = wait_slot(sk);
+            if (!ok) break;
+            ++slot_uses;
+            if ((i & 1) == t) {
+              issue_s(sk, qdesc_one);
+              issued = 1;
+              ++done;
+              if (lead) {
+                mma_commit(bar(C::kSFull + t));
+                mma_commit(bar(C::kSlotEmpty + sk));
+                if (done == mine) mma_commit(bar(C::kQEmpty));
+              }
+              ok = wait_slot(sv);
+              ++slot_uses;
+              held = pc.j0 + i;
+            } else {
+              if (lead) mbar_arrive(bar(C::kSlotEmpty + sk));
+              ok = wait_slot(sk);
+              if (!ok) break;
+              ++slot_uses;
+              if (lead) mbar_arrive(bar(C::kSlotEmpty + sk));
+              ok = flush();
+            }
+          }
+          if (ok) ok = flush();
+          continue;
+        }
+        // release a slot / the Q buffer after this tile's MMAs
+        auto release = [&](uint32_t b) {
+          if (lead) mma_commit(b);
+        };
         // prologue: S of the first key tile
         uint32_t sk;
         if (!wait_slot(sk) || !take_turn()) {
           ok = false;
           break;
         }
-        if (mine) {
-          issue_s(sk);
-          issued = 1;
-        }
+        issue_s(sk, qdesc0);
+        issued = 1;
         pass_turn();
-        if (mine && lead) mma_commit(bar(C::kSFull + t));
+        if (lead) mma_commit(bar(C::kSFull + t));
         release(bar(C::kSlotEmpty + sk));
         ++slot_uses;
         if (pc.j1 - pc.j0 == 1) release(bar(C::kQEmpty));
@@ -569,8 +619,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
           ++slot_uses;
           // V rows past the sequence's last key: P is 0 there, but 0 * Inf and
-          // 0 * NaN are NaN.  Tile 0's issuer runs for every item and issues
-          // its PV before tile 1's (the turn order), so it alone clears them.
+          // 0 * NaN are NaN.  Tile 0's issuer issues its PV before tile 1's (the
+          // turn order), so it alone clears them.
           // (Widened V tiles come with those rows as zeros.)
           if (!kQuant && t == 0 && j == last_tile) {
             const int valid = pc.lk - j * kTile;
@@ -587,19 +637,17 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             ok = false;
             break;
           }
-          if (mine) {
-            if (!wait_all(bar(C::kPReady + t), p_waits & 1u)) {
-              ok = false;
-              break;
-            }
-            ++p_waits;
-            fence_after_sync();
-            // PV_j, then S_{j+1} (after the PV that reads P from the S buffer)
-            issue_pv(sv, j == pc.j0);
-            if (more) issue_s(sk2);
+          if (!wait_all(bar(C::kPReady + t), p_waits & 1u)) {
+            ok = false;
+            break;
           }
+          ++p_waits;
+          fence_after_sync();
+          // PV_j, then S_{j+1} (after the PV that reads P from the S buffer)
+          issue_pv(sv, j == pc.j0);
+          if (more) issue_s(sk2, qdesc0);
           pass_turn();
-          if (mine && lead) mma_commit(more ? bar(C::kSFull + t) : bar(C::kOFull + t));
+          if (lead) mma_commit(more ? bar(C::kSFull + t) : bar(C::kOFull + t));
           release(bar(C::kSlotEmpty + sv));
           if (more) {
             release(bar(C::kSlotEmpty + sk2));
@@ -719,20 +767,23 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     const float sl2 = p.scale_log2;
     const bool pos_scale = sl2 > 0.f;
     const float mul = pos_scale ? sl2 : 1.f;
-    uint32_t s_waits = 0, o_waits = 0;
+    uint32_t s_waits = 0, o_waits = 0, shares = 0;
     bool ok = true;
     {
       Piece pc;
       while (ok && next_piece(pc)) {
         const int tok0 = pc.tok0, tokens = pc.tokens;
-        if (tokens <= t * tile_tokens) continue;   // tile absent: nothing issued for it
-        const int token = t * tile_tokens + row_token;
+        // one tile of rows: tiles 0 and 1 are its even and its odd key tiles
+        const bool shared = tokens <= tile_tokens;
+        const int row0 = shared ? 0 : t * tile_rows;   // of this tile in the item
+        const int token = shared ? row_token : t * tile_tokens + row_token;
+        const int j_first = pc.j0 + (shared ? t : 0), j_step = shared ? 2 : 1;
         const bool store = row < tile_rows && token < tokens;
         // keys that this row sees
         int lim = pc.lk;
         if (p.causal) lim = min(lim, pc.before + tok0 + token + 1);
         float m = -INFINITY, l = 0.f;
-        for (int j = pc.j0; j < pc.j1; ++j) {
+        for (int j = j_first; j < pc.j1; j += j_step) {
           ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kWaitLimit);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
@@ -785,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           if (mx > m + kRescaleThreshold) {   // from -inf: any finite score
             alpha = ex2(m - mx);
             m = mx;
-            rescale = j > pc.j0;
+            rescale = j > j_first;
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-ref, -ref);
@@ -829,56 +880,99 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         }
         if (!ok) break;
         // epilogue: wait for this tile's last PV, then store the valid rows
-        ok = bounded_wait(bar(C::kOFull + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+        if (j_first < pc.j1) {
+          ok = bounded_wait(bar(C::kOFull + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ++o_waits;
+          fence_after_sync();
         }
-        ++o_waits;
-        fence_after_sync();
-        if (pc.slot < 0) {
-          // a row that sees no key: O and l are 0 (or NaN, if a score was)
-          const float inv = m == -INFINITY ? 0.f : 1.f / l;
-          __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(pc.q0 + tok0 + token) * p.Hq +
-                                        pc.head * p.G + (row - row_token * p.G)) * D;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + colO + c * 32, r);
+        // O is f0 O_t (+ f1 O_1 where the tiles share the rows, each of them then
+        // storing half of the columns)
+        float f0 = 1.f, f1 = 0.f;
+        const bool two = shared && pc.j1 - pc.j0 > 1;
+        if (shared) {
+          float2 *stat = reinterpret_cast<float2 *>(gbase + C::kStatOff);
+          stat[t * kTile + row] = make_float2(m, l);
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBothDone));
+          ok = bounded_wait(bar(C::kBothDone), shares & 1u, abort_flag, p.status, kWaitLimit);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          fence_after_sync();
+          const float2 a = stat[row], c = stat[kTile + row];
+          m = fmaxf(a.x, c.x);
+          const float ref = m == -INFINITY ? 0.f : m;
+          f0 = ex2(a.x - ref);
+          f1 = ex2(c.x - ref);
+          l = f0 * a.y + f1 * c.y;
+        }
+        const uint32_t src0 = lane_base + (shared ? C::kColO : colO), src1 = lane_base + C::kColO + D;
+        const int c_first = shared ? t * (D / 64) : 0, c_end = shared ? c_first + D / 64 : D / 32;
+        // a row that sees no key: O and l are 0 (or NaN, if a score was)
+        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(pc.q0 + tok0 + token) * p.Hq +
+                                      pc.head * p.G + (row - row_token * p.G)) * D;
+        // a part lies in the workspace column by column, four at a time, so
+        // that a warp's stores are runs of 512 bytes
+        float4 *part = reinterpret_cast<float4 *>(p.chunk_o + static_cast<int64_t>(pc.slot) * D) +
+                       row0 + row;
+#pragma unroll 1
+        for (int c = c_first; c < c_end; ++c) {
+          uint32_t r[32];
+          tmem_ld32(src0 + c * 32, r);
+          if (two) {
+            uint32_t r1[32];
+            tmem_ld32(src1 + c * 32, r1);
             tmem_wait_ld();
-            if (store) {
-              uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                uint32_t w[4];
+            for (int e = 0; e < 32; ++e)
+              r[e] = __float_as_uint(f0 * __uint_as_float(r[e]) + f1 * __uint_as_float(r1[e]));
+          } else {
+            tmem_wait_ld();
+            if (shared) {   // f0 is 1, or 0 for a row that sees no key (its O is 0, or NaN)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * e]) * inv,
-                                     __uint_as_float(r[8 * v + 2 * e + 1]) * inv);
-                d4[v] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(f0 * __uint_as_float(r[e]));
             }
           }
-        } else {
-          // a part lies in the workspace column by column, four at a time, so
-          // that a warp's stores are runs of 512 bytes
-          const int64_t slot = static_cast<int64_t>(pc.slot) + t * tile_rows + row;
-          float4 *dst = reinterpret_cast<float4 *>(p.chunk_o + static_cast<int64_t>(pc.slot) * D) +
-                        t * tile_rows + row;
+          if (!store) continue;
+          if (pc.slot < 0) {
+            uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + colO + c * 32, r);
-            tmem_wait_ld();
-            if (store) {
+            for (int v = 0; v < 4; ++v) {
+              uint32_t w[4];
 #pragma unroll
-              for (int v = 0; v < 8; ++v)
-                dst[static_cast<int64_t>(c * 8 + v) * pc.part_rows] =
-                    make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * e]) * inv,
+                                   __uint_as_float(r[8 * v + 2 * e + 1]) * inv);
+              d4[v] = make_uint4(w[0], w[1], w[2], w[3]);
             }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              part[static_cast<int64_t>(c * 8 + v) * pc.part_rows] =
+                  make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                              __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
           }
-          if (store) p.chunk_ml[slot] = make_float2(m, l);
+        }
+        if (pc.slot >= 0 && store && (!shared || t == 0))
+          p.chunk_ml[static_cast<int64_t>(pc.slot) + row0 + row] = make_float2(m, l);
+        if (shared) {
+          // neither tile's O is written again before both have been read
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBothRead));
+          ok = bounded_wait(bar(C::kBothRead), shares & 1u, abort_flag, p.status, kWaitLimit);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ++shares;
         }
       }
     }
