@@ -27,6 +27,7 @@ struct CopyParams {
   const int32_t *cu, *pos_offset;
   int total;
   int row_vecs;                  // cache vectors of one token: Hkv * D / elements per vector
+  uint32_t row_inv;              // ceil(2^32 / row_vecs); row_vecs > 1
   int tile_tokens;
   int32_t *status;
 };
@@ -39,25 +40,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Larger of two pairs of magnitudes; NaN wins.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // kLanes = lanes that share a row; all lanes of the warp call it.
 template <int kLanes>
 __device__ __forceinline__ uint4 quantise16(const uint4 &a, const uint4 &b, int &byte) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t top = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = max_bf16x2(top, w[i] & 0x7fff7fffu);
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) top = max_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // magnitudes as integers: they order like the values, and a NaN is above all
+  const uint32_t m = max(top << 16, top & 0xffff0000u);
+  if (m > 0x7f800000u) {
+    byte = kExpNan;
+    return make_uint4(0u, 0u, 0u, 0u);
+  }
   float x[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = bf16_lo(w[i]);
     x[2 * i + 1] = bf16_hi(w[i]);
-  }
-  // magnitudes as integers: they order like the values, and a NaN is above all
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m > 0x7f800000u) {
-    byte = kExpNan;
-    return make_uint4(0u, 0u, 0u, 0u);
   }
   const int e = row_exponent(__uint_as_float(m));
   byte = e + kExpBias;
@@ -106,7 +115,9 @@ __device__ __forceinline__ void copy_rows(const CopyParams &p, int b, bool is_v,
     for (int i0 = threadIdx.x & ~31; i0 < vecs; i0 += kThreads) {
       const int i = i0 + (threadIdx.x & 31);
       const bool on = i < vecs;
-      const int jt = on ? i / p.row_vecs : 0, vec = on ? i - jt * p.row_vecs : 0;
+      // i / row_vecs: i below 2^16 (a tile's vectors), so the rounded-up inverse is exact
+      const int jt = on ? static_cast<int>(__umulhi(i, p.row_inv)) : 0;
+      const int vec = on ? i - jt * p.row_vecs : 0;
       const int64_t j = j0 + jt, pos = off + j;
       const int32_t page = __ldg(table + (pos >> p.c.page_shift));
       const int row = static_cast<int>(pos) & page_mask, head = vec / kLanes;
@@ -237,6 +248,7 @@ pa_status cache_copy(void *k_rows, void *v_rows, const PagedCacheArgs &a, const 
   p.pos_offset = pos_offset;
   p.total = total;
   p.row_vecs = static_cast<int>(row / (quant ? 16 : 8));
+  p.row_inv = 0xffffffffu / static_cast<uint32_t>(p.row_vecs) + 1;
   p.tile_tokens = p.row_vecs >= kTileVecs ? 1 : kTileVecs / p.row_vecs;
   // as many tiles as the longest sequence can have, at most eight CTAs per SM over the call
   int64_t per_seq = (static_cast<int64_t>(sms) * 8 + batch - 1) / batch;
@@ -270,6 +282,7 @@ cudaError_t launch_paged_widen(const PagedAttnParams &a, int num_sms, cudaStream
   p.pos_offset = nullptr;
   p.total = 0;
   p.row_vecs = a.c.Hkv * a.c.D / 16;
+  p.row_inv = 0xffffffffu / static_cast<uint32_t>(p.row_vecs) + 1;
   p.tile_tokens = p.row_vecs >= kTileVecs ? 1 : kTileVecs / p.row_vecs;
   p.status = a.status;
   int64_t per_seq = (static_cast<int64_t>(num_sms) * 8 + a.batch - 1) / a.batch;
