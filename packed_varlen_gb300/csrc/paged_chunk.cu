@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int kThreads = (kWidenWarp + (kQuant ? kWideners : 0)) * 32;
   // columns of S that a softmax thread holds at a time: what the registers of
   // 352 or 608 threads allow
-  static constexpr int kCols = kQuant ? 32 : 64;
+  static constexpr int kCols = kQuant ? 32 : 128;
   static constexpr int kSlots = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
   static constexpr int kRaws = kQuant ? kSlots : 0;         // 8-bit tiles as they arrive
   static constexpr int kRawBytes = kTile * D;
@@ -770,20 +770,28 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     uint32_t s_waits = 0, o_waits = 0, shares = 0;
     bool ok = true;
     {
-      Piece pc;
-      while (ok && next_piece(pc)) {
-        const int tok0 = pc.tok0, tokens = pc.tokens;
+      // (a piece is kept where it was told until its rows are stored: its fields
+      // would cost registers that the scores need)
+      while (ok) {
+        const uint32_t told_at = pieces_read % C::kPieces;
+        ok = bounded_wait(bar(C::kPieceFull + told_at), (pieces_read / C::kPieces) & 1u, abort_flag,
+                          p.status, kWaitLimit);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++pieces_read;
+        const volatile Piece &pc = pieces[told_at];
+        const int j1 = pc.j1;
+        if (j1 == 0) break;
         // one tile of rows: tiles 0 and 1 are its even and its odd key tiles
-        const bool shared = tokens <= tile_tokens;
-        const int row0 = shared ? 0 : t * tile_rows;   // of this tile in the item
-        const int token = shared ? row_token : t * tile_tokens + row_token;
-        const int j_first = pc.j0 + (shared ? t : 0), j_step = shared ? 2 : 1;
-        const bool store = row < tile_rows && token < tokens;
+        const int j_step = pc.tokens <= tile_tokens ? 2 : 1;
         // keys that this row sees
         int lim = pc.lk;
-        if (p.causal) lim = min(lim, pc.before + tok0 + token + 1);
+        if (p.causal)
+          lim = min(lim, pc.before + pc.tok0 + 1 + row_token + (j_step == 2 ? 0 : t * tile_tokens));
         float m = -INFINITY, l = 0.f;
-        for (int j = j_first; j < pc.j1; j += j_step) {
+        for (int j = pc.j0 + (j_step == 2 ? t : 0); j < j1; j += j_step) {
           ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kWaitLimit);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
@@ -836,7 +844,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           if (mx > m + kRescaleThreshold) {   // from -inf: any finite score
             alpha = ex2(m - mx);
             m = mx;
-            rescale = j > j_first;
+            rescale = l != 0.f;   // without weights so far O is zero, or nothing yet
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-ref, -ref);
@@ -847,17 +855,19 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           // columns that have been read already
 #pragma unroll 1
           for (int h = 0; h < kTile / C::kCols; ++h) {
-            read_part(h);
-            uint32_t pk[kPairs];
+            if (C::kCols < kTile) read_part(h);
 #pragma unroll
-            for (int c = 0; c < kPairs; ++c) {
-              const float2 tt = __ffma2_rn(sc[c], mul2, negm2);
-              const float2 pp = make_float2(ex2(tt.x), ex2(tt.y));
-              sum4[c & 3] = __fadd2_rn(sum4[c & 3], pp);
-              pk[c] = pack_bf16x2(pp.x, pp.y);
+            for (int c0 = 0; c0 < kPairs; c0 += 16) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float2 tt = __ffma2_rn(sc[c0 + c], mul2, negm2);
+                const float2 pp = make_float2(ex2(tt.x), ex2(tt.y));
+                sum4[c & 3] = __fadd2_rn(sum4[c & 3], pp);
+                pk[c] = pack_bf16x2(pp.x, pp.y);
+              }
+              tmem_st16(lane_base + colS + h * kPairs + c0, pk);
             }
-#pragma unroll
-            for (int c = 0; c < kPairs; c += 16) tmem_st16(lane_base + colS + h * kPairs + c, pk + c);
           }
           const float2 s4 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
           l = l * alpha + (s4.x + s4.y);
@@ -880,7 +890,11 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         }
         if (!ok) break;
         // epilogue: wait for this tile's last PV, then store the valid rows
-        if (j_first < pc.j1) {
+        const bool shared = j_step == 2, two = shared && j1 - pc.j0 > 1;
+        const int row0 = shared ? 0 : t * tile_rows;   // of this tile in the item
+        const int token = row_token + (shared ? 0 : t * tile_tokens);
+        const bool store = row < tile_rows && token < pc.tokens;
+        if (t == 0 || !shared || two) {
           ok = bounded_wait(bar(C::kOFull + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
@@ -892,7 +906,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         // O is f0 O_t (+ f1 O_1 where the tiles share the rows, each of them then
         // storing half of the columns)
         float f0 = 1.f, f1 = 0.f;
-        const bool two = shared && pc.j1 - pc.j0 > 1;
         if (shared) {
           float2 *stat = reinterpret_cast<float2 *>(gbase + C::kStatOff);
           stat[t * kTile + row] = make_float2(m, l);
@@ -916,11 +929,12 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         const int c_first = shared ? t * (D / 64) : 0, c_end = shared ? c_first + D / 64 : D / 32;
         // a row that sees no key: O and l are 0 (or NaN, if a score was)
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
-        __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(pc.q0 + tok0 + token) * p.Hq +
+        const int slot = pc.slot, part_rows = pc.part_rows;
+        __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(pc.q0 + pc.tok0 + token) * p.Hq +
                                       pc.head * p.G + (row - row_token * p.G)) * D;
         // a part lies in the workspace column by column, four at a time, so
         // that a warp's stores are runs of 512 bytes
-        float4 *part = reinterpret_cast<float4 *>(p.chunk_o + static_cast<int64_t>(pc.slot) * D) +
+        float4 *part = reinterpret_cast<float4 *>(p.chunk_o + static_cast<int64_t>(slot) * D) +
                        row0 + row;
 #pragma unroll 1
         for (int c = c_first; c < c_end; ++c) {
@@ -941,7 +955,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             }
           }
           if (!store) continue;
-          if (pc.slot < 0) {
+          if (slot < 0) {
             uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
@@ -955,13 +969,13 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           } else {
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              part[static_cast<int64_t>(c * 8 + v) * pc.part_rows] =
+              part[static_cast<int64_t>(c * 8 + v) * part_rows] =
                   make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
                               __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
           }
         }
-        if (pc.slot >= 0 && store && (!shared || t == 0))
-          p.chunk_ml[static_cast<int64_t>(pc.slot) + row0 + row] = make_float2(m, l);
+        if (slot >= 0 && store && (!shared || t == 0))
+          p.chunk_ml[static_cast<int64_t>(slot) + row0 + row] = make_float2(m, l);
         if (shared) {
           // neither tile's O is written again before both have been read
           fence_before_sync();
@@ -974,6 +988,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
           ++shares;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kPieceEmpty + told_at));
       }
     }
   }
