@@ -226,7 +226,7 @@ pa_status pa_rope_packed(void *q, void *k, const int32_t *cu_seqlens_q,
  *   page_table        device int32 [batch, table_pages]: position p of
  *                     sequence b is row p % page_size of page
  *                     page_table[b, p / page_size].  Entries past a
- *                     sequence's last position are never read.
+ *                     sequence's last position may hold anything.
  *   format            PA_CACHE_BF16: bf16 rows; k_exp and v_exp are ignored.
  *                     PA_CACHE_E4M3: 8-bit rows.  A row (one token and head)
  *                     x[0..D) is held as e4m3 values y and one exponent e

@@ -307,6 +307,20 @@ CHUNKS = [
     ([5, 2], [700, 5], 100, 1, 64, 16),
     ([700], [1500], 4, 1, 128, 64),
     ([1, 300, 1, 1, 0, 40], [900, 300, 1, 250, 30, 41], 8, 2, 128, 16),
+    # either side of 32 rows of a K/V head, where another kernel takes over
+    ([8, 9, 7, 8, 9], [8, 9, 500, 2000, 2100], 8, 2, 128, 16),
+    ([32, 33, 31, 1], [1025, 1024, 1023, 513], 4, 4, 64, 64),
+    # either side of one tile of rows, of two and of four
+    ([32, 33, 64, 65, 128, 129], [600, 600, 600, 601, 129, 700], 4, 1, 128, 32),
+]
+# few heads and many keys: a sequence's key tiles are shared out over the SMs
+SHARED = [
+    ([20], [9000], 8, 2, 128, 16),                   # one tile of rows
+    ([300, 40, 1], [7000, 4001, 6500], 4, 1, 128, 64),
+    ([150, 33], [3000, 5555], 2, 2, 64, 32),
+    ([90], [2500], 14, 2, 128, 128),                 # 7 query heads to a K/V head
+    ([500], [450 + 4000], 3, 1, 64, 256),
+    ([260, 9], [16, 3000], 16, 1, 128, 16),          # fewer keys than queries beside many
 ]
 
 
@@ -315,6 +329,20 @@ CHUNKS = [
 @pytest.mark.parametrize("lengths,seq_lens,Hq,H,D,page", CHUNKS)
 def test_chunks(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal):
     _attention_case(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lengths,seq_lens,Hq,H,D,page", SHARED)
+def test_shared_out_keys(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal):
+    _attention_case(pv, lengths, seq_lens, Hq, H, D, page, fmt, causal, heads=[0, Hq // 2, Hq - 1])
+
+
+def test_no_keys_in_the_call(pv):
+    for fmt in FORMATS:
+        for lq in (1, 100):
+            out = _attention_case(pv, [lq, lq], [0, 0], 4, 2, 128, 16, fmt, True)
+            assert (out[:2 * lq] == 0).all()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -435,6 +463,25 @@ def test_same_bits_whatever_the_bounds(pv, lq, fmt):
         assert torch.equal(attend(max_q, max_k).view(torch.int16), want.view(torch.int16))
     many = attend(lq, 1024, 40)
     assert torch.equal(many.view(torch.int16), want.repeat(40, 1, 1).view(torch.int16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_widened_ahead_or_in_place(pv, D):
+    """Long sequences over an 8-bit cache: their rows as bf16 ahead of the products where
+    that takes little memory, else inside the kernel.  The same bits."""
+    Hq, H, page = 8, 2, 16
+    lengths, seq_lens = [300, 200, 40, 1], [2500, 200, 3000, 77]
+    c = Cache(seq_lens, page, H, D, "e4m3")
+    _fill(pv, c, seq_lens, 1)
+    q = _rows(sum(lengths), Hq, D, 2, 0.0).cuda()
+    outs = [pv.paged_attn_fwd(q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, 300, max_k,
+                              **c.exps()) for max_k in (3000, 1 << 20)]
+    assert pv.get_device_status() == 0
+    sizes = [pv.paged_attn_workspace_bytes(4, 541, 300, m, Hq, H, D, torch.float8_e4m3fn) -
+             pv.paged_attn_workspace_bytes(4, 541, 300, m, Hq, H, D) for m in (3000, 1 << 20)]
+    assert sizes[0] > 0 and sizes[1] == 0          # the second call widens nothing ahead
+    assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+    _check(outs[0], c, q.cpu(), lengths, seq_lens, True, 1 / math.sqrt(D), heads=[0, 5])
 
 
 @pytest.mark.parametrize("lq", [1, 33])
@@ -639,15 +686,18 @@ def test_attention_over_cache_matches_packed_attention(pv):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_graph_replays_with_new_lengths(pv, fmt):
+@pytest.mark.parametrize("n,max_k", [(1, 1024), (1, 4096), (5, 1024), (60, 4096), (150, 4096)])
+def test_graph_replays_with_new_lengths(pv, n, max_k, fmt):
     """One captured step, replayed as the sequences grow; two graphs with their own workspaces."""
     Hq, H, D, page, B = 8, 2, 128, 16, 3
-    c = Cache([900, 40, 300], page, H, D, fmt, width=64)
-    lens0 = [850, 20, 270]
+    lens0 = [850 if max_k == 1024 else 3000, 20, 270]
+    c = Cache([x + 4 + n for x in lens0], page, H, D, fmt, width=256)
     _fill(pv, c, lens0, 1)
-    cu, lens, off = _cu([1] * B), _i32(lens0), _i32(lens0)
-    q = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device="cuda")
-    k, v = (torch.zeros(B, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lengths = [1, n, 1]
+    T = sum(lengths)
+    cu, lens, off = _cu(lengths), _i32(lens0), _i32(lens0)
+    q = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     outs = [torch.zeros_like(q), torch.zeros_like(q)]
     side = torch.cuda.Stream()
     graphs = []
@@ -656,19 +706,20 @@ def test_graph_replays_with_new_lengths(pv, fmt):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=side):
             pv.kv_cache_write(k, v, c.k, c.v, cu, c.dev_table, pos_offset=off, **c.exps())
-            pv.paged_attn_fwd(q, c.k, c.v, cu, lens, c.dev_table, 1, 1024, out=o, **c.exps())
+            pv.paged_attn_fwd(q, c.k, c.v, cu, lens, c.dev_table, n, max_k, out=o, **c.exps())
         graphs.append(g)
     for step in range(4):
-        now = [n + step for n in lens0]
+        now = [x + step for x in lens0]
+        after = [x + y for x, y in zip(now, lengths)]
         off.copy_(_i32(now))
-        lens.copy_(_i32([n + 1 for n in now]))
+        lens.copy_(_i32(after))
         for x, h, s in ((q, Hq, 0), (k, H, 1), (v, H, 2)):
-            x.copy_(_rows(B, h, D, 50 * step + s, 0.0).cuda())
+            x.copy_(_rows(T, h, D, 50 * step + s, 0.0).cuda())
         for g in graphs:
             g.replay()
         torch.cuda.synchronize()
         assert pv.get_device_status() == 0
-        _check(outs[0], c, q.cpu(), [1] * B, [n + 1 for n in now], True, 1 / math.sqrt(D))
+        _check(outs[0], c, q.cpu(), lengths, after, True, 1 / math.sqrt(D))
         assert torch.equal(outs[0], outs[1])
 
 
