@@ -309,8 +309,9 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  * at the rows that belong to a sequence only, and not overlapping q or the
  * cache.  cu_seqlens_q device int32 [batch + 1], seq_lens device int32
  * [batch], batch in [1, PA_MAX_BATCH]; total_q >= cu_seqlens_q[batch]
- * (total_q = 0 does nothing, and q, out may then be NULL); max_q / max_k bound every L_b and
- * seq_lens[b]; Hq a multiple of Hkv, Hq / Hkv <= 128; scale finite.
+ * (total_q = 0 or max_q = 0 does nothing; with total_q = 0 q and out may be
+ * NULL); max_q / max_k bound every L_b and seq_lens[b]; total_q, max_q and
+ * max_k at most 2^30; Hq a multiple of Hkv, Hq / Hkv <= 128; scale finite.
  * Rows of a page past a sequence's last position never reach a result,
  * whatever their bits.  A key that causal order hides from a query has weight
  * zero there; a NaN or infinity in its V row can still reach that query as
@@ -325,7 +326,8 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  * A sequence with bad boundaries (PA_DEVICE_ERR_CU_SEQLENS), a negative
  * seq_lens (PA_DEVICE_ERR_LENGTH), or a length beyond max_q, max_k or
  * table_pages * page_size (PA_DEVICE_ERR_MAX_LEN) is skipped, its rows left
- * untouched.  Deterministic, and independent of the batch around a sequence:
+ * untouched; where bad boundaries make sequences overlap, others may be too.
+ * Deterministic, and independent of the batch around a sequence:
  * how its keys are split depends on its own lengths alone.
  */
 pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,

@@ -14,6 +14,9 @@
 namespace pa {
 namespace {
 
+// Largest token counts and lengths: sums of two stay within 32 bits.
+constexpr int32_t kMostTokens = 1 << 30;
+
 // Bytes of widened rows up to which a call over an 8-bit cache widens ahead.
 constexpr int64_t kWidenMost = int64_t{1} << 30;
 
@@ -111,7 +114,8 @@ extern "C" int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q,
                                                  int32_t max_k, int32_t Hq, int32_t Hkv,
                                                  int32_t D, int32_t format) {
   if (batch < 1 || batch > PA_MAX_BATCH || total_q < 0 || max_q < 0 || max_k < 0 || Hkv < 1 ||
-      Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > kChunkTile || (D != 64 && D != 128) ||
+      Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > kChunkTile || Hkv > 4096 || total_q > kMostTokens ||
+      max_q > kMostTokens || max_k > kMostTokens || (D != 64 && D != 128) ||
       (format != PA_CACHE_BF16 && format != PA_CACHE_E4M3))
     return -1;
   return workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format).bytes;
@@ -139,7 +143,8 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   const pa_status st = check_cache(a, p.c);
   if (st != PA_OK) return st;
   if (Hq % Hkv != 0 || q_stride < static_cast<int64_t>(Hq) * D) return PA_ERR_INVALID_ARG;
-  if (batch > PA_MAX_BATCH || Hq / Hkv > 128 || q_stride > (int64_t{1} << 38))
+  if (batch > PA_MAX_BATCH || Hq / Hkv > kChunkTile || q_stride > (int64_t{1} << 38) ||
+      total_q > kMostTokens || max_q > kMostTokens || max_k > kMostTokens)
     return PA_ERR_UNSUPPORTED;
   if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(cu_seqlens_q, 4) ||
       !aligned_to(seq_lens, 4) || (q_stride & 7) != 0 || !aligned_to(workspace, 16))

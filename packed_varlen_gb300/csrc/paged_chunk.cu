@@ -53,8 +53,9 @@ struct Cfg {
   static constexpr int kWidenWarp = kSoftmaxWarp + 8;       // first of kWideners (8-bit caches)
   static constexpr int kWideners = 8;
   static constexpr int kThreads = (kWidenWarp + (kQuant ? kWideners : 0)) * 32;
-  // columns of S that a softmax thread holds at a time: what the registers of
-  // 352 or 608 threads allow
+  // columns of S that a softmax thread holds at a time: the whole row where 352
+  // threads share the registers (read once: 2048 tokens over 14k keys in 336 us,
+  // 360 with two passes over 64), a quarter where 608 do
   static constexpr int kCols = kQuant ? 32 : 128;
   static constexpr int kSlots = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
   static constexpr int kRaws = kQuant ? kSlots : 0;         // 8-bit tiles as they arrive
@@ -195,9 +196,26 @@ __device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32
       first[n] = units;
       cut0[n] = cuts;
     }
+    // Boundaries that overlap can name more tokens than the call has, and so
+    // more parts than the workspace has room for: the list ends before those.
+    const int most_cuts = p.chunk_set == kSetFlat ? p.chunk_cut0_rest : p.chunk_cuts;
+    const int64_t most_rows = p.chunk_set == kSetFlat ? p.chunk_row0_rest : p.chunk_rows;
+    int fit = n;
+    for (int x = tid; x < n; x += 32) {
+      const int u = tmp_seq[x], pr = tmp_lk[x];
+      if (pr > 0 && (cut0[x] + u > most_cuts || part0[x] + static_cast<int64_t>(2 * u) * pr > most_rows)) {
+        fit = x;
+        break;
+      }
+    }
+    fit = __reduce_min_sync(0xffffffffu, fit);
+    if (tid == 0) {
+      *count = fit;
+      if (fit < n && report) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
+    }
   }
   __syncthreads();
-  return n;
+  return *count;
 }
 
 // A piece as the producer tells the other warps of it: finding a unit's place
@@ -799,8 +817,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
           ++s_waits;
           fence_after_sync();
-          // The row is read twice, kCols columns at a time: for its maximum,
-          // then for the weights.  Holding all of it would cost 128 registers.
+          // The row's maximum, then its weights, kCols columns at a time: read
+          // once where a thread holds all 128, else twice.
           const int seen = lim - j * kTile;
           const bool masked = __any_sync(0xffffffffu, seen < kTile);
           constexpr int kPairs = C::kCols / 2;

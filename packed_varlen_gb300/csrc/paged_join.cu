@@ -141,6 +141,7 @@ __device__ __forceinline__ void join_item_block(const PagedAttnParams &p, int cu
   if (parts < 2 || parts > kChunkShares + 1 || rows < 1 || part_rows < rows ||
       part_rows > 2 * kChunkTile || a.y < 0 ||
       a.y + static_cast<int64_t>(2 * parts - 2) * part_rows > p.chunk_rows || c.y < 0 ||
+      rows % p.G != 0 ||
       c.y + static_cast<int64_t>(rows) / p.G > p.total_q || c.z < 0 || c.z >= p.c.Hkv || r >= rows)
     return;
   auto first_row = [&](int n) -> int64_t {

@@ -561,6 +561,26 @@ def test_attention_refusals_on_the_device(pv, lq, fmt):
         assert torch.equal(out[:lq], want[:lq]) and torch.isfinite(out.float()).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lq", [1, 10, 30, 200])
+def test_overlapping_boundaries_stay_in_the_workspace(pv, lq, fmt):
+    """Boundaries that name every token many times over: an error, and nothing written beyond
+    the workspace that the arguments ask for."""
+    Hq, H, D, page, n = 8, 2, 128, 16, 300
+    c = Cache([3000], page, H, D, fmt)
+    _fill(pv, c, [3000], 1)
+    q = _rows(lq, Hq, D, 2, 0.0).cuda()
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    cu, lens = _i32([0, lq] * n + [0]), _i32([3000] * 2 * n)
+    need = pv.paged_attn_workspace_bytes(2 * n, lq, lq, 3000, Hq, H, D, dtype)
+    ws = torch.full((need + (64 << 20),), 171, dtype=torch.uint8, device="cuda")
+    pv.paged_attn_fwd(q, c.k, c.v, cu, lens, c.dev_table.repeat(2 * n, 1), lq, 3000,
+                      workspace=ws[:need], **c.exps())
+    assert pv.get_device_status() == 1
+    assert (ws[need:] == 171).all()
+    _attention_case(pv, [lq], [3000], Hq, H, D, page, fmt, True)
+
+
 def test_binding_refusals(pv):
     c = Cache([40], 16, 2, 64, "e4m3")
     x = _rows(4, 2, 64, 1).cuda()

@@ -128,6 +128,7 @@ ATTN = dict(q=A, kc=A, vc=A, ke=A, ve=A, out=A, cu=A, lens=A, table=A, batch=2, 
     (dict(max_q=-1), 1), (dict(max_k=-1), 1), (dict(Hq=0), 1), (dict(Hq=30), 1),
     (dict(qs=4095), 1), (dict(scale=math.inf), 1), (dict(scale=math.nan), 1), (dict(fmt=7), 1),
     (dict(D=96), 2), (dict(page=24), 2), (dict(batch=1025), 2), (dict(H=1, Hq=129, qs=1 << 20), 2),
+    (dict(total=(1 << 30) + 1), 2), (dict(max_q=(1 << 30) + 1), 2), (dict(max_k=(1 << 31) - 1), 2),
     (dict(q=MIS), 3), (dict(out=MIS), 3), (dict(vc=MIS), 3), (dict(cu=A + 2), 3),
     (dict(lens=A + 2), 3), (dict(qs=32 * 128 + 4), 3), (dict(ws=MIS), 3)])
 def test_attention_host_checks(lib, kw, code):
@@ -136,8 +137,9 @@ def test_attention_host_checks(lib, kw, code):
 
 
 def test_empty_calls_touch_nothing(lib):
-    a = dict(ATTN, total=0)
-    assert lib.pa_paged_attn_fwd(*[a[n] for n in ATTN], None) == 0
+    for kw in (dict(total=0), dict(total=0, q=None, out=None), dict(max_q=0)):
+        a = dict(ATTN, **kw)
+        assert lib.pa_paged_attn_fwd(*[a[n] for n in ATTN], None) == 0
     a = dict(COPY, total=0)
     assert lib.pa_kv_cache_write(*[a[n] for n in COPY], None) == 0
 
@@ -148,7 +150,8 @@ def test_workspace_bytes(lib, fmt):
     assert f(0, 1, 1, 1, 8, 8, 128, fmt) == -1 and f(1, 1, 1, 1, 9, 8, 128, fmt) == -1
     assert f(1, -1, 1, 1, 8, 8, 128, fmt) == -1 and f(1, 1, 1, 1, 8, 8, 96, fmt) == -1
     assert f(2000, 1, 1, 1, 8, 8, 128, fmt) == -1 and f(1, 1, 1, 1, 8, 8, 128, 5) == -1
-    assert f(1, 1, 1, 1, 129, 1, 128, fmt) == -1
+    assert f(1, 1, 1, 1, 129, 1, 128, fmt) == -1 and f(1, 1, 1, 1, 5000, 5000, 128, fmt) == -1
+    assert f(1, 1, 1, (1 << 30) + 1, 8, 8, 128, fmt) == -1
     for batch, total, max_q, max_k in [(4, 100, 30, 5000), (4, 3000, 1000, 20000), (1, 7, 7, 90000),
                                        (1024, 100000, 9000, 1 << 20), (1, 1, 1, 1 << 30),
                                        (3, 1 << 20, 1 << 20, 1 << 20)]:
