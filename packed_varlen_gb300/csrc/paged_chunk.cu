@@ -129,93 +129,126 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t w, uint32_t scale, uint3
   return mul_bf16x2(odd_bytes(__byte_perm(w, 0u, sel)), scale);
 }
 
-// The sequences of the call that take this kernel, most keys first, with the
+// The sequences of the call that take this launch, most keys first, with the
 // prefixes of their units, of those that may cut items (shares), and of the
-// workspace rows of their parts.  Built by every CTA; all threads call it and
-// it ends with __syncthreads().  first[n] = all units, cut0[n] = all shares.
-__device__ inline int build_list(const PagedAttnParams &p, int32_t *order, int32_t *first,
-                                 int32_t *cut0, int32_t *part0, int32_t *tmp_seq,
-                                 int32_t *tmp_lk, int32_t *count, bool report) {
+// workspace rows of their parts: first[n] = all units, cut0[n] = all shares.
+// Only the producer reads it.  Up to 32 sequences that warp makes it alone, a
+// sequence to a lane, while the other warps go on; more are ranked by all of
+// the CTA's threads first.
+struct WorkList {
+  int32_t *order, *first, *cut0, *part0;   // in shared memory
+  int32_t *units, *rows;                   // temporaries: units, rows of one part (0: never cut)
+};
+__device__ __forceinline__ bool in_launch(const PagedAttnParams &p, int lq) {
+  return !decode_takes(lq, p.G) &&
+         (p.chunk_set == kSetAll || chunk_widens(lq, p.G) == (p.chunk_set == kSetFlat));
+}
+__device__ __forceinline__ ChunkWork note_units(const PagedAttnParams &p, const WorkList &x, int at,
+                                                const PagedSeq &s) {
+  const ChunkWork w = chunk_work(s.lq, s.lk, p.causal, p.G, p.c.Hkv);
+  x.units[at] = w.units;
+  x.rows[at] = w.share ? chunk_part_rows(s.lq, p.G) : 0;
+  return w;
+}
+// One warp.  Returns the sequences; lane b keeps sequence b and its work.
+__device__ __forceinline__ int rank_few(const PagedAttnParams &p, const WorkList &x, PagedSeq &s,
+                                        ChunkWork &w, bool report) {
+  const int lane = threadIdx.x & 31;
+  int err = 0;
+  if (lane < p.batch)
+    s = paged_seq(p.cu_q, p.seq_lens, lane, p.total_q, p.max_q, p.max_k, p.capacity, err);
+  if (err && report) record_error(p.status, err);
+  const bool in = lane < p.batch && in_launch(p, s.lq);
+  const uint32_t all = __ballot_sync(0xffffffffu, in);
+  int rank = 0;
+#pragma unroll 1
+  for (uint32_t rest = all; rest; rest &= rest - 1) {
+    const int y = __ffs(rest) - 1;
+    const int lk = __shfl_sync(0xffffffffu, s.lk, y);
+    rank += lk > s.lk || (lk == s.lk && y < lane);
+  }
+  if (in) {
+    x.order[rank] = lane;
+    w = note_units(p, x, rank, s);
+  }
+  __syncwarp();
+  return __popc(all);
+}
+// All threads; ends with __syncthreads().
+__device__ __forceinline__ int rank_many(const PagedAttnParams &p, const WorkList &x,
+                                         int32_t *count, bool report) {
   const int tid = threadIdx.x, nt = blockDim.x;
+  int32_t *seq = x.units, *keys = x.rows;
   for (int b = tid; b < p.batch; b += nt) {
     int err;
     const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
     if (err && report) record_error(p.status, err);
-    if (!decode_takes(s.lq, p.G) &&
-        (p.chunk_set == kSetAll || chunk_widens(s.lq, p.G) == (p.chunk_set == kSetFlat))) {
+    if (in_launch(p, s.lq)) {
       const int at = atomicAdd(count, 1);   // any order: the ranks below are the list's
-      tmp_seq[at] = b;
-      tmp_lk[at] = s.lk;
+      seq[at] = b;
+      keys[at] = s.lk;
     }
   }
   __syncthreads();
   const int n = *count;
-  for (int x = tid; x < n; x += nt) {
-    const int b = tmp_seq[x], lb = tmp_lk[x];
+  for (int y = tid; y < n; y += nt) {
+    const int b = seq[y], lb = keys[y];
     int rank = 0;
-    for (int y = 0; y < n; ++y) rank += (tmp_lk[y] > lb) || (tmp_lk[y] == lb && tmp_seq[y] < b);
-    order[rank] = b;
+    for (int z = 0; z < n; ++z) rank += (keys[z] > lb) || (keys[z] == lb && seq[z] < b);
+    x.order[rank] = b;
   }
   __syncthreads();
-  for (int x = tid; x < n; x += nt) {
+  for (int y = tid; y < n; y += nt) {
     int err;
-    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, order[x], p.total_q, p.max_q, p.max_k, p.capacity, err);
-    const ChunkWork w = chunk_work(s.lq, s.lk, p.causal, p.G, p.c.Hkv);
-    tmp_seq[x] = w.units;
-    tmp_lk[x] = w.share ? chunk_part_rows(s.lq, p.G) : 0;   // rows of one part
+    note_units(p, x, y, paged_seq(p.cu_q, p.seq_lens, x.order[y], p.total_q, p.max_q, p.max_k,
+                                  p.capacity, err));
   }
   __syncthreads();
-  if (tid < 32) {
-    int units = 0, cuts = p.chunk_cut0, rows = static_cast<int>(p.chunk_row0);
-    for (int base = 0; base < n; base += 32) {
-      const int x = base + tid;
-      const int u = x < n ? tmp_seq[x] : 0, pr = x < n ? tmp_lk[x] : 0;
-      const int k = pr > 0 ? u : 0, r = 2 * u * pr;   // two parts at most to a share
-      int iu = u, ik = k, ir = r;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int yu = __shfl_up_sync(0xffffffffu, iu, off);
-        const int yk = __shfl_up_sync(0xffffffffu, ik, off);
-        const int yr = __shfl_up_sync(0xffffffffu, ir, off);
-        if (tid >= off) {
-          iu += yu;
-          ik += yk;
-          ir += yr;
-        }
-      }
-      if (x < n) {
-        first[x] = units + iu - u;
-        cut0[x] = cuts + ik - k;
-        part0[x] = rows + ir - r;
-      }
-      units += __shfl_sync(0xffffffffu, iu, 31);
-      cuts += __shfl_sync(0xffffffffu, ik, 31);
-      rows += __shfl_sync(0xffffffffu, ir, 31);
-    }
-    if (tid == 0) {
-      first[n] = units;
-      cut0[n] = cuts;
-    }
-    // Boundaries that overlap can name more tokens than the call has, and so
-    // more parts than the workspace has room for: the list ends before those.
-    const int most_cuts = p.chunk_set == kSetFlat ? p.chunk_cut0_rest : p.chunk_cuts;
-    const int64_t most_rows = p.chunk_set == kSetFlat ? p.chunk_row0_rest : p.chunk_rows;
-    int fit = n;
-    for (int x = tid; x < n; x += 32) {
-      const int u = tmp_seq[x], pr = tmp_lk[x];
-      if (pr > 0 && (cut0[x] + u > most_cuts || part0[x] + static_cast<int64_t>(2 * u) * pr > most_rows)) {
-        fit = x;
-        break;
+  return n;
+}
+// One warp, after either: the prefixes.  Returns the sequences that are worked on.
+__device__ __forceinline__ int add_up(const PagedAttnParams &p, const WorkList &x, int n, bool report) {
+  const int lane = threadIdx.x & 31;
+  // Boundaries that overlap can name more tokens than the call has, and so
+  // more parts than the workspace has room for: the list ends before those.
+  const int most_cuts = p.chunk_set == kSetFlat ? p.chunk_cut0_rest : p.chunk_cuts;
+  const int64_t most_rows = p.chunk_set == kSetFlat ? p.chunk_row0_rest : p.chunk_rows;
+  int units = 0, cuts = p.chunk_cut0, rows = static_cast<int>(p.chunk_row0), fit = n;
+#pragma unroll 1
+  for (int base = 0; base < n; base += 32) {
+    const int y = base + lane;
+    const int u = y < n ? x.units[y] : 0, pr = y < n ? x.rows[y] : 0;
+    const int k = pr > 0 ? u : 0, r = 2 * u * pr;   // two parts at most to a share
+    int iu = u, ik = k, ir = r;
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+      const int yu = __shfl_up_sync(0xffffffffu, iu, off);
+      const int yk = __shfl_up_sync(0xffffffffu, ik, off);
+      const int yr = __shfl_up_sync(0xffffffffu, ir, off);
+      if (lane >= off) {
+        iu += yu;
+        ik += yk;
+        ir += yr;
       }
     }
-    fit = __reduce_min_sync(0xffffffffu, fit);
-    if (tid == 0) {
-      *count = fit;
-      if (fit < n && report) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
+    if (y < n) {
+      x.first[y] = units + iu - u;
+      x.cut0[y] = cuts + ik - k;
+      x.part0[y] = rows + ir - r;
+      if (pr > 0 && (cuts + ik > most_cuts || rows + ir > most_rows) && y < fit) fit = y;
     }
+    units += __shfl_sync(0xffffffffu, iu, 31);
+    cuts += __shfl_sync(0xffffffffu, ik, 31);
+    rows += __shfl_sync(0xffffffffu, ir, 31);
   }
-  __syncthreads();
-  return *count;
+  if (lane == 0) {
+    x.first[n] = units;
+    x.cut0[n] = cuts;
+  }
+  fit = __reduce_min_sync(0xffffffffu, fit);
+  if (fit < n && lane == 0 && report) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
+  __syncwarp();
+  return fit;
 }
 
 // A piece as the producer tells the other warps of it: finding a unit's place
@@ -244,25 +277,44 @@ struct Unit {
   ChunkWork w;
   ChunkCursor cur;
 };
-__device__ __forceinline__ void open_unit(const PagedAttnParams &p, const int32_t *order,
-                                       const int32_t *first, const int32_t *part0, int n, int u,
-                                       Unit &x) {
+// Whole warp.  `s` and `w`: sequence `lane` and its work, where the call has 32 at most.
+__device__ __forceinline__ void open_unit(const PagedAttnParams &p, const WorkList &list, int n, int u,
+                                          const PagedSeq &s, const ChunkWork &w, Unit &x) {
   int lo = 0, hi = n;   // largest i < n with first[i] <= u (every sequence has a unit)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (first[mid] <= u) lo = mid; else hi = mid;
+    if (list.first[mid] <= u) lo = mid; else hi = mid;
   }
-  x.b = order[lo];
-  int err;
-  x.s = paged_seq(p.cu_q, p.seq_lens, x.b, p.total_q, p.max_q, p.max_k,
-                  p.capacity, err);
-  x.local = u - first[lo];
+  x.b = list.order[lo];
+  if (p.batch <= 32) {
+    auto from = [&](auto v) { return __shfl_sync(0xffffffffu, v, x.b); };
+    x.s = PagedSeq{from(s.q0), from(s.lq), from(s.lk)};
+    x.w.lq = x.s.lq;
+    x.w.lk = x.s.lk;
+    x.w.causal = p.causal;
+    x.w.item_tokens = 2 * (kChunkTile / p.G);
+    x.w.items_head = from(w.items_head);
+    x.w.few = from(w.few);
+    x.w.head_keys = from(w.head_keys);
+    x.w.share = from(w.share);
+  } else {
+    int err;
+    x.s = paged_seq(p.cu_q, p.seq_lens, x.b, p.total_q, p.max_q, p.max_k, p.capacity, err);
+    x.w = chunk_work(x.s.lq, x.s.lk, p.causal, p.G, p.c.Hkv);
+  }
+  x.local = u - list.first[lo];
   x.at = lo;
-  x.part0 = part0[lo];
+  x.part0 = list.part0[lo];
   x.part_rows = chunk_part_rows(x.s.lq, p.G);
   x.flat_page = p.chunk_set == kSetFlat ? p.flat_page[x.b] : 0;
-  x.w = chunk_work(x.s.lq, x.s.lk, p.causal, p.G, p.c.Hkv);
-  x.cur.start(x.w, x.local, p.c.Hkv);
+  if (x.w.share == 0) {
+    x.cur.start_whole(x.w, x.local, p.c.Hkv);
+  } else {   // even lanes find the share's start, odd ones its end
+    const ChunkPlace y = x.w.place_at((x.local + (threadIdx.x & 1)) * x.w.share, p.c.Hkv);
+    auto from = [](int v, int lane) { return __shfl_sync(0xffffffffu, v, lane); };
+    x.cur.at = ChunkPlace{from(y.head, 0), from(y.item, 0), from(y.j, 0)};
+    x.cur.end = ChunkPlace{from(y.head, 1), from(y.item, 1), from(y.j, 1)};
+  }
 }
 
 template <int D, bool kQuant>
@@ -286,16 +338,19 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   uint32_t *tmem_base_ptr = reinterpret_cast<uint32_t *>(gbase + C::kMiscOff);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(gbase + C::kMiscOff + 4);
   int32_t *counter = reinterpret_cast<int32_t *>(gbase + C::kMiscOff + 8);
-  int32_t *order = reinterpret_cast<int32_t *>(gbase + C::kSchedOff);
-  int32_t *part0 = order + PA_MAX_BATCH;
-  int32_t *cut0 = part0 + PA_MAX_BATCH;
-  int32_t *first = cut0 + PA_MAX_BATCH + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();   // the streaming kernel may take the SMs that this one leaves
-
-  // ---- set-up: barriers, TMEM, work list --------------------------------
-  if (tid == 0) {
+  // ---- set-up: barriers (warp 2), TMEM (warp 1), work list (warp 0) -------
+  // (the ring is free until the first load: the list's temporaries lie there)
+  int32_t *sched = reinterpret_cast<int32_t *>(gbase + C::kSchedOff);
+  int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
+  const WorkList list{sched, sched + 3 * PA_MAX_BATCH + 1, sched + 2 * PA_MAX_BATCH,
+                      sched + PA_MAX_BATCH, tmp, tmp + PA_MAX_BATCH};
+  PagedSeq lane_seq{0, 0, 0};   // of sequence `lane`, where the call has 32 at most
+  ChunkWork lane_work;
+  int n_seqs = 0;
+  if (tid == 64) {
     mbar_init(bar(C::kQFull), 1);
     mbar_init(bar(C::kQEmpty), 2);   // one arrival per MMA issuer
     for (int t = 0; t < 2; ++t) {
@@ -324,21 +379,20 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(base + C::kMiscOff, C::kTmemCols);
-  __syncthreads();
-  // the ring is free until the first load: use it for the build's temporaries
-  int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
-  const int n_seqs = build_list(p, order, first, cut0, part0, tmp, tmp + PA_MAX_BATCH,
-                                counter, blockIdx.x == 0);
-  // rows that the launch before this one widens
-  if (p.chunk_set == kSetFlat) griddep_wait();
+  if (warp == 0) {
+    if (elect_one()) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    if (p.batch <= 32) n_seqs = rank_few(p, list, lane_seq, lane_work, blockIdx.x == 0);
+  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_base_ptr;
-  const int n_units = first[n_seqs];
   const int tile_tokens = kTile / p.G, tile_rows = tile_tokens * p.G;
-  if (blockIdx.x == 0 && tid == 0 && p.chunk_cuts > 0)
-    p.chunk_n_cuts[p.chunk_set == kSetRest] = cut0[n_seqs];
+  if (p.batch > 32) n_seqs = rank_many(p, list, counter, blockIdx.x == 0);
 
   Piece *pieces = reinterpret_cast<Piece *>(gbase + C::kPieceOff);
   uint32_t pieces_read = 0;
@@ -364,11 +418,12 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     constexpr int kBufBytes = kQuant ? C::kRawBytes : C::kTileBytes;
     const uint32_t sBuf = base + (kQuant ? C::kRawOff : C::kRingOff);
     const bool lead = elect_one();
-    if (lead) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
+    n_seqs = add_up(p, list, n_seqs, blockIdx.x == 0);
+    const int n_units = list.first[n_seqs];
+    if (blockIdx.x == 0 && lead && p.chunk_cuts > 0)
+      p.chunk_n_cuts[p.chunk_set == kSetRest] = list.cut0[n_seqs];
+    // rows that the launch before this one widens
+    if (p.chunk_set == kSetFlat) griddep_wait();
     uint32_t q_loads = 0, slot_loads = 0;
     bool ok = true;
     auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
@@ -420,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
     };
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
       Unit x;
-      open_unit(p, order, first, part0, n_seqs, u, x);
+      open_unit(p, list, n_seqs, u, lane_seq, lane_work, x);
       int4 join_a = make_int4(0, 0, 0, 0), join_b = join_a;   // no item is cut at this unit's end
       ChunkPiece pc;
       while (ok && x.cur.next(x.w, pc)) {
@@ -439,16 +494,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         piece.part_rows = x.part_rows;
         piece.slot = pc.j0 == 0 && pc.j1 == pc.nk
                          ? -1 : static_cast<int>(x.part0) + (2 * x.local + (pc.j0 == 0)) * x.part_rows;
-        if (!tell(piece)) {
-          ok = false;
-          break;
-        }
-        if (pc.j0 == 0 && pc.j1 < pc.nk) {
-          // this share begins the item, later ones go on with it: how many
-          const int more = x.w.shares_after(x.local, pc.head, pc.item);
-          join_a = make_int4(1 + more, piece.slot, x.part_rows, 0);
-          join_b = make_int4(piece.tokens * p.G, x.s.q0 + tok0, pc.head, 0);
-        }
         const int ntq = piece.tokens > tile_tokens ? 2 : 1;
         if (!wait_all(bar(C::kQEmpty), (q_loads & 1u) ^ 1u)) {
           ok = false;
@@ -464,6 +509,16 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           }
         }
         ++q_loads;
+        if (!tell(piece)) {
+          ok = false;
+          break;
+        }
+        if (pc.j0 == 0 && pc.j1 < pc.nk) {
+          // this share begins the item, later ones go on with it: how many
+          const int more = x.w.shares_after(x.local, pc.head, pc.item);
+          join_a = make_int4(1 + more, piece.slot, x.part_rows, 0);
+          join_b = make_int4(piece.tokens * p.G, x.s.q0 + tok0, pc.head, 0);
+        }
         for (int j = pc.j0; j < pc.j1 && ok; ++j) {
           const int32_t next = j + 1 < pc.j1 ? load_pages(x, j + 1) : -1;
           ok = load_kv(&tm_k, pages, j, pc.head);
@@ -472,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         }
       }
       if (lead && ok && x.w.share > 0) {
-        int4 *join = p.chunk_join + 2 * (static_cast<int64_t>(cut0[x.at]) + x.local);
+        int4 *join = p.chunk_join + 2 * (static_cast<int64_t>(list.cut0[x.at]) + x.local);
         join[0] = join_a;
         join[1] = join_b;
       }

@@ -155,22 +155,19 @@ struct ChunkPiece {
   int head, item, j0, j1, nk;
 };
 
-// Walks the pieces of unit `u` of a sequence.
+// Walks the pieces of a unit: from `at` to before `end`.  Share u runs from
+// place_at(u * share) to place_at((u + 1) * share).
 struct ChunkCursor {
   ChunkPlace at, end;
 
-  __host__ __device__ void start(const ChunkWork &w, int u, int Hkv) {
-    if (w.share == 0) {   // heaviest items first, the heads side by side
-      const int i = u / Hkv;
-      at.head = u - i * Hkv;
-      at.item = w.items_head - 1 - i;
-      at.j = 0;
-      end = at;
-      end.j = w.tiles_of(at.item);
-    } else {
-      at = w.place_at(u * w.share, Hkv);
-      end = w.place_at((u + 1) * w.share, Hkv);
-    }
+  // A whole item: heaviest first, the heads side by side.
+  __host__ __device__ void start_whole(const ChunkWork &w, int u, int Hkv) {
+    const int i = u / Hkv;
+    at.head = u - i * Hkv;
+    at.item = w.items_head - 1 - i;
+    at.j = 0;
+    end = at;
+    end.j = w.tiles_of(at.item);
   }
   __host__ __device__ bool next(const ChunkWork &w, ChunkPiece &p) {
     const bool last = at.head == end.head && at.item == end.item;
