@@ -10,6 +10,7 @@ without their ``pa_`` prefix.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -398,45 +399,66 @@ def linear_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] =
 
 # ---------------------------------------------------------------- paged K/V cache
 # A step of single tokens takes some ten microseconds on the GPU, so these calls
-# keep their checks short: each is one test on the good path, and the functions
-# that name what is wrong run only where it fails.
+# keep their checks short: what is usual passes one test, and the functions that
+# allow for the rest, and name what is wrong, run only where it fails.
 _CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+_NOT_USUAL = (AttributeError, KeyError, TypeError, ValueError)
 
 
 def _rows_stride(t: torch.Tensor, name: str, dev: int) -> int:
     """Elements from one token to the next of a packed [T, H, D] bf16 tensor
     whose rows (one token) are contiguous."""
+    try:
+        T, H, D = t.shape
+        sT, sH, sD = t.stride()
+        if sD == 1 and sH == D and t.dtype is _BF16 and t.get_device() == dev:
+            return sT if T > 1 else H * D
+    except _NOT_USUAL:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device, not {t.device}")
     T, H, D = t.shape
-    if t.is_contiguous():
-        return H * D
-    sT, sH, sD = t.stride()
-    if (D > 1 and sD != 1) or (H > 1 and sH != D):
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return sT if T > 1 else H * D
+    if not t.is_contiguous():
+        sT, sH, sD = t.stride()
+        if (D > 1 and sD != 1) or (H > 1 and sH != D):
+            raise ValueError(f"the rows of {name} must be contiguous")
+        return sT if T > 1 else H * D
+    return H * D
 
 
 def _need_index(t: torch.Tensor, name: str, n: int, dev: int):
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and \
-            t.is_contiguous() and t.dim() == 1 and t.numel() == n:
-        return
-    _need(t, name, torch.int32, 1)
+    try:
+        if t.dtype is _I32 and t.shape == (n,) and t.get_device() == dev and t.is_contiguous():
+            return
+    except _NOT_USUAL:
+        pass
+    _need(t, name, _I32, 1)
     raise ValueError(f"{name} must be [{n}] on the cache's device, got {list(t.shape)} on {t.device}")
 
 
 def _need_out(t: torch.Tensor, name: str, shape, dev: int):
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and \
-            t.is_contiguous() and t.shape == shape:
-        return
-    _need(t, name, torch.bfloat16, len(shape))
+    try:
+        if t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return
+    except _NOT_USUAL:
+        pass
+    _need(t, name, _BF16, len(shape))
     raise ValueError(f"{name} must be {list(shape)} on the cache's device")
+
+
+def _batch_of(cu: torch.Tensor, name: str) -> int:
+    try:
+        return cu.shape[0] - 1
+    except (AttributeError, IndexError, TypeError):
+        _need(cu, name, _I32, 1)
+        raise
 
 
 def _page_stride(t: torch.Tensor, name: str) -> int:
@@ -449,8 +471,29 @@ def _page_stride(t: torch.Tensor, name: str) -> int:
 
 def _need_cache(k_cache, v_cache, k_exp, v_exp, page_table, batch):
     """Checks the cache's tensors against each other; returns (device index,
-    format, num_pages, page_size, Hkv, D, page_stride, k_exp address, v_exp
-    address)."""
+    format, num_pages, page_size, Hkv, D, page_stride, table_pages, k_exp
+    address, v_exp address)."""
+    try:
+        shape, dtype, dev = k_cache.shape, k_cache.dtype, k_cache.get_device()
+        P, page, H, D = shape
+        B, width = page_table.shape
+        if dev >= 0 and v_cache.shape == shape and v_cache.dtype is dtype and \
+                v_cache.get_device() == dev and k_cache.is_contiguous() and \
+                v_cache.is_contiguous() and B == batch and page_table.dtype is _I32 and \
+                page_table.get_device() == dev and page_table.is_contiguous():
+            if dtype is _BF16:
+                if k_exp is None and v_exp is None:
+                    return dev, 0, P, page, H, D, page * H * D, width, None, None
+            elif dtype is torch.float8_e4m3fn:
+                of_rows = (P, H, page)
+                if k_exp.dtype is _U8 and v_exp.dtype is _U8 and k_exp.shape == of_rows and \
+                        v_exp.shape == of_rows and k_exp.get_device() == dev and \
+                        v_exp.get_device() == dev and k_exp.is_contiguous() and \
+                        v_exp.is_contiguous():
+                    return (dev, 1, P, page, H, D, page * H * D, width, k_exp.data_ptr(),
+                            v_exp.data_ptr())
+    except _NOT_USUAL:
+        pass
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
@@ -478,51 +521,49 @@ def _need_cache(k_cache, v_cache, k_exp, v_exp, page_table, batch):
         if k_exp is None or v_exp is None:
             raise ValueError("an 8-bit cache needs k_exp and v_exp")
         for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-            if not (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and
-                    t.get_device() == dev and t.is_contiguous() and t.shape == (P, H, page)):
-                _need(t, n, torch.uint8, 3)
+            _need(t, n, _U8, 3)
+            if t.get_device() != dev or t.shape != (P, H, page):
                 raise ValueError(f"{n} must be [num_pages, Hkv, page_size] on the cache's device")
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
         raise ValueError("a bf16 cache has no k_exp and v_exp")
-    if not (isinstance(page_table, torch.Tensor) and page_table.dtype is torch.int32 and
-            page_table.get_device() == dev and page_table.is_contiguous() and
-            page_table.dim() == 2 and page_table.shape[0] == batch):
-        _need(page_table, "page_table", torch.int32, 2)
+    _need(page_table, "page_table", _I32, 2)
+    if page_table.get_device() != dev or page_table.shape[0] != batch:
         raise ValueError("page_table must be [batch, table_pages] on the cache's device")
-    return dev, fmt, P, page, H, D, stride, ke, ve
+    return dev, fmt, P, page, H, D, stride, page_table.shape[1], ke, ve
 
 
-class _On:
-    """Device and stream of a call on tensors of device `dev`: the call itself
-    runs with that device current, and what it allocates belongs to the stream
-    that uses it, so that the memory is not handed on while it is in use."""
-    __slots__ = ("dev", "raw", "given", "guard")
+def _raw_stream(dev: int, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
-    def __init__(self, dev, stream):
-        self.dev, self.given, self.guard = dev, stream is not None, None
-        if stream is None:
-            self.raw = torch._C._cuda_getCurrentRawStream(dev)
-        else:
-            self.raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
-    def __enter__(self):
-        if torch._C._cuda_getDevice() != self.dev:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return self.raw
+def _call(name: str, fn, dev: int, *args):
+    """The C call, with the tensors' device current."""
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != PA_OK:
+        _check(name, st)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-            self.guard = None
 
-    def new(self, make, shape, dtype):
-        dev = torch.device("cuda", self.dev)
-        if not self.given:
-            return make(shape, dtype=dtype, device=dev)
-        with torch.cuda.stream(torch.cuda.ExternalStream(self.raw, device=dev)):
-            return make(shape, dtype=dtype, device=dev)
+def _new(make, shape, dtype, dev: int, stream, raw: int) -> torch.Tensor:
+    """A tensor that belongs to the stream that uses it, so that its memory is
+    not handed on while it is in use."""
+    device = torch.device("cuda", dev)
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
+        return make(shape, dtype=dtype, device=device)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(*sizes: int) -> int:
+    # arithmetic on the sizes alone; the call through ctypes costs a microsecond
+    return load_library().pa_paged_attn_workspace_bytes(*sizes)
 
 
 def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -536,22 +577,22 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     k_exp, v_exp [num_pages, Hkv, page_size] uint8; k and v may be slices of a
     wider tensor along its last dimensions.  Returns (k_cache, v_cache)."""
     lib = _lib or load_library()
-    B = cu_seqlens.numel() - 1
-    dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
-                                                      page_table, B)
+    B = _batch_of(cu_seqlens, "cu_seqlens")
+    dev, fmt, P, page, H, D, ps, width, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
+                                                             page_table, B)
     ks, vs = _rows_stride(k, "k", dev), _rows_stride(v, "v", dev)
-    if k.shape != v.shape or k.shape[1:] != (H, D):
+    T = k.shape[0]
+    if k.shape != (T, H, D) or v.shape != (T, H, D):
         raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
     _need_index(cu_seqlens, "cu_seqlens", B + 1, dev)
+    off = None
     if pos_offset is not None:
         _need_index(pos_offset, "pos_offset", B, dev)
-    with _On(dev, stream) as raw:
-        st = lib.pa_kv_cache_write(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-                                   v_cache.data_ptr(), ke, ve, cu_seqlens.data_ptr(),
-                                   None if pos_offset is None else pos_offset.data_ptr(),
-                                   page_table.data_ptr(), B, k.shape[0], ks, vs, P, page,
-                                   page_table.shape[1], ps, H, D, fmt, raw)
-    _check("pa_kv_cache_write", st)
+        off = pos_offset.data_ptr()
+    _call("pa_kv_cache_write", lib.pa_kv_cache_write, dev, k.data_ptr(), v.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, cu_seqlens.data_ptr(), off,
+          page_table.data_ptr(), B, T, ks, vs, P, page, width, ps, H, D, fmt,
+          _raw_stream(dev, stream))
     return k_cache, v_cache
 
 
@@ -567,26 +608,27 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torc
     cu_seqlens[B] are left as they are (fresh outputs are zero-filled).
     Returns (k_out, v_out)."""
     lib = _lib or load_library()
-    B = cu_seqlens.numel() - 1
-    dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
-                                                      page_table, B)
+    B = _batch_of(cu_seqlens, "cu_seqlens")
+    dev, fmt, P, page, H, D, ps, width, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
+                                                             page_table, B)
     _need_index(cu_seqlens, "cu_seqlens", B + 1, dev)
+    off = None
     if pos_offset is not None:
         _need_index(pos_offset, "pos_offset", B, dev)
-    on = _On(dev, stream)
-    with on as raw:
-        if k_out is None:
-            k_out = on.new(torch.zeros, (int(total), H, D), torch.bfloat16)
-        if v_out is None:
-            v_out = on.new(torch.zeros, (int(total), H, D), torch.bfloat16)
-        _need_out(k_out, "k_out", (int(total), H, D), dev)
-        _need_out(v_out, "v_out", (int(total), H, D), dev)
-        st = lib.pa_kv_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
-                                  k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(),
-                                  None if pos_offset is None else pos_offset.data_ptr(),
-                                  page_table.data_ptr(), B, int(total), P, page,
-                                  page_table.shape[1], ps, H, D, fmt, raw)
-    _check("pa_kv_cache_read", st)
+        off = pos_offset.data_ptr()
+    raw = _raw_stream(dev, stream)
+    shape = (int(total), H, D)
+    if k_out is None:
+        k_out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
+    else:
+        _need_out(k_out, "k_out", shape, dev)
+    if v_out is None:
+        v_out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
+    else:
+        _need_out(v_out, "v_out", shape, dev)
+    _call("pa_kv_cache_read", lib.pa_kv_cache_read, dev, k_cache.data_ptr(), v_cache.data_ptr(),
+          ke, ve, k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), off,
+          page_table.data_ptr(), B, shape[0], P, page, width, ps, H, D, fmt, raw)
     return k_out, v_out
 
 
@@ -617,37 +659,37 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``workspace`` (uint8, paged_attn_workspace_bytes) is allocated per call
     unless given; calls that may overlap need one each."""
     lib = _lib or load_library()
-    B = cu_seqlens_q.numel() - 1
-    dev, fmt, P, page, H, D, ps, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
-                                                      page_table, B)
+    B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
+    dev, fmt, P, page, H, D, ps, width, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
+                                                             page_table, B)
     qs = _rows_stride(q, "q", dev)
-    Tq, Hq, Dq = q.shape
+    Tq, Hq, Dq = shape = q.shape
     if Dq != D or Hq < 1 or Hq % H:
         raise ValueError("q must be [Tq, Hq, D] with the cache's D and Hq a multiple of its Hkv")
     _need_index(cu_seqlens_q, "cu_seqlens_q", B + 1, dev)
     _need_index(seq_lens, "seq_lens", B, dev)
     if scale is None:
         scale = D ** -0.5
-    need = lib.pa_paged_attn_workspace_bytes(B, Tq, int(max_q), int(max_k), Hq, H, D, fmt)
-    on = _On(dev, stream)
-    with on as raw:
-        if out is None:
-            out = on.new(torch.zeros, (Tq, Hq, D), torch.bfloat16)
-        else:
-            _need_out(out, "out", (Tq, Hq, D), dev)
-        if workspace is None and need > 0:
-            workspace = on.new(torch.empty, (need,), torch.uint8)
-        wp, wn = None, 0
-        if workspace is not None:
-            if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or \
-                    not workspace.is_contiguous():
-                _need(workspace, "workspace", torch.uint8)
-                raise ValueError("workspace must be on the cache's device")
-            wp, wn = workspace.data_ptr(), workspace.numel()
-        st = lib.pa_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
-                                   out.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-                                   page_table.data_ptr(), B, Tq, int(max_q), int(max_k), qs, P,
-                                   page, page_table.shape[1], ps, Hq, H, D, fmt, int(bool(causal)),
-                                   float(scale), wp, wn, raw)
-    _check("pa_paged_attn_fwd", st)
+    max_q, max_k = int(max_q), int(max_k)
+    raw = _raw_stream(dev, stream)
+    if out is None:
+        out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
+    else:
+        _need_out(out, "out", shape, dev)
+    wp, wn = None, 0
+    if workspace is None:
+        wn = _workspace_bytes(B, Tq, max_q, max_k, Hq, H, D, fmt)
+        if wn > 0:
+            workspace = _new(torch.empty, (wn,), _U8, dev, stream, raw)
+            wp = workspace.data_ptr()
+    else:
+        if workspace.dtype is not _U8 or workspace.get_device() != dev or \
+                not workspace.is_contiguous():
+            _need(workspace, "workspace", _U8)
+            raise ValueError("workspace must be on the cache's device")
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _call("pa_paged_attn_fwd", lib.pa_paged_attn_fwd, dev, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), ke, ve, out.data_ptr(), cu_seqlens_q.data_ptr(),
+          seq_lens.data_ptr(), page_table.data_ptr(), B, Tq, max_q, max_k, qs, P, page, width, ps,
+          Hq, H, D, fmt, 1 if causal else 0, float(scale), wp, wn, raw)
     return out
