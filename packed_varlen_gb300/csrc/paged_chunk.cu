@@ -1,7 +1,14 @@
 // Paged attention of sequences with many query rows, on the 5th-generation
 // tensor cores: chunks of long inputs over everything cached before them.
 //
-// Bound by the tensor pipe once a K/V head's rows fill its tiles.  Grouped
+// Bound by the tensor pipe once a K/V head's rows fill its tiles, and by what a
+// piece of work costs around its tiles where it has few: GPU time, 32 query
+// heads on 8 of 128, 2048 tokens over 14k keys 320 us (504 GFLOP, 1577
+// TFLOP/s; some 2900 cycles for a key tile of 256 rows, of which the products
+// are 2100); two 8-bit chunks of 600 tokens over 7000, 28 heads on 4, 124 us
+// (975 TFLOP/s).  A call's first weights come 20,000 cycles after its start, a
+// third of them cold instructions, and a piece ends with 5000 cycles in
+// which its 128 KB go out.  Grouped
 // query heads share their K/V head's keys, so a 128-row tile holds the whole
 // group of 128 / G tokens (row = token * G + head of the group): each K/V
 // byte brought to shared memory serves G heads.  Otherwise the kernel is the

@@ -1,14 +1,28 @@
 // Paged attention of sequences with few query rows: single-token steps, and
-// steps of a few tokens (up to 16 rows of one K/V head's group).
+// steps of a few tokens (up to 32 rows of one K/V head's group, in groups of
+// 16 that read the keys once each).
 //
-// Bound by the cache's bytes: each is used for 2 to 16 rows only.  So the
+// Softmax online, in units of log2: with m the largest score so far and
+// s' = s * scale * log2(e), a tile adds 2^(s' - m) v to O and 2^(s' - m) to l,
+// after both were multiplied by 2^(m_old - m) where m rose; out = O / l.
+//
+// Bound by the cache's bytes: each is used for 1 to 16 rows only.  So the
 // kernel is built around a stream of copies: a unit is one (sequence, K/V
-// head, part of the keys) and belongs to one warp, which fetches its tiles
+// head, part of the keys, group of rows) and belongs to one warp, which fetches its tiles
 // with TMA into a ring of its own and waits for nobody else.  Twelve warps
-// share an SM; a tile is 8 KB of K and V, so some 100 KB are in flight per SM.
+// share an SM (eight where 16 rows of D = 128 need the registers); a tile is
+// 8 KB of K and V, so some 100 KB are in flight per SM.
 // Against fetching into registers (16 loads a lane and their addresses for
 // every tile) the copies cost four instructions of one lane.
 //
+// GPU time, 32 query heads on 8 of 128, bf16: 64 sequences of 900-8000 keys
+// 184 us (1143 MB, 6.2 TB/s; 9 us of it the join), one of 131,000 91 us (5.9
+// TB/s), four of 180-700 9.7 us (latency: some 1150 cycles a tile, and 4500
+// before the first).  64 heads on 8, 8-bit rows, 96 sequences of 2-12k: 271 us
+// (1484 MB, 5.5 TB/s; parts add 85 MB of writes, see decode_min_part).
+//
+// (Tensor cores only save instructions here: 16 rows per key keep these busy 15%
+// of the time, so the 5th generation's faster ones would gain nothing.)
 // The products run with the keys as the M side of m16n8k16 MMAs, so that 8
 // query rows fill a tile (N = 8) that 16 rows of padding would waste:
 //   S^T [16 keys, 8 rows] = K [16 keys, D] Q^T

@@ -3,7 +3,8 @@
 // tiled kernel cut (paged_chunk.cu).  A part is an unnormalised output, the
 // maximum it was taken against and the sum of its weights:
 //   out = sum_n 2^(m_n - m) o_n / sum_n 2^(m_n - m) l_n,   m = max_n m_n.
-// Bound by latency: a row's parts are a few KB at most and lie in L2.
+// Bound by latency, then by L2: 2048 rows of 17 parts take some 8 us, 6144 rows
+// of 27 (85 MB) 12, 32 rows of 228 parts 9.
 #include <math.h>
 
 #include "internal.h"
