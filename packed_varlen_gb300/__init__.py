@@ -403,6 +403,7 @@ def linear_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] =
 # allow for the rest, and name what is wrong, run only where it fails.
 _CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _NOT_USUAL = (AttributeError, KeyError, TypeError, ValueError)
 
 
@@ -535,19 +536,14 @@ def _need_cache(k_cache, v_cache, k_exp, v_exp, page_table, batch):
 
 def _raw_stream(dev: int, stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _call(name: str, fn, dev: int, *args):
-    """The C call, with the tensors' device current."""
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args)
-    if st != PA_OK:
-        _check(name, st)
+def _call_on(dev: int, fn, args) -> int:
+    """The C call with another device current than the caller's."""
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _new(make, shape, dtype, dev: int, stream, raw: int) -> torch.Tensor:
@@ -589,10 +585,13 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     if pos_offset is not None:
         _need_index(pos_offset, "pos_offset", B, dev)
         off = pos_offset.data_ptr()
-    _call("pa_kv_cache_write", lib.pa_kv_cache_write, dev, k.data_ptr(), v.data_ptr(),
-          k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, cu_seqlens.data_ptr(), off,
-          page_table.data_ptr(), B, T, ks, vs, P, page, width, ps, H, D, fmt,
-          _raw_stream(dev, stream))
+    args = (k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ke, ve,
+            cu_seqlens.data_ptr(), off, page_table.data_ptr(), B, T, ks, vs, P, page, width, ps, H,
+            D, fmt, _raw_stream(dev, stream))
+    fn = lib.pa_kv_cache_write
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_kv_cache_write", st)
     return k_cache, v_cache
 
 
@@ -626,9 +625,13 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torc
         v_out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
     else:
         _need_out(v_out, "v_out", shape, dev)
-    _call("pa_kv_cache_read", lib.pa_kv_cache_read, dev, k_cache.data_ptr(), v_cache.data_ptr(),
-          ke, ve, k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), off,
-          page_table.data_ptr(), B, shape[0], P, page, width, ps, H, D, fmt, raw)
+    args = (k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, k_out.data_ptr(), v_out.data_ptr(),
+            cu_seqlens.data_ptr(), off, page_table.data_ptr(), B, shape[0], P, page, width, ps, H, D,
+            fmt, raw)
+    fn = lib.pa_kv_cache_read
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_kv_cache_read", st)
     return k_out, v_out
 
 
@@ -688,8 +691,11 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             _need(workspace, "workspace", _U8)
             raise ValueError("workspace must be on the cache's device")
         wp, wn = workspace.data_ptr(), workspace.numel()
-    _call("pa_paged_attn_fwd", lib.pa_paged_attn_fwd, dev, q.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), ke, ve, out.data_ptr(), cu_seqlens_q.data_ptr(),
-          seq_lens.data_ptr(), page_table.data_ptr(), B, Tq, max_q, max_k, qs, P, page, width, ps,
-          Hq, H, D, fmt, 1 if causal else 0, float(scale), wp, wn, raw)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, out.data_ptr(),
+            cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B, Tq, max_q, max_k,
+            qs, P, page, width, ps, Hq, H, D, fmt, 1 if causal else 0, float(scale), wp, wn, raw)
+    fn = lib.pa_paged_attn_fwd
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_paged_attn_fwd", st)
     return out

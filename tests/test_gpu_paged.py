@@ -602,7 +602,9 @@ def test_binding_refusals(pv):
         with pytest.raises(ValueError):
             attend(**kw)
     for kw in [dict(q=x.float()), dict(k_cache=c.k.view(torch.uint8)), dict(seq_lens=lens.long()),
-               dict(v_exp=c.ve.float())]:
+               dict(v_exp=c.ve.float()), dict(cu_seqlens_q=[0, 4]), dict(q=None), dict(out=7),
+               dict(cu_seqlens_q=cu.repeat(2)[::2]), dict(v_cache=None), dict(page_table=None),
+               dict(q=torch.zeros(4, 2, 64, 2, dtype=torch.bfloat16, device="cuda")[..., 0])]:
         with pytest.raises((TypeError, ValueError)):
             attend(**kw)
     for kw in [dict(scale=math.nan), dict(max_q=-1)]:
@@ -743,17 +745,17 @@ def test_graph_replays_with_new_lengths(pv, n, max_k, fmt):
         assert torch.equal(outs[0], outs[1])
 
 
-def test_calls_on_two_streams_at_once(pv):
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_calls_on_several_streams_at_once(pv, fmt):
     """Calls that overlap, each with the workspace that the binding allocates on its stream."""
     Hq, H, D, page = 8, 2, 128, 16
     seq_lens = [3000, 1500, 40]
-    c = Cache(seq_lens, page, H, D, "bf16")
+    c = Cache(seq_lens, page, H, D, fmt)
     _fill(pv, c, seq_lens, 1)
-    qs = [_rows(3, Hq, D, 10 + i, 0.0).cuda() for i in range(2)] + \
-         [_rows(90, Hq, D, 20, 0.0).cuda()]
-    lens = [[1, 1, 1], [1, 1, 1], [30, 20, 40]]
+    lens = [[1, 1, 1], [1, 1, 1], [30, 20, 40], [700, 300, 1]]
+    qs = [_rows(sum(n), Hq, D, 10 + i, 0.0).cuda() for i, n in enumerate(lens)]
     args = [(_cu(n), _i32(seq_lens)) for n in lens]
-    want = [pv.paged_attn_fwd(q, c.k, c.v, *a, c.dev_table, max(n), 3000)
+    want = [pv.paged_attn_fwd(q, c.k, c.v, *a, c.dev_table, max(n), 3000, **c.exps())
             for q, a, n in zip(qs, args, lens)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in qs]
@@ -762,7 +764,8 @@ def test_calls_on_two_streams_at_once(pv):
         torch.cuda.synchronize()
         for _ in range(4):
             for q, a, n, s, o in zip(qs, args, lens, streams, outs):
-                pv.paged_attn_fwd(q, c.k, c.v, *a, c.dev_table, max(n), 3000, out=o, stream=s)
+                pv.paged_attn_fwd(q, c.k, c.v, *a, c.dev_table, max(n), 3000, out=o, stream=s,
+                                  **c.exps())
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
