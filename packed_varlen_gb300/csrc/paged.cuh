@@ -138,7 +138,9 @@ __device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
 // 44 against 56; 64 rows: 681 against 421, 62 against 62, 69 against 56.
 constexpr int kGroupRows = 16;
 constexpr int kFewRows = 32;
-__host__ __device__ __forceinline__ bool decode_takes(int lq, int G) { return lq <= kFewRows / G; }
+__host__ __device__ __forceinline__ bool decode_takes(int lq, int G) {
+  return lq <= kFewRows && lq * G <= kFewRows;
+}
 __host__ __device__ __forceinline__ int row_groups(int lq, int G) {   // lq <= kFewRows / G
   return (lq * G + kGroupRows - 1) / kGroupRows;
 }
@@ -198,6 +200,7 @@ struct PagedAttnParams {
   int64_t q_stride;
   int64_t capacity;    // positions that the page table has room for
   int batch, total_q, max_q, max_k, Hq, G;
+  int g_inv;           // 2^16 / G + 1: r * g_inv >> 16 is r / G for rows r < 32, G <= 32
   int causal;
   float scale_log2;
   int32_t *status;

@@ -169,6 +169,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.scale_log2 = scale * 1.4426950408889634f;
   p.batch = batch;
   p.G = Hq / Hkv;
+  p.g_inv = (1 << 16) / p.G + 1;
   const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format);
   p.dec_parts = w.dec_parts;
   p.dec_rows = w.dec_rows;

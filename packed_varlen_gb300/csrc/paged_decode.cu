@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     ++issued;
   };
 
+  auto token_of = [&](int r) { return r * p.g_inv >> 16; };   // of a row of the sequence
   for (int u = u_first; ok && more_units(u); u += u_step) {
     const int lq = w.s_lq, lk = w.s_lk, hk = w.hk;
     const int r0 = w.rows0, R = min(lq * p.G - r0, kGroupRows);   // this unit's rows
@@ -354,9 +355,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     const int n_tiles = (keys + kTile - 1) / kTile;
     table = p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages;
     open_source(w.part);
-#pragma unroll
-    for (int n = 0; n < C::kStages - 1; ++n) issue();
-
     // Q^T, the B operand of every S^T product.  Over an 8-bit cache it is f16,
     // each row scaled by a power of two to the top of f16's range (what that
     // loses lies 2^-40 below the row's largest); the scores' factor takes it back.
@@ -366,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
       const bool live = r < R;
-      const int i = live ? (r0 + r) / p.G : 0, gg = live ? r0 + r - i * p.G : 0;
+      const int i = live ? token_of(r0 + r) : 0, gg = live ? r0 + r - i * p.G : 0;
       const __nv_bfloat16 *row =
           p.q + (w.s_q0 + i) * p.q_stride + static_cast<int64_t>(hk * p.G + gg) * D;
 #pragma unroll
@@ -379,6 +377,11 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         qf[nt][ks][0] = x.x;
         qf[nt][ks][1] = x.y;
       }
+    }
+#pragma unroll
+    for (int n = 0; n < C::kStages - 1; ++n) issue();   // while q is on its way
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float back = p.scale_log2;
       if constexpr (kQuant) {
         uint32_t top = 0;   // largest exponent field of the row, in place
@@ -412,9 +415,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * t + e;
-        lim[nt][e] = r >= R ? 0 : p.causal ? lk - lq + 1 + (r0 + r) / p.G : lk;
+        lim[nt][e] = r >= R ? 0 : p.causal ? lk - lq + 1 + token_of(r0 + r) : lk;
       }
-    const int all_see = p.causal ? lk - lq + 1 + r0 / p.G : lk;   // keys before it need no mask
+    const int all_see = p.causal ? lk - lq + 1 + token_of(r0) : lk;   // keys before it need no mask
 
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
         const int r = nt * 8 + 2 * t + e;
         if (r >= R) continue;
-        const int i = (r0 + r) / p.G, h = hk * p.G + r0 + r - i * p.G;
+        const int i = token_of(r0 + r), h = hk * p.G + r0 + r - i * p.G;
         if (parts <= 1) {
           const float inv = m[nt][e] == -INFINITY ? 0.f : grade / l[nt][e];
           __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D;
