@@ -530,9 +530,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
       }
 
       // online softmax over the tile's keys, all lanes of a column in step
-      uint32_t pf[C::kHalves][NT][2];
-      bool moved = false;
-      float alpha[NT][2];
+      constexpr float kRoomAbove = kQuant ? 0.f : kRescaleThreshold;   // f16 weights: none above one
+      float mx[NT][2];
+      bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -550,21 +550,44 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+          mx[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
 #pragma unroll
-          for (int h = 1; h < C::kHalves; ++h) mx = tc::fmax3(mx, sc[h][nt][e], sc[h][nt][e + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          alpha[nt][e] = 1.f;
-          // from -inf: any finite score.  f16 weights leave no room above one.
-          if (mx > m[nt][e] + (kQuant ? 0.f : kRescaleThreshold)) {
-            alpha[nt][e] = tc::ex2(m[nt][e] - mx);
-            m[nt][e] = mx;
-            moved = true;
+          for (int h = 1; h < C::kHalves; ++h)
+            mx[nt][e] = tc::fmax3(mx[nt][e], sc[h][nt][e], sc[h][nt][e + 2]);
+          above |= mx[nt][e] > m[nt][e] + kRoomAbove;   // from -inf: any finite score
+        }
+      }
+      // The columns' maxima are joined only where one has risen (a vote in place of
+      // six shuffles: 100 cycles of a tile's 1150).
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = mx[nt][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            alpha[e] = 1.f;
+            if (x > m[nt][e] + kRoomAbove) {
+              alpha[e] = tc::ex2(m[nt][e] - x);
+              m[nt][e] = x;
+            }
+            l[nt][e] *= alpha[e];
           }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
+        }
+      }
+      uint32_t pf[C::kHalves][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
           const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-          l[nt][e] *= alpha[nt][e];
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h) {
             const float p0 = tc::ex2(sc[h][nt][e] - ref), p1 = tc::ex2(sc[h][nt][e + 2] - ref);
@@ -581,15 +604,13 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
                                              : tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
         }
       }
-      if (__any_sync(0xffffffffu, moved) || (kQuant && regrade != 1.f)) {
+      if (kQuant && regrade != 1.f) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float a[2] = {alpha[nt][0] * regrade, alpha[nt][1] * regrade};
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= a[e & 1];
-        }
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= regrade;
       }
 
       // O^T += V^T P^T
