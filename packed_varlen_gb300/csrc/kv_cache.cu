@@ -43,10 +43,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Larger of two pairs of magnitudes; NaN wins.
+// Larger magnitudes of two pairs, with signs that mean nothing; NaN wins.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -54,30 +54,29 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 template <int kLanes>
 __device__ __forceinline__ uint4 quantise16(const uint4 &a, const uint4 &b, int &byte) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t top = w[0] & 0x7fff7fffu;
+  uint32_t top = w[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) top = max_bf16x2(top, w[i] & 0x7fff7fffu);
+  for (int i = 1; i < 8; ++i) top = max_bf16x2(top, w[i]);
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) top = max_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top &= 0x7fff7fffu;
   // magnitudes as integers: they order like the values, and a NaN is above all
   const uint32_t m = max(top << 16, top & 0xffff0000u);
   if (m > 0x7f800000u) {
     byte = kExpNan;
     return make_uint4(0u, 0u, 0u, 0u);
   }
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-  }
   const int e = row_exponent(__uint_as_float(m));
   byte = e + kExpBias;
-  const float s = pow2f(-e);
+  // 2^-e twice over in bf16: the products are exact, but for values so small that
+  // they end as zero all the same (e = 7 alone makes any smaller)
+  const uint32_t s = static_cast<uint32_t>(kExpBias - e) * 0x800080u;
   uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = pack_e4m3x4(x[4 * i] * s, x[4 * i + 1] * s, x[4 * i + 2] * s, x[4 * i + 3] * s);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = mul_bf16x2(w[2 * i], s), b = mul_bf16x2(w[2 * i + 1], s);
+    r[i] = pack_e4m3x4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
+  }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
@@ -114,6 +113,8 @@ __device__ __forceinline__ void copy_rows(const CopyParams &p, int b, bool is_v,
   for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * p.tile_tokens; j0 < n;
        j0 += static_cast<int64_t>(gridDim.x) * p.tile_tokens) {
     const int vecs = min(static_cast<int64_t>(p.tile_tokens), n - j0) * p.row_vecs;
+    uint8_t *tile_rows = rows + (row0 + j0) * stride;
+    const int64_t pos0 = off + j0;
     // the whole warp goes round together (a row's lanes shuffle)
     for (int i0 = threadIdx.x & ~31; i0 < vecs; i0 += kThreads) {
       const int i = i0 + (threadIdx.x & 31);
@@ -121,20 +122,22 @@ __device__ __forceinline__ void copy_rows(const CopyParams &p, int b, bool is_v,
       // i / row_vecs: i below 2^16 (a tile's vectors), so the rounded-up inverse is exact
       const int jt = on ? static_cast<int>(__umulhi(i, p.row_inv)) : 0;
       const int vec = on ? i - jt * p.row_vecs : 0;
-      const int64_t j = j0 + jt, pos = off + j;
+      const int64_t pos = pos0 + jt;
       const int32_t page = __ldg(table + (pos >> p.c.page_shift));
       const int row = static_cast<int>(pos) & page_mask, head = vec / kLanes;
       const bool good = page_ok(p.c, page);
       if (on && !good) record_error(p.status, PA_DEVICE_ERR_PAGE);
-      uint8_t *packed = rows + (row0 + j) * stride + static_cast<int64_t>(vec) * kElems * 2;
-      const int64_t at = page * p.c.page_stride + static_cast<int64_t>(row) * p.c.Hkv * D +
-                         static_cast<int64_t>(vec) * kElems;
+      uint8_t *packed = tile_rows + static_cast<uint32_t>(jt) * stride + vec * (kElems * 2);
+      // (a page has at most 256 x 4096 x 128 elements)
+      const int64_t at = page * p.c.page_stride + (row * (p.c.Hkv * D) + vec * kElems);
       const bool live = on && good;
       if constexpr (!kQuant) {
         uint4 *cached = reinterpret_cast<uint4 *>(pages + at * 2);
         uint4 *r = reinterpret_cast<uint4 *>(packed);
         if (kWrite) {
-          if (live) *cached = __ldg(r);
+          uint4 a = make_uint4(0u, 0u, 0u, 0u);
+          if (on) a = __ldg(r);   // while the page is looked up
+          if (live) *cached = a;
         } else if (on) {
           *r = good ? *cached : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -143,7 +146,7 @@ __device__ __forceinline__ void copy_rows(const CopyParams &p, int b, bool is_v,
         uint4 *r = reinterpret_cast<uint4 *>(packed);
         if (kWrite) {
           uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
-          if (live) {
+          if (on) {   // while the page is looked up
             a = __ldg(r);
             c = __ldg(r + 1);
           }
