@@ -7,10 +7,11 @@
 // written once, 16 bytes of cache row to a thread (8 bf16 or 16 e4m3
 // elements).  A row's D elements lie in D / 8 (or D / 16) neighbouring lanes,
 // so its largest magnitude is a butterfly of 2 to 3 shuffles and the row
-// never leaves registers between its load and its store.  GPU time, 8 heads of
-// 128: 32k tokens into 8-bit pages 37.6 us (196 MB, 5.2 TB/s: 184 instructions
-// for 16 elements keep the schedulers two thirds busy), 106k tokens out of them
-// 114 us (651 MB, 5.7 TB/s), 2.4k tokens out of bf16 pages 6.6 us.
+// never leaves registers between its load and its store.  Where each token of a
+// tile goes is found first, a token to a thread, so that a vector's address is
+// a lookup in shared memory.  GPU time, 8 heads of 128: 32k tokens into 8-bit
+// pages 35.6 us (196 MB, 5.5 TB/s), 106k tokens out of them 103 us (651 MB, 6.3
+// TB/s), 2.4k tokens out of bf16 pages 5.5 us.
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_chunk_work.cuh"
@@ -21,14 +22,19 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileVecs = 1024;   // cache vectors of a tile: four per thread
+constexpr int kTileTokens = 64;   // tokens of a tile, at most
+// Cache vectors of a tile: one per thread, and twice or four times as many where
+// that leaves three tiles per SM.  256 / 512 / 1024, GPU time: 96 tokens into 8-bit
+// pages 4.3 / 4.6 / 5.4 us, 2424 out of bf16 pages 7.4 / 5.5 / 5.5, 106k out of
+// 8-bit pages - / 109 / 103 (2048: 104).
+constexpr int kLeastVecs = kThreads, kMostVecs = 1024, kTilesPerSm = 3;
 
 struct CopyParams {
   PagedCache c;
   uint8_t *k_rows, *v_rows;      // packed rows, bf16
   int64_t k_stride, v_stride;    // bytes from one token to the next
   const int32_t *cu, *pos_offset;
-  int total;
+  int batch, total;
   int row_vecs;                  // cache vectors of one token: Hkv * D / elements per vector
   uint32_t row_inv;              // ceil(2^32 / row_vecs); row_vecs > 1
   int tile_tokens;
@@ -96,133 +102,202 @@ __device__ __forceinline__ uint2 dequantise4(uint32_t w, float scale) {
   return make_uint2(pack_bf16(f[0] * scale, f[1] * scale), pack_bf16(f[2] * scale, f[3] * scale));
 }
 
-// Positions [off, off + n) of sequence b, packed rows from row0 on: the CTAs of
-// blockIdx.x stride over tiles of tile_tokens tokens, a thread over a tile's
-// cache vectors.
+// A tile: consecutive packed rows, their places found a token to a thread.
+struct Tile {
+  int32_t seq[kTileTokens];     // sequence of each row, or -1
+  int64_t pos[kTileTokens];     // its position there
+  int64_t at[kTileTokens];      // element offset in the cache, or one of the two below
+  int64_t exp_at[kTileTokens];  // offset of its first head's exponent byte
+};
+constexpr int64_t kNoRow = -1, kNoPage = -2;
+
+// Rows [row0, row0 + tokens) whose seq and pos are known: their places, then
+// the copies, a thread over the tile's cache vectors.  All threads call it,
+// after a __syncthreads().
 template <bool kWrite, bool kQuant, int D>
-__device__ __forceinline__ void copy_rows(const CopyParams &p, int b, bool is_v, int64_t row0,
-                                          int64_t off, int n) {
+__device__ __forceinline__ void copy_tile(const CopyParams &p, Tile &tile, bool is_v, int64_t row0,
+                                          int tokens) {
   constexpr int kElems = kQuant ? 16 : 8;     // elements of a cache vector
   constexpr int kLanes = D / kElems;          // vectors (lanes) of a row
-  const int32_t *table = p.c.table + static_cast<int64_t>(b) * p.c.table_pages;
-  uint8_t *rows = is_v ? p.v_rows : p.k_rows;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  uint8_t *rows = (is_v ? p.v_rows : p.k_rows) + row0 * stride;
   uint8_t *pages = static_cast<uint8_t *>(is_v ? p.c.v : p.c.k);
   uint8_t *exps = is_v ? p.c.v_exp : p.c.k_exp;
-  const int page_mask = (1 << p.c.page_shift) - 1;
-  for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * p.tile_tokens; j0 < n;
-       j0 += static_cast<int64_t>(gridDim.x) * p.tile_tokens) {
-    const int vecs = min(static_cast<int64_t>(p.tile_tokens), n - j0) * p.row_vecs;
-    uint8_t *tile_rows = rows + (row0 + j0) * stride;
-    const int64_t pos0 = off + j0;
-    // the whole warp goes round together (a row's lanes shuffle)
-    for (int i0 = threadIdx.x & ~31; i0 < vecs; i0 += kThreads) {
-      const int i = i0 + (threadIdx.x & 31);
-      const bool on = i < vecs;
-      // i / row_vecs: i below 2^16 (a tile's vectors), so the rounded-up inverse is exact
-      const int jt = on ? static_cast<int>(__umulhi(i, p.row_inv)) : 0;
-      const int vec = on ? i - jt * p.row_vecs : 0;
-      const int64_t pos = pos0 + jt;
-      const int32_t page = __ldg(table + (pos >> p.c.page_shift));
-      const int row = static_cast<int>(pos) & page_mask, head = vec / kLanes;
-      const bool good = page_ok(p.c, page);
-      if (on && !good) record_error(p.status, PA_DEVICE_ERR_PAGE);
-      uint8_t *packed = tile_rows + static_cast<uint32_t>(jt) * stride + vec * (kElems * 2);
-      // (a page has at most 256 x 4096 x 128 elements)
-      const int64_t at = page * p.c.page_stride + (row * (p.c.Hkv * D) + vec * kElems);
-      const bool live = on && good;
-      if constexpr (!kQuant) {
-        uint4 *cached = reinterpret_cast<uint4 *>(pages + at * 2);
-        uint4 *r = reinterpret_cast<uint4 *>(packed);
-        if (kWrite) {
-          uint4 a = make_uint4(0u, 0u, 0u, 0u);
-          if (on) a = __ldg(r);   // while the page is looked up
-          if (live) *cached = a;
-        } else if (on) {
-          *r = good ? *cached : make_uint4(0u, 0u, 0u, 0u);
-        }
+  for (int x = threadIdx.x; x < tokens; x += kThreads) {
+    int64_t at = kNoRow, exp_at = 0;
+    if (tile.seq[x] >= 0) {
+      const int64_t pos = tile.pos[x];
+      const int32_t page = __ldg(p.c.table + static_cast<int64_t>(tile.seq[x]) * p.c.table_pages +
+                                 (pos >> p.c.page_shift));
+      const int row = static_cast<int>(pos) & ((1 << p.c.page_shift) - 1);
+      at = kNoPage;
+      if (page_ok(p.c, page)) {
+        at = row_offset(p.c, page, row, 0);
+        exp_at = exp_offset(p.c, page, row, 0);
       } else {
-        uint4 *cached = reinterpret_cast<uint4 *>(pages + at);
-        uint4 *r = reinterpret_cast<uint4 *>(packed);
-        if (kWrite) {
-          uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
-          if (on) {   // while the page is looked up
-            a = __ldg(r);
-            c = __ldg(r + 1);
-          }
-          int byte;
-          const uint4 y = quantise16<kLanes>(a, c, byte);
-          if (live) {
-            *cached = y;
-            if (vec % kLanes == 0)
-              exps[exp_offset(p.c, page, row, head)] = static_cast<uint8_t>(byte);
-          }
-        } else if (on) {
-          uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (good) {
-            const uint4 y = *cached;
-            const float s = row_scale(exps[exp_offset(p.c, page, row, head)]);
-            const uint2 d0 = dequantise4(y.x, s), d1 = dequantise4(y.y, s),
-                        d2 = dequantise4(y.z, s), d3 = dequantise4(y.w, s);
-            o[0] = make_uint4(d0.x, d0.y, d1.x, d1.y);
-            o[1] = make_uint4(d2.x, d2.y, d3.x, d3.y);
-          }
-          r[0] = o[0];
-          r[1] = o[1];
+        record_error(p.status, PA_DEVICE_ERR_PAGE);
+      }
+    }
+    tile.at[x] = at;
+    tile.exp_at[x] = exp_at;
+  }
+  __syncthreads();
+  const int vecs = tokens * p.row_vecs;
+  // the whole warp goes round together (a row's lanes shuffle)
+  for (int i0 = threadIdx.x & ~31; i0 < vecs; i0 += kThreads) {
+    const int i = i0 + (threadIdx.x & 31);
+    // i / row_vecs: i below 2^16 (a tile's vectors), so the rounded-up inverse is exact
+    const int jt = i < vecs ? static_cast<int>(__umulhi(i, p.row_inv)) : 0;
+    const int vec = i - jt * p.row_vecs;
+    const int64_t place = i < vecs ? tile.at[jt] : kNoRow, at = place + vec * kElems;
+    const bool live = place >= 0;
+    uint4 *r = reinterpret_cast<uint4 *>(rows + jt * stride + vec * (kElems * 2));
+    if constexpr (!kQuant) {
+      uint4 *cached = reinterpret_cast<uint4 *>(pages + at * 2);
+      if (kWrite) {
+        if (live) *cached = __ldg(r);
+      } else if (place != kNoRow) {
+        *r = live ? *cached : make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else {
+      uint4 *cached = reinterpret_cast<uint4 *>(pages + at);
+      uint8_t *exp = exps + (live ? tile.exp_at[jt] + ((vec / kLanes) << p.c.page_shift) : 0);
+      if (kWrite) {
+        uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
+        if (live) {
+          a = __ldg(r);
+          c = __ldg(r + 1);
         }
+        int byte;
+        const uint4 y = quantise16<kLanes>(a, c, byte);
+        if (live) {
+          *cached = y;
+          if (vec % kLanes == 0) *exp = static_cast<uint8_t>(byte);
+        }
+      } else if (place != kNoRow) {
+        uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (live) {
+          const uint4 y = *cached;
+          const float s = row_scale(*exp);
+          const uint2 d0 = dequantise4(y.x, s), d1 = dequantise4(y.y, s), d2 = dequantise4(y.z, s),
+                      d3 = dequantise4(y.w, s);
+          o[0] = make_uint4(d0.x, d0.y, d1.x, d1.y);
+          o[1] = make_uint4(d2.x, d2.y, d3.x, d3.y);
+        }
+        r[0] = o[0];
+        r[1] = o[1];
       }
     }
   }
 }
 
-// grid (CTAs of a sequence, batch, K or V)
+// grid (tiles of the packed rows, K or V).  Every thread looks at its share of
+// the sequences for those that the tile cuts; tiles are of the packed rows, not
+// of a sequence's, so that one long sequence among many short ones has as many
+// CTAs as its rows ask for.
 template <bool kWrite, bool kQuant, int D>
 __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams p) {
-  const int b = blockIdx.y;
-  const bool is_v = blockIdx.z == 1;
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-  const int64_t off = p.pos_offset ? __ldg(p.pos_offset + b) : 0;
-  const bool lead = blockIdx.x == 0 && threadIdx.x == 0 && !is_v;
-  if (c0 < 0 || c0 > c1 || c1 > p.total || (b == 0 && c0 != 0)) {
-    if (lead) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
-    return;
+  __shared__ Tile tile;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.tile_tokens;
+  const int tokens = min(static_cast<int64_t>(p.tile_tokens), p.total - row0);
+  const bool is_v = blockIdx.y == 1, report = blockIdx.x == 0 && !is_v;
+  for (int x = threadIdx.x; x < tokens; x += kThreads) tile.seq[x] = -1;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+    const int64_t off = p.pos_offset ? __ldg(p.pos_offset + b) : 0;
+    if (c0 < 0 || c0 > c1 || c1 > p.total || (b == 0 && c0 != 0)) {
+      if (report) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
+    } else if (c0 < c1 &&
+               (off < 0 || off + (c1 - c0) > static_cast<int64_t>(p.c.table_pages) << p.c.page_shift)) {
+      if (report) record_error(p.status, PA_DEVICE_ERR_MAX_LEN);
+    } else {
+      const int from = static_cast<int>(max(c0 - row0, int64_t{0}));
+      const int to = static_cast<int>(min(c1 - row0, static_cast<int64_t>(tokens)));
+      for (int x = from; x < to; ++x) {
+        tile.seq[x] = b;
+        tile.pos[x] = off + (row0 + x - c0);
+      }
+    }
   }
-  const int n = c1 - c0;
-  if (n == 0) return;
-  if (off < 0 || off + n > static_cast<int64_t>(p.c.table_pages) << p.c.page_shift) {
-    if (lead) record_error(p.status, PA_DEVICE_ERR_MAX_LEN);
-    return;
-  }
-  copy_rows<kWrite, kQuant, D>(p, b, is_v, c0, off, n);
+  __syncthreads();
+  copy_tile<kWrite, kQuant, D>(p, tile, is_v, row0, tokens);
 }
 
 // The keys of the long sequences of an attention call over an 8-bit cache as
 // bf16 rows, a sequence from a multiple of 128 rows on (flat_page: which).
+// grid (CTAs of a sequence, long sequences, K or V).
 // The keys of two sequences of 7000, 4 heads of 128: 12 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const PagedAttnParams a, const CopyParams p) {
-  __shared__ int32_t sums[kThreads / 32];
+  __shared__ Tile tile;
+  __shared__ int32_t warp_seqs[kThreads / 32], warp_pages[kThreads / 32], found[3];
   tc::griddep_launch_dependents();
-  const int b = blockIdx.y;
-  int err;
-  const PagedSeq s = paged_seq(a.cu_q, a.seq_lens, b, a.total_q, a.max_q, a.max_k, a.capacity, err);
-  if (decode_takes(s.lq, a.G) || !chunk_widens(s.lq, a.G)) return;
-  int before = 0;   // pages of the long sequences before this one
-  for (int x = threadIdx.x; x < b; x += kThreads) {
-    const PagedSeq o = paged_seq(a.cu_q, a.seq_lens, x, a.total_q, a.max_q, a.max_k, a.capacity, err);
-    if (!decode_takes(o.lq, a.G) && chunk_widens(o.lq, a.G))
-      before += (o.lk + kChunkTile - 1) / kChunkTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.y;
+  if (threadIdx.x == 0) found[0] = -1;
+  // the long sequence of that rank, and the pages of those before it
+  int seqs = 0, pages = 0;
+  for (int b0 = 0; b0 < a.batch && seqs <= rank; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    PagedSeq s{0, 0, 0};
+    int err;
+    if (b < a.batch)
+      s = paged_seq(a.cu_q, a.seq_lens, b, a.total_q, a.max_q, a.max_k, a.capacity, err);
+    const bool in = !decode_takes(s.lq, a.G) && chunk_widens(s.lq, a.G);
+    const uint32_t all = __ballot_sync(0xffffffffu, in);
+    const int mine = in ? (s.lk - 1) / kChunkTile + (s.lk > 0) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) {
+      warp_seqs[warp] = __popc(all);
+      warp_pages[warp] = incl;
+    }
+    __syncthreads();
+    int at = seqs + __popc(all & ((1u << lane) - 1u)), page = pages + incl - mine;
+    for (int x = 0; x < kThreads / 32; ++x) {
+      if (x < warp) {
+        at += warp_seqs[x];
+        page += warp_pages[x];
+      }
+      seqs += warp_seqs[x];
+      pages += warp_pages[x];
+    }
+    if (in && at == rank) {
+      found[0] = b;
+      found[1] = page;
+      found[2] = s.lk;
+      if (blockIdx.x == 0 && blockIdx.z == 0) a.flat_page[b] = page;
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = before;
-  __syncthreads();
-  int page = 0;
-#pragma unroll
-  for (int x = 0; x < kThreads / 32; ++x) page += sums[x];
-  if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) a.flat_page[b] = page;
-  if (page + static_cast<int64_t>(s.lk + kChunkTile - 1) / kChunkTile > a.flat_pages) return;
-  copy_rows<false, true, D>(p, b, blockIdx.z == 1, static_cast<int64_t>(page) * kChunkTile, 0, s.lk);
+  const int b = found[0], page = found[1], lk = found[2];
+  if (b < 0 || page + (static_cast<int64_t>(lk) + kChunkTile - 1) / kChunkTile > a.flat_pages) return;
+  for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * p.tile_tokens; j0 < lk;
+       j0 += static_cast<int64_t>(gridDim.x) * p.tile_tokens) {
+    const int tokens = min(static_cast<int64_t>(p.tile_tokens), lk - j0);
+    __syncthreads();   // the last tile's places have been read
+    for (int x = threadIdx.x; x < tokens; x += kThreads) {
+      tile.seq[x] = b;
+      tile.pos[x] = j0 + x;
+    }
+    __syncthreads();
+    copy_tile<false, true, D>(p, tile, blockIdx.z == 1, static_cast<int64_t>(page) * kChunkTile + j0,
+                              tokens);
+  }
+}
+
+// K and V of so many tokens as tiles.
+void plan_tiles(CopyParams &p, int row_vecs, int64_t tokens, int sms) {
+  p.row_vecs = row_vecs;
+  p.row_inv = 0xffffffffu / static_cast<uint32_t>(row_vecs) + 1;
+  int vecs = kLeastVecs;
+  while (vecs < kMostVecs && 2 * tokens * row_vecs >= static_cast<int64_t>(2 * vecs) * kTilesPerSm * sms) vecs *= 2;
+  const int rows = row_vecs >= vecs ? 1 : vecs / row_vecs;
+  p.tile_tokens = rows < kTileTokens ? rows : kTileTokens;
 }
 
 template <bool kWrite>
@@ -254,14 +329,9 @@ pa_status cache_copy(void *k_rows, void *v_rows, const PagedCacheArgs &a, const 
   p.cu = cu;
   p.pos_offset = pos_offset;
   p.total = total;
-  p.row_vecs = static_cast<int>(row / (quant ? 16 : 8));
-  p.row_inv = 0xffffffffu / static_cast<uint32_t>(p.row_vecs) + 1;
-  p.tile_tokens = p.row_vecs >= kTileVecs ? 1 : kTileVecs / p.row_vecs;
-  // as many tiles as the longest sequence can have, at most eight CTAs per SM over the call
-  int64_t per_seq = (static_cast<int64_t>(sms) * 8 + batch - 1) / batch;
-  const int64_t most = (static_cast<int64_t>(total) + p.tile_tokens - 1) / p.tile_tokens;
-  if (per_seq > most) per_seq = most;
-  const dim3 grid(static_cast<unsigned>(per_seq), batch, 2);
+  p.batch = batch;
+  plan_tiles(p, static_cast<int>(row / (quant ? 16 : 8)), total, sms);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(total) + p.tile_tokens - 1) / p.tile_tokens), 2);
   auto s = reinterpret_cast<cudaStream_t>(stream);
   if (quant) {
     if (a.D == 128)
@@ -287,15 +357,13 @@ cudaError_t launch_paged_widen(const PagedAttnParams &a, int num_sms, cudaStream
   p.k_stride = p.v_stride = static_cast<int64_t>(a.c.Hkv) * a.c.D * 2;
   p.cu = nullptr;
   p.pos_offset = nullptr;
-  p.total = 0;
-  p.row_vecs = a.c.Hkv * a.c.D / 16;
-  p.row_inv = 0xffffffffu / static_cast<uint32_t>(p.row_vecs) + 1;
-  p.tile_tokens = p.row_vecs >= kTileVecs ? 1 : kTileVecs / p.row_vecs;
+  p.batch = p.total = 0;
+  plan_tiles(p, a.c.Hkv * a.c.D / 16, static_cast<int64_t>(a.flat_pages) * kChunkTile, num_sms);
   p.status = a.status;
-  int64_t per_seq = (static_cast<int64_t>(num_sms) * 8 + a.batch - 1) / a.batch;
+  int64_t per_seq = (static_cast<int64_t>(num_sms) * 16 + a.flat_seqs - 1) / a.flat_seqs;
   const int64_t most = (static_cast<int64_t>(a.max_k) + p.tile_tokens - 1) / p.tile_tokens;
   if (per_seq > most) per_seq = most;
-  const dim3 grid(static_cast<unsigned>(per_seq), a.batch, 2);
+  const dim3 grid(static_cast<unsigned>(per_seq), a.flat_seqs, 2);
   if (a.c.D == 128)
     widen_kernel<128><<<grid, kThreads, 0, stream>>>(a, p);
   else

@@ -225,6 +225,7 @@ struct PagedAttnParams {
   __nv_bfloat16 *flat_k, *flat_v;
   int32_t *flat_page;
   int flat_pages;      // room for so many; 0: the call widens nothing ahead
+  int flat_seqs;       // the most sequences that are widened
   int chunk_set;       // the sequences that a launch of the tiled kernel takes
 };
 enum { kSetAll = 0, kSetFlat = 1, kSetRest = 2 };

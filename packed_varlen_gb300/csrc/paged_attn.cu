@@ -27,6 +27,7 @@ struct WorkspacePlan {
   int64_t chunk_rows, chunk_row0_rest;
   int chunk_cuts, chunk_cut0_rest;
   int64_t flat_pages;
+  int flat_seqs;
   int64_t dec_o, dec_ml, chunk_o, chunk_ml, chunk_join, chunk_n_cuts;   // byte offsets
   int64_t flat_k, flat_v, flat_page;
   int64_t bytes;
@@ -77,6 +78,7 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
   if (format == PA_CACHE_E4M3) {
     const int64_t seqs = most_seqs(2 * item_tokens + 1), pages = seqs * tiles_k;
     if (pages * kChunkTile * Hkv * D * 4 <= kWidenMost && pages < (1 << 24)) w.flat_pages = pages;
+    w.flat_seqs = static_cast<int>(seqs);
   }
   if (w.flat_pages > 0) {
     add_cuts(most_seqs(2 * item_tokens + 1), items);
@@ -191,6 +193,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.flat_v = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_v);
   p.flat_page = reinterpret_cast<int32_t *>(ws + w.flat_page);
   p.flat_pages = static_cast<int>(w.flat_pages);
+  p.flat_seqs = w.flat_seqs;
   p.chunk_set = kSetAll;
   p.capacity = static_cast<int64_t>(table_pages) * page_size;
   auto s = reinterpret_cast<cudaStream_t>(stream);

@@ -93,6 +93,9 @@ WRITES = [
     ([1000, 3], [1, 0], 64, 5, 128),
     ([2, 513], [255, 256], 256, 20, 64),
     ([700], [12], 128, 12, 128),
+    # one long sequence among many short ones, more sequences than a CTA has threads
+    ([1] * 170 + [600] + [0, 1, 2] * 50, list(range(321)), 16, 2, 64),
+    ([0] * 300 + [9], [3] * 301, 32, 1, 128),
 ]
 
 
@@ -781,6 +784,10 @@ def test_many_sequences(pv):
     _attention_case(pv, lengths, seq_lens, Hq, H, D, page, "bf16", True)
     lengths[500], seq_lens[500] = 50, 400
     _attention_case(pv, lengths, seq_lens, Hq, H, D, page, "e4m3", True)
+    # and long ones far apart, whose 8-bit rows are widened ahead
+    for b, n, keys in ((3, 300, 900), (290, 257, 257), (291, 260, 1500), (1000, 400, 401)):
+        lengths[b], seq_lens[b] = n, keys
+    _attention_case(pv, lengths, seq_lens, Hq, H, D, page, "e4m3", True, heads=[0, 3])
 
 
 def test_random_sweep(pv):
