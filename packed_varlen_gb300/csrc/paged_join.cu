@@ -227,7 +227,11 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_join(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
-  const bool wide = p.dec_parts > 64;
+  // Many parts are worth eight warps to a row where the rows are few; where they are
+  // many a warp each fills the GPU, and the bound on the parts may be far above
+  // what the sequences have (64 of 900-8000 keys, bounds of 131,072: 191 us with
+  // eight warps to a row, 184 with one).
+  const bool wide = p.dec_parts > 64 && static_cast<int64_t>(p.batch) * p.dec_rows <= 1024;
   if (p.c.D == 128)
     return wide ? launch<128, true>(p, num_sms, stream) : launch<128, false>(p, num_sms, stream);
   return wide ? launch<64, true>(p, num_sms, stream) : launch<64, false>(p, num_sms, stream);
