@@ -815,7 +815,7 @@ static cudaError_t launch_for(const PagedAttnParams &p, int num_sms, bool after_
                        cudaStream_t stream) {
   // 8 columns where no sequence of the call can have more rows: a column's
   // results do not depend on the others, so this changes no bits
-  const int few = kFewRows / p.G, tokens = p.max_q < few ? p.max_q : few;
+  const int tokens = p.dec_rows / p.Hq;   // the bound that the workspace was planned for
   if (paged_decode_is_local(p.batch, tokens, p.max_k, p.G, p.c.Hkv))
     return launch<D, kQuant, 1, true>(p, num_sms, after_chunk, stream);
   return tokens * p.G > 8 ? launch<D, kQuant, 2, false>(p, num_sms, after_chunk, stream)

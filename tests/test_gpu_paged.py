@@ -468,6 +468,37 @@ def test_same_bits_whatever_the_bounds(pv, lq, fmt):
     assert torch.equal(many.view(torch.int16), want.repeat(40, 1, 1).view(torch.int16))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lengths,seq_lens", [([1], [1000]), ([1], [3000]), ([2, 0, 1], [900, 7, 513]),
+                                              ([9], [2000]), ([20, 1], [1024, 700])])
+def test_bounds_beyond_the_queries(pv, lengths, seq_lens, fmt):
+    """max_q far above the queries that the call has: the same bits, and nothing written beyond
+    the workspace that these arguments ask for."""
+    Hq, H, D, page = 8, 2, 128, 16
+    c = Cache(seq_lens, page, H, D, fmt, width=200)
+    _fill(pv, c, seq_lens, 1)
+    q = _rows(sum(lengths), Hq, D, 2, 0.0).cuda()
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    top = max(seq_lens)
+    want = pv.paged_attn_fwd(q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, max(lengths),
+                             top, **c.exps())
+    _check(want, c, q.cpu(), lengths, seq_lens, True, 1 / math.sqrt(D))
+    for max_q in (4, 5, 8, 9, 100, 5000, 1 << 30):
+        if max_q < max(lengths):
+            continue
+        for max_k in (top, 1024, 3000, 1 << 30):
+            if max_k < top:
+                continue
+            need = pv.paged_attn_workspace_bytes(len(lengths), sum(lengths), max_q, max_k, Hq, H, D,
+                                                 dtype)
+            ws = torch.full((need + (8 << 20),), 171, dtype=torch.uint8, device="cuda")
+            out = pv.paged_attn_fwd(q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, max_q,
+                                    max_k, workspace=ws[:need], **c.exps())
+            assert pv.get_device_status() == 0
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+            assert (ws[need:] == 171).all()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_rows_widened_ahead_or_in_place(pv, D):
     """Long sequences over an 8-bit cache: their rows as bf16 ahead of the products where
