@@ -832,3 +832,38 @@ def test_random_sweep(pv):
         heads = sorted(set(rng.integers(0, H * G, 4).tolist()))
         _attention_case(pv, lengths, seq_lens, H * G, H, D, page, FORMATS[n % 2],
                         bool(rng.random() < 0.7), seed=n, heads=heads)
+
+
+def test_random_bounds(pv):
+    """Random calls whose bounds and buffers are larger than what they hold: the bits of the
+    call with the least bounds, rows and workspace beyond theirs untouched."""
+    rng = np.random.default_rng(123)
+    for n in range(60):
+        B, H, G = int(rng.integers(1, 40)), int(rng.choice([1, 2, 3, 8])), int(rng.integers(1, 41))
+        D, page, fmt = int(rng.choice([64, 128])), int(rng.choice([16, 64, 256])), FORMATS[n % 2]
+        causal = bool(rng.random() < 0.7)
+        tops = rng.choice([0, 1, 3, 20, 200], B)
+        lengths = [int(rng.integers(0, t + 1)) for t in tops]
+        lengths[int(rng.integers(B))] += 1
+        seq_lens = [int(a * causal + rng.integers(0, rng.choice([2, 600, 3000]))) for a in lengths]
+        if sum(lengths) * H * G > 60000:
+            continue
+        c = Cache(seq_lens, page, H, D, fmt, seed=n, width=max(seq_lens) // page + 9)
+        _fill(pv, c, seq_lens, n)
+        T, extra = sum(lengths), int(rng.integers(0, 50))
+        q = _rows(T + extra, H * G, D, n + 1, 0.0).cuda()
+        cu, lens = _cu(lengths), _i32(seq_lens)
+        want = pv.paged_attn_fwd(q[:T], c.k, c.v, cu, lens, c.dev_table, max(lengths),
+                                 max(seq_lens), causal=causal, **c.exps())
+        dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+        max_q = max(lengths) + int(rng.choice([0, 1, 7, 40, 3000]))
+        max_k = max(seq_lens) + int(rng.choice([0, 1, 500, 1024, 50000]))
+        need = pv.paged_attn_workspace_bytes(B, T + extra, max_q, max_k, H * G, H, D, dtype)
+        ws = torch.full((need + (4 << 20),), 171, dtype=torch.uint8, device="cuda")
+        out = torch.full_like(q, 5.0)
+        pv.paged_attn_fwd(q, c.k, c.v, cu, lens, c.dev_table, max_q, max_k, causal=causal, out=out,
+                          workspace=ws[:need], **c.exps())
+        assert pv.get_device_status() == 0
+        what = (n, B, H, G, D, page, lengths, seq_lens, max_q, max_k, extra)
+        assert torch.equal(out[:T].view(torch.int16), want.view(torch.int16)), what
+        assert (out[T:] == 5.0).all() and (ws[need:] == 171).all(), what
