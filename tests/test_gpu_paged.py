@@ -821,6 +821,41 @@ def test_many_sequences(pv):
     _attention_case(pv, lengths, seq_lens, Hq, H, D, page, "e4m3", True, heads=[0, 3])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_most_heads(pv, fmt):
+    """4096 K/V heads: one token fills a tile of the copies, and a head has one part of the keys."""
+    H, D, page = 4096, 128, 16
+    _write_case(pv, [1, 2], [0, 15], page, H, D, fmt, False, False)
+    _attention_case(pv, [1, 40], [300, 45], H, H, D, page, fmt, True, heads=[0, 1, 2047, 4095])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_largest_batch_of_copies(pv, fmt):
+    H, D, page, B = 1, 64, 16, 65535
+    lengths = np.zeros(B, dtype=np.int64)
+    where = [0, 1, 255, 256, 40000, 65534]
+    lengths[where] = [3, 1, 20, 1, 2, 5]
+    table = np.full((B, 2), -1)
+    table[where] = np.arange(12).reshape(6, 2)
+    c = Cache([12 * page], page, H, D, fmt)
+    k, v = _rows(32, H, D, 1).cuda(), _rows(32, H, D, 2).cuda()
+    cu, dev_table = _cu(lengths.tolist()), _i32(table.tolist())
+    pv.kv_cache_write(k, v, c.k, c.v, cu, dev_table, **c.exps())
+    got = pv.kv_cache_read(c.k, c.v, cu, dev_table, 32, **c.exps())
+    assert pv.get_device_status() == 0
+    for x, y in zip((k, v), got):
+        # what a row holds after it: half a step of e4m3 off, or the same bits
+        want, row_max = x.float(), x.float().abs().amax(-1, keepdim=True)
+        bound = 0 if fmt == "bf16" else want.abs() / 16 + row_max * 2.0 ** -17
+        assert ((y.float() - want).abs() <= bound).all()
+    places = oracle.places(lengths[where].tolist(), None, table[where], page)
+    kept = torch.ones(c.P, page, dtype=torch.bool)
+    for g, r in places:
+        kept[g, r] = False
+    old = torch.tensor(7.0).to(c.k.dtype).float()
+    assert (c.k.float().cpu()[kept] == old).all() and (c.v.float().cpu()[kept] == old).all()
+
+
 def test_random_sweep(pv):
     rng = np.random.default_rng(77)
     for n in range(40):
