@@ -295,7 +295,9 @@ void plan_tiles(CopyParams &p, int row_vecs, int64_t tokens, int sms) {
   p.row_vecs = row_vecs;
   p.row_inv = 0xffffffffu / static_cast<uint32_t>(row_vecs) + 1;
   int vecs = kLeastVecs;
-  while (vecs < kMostVecs && 2 * tokens * row_vecs >= static_cast<int64_t>(2 * vecs) * kTilesPerSm * sms) vecs *= 2;
+  while (vecs < kMostVecs &&
+         2 * tokens * row_vecs >= static_cast<int64_t>(2 * vecs) * kTilesPerSm * sms)
+    vecs *= 2;
   const int rows = row_vecs >= vecs ? 1 : vecs / row_vecs;
   p.tile_tokens = rows < kTileTokens ? rows : kTileTokens;
 }
@@ -331,7 +333,8 @@ pa_status cache_copy(void *k_rows, void *v_rows, const PagedCacheArgs &a, const 
   p.total = total;
   p.batch = batch;
   plan_tiles(p, static_cast<int>(row / (quant ? 16 : 8)), total, sms);
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(total) + p.tile_tokens - 1) / p.tile_tokens), 2);
+  const int64_t tiles = (static_cast<int64_t>(total) + p.tile_tokens - 1) / p.tile_tokens;
+  const dim3 grid(static_cast<unsigned>(tiles), 2);
   auto s = reinterpret_cast<cudaStream_t>(stream);
   if (quant) {
     if (a.D == 128)

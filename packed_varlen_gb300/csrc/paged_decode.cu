@@ -807,7 +807,8 @@ cudaError_t launch(const PagedAttnParams &p, int num_sms, bool after_chunk, cuda
 }  // namespace
 
 bool paged_decode_is_local(int batch, int tokens, int max_k, int G, int Hkv) {
-  return tokens > 0 && tokens * G <= 8 && max_k <= kLocalKeys && static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
+  return tokens > 0 && tokens * G <= 8 && max_k <= kLocalKeys &&
+         static_cast<int64_t>(batch) * Hkv <= kLocalUnits;
 }
 
 template <int D, bool kQuant>

@@ -208,9 +208,12 @@ __global__ void __launch_bounds__(kWarps<kWide> * 32)
 
 template <int D, bool kWide>
 cudaError_t launch(const PagedAttnParams &p, int num_sms, cudaStream_t stream) {
-  const int per_seq = p.dec_parts <= 1 ? 0 : kWide ? p.dec_rows : (p.dec_rows + kWarps<kWide> - 1) / kWarps<kWide>;
+  const int per_seq = p.dec_parts <= 1 ? 0
+                      : kWide          ? p.dec_rows
+                                       : (p.dec_rows + kWarps<kWide> - 1) / kWarps<kWide>;
   const int dec_ctas = per_seq * p.batch;
-  const int64_t cut_ctas = static_cast<int64_t>(p.chunk_cuts) * (2 * kChunkTile / 32 * (D / 32) / kWarps<kWide>);
+  const int64_t cut_ctas =
+      static_cast<int64_t>(p.chunk_cuts) * (2 * kChunkTile / 32 * (D / 32) / kWarps<kWide>);
   const int most = num_sms * (kWide ? 6 : 12);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
