@@ -41,6 +41,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_launch.h"
@@ -431,239 +433,250 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     }
 
     int unit = 0;   // exponent byte that the output's units go by (8-bit caches)
-    for (int n = 0; n < n_tiles; ++n) {
-      const int key = k0 + n * kTile;
-      // every lane has read the stage that is filled next (the tile before this one)
-      __syncwarp();
-      issue();
-      const uint32_t stage = used % C::kStages;
-      ok = tc::bounded_wait(bars + 8 * stage, (used / C::kStages) & 1u, gave_up, p.status, kWaitLimit);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      ++used;
-      const uint8_t *st = ring + stage * C::kStageBytes;
-      const uint32_t bad_runs = bad >> (stage * C::kHalves);
-      // byte address of 16-byte vector `vec` of row `row` of a run
-      auto vector = [&](const uint8_t *run, int row, int vec) -> const uint8_t * {
-        if constexpr (C::kLine == 128)
-          return run + (vec >> 3) * 2048 + row * 128 + (((vec & 7) ^ (row & 7)) << 4);
-        else
-          return run + row * C::kLine + (vec << 4);
-      };
+    // A sequence of at most eight rows takes one group of columns, whatever the call's
+    // others need: 96 8-bit sequences of one token in a call that allows for 32 rows 324
+    // / 300 us.  (Not the second half of more rows: its warps would run ahead of those
+    // that read the same keys, 246 / 275 us with five tokens of four heads each.)
+    auto walk = [&](auto columns) {
+      constexpr int NC = decltype(columns)::value;
+      for (int n = 0; n < n_tiles; ++n) {
+        const int key = k0 + n * kTile;
+        // every lane has read the stage that is filled next (the tile before this one)
+        __syncwarp();
+        issue();
+        const uint32_t stage = used % C::kStages;
+        ok = tc::bounded_wait(bars + 8 * stage, (used / C::kStages) & 1u, gave_up, p.status, kWaitLimit);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++used;
+        const uint8_t *st = ring + stage * C::kStageBytes;
+        [[maybe_unused]] const uint32_t bad_runs = bad >> (stage * C::kHalves);
+        // byte address of 16-byte vector `vec` of row `row` of a run
+        auto vector = [&](const uint8_t *run, int row, int vec) -> const uint8_t * {
+          if constexpr (C::kLine == 128)
+            return run + (vec >> 3) * 2048 + row * 128 + (((vec & 7) ^ (row & 7)) << 4);
+          else
+            return run + row * C::kLine + (vec << 4);
+        };
 
-      // S^T = K Q^T, in two chains
-      float sc[C::kHalves][NT][4];
-      float kf[C::kHalves][2], vf[C::kHalves][2];
-      int vexp[C::kHalves][2];   // of keys key_of(g) and 8 later
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) {
-        float s2[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[h][nt][e] = s2[nt][e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < C::kKVecs / 2; ++i) {
-          const uint8_t *run = st + h * C::kRunBytes;
-          const uint4 a = *reinterpret_cast<const uint4 *>(vector(run, kkey, t + 4 * i));
-          const uint4 c = *reinterpret_cast<const uint4 *>(vector(run, kkey + 8, t + 4 * i));
-          if constexpr (!kQuant) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma16816(sc[h][nt], a.x, c.x, a.y, c.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-              mma16816(s2[nt], a.z, c.z, a.w, c.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
-            }
-          } else {
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t a0 = f16_low(aw[x]), a2 = f16_high(aw[x]);
-              const uint32_t a1 = f16_low(cw[x]), a3 = f16_high(cw[x]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816_f16(x & 1 ? s2[nt] : sc[h][nt], a0, a1, a2, a3, qf[nt][4 * i + x][0],
-                             qf[nt][4 * i + x][1]);
-            }
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[h][nt][e] += s2[nt][e];
-        if constexpr (kQuant) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // bytes of rows that are not the sequence's may be anything
-            const bool mine = key + 16 * h + 8 * e + kkey < lk && !(bad_runs >> h & 1u);
-            const uint8_t *ex = st + C::kExpOff + h * 16 + 8 * e + kkey;
-            kf[h][e] = mine ? row_scale(ex[0]) : 0.f;
-            vexp[h][e] = mine ? ex[C::kHalves * 16] : 0;
-          }
-        }
-      }
-      // V's scales go into the weights: w 2^(e - unit + 14) in f16, unit the
-      // largest exponent so far, so nothing exceeds 2^14, and full precision is
-      // kept down to 2^-28 of a weight of one on the largest rows.  The output
-      // accumulates in units of 2^(unit - 14).
-      float regrade = 1.f;
-      if constexpr (kQuant) {
-        int top = 0;
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (vexp[h][e] != kExpNan) top = max(top, vexp[h][e]);
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top > unit) {
-          regrade = pow2f(max(unit - top, -126));
-          unit = top;
-        }
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            vf[h][e] = vexp[h][e] == 0 ? 0.f
-                       : vexp[h][e] == kExpNan ? __int_as_float(0x7fffffff)
-                                               : pow2f(max(vexp[h][e] - unit, -126) + 14);
-      }
-
-      // online softmax over the tile's keys, all lanes of a column in step
-      constexpr float kRoomAbove = kQuant ? 0.f : kRescaleThreshold;   // f16 weights: none above one
-      float mx[NT][2];
-      bool above = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        // S^T = K Q^T, in two chains
+        float sc[C::kHalves][NC][4];
+        float kf[C::kHalves][2], vf[C::kHalves][2];
+        [[maybe_unused]] int vexp[C::kHalves][2];   // of keys key_of(g) and 8 later
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
+          float s2[NC][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (kQuant) sc[h][nt][e] *= kf[h][e >> 1];
-            sc[h][nt][e] *= factor[nt][e & 1];
-          }
-          if (key + kTile > all_see) {
+          for (int nt = 0; nt < NC; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key + 16 * h + kkey + 8 * (e >> 1) >= lim[nt][e & 1]) sc[h][nt][e] = -INFINITY;
-          }
-        }
+            for (int e = 0; e < 4; ++e) sc[h][nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+          for (int i = 0; i < C::kKVecs / 2; ++i) {
+            const uint8_t *run = st + h * C::kRunBytes;
+            const uint4 a = *reinterpret_cast<const uint4 *>(vector(run, kkey, t + 4 * i));
+            const uint4 c = *reinterpret_cast<const uint4 *>(vector(run, kkey + 8, t + 4 * i));
+            if constexpr (!kQuant) {
 #pragma unroll
-          for (int h = 1; h < C::kHalves; ++h)
-            mx[nt][e] = tc::fmax3(mx[nt][e], sc[h][nt][e], sc[h][nt][e + 2]);
-          above |= mx[nt][e] > m[nt][e] + kRoomAbove;   // from -inf: any finite score
-        }
-      }
-      // The columns' maxima are joined only where one has risen (a vote in place of
-      // six shuffles: 100 cycles of a tile's 1150).
-      if (__any_sync(0xffffffffu, above)) {
+              for (int nt = 0; nt < NC; ++nt) {
+                mma16816(sc[h][nt], a.x, c.x, a.y, c.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+                mma16816(s2[nt], a.z, c.z, a.w, c.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+              }
+            } else {
+              const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float alpha[2];
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t a0 = f16_low(aw[x]), a2 = f16_high(aw[x]);
+                const uint32_t a1 = f16_low(cw[x]), a3 = f16_high(cw[x]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = mx[nt][e];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            alpha[e] = 1.f;
-            if (x > m[nt][e] + kRoomAbove) {
-              alpha[e] = tc::ex2(m[nt][e] - x);
-              m[nt][e] = x;
+                for (int nt = 0; nt < NC; ++nt)
+                  mma16816_f16(x & 1 ? s2[nt] : sc[h][nt], a0, a1, a2, a3, qf[nt][4 * i + x][0],
+                               qf[nt][4 * i + x][1]);
+              }
             }
-            l[nt][e] *= alpha[e];
           }
 #pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt)
+          for (int nt = 0; nt < NC; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
+            for (int e = 0; e < 4; ++e) sc[h][nt][e] += s2[nt][e];
+          if constexpr (kQuant) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // bytes of rows that are not the sequence's may be anything
+              const bool mine = key + 16 * h + 8 * e + kkey < lk && !(bad_runs >> h & 1u);
+              const uint8_t *ex = st + C::kExpOff + h * 16 + 8 * e + kkey;
+              kf[h][e] = mine ? row_scale(ex[0]) : 0.f;
+              vexp[h][e] = mine ? ex[C::kHalves * 16] : 0;
+            }
+          }
         }
-      }
-      uint32_t pf[C::kHalves][NT][2];
+        // V's scales go into the weights: w 2^(e - unit + 14) in f16, unit the
+        // largest exponent so far, so nothing exceeds 2^14, and full precision is
+        // kept down to 2^-28 of a weight of one on the largest rows.  The output
+        // accumulates in units of 2^(unit - 14).
+        float regrade = 1.f;
+        if constexpr (kQuant) {
+          int top = 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+          for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+            for (int e = 0; e < 2; ++e)
+              if (vexp[h][e] != kExpNan) top = max(top, vexp[h][e]);
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (top > unit) {
+            regrade = pow2f(max(unit - top, -126));
+            unit = top;
+          }
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              vf[h][e] = vexp[h][e] == 0 ? 0.f
+                         : vexp[h][e] == kExpNan ? __int_as_float(0x7fffffff)
+                                                 : pow2f(max(vexp[h][e] - unit, -126) + 14);
+        }
+
+        // online softmax over the tile's keys, all lanes of a column in step
+        constexpr float kRoomAbove = kQuant ? 0.f : kRescaleThreshold;   // f16 weights: none above one
+        float mx[NC][2];
+        bool above = false;
+#pragma unroll
+        for (int nt = 0; nt < NC; ++nt) {
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h) {
-            const float p0 = tc::ex2(sc[h][nt][e] - ref), p1 = tc::ex2(sc[h][nt][e + 2] - ref);
-            l[nt][e] += p0 + p1;
-            sc[h][nt][e] = kQuant ? p0 * vf[h][0] : p0;
-            sc[h][nt][e + 2] = kQuant ? p1 * vf[h][1] : p1;
-          }
-        }
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-          pf[h][nt][0] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][0], sc[h][nt][1])
-                                             : tc::pack_bf16x2(sc[h][nt][0], sc[h][nt][1]));
-          pf[h][nt][1] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][2], sc[h][nt][3])
-                                             : tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
-        }
-      }
-      if (kQuant && regrade != 1.f) {
+            for (int e = 0; e < 4; ++e) {
+              if (kQuant) sc[h][nt][e] *= kf[h][e >> 1];
+              sc[h][nt][e] *= factor[nt][e & 1];
+            }
+            if (key + kTile > all_see) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= regrade;
-      }
-
-      // O^T += V^T P^T
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) {
-#pragma unroll
-        for (int cs = 0; cs < C::kVSets; ++cs) {
-          uint32_t va[4][C::kVWords];
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int row = vkey[kk & 1] + 8 * (kk >> 1);
-            const uint8_t *run = st + (C::kHalves + h) * C::kRunBytes;
-            if constexpr (C::kVBytes == 16) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(vector(run, row, g + 8 * cs));
-              va[kk][0] = x.x;
-              va[kk][1] = x.y;
-              va[kk][2] = x.z;
-              va[kk][3] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2 *>(run + row * C::kLine + g * 8);
-              va[kk][0] = x.x;
-              va[kk][1] = x.y;
+              for (int e = 0; e < 4; ++e)
+                if (key + 16 * h + kkey + 8 * (e >> 1) >= lim[nt][e & 1]) sc[h][nt][e] = -INFINITY;
             }
           }
-          if (key + kTile > lk) {   // rows past the last key: weight 0, whatever they hold
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (key + 16 * h + vkey[kk & 1] + 8 * (kk >> 1) >= lk)
+          for (int e = 0; e < 2; ++e) {
+            mx[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
 #pragma unroll
-                for (int x = 0; x < C::kVWords; ++x) va[kk][x] = 0u;
+            for (int h = 1; h < C::kHalves; ++h)
+              mx[nt][e] = tc::fmax3(mx[nt][e], sc[h][nt][e], sc[h][nt][e + 2]);
+            above |= mx[nt][e] > m[nt][e] + kRoomAbove;   // from -inf: any finite score
+          }
+        }
+        // The columns' maxima are joined only where one has risen (a vote in place of
+        // six shuffles: 100 cycles of a tile's 1150).
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+          for (int nt = 0; nt < NC; ++nt) {
+            float alpha[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = mx[nt][e];
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              alpha[e] = 1.f;
+              if (x > m[nt][e] + kRoomAbove) {
+                alpha[e] = tc::ex2(m[nt][e] - x);
+                m[nt][e] = x;
+              }
+              l[nt][e] *= alpha[e];
+            }
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
+          }
+        }
+        uint32_t pf[C::kHalves][NC][2];
+#pragma unroll
+        for (int nt = 0; nt < NC; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+              const float p0 = tc::ex2(sc[h][nt][e] - ref), p1 = tc::ex2(sc[h][nt][e + 2] - ref);
+              l[nt][e] += p0 + p1;
+              sc[h][nt][e] = kQuant ? p0 * vf[h][0] : p0;
+              sc[h][nt][e + 2] = kQuant ? p1 * vf[h][1] : p1;
+            }
           }
 #pragma unroll
-          for (int x = 0; x < C::kVWords; ++x) {
-            // bf16: values 0 and 1 of the word, of two keys each; e4m3: 0, 1 and 2, 3
-            const uint32_t ab0 = __byte_perm(va[0][x], va[1][x], kQuant ? 0x5140 : 0x5410);
-            const uint32_t ab1 = __byte_perm(va[0][x], va[1][x], kQuant ? 0x7362 : 0x7632);
-            const uint32_t cd0 = __byte_perm(va[2][x], va[3][x], kQuant ? 0x5140 : 0x5410);
-            const uint32_t cd1 = __byte_perm(va[2][x], va[3][x], kQuant ? 0x7362 : 0x7632);
+          for (int h = 0; h < C::kHalves; ++h) {
+            pf[h][nt][0] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][0], sc[h][nt][1])
+                                               : tc::pack_bf16x2(sc[h][nt][0], sc[h][nt][1]));
+            pf[h][nt][1] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][2], sc[h][nt][3])
+                                               : tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
+          }
+        }
+        if (kQuant && regrade != 1.f) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (!kQuant) {
-                mma16816(o[nt][cs * 4 + x], ab0, ab1, cd0, cd1, pf[h][nt][0], pf[h][nt][1]);
+          for (int nt = 0; nt < NC; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][mt][e] *= regrade;
+        }
+
+        // O^T += V^T P^T
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+#pragma unroll
+          for (int cs = 0; cs < C::kVSets; ++cs) {
+            uint32_t va[4][C::kVWords];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const int row = vkey[kk & 1] + 8 * (kk >> 1);
+              const uint8_t *run = st + (C::kHalves + h) * C::kRunBytes;
+              if constexpr (C::kVBytes == 16) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(vector(run, row, g + 8 * cs));
+                va[kk][0] = x.x;
+                va[kk][1] = x.y;
+                va[kk][2] = x.z;
+                va[kk][3] = x.w;
               } else {
-                mma16816_f16(o[nt][2 * x], f16_low(ab0), f16_high(ab0), f16_low(cd0),
-                             f16_high(cd0), pf[h][nt][0], pf[h][nt][1]);
-                mma16816_f16(o[nt][2 * x + 1], f16_low(ab1), f16_high(ab1), f16_low(cd1),
-                             f16_high(cd1), pf[h][nt][0], pf[h][nt][1]);
+                const uint2 x = *reinterpret_cast<const uint2 *>(run + row * C::kLine + g * 8);
+                va[kk][0] = x.x;
+                va[kk][1] = x.y;
+              }
+            }
+            if (key + kTile > lk) {   // rows past the last key: weight 0, whatever they hold
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (key + 16 * h + vkey[kk & 1] + 8 * (kk >> 1) >= lk)
+#pragma unroll
+                  for (int x = 0; x < C::kVWords; ++x) va[kk][x] = 0u;
+            }
+#pragma unroll
+            for (int x = 0; x < C::kVWords; ++x) {
+              // bf16: values 0 and 1 of the word, of two keys each; e4m3: 0, 1 and 2, 3
+              const uint32_t ab0 = __byte_perm(va[0][x], va[1][x], kQuant ? 0x5140 : 0x5410);
+              const uint32_t ab1 = __byte_perm(va[0][x], va[1][x], kQuant ? 0x7362 : 0x7632);
+              const uint32_t cd0 = __byte_perm(va[2][x], va[3][x], kQuant ? 0x5140 : 0x5410);
+              const uint32_t cd1 = __byte_perm(va[2][x], va[3][x], kQuant ? 0x7362 : 0x7632);
+#pragma unroll
+              for (int nt = 0; nt < NC; ++nt) {
+                if constexpr (!kQuant) {
+                  mma16816(o[nt][cs * 4 + x], ab0, ab1, cd0, cd1, pf[h][nt][0], pf[h][nt][1]);
+                } else {
+                  mma16816_f16(o[nt][2 * x], f16_low(ab0), f16_high(ab0), f16_low(cd0),
+                               f16_high(cd0), pf[h][nt][0], pf[h][nt][1]);
+                  mma16816_f16(o[nt][2 * x + 1], f16_low(ab1), f16_high(ab1), f16_low(cd1),
+                               f16_high(cd1), pf[h][nt][0], pf[h][nt][1]);
+                }
               }
             }
           }
         }
       }
-    }
+    };
+    if (NT == 1 || lq * p.G <= 8)
+      walk(std::integral_constant<int, 1>{});
+    else
+      walk(std::integral_constant<int, NT>{});
 
     // ---- this lane's columns: D / 8 dims each of rows 2 t and 2 t + 1, in runs
     // of 2 KR consecutive ones
