@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       mbar_init(bar(C::kPieceEmpty + s), C::kReaders);
     }
     *abort_flag = 0;
-    *counter = 0;
+    if (p.batch > 32) *counter = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(base + C::kMiscOff, C::kTmemCols);
@@ -392,7 +392,10 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    if (p.batch <= 32) n_seqs = rank_few(p, list, lane_seq, lane_work, blockIdx.x == 0);
+    if (p.batch <= 32) {
+      n_seqs = rank_few(p, list, lane_seq, lane_work, blockIdx.x == 0);
+      if (lane == 0) *counter = n_seqs;
+    }
   }
   fence_before_sync();
   __syncthreads();
@@ -400,6 +403,13 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
   const uint32_t tmem = *tmem_base_ptr;
   const int tile_tokens = kTile / p.G, tile_rows = tile_tokens * p.G;
   if (p.batch > 32) n_seqs = rank_many(p, list, counter, blockIdx.x == 0);
+  if (*counter == 0) {   // none for this launch, as in a call whose bounds allow for them only
+    if (blockIdx.x == 0 && tid == 0 && p.chunk_cuts > 0)
+      p.chunk_n_cuts[p.chunk_set == kSetRest] = p.chunk_cut0;
+    if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+    griddep_wait();
+    return;
+  }
 
   Piece *pieces = reinterpret_cast<Piece *>(gbase + C::kPieceOff);
   uint32_t pieces_read = 0;
