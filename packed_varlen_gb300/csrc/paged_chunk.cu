@@ -210,6 +210,7 @@ __device__ __forceinline__ int rank_many(const PagedAttnParams &p, const WorkLis
     note_units(p, x, y, paged_seq(p.cu_q, p.seq_lens, x.order[y], p.total_q, p.max_q, p.max_k,
                                   p.capacity, err));
   }
+  fence_proxy_async();   // the ring's copies come after every access to the temporaries there
   __syncthreads();
   return n;
 }
@@ -254,6 +255,7 @@ __device__ __forceinline__ int add_up(const PagedAttnParams &p, const WorkList &
   }
   fit = __reduce_min_sync(0xffffffffu, fit);
   if (fit < n && lane == 0 && report) record_error(p.status, PA_DEVICE_ERR_CU_SEQLENS);
+  fence_proxy_async();   // as in rank_many
   __syncwarp();
   return fit;
 }

@@ -902,3 +902,23 @@ def test_random_bounds(pv):
         what = (n, B, H, G, D, page, lengths, seq_lens, max_q, max_k, extra)
         assert torch.equal(out[:T].view(torch.int16), want.view(torch.int16)), what
         assert (out[T:] == 5.0).all() and (ws[need:] == 171).all(), what
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B", [31, 32, 33, 700])
+def test_work_list_beside_the_first_tiles(pv, B, fmt):
+    """The list of work is made where the first K tile lands: batches on both ways of making
+    it, every CTA's first tiles right behind it, over and over with the same bits."""
+    Hq, H, D, page = 4, 2, 128, 16
+    lengths = [33 + b % 7 if b % (B // 30) == 0 else 0 for b in range(B)]
+    seq_lens = [n + 3 * (b % 50) if n else 0 for b, n in enumerate(lengths)]
+    c = Cache(seq_lens, page, H, D, fmt)
+    _fill(pv, c, seq_lens, 1)
+    q = _rows(sum(lengths), Hq, D, 2, 0.0).cuda()
+    args = (q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, 40, max(seq_lens))
+    want = pv.paged_attn_fwd(*args, **c.exps())
+    _check(want, c, q.cpu(), lengths, seq_lens, True, 1 / math.sqrt(D), heads=[0, 3])
+    for _ in range(20):
+        assert torch.equal(pv.paged_attn_fwd(*args, **c.exps()).view(torch.int16),
+                           want.view(torch.int16))
+    assert pv.get_device_status() == 0
