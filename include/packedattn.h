@@ -300,9 +300,12 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  *   out[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], k[j,h',:]>) * v[j,h',:]
  * A query that sees no key gets zeros.  8-bit rows enter the products as the
  * bf16 values that pa_kv_cache_read returns.  Scores, maxima, sums and the
- * output's accumulation are fp32; softmax weights are rounded to bf16 (f16 for
- * few queries over an 8-bit cache) for the product with V, and the output once
- * to bf16.
+ * output's accumulation are fp32; softmax weights are rounded to bf16 for the
+ * product with V, and the output once to bf16.  Few queries (L_b * Hq / Hkv
+ * <= 32) over an 8-bit cache: w * 2^e, weight times the exponent of the V row,
+ * is rounded to f16 instead, in full down to 2^-28 of the largest that the
+ * query and head sees and in steps of at most 2^-38 of that below; and so are
+ * q's elements, against the largest of their row.
  *
  * q [total_q, Hq, D] bf16, q_stride elements from one token to the next
  * (>= Hq * D, a multiple of 8); out [total_q, Hq, D] bf16 contiguous, written

@@ -37,7 +37,13 @@
 // V) fall on different banks of the 128-byte swizzle.
 //
 // 8-bit rows become f16, which holds e4m3 exactly, one conversion for two
-// values; the rows' scales go to the scores (K) and into the weights (V).
+// values; the rows' scales go to the scores (K) and into the weights (V).  The
+// weight that is rounded to f16 is then w 2^e of a V row held in units of 2^e,
+// so a row of q's running reference is the largest s' + e in place of the
+// largest s': among the keys that it sees, the one whose values move the output
+// most has a weight near f16's top, whatever the exponents of rows that are
+// hidden or weigh nothing.  Full precision is kept down to 2^-28 of that, and a
+// step of 2^-38 below.
 #include <cuda.h>
 #include <math.h>
 
@@ -58,6 +64,12 @@ constexpr int kLocalWarps = 8;    // of a CTA that joins its parts itself
 constexpr int kLocalUnits = 304;
 constexpr int kLocalKeys = 1024;  // longest sequence that has at most a part for each warp
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
+// 8-bit caches: weights are 2^(s' - m) 2^(e + kExpMid), m the largest s' + e + kExpMid
+// less kWeightTop at its last rise, so at most 2^(kWeightTop + kWeightRoom), within f16.
+// With e + kExpMid in [-54, 53] the sum of the 2^(s' - m) stays within 2^-39 and
+// 2^69 for each key.  A rise costs the output's rescaling: room for one binade.
+constexpr int kExpMid = 46;
+constexpr float kWeightTop = 14.f, kWeightRoom = 1.f;
 
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (~2 s)
 constexpr long long kDrainLimit = 400000000LL;
@@ -432,7 +444,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    int unit = 0;   // exponent byte that the output's units go by (8-bit caches)
     // A sequence of at most eight rows takes one group of columns, whatever the call's
     // others need: 96 8-bit sequences of one token in a call that allows for 32 rows 324
     // / 300 us.  (Not the second half of more rows: its warps would run ahead of those
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         // S^T = K Q^T, in two chains
         float sc[C::kHalves][NC][4];
         float kf[C::kHalves][2], vf[C::kHalves][2];
-        [[maybe_unused]] int vexp[C::kHalves][2];   // of keys key_of(g) and 8 later
+        [[maybe_unused]] float ve[C::kHalves][2];   // log2 of vf: keys key_of(g) and 8 later
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
           float s2[NC][4];
@@ -507,38 +518,17 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
               const bool mine = key + 16 * h + 8 * e + kkey < lk && !(bad_runs >> h & 1u);
               const uint8_t *ex = st + C::kExpOff + h * 16 + 8 * e + kkey;
               kf[h][e] = mine ? row_scale(ex[0]) : 0.f;
-              vexp[h][e] = mine ? ex[C::kHalves * 16] : 0;
+              const int byte = mine ? ex[C::kHalves * 16] : kExpNan;
+              const bool has = byte != kExpNan;   // an exponent
+              ve[h][e] = static_cast<float>((has ? byte : kExpBias + kExpMin) - (kExpBias - kExpMid));
+              vf[h][e] = has ? pow2f(byte - (kExpBias - kExpMid))
+                             : mine ? __int_as_float(0x7fffffff) : 0.f;
             }
           }
         }
-        // V's scales go into the weights: w 2^(e - unit + 14) in f16, unit the
-        // largest exponent so far, so nothing exceeds 2^14, and full precision is
-        // kept down to 2^-28 of a weight of one on the largest rows.  The output
-        // accumulates in units of 2^(unit - 14).
-        float regrade = 1.f;
-        if constexpr (kQuant) {
-          int top = 0;
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (vexp[h][e] != kExpNan) top = max(top, vexp[h][e]);
-          top = __reduce_max_sync(0xffffffffu, top);
-          if (top > unit) {
-            regrade = pow2f(max(unit - top, -126));
-            unit = top;
-          }
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              vf[h][e] = vexp[h][e] == 0 ? 0.f
-                         : vexp[h][e] == kExpNan ? __int_as_float(0x7fffffff)
-                                                 : pow2f(max(vexp[h][e] - unit, -126) + 14);
-        }
 
         // online softmax over the tile's keys, all lanes of a column in step
-        constexpr float kRoomAbove = kQuant ? 0.f : kRescaleThreshold;   // f16 weights: none above one
+        constexpr float kRoomAbove = kQuant ? kWeightTop + kWeightRoom : kRescaleThreshold;
         float mx[NC][2];
         bool above = false;
 #pragma unroll
@@ -558,10 +548,14 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+            // over an 8-bit cache: of score and V's scale together
+            auto level = [&](int h, int x) {
+              return kQuant ? sc[h][nt][e + 2 * x] + ve[h][x] : sc[h][nt][e + 2 * x];
+            };
+            mx[nt][e] = fmaxf(level(0, 0), level(0, 1));
 #pragma unroll
             for (int h = 1; h < C::kHalves; ++h)
-              mx[nt][e] = tc::fmax3(mx[nt][e], sc[h][nt][e], sc[h][nt][e + 2]);
+              mx[nt][e] = tc::fmax3(mx[nt][e], level(h, 0), level(h, 1));
             above |= mx[nt][e] > m[nt][e] + kRoomAbove;   // from -inf: any finite score
           }
         }
@@ -579,6 +573,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
               alpha[e] = 1.f;
               if (x > m[nt][e] + kRoomAbove) {
+                if (kQuant) x -= kWeightTop;
                 alpha[e] = tc::ex2(m[nt][e] - x);
                 m[nt][e] = x;
               }
@@ -611,14 +606,6 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
             pf[h][nt][1] = transpose8x8(kQuant ? pack_f16x2(sc[h][nt][2], sc[h][nt][3])
                                                : tc::pack_bf16x2(sc[h][nt][2], sc[h][nt][3]));
           }
-        }
-        if (kQuant && regrade != 1.f) {
-#pragma unroll
-          for (int nt = 0; nt < NC; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][mt][e] *= regrade;
         }
 
         // O^T += V^T P^T
@@ -680,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
 
     // ---- this lane's columns: D / 8 dims each of rows 2 t and 2 t + 1, in runs
     // of 2 KR consecutive ones
-    const float grade = kQuant && unit > 0 ? pow2f(unit - kExpBias - 14) : 1.f;
+    const float grade = kQuant ? pow2f(-kExpMid) : 1.f;
     constexpr int KR = !kQuant && D == 128 ? 4 : D / 16;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -692,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         if (r >= R) continue;
         const int i = token_of(r0 + r), h = hk * p.G + r0 + r - i * p.G;
         if (parts <= 1) {
-          const float inv = m[nt][e] == -INFINITY ? 0.f : grade / l[nt][e];
+          const float inv = m[nt][e] == -INFINITY ? 0.f : 1.f / l[nt][e];
           __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D;
 #pragma unroll
           for (int mt = 0; mt < D / 16; mt += 4) {
@@ -700,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
             uint32_t x[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              x[y] = tc::pack_bf16x2(o[nt][mt + y][e] * inv, o[nt][mt + y][e + 2] * inv);
+              x[y] = tc::pack_bf16x2(o[nt][mt + y][e] * grade * inv, o[nt][mt + y][e + 2] * grade * inv);
             *reinterpret_cast<uint4 *>(dst + d) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         } else {

@@ -922,3 +922,45 @@ def test_work_list_beside_the_first_tiles(pv, B, fmt):
         assert torch.equal(pv.paged_attn_fwd(*args, **c.exps()).view(torch.int16),
                            want.view(torch.int16))
     assert pv.get_device_status() == 0
+
+
+@pytest.mark.parametrize("gap", [20, 40, 60, 95])
+@pytest.mark.parametrize("n", [40, 700, 3000])
+@pytest.mark.parametrize("lq,Hq,D", [(2, 4, 128), (5, 4, 128), (8, 2, 64), (8, 8, 128)])
+def test_hidden_rows_of_large_scale(pv, lq, Hq, D, n, gap):
+    """8-bit values of later tokens far above those that a token sees: its result is held to the
+    values that it sees, as in the other kernels."""
+    H = 2
+    c = Cache([n, n + 9], 16, H, D, "e4m3")
+    k, v = _rows(2 * n + 9, H, D, 3, 0.3), _rows(2 * n + 9, H, D, 4, 0.3).float()
+    up = torch.zeros(2 * n + 9)
+    for i in range(lq):                    # every new token far above the one before it
+        up[n - lq + i] = up[2 * n + 9 - lq + i] = gap * (i + 1) / lq
+    v = (v * torch.exp2(up.round() + 4 - gap)[:, None, None]).to(torch.bfloat16)
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n, n + 9]), c.dev_table, **c.exps())
+    q = _rows(2 * lq, Hq, D, 5, 0.0)
+    out = _attend(pv, c, q, [lq, lq], [n, n + 9], True)
+    _check(out, c, q, [lq, lq], [n, n + 9], True, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("below,gap", [(115, 60), (115, 95), (40, 40), (40, 36), (60, 20), (110, 107)])
+@pytest.mark.parametrize("n", [50, 900, 5000])
+@pytest.mark.parametrize("lq,D", [(1, 128), (1, 64), (4, 128)])
+def test_weightless_rows_of_large_scale(pv, lq, D, n, below, gap):
+    """Keys that weigh 2^-below and hold 8-bit values 2^gap above the others': neither is lost,
+    whichever comes first and wherever the parts of the keys end."""
+    H, Hq = 1, 2
+    g = torch.Generator().manual_seed(9)
+    u = (torch.randint(0, 2, (D,), generator=g) * 2 - 1).float()
+    for places in ([0], [n // 2, n // 2 + 1], [n - lq - 1], list(range(0, n - lq, 7))):
+        c = Cache([n], 16, H, D, "e4m3")
+        k, v = _rows(n, H, D, 3, 0.0).float() * 0.25, _rows(n, H, D, 4, 0.3).float()
+        k -= (k @ u)[..., None] * u / D
+        v *= 2.0 ** (6 - gap)
+        k[places], v[places] = -u, v[places] * 2.0 ** gap
+        k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+        pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n]), c.dev_table, **c.exps())
+        q = u.expand(lq, Hq, D).to(torch.bfloat16).contiguous()
+        scale = below * math.log(2) / D
+        out = _attend(pv, c, q, [lq], [n], True, scale=scale)
+        _check(out, c, q, [lq], [n], True, scale)
