@@ -237,6 +237,8 @@ pa_status pa_rope_packed(void *q, void *k, const int32_t *cu_seqlens_q,
  *                     them, read back as 57344).  e + 127 is the row's byte in
  *   k_exp, v_exp      [num_pages, Hkv, page_size], contiguous.  Byte 255: the
  *                     row held a NaN and reads back as NaN throughout.
+ *                     (A cache filled by other means holds bytes 27 to 134,
+ *                     or 255; an e4m3 NaN in it is a NaN wherever it is read.)
  *
  * page_size a power of two in [16, 256], D in {64, 128}, Hkv in [1, 4096],
  * num_pages and table_pages >= 1; page_stride * element size a multiple of 16

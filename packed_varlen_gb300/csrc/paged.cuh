@@ -77,21 +77,10 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Widening in registers: e4m3's bits moved to bf16's place (sign, then the
-// exponent's four bits at the low end of bf16's eight) are the value times
-// 2^-120, subnormals included, and one packed bf16 multiply by 2^(120 + e)
-// makes it the exact stored value.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-// Bytes 1 and 3 (0 and 2) of w, e4m3, as two bf16 of 2^-120 their value.
-__device__ __forceinline__ uint32_t odd_bytes(uint32_t w) {
-  return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t even_bytes(uint32_t w) {
-  return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
 }
 // 2^(120 + e) in bf16 bits for an exponent byte e + 127; NaN for a NaN row.
 __device__ __forceinline__ uint32_t widen_scale(uint32_t byte) {

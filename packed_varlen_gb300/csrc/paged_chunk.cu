@@ -130,10 +130,26 @@ __device__ __forceinline__ int load_now(const uint8_t *p) {
   return static_cast<int>(v);
 }
 
-// Two e4m3 bytes of w, as `sel` puts them in bytes 1 and 3, to bf16 times
-// 2^-120, times the row's scale.
+// Two e4m3 bytes of w, as `sel` puts them in bytes 0 and 2, to bf16: times 16
+// their seven low bits lie in bf16's place and the sign at bit 11, which the sum
+// carries on to bit 15.  That is the value times 2^-120, subnormals included, and
+// one packed multiply by 2^(120 + e) makes it the exact stored value.
 __device__ __forceinline__ uint32_t widen_pair(uint32_t w, uint32_t scale, uint32_t sel) {
-  return mul_bf16x2(odd_bytes(__byte_perm(w, 0u, sel)), scale);
+  return mul_bf16x2((__byte_perm(w, 0u, sel) * 16u + 0x78007800u) & 0x87f087f0u, scale);
+}
+// A byte of 0x7f or 0xff is e4m3's NaN, which a write never makes but a cache
+// filled elsewhere may hold; widen_pair takes it for 480.  Not 0 where 16 bytes hold one:
+__device__ __forceinline__ uint32_t holds_nan(const uint4 &y) {
+  auto carry = [](uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; };
+  return (carry(y.x) | carry(y.y) | carry(y.z) | carry(y.w)) & 0x80808080u;
+}
+// widen_pair with NaN in its place; scale 0: no row of the sequence, and zeros.
+__device__ __forceinline__ uint32_t widen_pair_nan(uint32_t w, uint32_t scale, uint32_t sel) {
+  uint32_t r = widen_pair(w, scale, sel);
+  const uint32_t y = __byte_perm(w, 0u, sel);
+  if (scale != 0u && (y & 0x7fu) == 0x7fu) r |= 0x7fffu;
+  if (scale != 0u && (y & 0x7f0000u) == 0x7f0000u) r |= 0x7fff0000u;
+  return r;
 }
 
 // The sequences of the call that take this launch, most keys first, with the
@@ -820,23 +836,32 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
               }
               if (lane == 0) mbar_arrive(bar(C::kRawEmpty + r));   // every lane has its bytes
               uint8_t *tile = gbase + C::kRingOff + s * C::kTileBytes + hf * C::kHalfBytes;
+              auto store_rows = [&](auto &&widen) {
 #pragma unroll
-              for (int i = 0; i < kPasses; ++i) {
-                const int row = i * kPass + sub;
-                uint4 a, c;
-                a.x = widen_pair(y[i].x, sc[i], 0x1100);
-                a.y = widen_pair(y[i].x, sc[i], 0x3322);
-                a.z = widen_pair(y[i].y, sc[i], 0x1100);
-                a.w = widen_pair(y[i].y, sc[i], 0x3322);
-                c.x = widen_pair(y[i].z, sc[i], 0x1100);
-                c.y = widen_pair(y[i].z, sc[i], 0x3322);
-                c.z = widen_pair(y[i].w, sc[i], 0x1100);
-                c.w = widen_pair(y[i].w, sc[i], 0x3322);
-                uint8_t *dst = tile + (w * kRows + row) * 128;
-                const int even = ((chunk ^ (row & 7)) * 16), odd = (((chunk + 1) ^ (row & 7)) * 16);
-                *reinterpret_cast<uint4 *>(dst + (hf ? odd : even)) = hf ? c : a;
-                *reinterpret_cast<uint4 *>(dst + (hf ? even : odd)) = hf ? a : c;
-              }
+                for (int i = 0; i < kPasses; ++i) {
+                  const int row = i * kPass + sub;
+                  uint4 a, c;
+                  a.x = widen(y[i].x, sc[i], 0x4140);
+                  a.y = widen(y[i].x, sc[i], 0x4342);
+                  a.z = widen(y[i].y, sc[i], 0x4140);
+                  a.w = widen(y[i].y, sc[i], 0x4342);
+                  c.x = widen(y[i].z, sc[i], 0x4140);
+                  c.y = widen(y[i].z, sc[i], 0x4342);
+                  c.z = widen(y[i].w, sc[i], 0x4140);
+                  c.w = widen(y[i].w, sc[i], 0x4342);
+                  uint8_t *dst = tile + (w * kRows + row) * 128;
+                  const int even = ((chunk ^ (row & 7)) * 16), odd = (((chunk + 1) ^ (row & 7)) * 16);
+                  *reinterpret_cast<uint4 *>(dst + (hf ? odd : even)) = hf ? c : a;
+                  *reinterpret_cast<uint4 *>(dst + (hf ? even : odd)) = hf ? a : c;
+                }
+              };
+              uint32_t nan = 0u;
+#pragma unroll
+              for (int i = 0; i < kPasses; ++i) nan |= holds_nan(y[i]);
+              if (__any_sync(0xffffffffu, nan))
+                store_rows(widen_pair_nan);
+              else
+                store_rows(widen_pair);
               fence_proxy_async();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(C::kSlotFull + s));

@@ -964,3 +964,38 @@ def test_weightless_rows_of_large_scale(pv, lq, D, n, below, gap):
         scale = below * math.log(2) / D
         out = _attend(pv, c, q, [lq], [n], True, scale=scale)
         _check(out, c, q, [lq], [n], True, scale)
+
+
+@pytest.mark.parametrize("lq,max_k", [(1, 700), (1, 5000), (5, 700), (40, 700), (300, 700),
+                                      (300, 1 << 20)])
+@pytest.mark.parametrize("D,sign", [(64, 0), (128, 128)])
+def test_nan_among_8bit_values(pv, lq, max_k, D, sign):
+    """An e4m3 NaN in a cache that something else filled: NaN in every kernel, whether rows are
+    widened ahead or in place."""
+    Hq, H, page, n = 6, 2, 16, 700
+    c = Cache([n, n], page, H, D, "e4m3", width=max(44, n // page))
+    _fill(pv, c, [n, n], 1)
+    q = _rows(2 * lq, Hq, D, 2, 0.0)
+
+    def attend():
+        out = pv.paged_attn_fwd(q.cuda(), c.k, c.v, _cu([lq, lq]), _i32([n, n]), c.dev_table, lq,
+                                max_k, causal=False, **c.exps())
+        assert pv.get_device_status() == 0
+        return out
+
+    want = attend()
+    _check(want, c, q, [lq, lq], [n, n], False, 1 / math.sqrt(D), heads=[0, 5])
+    spots = [(3, 0, 0), (130, 1, D - 1), (511, 0, 37), (512, 0, 38), (699, 1, 5)]
+    for pos, h, d in spots:                # of the first sequence's values
+        c.v.view(torch.uint8)[c.table[0, pos // page], pos % page, h, d] = 127 | sign
+    hit = torch.zeros(2 * lq, Hq, D, dtype=torch.bool, device="cuda")
+    for _, h, d in spots:
+        hit[:lq, 3 * h:3 * h + 3, d] = True
+    out = attend()
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], want[~hit])
+    _, rv = pv.kv_cache_read(c.k, c.v, _cu([n, n]), c.dev_table, 2 * n, **c.exps())
+    assert torch.isnan(rv).sum() == len(spots) and all(torch.isnan(rv[s]) for s in spots)
+    c.k.view(torch.uint8)[c.table[1, 20], 3, 1, 9] = 127 | sign      # a key of the second's
+    out = attend()
+    assert torch.isnan(out[lq:, 3:]).all() and torch.equal(out[lq:, :3], want[lq:, :3])
+    assert torch.equal(out[:lq][~hit[:lq]], want[:lq][~hit[:lq]])
