@@ -559,6 +559,13 @@ def _new(make, shape, dtype, dev: int, stream, raw: int) -> torch.Tensor:
         return make(shape, dtype=dtype, device=device)
 
 
+def _fits_32_bits(name: str, *counts: int):
+    # ctypes cuts integers to the parameter's width without a word
+    for n in counts:
+        if n >> 31:
+            raise PackedAttnError(name, 1 if n < 0 else 2)
+
+
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(*sizes: int) -> int:
     # arithmetic on the sizes alone; the call through ctypes costs a microsecond
@@ -610,6 +617,9 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torc
     cu_seqlens[B] are left as they are (fresh outputs are zero-filled).
     Returns (k_out, v_out)."""
     lib = _lib or load_library()
+    total = int(total)
+    if total >> 31:
+        _fits_32_bits("pa_kv_cache_read", total)
     B = _batch_of(cu_seqlens, "cu_seqlens")
     dev, fmt, P, page, H, D, ps, width, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
                                                              page_table, B)
@@ -619,7 +629,7 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens: torc
         _need_index(pos_offset, "pos_offset", B, dev)
         off = pos_offset.data_ptr()
     raw = _raw_stream(dev, stream)
-    shape = (int(total), H, D)
+    shape = (total, H, D)
     if k_out is None:
         k_out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
     else:
@@ -642,9 +652,9 @@ def paged_attn_workspace_bytes(batch: int, total_q: int, max_q: int, max_k: int,
                                Hkv: int, D: int, dtype: torch.dtype = torch.bfloat16) -> int:
     """Workspace of paged_attn_fwd over a cache of `dtype`, in bytes
     (pa_paged_attn_workspace_bytes)."""
-    n = load_library().pa_paged_attn_workspace_bytes(int(batch), int(total_q), int(max_q),
-                                                     int(max_k), int(Hq), int(Hkv), int(D),
-                                                     _CACHE_FORMATS.get(dtype, -1))
+    sizes = [int(x) for x in (batch, total_q, max_q, max_k, Hq, Hkv, D)]
+    _fits_32_bits("pa_paged_attn_workspace_bytes", *sizes)
+    n = load_library().pa_paged_attn_workspace_bytes(*sizes, _CACHE_FORMATS.get(dtype, -1))
     if n < 0:
         raise PackedAttnError("pa_paged_attn_workspace_bytes", 1)
     return int(n)
@@ -665,6 +675,9 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``workspace`` (uint8, paged_attn_workspace_bytes) is allocated per call
     unless given; calls that may overlap need one each."""
     lib = _lib or load_library()
+    max_q, max_k = int(max_q), int(max_k)
+    if (max_q | max_k) >> 31:
+        _fits_32_bits("pa_paged_attn_fwd", max_q, max_k)
     B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
     dev, fmt, P, page, H, D, ps, width, ke, ve = _need_cache(k_cache, v_cache, k_exp, v_exp,
                                                              page_table, B)
@@ -676,7 +689,6 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     _need_index(seq_lens, "seq_lens", B, dev)
     if scale is None:
         scale = D ** -0.5
-    max_q, max_k = int(max_q), int(max_k)
     raw = _raw_stream(dev, stream)
     if out is None:
         out = _new(torch.zeros, shape, _BF16, dev, stream, raw)

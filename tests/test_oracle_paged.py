@@ -180,3 +180,22 @@ def test_binding_refuses_host_tensors(lib):
         pv.kv_cache_write(x, x, None, c, cu, t)
     with pytest.raises(pv.PackedAttnError):
         pv.paged_attn_workspace_bytes(0, 1, 1, 1, 8, 8, 128)
+
+
+@pytest.mark.parametrize("n", [1 << 31, 1 << 32, (1 << 32) + 4, (1 << 40) + 64, -1, -(1 << 32) + 4])
+def test_binding_refuses_counts_that_32_bits_cut(lib, n):
+    import packed_varlen_gb300 as pv
+    c = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 1], dtype=torch.int32)
+    t = torch.zeros(1, 4, dtype=torch.int32)
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    for max_q, max_k in ((n, 4), (1, n), (n, n)):
+        with pytest.raises(pv.PackedAttnError):
+            pv.paged_attn_fwd(x, c, c, cu, cu[1:], t, max_q, max_k)
+    with pytest.raises(pv.PackedAttnError):
+        pv.kv_cache_read(c, c, cu, t, n)
+    for at in range(7):
+        sizes = [2, 10, 8, 64, 32, 8, 128]
+        sizes[at] = n
+        with pytest.raises(pv.PackedAttnError):
+            pv.paged_attn_workspace_bytes(*sizes)
