@@ -326,7 +326,12 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  * 16-byte aligned, for the partial results of keys that are split over
  * several CTAs, and for the 8-bit rows of long sequences as bf16 where these
  * take at most 1 GB (NULL where that is 0).  Its contents need not be kept or
- * cleared; two calls that may run at the same time need one each.
+ * cleared; two calls that may run at the same time need one each.  The bytes
+ * follow from the bounds: with 32 heads on 8 of 128 and max_k = 16,384 a
+ * sequence of one token takes 1 MB, one of 64 tokens up to 23 MB.  They are never
+ * more than 2 GB: a call whose batch could need more asks for that and takes its
+ * sequences in turns, each with launches of its own, and in fewer where
+ * workspace_bytes is larger.
  *
  * A sequence with bad boundaries (PA_DEVICE_ERR_CU_SEQLENS), a negative
  * seq_lens (PA_DEVICE_ERR_LENGTH), or a length beyond max_q, max_k or
@@ -347,7 +352,9 @@ pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_ca
 
 /* Workspace of a pa_paged_attn_fwd call with these arguments, in bytes (host
  * arithmetic alone); -1 where that call would be refused.  A workspace serves
- * every call that needs no more than it has. */
+ * every call that needs no more than it has.  (Over a bf16 cache that is every
+ * call of smaller bounds; over an 8-bit one such a call may widen rows that the larger
+ * bounds leave no room for, and need more.) */
 int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q, int32_t max_q,
                                       int32_t max_k, int32_t Hq, int32_t Hkv, int32_t D,
                                       int32_t format);

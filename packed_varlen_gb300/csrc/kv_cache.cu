@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const PagedAttnParams a
     PagedSeq s{0, 0, 0};
     int err;
     if (b < a.batch)
-      s = paged_seq(a.cu_q, a.seq_lens, b, a.total_q, a.max_q, a.max_k, a.capacity, err);
+      s = paged_seq(a, b, err);
     const bool in = !decode_takes(s.lq, a.G) && chunk_widens(s.lq, a.G);
     const uint32_t all = __ballot_sync(0xffffffffu, in);
     const int mine = in ? (s.lk - 1) / kChunkTile + (s.lk > 0) : 0;

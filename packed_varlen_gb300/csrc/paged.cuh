@@ -87,33 +87,6 @@ __device__ __forceinline__ uint32_t widen_scale(uint32_t byte) {
   return byte == kExpNan ? 0x7fffu : (byte + 120u) << 7;
 }
 
-// Sequence b of a paged attention call: query rows [q0, q0 + lq), lk keys.
-// Read like seq_bounds: a sequence that breaks the rules is returned without
-// queries and `err` says why.
-struct PagedSeq {
-  int32_t q0, lq, lk;
-};
-__device__ __forceinline__ PagedSeq paged_seq(const int32_t *__restrict__ cu_q,
-                                              const int32_t *__restrict__ seq_lens, int b,
-                                              int total_q, int max_q, int max_k,
-                                              int64_t capacity, int &err) {
-  const int q0 = __ldg(cu_q + b), q1 = __ldg(cu_q + b + 1), lk = __ldg(seq_lens + b);
-  PagedSeq s{0, 0, 0};
-  err = 0;
-  if (!(q0 >= 0 && q0 <= q1 && q1 <= total_q && (b > 0 || q0 == 0))) {
-    err = PA_DEVICE_ERR_CU_SEQLENS;
-  } else if (lk < 0) {
-    err = PA_DEVICE_ERR_LENGTH;
-  } else if (q1 - q0 > max_q || lk > max_k || lk > capacity) {
-    err = PA_DEVICE_ERR_MAX_LEN;
-  } else {
-    s.q0 = q0;
-    s.lq = q1 - q0;
-    s.lk = lk;
-  }
-  return s;
-}
-
 // ---------------------------------------------------------------- splits
 // Keys of one (sequence, K/V head) are split over CTAs, and the parts joined
 // by paged_join_kernel (paged_join.cu).  The rule looks at the sequence's own lengths and the
@@ -188,6 +161,8 @@ struct PagedAttnParams {
   const int32_t *cu_q, *seq_lens;
   int64_t q_stride;
   int64_t capacity;    // positions that the page table has room for
+  int batch0;          // sequences of the call before this launch's (cu_q, seq_lens and
+                       // c.table begin at its first)
   int batch, total_q, max_q, max_k, Hq, G;
   int g_inv;           // 2^16 / G + 1: r * g_inv >> 16 is r / G for rows r < 32, G <= 32
   int causal;
@@ -218,5 +193,29 @@ struct PagedAttnParams {
   int chunk_set;       // the sequences that a launch of the tiled kernel takes
 };
 enum { kSetAll = 0, kSetFlat = 1, kSetRest = 2 };
+
+// Sequence b of the launch: query rows [q0, q0 + lq), lk keys.  Read like
+// seq_bounds: a sequence that breaks the rules is returned without queries and
+// `err` says why.
+struct PagedSeq {
+  int32_t q0, lq, lk;
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedAttnParams &p, int b, int &err) {
+  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), lk = __ldg(p.seq_lens + b);
+  PagedSeq s{0, 0, 0};
+  err = 0;
+  if (!(q0 >= 0 && q0 <= q1 && q1 <= p.total_q && (b + p.batch0 > 0 || q0 == 0))) {
+    err = PA_DEVICE_ERR_CU_SEQLENS;
+  } else if (lk < 0) {
+    err = PA_DEVICE_ERR_LENGTH;
+  } else if (q1 - q0 > p.max_q || lk > p.max_k || lk > p.capacity) {
+    err = PA_DEVICE_ERR_MAX_LEN;
+  } else {
+    s.q0 = q0;
+    s.lq = q1 - q0;
+    s.lk = lk;
+  }
+  return s;
+}
 
 }  // namespace pa

@@ -20,7 +20,14 @@ constexpr int32_t kMostTokens = 1 << 30;
 // Bytes of widened rows up to which a call over an 8-bit cache widens ahead.
 constexpr int64_t kWidenMost = int64_t{1} << 30;
 
-// Where the partial results lie in the workspace.
+// The most workspace that a call asks for.  Where the bounds could need more for the
+// whole batch at once, the sequences go in several turns that use the same memory, as
+// few as fit (a sequence's bits are its own, so the turns change none); a caller
+// that gives more gets fewer.  GPU time of two turns against one: 100 sequences of
+// 60-64 tokens over 2-30k keys 1811 / 1772 us, 128 of 1-12 over 0-40k 1409 / 1376.
+constexpr int64_t kWorkspaceMost = int64_t{1} << 31;
+
+// Where the partial results of a turn lie in the workspace.
 struct WorkspacePlan {
   int64_t dec_slots;
   int dec_parts, dec_rows;
@@ -59,20 +66,33 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
     const int64_t n = max_q < least ? 0 : total_q / least;
     return n < batch ? n : batch;
   };
-  // Shares that sequences of the tiled kernel are cut into, and the rows that
-  // these may leave: a share has at least kChunkMinShare key tiles, and two
-  // parts of at most an item's rows; none where no sequence can have enough
-  // keys to be cut.
-  auto add_cuts = [&](int64_t seqs, int64_t items) {
+  // Shares of a sequence of i items a head, of at least kChunkMinShare key tiles each;
+  // none where no sequence can have enough keys to be cut.
+  auto shares_of = [&](int64_t i) -> int64_t {
+    if (i * Hkv > kChunkShares * kChunkMinShare) return kChunkShares;   // (nothing overflows)
+    const int64_t n = (i * Hkv * tiles_k + kChunkMinShare - 1) / kChunkMinShare;
+    return n < kChunkShares ? n : kChunkShares;
+  };
+  // Cuts and workspace rows of so many sequences of i_from to i_to items a head: the
+  // rows are bounded by the sequences and by the tokens, of which few make few items
+  // and these few shares.
+  auto add_cuts = [&](int64_t seqs, int64_t i_from, int64_t i_to) {
     if (tiles_k <= kChunkMinShare || seqs == 0) return;
-    // key tiles of a sequence's items, kept from overflowing
-    const int64_t all = items * Hkv > kChunkShares * kChunkMinShare ? kChunkShares * kChunkMinShare
-                                                                    : items * Hkv * tiles_k;
-    int64_t shares = (all + kChunkMinShare - 1) / kChunkMinShare;
-    if (shares > kChunkShares) shares = kChunkShares;
-    const int64_t by_items = seqs * item_tokens * G, by_tokens = static_cast<int64_t>(total_q) * G;
-    w.chunk_cuts += static_cast<int>(seqs * shares);
-    w.chunk_rows += 2 * shares * (by_items < by_tokens ? by_items : by_tokens);
+    auto slots_of = [&](int64_t i) { return chunk_slots(shares_of(i), i * Hkv); };
+    const int64_t all = static_cast<int64_t>(G) * total_q;
+    int64_t by_tokens = 0;
+    for (int64_t i = i_from; i <= i_to; ++i) {
+      // rows of sequences of the least tokens that have i items, as many as the call
+      // can have (one item: rows go with its tokens)
+      auto rows = [&](int64_t slots) {
+        return i == 1 ? slots * all : slots * all * item_tokens / ((i - 1) * item_tokens + 1) + 1;
+      };
+      if (rows(2 * kChunkShares) <= by_tokens) break;   // nor has any i after this one more
+      if (rows(slots_of(i)) > by_tokens) by_tokens = rows(slots_of(i));
+    }
+    const int64_t by_seqs = slots_of(i_to) * seqs * G * (max_q < item_tokens ? max_q : item_tokens);
+    w.chunk_cuts += static_cast<int>(seqs * shares_of(i_to));
+    w.chunk_rows += by_seqs < by_tokens ? by_seqs : by_tokens;
   };
   const int64_t items = (static_cast<int64_t>(max_q) + item_tokens - 1) / item_tokens;
   if (format == PA_CACHE_E4M3) {
@@ -81,12 +101,12 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
     w.flat_seqs = static_cast<int>(seqs);
   }
   if (w.flat_pages > 0) {
-    add_cuts(most_seqs(2 * item_tokens + 1), items);
+    add_cuts(most_seqs(2 * item_tokens + 1), 3, items);
     w.chunk_row0_rest = w.chunk_rows;
     w.chunk_cut0_rest = w.chunk_cuts;
-    add_cuts(most_seqs(few + 1), 2);
+    add_cuts(most_seqs(few + 1), 1, items < 2 ? items : 2);
   } else {
-    add_cuts(most_seqs(few + 1), items);
+    add_cuts(most_seqs(few + 1), 1, items);
   }
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -107,6 +127,55 @@ WorkspacePlan workspace_plan(int batch, int total_q, int max_q, int max_k, int H
   return w;
 }
 
+// The turns of a call: `batch` sequences each, the last one the rest.
+struct TurnPlan {
+  int batch, last;
+  WorkspacePlan w, w_last;
+};
+// As few as `most` bytes have room for (a sequence alone takes 1.1 GB at most).
+TurnPlan turn_plan(int batch, int total_q, int max_q, int max_k, int Hq, int Hkv, int D, int format,
+                   int64_t most) {
+  auto plan = [&](int n) { return workspace_plan(n, total_q, max_q, max_k, Hq, Hkv, D, format); };
+  TurnPlan t{batch, batch, plan(batch), {}};
+  for (int turns = 2; (t.w.bytes > most || t.w_last.bytes > most) && t.batch > 1; ++turns) {
+    t.batch = (batch + turns - 1) / turns;
+    t.last = (batch - 1) % t.batch + 1;
+    t.w = plan(t.batch);
+    t.w_last = plan(t.last);
+  }
+  return t;
+}
+
+// Launches of one turn, whose sequences p.cu_q, p.seq_lens and p.c.table begin at.
+cudaError_t launch_turn(PagedAttnParams &p, const WorkspacePlan &w, uint8_t *ws, bool quant, int sms,
+                        cudaStream_t s) {
+  p.dec_parts = w.dec_parts;
+  p.dec_rows = w.dec_rows;
+  p.dec_slots = w.dec_slots;
+  p.dec_o = reinterpret_cast<float *>(ws + w.dec_o);
+  p.dec_ml = reinterpret_cast<float2 *>(ws + w.dec_ml);
+  p.chunk_o = reinterpret_cast<float *>(ws + w.chunk_o);
+  p.chunk_ml = reinterpret_cast<float2 *>(ws + w.chunk_ml);
+  p.chunk_join = reinterpret_cast<int4 *>(ws + w.chunk_join);
+  p.chunk_n_cuts = reinterpret_cast<int32_t *>(ws + w.chunk_n_cuts);
+  p.chunk_rows = w.chunk_rows;
+  p.chunk_cuts = w.chunk_cuts;
+  p.chunk_row0_rest = w.chunk_row0_rest;
+  p.chunk_cut0_rest = w.chunk_cut0_rest;
+  p.flat_k = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_k);
+  p.flat_v = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_v);
+  p.flat_page = reinterpret_cast<int32_t *>(ws + w.flat_page);
+  p.flat_pages = static_cast<int>(w.flat_pages);
+  p.flat_seqs = w.flat_seqs;
+  // The long sequences first; the streaming kernel fills the SMs that they leave.
+  const bool chunk = !decode_takes(p.max_q, p.G), few = p.G <= kFewRows;
+  cudaError_t e = cudaSuccess;
+  if (chunk) e = launch_paged_chunk(p, quant, sms, s);
+  if (e == cudaSuccess && few) e = launch_paged_decode(p, quant, sms, chunk, s);
+  if (e == cudaSuccess && (p.dec_parts > 1 || p.chunk_cuts > 0)) e = launch_paged_join(p, sms, s);
+  return e;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -120,7 +189,8 @@ extern "C" int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q,
       max_q > kMostTokens || max_k > kMostTokens || (D != 64 && D != 128) ||
       (format != PA_CACHE_BF16 && format != PA_CACHE_E4M3))
     return -1;
-  return workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format).bytes;
+  const int64_t bytes = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format).bytes;
+  return bytes < kWorkspaceMost ? bytes : kWorkspaceMost;
 }
 
 extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
@@ -151,17 +221,18 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(cu_seqlens_q, 4) ||
       !aligned_to(seq_lens, 4) || (q_stride & 7) != 0 || !aligned_to(workspace, 16))
     return PA_ERR_MISALIGNED;
-  const int64_t need =
-      pa_paged_attn_workspace_bytes(batch, total_q, max_q, max_k, Hq, Hkv, D, format);
-  if (need < 0 || workspace_bytes < need || (need > 0 && !workspace)) return PA_ERR_INVALID_ARG;
+  // (every size that the plan needs has been checked by now)
+  const TurnPlan turns =
+      turn_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format,
+                workspace_bytes > kWorkspaceMost ? workspace_bytes : kWorkspaceMost);
+  const int64_t need = turns.batch < batch ? kWorkspaceMost : turns.w.bytes;
+  if (workspace_bytes < need || (need > 0 && !workspace)) return PA_ERR_INVALID_ARG;
   if (total_q == 0 || max_q == 0) return PA_OK;
   int sms;
   cudaError_t e = device_context(&p.status, &sms);
   if (e != cudaSuccess) return from_cuda(e);
   p.q = static_cast<const __nv_bfloat16 *>(q);
   p.out = static_cast<__nv_bfloat16 *>(out);
-  p.cu_q = cu_seqlens_q;
-  p.seq_lens = seq_lens;
   p.q_stride = q_stride;
   p.total_q = total_q;
   p.max_q = max_q;
@@ -169,39 +240,21 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.Hq = Hq;
   p.causal = causal;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.batch = batch;
   p.G = Hq / Hkv;
   p.g_inv = (1 << 16) / p.G + 1;
-  const WorkspacePlan w = workspace_plan(batch, total_q, max_q, max_k, Hq, Hkv, D, format);
-  p.dec_parts = w.dec_parts;
-  p.dec_rows = w.dec_rows;
-  p.dec_slots = w.dec_slots;
   p.dec_most = decode_most_parts(Hkv);
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  p.dec_o = reinterpret_cast<float *>(ws + w.dec_o);
-  p.dec_ml = reinterpret_cast<float2 *>(ws + w.dec_ml);
-  p.chunk_o = reinterpret_cast<float *>(ws + w.chunk_o);
-  p.chunk_ml = reinterpret_cast<float2 *>(ws + w.chunk_ml);
-  p.chunk_join = reinterpret_cast<int4 *>(ws + w.chunk_join);
-  p.chunk_n_cuts = reinterpret_cast<int32_t *>(ws + w.chunk_n_cuts);
-  p.chunk_rows = w.chunk_rows;
-  p.chunk_cuts = w.chunk_cuts;
-  p.chunk_row0 = p.chunk_cut0 = 0;
-  p.chunk_row0_rest = w.chunk_row0_rest;
-  p.chunk_cut0_rest = w.chunk_cut0_rest;
-  p.flat_k = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_k);
-  p.flat_v = reinterpret_cast<__nv_bfloat16 *>(ws + w.flat_v);
-  p.flat_page = reinterpret_cast<int32_t *>(ws + w.flat_page);
-  p.flat_pages = static_cast<int>(w.flat_pages);
-  p.flat_seqs = w.flat_seqs;
-  p.chunk_set = kSetAll;
   p.capacity = static_cast<int64_t>(table_pages) * page_size;
+  p.chunk_set = kSetAll;
+  p.chunk_row0 = p.chunk_cut0 = 0;
   auto s = reinterpret_cast<cudaStream_t>(stream);
-  const bool quant = format == PA_CACHE_E4M3;
-  // The long sequences first; the streaming kernel fills the SMs that they leave.
-  const bool chunk = !decode_takes(max_q, p.G), few = p.G <= kFewRows;
-  if (chunk) e = launch_paged_chunk(p, quant, sms, s);
-  if (e == cudaSuccess && few) e = launch_paged_decode(p, quant, sms, chunk, s);
-  if (e == cudaSuccess && (p.dec_parts > 1 || p.chunk_cuts > 0)) e = launch_paged_join(p, sms, s);
+  for (p.batch0 = 0; p.batch0 < batch && e == cudaSuccess; p.batch0 += turns.batch) {
+    const bool rest = batch - p.batch0 < turns.batch;
+    p.batch = rest ? turns.last : turns.batch;
+    p.cu_q = cu_seqlens_q + p.batch0;
+    p.seq_lens = seq_lens + p.batch0;
+    p.c.table = page_table + static_cast<int64_t>(p.batch0) * table_pages;
+    e = launch_turn(p, rest ? turns.w_last : turns.w, static_cast<uint8_t *>(workspace),
+                    format == PA_CACHE_E4M3, sms, s);
+  }
   return from_cuda(e);
 }

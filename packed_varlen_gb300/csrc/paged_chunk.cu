@@ -160,7 +160,7 @@ __device__ __forceinline__ uint32_t widen_pair_nan(uint32_t w, uint32_t scale, u
 // the CTA's threads first.
 struct WorkList {
   int32_t *order, *first, *cut0, *part0;   // in shared memory
-  int32_t *units, *rows;                   // temporaries: units, rows of one part (0: never cut)
+  int32_t *units, *rows;                   // temporaries: units, rows of all parts (0: never cut)
 };
 __device__ __forceinline__ bool in_launch(const PagedAttnParams &p, int lq) {
   return !decode_takes(lq, p.G) &&
@@ -170,7 +170,9 @@ __device__ __forceinline__ ChunkWork note_units(const PagedAttnParams &p, const 
                                                 const PagedSeq &s) {
   const ChunkWork w = chunk_work(s.lq, s.lk, p.causal, p.G, p.c.Hkv);
   x.units[at] = w.units;
-  x.rows[at] = w.share ? chunk_part_rows(s.lq, p.G) : 0;
+  x.rows[at] = w.share ? static_cast<int32_t>(chunk_slots(w.units, w.items_head * p.c.Hkv)) *
+                             chunk_part_rows(s.lq, p.G)
+                       : 0;
   return w;
 }
 // One warp.  Returns the sequences; lane b keeps sequence b and its work.
@@ -179,7 +181,7 @@ __device__ __forceinline__ int rank_few(const PagedAttnParams &p, const WorkList
   const int lane = threadIdx.x & 31;
   int err = 0;
   if (lane < p.batch)
-    s = paged_seq(p.cu_q, p.seq_lens, lane, p.total_q, p.max_q, p.max_k, p.capacity, err);
+    s = paged_seq(p, lane, err);
   if (err && report) record_error(p.status, err);
   const bool in = lane < p.batch && in_launch(p, s.lq);
   const uint32_t all = __ballot_sync(0xffffffffu, in);
@@ -204,7 +206,7 @@ __device__ __forceinline__ int rank_many(const PagedAttnParams &p, const WorkLis
   int32_t *seq = x.units, *keys = x.rows;
   for (int b = tid; b < p.batch; b += nt) {
     int err;
-    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
+    const PagedSeq s = paged_seq(p, b, err);
     if (err && report) record_error(p.status, err);
     if (in_launch(p, s.lq)) {
       const int at = atomicAdd(count, 1);   // any order: the ranks below are the list's
@@ -223,8 +225,7 @@ __device__ __forceinline__ int rank_many(const PagedAttnParams &p, const WorkLis
   __syncthreads();
   for (int y = tid; y < n; y += nt) {
     int err;
-    note_units(p, x, y, paged_seq(p.cu_q, p.seq_lens, x.order[y], p.total_q, p.max_q, p.max_k,
-                                  p.capacity, err));
+    note_units(p, x, y, paged_seq(p, x.order[y], err));
   }
   fence_proxy_async();   // the ring's copies come after every access to the temporaries there
   __syncthreads();
@@ -241,8 +242,8 @@ __device__ __forceinline__ int add_up(const PagedAttnParams &p, const WorkList &
 #pragma unroll 1
   for (int base = 0; base < n; base += 32) {
     const int y = base + lane;
-    const int u = y < n ? x.units[y] : 0, pr = y < n ? x.rows[y] : 0;
-    const int k = pr > 0 ? u : 0, r = 2 * u * pr;   // two parts at most to a share
+    const int u = y < n ? x.units[y] : 0, r = y < n ? x.rows[y] : 0;
+    const int k = r > 0 ? u : 0;
     int iu = u, ik = k, ir = r;
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
@@ -259,7 +260,7 @@ __device__ __forceinline__ int add_up(const PagedAttnParams &p, const WorkList &
       x.first[y] = units + iu - u;
       x.cut0[y] = cuts + ik - k;
       x.part0[y] = rows + ir - r;
-      if (pr > 0 && (cuts + ik > most_cuts || rows + ir > most_rows) && y < fit) fit = y;
+      if (r > 0 && (cuts + ik > most_cuts || rows + ir > most_rows) && y < fit) fit = y;
     }
     units += __shfl_sync(0xffffffffu, iu, 31);
     cuts += __shfl_sync(0xffffffffu, ik, 31);
@@ -297,6 +298,7 @@ struct Unit {
   int b, local;       // sequence, unit within it
   int at;             // place of the sequence in the list
   int part_rows;      // workspace rows of one part
+  bool by_piece;      // how its parts are placed (chunk_slots)
   int flat_page;      // first page of its widened rows (kSetFlat)
   int64_t part0;      // workspace row of the sequence's first part
   ChunkWork w;
@@ -324,13 +326,14 @@ __device__ __forceinline__ void open_unit(const PagedAttnParams &p, const WorkLi
     x.w.share = from(w.share);
   } else {
     int err;
-    x.s = paged_seq(p.cu_q, p.seq_lens, x.b, p.total_q, p.max_q, p.max_k, p.capacity, err);
+    x.s = paged_seq(p, x.b, err);
     x.w = chunk_work(x.s.lq, x.s.lk, p.causal, p.G, p.c.Hkv);
   }
   x.local = u - list.first[lo];
   x.at = lo;
   x.part0 = list.part0[lo];
   x.part_rows = chunk_part_rows(x.s.lq, p.G);
+  x.by_piece = x.w.items_head * p.c.Hkv < list.first[lo + 1] - list.first[lo];
   x.flat_page = p.chunk_set == kSetFlat ? p.flat_page[x.b] : 0;
   if (x.w.share == 0) {
     x.cur.start_whole(x.w, x.local, p.c.Hkv);
@@ -527,8 +530,10 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         piece.before = x.s.lk - x.s.lq;
         piece.b = x.b;
         piece.part_rows = x.part_rows;
-        piece.slot = pc.j0 == 0 && pc.j1 == pc.nk
-                         ? -1 : static_cast<int>(x.part0) + (2 * x.local + (pc.j0 == 0)) * x.part_rows;
+        const int part = x.by_piece ? x.local + pc.head * x.w.items_head + pc.item
+                                    : 2 * x.local + (pc.j0 == 0);
+        piece.slot = pc.j0 == 0 && pc.j1 == pc.nk ? -1
+                                                  : static_cast<int>(x.part0) + part * x.part_rows;
         const int ntq = piece.tokens > tile_tokens ? 2 : 1;
         if (!wait_all(bar(C::kQEmpty), (q_loads & 1u) ^ 1u)) {
           ok = false;
@@ -551,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
         if (pc.j0 == 0 && pc.j1 < pc.nk) {
           // this share begins the item, later ones go on with it: how many
           const int more = x.w.shares_after(x.local, pc.head, pc.item);
-          join_a = make_int4(1 + more, piece.slot, x.part_rows, 0);
+          join_a = make_int4(1 + more, piece.slot, x.part_rows, x.by_piece);
           join_b = make_int4(piece.tokens * p.G, x.s.q0 + tok0, pc.head, 0);
         }
         for (int j = pc.j0; j < pc.j1 && ok; ++j) {

@@ -150,6 +150,15 @@ __host__ __device__ inline int chunk_part_rows(int lq, int G) {
   return (lq < tokens ? lq : tokens) * G;
 }
 
+// Places for such parts that a sequence of so many shares and items (of all heads)
+// has.  A share leaves two parts at most, so share u's are 2 u (it goes on with an
+// item) and 2 u + 1 (it begins one); where items are fewer than shares, piece by
+// piece: part of item i in share u at u + i.  Either way the parts of an item are in
+// order, the first one at slot s and part n at s + 2 n - 1 or s + n.
+__host__ __device__ inline int64_t chunk_slots(int64_t shares, int64_t items) {
+  return shares + (items < shares ? items : shares);
+}
+
 // A run of key tiles [j0, j1) of one item.
 struct ChunkPiece {
   int head, item, j0, j1, nk;

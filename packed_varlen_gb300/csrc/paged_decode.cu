@@ -164,8 +164,7 @@ struct Walk {
     q0 = lq = lk = units = 0;
     if (x < p.batch) {
       int err;
-      const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, x, p.total_q, p.max_q, p.max_k,
-                                   p.capacity, err);
+      const PagedSeq s = paged_seq(p, x, err);
       if (err && report) record_error(p.status, err);
       q0 = s.q0;
       lq = s.lq;
@@ -273,8 +272,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     if ((lane < 4 || (lane & 24) == 8) && entry < p.c.table_pages)
       early = __ldg(p.c.table + static_cast<int64_t>(w.b) * p.c.table_pages + entry);
     int err;
-    const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, w.b, p.total_q, p.max_q, p.max_k,
-                                 p.capacity, err);
+    const PagedSeq s = paged_seq(p, w.b, err);
     if (err && w.hk == 0 && threadIdx.x == 0) record_error(p.status, err);
     if (s.lq == 0 || !decode_takes(s.lq, p.G)) {
       tc::griddep_wait();

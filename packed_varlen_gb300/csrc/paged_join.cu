@@ -55,7 +55,7 @@ __device__ __forceinline__ void join_row(const PagedAttnParams &p, int b, int ro
   __shared__ float sum_s[kJoinSums];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int err;
-  const PagedSeq s = paged_seq(p.cu_q, p.seq_lens, b, p.total_q, p.max_q, p.max_k, p.capacity, err);
+  const PagedSeq s = paged_seq(p, b, err);
   if (!decode_takes(s.lq, p.G) || row >= s.lq * p.Hq) return;
   const int parts = decode_split(s.lk, row_groups(s.lq, p.G), p.dec_most).parts;
   if (parts <= 1) return;
@@ -137,17 +137,18 @@ __device__ __forceinline__ void join_item_block(const PagedAttnParams &p, int cu
   const int r = block / (D / 32) * 32 + (threadIdx.x & 31), c0 = block % (D / 32) * kCols;
   const int4 a = p.chunk_join[2 * static_cast<int64_t>(cut)];
   const int4 c = p.chunk_join[2 * static_cast<int64_t>(cut) + 1];
-  // part 0 at row a.y of the workspace, part 1 one part further, then every second
+  // part 0 at row a.y of the workspace, part 1 one part further, then every second or
+  // the next (chunk_slots)
   const int parts = a.x, rows = c.x, part_rows = a.z;
+  auto first_row = [&](int n) -> int64_t {
+    return a.y + static_cast<int64_t>(a.w || n == 0 ? n : 2 * n - 1) * part_rows;
+  };
   if (parts < 2 || parts > kChunkShares + 1 || rows < 1 || part_rows < rows ||
       part_rows > 2 * kChunkTile || a.y < 0 ||
-      a.y + static_cast<int64_t>(2 * parts - 2) * part_rows > p.chunk_rows || c.y < 0 ||
+      first_row(parts - 1) + part_rows > p.chunk_rows || c.y < 0 ||
       rows % p.G != 0 ||
       c.y + static_cast<int64_t>(rows) / p.G > p.total_q || c.z < 0 || c.z >= p.c.Hkv || r >= rows)
     return;
-  auto first_row = [&](int n) -> int64_t {
-    return a.y + static_cast<int64_t>(n == 0 ? 0 : 2 * n - 1) * part_rows;
-  };
   float top = -INFINITY;
   for (int n = 0; n < parts; ++n) top = fmaxf(top, p.chunk_ml[first_row(n) + r].x);
   const float ref = top == -INFINITY ? 0.f : top;

@@ -999,3 +999,61 @@ def test_nan_among_8bit_values(pv, lq, max_k, D, sign):
     out = attend()
     assert torch.isnan(out[lq:, 3:]).all() and torch.equal(out[lq:, :3], want[lq:, :3])
     assert torch.equal(out[:lq][~hit[:lq]], want[:lq][~hit[:lq]])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("Hq,H,D,B", [(64, 8, 128, 330), (32, 32, 64, 701)])
+def test_batches_taken_in_turns(pv, Hq, H, D, B, fmt):
+    """Bounds that would need more than 2 GB for the whole batch at once: the sequences go in
+    turns, to the bits that one turn gives; bad ones in any turn are skipped alone."""
+    page = 16
+    rng = np.random.default_rng(B)
+    lengths, seq_lens = np.ones(B, dtype=int), rng.integers(1, 80, B)
+    for b, n, m in [(0, 1, 900), (3, 40, 2500), (100, 3, 2600), (101, 0, 50), (150, 130, 2100),
+                    (180, 1, 2000), (181, 9, 9), (200, 300, 2300), (B - 2, 70, 2200), (B - 1, 2, 1500)]:
+        lengths[b], seq_lens[b] = n, m
+    lengths, seq_lens = lengths.tolist(), np.maximum(seq_lens, lengths).tolist()
+    c = Cache(seq_lens, page, H, D, fmt)
+    _fill(pv, c, seq_lens, 1)
+    T = sum(lengths)
+    q = _rows(T, Hq, D, 2, 0.0).cuda()
+    cu, top = _cu(lengths), 1 << 20
+    dtype = c.k.dtype
+    need = pv.paged_attn_workspace_bytes(B, T + 1, 300, top, Hq, H, D, dtype)
+    assert need <= 1 << 31
+    ws = torch.full(((12 << 30),), 171, dtype=torch.uint8, device="cuda")
+
+    def attend(cu, lens, size):
+        out = torch.full((T + 1, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        qd = torch.cat([q, q[:1]])
+        pv.paged_attn_fwd(qd, c.k, c.v, cu, lens, c.dev_table, 300, top, out=out,
+                          workspace=ws[:size], **c.exps())
+        return out
+
+    got = attend(cu, _i32(seq_lens), need)
+    assert pv.get_device_status() == 0
+    assert (ws[need:need + (64 << 20)] == 171).all()
+    one = attend(cu, _i32(seq_lens), ws.numel())
+    assert pv.get_device_status() == 0
+    assert (ws[need:] != 171).any()                       # all at once took more
+    assert torch.equal(got.view(torch.int16), one.view(torch.int16))
+    _check(got, c, q.cpu(), lengths, seq_lens, True, 1 / math.sqrt(D), heads=[0, Hq - 1])
+    # a bad length in every part of the batch
+    where = [1, 99, B // 2, B - 3]
+    lens = list(seq_lens)
+    for b in where:
+        lens[b] = -1
+    bad = attend(cu, _i32(lens), need)
+    assert pv.get_device_status() == 4
+    rows = torch.ones(T + 1, dtype=torch.bool, device="cuda")
+    start = np.concatenate([[0], np.cumsum(lengths)])
+    for b in where:
+        rows[start[b]:start[b + 1]] = False
+    assert torch.equal(bad[rows], got[rows]) and (bad[~rows] == 5.0).all()
+    # boundaries that do not begin at 0: the first sequence's alone are bad
+    late = cu.clone()
+    late[0] = 1
+    lens = list(seq_lens)
+    out = attend(late, _i32(lens), need)
+    assert pv.get_device_status() == 1
+    assert torch.equal(out[lengths[0]:], got[lengths[0]:])

@@ -199,3 +199,68 @@ def test_binding_refuses_counts_that_32_bits_cut(lib, n):
         sizes[at] = n
         with pytest.raises(pv.PackedAttnError):
             pv.paged_attn_workspace_bytes(*sizes)
+
+
+def _rows_of_parts(lq, lk, causal, G, Hkv):
+    """(shares, items of all heads, rows of a part) of a sequence whose keys are split, else None:
+    items of 2 * (128 / G) queries, a lone sequence's shares of at least ten tiles of 128 keys."""
+    tokens = 2 * (128 // G)
+    items = -(-lq // tokens)
+    keys = [max(min(lk, lk - lq + (i + 1) * tokens) if causal else lk, 128) for i in range(items)]
+    if items * Hkv >= 6 * 152 or keys[-1] <= 15 * 128:
+        return None
+    share = max(-(-sum(keys) * Hkv // 152), 1280)
+    return -(-sum(keys) * Hkv // share), items * Hkv, min(lq, tokens) * G
+
+
+def test_workspace_holds_the_parts_of_any_batch(lib):
+    """Random batches: the rows that the kernels leave fit what the bounds ask for."""
+    rng = np.random.default_rng(3)
+    tight = 0.0
+    for _ in range(3000):
+        B, G = int(rng.integers(1, 12)), int(rng.choice([1, 2, 4, 7, 8, 40, 128]))
+        H, D = int(rng.choice([1, 2, 8, 20])), int(rng.choice([64, 128]))
+        top = int(rng.choice([3, 40, 200, 900]))
+        lq = rng.integers(0, top + 1, B)
+        lk = lq + rng.integers(0, int(rng.choice([100, 3000, 40000])), B)
+        causal = bool(rng.integers(2))
+        few, rows = 32 // G, 0
+        for n, m in zip(lq.tolist(), lk.tolist()):
+            split = _rows_of_parts(n, m, causal, G, H) if n > few else None
+            if split:
+                shares, items, part = split
+                rows += (shares + min(shares, items)) * part
+        bytes_ = lib.pa_paged_attn_workspace_bytes(B, int(lq.sum()), int(lq.max()), int(lk.max()),
+                                                   G * H, H, D, 0)
+        assert rows * (D * 4 + 8) <= bytes_
+        tight = max(tight, rows * (D * 4 + 8) / max(bytes_, 1))
+    assert tight > 0.8                     # some batch needs nearly all of it
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_workspace_is_bounded(lib, fmt):
+    """A call asks for no more than 2 GB whatever its bounds, and for little where little can
+    be split: two chunks beside single tokens, single tokens over long caches."""
+    f = lib.pa_paged_attn_workspace_bytes
+    rng = np.random.default_rng(4)
+    for _ in range(2000):
+        G, B = int(rng.choice([1, 4, 8, 128])), int(2 ** rng.uniform(0, 10))
+        H = int(2 ** rng.uniform(0, 12 if G < 128 else 5))
+        total, max_q, max_k = (int(2 ** rng.uniform(0, 30)) for _ in range(3))
+        assert 0 <= f(B, total, max_q, max_k, G * H, H, 128, fmt) <= 1 << 31
+    for args, most in [((128, 8192, 2048, 32768, 32, 8), 2048), ((256, 8192, 2048, 131072, 32, 8), 2048),
+                       ((256, 8447, 8192, 131072, 64, 8), 2048), ((24, 860, 500, 4000, 32, 8), 380),
+                       ((64, 64, 1, 131072, 32, 8), 250), ((1, 2048, 2048, 16048, 32, 8), 140),
+                       ((1, 1, 1, 131072, 32, 8), 5)]:
+        assert f(*args, 128, fmt) <= most << 20
+
+
+def test_workspace_of_smaller_bounds(lib):
+    """One workspace, made for the largest bounds, serves every call over a bf16 cache."""
+    f = lib.pa_paged_attn_workspace_bytes
+    rng = np.random.default_rng(5)
+    for _ in range(5000):
+        G, H = int(rng.choice([1, 4, 7, 8, 128])), int(rng.choice([1, 2, 8, 20]))
+        big = [int(2 ** rng.uniform(0, x)) for x in (10, 17, 13, 20)]
+        small = [int(rng.integers(1, x + 1)) if rng.integers(2) else x for x in big]
+        assert f(*small, G * H, H, 128, 0) <= f(*big, G * H, H, 128, 0)
