@@ -39,11 +39,10 @@
 // 8-bit rows become f16, which holds e4m3 exactly, one conversion for two
 // values; the rows' scales go to the scores (K) and into the weights (V).  The
 // weight that is rounded to f16 is then w 2^e of a V row held in units of 2^e,
-// so a row of q's running reference is the largest s' + e in place of the
-// largest s': among the keys that it sees, the one whose values move the output
-// most has a weight near f16's top, whatever the exponents of rows that are
-// hidden or weigh nothing.  Full precision is kept down to 2^-28 of that, and a
-// step of 2^-38 below.
+// so it is taken against the largest s' + e in place of the largest s': among the
+// keys that a row of q sees, the one whose values move the output most has a weight
+// near f16's top, whatever the exponents of rows that are hidden or weigh nothing.
+// Full precision is kept down to 2^-28 of that, and a step of 2^-38 below.
 #include <cuda.h>
 #include <math.h>
 
@@ -68,8 +67,14 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 // less kWeightTop at its last rise, so at most 2^(kWeightTop + kWeightRoom), within f16.
 // With e + kExpMid in [-54, 53] the sum of the 2^(s' - m) stays within 2^-39 and
 // 2^69 for each key.  A rise costs the output's rescaling: room for one binade.
+// Beyond kLargeScore a score's own steps would swallow the exponents: from the first
+// such rise on, a part's weights are 2^(s' - m - c) 2^(e + kExpMid), with m the
+// largest s' and c the largest s' - m + e + kExpMid less kWeightTop.  (That from the
+// start costs 14% of four tokens each of 96 sequences, and 1 us of 9.6 where the
+// contexts are few and short.)
 constexpr int kExpMid = 46;
 constexpr float kWeightTop = 14.f, kWeightRoom = 1.f;
+constexpr float kLargeScore = 1 << 20;   // log2 units; steps of 2^-4
 
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (~2 s)
 constexpr long long kDrainLimit = 400000000LL;
@@ -432,6 +437,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
     const int all_see = p.causal ? lk - lq + 1 + token_of(r0) : lk;   // keys before it need no mask
 
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
+    [[maybe_unused]] float c[NT][2];   // with large scores over an 8-bit cache
+    bool large = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -442,24 +449,25 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // A sequence of at most eight rows takes one group of columns, whatever the call's
-    // others need: 96 8-bit sequences of one token in a call that allows for 32 rows 324
-    // / 300 us.  (Not the second half of more rows: its warps would run ahead of those
-    // that read the same keys, 246 / 275 us with five tokens of four heads each.)
-    auto walk = [&](auto columns) {
+    // Tiles from n on, until the first large score (not kLarge).
+    int n = 0;
+    auto walk = [&](auto columns, auto with_large) {
       constexpr int NC = decltype(columns)::value;
-      for (int n = 0; n < n_tiles; ++n) {
+      constexpr bool kLarge = decltype(with_large)::value;
+      const int n_here = kLarge ? n : -1;   // this tile's copies are waited for already
+      for (; n < n_tiles; ++n) {
         const int key = k0 + n * kTile;
-        // every lane has read the stage that is filled next (the tile before this one)
-        __syncwarp();
-        issue();
+        if (n != n_here) {
+          // every lane has read the stage that is filled next (the tile before this one)
+          __syncwarp();
+          issue();
+        }
         const uint32_t stage = used % C::kStages;
         ok = tc::bounded_wait(bars + 8 * stage, (used / C::kStages) & 1u, gave_up, p.status, kWaitLimit);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        ++used;
         const uint8_t *st = ring + stage * C::kStageBytes;
         [[maybe_unused]] const uint32_t bad_runs = bad >> (stage * C::kHalves);
         // byte address of 16-byte vector `vec` of row `row` of a run
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         // S^T = K Q^T, in two chains
         float sc[C::kHalves][NC][4];
         float kf[C::kHalves][2], vf[C::kHalves][2];
-        [[maybe_unused]] float ve[C::kHalves][2];   // log2 of vf: keys key_of(g) and 8 later
+        [[maybe_unused]] float ve[C::kHalves][2] = {};   // log2 of vf: keys key_of(g) and 8 later
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
           float s2[NC][4];
@@ -526,9 +534,26 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         }
 
         // online softmax over the tile's keys, all lanes of a column in step
-        constexpr float kRoomAbove = kQuant ? kWeightTop + kWeightRoom : kRescaleThreshold;
+        bool above = false, up[NC][2];
         float mx[NC][2];
-        bool above = false;
+        // highest score of this lane's keys in a column; `graded`: with V's exponents
+        auto highest = [&](auto graded, int nt, int e, float ref) {
+          auto level = [&](int h, int x) {
+            const float y = kLarge ? sc[h][nt][e + 2 * x] - ref : sc[h][nt][e + 2 * x];
+            if constexpr (decltype(graded)::value) return y + ve[h][x];
+            return y;
+          };
+          float y = fmaxf(level(0, 0), level(0, 1));
+#pragma unroll
+          for (int h = 1; h < C::kHalves; ++h) y = tc::fmax3(y, level(h, 0), level(h, 1));
+          return y;
+        };
+        constexpr std::bool_constant<kQuant> by_level;
+        auto of_column = [](float x) {   // largest of the eight lanes of a column
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        };
 #pragma unroll
         for (int nt = 0; nt < NC; ++nt) {
 #pragma unroll
@@ -546,34 +571,52 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            // over an 8-bit cache: of score and V's scale together
-            auto level = [&](int h, int x) {
-              return kQuant ? sc[h][nt][e + 2 * x] + ve[h][x] : sc[h][nt][e + 2 * x];
-            };
-            mx[nt][e] = fmaxf(level(0, 0), level(0, 1));
-#pragma unroll
-            for (int h = 1; h < C::kHalves; ++h)
-              mx[nt][e] = tc::fmax3(mx[nt][e], level(h, 0), level(h, 1));
-            above |= mx[nt][e] > m[nt][e] + kRoomAbove;   // from -inf: any finite score
+            mx[nt][e] = highest(by_level, nt, e, m[nt][e] == -INFINITY ? 0.f : m[nt][e]);
+            // from -inf: any finite score
+            up[nt][e] = mx[nt][e] > (kLarge ? c[nt][e] : m[nt][e]) +
+                                        (kQuant ? kWeightTop + kWeightRoom : kRescaleThreshold);
+            above |= up[nt][e];
           }
         }
         // The columns' maxima are joined only where one has risen (a vote in place of
         // six shuffles: 100 cycles of a tile's 1150).
         if (__any_sync(0xffffffffu, above)) {
+          if constexpr (kQuant && !kLarge) {
+            bool far = false;
+#pragma unroll
+            for (int nt = 0; nt < NC; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                mx[nt][e] = of_column(mx[nt][e]);
+                far |= fabsf(mx[nt][e]) > kLargeScore && mx[nt][e] > -INFINITY;
+              }
+            if (__any_sync(0xffffffffu, far)) {
+              large = true;
+              break;
+            }
+          }
 #pragma unroll
           for (int nt = 0; nt < NC; ++nt) {
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = mx[nt][e];
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
               alpha[e] = 1.f;
-              if (x > m[nt][e] + kRoomAbove) {
-                if (kQuant) x -= kWeightTop;
-                alpha[e] = tc::ex2(m[nt][e] - x);
-                m[nt][e] = x;
+              if constexpr (kLarge) {
+                const float top =
+                    fmaxf(of_column(highest(std::false_type{}, nt, e, 0.f)), m[nt][e]);
+                const float x = of_column(highest(by_level, nt, e, top == -INFINITY ? 0.f : top));
+                if (__ballot_sync(0xffffffffu, up[nt][e]) & (0x11111111u << t)) {
+                  alpha[e] = tc::ex2((m[nt][e] - top) + (c[nt][e] - (x - kWeightTop)));
+                  m[nt][e] = top;
+                  c[nt][e] = x - kWeightTop;
+                }
+              } else {
+                float x = kQuant ? mx[nt][e] : of_column(mx[nt][e]);
+                if (x > m[nt][e] + (kQuant ? kWeightTop + kWeightRoom : kRescaleThreshold)) {
+                  if (kQuant) x -= kWeightTop;
+                  alpha[e] = tc::ex2(m[nt][e] - x);
+                  m[nt][e] = x;
+                }
               }
               l[nt][e] *= alpha[e];
             }
@@ -588,10 +631,15 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         for (int nt = 0; nt < NC; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+            const bool none = m[nt][e] == -INFINITY;
+            const float ref = none ? 0.f : m[nt][e];
+            auto weight = [&](float x) {
+              if constexpr (kLarge) return tc::ex2(x - ref - (none ? 0.f : c[nt][e]));
+              return tc::ex2(x - ref);
+            };
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
-              const float p0 = tc::ex2(sc[h][nt][e] - ref), p1 = tc::ex2(sc[h][nt][e + 2] - ref);
+              const float p0 = weight(sc[h][nt][e]), p1 = weight(sc[h][nt][e + 2]);
               l[nt][e] += p0 + p1;
               sc[h][nt][e] = kQuant ? p0 * vf[h][0] : p0;
               sc[h][nt][e + 2] = kQuant ? p1 * vf[h][1] : p1;
@@ -656,16 +704,32 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
             }
           }
         }
+        ++used;
+      }
+    };
+    // A sequence of at most eight rows takes one group of columns, whatever the call's
+    // others need: 96 8-bit sequences of one token in a call that allows for 32 rows 324
+    // / 300 us.  (Not the second half of more rows: its warps would run ahead of those
+    // that read the same keys, 246 / 275 us with five tokens of four heads each.)
+    auto walk_all = [&](auto columns) {
+      walk(columns, std::false_type{});
+      if constexpr (kQuant) {
+        if (large) {   // from here on with m and c
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) c[nt][e] = m[nt][e] == -INFINITY ? -INFINITY : 0.f;
+          walk(columns, std::true_type{});
+        }
       }
     };
     if (NT == 1 || lq * p.G <= 8)
-      walk(std::integral_constant<int, 1>{});
+      walk_all(std::integral_constant<int, 1>{});
     else
-      walk(std::integral_constant<int, NT>{});
+      walk_all(std::integral_constant<int, NT>{});
 
     // ---- this lane's columns: D / 8 dims each of rows 2 t and 2 t + 1, in runs
     // of 2 KR consecutive ones
-    const float grade = kQuant ? pow2f(-kExpMid) : 1.f;
     constexpr int KR = !kQuant && D == 128 ? 4 : D / 16;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -677,6 +741,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
         if (r >= R) continue;
         const int i = token_of(r0 + r), h = hk * p.G + r0 + r - i * p.G;
         if (parts <= 1) {
+          constexpr float grade = kQuant ? 1.f / (1ll << kExpMid) : 1.f;
           const float inv = m[nt][e] == -INFINITY ? 0.f : 1.f / l[nt][e];
           __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(w.s_q0 + i) * p.Hq + h) * D;
 #pragma unroll
@@ -692,6 +757,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
           const int64_t slot =
               w.b * p.dec_slots + static_cast<int64_t>(w.part * lq + i) * p.Hq + h;
           float *dst = kLocal ? part_o + (w.part * 8 * NT + r) * D : p.dec_o + slot * D;
+          // both against m alone, as the join takes them
+          const float from_c = kQuant && large && m[nt][e] != -INFINITY ? tc::ex2(c[nt][e]) : 1.f;
+          const float grade = kQuant ? from_c * pow2f(-kExpMid) : 1.f;
 #pragma unroll
           for (int mt = 0; mt < D / 16; mt += 2) {
             const int d = g * 2 * KR + 16 * KR * (mt / KR) + 2 * (mt % KR);
@@ -700,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
                             o[nt][mt + 1][e + 2] * grade);
           }
           float2 *ml = kLocal ? part_ml + w.part * 8 * NT + r : p.dec_ml + slot;
-          if (g == 0) *ml = make_float2(m[nt][e], l[nt][e]);
+          if (g == 0) *ml = make_float2(m[nt][e], l[nt][e] * from_c);
         }
       }
     }

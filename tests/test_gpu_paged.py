@@ -1057,3 +1057,35 @@ def test_batches_taken_in_turns(pv, Hq, H, D, B, fmt):
     out = attend(late, _i32(lens), need)
     assert pv.get_device_status() == 1
     assert torch.equal(out[lengths[0]:], got[lengths[0]:])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size", [10, 16, 20, 24, 28])
+@pytest.mark.parametrize("lq,n,D", [(1, 700, 128), (1, 5000, 64), (4, 3000, 128), (40, 3000, 128),
+                                    (150, 400, 64)])
+def test_scores_of_any_size(pv, lq, n, D, size, fmt):
+    """Keys of equal scores of some 2^size among keys far below them: the mean of their values,
+    wherever they lie and however unlike their scale."""
+    H, Hq = 1, 2
+    g = torch.Generator().manual_seed(size)
+    u = (torch.randint(0, 2, (D,), generator=g) * 2 - 1).float()
+    c = Cache([n], 16, H, D, fmt)
+    # u times signs that repeat in three keys of four sum to less than u u
+    k = u * (1 - 2 * (torch.arange(D) % 4 == 3).float()) * 2.0 ** 6
+    k = k.expand(n, H, D).clone()
+    like = torch.arange(n) % 37 == 5
+    like[[n // 2, n // 2 + 1]] = True
+    like[n - lq:] = False
+    k[like] = u * 2.0 ** 6
+    v = _rows(n, H, D, 4, 0.3).float() * torch.exp2(-3.0 * (torch.arange(n) // 37 % 9))[:, None, None]
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n]), c.dev_table, **c.exps())
+    q = (u * 2.0 ** (size - 6)).expand(lq, Hq, D).to(torch.bfloat16).contiguous()
+    scale = 1.37 / D                       # scores of 1.37 2^size and of half of that
+    out = oracle.to_f64(_attend(pv, c, q, [lq], [n], False, scale=scale))[:lq]
+    _, vc = c.values()
+    rows = oracle.cached_rows(vc, c.table[0], n)[like.numpy()][:, 0]
+    want, weight = rows.mean(axis=0), np.abs(rows).mean(axis=0)
+    # equal weights, exact up to 2^-21 where they are rounded (f16, bf16: powers of two, or
+    # half a step of bf16), fp32 sums, one rounding to bf16
+    assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -14) * weight + 2.0 ** -8 * np.abs(want)).all()
