@@ -960,7 +960,9 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kPairs; ++c) mx4[c & 3] = fmax3(mx4[c & 3], sc[c].x, sc[c].y);
           }
-          const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * mul;
+          // (Rounding steps are written out wherever the compiler could choose: the kernels
+          // over bf16 and over 8-bit rows give the same bits.)
+          const float mx = __fmul_rn(fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]), mul);
           float alpha = 1.f;
           bool rescale = false;
           if (mx > m + kRescaleThreshold) {   // from -inf: any finite score
@@ -992,7 +994,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             }
           }
           const float2 s4 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
-          l = l * alpha + (s4.x + s4.y);
+          l = __fmaf_rn(l, alpha, __fadd_rn(s4.x, s4.y));
           // S_j complete implies the PV issued before it is complete: O is
           // current and can be rescaled in place
           if (__any_sync(0xffffffffu, rescale)) {
@@ -1045,7 +1047,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
           const float ref = m == -INFINITY ? 0.f : m;
           f0 = ex2(a.x - ref);
           f1 = ex2(c.x - ref);
-          l = f0 * a.y + f1 * c.y;
+          l = __fmaf_rn(f0, a.y, __fmul_rn(f1, c.y));
         }
         const uint32_t src0 = lane_base + (shared ? C::kColO : colO), src1 = lane_base + C::kColO + D;
         const int c_first = shared ? t * (D / 64) : 0, c_end = shared ? c_first + D / 64 : D / 32;
@@ -1068,7 +1070,8 @@ __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              r[e] = __float_as_uint(f0 * __uint_as_float(r[e]) + f1 * __uint_as_float(r1[e]));
+              r[e] = __float_as_uint(
+                  __fmaf_rn(f0, __uint_as_float(r[e]), __fmul_rn(f1, __uint_as_float(r1[e]))));
           } else {
             tmem_wait_ld();
             if (shared) {   // f0 is 1, or 0 for a row that sees no key (its O is 0, or NaN)

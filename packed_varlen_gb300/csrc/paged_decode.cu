@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<D, kQuant, NT, kLocal>::kCtaWarps * 32,
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (kQuant) sc[h][nt][e] *= kf[h][e >> 1];
-              sc[h][nt][e] *= factor[nt][e & 1];
+              sc[h][nt][e] = __fmul_rn(sc[h][nt][e], factor[nt][e & 1]);   // (no FFMA with a maximum)
             }
             if (key + kTile > all_see) {
 #pragma unroll
