@@ -316,9 +316,9 @@ pa_status pa_kv_cache_read(const void *k_cache, const void *v_cache, const uint8
  * [batch], batch in [1, PA_MAX_BATCH]; total_q >= cu_seqlens_q[batch]
  * (total_q = 0 or max_q = 0 does nothing; with total_q = 0 q and out may be
  * NULL); max_q / max_k bound every L_b and seq_lens[b]; total_q, max_q and
- * max_k at most 2^30; Hq a multiple of Hkv, Hq / Hkv <= 128; scale finite, and
- * so small that scale * <q, k> stays below 2^29 (beyond, where fp32 scores lie 32 and
- * more apart, a result may be NaN).
+ * max_k at most 2^30; Hq a multiple of Hkv, Hq / Hkv <= 128; scale and
+ * scale * log2(e) finite, and scale * <q, k> below 2^29 in magnitude (beyond, where
+ * fp32 scores lie 32 and more apart, a result may be NaN).
  * Rows of a page past a sequence's last position never reach a result,
  * whatever their bits.  A key that causal order hides from a query has weight
  * zero there; a NaN or infinity in its V row can still reach that query as

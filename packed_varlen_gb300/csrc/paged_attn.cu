@@ -206,7 +206,8 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   if (!cu_seqlens_q || !seq_lens) return PA_ERR_INVALID_ARG;
   if (batch < 1 || total_q < 0 || max_q < 0 || max_k < 0 || Hq < 1) return PA_ERR_INVALID_ARG;
   if (total_q > 0 && (!q || !out)) return PA_ERR_INVALID_ARG;
-  if (!isfinite(scale)) return PA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;   // of weights as powers of two
+  if (!isfinite(scale_log2)) return PA_ERR_INVALID_ARG;
   PagedAttnParams p;
   const PagedCacheArgs a{const_cast<void *>(k_cache), const_cast<void *>(v_cache),
                          const_cast<uint8_t *>(k_exp), const_cast<uint8_t *>(v_exp),
@@ -239,7 +240,7 @@ extern "C" pa_status pa_paged_attn_fwd(const void *q, const void *k_cache, const
   p.max_k = max_k;
   p.Hq = Hq;
   p.causal = causal;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.G = Hq / Hkv;
   p.g_inv = (1 << 16) / p.G + 1;
   p.dec_most = decode_most_parts(Hkv);

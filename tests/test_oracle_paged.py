@@ -264,3 +264,10 @@ def test_workspace_of_smaller_bounds(lib):
         big = [int(2 ** rng.uniform(0, x)) for x in (10, 17, 13, 20)]
         small = [int(rng.integers(1, x + 1)) if rng.integers(2) else x for x in big]
         assert f(*small, G * H, H, 128, 0) <= f(*big, G * H, H, 128, 0)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38])
+def test_scale_that_overflows_is_refused(lib, scale):
+    """A finite scale whose product with log2(e), which the kernels use, is not."""
+    a = dict(ATTN, scale=scale)
+    assert lib.pa_paged_attn_fwd(*[a[n] for n in ATTN], None) == 1
