@@ -1089,3 +1089,53 @@ def test_scores_of_any_size(pv, lq, n, D, size, fmt):
     # equal weights, exact up to 2^-21 where they are rounded (f16, bf16: powers of two, or
     # half a step of bf16), fp32 sums, one rounding to bf16
     assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -14) * weight + 2.0 ** -8 * np.abs(want)).all()
+
+
+def test_turns_with_rows_widened_ahead(pv):
+    """Turns over an 8-bit cache whose long sequences' rows are widened ahead in each of them."""
+    Hq, H, D, page, B, T = 64, 8, 128, 16, 60, 24000
+    rng = np.random.default_rng(8)
+    lengths = [int(x) for x in rng.choice([1, 2, 40, 70, 130, 300], B)]
+    seq_lens = [n + int(rng.integers(0, 2300)) for n in lengths]
+    c = Cache(seq_lens, page, H, D, "e4m3")
+    _fill(pv, c, seq_lens, 1)
+    n = sum(lengths)
+    q = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    q[:n] = _rows(n, Hq, D, 2, 0.0).cuda()
+    args = (q, c.k, c.v, _cu(lengths), _i32(seq_lens), c.dev_table, 300, 2700)
+    need = pv.paged_attn_workspace_bytes(B, T, 300, 2700, Hq, H, D, torch.float8_e4m3fn)
+    assert need == 1 << 31 and n < T
+    ws = torch.full((need + (3 << 30),), 171, dtype=torch.uint8, device="cuda")
+    got = pv.paged_attn_fwd(*args, workspace=ws[:need], **c.exps())
+    assert (ws[need:] == 171).all()
+    one = pv.paged_attn_fwd(*args, workspace=ws, **c.exps())
+    assert pv.get_device_status() == 0
+    assert torch.equal(got.view(torch.int16), one.view(torch.int16))
+    _check(got[:n], c, q[:n].cpu(), lengths, seq_lens, True, 1 / math.sqrt(D), heads=[0, 63])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()                     # and captured
+    out = torch.zeros_like(q)
+    with torch.cuda.graph(graph):
+        pv.paged_attn_fwd(*args, out=out, workspace=ws[:need], **c.exps())
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), got.view(torch.int16))
+    assert pv.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lq,n", [(1, 1), (1, 300), (1, 3000), (5, 900), (40, 900), (300, 900)])
+def test_nan_values_in_a_visible_row(pv, lq, n, fmt):
+    """A V row that held a NaN: the queries that see it, and no other sequence's."""
+    H, Hq, D = 2, 8, 128
+    c = Cache([n + lq, n + lq], 16, H, D, fmt)
+    k, v = _rows(2 * (n + lq), H, D, 1), _rows(2 * (n + lq), H, D, 2)
+    v[n // 2, 1, 7] = math.nan
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n + lq, n + lq]), c.dev_table, **c.exps())
+    q = _rows(2 * lq, Hq, D, 3, 0.0)
+    out = _attend(pv, c, q, [lq, lq], [n + lq, n + lq], True)[:2 * lq]
+    dims = slice(None) if fmt == "e4m3" else 7          # an 8-bit row is NaN throughout
+    assert torch.isnan(out[:lq, 4:, dims]).all()
+    assert torch.isfinite(out[:lq, :4]).all() and torch.isfinite(out[lq:]).all()
