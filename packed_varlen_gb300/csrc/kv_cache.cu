@@ -43,11 +43,6 @@ struct CopyParams {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Larger magnitudes of two pairs, with signs that mean nothing; NaN wins.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -99,7 +94,7 @@ __device__ __forceinline__ uint2 dequantise4(uint32_t w, float scale) {
   asm("{.reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;}\n"
       : "=f"(f[2]), "=f"(f[3])
       : "r"(h1));
-  return make_uint2(pack_bf16(f[0] * scale, f[1] * scale), pack_bf16(f[2] * scale, f[3] * scale));
+  return make_uint2(tc::pack_bf16x2(f[0] * scale, f[1] * scale), tc::pack_bf16x2(f[2] * scale, f[3] * scale));
 }
 
 // A tile: consecutive packed rows, their places found a token to a thread.
