@@ -13,9 +13,11 @@
 //    workspace.  Shares are cut in keys rather than in key tiles, which keeps
 //    the sum over the items before a place a quadratic, and rounded down to a
 //    tile where they meet an item (at most one tile in six or more).
-// Smallest share, 6 / 10 / 16 key tiles, GPU time: 16 tokens of 32 sequences over
-// 10-12k keys 429 / 380 / 371 us, of one 34 / 38 / 46; a mixed step 101 / 97 /
-// 90; cross attention to 700-1500 states 52 / 45 / 45.
+// Smallest share, 6 / 10 / 12 / 16 key tiles, GPU time: 16 tokens of 32 sequences over
+// 10-12k keys 372 / 342 / 336 / 334 us, of one 28 / 30 / 31 / 37; a mixed step 93 / 93 /
+// 81 / 83; cross attention to 700-1500 states 48 / 42 / 42 / 42; two 8-bit chunks 125 /
+// 125 / 124 / 124; a long chunk the same.  10 was taken with a set-up that cost more; 12
+// would take 12 us off the mixed step for one off the lone sequence, and other bits.
 // The choice looks at the sequence alone, as if it had the GPU (152 CTAs) to
 // itself, so its bits do not depend on the batch.
 #pragma once

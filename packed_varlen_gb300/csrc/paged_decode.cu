@@ -18,8 +18,8 @@
 // GPU time, 32 query heads on 8 of 128, bf16: 64 sequences of 900-8000 keys
 // 181 us (1143 MB, 6.3 TB/s; 9 us of it the join), one of 131,000 89 us (6.0
 // TB/s), four of 370-700 9.5 us (latency: some 1100 cycles a tile, and 4200
-// before the first).  64 heads on 8, 8-bit rows, 96 sequences of 2-12k: 274 us
-// (1484 MB, 5.4 TB/s; parts add 85 MB of writes, see decode_min_part).
+// before the first).  64 heads on 8, 8-bit rows, 96 sequences of 2-12k: 273-284 us
+// (1484 MB, 5.2-5.4 TB/s; parts add 85 MB of writes, see decode_min_part).
 //
 // (Tensor cores only save instructions here: 16 rows per key keep these busy 15%
 // of the time, so the 5th generation's faster ones would gain nothing.)
