@@ -1139,3 +1139,26 @@ def test_nan_values_in_a_visible_row(pv, lq, n, fmt):
     dims = slice(None) if fmt == "e4m3" else 7          # an 8-bit row is NaN throughout
     assert torch.isnan(out[:lq, 4:, dims]).all()
     assert torch.isfinite(out[:lq, :4]).all() and torch.isfinite(out[lq:]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lq,n,D,size", [(8, 3000, 128, 24), (16, 700, 128, 21), (13, 1500, 64, 28)])
+def test_large_scores_of_more_rows(pv, lq, n, D, size, fmt):
+    test_scores_of_any_size(pv, lq, n, D, size, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [60, 1000, 4000])
+@pytest.mark.parametrize("lq,Hq", [(4, 2), (7, 4), (16, 2)])
+def test_large_scores_beside_ordinary_ones(pv, lq, Hq, n, fmt):
+    """Rows of q whose scores are large among rows whose scores are not, over values of unlike
+    scale: every row is held to its own bound."""
+    H, D = 1, 128
+    c = Cache([n], 16, H, D, fmt)
+    k, v = _rows(n, H, D, 3, 0.3), _rows(n, H, D, 4, 2.0)
+    pv.kv_cache_write(k.cuda(), v.cuda(), c.k, c.v, _cu([n]), c.dev_table, **c.exps())
+    q = _rows(lq, Hq, D, 5, 0.0).float()
+    q[1::3] *= 2.0 ** 22
+    q = q.to(torch.bfloat16)
+    out = _attend(pv, c, q, [lq], [n], True)
+    _check(out, c, q, [lq], [n], True, 1 / math.sqrt(D))
