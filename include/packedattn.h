@@ -64,6 +64,15 @@ typedef enum {
 #define PA_CACHE_BF16 0
 #define PA_CACHE_E4M3 1
 
+/* Activations of the linear layers with an epilogue: x; max(x, 0); x s(x) with the
+ * logistic function s; x (1 + erf(x / sqrt 2)) / 2; and its approximation
+ * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2. */
+#define PA_ACT_NONE 0
+#define PA_ACT_RELU 1
+#define PA_ACT_SILU 2
+#define PA_ACT_GELU 3
+#define PA_ACT_GELU_TANH 4
+
 /* Query rows per work item of pa_varlen_attn_fwd (two 128-row tensor-core tiles). */
 #define PA_VARLEN_TILE_M 256
 
@@ -104,6 +113,44 @@ pa_status pa_varlen_attn_fwd(const void *q, const void *k, const void *v, void *
                              int32_t batch, int32_t total_q, int32_t total_k,
                              int32_t max_q, int32_t max_k, int32_t H, int32_t D,
                              float scale, pa_stream_t stream);
+
+/*
+ * pa_prompt_attn_fwd -- softmax attention of packed prompts, causal and with
+ * grouped heads, over K and V rows that are packed too (a prompt before it is
+ * in a cache, or behind a prefix that pa_kv_cache_read returned).
+ *
+ * Sequence b has L_b queries (from cu_seqlens_q) and K_b keys (cu_seqlens_k).
+ * With causal != 0 its queries are the last L_b of K_b positions: query i sees
+ * key j iff j <= K_b - L_b + i (K_b = L_b: the tokens up to its own); with
+ * causal = 0 it sees every key.  Query head h reads K/V head h / (Hq / Hkv).
+ *   out[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], k[j,h',:]>) * v[j,h',:]
+ * A query that sees no key gets zeros.  Scores, maxima, sums and the output's
+ * accumulation are fp32; softmax weights are rounded to bf16 for the product
+ * with V, and the output once to bf16.
+ *
+ * q [total_q, Hq, D], k, v [total_k, Hkv, D] bf16, with q_stride, k_stride,
+ * v_stride elements from one token to the next (>= heads * D, multiples of 8:
+ * the rows may be slices of a fused projection's output); out [total_q, Hq, D]
+ * bf16 contiguous, written at the rows that belong to a sequence only, and not
+ * overlapping q, k or v.  cu_seqlens_q / cu_seqlens_k device int32 [batch + 1],
+ * batch in [1, PA_MAX_BATCH]; total_q, total_k >= cu[batch] and at most 2^30
+ * (total_q = 0 or max_q = 0 does nothing; q and out, k and v may be NULL where
+ * their total is 0); max_q / max_k bound every length; Hq a multiple of Hkv
+ * and at most 65535; (total_q / 256 + batch) * Hq at most 2^30; D in
+ * {64, 128}; scale and scale * log2(e) finite.
+ * Rows outside a sequence never reach its result, whatever their bits.  A key
+ * that causal order hides from a query has weight zero there; a NaN or infinity
+ * in its V row can still reach that query as 0 * NaN (in its K row it cannot).
+ * A sequence with bad boundaries (PA_DEVICE_ERR_CU_SEQLENS) or longer than
+ * max_q / max_k (PA_DEVICE_ERR_MAX_LEN) is skipped, its rows left untouched.
+ * Deterministic, and independent of the batch around a sequence.
+ */
+pa_status pa_prompt_attn_fwd(const void *q, const void *k, const void *v, void *out,
+                             const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                             int32_t batch, int32_t total_q, int32_t total_k,
+                             int32_t max_q, int32_t max_k, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int32_t Hq, int32_t Hkv,
+                             int32_t D, int32_t causal, float scale, pa_stream_t stream);
 
 /*
  * pa_block_window_attn_fwd -- block-local attention of the Token2Wav DiT.
@@ -211,6 +258,37 @@ pa_status pa_rope_packed(void *q, void *k, const int32_t *cu_seqlens_q,
                          const int32_t *cu_seqlens_k, const int32_t *pos_offset,
                          int32_t batch, int32_t total_q, int32_t total_k, int32_t H,
                          int32_t D, float base, pa_stream_t stream);
+
+/*
+ * pa_rope_axes -- rotary positions with several axes (time, height, width of
+ * image and video tokens), on packed q and k.
+ *
+ * Pair i of a head's rotated width R = sum of axis_dims, i in [0, R / 2), belongs
+ * to the axis whose stretch of axis_dims[a] / 2 pairs holds it, the axes in order.
+ * Its two elements, 2i and 2i + 1 or (halves != 0) i and i + R / 2, are turned by
+ * the angle positions[a, t] * theta_i: (x, y) -> (x cos - y sin, x sin + y cos).
+ * theta_i = base^(-2 j / axis_dims[a]) with j the pair's place on its axis, or
+ * (shared != 0: one spectrum over all axes) base^(-2 i / R).  Elements past R
+ * are copied.  The fraction of a turn is exact to 2^-53 of theta times the
+ * position, sin, cos and the rotation are fp32, the output is rounded once.
+ *
+ * q, q_out [total, Hq, D], k, k_out [total, Hkv, D] bf16 with their strides in
+ * elements from one token to the next (>= heads * D, multiples of 8); q_out = q
+ * and k_out = k (with the same stride) turn in place, else outputs must not
+ * overlap inputs; Hkv = 0: no k.  positions: device int32 [axes, total],
+ * any values.  num_tokens: device int32, or NULL: only rows below it are
+ * turned, the others left untouched (cu_seqlens + batch, for buffers with rows
+ * behind the last sequence).  axis_dims: HOST int32 [axes], even, >= 2; axes
+ * in [1, 8]; R a multiple of 8 and at most D; D a multiple of 8 and at most
+ * 256; heads at most 2^20 each; total * heads at most 2^30; base finite and
+ * > 0.  total = 0 does nothing (pointers may then be NULL).
+ */
+pa_status pa_rope_axes(const void *q, const void *k, void *q_out, void *k_out,
+                       const int32_t *positions, const int32_t *num_tokens,
+                       const int32_t *axis_dims, int32_t axes, int32_t total,
+                       int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                       int64_t k_out_stride, int32_t Hq, int32_t Hkv, int32_t D,
+                       int32_t halves, int32_t shared, float base, pa_stream_t stream);
 
 /*
  * Paged K/V caches
@@ -384,6 +462,41 @@ int64_t pa_paged_attn_workspace_bytes(int32_t batch, int32_t total_q, int32_t ma
  */
 pa_status pa_linear_bf16(const void *x, const void *w, const void *bias, void *y, int32_t M,
                          int32_t N, int32_t K, pa_stream_t stream);
+
+/*
+ * pa_linear_act_bf16 -- the packed-M linear layer with bias, activation and
+ * residual in its epilogue.
+ *
+ *   y[m, n] = residual[m, n] + act(sum_k x[m, k] * w[n, k] + bias[n])
+ *
+ * x [M, K], residual, y [M, N] bf16 with their strides in elements from one row
+ * to the next (>= K or N, multiples of 8); w [N, K] bf16 contiguous; bias bf16
+ * [N] or NULL; residual or NULL (its stride is then ignored); act one of
+ * PA_ACT_*.  y may be residual itself (in place, with the same stride), and must
+ * not overlap x, w, bias or the residual otherwise.  Accumulation, activation
+ * and sums are fp32, rounded to bf16 once.  A row depends on its own x and
+ * residual row, w and bias alone: packed, alone or at any row offset its bits
+ * agree.  M >= 0 (0 does nothing; x and y may then be NULL), N >= 1, K >= 1; K
+ * and N multiples of 8; every pointer 16-byte aligned.
+ */
+pa_status pa_linear_act_bf16(const void *x, const void *w, const void *bias,
+                             const void *residual, void *y, int32_t M, int32_t N, int32_t K,
+                             int64_t x_stride, int64_t residual_stride, int64_t y_stride,
+                             int32_t act, pa_stream_t stream);
+
+/*
+ * pa_linear_gated_bf16 -- the first half of a gated feed-forward block: two
+ * projections, the activation of one and their product.
+ *
+ *   y[m, n] = act(sum_k x[m, k] * w_gate[n, k]) * (sum_k x[m, k] * w_up[n, k])
+ *
+ * w_gate, w_up [N, K] bf16, contiguous each (two tensors, or the halves of one).
+ * Neither product is rounded before the last step.  The other rules are
+ * pa_linear_act_bf16's.
+ */
+pa_status pa_linear_gated_bf16(const void *x, const void *w_gate, const void *w_up, void *y,
+                               int32_t M, int32_t N, int32_t K, int64_t x_stride,
+                               int64_t y_stride, int32_t act, pa_stream_t stream);
 
 /*
  * pa_cfg_combine -- segment-aware unpack of each request's image span with

@@ -29,10 +29,13 @@ the integer steps), written for a reader to check against the definitions:
 
 * ``quantise_rows``, ``dequantise_rows``, ``places``, ``cached_rows``,
   ``paged_attention``: the paged K/V cache and attention over it.
+* ``prompt_attention``, ``rope_axes``, ``activation``, ``linear_act``,
+  ``linear_gated``: the operators of a layer over packed prompts.
 
 Every function is pinned by tests in ``tests/test_oracle_pins.py`` and
 ``tests/test_oracle_cfg.py``, ``tests/test_oracle_rope.py`` and
-``tests/test_oracle_linear.py`` and ``tests/test_oracle_paged.py`` against
+``tests/test_oracle_linear.py``, ``tests/test_oracle_paged.py`` and
+``tests/test_oracle_prompt.py`` against
 brute force, closed forms, a library routine and the pages' invariants.
 """
 from .packing import cu_seqlens_from_lengths, pack, unpack, work_order
@@ -45,6 +48,14 @@ from .paged import (
     places,
     cached_rows,
     paged_attention,
+)
+from .prompt import (
+    prompt_attention,
+    axis_angles,
+    rope_axes,
+    activation,
+    linear_act,
+    linear_gated,
 )
 from .linear import linear, linear_rows, linear_flops
 from .attention import (
@@ -66,4 +77,5 @@ __all__ = [
     "varlen_useful_flops", "block_window_useful_flops", "cfg_combine", "rope", "rope_positions",
     "linear", "linear_rows", "linear_flops", "e4m3_round", "quantise_rows",
     "dequantise_rows", "places", "cached_rows", "paged_attention",
+    "prompt_attention", "axis_angles", "rope_axes", "activation", "linear_act", "linear_gated",
 ]

@@ -72,6 +72,11 @@ _SIGNATURES = {
     "pa_paged_attn_fwd": ([_c_ptr] * 9 + [_c_word] * 14 + [_c_f32, _c_ptr, _c_word, _c_ptr],
                           _c_i32),
     "pa_paged_attn_workspace_bytes": ([_c_i32] * 8, _c_i64),
+    # (as the three above)
+    "pa_prompt_attn_fwd": ([_c_ptr] * 6 + [_c_word] * 12 + [_c_f32, _c_ptr], _c_i32),
+    "pa_rope_axes": ([_c_ptr] * 7 + [_c_word] * 11 + [_c_f32, _c_ptr], _c_i32),
+    "pa_linear_act_bf16": ([_c_ptr] * 5 + [_c_word] * 7 + [_c_ptr], _c_i32),
+    "pa_linear_gated_bf16": ([_c_ptr] * 4 + [_c_word] * 6 + [_c_ptr], _c_i32),
 }
 
 
@@ -713,4 +718,210 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
     if st != PA_OK:
         _check("pa_paged_attn_fwd", st)
+    return out
+
+
+# ---------------------------------------------------------------- a layer over packed prompts
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_q: int,
+                    max_k: int, causal: bool = True, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of packed prompts, causal and with grouped heads (pa_prompt_attn_fwd).
+    q [Tq, Hq, D], k, v [Tk, Hkv, D] bf16, each possibly a slice of a wider tensor
+    along its last dimensions; cu_seqlens int32 [B + 1].  Causal order lines up
+    the ends: query i of a sequence sees key j iff j <= Lk - Lq + i.  Rows of
+    ``out`` beyond cu_seqlens_q[B] are not written (a fresh ``out`` is zero-filled)."""
+    lib = _lib or load_library()
+    max_q, max_k = int(max_q), int(max_k)
+    if (max_q | max_k) >> 31:
+        _fits_32_bits("pa_prompt_attn_fwd", max_q, max_k)
+    dev = _device_of(q, "q")
+    qs, ks, vs = _rows_stride(q, "q", dev), _rows_stride(k, "k", dev), _rows_stride(v, "v", dev)
+    Tq, Hq, D = shape = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D or v.shape != k.shape or Hkv < 1 or Hq < 1 or Hq % Hkv:
+        raise ValueError("k and v must be [Tk, Hkv, D] with q's D and Hq a multiple of Hkv")
+    B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
+    _need_index(cu_seqlens_q, "cu_seqlens_q", B + 1, dev)
+    _need_index(cu_seqlens_k, "cu_seqlens_k", B + 1, dev)
+    if scale is None:
+        scale = D ** -0.5
+    raw = _raw_stream(dev, stream)
+    if out is None:
+        out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
+    else:
+        _need_out(out, "out", shape, dev)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), cu_seqlens_q.data_ptr(),
+            cu_seqlens_k.data_ptr(), B, Tq, Tk, max_q, max_k, qs, ks, vs, Hq, Hkv, D,
+            1 if causal else 0, float(scale), raw)
+    fn = lib.pa_prompt_attn_fwd
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_prompt_attn_fwd", st)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _host_ints(*values: int):
+    """The values as a host int32 array, and its address."""
+    _fits_32_bits("pa_rope_axes", *values)
+    arr = (ctypes.c_int32 * len(values))(*values)
+    return arr, ctypes.addressof(arr)
+
+
+def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, axis_dims,
+              base: float = 10000.0, halves: bool = False, shared: bool = False,
+              num_tokens: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions with several axes on packed q [T, Hq, D] and k [T, Hkv, D]
+    bf16 (pa_rope_axes), each possibly a slice of a wider tensor along its last
+    dimensions, and k possibly None.  positions int32 [axes, T]; axis_dims: the
+    elements of a head that each axis turns.  ``halves``: pairs are (i, i + R/2)
+    instead of (2i, 2i + 1); ``shared``: one spectrum over all axes.  In place
+    unless q_out / k_out are given.  ``num_tokens`` (int32, one element, for
+    instance cu_seqlens[-1:]): rows from there on are left as they are.
+    Returns (q_out, k_out)."""
+    lib = _lib or load_library()
+    dev = _device_of(q, "q")
+    q_out = q if q_out is None else q_out
+    qs, qo = _rows_stride(q, "q", dev), _rows_stride(q_out, "q_out", dev)
+    T, Hq, D = q.shape
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    kp = ko_p = None
+    ks = ko = Hkv = 0
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        ks, ko = _rows_stride(k, "k", dev), _rows_stride(k_out, "k_out", dev)
+        Hkv = k.shape[1]
+        if k.shape != (T, Hkv, D) or k_out.shape != k.shape:
+            raise ValueError("k and k_out must be [T, Hkv, D] with q's T and D")
+        kp, ko_p = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    dims, dims_at = _host_ints(*[int(d) for d in axis_dims])
+    _need(positions, "positions", _I32, 2)
+    if positions.shape != (len(dims), T) or positions.get_device() != dev:
+        raise ValueError("positions must be [axes, T] on q's device")
+    n_at = None
+    if num_tokens is not None:
+        _need(num_tokens, "num_tokens", _I32)
+        if num_tokens.numel() != 1 or num_tokens.get_device() != dev:
+            raise ValueError("num_tokens must be one element on q's device")
+        n_at = num_tokens.data_ptr()
+    args = (q.data_ptr(), kp, q_out.data_ptr(), ko_p, positions.data_ptr(), n_at, dims_at,
+            len(dims), T, qs, ks, qo, ko, Hq, Hkv, D, 1 if halves else 0, 1 if shared else 0,
+            float(base), _raw_stream(dev, stream))
+    fn = lib.pa_rope_axes
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_rope_axes", st)
+    return q_out, k_out
+
+
+def _matrix_stride(t: torch.Tensor, name: str, dev: int) -> int:
+    """Elements from one row to the next of a bf16 matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on x's device, not {t.device}")
+    M, N = t.shape
+    if N > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if M > 1 else N
+
+
+def _weight(w: torch.Tensor, name: str, K: int, dev: int) -> int:
+    _need(w, name, _BF16, 2)
+    if w.shape[1] != K or w.get_device() != dev:
+        raise ValueError(f"{name} must be [N, {K}] on x's device, got {list(w.shape)}")
+    return w.shape[0]
+
+
+def _activation(act: str) -> int:
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}") from None
+
+
+def linear_act_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    act: str = "none", residual: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = residual + act(x w^T + bias) (pa_linear_act_bf16); x [M, K], w [N, K], bias
+    [N], residual [M, N] bf16; act: a name in ACTIVATIONS.  x, residual and out
+    may be slices of wider matrices; out may be residual itself."""
+    lib = _lib or load_library()
+    dev = _device_of(x, "x")
+    xs = _matrix_stride(x, "x", dev)
+    M, K = x.shape
+    N = _weight(w, "w", K, dev)
+    code = _activation(act)
+    b = r = None
+    rs = 0
+    if bias is not None:
+        _need(bias, "bias", _BF16, 1)
+        if bias.shape[0] != N or bias.get_device() != dev:
+            raise ValueError("bias must be [N] on x's device")
+        b = bias.data_ptr()
+    if residual is not None:
+        rs = _matrix_stride(residual, "residual", dev)
+        if residual.shape != (M, N):
+            raise ValueError("residual must be [M, N]")
+        r = residual.data_ptr()
+    raw = _raw_stream(dev, stream)
+    if out is None:
+        out = _new(torch.empty, (M, N), _BF16, dev, stream, raw)
+    ys = _matrix_stride(out, "out", dev)
+    if out.shape != (M, N):
+        raise ValueError("out must be [M, N]")
+    args = (x.data_ptr(), w.data_ptr(), b, r, out.data_ptr(), M, N, K, xs, rs, ys, code, raw)
+    fn = lib.pa_linear_act_bf16
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_linear_act_bf16", st)
+    return out
+
+
+def linear_gated_bf16(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                      act: str = "silu", out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """y = act(x w_gate^T) * (x w_up^T) (pa_linear_gated_bf16); x [M, K], w_gate, w_up
+    [N, K] bf16 (two tensors, or the halves of one); act: a name in ACTIVATIONS.
+    x and out may be slices of wider matrices."""
+    lib = _lib or load_library()
+    dev = _device_of(x, "x")
+    xs = _matrix_stride(x, "x", dev)
+    M, K = x.shape
+    N = _weight(w_gate, "w_gate", K, dev)
+    if _weight(w_up, "w_up", K, dev) != N:
+        raise ValueError("w_gate and w_up must have the same shape")
+    code = _activation(act)
+    raw = _raw_stream(dev, stream)
+    if out is None:
+        out = _new(torch.empty, (M, N), _BF16, dev, stream, raw)
+    ys = _matrix_stride(out, "out", dev)
+    if out.shape != (M, N):
+        raise ValueError("out must be [M, N]")
+    args = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), M, N, K, xs, ys,
+            code, raw)
+    fn = lib.pa_linear_gated_bf16
+    st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
+    if st != PA_OK:
+        _check("pa_linear_gated_bf16", st)
     return out

@@ -243,7 +243,8 @@ pa_status pa_varlen_attn_fwd(const void *q, const void *k, const void *v, void *
     return PA_ERR_MISALIGNED;
   if (total_q == 0 || max_q == 0) return PA_OK;  // no query rows: nothing to write
   VarlenArgs a{q, k, v, out, cu_seqlens_q, cu_seqlens_k, batch, total_q, total_k, max_q,
-               max_k, H, D, scale, nullptr, 0};
+               max_k, H, D, scale, nullptr, 0, H, 0, int64_t{H} * D, int64_t{H} * D,
+               int64_t{H} * D};
   cudaError_t e = device_context(&a.status, &a.num_sms);
   if (e != cudaSuccess) return from_cuda(e);
   return from_cuda(launch_varlen_attn(a, reinterpret_cast<cudaStream_t>(stream)));

@@ -101,36 +101,39 @@ struct PairCfg {
   static constexpr uint32_t kIdescO = idesc_bf16_f32(kCluster * kTile, kD, true);
 };
 
-// A position in a pair's stream of key tiles: items i0, i0 + stride, ...,
-// skipping items without keys; tile j of item i.  done() once past the end.
+// A position in a pair's stream of key tiles: the items of worker `cl` of
+// `n_cl`, skipping items without keys; n-th item i, its tile j.  done() once
+// past the end.
+template <bool kPrompt>
 struct Walk {
-  int i, j, n_items, stride;
+  int n, j, n_items, cl, n_cl, i;
   ItemInfo it;
   __device__ __forceinline__ bool done() const { return i >= n_items; }
-};
-__device__ __forceinline__ void walk_seek(Walk &w, const VarlenParams &p, const int32_t *order,
-                                          const int32_t *prefix) {
-  w.j = 0;
-  while (w.i < w.n_items) {
-    w.it = item_info(p, order, prefix, w.i);
-    if (w.it.nk > 0) return;
-    w.i += w.stride;
+  __device__ __forceinline__ void seek(const VarlenParams &p, const int32_t *order,
+                                       const int32_t *prefix) {
+    j = 0;
+    for (; (i = item_at<kPrompt>(p, n, cl, n_cl)) < n_items; ++n) {
+      it = item_info<kPrompt>(p, order, prefix, i);
+      if (it.nk > 0) return;
+    }
   }
-}
-__device__ __forceinline__ void walk_next(Walk &w, const VarlenParams &p, const int32_t *order,
-                                          const int32_t *prefix) {
-  if (++w.j < w.it.nk) return;
-  w.i += w.stride;
-  walk_seek(w, p, order, prefix);
-}
+  __device__ __forceinline__ void next(const VarlenParams &p, const int32_t *order,
+                                       const int32_t *prefix) {
+    if (++j < it.nk) return;
+    ++n;
+    seek(p, order, prefix);
+  }
+};
 
-// Row maximum of 128 raw scores (TMEM words), over the first `valid` keys;
+// Row maximum of 128 raw scores (TMEM words), over the first `valid` keys
+// (masked: some row of the warp has fewer than 128);
 // with a positive scale the maximum of the raw scores is scaled once,
 // otherwise every score is scaled first.  The unmasked positive-scale form
 // (every tile but a sequence's last) is three-input max chains only.
-__device__ __forceinline__ float tile_max(const uint32_t (&sr)[kTile], int valid, float sl2) {
+__device__ __forceinline__ float tile_max(const uint32_t (&sr)[kTile], int valid, bool masked,
+                                          float sl2) {
   float mx8[8];
-  if (sl2 > 0.f && valid >= kTile) {
+  if (sl2 > 0.f && !masked) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       mx8[e] = fmaxf(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
@@ -156,7 +159,7 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sr)[kTile], int valid
 // P = 2^(s * scale_log2 - m) for the 128 keys of one TMEM lane's S row at
 // `taddr`, 64 at a time, written as bf16 pairs over the row's first 64
 // columns; adds P to the eight partial sums.  kMasked: keys from `valid` on
-// get P = 0 (a sequence's last key tile).
+// get P = 0 (a sequence's last key tile, tiles that causal order cuts).
 template <bool kMasked>
 __device__ __forceinline__ void tile_p(uint32_t taddr, int valid, float sl2, float m,
                                        float2 (&sum8)[8]) {
@@ -184,6 +187,7 @@ __device__ __forceinline__ void tile_p(uint32_t taddr, int valid, float sl2, flo
   }
 }
 
+template <bool kPrompt>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     varlen_attn_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
@@ -233,8 +237,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc_pair(base + C::kMiscOff, C::kTmemCols);
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
-  sched_build(order, prefix, tmp, tmp + PA_MAX_BATCH, p.cu_q, p.cu_k, p.batch, p.H, kItemRows,
-              p.total_q, p.total_k, p.max_q, p.max_k, p.status, blockIdx.x == 0);
+  item_list<kPrompt>(p, order, prefix, tmp, tmp + PA_MAX_BATCH, blockIdx.x == 0);
   fence_before_sync();
   __syncwarp();     // the cluster barrier is warp-aligned
   cluster_sync();   // barriers of both CTAs initialised before any remote use
@@ -277,7 +280,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       return true;
     };
     // this CTA's 64 keys of the K tile, all 128 columns
-    auto load_k = [&](const Walk &w) -> bool {
+    auto load_k = [&](const Walk<kPrompt> &w) -> bool {
       uint32_t s;
       if (!take_slot(s)) return false;
       const int row = w.it.k0 + key_tile(w.it, w.j) * kTile + static_cast<int>(rank) * 64;
@@ -287,13 +290,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
           tma_load_3d_pair(sRing + s * C::kSlotBytes + hf * C::kKHalfBytes, &tm_k, full,
-                           hf * 64, w.it.head, row);
+                           hf * 64, w.it.kv_head, row);
       }
       ++loads;
       return true;
     };
     // this CTA's 64 columns of the V tile, all 128 keys
-    auto load_v = [&](const Walk &w) -> bool {
+    auto load_v = [&](const Walk<kPrompt> &w) -> bool {
       uint32_t s;
       if (!take_slot(s)) return false;
       const int kt = key_tile(w.it, w.j);
@@ -303,7 +306,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t full = mapa_shared(bar(C::kSlotFull + s), 0);
       if (lead && leader) mbar_arrive_expect_tx(bar(C::kSlotFull + s), kCluster * C::kSlotBytes);
       if (valid >= kTile) {
-        if (lead) tma_load_3d_pair(dst, &tm_v, full, static_cast<int>(rank) * 64, w.it.head, row);
+        if (lead) tma_load_3d_pair(dst, &tm_v, full, static_cast<int>(rank) * 64, w.it.kv_head, row);
       } else {
         // The tile holds rows past the sequence end (the next sequence's, or
         // the buffer's trailing rows).  P is 0 there, but 0 * Inf and
@@ -312,7 +315,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         // are cleared, and only then are its bytes counted on the slot.
         if (lead) {
           mbar_arrive_expect_tx(bar(C::kTail), C::kSlotBytes);
-          tma_load_3d(dst, &tm_v, bar(C::kTail), static_cast<int>(rank) * 64, w.it.head, row);
+          tma_load_3d(dst, &tm_v, bar(C::kTail), static_cast<int>(rank) * 64, w.it.kv_head, row);
         }
         tail_pending = true;
         if (!wait_all(bar(C::kTail), tails & 1u)) return false;
@@ -336,21 +339,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       ++loads;
       return true;
     };
-    Walk kw{cl, 0, n_items, n_cl, {}}, vw{cl, 0, n_items, n_cl, {}};
-    walk_seek(kw, p, order, prefix);
-    walk_seek(vw, p, order, prefix);
+    Walk<kPrompt> kw{0, 0, n_items, cl, n_cl, 0, {}}, vw{0, 0, n_items, cl, n_cl, 0, {}};
+    kw.seek(p, order, prefix);
+    vw.seek(p, order, prefix);
     // the order of the MMA issuer: K of the first kSBufs tiles, then V_g, K_{g+3}
     auto next_k = [&]() -> bool {
       if (kw.done()) return true;
       if (kw.j == 0 && !load_q(kw.it)) return false;
       if (!load_k(kw)) return false;
-      walk_next(kw, p, order, prefix);
+      kw.next(p, order, prefix);
       return true;
     };
     for (int t = 0; t < kSBufs && ok; ++t) ok = next_k();
     while (ok && !vw.done()) {
       ok = load_v(vw);
-      walk_next(vw, p, order, prefix);
+      vw.next(p, order, prefix);
       if (ok) ok = next_k();
     }
     if (!ok) {
@@ -406,9 +409,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
       // V (MN-major): one 64-column half per CTA, next 8 keys at SBO = 1024
       const uint64_t vdesc0 = sdesc_sw128(sRing, 1024, 1024);
-      Walk kw{cl, 0, n_items, n_cl, {}}, vw{cl, 0, n_items, n_cl, {}};
-      walk_seek(kw, p, order, prefix);
-      walk_seek(vw, p, order, prefix);
+      Walk<kPrompt> kw{0, 0, n_items, cl, n_cl, 0, {}}, vw{0, 0, n_items, cl, n_cl, 0, {}};
+      kw.seek(p, order, prefix);
+      vw.seek(p, order, prefix);
       // S_gs = Q K^T of the K walk's tile (or a bare commit past the end)
       auto issue_s = [&]() -> bool {
         const uint32_t b = gs % kSBufs;
@@ -438,7 +441,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
           ++kq;
         }
         ++gs;
-        walk_next(kw, p, order, prefix);
+        kw.next(p, order, prefix);
         return true;
       };
       if (!vw.done())
@@ -469,7 +472,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         if (vw.j == vw.it.nk - 1) commit_both(bar(C::kOFull));
         commit_both(bar(C::kSlotEmpty + s));
         ++gv;
-        walk_next(vw, p, order, prefix);
+        vw.next(p, order, prefix);
         ok = issue_s();
       }
       // every MMA issued so far has finished before TMEM is released
@@ -501,14 +504,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale_log2;
     uint32_t g = 0, o_waits = 0;
     bool ok = true;
-    for (int i = cl; i < n_items && ok; i += n_cl) {
-      const ItemInfo it = item_info(p, order, prefix, i);
+    for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, cl, n_cl)) < n_items; ++n) {
+      const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
       const int rows_c = it.rows - static_cast<int>(rank) * kTile;   // may be <= 0
       __nv_bfloat16 *dst =
           p.out +
           (static_cast<int64_t>(it.q_row0 + static_cast<int>(rank) * kTile + row) * p.H +
            it.head) * kD + side * 64;
       const bool store = row < rows_c;
+      // prompts: the keys that this row sees (none: its output is zero)
+      const int row_keys =
+          kPrompt ? min(it.lk, it.seen + static_cast<int>(rank) * kTile + row + 1) : it.lk;
       if (it.nk == 0) {
         if (store) {
           uint4 *d4 = reinterpret_cast<uint4 *>(dst);
@@ -528,7 +534,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         okt = __all_sync(0xffffffffu, okt);
         // pass 1: the tile's row maximum (scores are read again for P, so
         // no 128-value array stays live across the hand-off)
-        const int valid = key_tile(it, j) == it.nk - 1 ? it.lk - (it.nk - 1) * kTile : kTile;
+        const int valid = kPrompt ? row_keys - key_tile(it, j) * kTile
+                          : key_tile(it, j) == it.nk - 1 ? it.lk - (it.nk - 1) * kTile
+                                                         : kTile;
+        const bool masked =
+            kPrompt ? __any_sync(0xffffffffu, valid < kTile) != 0 : valid < kTile;
         float mx = -INFINITY;
         if (okt) {
           fence_after_sync();
@@ -538,7 +548,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld32(lane_base + b * kTile + c * 32,
                       *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           tmem_wait_ld();
-          mx = tile_max(sr, valid, sl2);
+          mx = tile_max(sr, valid, masked, sl2);
         }
         // the running maximum after the previous tile (the other warp's)
         float m_prev = -INFINITY;
@@ -582,7 +592,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         float2 sum8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum8[e] = make_float2(0.f, 0.f);
-        if (valid >= kTile)
+        if (!masked)
           tile_p<false>(lane_base + b * kTile, valid, sl2, m, sum8);
         else
           tile_p<true>(lane_base + b * kTile, valid, sl2, m, sum8);
@@ -646,6 +656,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
+            if (kPrompt && row_keys <= 0) {   // (its sums are NaN)
+              d4[v] = make_uint4(0, 0, 0, 0);
+              continue;
+            }
             w.x = pack_bf16x2(__uint_as_float(r[8 * v + 0]) * inv, __uint_as_float(r[8 * v + 1]) * inv);
             w.y = pack_bf16x2(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
             w.z = pack_bf16x2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
@@ -667,15 +681,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::kTmemCols);
 }
 
-// [rows, H, 128] bf16 viewed as a 3-D tensor (D, H, rows); box 64 x 1 x
-// box_rows with 128-byte swizzle.  Rows past the end read as zero.
-bool make_map_rows(CUtensorMap *map, const void *ptr, int rows, int H, int box_rows) {
+// [rows, H, 128] bf16 viewed as a 3-D tensor (D, H, rows), rows row_elems
+// elements apart; box 64 x 1 x box_rows with 128-byte swizzle.  Rows past the end read as zero.
+bool make_map_rows(CUtensorMap *map, const void *ptr, int rows, int H, int64_t row_elems,
+                   int box_rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2,
-                                 static_cast<cuuint64_t>(H) * kD * 2};
+                                 static_cast<cuuint64_t>(row_elems) * 2};
   const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides,
@@ -684,33 +699,30 @@ bool make_map_rows(CUtensorMap *map, const void *ptr, int rows, int H, int box_r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-cudaError_t launch_varlen_attn_pair(const VarlenArgs &a, cudaStream_t stream) {
+template <bool kPrompt>
+cudaError_t launch_pair(const VarlenArgs &a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
-  if (!make_map_rows(&mq, a.q, a.total_q, a.H, kTile) ||
-      !make_map_rows(&mk, a.k, a.total_k, a.H, 64) ||
-      !make_map_rows(&mv, a.v, a.total_k, a.H, kTile))
+  if (!make_map_rows(&mq, a.q, a.total_q, a.H, a.q_stride, kTile) ||
+      !make_map_rows(&mk, a.k, a.total_k, a.Hkv, a.k_stride, 64) ||
+      !make_map_rows(&mv, a.v, a.total_k, a.Hkv, a.v_stride, kTile))
     return cudaErrorInvalidValue;
-  VarlenParams p;
-  p.out = static_cast<__nv_bfloat16 *>(a.out);
-  p.cu_q = a.cu_q;
-  p.cu_k = a.cu_k;
-  p.batch = a.batch;
-  p.H = a.H;
-  p.total_q = a.total_q;
-  p.total_k = a.total_k;
-  p.max_q = a.max_q;
-  p.max_k = a.max_k;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.status = a.status;
+  const VarlenParams p = varlen_params(a);
   static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(varlen_attn_pair_kernel),
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(varlen_attn_pair_kernel<kPrompt>),
                                 PairCfg::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   const int grid = a.num_sms / kCluster * kCluster;   // whole pairs, one CTA per SM
-  varlen_attn_pair_kernel<<<grid, kThreads, PairCfg::kSmemBytes, stream>>>(mq, mk, mv, p);
+  varlen_attn_pair_kernel<kPrompt><<<grid, kThreads, PairCfg::kSmemBytes, stream>>>(mq, mk, mv, p);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_varlen_attn_pair(const VarlenArgs &a, cudaStream_t stream) {
+  return launch_pair<false>(a, stream);
+}
+cudaError_t launch_prompt_attn_pair(const VarlenArgs &a, cudaStream_t stream) {
+  return launch_pair<true>(a, stream);
 }
 
 }  // namespace pa

@@ -113,7 +113,7 @@ __device__ __forceinline__ void zero_v_tail(uint8_t *tile, int valid, int lane) 
   __syncwarp();
 }
 
-template <int D, int kSlots, int kMaxSeqs>
+template <int D, int kSlots, int kMaxSeqs, bool kPrompt>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
@@ -160,8 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(base + C::kMiscOff, C::kTmemCols);
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
-  sched_build(order, prefix, tmp, tmp + kMaxSeqs, p.cu_q, p.cu_k, p.batch, p.H,
-              kItemRows, p.total_q, p.total_k, p.max_q, p.max_k, p.status, blockIdx.x == 0);
+  item_list<kPrompt>(p, order, prefix, tmp, tmp + kMaxSeqs, blockIdx.x == 0);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -198,8 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++slot_loads;
         return true;
       };
-      for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-        const ItemInfo it = item_info(p, order, prefix, i);
+      for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, blockIdx.x, gridDim.x)) < n_items; ++n) {
+        const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
         if (it.nk == 0) continue;
         const int ntq = it.rows > kTile ? 2 : 1;
         if (!wait_all(bar(C::kQEmpty), (q_loads & 1u) ^ 1u)) {
@@ -218,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++q_loads;
         for (int j = 0; j < it.nk && ok; ++j) {
           const int row = it.k0 + key_tile(it, j) * kTile;
-          ok = load_kv(&tm_k, row, it.head);
-          if (ok) ok = load_kv(&tm_v, row, it.head);
+          ok = load_kv(&tm_k, row, it.kv_head);
+          if (ok) ok = load_kv(&tm_v, row, it.kv_head);
         }
       }
       if (!ok) {
@@ -294,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++turns;
         if (lead) mbar_arrive(bar(C::kTurn + (1 - t)));
       };
-      for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-        const ItemInfo it = item_info(p, order, prefix, i);
+      for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, blockIdx.x, gridDim.x)) < n_items; ++n) {
+        const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
         if (it.nk == 0) continue;
         const bool mine = it.rows > t * kTile;   // this issuer's tile is in the item
         // release a slot / the Q buffer: after this tile's MMAs, or at once
@@ -404,13 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float mul = pos_scale ? sl2 : 1.f;
     uint32_t s_waits = 0, o_waits = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-      const ItemInfo it = item_info(p, order, prefix, i);
+    for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, blockIdx.x, gridDim.x)) < n_items; ++n) {
+      const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
       const int rows_t = it.rows - t * kTile;   // this tile's valid rows (may be <= 0)
       if (rows_t <= 0) continue;                // tile absent: nothing issued for it
       __nv_bfloat16 *dst =
           p.out + (static_cast<int64_t>(it.q_row0 + t * kTile + row) * p.H + it.head) * D;
       const bool store = row < rows_t;
+      // prompts: the keys that this row sees (none: its output is zero)
+      const int row_keys = kPrompt ? min(it.lk, it.seen + t * kTile + row + 1) : it.lk;
       if (it.nk == 0) {
         if (store) {
           uint4 *d4 = reinterpret_cast<uint4 *>(dst);
@@ -445,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kTile / 2; ++c) x[c] = __fmul2_rn(x[c], s2);
         }
-        if (key_tile(it, j) == it.nk - 1) {
-          const int valid = it.lk - (it.nk - 1) * kTile;
+        const int valid = row_keys - key_tile(it, j) * kTile;
+        if (kPrompt ? __any_sync(0xffffffffu, valid < kTile) != 0 : key_tile(it, j) == it.nk - 1) {
 #pragma unroll
           for (int c = 0; c < kTile / 2; ++c) {
             if (2 * c >= valid) x[c].x = -INFINITY;
@@ -533,6 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
+            if (kPrompt && row_keys <= 0) {   // (its sums are NaN)
+              d4[v] = make_uint4(0, 0, 0, 0);
+              continue;
+            }
             w.x = pack_bf16x2(__uint_as_float(r[8 * v + 0]) * inv, __uint_as_float(r[8 * v + 1]) * inv);
             w.y = pack_bf16x2(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
             w.z = pack_bf16x2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
@@ -551,15 +556,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// [rows, H, D] bf16 viewed as a 3-D tensor (D, H, rows); box 64 x 1 x 128
-// with 128-byte swizzle: one 128-row, 64-column half tile per load.
-bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D) {
+// [rows, H, D] bf16 viewed as a 3-D tensor (D, H, rows), rows row_elems
+// elements apart; box 64 x 1 x 128 with 128-byte swizzle: one 128-row, 64-column half tile per load.
+bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t row_elems) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
-                                 static_cast<cuuint64_t>(H) * D * 2};
+                                 static_cast<cuuint64_t>(row_elems) * 2};
   const cuuint32_t box[3] = {64, 1, kTile};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides,
@@ -568,31 +573,20 @@ bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kSlots, int kMaxSeqs>
+template <int D, int kSlots, int kMaxSeqs, bool kPrompt>
 cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
-  if (!make_map(&mq, a.q, a.total_q, a.H, D) || !make_map(&mk, a.k, a.total_k, a.H, D) ||
-      !make_map(&mv, a.v, a.total_k, a.H, D))
+  if (!make_map(&mq, a.q, a.total_q, a.H, D, a.q_stride) ||
+      !make_map(&mk, a.k, a.total_k, a.Hkv, D, a.k_stride) ||
+      !make_map(&mv, a.v, a.total_k, a.Hkv, D, a.v_stride))
     return cudaErrorInvalidValue;
-  VarlenParams p;
-  p.out = static_cast<__nv_bfloat16 *>(a.out);
-  p.cu_q = a.cu_q;
-  p.cu_k = a.cu_k;
-  p.batch = a.batch;
-  p.H = a.H;
-  p.total_q = a.total_q;
-  p.total_k = a.total_k;
-  p.max_q = a.max_q;
-  p.max_k = a.max_k;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.status = a.status;
+  const VarlenParams p = varlen_params(a);
   const int smem = Cfg<D, kSlots, kMaxSeqs>::kSmemBytes;
+  const auto kernel = varlen_attn_tc_kernel<D, kSlots, kMaxSeqs, kPrompt>;
   static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(
-      reinterpret_cast<const void *>(varlen_attn_tc_kernel<D, kSlots, kMaxSeqs>), smem,
-      configured);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), smem, configured);
   if (e != cudaSuccess) return e;
-  varlen_attn_tc_kernel<D, kSlots, kMaxSeqs><<<a.num_sms, kThreads, smem, stream>>>(mq, mk, mv, p);
+  kernel<<<a.num_sms, kThreads, smem, stream>>>(mq, mk, mv, p);
   return cudaGetLastError();
 }
 
@@ -602,7 +596,10 @@ cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
 // ten-slot K/V ring beside a work list of up to PA_MAX_BATCH sequences.
 cudaError_t launch_varlen_attn(const VarlenArgs &a, cudaStream_t stream) {
   if (a.D == 128) return launch_varlen_attn_pair(a, stream);
-  return launch_tc<64, 10, PA_MAX_BATCH>(a, stream);
+  return launch_tc<64, 10, PA_MAX_BATCH, false>(a, stream);
+}
+cudaError_t launch_prompt_attn_tc(const VarlenArgs &a, cudaStream_t stream) {
+  return launch_tc<64, 10, PA_MAX_BATCH, true>(a, stream);
 }
 
 }  // namespace pa

@@ -37,9 +37,18 @@
 // round-robin over the clusters, N-block fastest, so a wave shares x rows and
 // w stays in L2.  Every wait is bounded; a timeout records
 // PA_DEVICE_ERR_TIMEOUT.
+//
+// The same kernel with other epilogues:
+//   kAct    y = residual + act(x w^T + bias)
+//   kGated  y = act(x w_gate^T) * (x w_up^T): the even CTA's half of the w tile
+//           is 128 rows of w_gate and the odd CTA's 128 rows of w_up, so one
+//           accumulator holds both products of 128 columns of y.
+// All of it is fp32, rounded once, and of a row alone, so the rows stay batch
+// invariant.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "activation.cuh"
 #include "internal.h"
 #include "sched.cuh"
 #include "tc_ptx.cuh"
@@ -73,9 +82,14 @@ struct GemmCfg {
 };
 static_assert(GemmCfg::kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
 
+enum GemmMode { kLinear, kAct, kGated };
+
 struct GemmParams {
   const __nv_bfloat16 *bias;  // [N] or nullptr
+  const __nv_bfloat16 *residual;   // [M, N] or nullptr (kAct)
   __nv_bfloat16 *y;           // [M, N]
+  int64_t y_stride, residual_stride;   // elements from one row to the next
+  int act;
   int M, N, K;
   int tiles_n, n_pairs, k_blocks;   // n_pairs: (pair of 128-row blocks, N block)
   int32_t *status;
@@ -83,6 +97,14 @@ struct GemmParams {
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ void add8(float (&f)[8], const __nv_bfloat16 *x) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x));
+  f[0] += bf16_lo(v.x); f[1] += bf16_hi(v.x);
+  f[2] += bf16_lo(v.y); f[3] += bf16_hi(v.y);
+  f[4] += bf16_lo(v.z); f[5] += bf16_hi(v.z);
+  f[6] += bf16_lo(v.w); f[7] += bf16_hi(v.w);
+}
 
 // bounded_wait with cluster-scope acquire, for barriers the other CTA of the
 // pair (or its TMA and MMA completions) arrives on.
@@ -101,10 +123,14 @@ __device__ __forceinline__ bool bounded_wait_cl(uint32_t bar, uint32_t parity,
   }
 }
 
+// tm_w2: w_up (kGated only; tm_w is w_gate).
+template <int kMode>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     linear_bf16_kernel(const __grid_constant__ CUtensorMap tm_x,
-                       const __grid_constant__ CUtensorMap tm_w, const GemmParams p) {
+                       const __grid_constant__ CUtensorMap tm_w,
+                       const __grid_constant__ CUtensorMap tm_w2, const GemmParams p) {
   using C = GemmCfg;
+  constexpr int kYN = kMode == kGated ? kBN / 2 : kBN;   // columns of y per tile
   extern __shared__ uint8_t smem_raw[];
   // 128-byte swizzle atoms need a 1024-byte aligned base.  Both CTAs of a
   // pair run the same code on the same layout, so both skip or neither.
@@ -144,15 +170,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ================= TMA producer (both CTAs) =================
     const bool lead = elect_one();
+    const CUtensorMap *w_map = kMode == kGated && rank == 1 ? &tm_w2 : &tm_w;
     if (lead) {
       tma_prefetch_desc(&tm_x);
-      tma_prefetch_desc(&tm_w);
+      tma_prefetch_desc(w_map);
     }
     uint32_t loads = 0;
     bool ok = true;
     for (int tp = cl; tp < p.n_pairs && ok; tp += n_cl) {
       const int m0 = ((tp / p.tiles_n) * kCluster + rank) * kBM;
-      const int n0 = (tp % p.tiles_n) * kBN + rank * (kBN / kCluster);
+      const int n0 = (tp % p.tiles_n) * kYN + (kMode == kGated ? 0 : rank * (kBN / kCluster));
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         const uint32_t s = loads % kStages, use = loads / kStages;
         const bool w = bounded_wait_cl(bar(C::kEmpty + s), (use & 1u) ^ 1u, abort_flag, p.status);
@@ -165,7 +192,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         if (lead) {
           if (leader) mbar_arrive_expect_tx(bar(C::kFull + s), kCluster * C::kStageBytes);
           tma_load_2d_pair(dst, &tm_x, full, kb * kBK, m0);
-          tma_load_2d_pair(dst + C::kABytes, &tm_w, full, kb * kBK, n0);
+          tma_load_2d_pair(dst + C::kABytes, w_map, full, kb * kBK, n0);
         }
         ++loads;
       }
@@ -250,17 +277,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
       const int m = ((tp / p.tiles_n) * kCluster + rank) * kBM + r;
-      const int n0 = (tp % p.tiles_n) * kBN;
+      const int n0 = (tp % p.tiles_n) * kYN;
       const bool row_ok = m < p.M;
-      __nv_bfloat16 *yrow = p.y + static_cast<int64_t>(row_ok ? m : 0) * p.N;
+      __nv_bfloat16 *yrow = p.y + (row_ok ? m : 0) * p.y_stride;
+      const __nv_bfloat16 *rrow =
+          kMode == kAct && p.residual ? p.residual + (row_ok ? m : 0) * p.residual_stride : nullptr;
+      // 32 columns of y from a0, and 32 more from a1 (kGated: their factors)
 #pragma unroll 1
-      for (int c = 0; c < kBN / 32; c += 2) {
+      for (int c = 0; c < kYN / 32; c += kMode == kGated ? 1 : 2) {
         uint32_t a0[32], a1[32];
         tmem_ld32(lane_base + buf * kBN + c * 32, a0);
-        tmem_ld32(lane_base + buf * kBN + (c + 1) * 32, a1);
+        tmem_ld32(lane_base + buf * kBN + (kMode == kGated ? kYN + c * 32 : (c + 1) * 32), a1);
         tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < (kMode == kGated ? 1 : 2); ++h) {
           const uint32_t *acc = h == 0 ? a0 : a1;
           const int col = n0 + (c + h) * 32;
           if (!row_ok || col >= p.N) continue;
@@ -271,13 +301,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(acc[8 * v + e]);
-            if (p.bias) {
-              const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(p.bias + c8));
-              f[0] += bf16_lo(bv.x); f[1] += bf16_hi(bv.x);
-              f[2] += bf16_lo(bv.y); f[3] += bf16_hi(bv.y);
-              f[4] += bf16_lo(bv.z); f[5] += bf16_hi(bv.z);
-              f[6] += bf16_lo(bv.w); f[7] += bf16_hi(bv.w);
+            if (kMode != kGated && p.bias) add8(f, p.bias + c8);
+            if (kMode != kLinear) activate(f, p.act);
+            if (kMode == kGated) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= __uint_as_float(a1[8 * v + e]);
             }
+            if (kMode == kAct && rrow) add8(f, rrow + c8);
             uint4 o;
             o.x = pack_bf16x2(f[0], f[1]);
             o.y = pack_bf16x2(f[2], f[3]);
@@ -305,20 +335,91 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::kTmemCols);
 }
 
-// [rows, K] bf16 row-major as a 2-D tensor (K, rows); box 64 x box_rows with
-// 128-byte swizzle: one K-block of box_rows rows per load.  Rows and columns
-// past the end read as zero.
-bool make_map_2d(CUtensorMap *map, const void *ptr, int rows, int K, int box_rows) {
+// [rows, K] bf16, rows row_elems apart, as a 2-D tensor (K, rows); box 64 x
+// box_rows with 128-byte swizzle: one K-block of box_rows rows per load.
+// Rows and columns past the end read as zero.
+bool make_map_2d(CUtensorMap *map, const void *ptr, int rows, int K, int64_t row_elems,
+                 int box_rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_elems) * 2};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One call, as the entry points receive it (strides in elements).
+struct GemmArgs {
+  const void *x, *w, *w2, *bias, *residual;
+  void *y;
+  int32_t M, N, K;
+  int64_t x_stride, residual_stride, y_stride;
+  int32_t act;
+};
+
+template <int kMode>
+pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
+  int32_t *status;
+  int sms;
+  cudaError_t e = device_context(&status, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  CUtensorMap mx, mw, mw2;
+  if (!make_map_2d(&mx, a.x, a.M, a.K, a.x_stride, kBM) ||
+      !make_map_2d(&mw, a.w, a.N, a.K, a.K, kBN / kCluster) ||
+      !make_map_2d(&mw2, kMode == kGated ? a.w2 : a.w, a.N, a.K, a.K, kBN / kCluster))
+    return from_cuda(cudaErrorInvalidValue);
+  GemmParams p;
+  p.bias = static_cast<const __nv_bfloat16 *>(a.bias);
+  p.residual = static_cast<const __nv_bfloat16 *>(a.residual);
+  p.y = static_cast<__nv_bfloat16 *>(a.y);
+  p.y_stride = a.y_stride;
+  p.residual_stride = a.residual_stride;
+  p.act = a.act;
+  p.M = a.M;
+  p.N = a.N;
+  p.K = a.K;
+  const int tile_n = kMode == kGated ? kBN / 2 : kBN;
+  p.tiles_n = (a.N - 1) / tile_n + 1;
+  const int64_t m_pairs = (int64_t{a.M} + kCluster * kBM - 1) / (kCluster * kBM);
+  const int64_t pairs = m_pairs * p.tiles_n;
+  if (pairs > 0x3fffffff) return PA_ERR_UNSUPPORTED;
+  p.n_pairs = static_cast<int>(pairs);
+  p.k_blocks = (a.K - 1) / kBK + 1;
+  p.status = status;
+  static unsigned long long configured = 0;
+  e = set_smem_once(reinterpret_cast<const void *>(linear_bf16_kernel<kMode>),
+                    GemmCfg::kSmemBytes, configured);
+  if (e != cudaSuccess) return from_cuda(e);
+  // whole clusters, at most one CTA per SM
+  const int max_ctas = sms / kCluster * kCluster;
+  const int grid = kCluster * p.n_pairs < max_ctas ? kCluster * p.n_pairs : max_ctas;
+  linear_bf16_kernel<kMode><<<grid, kThreads, GemmCfg::kSmemBytes, stream>>>(mx, mw, mw2, p);
+  return from_cuda(cudaGetLastError());
+}
+
+// Largest row stride, in elements (TMA strides are below 2^40 bytes).
+constexpr int64_t kMostStride = int64_t{1} << 38;
+
+// The checks of the entry points with strides (bias, residual: may be null).
+pa_status check_gemm(const GemmArgs &a) {
+  if (a.M < 0 || a.N < 1 || a.K < 1 || a.act < PA_ACT_NONE || a.act > PA_ACT_GELU_TANH)
+    return PA_ERR_INVALID_ARG;
+  if (a.M > 0 && (!a.x || !a.y)) return PA_ERR_INVALID_ARG;
+  if (a.x_stride < a.K || a.y_stride < a.N || (a.residual && a.residual_stride < a.N) ||
+      (a.residual && a.residual == a.y && a.residual_stride != a.y_stride))
+    return PA_ERR_INVALID_ARG;
+  if (a.x_stride > kMostStride || a.y_stride > kMostStride || a.residual_stride > kMostStride)
+    return PA_ERR_UNSUPPORTED;
+  if (((a.K | a.N | a.x_stride | a.y_stride) & 7) != 0 ||
+      (a.residual && (a.residual_stride & 7) != 0) || !aligned_to(a.x, 16) ||
+      !aligned_to(a.w, 16) || !aligned_to(a.w2, 16) || !aligned_to(a.y, 16) ||
+      !aligned_to(a.bias, 16) || !aligned_to(a.residual, 16))
+    return PA_ERR_MISALIGNED;
+  return PA_OK;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -335,34 +436,31 @@ extern "C" pa_status pa_linear_bf16(const void *x, const void *w, const void *bi
   if ((K & 7) != 0 || (N & 7) != 0 || !aligned16(x) || !aligned16(w) || !aligned16(y) ||
       (bias && !aligned16(bias)))
     return PA_ERR_MISALIGNED;
-  int32_t *status;
-  int sms;
-  cudaError_t e = device_context(&status, &sms);
-  if (e != cudaSuccess) return from_cuda(e);
-  CUtensorMap mx, mw;
-  if (!make_map_2d(&mx, x, M, K, kBM) || !make_map_2d(&mw, w, N, K, kBN / kCluster))
-    return from_cuda(cudaErrorInvalidValue);
-  GemmParams p;
-  p.bias = static_cast<const __nv_bfloat16 *>(bias);
-  p.y = static_cast<__nv_bfloat16 *>(y);
-  p.M = M;
-  p.N = N;
-  p.K = K;
-  p.tiles_n = (N + kBN - 1) / kBN;
-  const int64_t m_pairs = ((M + kBM - 1) / kBM + kCluster - 1) / kCluster;
-  const int64_t pairs = m_pairs * p.tiles_n;
-  if (pairs > 0x3fffffff) return PA_ERR_UNSUPPORTED;
-  p.n_pairs = static_cast<int>(pairs);
-  p.k_blocks = (K + kBK - 1) / kBK;
-  p.status = status;
-  static unsigned long long configured = 0;
-  e = set_smem_once(reinterpret_cast<const void *>(linear_bf16_kernel), GemmCfg::kSmemBytes,
-                    configured);
-  if (e != cudaSuccess) return from_cuda(e);
-  // whole clusters, at most one CTA per SM
-  const int max_ctas = sms / kCluster * kCluster;
-  const int grid = kCluster * p.n_pairs < max_ctas ? kCluster * p.n_pairs : max_ctas;
-  linear_bf16_kernel<<<grid, kThreads, GemmCfg::kSmemBytes,
-                       reinterpret_cast<cudaStream_t>(stream)>>>(mx, mw, p);
-  return from_cuda(cudaGetLastError());
+  const GemmArgs a{x, w, nullptr, bias, nullptr, y, M, N, K, K, 0, N, PA_ACT_NONE};
+  return launch_gemm<kLinear>(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" pa_status pa_linear_act_bf16(const void *x, const void *w, const void *bias,
+                                        const void *residual, void *y, int32_t M, int32_t N,
+                                        int32_t K, int64_t x_stride, int64_t residual_stride,
+                                        int64_t y_stride, int32_t act, pa_stream_t stream) {
+  using namespace pa;
+  if (!w) return PA_ERR_INVALID_ARG;
+  const GemmArgs a{x, w, nullptr, bias, residual, y, M, N, K, x_stride, residual_stride, y_stride,
+                   act};
+  const pa_status st = check_gemm(a);
+  if (st != PA_OK || M == 0) return st;
+  return launch_gemm<kAct>(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" pa_status pa_linear_gated_bf16(const void *x, const void *w_gate, const void *w_up,
+                                          void *y, int32_t M, int32_t N, int32_t K,
+                                          int64_t x_stride, int64_t y_stride, int32_t act,
+                                          pa_stream_t stream) {
+  using namespace pa;
+  if (!w_gate || !w_up) return PA_ERR_INVALID_ARG;
+  const GemmArgs a{x, w_gate, w_up, nullptr, nullptr, y, M, N, K, x_stride, 0, y_stride, act};
+  const pa_status st = check_gemm(a);
+  if (st != PA_OK || M == 0) return st;
+  return launch_gemm<kGated>(a, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -57,6 +57,14 @@ __device__ __forceinline__ SeqBounds seq_bounds(const int32_t *__restrict__ cu_q
 // tmp_lq / tmp_lk [batch] are only used during the build (they may alias
 // memory the caller reuses afterwards).  All threads of the CTA call it; it
 // ends with __syncthreads().  Item count = prefix[batch].
+//
+// kLevels: the list of causal attention, where a query tile's work grows with
+// its place in the sequence.  Sequences are sorted by query length, and the
+// items go level by level, the last tiles first: level t holds tile t of every
+// sequence that has one, which are the first s + 1 of the order for t in
+// [T_{s+1}, T_s), T_s the tiles of sequence order[s].  prefix[s] counts the
+// items before that stretch of levels (sched_level_item decodes them).
+template <bool kLevels = false>
 __device__ inline void sched_build(int32_t *order, int32_t *prefix, int32_t *tmp_lq,
                                    int32_t *tmp_lk, const int32_t *__restrict__ cu_q,
                                    const int32_t *__restrict__ cu_k, int batch, int H,
@@ -72,11 +80,12 @@ __device__ inline void sched_build(int32_t *order, int32_t *prefix, int32_t *tmp
   }
   __syncthreads();
   // Rank sort by (key length descending, index ascending).
+  const int32_t *by = kLevels ? tmp_lq : tmp_lk;
   for (int b = tid; b < batch; b += nt) {
-    const int lb = tmp_lk[b];
+    const int lb = by[b];
     int rank = 0;
     for (int j = 0; j < batch; ++j) {
-      const int lj = tmp_lk[j];
+      const int lj = by[j];
       rank += (lj > lb) || (lj == lb && j < b);
     }
     order[rank] = b;
@@ -89,6 +98,10 @@ __device__ inline void sched_build(int32_t *order, int32_t *prefix, int32_t *tmp
       const int idx = base + tid;
       int cnt = 0;
       if (idx < batch) cnt = H * ((tmp_lq[order[idx]] + tile_m - 1) / tile_m);
+      if (kLevels && idx < batch) {   // (the items of this stretch of levels)
+        const int below = idx + 1 < batch ? (tmp_lq[order[idx + 1]] + tile_m - 1) / tile_m : 0;
+        cnt = (cnt - H * below) * (idx + 1);
+      }
       int incl = cnt;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -121,6 +134,27 @@ __device__ __forceinline__ WorkItem sched_item(const int32_t *order, const int32
   w.seq = order[lo];
   w.head = r / ntiles;
   w.tile = r - w.head * ntiles;
+  return w;
+}
+
+// Item i of a list built with kLevels.  Within a level the sequences in order,
+// heads innermost, so that heads which share a K/V head run side by side.
+__device__ __forceinline__ WorkItem sched_level_item(const int32_t *order, const int32_t *prefix,
+                                                     const int32_t *__restrict__ cu_q, int batch,
+                                                     int H, int tile_m, int i) {
+  int lo = 0, hi = batch;  // largest s < batch with prefix[s] <= i: its stretch has items
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= i) lo = mid; else hi = mid;
+  }
+  const int lq = __ldg(cu_q + order[lo] + 1) - __ldg(cu_q + order[lo]);
+  const int per_level = (lo + 1) * H;
+  const int r = i - prefix[lo];
+  const int down = r / per_level, in = r - down * per_level;
+  WorkItem w;
+  w.seq = order[in / H];
+  w.head = in % H;
+  w.tile = (lq + tile_m - 1) / tile_m - 1 - down;
   return w;
 }
 
