@@ -50,6 +50,7 @@
 
 #include "activation.cuh"
 #include "internal.h"
+#include "linear.cuh"
 #include "sched.cuh"
 #include "tc_ptx.cuh"
 #include "tma_map.h"
@@ -59,7 +60,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;   // kBM rows per CTA, kBN columns per pair
+constexpr int kBM = 128, kBN = 256;             // kBM rows per CTA, kBN columns per pair
+constexpr int kBK = kLinearBK;
 constexpr int kStages = 6;
 constexpr int kCluster = 2;                     // the CTA pair of one MMA
 constexpr int kThreads = 192;                   // TMA, MMA, 4 epilogue warps
@@ -82,8 +84,6 @@ struct GemmCfg {
 };
 static_assert(GemmCfg::kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
 
-enum GemmMode { kLinear, kAct, kGated };
-
 struct GemmParams {
   const __nv_bfloat16 *bias;  // [N] or nullptr
   const __nv_bfloat16 *residual;   // [M, N] or nullptr (kAct)
@@ -94,9 +94,6 @@ struct GemmParams {
   int tiles_n, n_pairs, k_blocks;   // n_pairs: (pair of 128-row blocks, N block)
   int32_t *status;
 };
-
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 __device__ __forceinline__ void add8(float (&f)[8], const __nv_bfloat16 *x) {
   const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x));
@@ -335,32 +332,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, C::kTmemCols);
 }
 
-// [rows, K] bf16, rows row_elems apart, as a 2-D tensor (K, rows); box 64 x
-// box_rows with 128-byte swizzle: one K-block of box_rows rows per load.
-// Rows and columns past the end read as zero.
-bool make_map_2d(CUtensorMap *map, const void *ptr, int rows, int K, int64_t row_elems,
-                 int box_rows) {
-  EncodeTiledFn enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_elems) * 2};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// One call, as the entry points receive it (strides in elements).
-struct GemmArgs {
-  const void *x, *w, *w2, *bias, *residual;
-  void *y;
-  int32_t M, N, K;
-  int64_t x_stride, residual_stride, y_stride;
-  int32_t act;
-};
-
 template <int kMode>
 pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
   int32_t *status;
@@ -422,6 +393,15 @@ pa_status check_gemm(const GemmArgs &a) {
   return PA_OK;
 }
 
+template <int kMode>
+pa_status linear_call(const GemmArgs &a, cudaStream_t stream) {
+  pa_status st = check_gemm(a);
+  if (st != PA_OK || a.M == 0) return st;
+  bool taken = false;
+  st = launch_linear_few(a, kMode, taken, stream);
+  return taken ? st : launch_gemm<kMode>(a, stream);
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -448,9 +428,7 @@ extern "C" pa_status pa_linear_act_bf16(const void *x, const void *w, const void
   if (!w) return PA_ERR_INVALID_ARG;
   const GemmArgs a{x, w, nullptr, bias, residual, y, M, N, K, x_stride, residual_stride, y_stride,
                    act};
-  const pa_status st = check_gemm(a);
-  if (st != PA_OK || M == 0) return st;
-  return launch_gemm<kAct>(a, reinterpret_cast<cudaStream_t>(stream));
+  return linear_call<kAct>(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" pa_status pa_linear_gated_bf16(const void *x, const void *w_gate, const void *w_up,
@@ -460,7 +438,5 @@ extern "C" pa_status pa_linear_gated_bf16(const void *x, const void *w_gate, con
   using namespace pa;
   if (!w_gate || !w_up) return PA_ERR_INVALID_ARG;
   const GemmArgs a{x, w_gate, w_up, nullptr, nullptr, y, M, N, K, x_stride, 0, y_stride, act};
-  const pa_status st = check_gemm(a);
-  if (st != PA_OK || M == 0) return st;
-  return launch_gemm<kGated>(a, reinterpret_cast<cudaStream_t>(stream));
+  return linear_call<kGated>(a, reinterpret_cast<cudaStream_t>(stream));
 }

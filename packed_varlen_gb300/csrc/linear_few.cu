@@ -1,0 +1,279 @@
+// The linear layers with an epilogue (gemm_tc.cu) for few rows: a step of single
+// tokens, a short prompt.
+//
+// Few rows are bound by w's bytes (2 N K of them for 2 M N K operations), so the
+// work is split over the features, finely enough that every SM streams a part
+// of w: a CTA computes F features (a multiple of 8, at most 128) of up to 256 rows
+// of x.  The product is turned around: w is the MMA's A operand, its rows
+// the accumulator's TMEM lanes, and x is B, its rows the columns, so
+// a call of 13 rows pays for 16 columns and not for a tile of 128 rows.  An MMA
+// has 64 or 128 rows; where F is less, the rows of shared memory past F hold
+// anything, and what they give in the lanes past F is never read.
+//
+// An element's products are added in the same order as in the large kernel (K
+// in steps of 16, one accumulator, no split over K), and the epilogue is the
+// same arithmetic, so rows come out with the same bits by either.
+//
+//   warp 0      TMA producer: groups of K-blocks of w and x into a ring
+//   warp 1      allocates TMEM, issues the MMAs
+//   warps 2-5   epilogue, a lane a feature: bias, activation, residual (read ahead of
+//               the accumulator's end), columns of y as runs of 32 features
+// Every wait is bounded; a timeout records PA_DEVICE_ERR_TIMEOUT.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "activation.cuh"
+#include "internal.h"
+#include "linear.cuh"
+#include "sched.cuh"
+#include "tc_ptx.cuh"
+#include "tma_map.h"
+
+namespace pa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 192;
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 220 * 1024;          // stages, at most
+constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
+constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
+constexpr int kRowBytes = kLinearBK * 2;        // of a K-block: 128
+constexpr int kChunk = 16;                      // columns the epilogue takes at once
+
+// Shared memory: full and empty barriers, the accumulator's, TMEM address and
+// abort flag; then the ring on 1024 bytes.
+constexpr int kBarBytes = (2 * kMaxStages + 1) * 8;
+constexpr int kMiscOff = kBarBytes;
+constexpr int kRingOff = 1024;
+static_assert(kMiscOff + 8 <= kRingOff && kRingOff + kRingBytes <= 232448, "shared memory plan");
+
+struct FewParams {
+  const __nv_bfloat16 *bias;       // [N] or nullptr
+  const __nv_bfloat16 *residual;   // or nullptr
+  __nv_bfloat16 *y;
+  int64_t y_stride, residual_stride;
+  int act;
+  int M, N, K;
+  int features, rows;              // of a CTA: F, and columns of its accumulator
+  int k_blocks, group, stages;     // K-blocks, those of a stage
+  int stage_bytes;
+  uint32_t idesc, tmem_cols;
+  int32_t *status;
+};
+
+// kM: rows of an MMA, at least the features of a CTA.
+template <int kMode, int kM>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tm_x,
+                      const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_w2, const FewParams p) {
+  constexpr int kParts = kMode == kGated ? 2 : 1;   // weights, accumulators
+  constexpr int kABytes = kM * kRowBytes;           // a K-block of one weight
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  if (base & 1023u) {   // swizzle atoms need a 1024-byte aligned base
+    if (threadIdx.x == 0) record_error(p.status, PA_DEVICE_ERR_SMEM_ALIGN);
+    return;
+  }
+  auto full = [&](uint32_t s) -> uint32_t { return base + 8u * s; };
+  auto empty = [&](uint32_t s) -> uint32_t { return base + 8u * (kMaxStages + s); };
+  const uint32_t acc_full = base + 8u * (2 * kMaxStages);
+  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem_raw + kMiscOff);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem_raw + kMiscOff + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n0 = blockIdx.x * p.features, m0 = blockIdx.y * p.rows;
+  const int b_bytes = p.rows * kRowBytes;
+  const int n_stages = (p.k_blocks + p.group - 1) / p.group;   // filled in all
+
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(base + kMiscOff, p.tmem_cols);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_ptr;
+
+  if (warp == 0) {
+    const bool lead = elect_one();
+    if (lead) {
+      tma_prefetch_desc(&tm_x);
+      tma_prefetch_desc(&tm_w);
+      if (kMode == kGated) tma_prefetch_desc(&tm_w2);
+    }
+    bool ok = true;
+    int i = 0;
+    for (; i < n_stages; ++i) {
+      const uint32_t s = i % p.stages;
+      ok = bounded_wait(empty(s), ((i / p.stages) & 1u) ^ 1u, abort_flag, p.status, kWaitLimit);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int kb0 = i * p.group, blocks = min(p.group, p.k_blocks - kb0);
+      const uint32_t dst = base + kRingOff + s * p.stage_bytes;
+      if (lead) {
+        mbar_arrive_expect_tx(full(s), blocks * (kParts * p.features * kRowBytes + b_bytes));
+        for (int b = 0; b < blocks; ++b) {
+          const uint32_t a = dst + b * (kParts * kABytes + b_bytes);
+          const int k = (kb0 + b) * kLinearBK;
+          tma_load_2d(a, &tm_w, full(s), k, n0);
+          if (kMode == kGated) tma_load_2d(a + kABytes, &tm_w2, full(s), k, n0);
+          tma_load_2d(a + kParts * kABytes, &tm_x, full(s), k, m0);
+        }
+      }
+    }
+    if (!ok) {   // give the copies already issued a bounded chance to land
+      for (int s = 0; s < p.stages && s < i; ++s)
+        drain_wait(full(s), ((i - s + p.stages - 1) / p.stages - 1) & 1u, kDrainLimit);
+    }
+  } else if (warp == 1) {
+    const bool lead = elect_one();
+    const uint64_t desc0 = sdesc_sw128(base + kRingOff, 16, 1024);
+    bool ok = true;
+    int i = 0;
+    for (; i < n_stages; ++i) {
+      const uint32_t s = i % p.stages;
+      ok = bounded_wait(full(s), (i / p.stages) & 1u, abort_flag, p.status, kWaitLimit);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int blocks = min(p.group, p.k_blocks - i * p.group);
+      for (int b = 0; b < blocks; ++b) {
+        const uint32_t off = s * p.stage_bytes + b * (kParts * kABytes + b_bytes);
+        const uint64_t a = desc0 + (off >> 4), x = desc0 + ((off + kParts * kABytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kLinearBK / 16; ++kk)
+          if (lead) {
+            const uint32_t more = (i > 0 || b > 0 || kk > 0) ? 1u : 0u;
+            mma_ss(tmem, a + kk * 2, x + kk * 2, p.idesc, more);
+            if (kMode == kGated)
+              mma_ss(tmem + p.rows, a + (kABytes >> 4) + kk * 2, x + kk * 2, p.idesc, more);
+          }
+      }
+      if (lead) mma_commit(empty(s));
+    }
+    if (lead) mma_commit(acc_full);   // every MMA issued so far is done
+    if (!ok) drain_wait(acc_full, 0, kWaitLimit);
+    __syncwarp();
+  } else {
+    const int quad = warp & 3;
+    // accumulator rows: 32 a quadrant, or (an MMA of 64 rows) its first 16 lanes
+    const int f = kM == 128 ? quad * 32 + lane : quad * 16 + lane;
+    const int n = n0 + f;
+    const bool mine = (kM == 128 || lane < 16) && f < p.features && n < p.N;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int rows = min(p.rows, p.M - m0);
+    float bias = 0.f;
+    if (kMode == kAct && p.bias && mine) bias = __bfloat162float(p.bias[n]);
+    __nv_bfloat16 *y = p.y + m0 * p.y_stride + n;
+    const bool add = kMode == kAct && p.residual != nullptr && mine;
+    const __nv_bfloat16 *res = p.residual + m0 * p.residual_stride + n;
+    __nv_bfloat16 r[kChunk];
+    auto read_ahead = [&](int c) {
+      if (!add) return;
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e)
+        if (c + e < rows) r[e] = res[(c + e) * p.residual_stride];
+    };
+    read_ahead(0);
+    const bool ok = bounded_wait(acc_full, 0, abort_flag, p.status, kWaitLimit);
+    if (__all_sync(0xffffffffu, ok) && *abort_flag == 0) {
+      fence_after_sync();
+      for (int c = 0; c < rows; c += kChunk) {
+        uint32_t a[kChunk], u[kChunk];
+        tmem_ld8(acc + c, a);
+        tmem_ld8(acc + c + 8, a + 8);
+        if (kMode == kGated) {
+          tmem_ld8(acc + p.rows + c, u);
+          tmem_ld8(acc + p.rows + c + 8, u + 8);
+        }
+        tmem_wait_ld();
+        float v[kChunk];
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) v[e] = __uint_as_float(a[e]) + (kMode == kAct ? bias : 0.f);
+        activate(v, p.act);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+          if (kMode == kGated) v[e] *= __uint_as_float(u[e]);
+          if (add && c + e < rows) v[e] += __bfloat162float(r[e]);
+        }
+        if (c + kChunk < rows) read_ahead(c + kChunk);
+        if (mine) {
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e)
+            if (c + e < rows) y[(c + e) * p.y_stride] = __float2bfloat16_rn(v[e]);
+        }
+      }
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+}
+
+int round_up(int x, int to) { return (x + to - 1) / to * to; }
+
+template <int kMode, int kM>
+pa_status launch(const GemmArgs &a, FewParams &p, cudaStream_t stream) {
+  CUtensorMap mx, mw, mw2;
+  if (!make_map_2d(&mx, a.x, a.M, a.K, a.x_stride, p.rows) ||
+      !make_map_2d(&mw, a.w, a.N, a.K, a.K, p.features) ||
+      !make_map_2d(&mw2, kMode == kGated ? a.w2 : a.w, a.N, a.K, a.K, p.features))
+    return from_cuda(cudaErrorInvalidValue);
+  const int block = (kMode == kGated ? 2 : 1) * kM * kRowBytes + p.rows * kRowBytes;
+  p.idesc = idesc_bf16_f32(kM, p.rows, false);
+  // stages of about 32 KB, so that a barrier stands for several copies and MMAs
+  p.group = 32768 / block > 1 ? 32768 / block : 1;
+  if (p.group > p.k_blocks) p.group = p.k_blocks;
+  p.stage_bytes = p.group * block;
+  p.stages = kRingBytes / p.stage_bytes < kMaxStages ? kRingBytes / p.stage_bytes : kMaxStages;
+  static unsigned long long configured = 0;
+  const auto kernel = linear_few_kernel<kMode, kM>;
+  const cudaError_t e =
+      set_smem_once(reinterpret_cast<const void *>(kernel), kRingOff + kRingBytes, configured);
+  if (e != cudaSuccess) return from_cuda(e);
+  const dim3 grid((a.N + p.features - 1) / p.features, (a.M + p.rows - 1) / p.rows);
+  kernel<<<grid, kThreads, kRingOff + kRingBytes, stream>>>(mx, mw, mw2, p);
+  return from_cuda(cudaGetLastError());
+}
+
+}  // namespace
+
+pa_status launch_linear_few(const GemmArgs &a, int mode, bool &taken, cudaStream_t stream) {
+  taken = a.M <= 128;
+  if (!taken) return PA_OK;
+  FewParams p;
+  int sms;
+  const cudaError_t e = device_context(&p.status, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  p.bias = static_cast<const __nv_bfloat16 *>(a.bias);
+  p.residual = static_cast<const __nv_bfloat16 *>(a.residual);
+  p.y = static_cast<__nv_bfloat16 *>(a.y);
+  p.y_stride = a.y_stride;
+  p.residual_stride = a.residual_stride;
+  p.act = a.act;
+  p.M = a.M;
+  p.N = a.N;
+  p.K = a.K;
+  p.k_blocks = (a.K - 1) / kLinearBK + 1;
+  p.rows = round_up(a.M, 16);
+  // as few features as fill the SMs, in as few rounds as 128 of them allow
+  const int rounds = (a.N - 1) / (128 * sms) + 1;
+  p.features = round_up((a.N - 1) / (rounds * sms) + 1, 8);
+  const int cols = (mode == kGated ? 2 : 1) * p.rows;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < static_cast<uint32_t>(cols)) p.tmem_cols *= 2;
+  if (mode == kGated)
+    return p.features <= 64 ? launch<kGated, 64>(a, p, stream) : launch<kGated, 128>(a, p, stream);
+  return p.features <= 64 ? launch<kAct, 64>(a, p, stream) : launch<kAct, 128>(a, p, stream);
+}
+
+}  // namespace pa
