@@ -28,14 +28,19 @@
 //               in the even CTA it issues the MMAs into one of two TMEM
 //               accumulators (2 x 256 fp32 columns) and frees each ring slot
 //               in both CTAs with one commit per CTA.
-//   warps 2-5   drain a finished accumulator (each warp its TMEM lane
-//               quadrant), add the bias, round to bf16 and store, while the
-//               MMA warp fills the other; each warp then reports the
-//               accumulator free on the even CTA's barrier.
+//   warps 2-9   drain a finished accumulator (two warps to a TMEM lane
+//               quadrant, half the columns each), add the bias, round to bf16
+//               and store, while the MMA warp fills the other; each warp then
+//               reports the accumulator free on the even CTA's barrier.  A
+//               warp's 32 rows x 64 columns go through 4 KB of shared memory
+//               that copies fill with the residual, ahead of the accumulator,
+//               and write out as y: a lane has a row of its own, and rows stored
+//               by lanes would be 32 separate pieces of 16 bytes a time.
 // Warps 0 and 1 run their loops warp-wide and one elected lane issues each
 // copy, MMA and commit, so MMA operands are warp-uniform.  Tile pairs go
-// round-robin over the clusters, N-block fastest, so a wave shares x rows and
-// w stays in L2.  Every wait is bounded; a timeout records
+// round-robin over the clusters, in groups of kGroupM row blocks with the row
+// block fastest: a wave of 76 pairs then spans about 8 x 10 tiles and reads the
+// fewest rows of x and w.  Every wait is bounded; a timeout records
 // PA_DEVICE_ERR_TIMEOUT.
 //
 // The same kernel with other epilogues:
@@ -64,7 +69,9 @@ constexpr int kBM = 128, kBN = 256;             // kBM rows per CTA, kBN columns
 constexpr int kBK = kLinearBK;
 constexpr int kStages = 6;
 constexpr int kCluster = 2;                     // the CTA pair of one MMA
-constexpr int kThreads = 192;                   // TMA, MMA, 4 epilogue warps
+constexpr int kThreads = 320;                   // TMA, MMA, 8 epilogue warps
+constexpr int kGroupM = 8;                      // row blocks (of a pair) of a group
+constexpr int kOutN = 64, kOutBytes = 32 * kOutN * 2;   // a warp's part of y in shared memory
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 
@@ -72,10 +79,12 @@ struct GemmCfg {
   static constexpr int kABytes = kBM * kBK * 2;                // 16 KB: 128 x rows x 128 B
   static constexpr int kBBytes = (kBN / kCluster) * kBK * 2;   // 16 KB: 128 w rows x 128 B
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kOutOff = kStages * kStageBytes;        // 8 epilogue warps' buffers
+  static constexpr int kBarOff = kOutOff + 8 * kOutBytes;
   static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages,
-                       kAccEmpty = 2 * kStages + 2, kFinal = 2 * kStages + 4;
-  static constexpr int kNumBars = 2 * kStages + 5;
+                       kAccEmpty = 2 * kStages + 2, kFinal = 2 * kStages + 4,
+                       kResidual = 2 * kStages + 5;   // an epilogue warp's residual landed
+  static constexpr int kNumBars = 2 * kStages + 13;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base, abort flag
   static constexpr int kSmemBytes = kMiscOff + 16;
   static constexpr uint32_t kTmemCols = 2 * kBN;
@@ -86,46 +95,43 @@ static_assert(GemmCfg::kSmemBytes <= 232448, "shared memory plan exceeds the per
 
 struct GemmParams {
   const __nv_bfloat16 *bias;  // [N] or nullptr
-  const __nv_bfloat16 *residual;   // [M, N] or nullptr (kAct)
-  __nv_bfloat16 *y;           // [M, N]
-  int64_t y_stride, residual_stride;   // elements from one row to the next
+  int residual;               // add the residual (kAct)
   int act;
   int M, N, K;
-  int tiles_n, n_pairs, k_blocks;   // n_pairs: (pair of 128-row blocks, N block)
+  int tiles_m, tiles_n, n_pairs, k_blocks;   // n_pairs: (pair of 128-row blocks, N block)
   int32_t *status;
 };
 
-__device__ __forceinline__ void add8(float (&f)[8], const __nv_bfloat16 *x) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x));
+__device__ __forceinline__ void add8(float (&f)[8], const uint4 &v) {
   f[0] += bf16_lo(v.x); f[1] += bf16_hi(v.x);
   f[2] += bf16_lo(v.y); f[3] += bf16_hi(v.y);
   f[4] += bf16_lo(v.z); f[5] += bf16_hi(v.z);
   f[6] += bf16_lo(v.w); f[7] += bf16_hi(v.w);
 }
 
-// bounded_wait with cluster-scope acquire, for barriers the other CTA of the
-// pair (or its TMA and MMA completions) arrives on.
-__device__ __forceinline__ bool bounded_wait_cl(uint32_t bar, uint32_t parity,
-                                                volatile int32_t *abort_flag, int32_t *status) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitLimit) {
-      *abort_flag = 1;
-      record_error(status, PA_DEVICE_ERR_TIMEOUT);
-      return false;
-    }
-  }
+// Tile pair tp -> its pair of 128-row blocks and its N block.
+struct TilePair {
+  int m, n;
+};
+__device__ __forceinline__ TilePair tile_pair(const GemmParams &p, int tp) {
+  const int per_group = kGroupM * p.tiles_n;
+  const int g = tp / per_group, r = tp - g * per_group;
+  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
+  TilePair t;
+  t.n = r / rows;
+  t.m = g * kGroupM + r - t.n * rows;
+  return t;
 }
 
-// tm_w2: w_up (kGated only; tm_w is w_gate).
+// tm_w2: w_up (kGated only; tm_w is w_gate).  tm_r, tm_y: residual and y, in
+// boxes of 32 rows x 64 columns.
 template <int kMode>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     linear_bf16_kernel(const __grid_constant__ CUtensorMap tm_x,
                        const __grid_constant__ CUtensorMap tm_w,
-                       const __grid_constant__ CUtensorMap tm_w2, const GemmParams p) {
+                       const __grid_constant__ CUtensorMap tm_w2,
+                       const __grid_constant__ CUtensorMap tm_r,
+                       const __grid_constant__ CUtensorMap tm_y, const GemmParams p) {
   using C = GemmCfg;
   constexpr int kYN = kMode == kGated ? kBN / 2 : kBN;   // columns of y per tile
   extern __shared__ uint8_t smem_raw[];
@@ -150,8 +156,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(C::kAccFull + b), 1);
-      mbar_init(bar(C::kAccEmpty + b), 4 * kCluster);   // every epilogue warp of the pair
+      mbar_init(bar(C::kAccEmpty + b), 8 * kCluster);   // every epilogue warp of the pair
     }
+    for (int w = 0; w < 8; ++w) mbar_init(bar(C::kResidual + w), 1);
     mbar_init(bar(C::kFinal), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -175,11 +182,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t loads = 0;
     bool ok = true;
     for (int tp = cl; tp < p.n_pairs && ok; tp += n_cl) {
-      const int m0 = ((tp / p.tiles_n) * kCluster + rank) * kBM;
-      const int n0 = (tp % p.tiles_n) * kYN + (kMode == kGated ? 0 : rank * (kBN / kCluster));
+      const TilePair t = tile_pair(p, tp);
+      const int m0 = (t.m * kCluster + rank) * kBM;
+      const int n0 = t.n * kYN + (kMode == kGated ? 0 : rank * (kBN / kCluster));
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         const uint32_t s = loads % kStages, use = loads / kStages;
-        const bool w = bounded_wait_cl(bar(C::kEmpty + s), (use & 1u) ^ 1u, abort_flag, p.status);
+        const bool w = bounded_wait_cluster(bar(C::kEmpty + s), (use & 1u) ^ 1u, abort_flag,
+                                            p.status, kWaitLimit);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -210,7 +219,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     if (leader) {
       const bool lead = elect_one();
       auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
-        const bool w = bounded_wait_cl(b, parity, abort_flag, p.status);
+        const bool w = bounded_wait_cluster(b, parity, abort_flag, p.status, kWaitLimit);
         return __all_sync(0xffffffffu, w);
       };
       // commit to the same barrier in both CTAs of the pair
@@ -262,64 +271,103 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ================= epilogue: warps 2..5, TMEM lane quadrant warp % 4 =========
-    const int quad = warp & 3;
-    const int r = quad * 32 + lane;
+    // ================= epilogue: warps 2..9, TMEM lane quadrant warp % 4 =========
+    constexpr int kParts = kYN / 2 / kOutN;   // parts of 64 columns of a warp
+    const int quad = warp & 3, side = (warp - 2) >> 2;
+    const bool lead = elect_one();
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t acc_empty0 = mapa_shared(bar(C::kAccEmpty), 0);   // the leader's
-    uint32_t tiles_done = 0;
+    const uint32_t out = base + C::kOutOff + (warp - 2) * kOutBytes;
+    // this lane's row; the 128-byte swizzle permutes the 16-byte pieces of a row
+    uint8_t *row = smem_raw + C::kOutOff + (warp - 2) * kOutBytes + lane * 128;
+    const uint32_t landed = bar(C::kResidual + warp - 2);
+    const bool add = kMode == kAct && p.residual;
+    uint32_t tiles_done = 0, loads = 0, taken = 0;
+    // part `part` of tile pair tp, if it has any of y
+    int m0 = 0, c0 = 0;
+    auto seek = [&](int tp, int part) -> bool {
+      const TilePair t = tile_pair(p, tp);
+      m0 = (t.m * kCluster + rank) * kBM + quad * 32;
+      c0 = t.n * kYN + (side * kParts + part) * kOutN;
+      return m0 < p.M && c0 < p.N;
+    };
+    // the residual of a part into the buffer, which the part before it has left
+    auto load_residual = [&](int tp, int part) {
+      if (!add || tp >= p.n_pairs || !seek(tp, part)) return;
+      if (lead) {
+        mbar_arrive_expect_tx(landed, kOutBytes);
+        tma_load_2d(out, &tm_r, landed, c0, m0);
+      }
+      ++loads;
+    };
+    load_residual(cl, 0);
     for (int tp = cl; tp < p.n_pairs; tp += n_cl, ++tiles_done) {
       const uint32_t buf = tiles_done & 1u, buse = tiles_done >> 1;
-      const bool ok = bounded_wait_cl(bar(C::kAccFull + buf), buse & 1u, abort_flag, p.status);
+      const bool ok = bounded_wait_cluster(bar(C::kAccFull + buf), buse & 1u, abort_flag, p.status,
+                                           kWaitLimit);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
-      const int m = ((tp / p.tiles_n) * kCluster + rank) * kBM + r;
-      const int n0 = (tp % p.tiles_n) * kYN;
-      const bool row_ok = m < p.M;
-      __nv_bfloat16 *yrow = p.y + (row_ok ? m : 0) * p.y_stride;
-      const __nv_bfloat16 *rrow =
-          kMode == kAct && p.residual ? p.residual + (row_ok ? m : 0) * p.residual_stride : nullptr;
-      // 32 columns of y from a0, and 32 more from a1 (kGated: their factors)
+      bool landed_ok = true;
 #pragma unroll 1
-      for (int c = 0; c < kYN / 32; c += kMode == kGated ? 1 : 2) {
-        uint32_t a0[32], a1[32];
-        tmem_ld32(lane_base + buf * kBN + c * 32, a0);
-        tmem_ld32(lane_base + buf * kBN + (kMode == kGated ? kYN + c * 32 : (c + 1) * 32), a1);
-        tmem_wait_ld();
+      for (int part = 0; part < kParts; ++part) {
+        const bool here = seek(tp, part);
+        if (here && add) {
+          landed_ok = bounded_wait(landed, taken & 1u, abort_flag, p.status, kWaitLimit);
+          if (!__all_sync(0xffffffffu, landed_ok)) {
+            landed_ok = false;
+            break;
+          }
+          ++taken;
+        }
+        const uint32_t acc = lane_base + buf * kBN + (side * kParts + part) * kOutN;
 #pragma unroll
-        for (int h = 0; h < (kMode == kGated ? 1 : 2); ++h) {
-          const uint32_t *acc = h == 0 ? a0 : a1;
-          const int col = n0 + (c + h) * 32;
-          if (!row_ok || col >= p.N) continue;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a0[32], a1[32];
+          tmem_ld32(acc + h * 32, a0);
+          if (kMode == kGated) tmem_ld32(acc + kYN + h * 32, a1);
+          tmem_wait_ld();
+          if (!here) continue;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int c8 = col + 8 * v;
-            if (c8 >= p.N) break;   // N is a multiple of 8
+            uint4 *piece = reinterpret_cast<uint4 *>(row + (((h * 4 + v) ^ (lane & 7)) << 4));
+            const int c8 = c0 + h * 32 + 8 * v;
             float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(acc[8 * v + e]);
-            if (kMode != kGated && p.bias) add8(f, p.bias + c8);
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(a0[8 * v + e]);
+            if (kMode != kGated && p.bias && c8 < p.N)   // N is a multiple of 8
+              add8(f, __ldg(reinterpret_cast<const uint4 *>(p.bias + c8)));
             if (kMode != kLinear) activate(f, p.act);
             if (kMode == kGated) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) f[e] *= __uint_as_float(a1[8 * v + e]);
             }
-            if (kMode == kAct && rrow) add8(f, rrow + c8);
-            uint4 o;
-            o.x = pack_bf16x2(f[0], f[1]);
-            o.y = pack_bf16x2(f[2], f[3]);
-            o.z = pack_bf16x2(f[4], f[5]);
-            o.w = pack_bf16x2(f[6], f[7]);
-            *reinterpret_cast<uint4 *>(yrow + c8) = o;
+            if (add) add8(f, *piece);
+            *piece = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
           }
         }
+        if (part == kParts - 1) {
+          // every lane's TMEM reads are done; one arrival per warp on the
+          // leader's barrier lets the MMA warp refill this accumulator
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(acc_empty0 + 8u * buf);
+        }
+        if (here) {
+          fence_proxy_async();   // each lane's row, before the copy reads it
+          __syncwarp();
+          if (lead) {
+            tma_store_2d(&tm_y, out, c0, m0);
+            bulk_commit();
+            bulk_wait_read();    // the buffer is free again
+          }
+          __syncwarp();
+        }
+        load_residual(part + 1 < kParts ? tp : tp + n_cl, part + 1 < kParts ? part + 1 : 0);
       }
-      // every lane's TMEM reads are done; one arrival per warp on the
-      // leader's barrier lets the MMA warp refill this accumulator
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(acc_empty0 + 8u * buf);
+      if (!landed_ok) break;
     }
+    if (taken != loads) drain_wait(landed, taken & 1u, kDrainLimit);   // after an abort
   }
 
   // ---- teardown -------------------------------------------------------------
@@ -338,25 +386,25 @@ pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
   int sms;
   cudaError_t e = device_context(&status, &sms);
   if (e != cudaSuccess) return from_cuda(e);
-  CUtensorMap mx, mw, mw2;
+  CUtensorMap mx, mw, mw2, mr, my;
   if (!make_map_2d(&mx, a.x, a.M, a.K, a.x_stride, kBM) ||
       !make_map_2d(&mw, a.w, a.N, a.K, a.K, kBN / kCluster) ||
-      !make_map_2d(&mw2, kMode == kGated ? a.w2 : a.w, a.N, a.K, a.K, kBN / kCluster))
+      !make_map_2d(&mw2, kMode == kGated ? a.w2 : a.w, a.N, a.K, a.K, kBN / kCluster) ||
+      !make_map_2d(&mr, a.residual ? a.residual : a.y, a.M, a.N,
+                   a.residual ? a.residual_stride : a.y_stride, 32) ||
+      !make_map_2d(&my, a.y, a.M, a.N, a.y_stride, 32))
     return from_cuda(cudaErrorInvalidValue);
   GemmParams p;
   p.bias = static_cast<const __nv_bfloat16 *>(a.bias);
-  p.residual = static_cast<const __nv_bfloat16 *>(a.residual);
-  p.y = static_cast<__nv_bfloat16 *>(a.y);
-  p.y_stride = a.y_stride;
-  p.residual_stride = a.residual_stride;
+  p.residual = a.residual != nullptr;
   p.act = a.act;
   p.M = a.M;
   p.N = a.N;
   p.K = a.K;
   const int tile_n = kMode == kGated ? kBN / 2 : kBN;
   p.tiles_n = (a.N - 1) / tile_n + 1;
-  const int64_t m_pairs = (int64_t{a.M} + kCluster * kBM - 1) / (kCluster * kBM);
-  const int64_t pairs = m_pairs * p.tiles_n;
+  p.tiles_m = (a.M - 1) / (kCluster * kBM) + 1;
+  const int64_t pairs = int64_t{p.tiles_m} * p.tiles_n;
   if (pairs > 0x3fffffff) return PA_ERR_UNSUPPORTED;
   p.n_pairs = static_cast<int>(pairs);
   p.k_blocks = (a.K - 1) / kBK + 1;
@@ -368,7 +416,8 @@ pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
   // whole clusters, at most one CTA per SM
   const int max_ctas = sms / kCluster * kCluster;
   const int grid = kCluster * p.n_pairs < max_ctas ? kCluster * p.n_pairs : max_ctas;
-  linear_bf16_kernel<kMode><<<grid, kThreads, GemmCfg::kSmemBytes, stream>>>(mx, mw, mw2, p);
+  linear_bf16_kernel<kMode><<<grid, kThreads, GemmCfg::kSmemBytes, stream>>>(mx, mw, mw2, mr, my,
+                                                                               p);
   return from_cuda(cudaGetLastError());
 }
 
