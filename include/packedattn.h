@@ -136,8 +136,8 @@ pa_status pa_varlen_attn_fwd(const void *q, const void *k, const void *v, void *
  * batch in [1, PA_MAX_BATCH]; total_q, total_k >= cu[batch] and at most 2^30
  * (total_q = 0 or max_q = 0 does nothing; q and out, k and v may be NULL where
  * their total is 0); max_q / max_k bound every length; Hq a multiple of Hkv
- * and at most 65535; (total_q / 256 + batch) * Hq at most 2^30; D in
- * {64, 128}; scale and scale * log2(e) finite.
+ * and at most 65535, Hq / Hkv <= 128; (total_q * Hq / 128 + batch * Hkv at most
+ * 2^30); D in {64, 128}; scale and scale * log2(e) finite.
  * Rows outside a sequence never reach its result, whatever their bits.  A key
  * that causal order hides from a query has weight zero there; a NaN or infinity
  * in its V row can still reach that query as 0 * NaN (in its K row it cannot).

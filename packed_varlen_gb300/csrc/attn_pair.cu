@@ -7,8 +7,10 @@
 // batching for heterogeneous diffusion requests", AttentionMetadata).
 //
 // Design: persistent CTAs in clusters of two.  A work item is 256 query rows
-// of one (sequence, head); the even CTA of the pair holds rows 0-127 and the
-// odd CTA rows 128-255, and every MMA spans the pair (M = 256):
+// of one (sequence, K/V head), its group's heads of 256 / G tokens
+// (varlen_items.cuh; G = 1 for pa_varlen_attn_fwd); the even CTA of the pair
+// holds rows 0-127 and the odd CTA rows 128-255, and every MMA spans the pair
+// (M = 256):
 //   S = Q K^T   each CTA holds its Q tile and one 64-key half of the K tile
 //               (keys 0-63 in the even CTA, 64-127 in the odd one);
 //   O += P V    P comes from each CTA's own TMEM, and each CTA holds one
@@ -54,11 +56,10 @@ namespace {
 using namespace tc;
 
 constexpr int kD = 128;
-constexpr int kTile = kVarlenTile;          // query rows per CTA, keys per key tile
-constexpr int kItemRows = kVarlenItemRows;  // query rows per work item (one pair)
+constexpr int kTile = kVarlenTile;  // query rows per CTA, keys per key tile
 constexpr int kCluster = 2;
 constexpr int kSBufs = 3;           // S/P buffers in TMEM
-constexpr int kThreads = 320;       // producer, MMA issuer, 8 softmax warps
+constexpr int kThreads = 352;       // producer, MMA issuer, 8 softmax warps, item finder
 constexpr int kQBufs = 2;           // Q tile buffers
 constexpr int kSlots = 9;           // K/V ring slots
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
@@ -81,8 +82,10 @@ struct PairCfg {
       kFinal = 11,                      // even CTA: every MMA done (teardown)
       kTail = 12,                       // own: a V half-tile whose tail rows are cleared
       kSlotFull = 13,                   // [kSlots] even CTA: both CTAs' bytes
-      kSlotEmpty = 13 + kSlots;         // [kSlots] both
-  static constexpr int kNumBars = 13 + 2 * kSlots;
+      kSlotEmpty = 13 + kSlots,         // [kSlots] both
+      kItemFull = 13 + 2 * kSlots,      // [kItemSlots] own: the ring of items
+      kItemEmpty = kItemFull + kItemSlots;
+  static constexpr int kNumBars = kItemEmpty + kItemSlots;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag
   // softmax hand-off: running row maxima [quadrant][to side][lane] and
   // their ok flags [quadrant][to side]; epilogue (sum, its maximum) pairs
@@ -91,7 +94,8 @@ struct PairCfg {
   static constexpr int kXOkOff = kXMaxOff + 4 * 2 * 32 * 4;
   static constexpr int kXSumOff = kXOkOff + 4 * 2 * 4;
   static constexpr int kXSumOkOff = kXSumOff + 2 * 4 * 2 * 32 * 8;
-  static constexpr int kSchedOff = (kXSumOkOff + 2 * 4 * 2 * 4 + 127) / 128 * 128;
+  static constexpr int kItemOff = (kXSumOkOff + 2 * 4 * 2 * 4 + 127) / 128 * 128;
+  static constexpr int kSchedOff = kItemOff + kItemSlots * 32;
   static constexpr int kSmemBytes = kSchedOff + (2 * PA_MAX_BATCH + 1) * 4;
   static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
   static constexpr uint32_t kColO = kSBufs * kTile;  // S buffers at 0, 128, 256
@@ -101,27 +105,23 @@ struct PairCfg {
   static constexpr uint32_t kIdescO = idesc_bf16_f32(kCluster * kTile, kD, true);
 };
 
-// A position in a pair's stream of key tiles: the items of worker `cl` of
-// `n_cl`, skipping items without keys; n-th item i, its tile j.  done() once
-// past the end.
-template <bool kPrompt>
+// A position in a pair's stream of key tiles: tile j of item `it`.  done() once
+// past the end (or a wait for an item ran out: ok is false).
 struct Walk {
-  int n, j, n_items, cl, n_cl, i;
+  ItemReader at;
   ItemInfo it;
-  __device__ __forceinline__ bool done() const { return i >= n_items; }
-  __device__ __forceinline__ void seek(const VarlenParams &p, const int32_t *order,
-                                       const int32_t *prefix) {
+  int j;
+  bool ok, last;
+  __device__ __forceinline__ bool done() const { return it.nk < 0; }
+  __device__ __forceinline__ void seek(const ItemRing &ring, volatile int32_t *abort_flag,
+                                       int32_t *status) {
     j = 0;
-    for (; (i = item_at<kPrompt>(p, n, cl, n_cl)) < n_items; ++n) {
-      it = item_info<kPrompt>(p, order, prefix, i);
-      if (it.nk > 0) return;
-    }
+    ok = at.next(ring, it, last, abort_flag, status, kWaitLimit);
+    if (!ok) it.nk = -1;
   }
-  __device__ __forceinline__ void next(const VarlenParams &p, const int32_t *order,
-                                       const int32_t *prefix) {
-    if (++j < it.nk) return;
-    ++n;
-    seek(p, order, prefix);
+  __device__ __forceinline__ void next(const ItemRing &ring, volatile int32_t *abort_flag,
+                                       int32_t *status) {
+    if (++j >= it.nk) seek(ring, abort_flag, status);
   }
 };
 
@@ -187,7 +187,6 @@ __device__ __forceinline__ void tile_p(uint32_t taddr, int valid, float sl2, flo
   }
 }
 
-template <bool kPrompt>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     varlen_attn_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
@@ -210,7 +209,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   int32_t *order = reinterpret_cast<int32_t *>(gbase + C::kSchedOff);
   int32_t *prefix = order + PA_MAX_BATCH;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the same in every lane, and the compiler knows: what follows from it takes
+  // uniform registers; without this the softmax spilled, 16k causal keys in
+  // 1570 us instead of 1180)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
 
@@ -231,20 +233,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::kSlotFull + s), 1);   // as kQFull
       mbar_init(bar(C::kSlotEmpty + s), 1);
     }
+    for (int s = 0; s < kItemSlots; ++s) {
+      mbar_init(bar(C::kItemFull + s), 1);
+      mbar_init(bar(C::kItemEmpty + s), leader ? 10 : 9);   // producer, softmax, MMA issuer
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(base + C::kMiscOff, C::kTmemCols);
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
-  item_list<kPrompt>(p, order, prefix, tmp, tmp + PA_MAX_BATCH, blockIdx.x == 0);
+  item_list(p, order, prefix, tmp, tmp + PA_MAX_BATCH, blockIdx.x == 0);
   fence_before_sync();
   __syncwarp();     // the cluster barrier is warp-aligned
   cluster_sync();   // barriers of both CTAs initialised before any remote use
   fence_after_sync();
   const uint32_t tmem = *tmem_base_ptr;
-  const int n_items = prefix[p.batch];
-  const int cl = blockIdx.x / kCluster, n_cl = gridDim.x / kCluster;
+  const ItemRing ring{reinterpret_cast<ItemInfo *>(gbase + C::kItemOff), bar(C::kItemFull),
+                      bar(C::kItemEmpty)};
 
   if (warp == 0) {
     // ================= TMA producer (both CTAs) =================
@@ -270,17 +276,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       if (!wait_all(bar(C::kQEmpty + qb), ((q_loads / kQBufs) & 1u) ^ 1u)) return false;
       if (lead) {
         const uint32_t full = mapa_shared(bar(C::kQFull + qb), 0);
-        if (leader) mbar_arrive_expect_tx(bar(C::kQFull + qb), kCluster * C::kQBytes);
+        if (leader)
+          mbar_arrive_expect_tx(bar(C::kQFull + qb), kCluster * 2 * (p.tokens * p.G * 128));
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
           tma_load_3d_pair(sQ + qb * C::kQBytes + hf * C::kHalfBytes, &tm_q, full, hf * 64,
-                           it.head, it.q_row0 + static_cast<int>(rank) * kTile);
+                           it.head * p.G, it.q_row0 + static_cast<int>(rank) * p.tokens);
       }
       ++q_loads;
       return true;
     };
     // this CTA's 64 keys of the K tile, all 128 columns
-    auto load_k = [&](const Walk<kPrompt> &w) -> bool {
+    auto load_k = [&](const Walk &w) -> bool {
       uint32_t s;
       if (!take_slot(s)) return false;
       const int row = w.it.k0 + key_tile(w.it, w.j) * kTile + static_cast<int>(rank) * 64;
@@ -290,13 +297,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
           tma_load_3d_pair(sRing + s * C::kSlotBytes + hf * C::kKHalfBytes, &tm_k, full,
-                           hf * 64, w.it.kv_head, row);
+                           hf * 64, w.it.head, row);
       }
       ++loads;
       return true;
     };
     // this CTA's 64 columns of the V tile, all 128 keys
-    auto load_v = [&](const Walk<kPrompt> &w) -> bool {
+    auto load_v = [&](const Walk &w) -> bool {
       uint32_t s;
       if (!take_slot(s)) return false;
       const int kt = key_tile(w.it, w.j);
@@ -306,7 +313,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t full = mapa_shared(bar(C::kSlotFull + s), 0);
       if (lead && leader) mbar_arrive_expect_tx(bar(C::kSlotFull + s), kCluster * C::kSlotBytes);
       if (valid >= kTile) {
-        if (lead) tma_load_3d_pair(dst, &tm_v, full, static_cast<int>(rank) * 64, w.it.kv_head, row);
+        if (lead) tma_load_3d_pair(dst, &tm_v, full, static_cast<int>(rank) * 64, w.it.head, row);
       } else {
         // The tile holds rows past the sequence end (the next sequence's, or
         // the buffer's trailing rows).  P is 0 there, but 0 * Inf and
@@ -315,7 +322,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         // are cleared, and only then are its bytes counted on the slot.
         if (lead) {
           mbar_arrive_expect_tx(bar(C::kTail), C::kSlotBytes);
-          tma_load_3d(dst, &tm_v, bar(C::kTail), static_cast<int>(rank) * 64, w.it.kv_head, row);
+          tma_load_3d(dst, &tm_v, bar(C::kTail), static_cast<int>(rank) * 64, w.it.head, row);
         }
         tail_pending = true;
         if (!wait_all(bar(C::kTail), tails & 1u)) return false;
@@ -339,23 +346,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       ++loads;
       return true;
     };
-    Walk<kPrompt> kw{0, 0, n_items, cl, n_cl, 0, {}}, vw{0, 0, n_items, cl, n_cl, 0, {}};
-    kw.seek(p, order, prefix);
-    vw.seek(p, order, prefix);
+    Walk kw{{0}, {}, 0, true, false}, vw{{0}, {}, 0, true, true};
+    kw.seek(ring, abort_flag, p.status);
+    vw.seek(ring, abort_flag, p.status);
     // the order of the MMA issuer: K of the first kSBufs tiles, then V_g, K_{g+3}
     auto next_k = [&]() -> bool {
       if (kw.done()) return true;
       if (kw.j == 0 && !load_q(kw.it)) return false;
       if (!load_k(kw)) return false;
-      kw.next(p, order, prefix);
+      kw.next(ring, abort_flag, p.status);
       return true;
     };
     for (int t = 0; t < kSBufs && ok; ++t) ok = next_k();
     while (ok && !vw.done()) {
       ok = load_v(vw);
-      vw.next(p, order, prefix);
+      vw.next(ring, abort_flag, p.status);
       if (ok) ok = next_k();
     }
+    ok = ok && kw.ok && vw.ok;
     if (!ok) {
       // give the copies already issued a bounded chance to land (the even
       // CTA's barriers count both CTAs' bytes)
@@ -409,9 +417,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
       // V (MN-major): one 64-column half per CTA, next 8 keys at SBO = 1024
       const uint64_t vdesc0 = sdesc_sw128(sRing, 1024, 1024);
-      Walk<kPrompt> kw{0, 0, n_items, cl, n_cl, 0, {}}, vw{0, 0, n_items, cl, n_cl, 0, {}};
-      kw.seek(p, order, prefix);
-      vw.seek(p, order, prefix);
+      Walk kw{{0}, {}, 0, true, false}, vw{{0}, {}, 0, true, true};
+      kw.seek(ring, abort_flag, p.status);
+      vw.seek(ring, abort_flag, p.status);
       // S_gs = Q K^T of the K walk's tile (or a bare commit past the end)
       auto issue_s = [&]() -> bool {
         const uint32_t b = gs % kSBufs;
@@ -441,7 +449,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
           ++kq;
         }
         ++gs;
-        kw.next(p, order, prefix);
+        kw.next(ring, abort_flag, p.status);
         return true;
       };
       if (!vw.done())
@@ -472,7 +480,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         if (vw.j == vw.it.nk - 1) commit_both(bar(C::kOFull));
         commit_both(bar(C::kSlotEmpty + s));
         ++gv;
-        vw.next(p, order, prefix);
+        vw.next(ring, abort_flag, p.status);
         ok = issue_s();
       }
       // every MMA issued so far has finished before TMEM is released
@@ -482,6 +490,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == kThreads / 32 - 1) {
+    // ================= the items, ahead of everyone =================
+    tell_items(p, order, prefix, blockIdx.x / kCluster, gridDim.x / kCluster, ring, kD,
+               static_cast<int>(rank), kCluster, abort_flag, kWaitLimit);
   } else {
     // ================= softmax / rescale / epilogue =================
     // The two warps of a TMEM lane quadrant (warp % 4, a hardware rule) take
@@ -502,27 +514,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     int32_t *xs_ok = reinterpret_cast<int32_t *>(gbase + C::kXSumOkOff);  // [item parity][quad][side]
     const int to_me = quad * 2 + side, to_other = quad * 2 + (side ^ 1);
     const float sl2 = p.scale_log2;
+    const int row_token = row / p.G, row_head = row - row_token * p.G;   // of the tile, the group
     uint32_t g = 0, o_waits = 0;
     bool ok = true;
-    for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, cl, n_cl)) < n_items; ++n) {
-      const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
-      const int rows_c = it.rows - static_cast<int>(rank) * kTile;   // may be <= 0
-      __nv_bfloat16 *dst =
-          p.out +
-          (static_cast<int64_t>(it.q_row0 + static_cast<int>(rank) * kTile + row) * p.H +
-           it.head) * kD + side * 64;
-      const bool store = row < rows_c;
-      // prompts: the keys that this row sees (none: its output is zero)
-      const int row_keys =
-          kPrompt ? min(it.lk, it.seen + static_cast<int>(rank) * kTile + row + 1) : it.lk;
-      if (it.nk == 0) {
-        if (store) {
-          uint4 *d4 = reinterpret_cast<uint4 *>(dst);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) d4[c] = make_uint4(0, 0, 0, 0);
-        }
-        continue;
+    ItemReader at{0};
+    ItemInfo it;
+    while (ok) {
+      const bool told = at.next(ring, it, true, abort_flag, p.status, kWaitLimit);
+      if (!told || it.nk < 0) {
+        // Both warps of the quadrant stop together.  Where only this one has not
+        // heard of an item, the other one is on its way through it: a maximum
+        // that says so is handed on, and they meet where the item ends.
+        if (lane == 0) xok[to_other] = xs_ok[static_cast<int>(o_waits & 1u) * 8 + to_me] = 0;
+        __syncwarp();
+        if (!told) named_bar_arrive(1 + to_other, 64);
+        named_bar_sync(9 + quad, 64);
+        break;
       }
+      it.nk = __shfl_sync(0xffffffffu, it.nk, 0);   // (uniform, as `warp` above)
+      it.rot = __shfl_sync(0xffffffffu, it.rot, 0);
+      const int token = static_cast<int>(rank) * p.tokens + row_token;   // of the item
+      __nv_bfloat16 *dst = p.out +
+                           (static_cast<int64_t>(it.q_row0 + token) * p.H + it.head * p.G +
+                            row_head) * kD + side * 64;
+      const bool store = token < it.tokens && row_token < p.tokens;
+      const int row_keys = min(it.lk, it.seen + token + 1);   // that this row sees
       // m: running maximum after this warp's latest tile; l: this warp's P
       // sum, scaled to m_ref
       float m = -INFINITY, l = 0.f, m_ref = -INFINITY;
@@ -534,11 +550,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         okt = __all_sync(0xffffffffu, okt);
         // pass 1: the tile's row maximum (scores are read again for P, so
         // no 128-value array stays live across the hand-off)
-        const int valid = kPrompt ? row_keys - key_tile(it, j) * kTile
-                          : key_tile(it, j) == it.nk - 1 ? it.lk - (it.nk - 1) * kTile
-                                                         : kTile;
-        const bool masked =
-            kPrompt ? __any_sync(0xffffffffu, valid < kTile) != 0 : valid < kTile;
+        const int valid = row_keys - key_tile(it, j) * kTile;
+        const bool masked = __any_sync(0xffffffffu, valid < kTile) != 0;
         float mx = -INFINITY;
         if (okt) {
           fence_after_sync();
@@ -656,7 +669,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
-            if (kPrompt && row_keys <= 0) {   // (its sums are NaN)
+            if (row_keys <= 0) {   // it sees no key (its sums are NaN)
               d4[v] = make_uint4(0, 0, 0, 0);
               continue;
             }
@@ -682,16 +695,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // [rows, H, 128] bf16 viewed as a 3-D tensor (D, H, rows), rows row_elems
-// elements apart; box 64 x 1 x box_rows with 128-byte swizzle.  Rows past the end read as zero.
+// elements apart; box 64 x box_heads x box_rows with 128-byte swizzle.  Rows past the end read as zero.
 bool make_map_rows(CUtensorMap *map, const void *ptr, int rows, int H, int64_t row_elems,
-                   int box_rows) {
+                   int box_heads, int box_rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2,
                                  static_cast<cuuint64_t>(row_elems) * 2};
-  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -699,30 +713,22 @@ bool make_map_rows(CUtensorMap *map, const void *ptr, int rows, int H, int64_t r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kPrompt>
-cudaError_t launch_pair(const VarlenArgs &a, cudaStream_t stream) {
-  CUtensorMap mq, mk, mv;
-  if (!make_map_rows(&mq, a.q, a.total_q, a.H, a.q_stride, kTile) ||
-      !make_map_rows(&mk, a.k, a.total_k, a.Hkv, a.k_stride, 64) ||
-      !make_map_rows(&mv, a.v, a.total_k, a.Hkv, a.v_stride, kTile))
-    return cudaErrorInvalidValue;
-  const VarlenParams p = varlen_params(a);
-  static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(varlen_attn_pair_kernel<kPrompt>),
-                                PairCfg::kSmemBytes, configured);
-  if (e != cudaSuccess) return e;
-  const int grid = a.num_sms / kCluster * kCluster;   // whole pairs, one CTA per SM
-  varlen_attn_pair_kernel<kPrompt><<<grid, kThreads, PairCfg::kSmemBytes, stream>>>(mq, mk, mv, p);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_varlen_attn_pair(const VarlenArgs &a, cudaStream_t stream) {
-  return launch_pair<false>(a, stream);
-}
-cudaError_t launch_prompt_attn_pair(const VarlenArgs &a, cudaStream_t stream) {
-  return launch_pair<true>(a, stream);
+  CUtensorMap mq, mk, mv;
+  const VarlenParams p = varlen_params(a);
+  if (!make_map_rows(&mq, a.q, a.total_q, a.H, a.q_stride, p.G, p.tokens) ||
+      !make_map_rows(&mk, a.k, a.total_k, a.Hkv, a.k_stride, 1, 64) ||
+      !make_map_rows(&mv, a.v, a.total_k, a.Hkv, a.v_stride, 1, kTile))
+    return cudaErrorInvalidValue;
+  static unsigned long long configured = 0;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(varlen_attn_pair_kernel),
+                                PairCfg::kSmemBytes, configured);
+  if (e != cudaSuccess) return e;
+  const int grid = a.num_sms / kCluster * kCluster;   // whole pairs, one CTA per SM
+  varlen_attn_pair_kernel<<<grid, kThreads, PairCfg::kSmemBytes, stream>>>(mq, mk, mv, p);
+  return cudaGetLastError();
 }
 
 }  // namespace pa

@@ -10,8 +10,9 @@
 // (attn_pair.cu), whose M = 256 MMAs leave TMEM room to compute scores
 // ahead of the softmax.
 //
-// Design: one persistent CTA per SM, 11 warps.  A work item is 256 query
-// rows of one (sequence, head), held as two 128-row tiles Q0 and Q1 that share
+// Design: one persistent CTA per SM, 12 warps.  A work item is 256 query
+// rows of one (sequence, K/V head), its group's heads of 256 / G tokens
+// (varlen_items.cuh), held as two 128-row tiles Q0 and Q1 that share
 // every K/V tile loaded, so each K/V byte brought into shared memory feeds
 // twice the tensor-core work of a single-tile item.
 //   warp 0      TMA producer: Q0/Q1 once per item, then K0, V0, K1, V1, ...
@@ -57,9 +58,8 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = kVarlenTile;          // rows of a Q tile, keys of a K/V tile
-constexpr int kItemRows = kVarlenItemRows;  // query rows per work item (two tiles)
-constexpr int kThreads = 352;       // producer, 2 MMA issuers, 2 x 4 softmax warps
-constexpr int kMmaWarp1 = kThreads / 32 - 1;   // issuer of tile 1
+constexpr int kThreads = 384;       // producer, 2 MMA issuers, 2 x 4 softmax warps, item finder
+constexpr int kMmaWarp1 = 10;       // issuer of tile 1
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
@@ -79,9 +79,11 @@ struct Cfg {
   // barriers: per Q tile t an S-full, a P-ready and an O-full barrier
   static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
                        kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots;
-  static constexpr int kNumBars = 12 + 2 * kSlots;
+  static constexpr int kItemFull = 12 + 2 * kSlots, kItemEmpty = kItemFull + kItemSlots;
+  static constexpr int kNumBars = kItemEmpty + kItemSlots;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag
-  static constexpr int kSchedOff = (kMiscOff + 16 + 127) / 128 * 128;
+  static constexpr int kItemOff = (kMiscOff + 16 + 127) / 128 * 128;
+  static constexpr int kSchedOff = kItemOff + kItemSlots * 32;
   static constexpr int kSmemBytes = kSchedOff + (2 * kMaxSeqs + 1) * 4;
   static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
   // TMEM columns: S_t at 128 t (P_t over its first 64), O_t at 256 + D t
@@ -113,7 +115,7 @@ __device__ __forceinline__ void zero_v_tail(uint8_t *tile, int valid, int lane) 
   __syncwarp();
 }
 
-template <int D, int kSlots, int kMaxSeqs, bool kPrompt>
+template <int D, int kSlots, int kMaxSeqs>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t *order = reinterpret_cast<int32_t *>(gbase + C::kSchedOff);
   int32_t *prefix = order + kMaxSeqs;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (uniform, and the compiler knows, as in attn_pair.cu)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // ---- set-up: barriers, TMEM, work list --------------------------------
   if (tid == 0) {
@@ -154,18 +157,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::kSlotFull + s), 1);
       mbar_init(bar(C::kSlotEmpty + s), 2);   // one arrival per MMA issuer
     }
+    for (int s = 0; s < kItemSlots; ++s) {
+      mbar_init(bar(C::kItemFull + s), 1);
+      mbar_init(bar(C::kItemEmpty + s), 11);   // producer, two MMA issuers, softmax
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(base + C::kMiscOff, C::kTmemCols);
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
-  item_list<kPrompt>(p, order, prefix, tmp, tmp + kMaxSeqs, blockIdx.x == 0);
+  item_list(p, order, prefix, tmp, tmp + kMaxSeqs, blockIdx.x == 0);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_base_ptr;
-  const int n_items = prefix[p.batch];
+  const ItemRing ring{reinterpret_cast<ItemInfo *>(gbase + C::kItemOff), bar(C::kItemFull),
+                      bar(C::kItemEmpty)};
+  // the next item of a warp, or nk < 0 (ok: not because a wait ran out)
+  ItemReader at{0};
+  auto next_item = [&](ItemInfo &it, bool &ok) -> bool {
+    ok = at.next(ring, it, true, abort_flag, p.status, kWaitLimit);
+    return ok && it.nk >= 0;
+  };
 
   if (warp == 0) {
     // ================= TMA producer =================
@@ -197,28 +211,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++slot_loads;
         return true;
       };
-      for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, blockIdx.x, gridDim.x)) < n_items; ++n) {
-        const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
-        if (it.nk == 0) continue;
-        const int ntq = it.rows > kTile ? 2 : 1;
+      ItemInfo it;
+      while (ok && next_item(it, ok)) {
+        const int ntq = it.tokens > p.tokens ? 2 : 1;
         if (!wait_all(bar(C::kQEmpty), (q_loads & 1u) ^ 1u)) {
           ok = false;
           break;
         }
         if (lead) {
-          mbar_arrive_expect_tx(bar(C::kQFull), ntq * C::kTileBytes);
+          mbar_arrive_expect_tx(bar(C::kQFull), ntq * p.tokens * p.G * D * 2);
           for (int t = 0; t < ntq; ++t) {
 #pragma unroll
             for (int hf = 0; hf < D / 64; ++hf)
               tma_load_3d(sQ + t * C::kTileBytes + hf * C::kHalfBytes, &tm_q, bar(C::kQFull),
-                          hf * 64, it.head, it.q_row0 + t * kTile);
+                          hf * 64, it.head * p.G, it.q_row0 + t * p.tokens);
           }
         }
         ++q_loads;
         for (int j = 0; j < it.nk && ok; ++j) {
           const int row = it.k0 + key_tile(it, j) * kTile;
-          ok = load_kv(&tm_k, row, it.kv_head);
-          if (ok) ok = load_kv(&tm_v, row, it.kv_head);
+          ok = load_kv(&tm_k, row, it.head);
+          if (ok) ok = load_kv(&tm_v, row, it.head);
         }
       }
       if (!ok) {
@@ -293,10 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++turns;
         if (lead) mbar_arrive(bar(C::kTurn + (1 - t)));
       };
-      for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, blockIdx.x, gridDim.x)) < n_items; ++n) {
-        const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
-        if (it.nk == 0) continue;
-        const bool mine = it.rows > t * kTile;   // this issuer's tile is in the item
+      ItemInfo it;
+      while (ok && next_item(it, ok)) {
+        const bool mine = it.tokens > t * p.tokens;   // this issuer's tile is in the item
         // release a slot / the Q buffer: after this tile's MMAs, or at once
         auto release = [&](uint32_t b) {
           if (!lead) return;
@@ -389,6 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == kThreads / 32 - 1) {
+    // ================= the items, ahead of everyone =================
+    tell_items(p, order, prefix, blockIdx.x, gridDim.x, ring, D, 0, 1, abort_flag, kWaitLimit);
   } else {
     // ================= softmax / correction / epilogue =================
     // warps 2..5: tile 0, warps 6..9: tile 1; TMEM lane quadrant = warp % 4
@@ -401,25 +416,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale_log2;
     const bool pos_scale = sl2 > 0.f;
     const float mul = pos_scale ? sl2 : 1.f;
+    const int row_token = row / p.G, row_head = row - row_token * p.G;   // of the tile, the group
     uint32_t s_waits = 0, o_waits = 0;
     bool ok = true;
-    for (int n = 0, i; ok && (i = item_at<kPrompt>(p, n, blockIdx.x, gridDim.x)) < n_items; ++n) {
-      const ItemInfo it = item_info<kPrompt>(p, order, prefix, i);
-      const int rows_t = it.rows - t * kTile;   // this tile's valid rows (may be <= 0)
-      if (rows_t <= 0) continue;                // tile absent: nothing issued for it
+    ItemInfo it;
+    while (ok && next_item(it, ok)) {
+      if (it.tokens <= t * p.tokens) continue;    // tile absent: nothing issued for it
+      const int token = t * p.tokens + row_token;   // of the item
       __nv_bfloat16 *dst =
-          p.out + (static_cast<int64_t>(it.q_row0 + t * kTile + row) * p.H + it.head) * D;
-      const bool store = row < rows_t;
-      // prompts: the keys that this row sees (none: its output is zero)
-      const int row_keys = kPrompt ? min(it.lk, it.seen + t * kTile + row + 1) : it.lk;
-      if (it.nk == 0) {
-        if (store) {
-          uint4 *d4 = reinterpret_cast<uint4 *>(dst);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) d4[c] = make_uint4(0, 0, 0, 0);
-        }
-        continue;
-      }
+          p.out + (static_cast<int64_t>(it.q_row0 + token) * p.H + it.head * p.G + row_head) * D;
+      const bool store = token < it.tokens && row_token < p.tokens;
+      const int row_keys = min(it.lk, it.seen + token + 1);   // that this row sees
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < it.nk; ++j) {
         ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kWaitLimit);
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kTile / 2; ++c) x[c] = __fmul2_rn(x[c], s2);
         }
         const int valid = row_keys - key_tile(it, j) * kTile;
-        if (kPrompt ? __any_sync(0xffffffffu, valid < kTile) != 0 : key_tile(it, j) == it.nk - 1) {
+        if (__any_sync(0xffffffffu, valid < kTile)) {
 #pragma unroll
           for (int c = 0; c < kTile / 2; ++c) {
             if (2 * c >= valid) x[c].x = -INFINITY;
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
-            if (kPrompt && row_keys <= 0) {   // (its sums are NaN)
+            if (row_keys <= 0) {   // it sees no key (its sums are NaN)
               d4[v] = make_uint4(0, 0, 0, 0);
               continue;
             }
@@ -557,15 +564,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // [rows, H, D] bf16 viewed as a 3-D tensor (D, H, rows), rows row_elems
-// elements apart; box 64 x 1 x 128 with 128-byte swizzle: one 128-row, 64-column half tile per load.
-bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t row_elems) {
+// elements apart; box 64 x box_heads x box_rows with 128-byte swizzle: one 128-row, 64-column half tile per load.
+bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t row_elems,
+              int box_heads, int box_rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
                                  static_cast<cuuint64_t>(row_elems) * 2};
-  const cuuint32_t box[3] = {64, 1, kTile};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -573,16 +582,16 @@ bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kSlots, int kMaxSeqs, bool kPrompt>
+template <int D, int kSlots, int kMaxSeqs>
 cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
-  if (!make_map(&mq, a.q, a.total_q, a.H, D, a.q_stride) ||
-      !make_map(&mk, a.k, a.total_k, a.Hkv, D, a.k_stride) ||
-      !make_map(&mv, a.v, a.total_k, a.Hkv, D, a.v_stride))
-    return cudaErrorInvalidValue;
   const VarlenParams p = varlen_params(a);
+  if (!make_map(&mq, a.q, a.total_q, a.H, D, a.q_stride, p.G, p.tokens) ||
+      !make_map(&mk, a.k, a.total_k, a.Hkv, D, a.k_stride, 1, kTile) ||
+      !make_map(&mv, a.v, a.total_k, a.Hkv, D, a.v_stride, 1, kTile))
+    return cudaErrorInvalidValue;
   const int smem = Cfg<D, kSlots, kMaxSeqs>::kSmemBytes;
-  const auto kernel = varlen_attn_tc_kernel<D, kSlots, kMaxSeqs, kPrompt>;
+  const auto kernel = varlen_attn_tc_kernel<D, kSlots, kMaxSeqs>;
   static unsigned long long configured = 0;
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), smem, configured);
   if (e != cudaSuccess) return e;
@@ -596,10 +605,7 @@ cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
 // ten-slot K/V ring beside a work list of up to PA_MAX_BATCH sequences.
 cudaError_t launch_varlen_attn(const VarlenArgs &a, cudaStream_t stream) {
   if (a.D == 128) return launch_varlen_attn_pair(a, stream);
-  return launch_tc<64, 10, PA_MAX_BATCH, false>(a, stream);
-}
-cudaError_t launch_prompt_attn_tc(const VarlenArgs &a, cudaStream_t stream) {
-  return launch_tc<64, 10, PA_MAX_BATCH, true>(a, stream);
+  return launch_tc<64, 10, PA_MAX_BATCH>(a, stream);
 }
 
 }  // namespace pa

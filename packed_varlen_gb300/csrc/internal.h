@@ -19,7 +19,7 @@ struct VarlenArgs {
   float scale;
   int32_t *status;  // device address of the per-device status word
   int num_sms;
-  int32_t Hkv, causal;                     // prompts: K/V heads, causal order
+  int32_t Hkv, causal;                     // K/V heads, causal order
   int64_t q_stride, k_stride, v_stride;    // elements from one token to the next
 };
 
@@ -74,8 +74,6 @@ pa_status from_cuda(cudaError_t e);
 // Launchers: return cudaSuccess or the launch error.
 cudaError_t launch_varlen_attn(const VarlenArgs &a, cudaStream_t stream);
 cudaError_t launch_varlen_attn_pair(const VarlenArgs &a, cudaStream_t stream);   // D = 128
-cudaError_t launch_prompt_attn_tc(const VarlenArgs &a, cudaStream_t stream);     // D = 64
-cudaError_t launch_prompt_attn_pair(const VarlenArgs &a, cudaStream_t stream);   // D = 128
 cudaError_t launch_block_window_attn(const BlockWindowArgs &a, cudaStream_t stream);
 
 }  // namespace pa

@@ -1,6 +1,6 @@
 // Attention of packed prompts, causal and with grouped heads: the entry point.
-// The kernels are the varlen ones' kPrompt forms (attn_pair.cu, attn_tc.cu;
-// varlen_items.cuh has what differs: the items, their order and their keys).
+// The kernels are those of pa_varlen_attn_fwd (attn_pair.cu, attn_tc.cu), which is
+// the call with groups of one head and no causal order.
 #include <math.h>
 
 #include "internal.h"
@@ -33,8 +33,9 @@ extern "C" pa_status pa_prompt_attn_fwd(const void *q, const void *k, const void
   if (q_stride < int64_t{Hq} * D || k_stride < int64_t{Hkv} * D || v_stride < int64_t{Hkv} * D)
     return PA_ERR_INVALID_ARG;
   if (!isfinite(scale * 1.4426950408889634f)) return PA_ERR_INVALID_ARG;
+  if (Hq / Hkv > kVarlenTile) return PA_ERR_UNSUPPORTED;
   // (every sequence's last item may be a partial one)
-  const int64_t items = (int64_t{total_q} / kVarlenItemRows + batch) * Hq;
+  const int64_t items = (total_q / (2 * (kVarlenTile / (Hq / Hkv))) + int64_t{batch}) * Hkv;
   if (batch > PA_MAX_BATCH || (D != 64 && D != 128) || Hq > 65535 || total_q > kMostTokens ||
       total_k > kMostTokens || items > kMostTokens || q_stride > kMostStride ||
       k_stride > kMostStride || v_stride > kMostStride)
@@ -52,6 +53,5 @@ extern "C" pa_status pa_prompt_attn_fwd(const void *q, const void *k, const void
                max_k, Hq, D, scale, nullptr, 0, Hkv, causal != 0, q_stride, k_stride, v_stride};
   cudaError_t e = device_context(&a.status, &a.num_sms);
   if (e != cudaSuccess) return from_cuda(e);
-  auto s = reinterpret_cast<cudaStream_t>(stream);
-  return from_cuda(D == 128 ? launch_prompt_attn_pair(a, s) : launch_prompt_attn_tc(a, s));
+  return from_cuda(launch_varlen_attn(a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -1,13 +1,15 @@
-// Work items of the packed varlen attention kernels (head dim 64 on single
-// CTAs, head dim 128 on CTA pairs): their parameters, the decode of item i of
-// the length-ordered list into rows and keys, and the key-tile order.  Both
-// kernels take a work item of kVarlenItemRows query rows of one (sequence,
-// head) and walk its keys in kVarlenTile-key tiles in the same order, so a
-// sequence's rows come out the same whatever the batch around it.
+// Work items of the packed attention kernels (head dim 64 on single CTAs, head
+// dim 128 on CTA pairs): their parameters, the decode of item i of the work list
+// into rows and keys, the key-tile order, and the ring through which one warp
+// tells the others of the items.
 //
-// kPrompt: the form for prompts, with grouped heads (query head h reads K/V
-// head h / G) and, where p.causal, causal order: query i of a sequence sees key
-// j iff j <= lk - lq + i.
+// Query head h reads K/V head h / G.  The rows of a 128-row tile are the group's
+// heads of 128 / G tokens (row = token * G + head of the group; G = 1: 128
+// tokens), so few tokens fill a tile, and causal order cuts all of its rows at
+// nearly the same key.  An item is two tiles of one (sequence, K/V head); its
+// keys come in kVarlenTile-key tiles in the same order on both kernels, so a
+// sequence's rows come out the same whatever the batch around it.
+// causal: query i of a sequence sees key j iff j <= lk - lq + i.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -15,11 +17,13 @@
 
 #include "internal.h"
 #include "sched.cuh"
+#include "tc_ptx.cuh"
 
 namespace pa {
 
 constexpr int kVarlenTile = 128;       // keys of a K/V tile, rows of a Q tile
 constexpr int kVarlenItemRows = 256;   // query rows of a work item
+constexpr int kItemSlots = 8;          // items told ahead
 
 struct VarlenParams {
   __nv_bfloat16 *out;
@@ -27,7 +31,7 @@ struct VarlenParams {
   int batch, H, total_q, total_k, max_q, max_k;
   float scale_log2;
   int32_t *status;
-  int G, causal;   // prompts: query heads per K/V head, causal order
+  int G, tokens, causal;   // query heads per K/V head, tokens of a tile, causal order
 };
 
 inline VarlenParams varlen_params(const VarlenArgs &a) {
@@ -44,24 +48,25 @@ inline VarlenParams varlen_params(const VarlenArgs &a) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
   p.G = a.H / a.Hkv;
+  p.tokens = kVarlenTile / p.G;
   p.causal = a.causal;
   return p;
 }
 
 struct ItemInfo {
-  int q_row0;   // global row of the item's first query
-  int rows;     // valid query rows in the item (1..kVarlenItemRows)
+  int q_row0;   // global row of the item's first token
+  int tokens;   // valid tokens in the item (1..2 * VarlenParams::tokens)
   int k0;       // global row of the sequence's first key
   int lk;       // keys of the sequence
   int nk;       // key tiles
-  int head;
+  int head;     // of K and V
   int rot;      // first key tile visited
-  int kv_head;  // head of its K and V rows
-  int seen;     // prompts: row r of the item sees the keys below min(lk, seen + r + 1)
+  int seen;     // token r of the item sees the keys below min(lk, seen + r + 1)
 };
+static_assert(sizeof(ItemInfo) == 32, "two 16-byte pieces");
 
-// Key tile visited j-th.  Items start at key tile (item index in the
-// sequence mod nk) and wrap around, so the workers of a wave, which hold
+// Key tile visited j-th.  Items start at another key tile each (their place in
+// the sequence) and wrap around, so the workers of a wave, which hold
 // consecutive query blocks of one head, read different K/V tiles at any
 // moment.  The order depends only on the sequence's own lengths and the
 // item's position in it, so a sequence's result is the same in any batch.
@@ -72,55 +77,123 @@ __device__ __forceinline__ int key_tile(const ItemInfo &it, int j) {
 
 // Item i (0 <= i < prefix[batch]) of the work list; a sequence whose
 // boundaries are invalid reads as empty (the list build records why).
-template <bool kPrompt = false>
 __device__ __forceinline__ ItemInfo item_info(const VarlenParams &p, const int32_t *order,
                                               const int32_t *prefix, int i) {
-  const bool causal = kPrompt && p.causal != 0;
-  const WorkItem w = causal ? sched_level_item(order, prefix, p.cu_q, p.batch, p.H,
-                                               kVarlenItemRows, i)
-                            : sched_item(order, prefix, p.batch, p.H, i);
+  const int heads = p.H / p.G, item = 2 * p.tokens;
+  const WorkItem w = p.causal ? sched_level_item(order, prefix, p.cu_q, p.batch, heads, item, i)
+                              : sched_item(order, prefix, p.batch, heads, i);
   int err;
   const SeqBounds sb = seq_bounds(p.cu_q, p.cu_k, w.seq, p.total_q, p.total_k, p.max_q,
                                   p.max_k, err);
   ItemInfo it;
-  it.q_row0 = sb.q0 + w.tile * kVarlenItemRows;
-  it.rows = min(kVarlenItemRows, sb.lq - w.tile * kVarlenItemRows);
+  it.q_row0 = sb.q0 + w.tile * item;
+  it.tokens = min(item, sb.lq - w.tile * item);
   it.k0 = sb.k0;
   it.lk = sb.lk;
   it.head = w.head;
-  it.kv_head = kPrompt ? w.head / p.G : w.head;
   it.seen = sb.lk;
   int keys = sb.lk;   // that any row of the item sees
-  if (causal) {
-    it.seen = sb.lk - sb.lq + w.tile * kVarlenItemRows;
-    keys = max(0, it.seen + it.rows);   // (at most lk)
+  if (p.causal) {
+    it.seen = sb.lk - sb.lq + w.tile * item;
+    keys = max(0, it.seen + it.tokens);   // (at most lk)
   }
   it.nk = (keys + kVarlenTile - 1) / kVarlenTile;
   // A causal item takes its tiles in order: each row that sees any key sees
   // the first one, so its maximum is finite before a tile that hides all.
-  it.rot = it.nk > 0 && !causal ? w.tile % it.nk : 0;
+  it.rot = it.nk > 0 && !p.causal ? w.tile * item / kVarlenItemRows % it.nk : 0;
   return it;
 }
 
 // The work list of a kernel, in shared memory (see sched_build).
-template <bool kPrompt = false>
 __device__ __forceinline__ void item_list(const VarlenParams &p, int32_t *order, int32_t *prefix,
                                           int32_t *tmp_lq, int32_t *tmp_lk, bool report) {
-  if (kPrompt && p.causal)
-    sched_build<true>(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H,
-                      kVarlenItemRows, p.total_q, p.total_k, p.max_q, p.max_k, p.status, report);
+  if (p.causal)
+    sched_build<true>(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H / p.G,
+                      2 * p.tokens, p.total_q, p.total_k, p.max_q, p.max_k, p.status, report);
   else
-    sched_build(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H, kVarlenItemRows,
+    sched_build(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H / p.G, 2 * p.tokens,
                 p.total_q, p.total_k, p.max_q, p.max_k, p.status, report);
 }
 
 // The worker's n-th item, of `workers`: round robin; in a causal list, whose
 // items grow cheaper, every second round backwards, which evens out what a
 // round's first worker has more than its last.
-template <bool kPrompt = false>
 __device__ __forceinline__ int item_at(const VarlenParams &p, int n, int worker, int workers) {
-  if (kPrompt && p.causal && (n & 1)) return n * workers + workers - 1 - worker;
-  return n * workers + worker;
+  return n * workers + (p.causal && (n & 1) ? workers - 1 - worker : worker);
 }
+
+// The ring of items.  Finding an item takes a search and a chain of loads, some
+// thousand cycles, so a warp of its own does it ahead of the others; they read
+// what it found.  Full and empty barriers lie one after the other at `full`
+// and `empty` (shared-memory addresses); an empty one takes an arrival from
+// every warp that reads.  The ring ends with an item of nk < 0.
+struct ItemRing {
+  ItemInfo *items;   // [kItemSlots]
+  uint32_t full, empty;
+};
+
+// Whole warp: all items of this worker with keys into the ring.  The rows of
+// items without keys are zeroed here; `rank` of `ranks` CTAs that share the
+// items, each with the rows of its own tiles.
+__device__ __forceinline__ void tell_items(const VarlenParams &p, const int32_t *order,
+                                           const int32_t *prefix, int worker, int workers,
+                                           const ItemRing &ring, int D, int rank, int ranks,
+                                           volatile int32_t *abort_flag, long long limit) {
+  const int lane = threadIdx.x & 31, n_items = prefix[p.batch];
+  uint32_t told = 0;
+  bool more = true;
+  for (int n = 0; more; ++n) {
+    const int i = item_at(p, n, worker, workers);
+    more = i < n_items;
+    ItemInfo it = {};
+    it.nk = -1;
+    if (more) it = item_info(p, order, prefix, i);
+    if (it.nk == 0) {
+      const int t0 = ranks == 2 ? rank * p.tokens : 0;
+      const int t1 = ranks == 2 ? min(it.tokens, t0 + p.tokens) : it.tokens;
+      const int vecs = p.G * D / 8;   // of a token's heads
+      for (int c = lane; c < (t1 - t0) * vecs; c += 32) {
+        const int t = c / vecs;
+        reinterpret_cast<uint4 *>(
+            p.out + (static_cast<int64_t>(it.q_row0 + t0 + t) * p.H + it.head * p.G) * D)[c - t * vecs] =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
+    const uint32_t s = told % kItemSlots;
+    const bool ok = tc::bounded_wait(ring.empty + 8u * s, ((told / kItemSlots) & 1u) ^ 1u, abort_flag,
+                                     p.status, limit);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    if (lane == 0) {
+      ring.items[s] = it;
+      tc::mbar_arrive(ring.full + 8u * s);
+    }
+    __syncwarp();
+    ++told;
+  }
+}
+
+// A warp's place in the ring.  next(): the item after, false where the wait for
+// it ran out.  last: this is the warp's last reading of its items.
+struct ItemReader {
+  uint32_t n;
+  __device__ __forceinline__ bool next(const ItemRing &ring, ItemInfo &it, bool last,
+                                       volatile int32_t *abort_flag, int32_t *status,
+                                       long long limit) {
+    const uint32_t s = n % kItemSlots;
+    bool ok = tc::bounded_wait(ring.full + 8u * s, (n / kItemSlots) & 1u, abort_flag, status, limit);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    const volatile int4 *src = reinterpret_cast<const volatile int4 *>(ring.items + s);
+    int4 a, b;
+    a.x = src[0].x; a.y = src[0].y; a.z = src[0].z; a.w = src[0].w;
+    b.x = src[1].x; b.y = src[1].y; b.z = src[1].z; b.w = src[1].w;
+    it = ItemInfo{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    __syncwarp();
+    if (last && (threadIdx.x & 31) == 0) tc::mbar_arrive(ring.empty + 8u * s);
+    ++n;
+    return true;
+  }
+};
 
 }  // namespace pa

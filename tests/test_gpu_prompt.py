@@ -131,6 +131,15 @@ def test_long_prompts(pv, lq, lk, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,H", [(24, 24), (32, 4), (128, 1)])
+def test_many_items(pv, Hq, H, D, causal):
+    """Several items for every SM, of one to six key tiles, in all orders."""
+    lengths = [700, 130, 1, 257, 64, 390, 128, 20, 513, 300]
+    _attention_case(pv, lengths, lengths, Hq, H, D, causal, sampled=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_rows_that_see_nothing_are_zero(pv, D):
     out = _attention_case(pv, [3, 300, 400, 0], [0, 130, 10, 20], 4, 2, D, True)
     assert (out[:3] == 0).all() and (out[3:173] == 0).all() and (out[303:693] == 0).all()
