@@ -61,7 +61,7 @@ constexpr int kCluster = 2;
 constexpr int kSBufs = 3;           // S/P buffers in TMEM
 constexpr int kThreads = 352;       // producer, MMA issuer, 8 softmax warps, item finder
 constexpr int kQBufs = 2;           // Q tile buffers
-constexpr int kSlots = 9;           // K/V ring slots
+constexpr int kSlots = 7;           // K/V ring slots (9 were no faster)
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
@@ -73,7 +73,8 @@ struct PairCfg {
   static constexpr int kSlotBytes = 16384;          // a K half-tile or a V half-tile
   static constexpr int kQOff = 0;                   // kQBufs Q buffers
   static constexpr int kRingOff = kQBufs * kQBytes;
-  static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kOutOff = kRingOff + kSlots * kSlotBytes;   // 4 KB a softmax warp
+  static constexpr int kBarOff = kOutOff + 8 * 4096;
   static constexpr int kQFull = 0,      // [kQBufs] even CTA: Q bytes of both CTAs
       kQEmpty = 2,                      // [kQBufs] both: the item's last S is done
       kSFull = 4,                       // [3] both: S of a key tile is done
@@ -81,9 +82,10 @@ struct PairCfg {
       kOFull = 10,                      // both: the item's last PV is done
       kFinal = 11,                      // even CTA: every MMA done (teardown)
       kTail = 12,                       // own: a V half-tile whose tail rows are cleared
-      kSlotFull = 13,                   // [kSlots] even CTA: both CTAs' bytes
-      kSlotEmpty = 13 + kSlots,         // [kSlots] both
-      kItemFull = 13 + 2 * kSlots,      // [kItemSlots] own: the ring of items
+      kOFree = 13,                      // even CTA: the pair's 16 softmax warps have read O
+      kSlotFull = 14,                   // [kSlots] even CTA: both CTAs' bytes
+      kSlotEmpty = 14 + kSlots,         // [kSlots] both
+      kItemFull = 14 + 2 * kSlots,      // [kItemSlots] own: the ring of items
       kItemEmpty = kItemFull + kItemSlots;
   static constexpr int kNumBars = kItemEmpty + kItemSlots;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag
@@ -229,6 +231,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::kOFull), 1);
     mbar_init(bar(C::kFinal), 1);
     mbar_init(bar(C::kTail), 1);
+    mbar_init(bar(C::kOFree), 8 * kCluster);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kSlotFull + s), 1);   // as kQFull
       mbar_init(bar(C::kSlotEmpty + s), 1);
@@ -403,7 +406,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
           mma_commit_pair(mapa_shared(b, 1));
         }
       };
-      uint32_t slot_uses = 0, kq = 0, gs = 0, gv = 0;
+      uint32_t slot_uses = 0, kq = 0, gs = 0, gv = 0, outs = 0;
       bool ok = true, issued = false;
       auto next_slot = [&](uint32_t &s) -> bool {
         s = slot_uses % kSlots;
@@ -461,6 +464,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        // the first PV of an item writes over the O of the item before it
+        if (vw.j == 0 && outs > 0 && !wait_all(bar(C::kOFree), (outs - 1) & 1u)) {
+          ok = false;
+          break;
+        }
         fence_after_sync();
         uint32_t s;
         if (!next_slot(s)) {
@@ -477,7 +485,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
                         (vw.j == 0 && kk == 0) ? 0u : 1u);
         }
         issued = true;
-        if (vw.j == vw.it.nk - 1) commit_both(bar(C::kOFull));
+        if (vw.j == vw.it.nk - 1) {
+          commit_both(bar(C::kOFull));
+          ++outs;
+        }
         commit_both(bar(C::kSlotEmpty + s));
         ++gv;
         vw.next(ring, abort_flag, p.status);
@@ -517,14 +528,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     const int row_token = row / p.G, row_head = row - row_token * p.G;   // of the tile, the group
     uint32_t g = 0, o_waits = 0;
     bool ok = true;
+    const uint32_t o_free0 = mapa_shared(bar(C::kOFree), 0);
     ItemReader at{0};
     ItemInfo it;
-    while (ok) {
-      const bool told = at.next(ring, it, true, abort_flag, p.status, kWaitLimit);
+    bool told = at.next(ring, it, true, abort_flag, p.status, kWaitLimit);
+    while (true) {
       if (!told || it.nk < 0) {
-        // Both warps of the quadrant stop together.  Where only this one has not
-        // heard of an item, the other one is on its way through it: a maximum
-        // that says so is handed on, and they meet where the item ends.
+        // Both warps of the quadrant stop together.  Where only this one goes no
+        // further, the other one is on its way through the next item: a maximum
+        // that says so is handed on, and they meet where that item ends.
         if (lane == 0) xok[to_other] = xs_ok[static_cast<int>(o_waits & 1u) * 8 + to_me] = 0;
         __syncwarp();
         if (!told) named_bar_arrive(1 + to_other, 64);
@@ -635,52 +647,42 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed(p_ready0 + 8u * b);
       }
-      // epilogue: wait for the item's last PV, combine the two warps' sums,
+      // Epilogue: combine the two warps' sums, wait for the item's last PV,
       // normalise this warp's 64 columns of O and store the valid rows.  The
-      // exchange runs even after a failure, so both warps stop together.
-      bool oko = ok;
-      if (oko) {
-        oko = bounded_wait_cluster(bar(C::kOFull), o_waits & 1u, abort_flag, p.status,
-                                   kWaitLimit);
-        oko = __all_sync(0xffffffffu, oko);
-      }
+      // exchange runs even after a failure, so that both warps stop together.
       const int par = static_cast<int>(o_waits & 1u) * 8;
-      ++o_waits;
       xs[((par + to_me) * 32 + lane) * 2 + 0] = l;
       xs[((par + to_me) * 32 + lane) * 2 + 1] = m_ref;
-      if (lane == 0) xs_ok[par + to_me] = oko ? 1 : 0;
+      if (lane == 0) xs_ok[par + to_me] = ok ? 1 : 0;
       named_bar_sync(9 + quad, 64);
-      if (!oko || xs_ok[par + to_other] == 0) {
-        ok = false;
-        break;
-      }
+      if (!ok || xs_ok[par + to_other] == 0) break;
       const float l_o = xs[((par + to_other) * 32 + lane) * 2 + 0];
       const float m_o = xs[((par + to_other) * 32 + lane) * 2 + 1];
       const float m_fin = fmaxf(m_ref, m_o);   // the maximum after the item's last tile
       const float inv = 1.f / (l * ex2(m_ref - m_fin) + l_o * ex2(m_o - m_fin));
-      fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t r[32];
-        tmem_ld32(lane_base + C::kColO + side * 64 + c * 32, r);
-        tmem_wait_ld();
-        if (store) {
-          uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4 w;
-            if (row_keys <= 0) {   // it sees no key (its sums are NaN)
-              d4[v] = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            w.x = pack_bf16x2(__uint_as_float(r[8 * v + 0]) * inv, __uint_as_float(r[8 * v + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv);
-            d4[v] = w;
-          }
-        }
+      told = at.next(ring, it, true, abort_flag, p.status, kWaitLimit);
+      const bool done = bounded_wait_cluster(bar(C::kOFull), o_waits & 1u, abort_flag, p.status,
+                                             kWaitLimit);
+      ++o_waits;
+      if (!__all_sync(0xffffffffu, done)) {
+        told = false;
+        continue;   // (to the stop above)
       }
+      fence_after_sync();
+      uint32_t r[64], words[32];
+      tmem_ld32(lane_base + C::kColO + side * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(lane_base + C::kColO + side * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_wait_ld();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(o_free0);
+      const bool none = row_keys <= 0;   // the row sees no key (its sums are NaN)
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        words[e] = none ? 0u
+                        : pack_bf16x2(__uint_as_float(r[2 * e]) * inv,
+                                      __uint_as_float(r[2 * e + 1]) * inv);
+      store_rows(gbase + C::kOutOff + (warp - 2) * 4096, words, store ? dst : nullptr);
     }
   }
 

@@ -75,7 +75,8 @@ struct Cfg {
   static constexpr int kTileBytes = kTile * D * 2;          // one Q/K/V tile
   static constexpr int kQOff = 0;                           // Q0, Q1
   static constexpr int kRingOff = 2 * kTileBytes;
-  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kOutOff = kRingOff + kSlots * kTileBytes;   // 4 KB a softmax warp
+  static constexpr int kBarOff = kOutOff + 8 * 4096;
   // barriers: per Q tile t an S-full, a P-ready and an O-full barrier
   static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
                        kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots;
@@ -421,6 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     ItemInfo it;
     while (ok && next_item(it, ok)) {
+      it.nk = __shfl_sync(0xffffffffu, it.nk, 0);   // (uniform, as `warp` above)
+      it.rot = __shfl_sync(0xffffffffu, it.rot, 0);
       if (it.tokens <= t * p.tokens) continue;    // tile absent: nothing issued for it
       const int token = t * p.tokens + row_token;   // of the item
       __nv_bfloat16 *dst =
@@ -531,27 +534,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++o_waits;
       fence_after_sync();
       const float inv = 1.f / l;
+      const bool none = row_keys <= 0;   // the row sees no key (its sums are NaN)
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(lane_base + colO + c * 32, r);
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t r[64], words[32];
+        tmem_ld32(lane_base + colO + c * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        tmem_ld32(lane_base + colO + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
         tmem_wait_ld();
-        if (store) {
-          uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4 w;
-            if (row_keys <= 0) {   // it sees no key (its sums are NaN)
-              d4[v] = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            w.x = pack_bf16x2(__uint_as_float(r[8 * v + 0]) * inv, __uint_as_float(r[8 * v + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv);
-            d4[v] = w;
-          }
-        }
+        for (int e = 0; e < 32; ++e)
+          words[e] = none ? 0u
+                          : pack_bf16x2(__uint_as_float(r[2 * e]) * inv,
+                                        __uint_as_float(r[2 * e + 1]) * inv);
+        store_rows(gbase + C::kOutOff + (warp - 2) * 4096, words, store ? dst + c * 64 : nullptr);
       }
     }
   }
@@ -602,10 +597,10 @@ cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
 }  // namespace
 
 // Head dim 128 runs on the CTA-pair kernel; head dim 64 here, with a
-// ten-slot K/V ring beside a work list of up to PA_MAX_BATCH sequences.
+// nine-slot K/V ring beside a work list of up to PA_MAX_BATCH sequences.
 cudaError_t launch_varlen_attn(const VarlenArgs &a, cudaStream_t stream) {
   if (a.D == 128) return launch_varlen_attn_pair(a, stream);
-  return launch_tc<64, 10, PA_MAX_BATCH>(a, stream);
+  return launch_tc<64, 9, PA_MAX_BATCH>(a, stream);
 }
 
 }  // namespace pa

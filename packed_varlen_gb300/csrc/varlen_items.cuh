@@ -122,6 +122,32 @@ __device__ __forceinline__ int item_at(const VarlenParams &p, int n, int worker,
   return n * workers + (p.causal && (n & 1) ? workers - 1 - worker : worker);
 }
 
+// A warp's 32 rows of 128 bytes (64 columns), a row to a lane in `words`, out to
+// where `dst` of the row's lane says (nullptr: not stored), through 4 KB of shared
+// memory: eight lanes write a row, four rows an instruction, where rows stored by
+// their own lanes are 32 separate pieces of 16 bytes (the end of an item of 64 KB
+// took 3300 cycles so, and 1850 this way).  Pieces of a row are permuted against
+// bank conflicts.
+__device__ __forceinline__ void store_rows(uint8_t *buf, const uint32_t (&words)[32],
+                                           __nv_bfloat16 *dst) {
+  const int lane = threadIdx.x & 31, piece = lane & 7;
+#pragma unroll
+  for (int v = 0; v < 8; ++v)
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((v ^ piece) << 4)) =
+        make_uint4(words[4 * v], words[4 * v + 1], words[4 * v + 2], words[4 * v + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 4 + (lane >> 3);
+    uint4 *to = reinterpret_cast<uint4 *>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+    const uint4 x =
+        *reinterpret_cast<const uint4 *>(buf + row * 128 + ((piece ^ (row & 7)) << 4));
+    if (to) to[piece] = x;
+  }
+  __syncwarp();   // the buffer is free again
+}
+
 // The ring of items.  Finding an item takes a search and a chain of loads, some
 // thousand cycles, so a warp of its own does it ahead of the others; they read
 // what it found.  Full and empty barriers lie one after the other at `full`
