@@ -525,6 +525,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     int32_t *xs_ok = reinterpret_cast<int32_t *>(gbase + C::kXSumOkOff);  // [item parity][quad][side]
     const int to_me = quad * 2 + side, to_other = quad * 2 + (side ^ 1);
     const float sl2 = p.scale_log2;
+    const float head = p.causal ? kWeightHead : 0.f;
     const int row_token = row / p.G, row_head = row - row_token * p.G;   // of the tile, the group
     uint32_t g = 0, o_waits = 0;
     bool ok = true;
@@ -585,10 +586,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         if (j == 0) {
-          m = mx;
+          m = mx + head;
         } else if (mx > m_prev + kRescaleThreshold) {
-          alpha = ex2(m_prev - mx);
-          m = mx;
+          m = mx + head;
+          alpha = ex2(m_prev - m);
           rescale = true;
         } else {
           m = m_prev;

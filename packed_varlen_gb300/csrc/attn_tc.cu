@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t colS = C::kColS + t * kTile;
     const uint32_t colO = C::kColO + t * D;
     const float sl2 = p.scale_log2;
+    const float head = p.causal ? kWeightHead : 0.f;
     const bool pos_scale = sl2 > 0.f;
     const float mul = pos_scale ? sl2 : 1.f;
     const int row_token = row / p.G, row_head = row - row_token * p.G;   // of the tile, the group
@@ -475,10 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         if (j == 0) {
-          m = mx;
+          m = mx + head;
         } else if (mx > m + kRescaleThreshold) {
-          alpha = ex2(m - mx);
-          m = mx;
+          alpha = ex2(m - (mx + head));
+          m = mx + head;
           rescale = true;
         }
         const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-m, -m);
