@@ -145,7 +145,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return base + C::kBarOff + 8u * i; };
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem_raw + C::kMiscOff);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem_raw + C::kMiscOff + 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
 

@@ -3,8 +3,8 @@
 //
 // Few rows are bound by w's bytes (2 N K of them for 2 M N K operations), so the
 // work is split over the features, finely enough that every SM streams a part
-// of w: a CTA computes F features (a multiple of 8, at most 128) of up to 256 rows
-// of x.  The product is turned around: w is the MMA's A operand, its rows
+// of w: a CTA computes F features (a multiple of 8, at most 128) of R rows of x
+// (a multiple of 16, at most 256; few_plan).  The product is turned around: w is the MMA's A operand, its rows
 // the accumulator's TMEM lanes, and x is B, its rows the columns, so
 // a call of 13 rows pays for 16 columns and not for a tile of 128 rows.  An MMA
 // has 64 or 128 rows; where F is less, the rows of shared memory past F hold
@@ -15,7 +15,9 @@
 // same arithmetic, so rows come out with the same bits by either.
 //
 //   warp 0      TMA producer: groups of K-blocks of w and x into a ring
-//   warp 1      allocates TMEM, issues the MMAs
+//   warp 1      allocates TMEM, issues the MMAs (what bounds short calls: an MMA of
+//               few columns takes its issuer some 45 cycles and the tensor core
+//               less, so the loop has one branch a K-block and no divisions)
 //   warps 2-5   epilogue, a lane a feature: bias, activation, residual (read ahead of
 //               the accumulator's end), columns of y as runs of 32 features
 // Every wait is bounded; a timeout records PA_DEVICE_ERR_TIMEOUT.
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t acc_full = base + 8u * (2 * kMaxStages);
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem_raw + kMiscOff);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem_raw + kMiscOff + 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int n0 = blockIdx.x * p.features, m0 = blockIdx.y * p.rows;
   const int b_bytes = p.rows * kRowBytes;
   const int n_stages = (p.k_blocks + p.group - 1) / p.group;   // filled in all
@@ -97,18 +99,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(base + kMiscOff, p.tmem_cols);
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w);
+    if (kMode == kGated) tma_prefetch_desc(&tm_w2);
+  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_ptr;
+  // The next kernel of the stream may set itself up on the SMs that this one
+  // leaves; everything above ran beside the kernel before, whose results (and
+  // reads of y) the rest waits for.
+  griddep_launch_dependents();
+  griddep_wait();
 
   if (warp == 0) {
     const bool lead = elect_one();
-    if (lead) {
-      tma_prefetch_desc(&tm_x);
-      tma_prefetch_desc(&tm_w);
-      if (kMode == kGated) tma_prefetch_desc(&tm_w2);
-    }
     bool ok = true;
     int i = 0;
     for (; i < n_stages; ++i) {
@@ -138,25 +145,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc0 = sdesc_sw128(base + kRingOff, 16, 1024);
     bool ok = true;
     int i = 0;
+    uint32_t s = 0, parity = 0, more = 0;
     for (; i < n_stages; ++i) {
-      const uint32_t s = i % p.stages;
-      ok = bounded_wait(full(s), (i / p.stages) & 1u, abort_flag, p.status, kWaitLimit);
+      ok = bounded_wait(full(s), parity, abort_flag, p.status, kWaitLimit);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int blocks = min(p.group, p.k_blocks - i * p.group);
+      uint64_t a = desc0 + ((s * p.stage_bytes) >> 4);
+#pragma unroll 1
       for (int b = 0; b < blocks; ++b) {
-        const uint32_t off = s * p.stage_bytes + b * (kParts * kABytes + b_bytes);
-        const uint64_t a = desc0 + (off >> 4), x = desc0 + ((off + kParts * kABytes) >> 4);
+        const uint64_t x = a + ((kParts * kABytes) >> 4);
+        if (lead) {
+          mma_ss(tmem, a, x, p.idesc, more);
+          if (kMode == kGated) mma_ss(tmem + p.rows, a + (kABytes >> 4), x, p.idesc, more);
 #pragma unroll
-        for (int kk = 0; kk < kLinearBK / 16; ++kk)
-          if (lead) {
-            const uint32_t more = (i > 0 || b > 0 || kk > 0) ? 1u : 0u;
-            mma_ss(tmem, a + kk * 2, x + kk * 2, p.idesc, more);
+          for (int kk = 1; kk < kLinearBK / 16; ++kk) {
+            mma_ss(tmem, a + kk * 2, x + kk * 2, p.idesc, 1u);
             if (kMode == kGated)
-              mma_ss(tmem + p.rows, a + (kABytes >> 4) + kk * 2, x + kk * 2, p.idesc, more);
+              mma_ss(tmem + p.rows, a + (kABytes >> 4) + kk * 2, x + kk * 2, p.idesc, 1u);
           }
+        }
+        more = 1;
+        a += (kParts * kABytes + b_bytes) >> 4;
       }
       if (lead) mma_commit(empty(s));
+      if (++s == static_cast<uint32_t>(p.stages)) {
+        s = 0;
+        parity ^= 1u;
+      }
     }
     if (lead) mma_commit(acc_full);   // every MMA issued so far is done
     if (!ok) drain_wait(acc_full, 0, kWaitLimit);
@@ -230,8 +246,9 @@ pa_status launch(const GemmArgs &a, FewParams &p, cudaStream_t stream) {
     return from_cuda(cudaErrorInvalidValue);
   const int block = (kMode == kGated ? 2 : 1) * kM * kRowBytes + p.rows * kRowBytes;
   p.idesc = idesc_bf16_f32(kM, p.rows, false);
-  // stages of about 32 KB, so that a barrier stands for several copies and MMAs
-  p.group = 32768 / block > 1 ? 32768 / block : 1;
+  // Stages of up to 64 KB: what a barrier costs the issuer is spread over some
+  // twenty MMAs (13 rows, 4096 x 4096: stages of 32 KB 11.9 us, 64 KB 9.8).
+  p.group = 65536 / block > 1 ? 65536 / block : 1;
   if (p.group > p.k_blocks) p.group = p.k_blocks;
   p.stage_bytes = p.group * block;
   p.stages = kRingBytes / p.stage_bytes < kMaxStages ? kRingBytes / p.stage_bytes : kMaxStages;
@@ -241,19 +258,74 @@ pa_status launch(const GemmArgs &a, FewParams &p, cudaStream_t stream) {
       set_smem_once(reinterpret_cast<const void *>(kernel), kRingOff + kRingBytes, configured);
   if (e != cudaSuccess) return from_cuda(e);
   const dim3 grid((a.N + p.features - 1) / p.features, (a.M + p.rows - 1) / p.rows);
-  kernel<<<grid, kThreads, kRingOff + kRingBytes, stream>>>(mx, mw, mw2, p);
-  return from_cuda(cudaGetLastError());
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRingOff + kRingBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return from_cuda(cudaLaunchKernelEx(&cfg, kernel, mx, mw, mw2, p));
+}
+
+// How a call is cut: CTAs of F features x R rows, and its time in ns.
+struct FewPlan {
+  int features, rows;
+  int64_t ns;
+};
+
+// A CTA's K-block takes 75 + 1.33 R ns with an MMA of 64 rows (F <= 64) and
+// 95 + 1.5 R with 128, 1.75 times that where there are two weights; all CTAs
+// together get 9.7 TB/s out of L2 and 5.6 of w out of HBM; and a call costs 3 us
+// besides.  This holds for what was measured within some 15 %: 4096 x 4096,
+// 64 / 128 / 256 / 512 rows 12.2 / 13.2 / 15.4 / 22.2 us where the large kernel
+// takes 25 to 26 (a tile's 64 K-blocks at 345 ns), and 1024 rows 34.5, where it
+// takes 28; two weights of 11264 x 4096, 128 / 192 rows 38 / 53 against 48.
+FewPlan few_plan(const GemmArgs &a, int mode, int sms) {
+  const int64_t parts = mode == kGated ? 2 : 1, blocks = (a.K - 1) / kLinearBK + 1;
+  FewPlan best{0, 0, INT64_MAX};
+  for (int tiles_m = (a.M - 1) / 256 + 1; tiles_m <= 16 && tiles_m * 16 < a.M + 16; ++tiles_m) {
+    const int64_t rows = round_up((a.M - 1) / tiles_m + 1, 16);
+    // as few features as fill the SMs, in as few rounds as 128 of them allow
+    const int64_t across = sms / tiles_m > 0 ? sms / tiles_m : 1;
+    const int64_t rounds = (a.N - 1) / (128 * across) + 1;
+    const int64_t features = round_up(static_cast<int>((a.N - 1) / (rounds * across) + 1), 8);
+    const int64_t ctas = ((a.N - 1) / features + 1) * tiles_m, waves = (ctas - 1) / sms + 1;
+    int64_t block = features <= 64 ? 75 + rows * 4 / 3 : 95 + rows * 3 / 2;
+    if (parts == 2) block = block * 7 / 4;
+    const int64_t tile = waves * blocks * block;
+    const int64_t l2 = ctas * blocks * (parts * features + rows) * kRowBytes / 9700;
+    const int64_t hbm = parts * a.N * a.K * 2 / 5600;
+    int64_t ns = tile > l2 ? tile : l2;
+    ns = 3000 + (ns > hbm ? ns : hbm);
+    if (ns < best.ns)
+      best = FewPlan{static_cast<int>(features), static_cast<int>(rows), ns};
+  }
+  return best;
+}
+
+// The large kernel's time of the same call: a round of tiles of 256 x 256 on pairs
+// of SMs (of 128 features, where there are two weights).
+int64_t large_ns(const GemmArgs &a, int mode, int sms) {
+  const int64_t tile_n = mode == kGated ? 128 : 256;
+  const int64_t tiles = ((a.N - 1) / tile_n + 1) * ((int64_t{a.M} - 1) / 256 + 1);
+  return 3000 + ((tiles - 1) / (sms / 2) + 1) * ((a.K - 1) / kLinearBK + 1) * 345;
 }
 
 }  // namespace
 
 pa_status launch_linear_few(const GemmArgs &a, int mode, bool &taken, cudaStream_t stream) {
-  taken = a.M <= 128;
-  if (!taken) return PA_OK;
+  taken = false;
   FewParams p;
   int sms;
   const cudaError_t e = device_context(&p.status, &sms);
   if (e != cudaSuccess) return from_cuda(e);
+  const FewPlan plan = few_plan(a, mode, sms);
+  if (plan.ns > large_ns(a, mode, sms)) return PA_OK;
+  taken = true;
   p.bias = static_cast<const __nv_bfloat16 *>(a.bias);
   p.residual = static_cast<const __nv_bfloat16 *>(a.residual);
   p.y = static_cast<__nv_bfloat16 *>(a.y);
@@ -264,10 +336,8 @@ pa_status launch_linear_few(const GemmArgs &a, int mode, bool &taken, cudaStream
   p.N = a.N;
   p.K = a.K;
   p.k_blocks = (a.K - 1) / kLinearBK + 1;
-  p.rows = round_up(a.M, 16);
-  // as few features as fill the SMs, in as few rounds as 128 of them allow
-  const int rounds = (a.N - 1) / (128 * sms) + 1;
-  p.features = round_up((a.N - 1) / (rounds * sms) + 1, 8);
+  p.rows = plan.rows;
+  p.features = plan.features;
   const int cols = (mode == kGated ? 2 : 1) * p.rows;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>(cols)) p.tmem_cols *= 2;
