@@ -726,6 +726,12 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
+    try:
+        dev = t.get_device()
+        if dev >= 0:
+            return dev
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -772,12 +778,20 @@ def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     return out
 
 
-@functools.lru_cache(maxsize=256)
-def _host_ints(*values: int):
-    """The values as a host int32 array, and its address."""
-    _fits_32_bits("pa_rope_axes", *values)
-    arr = (ctypes.c_int32 * len(values))(*values)
-    return arr, ctypes.addressof(arr)
+_int_arrays = {}    # host int32 arrays by their values: a program has a few
+
+
+def _host_ints(values):
+    """The values as a host int32 array, how many they are, and its address."""
+    known = _int_arrays.get(values)
+    if known is None:
+        ints = [int(v) for v in values]
+        _fits_32_bits("pa_rope_axes", *[abs(v) for v in ints])
+        arr = (ctypes.c_int32 * len(ints))(*ints)
+        if len(_int_arrays) >= 256:
+            _int_arrays.clear()
+        known = _int_arrays[values] = (arr, len(ints), ctypes.addressof(arr))
+    return known
 
 
 def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, axis_dims,
@@ -810,9 +824,14 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
         kp, ko_p = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    dims, dims_at = _host_ints(*[int(d) for d in axis_dims])
-    _need(positions, "positions", _I32, 2)
-    if positions.shape != (len(dims), T) or positions.get_device() != dev:
+    dims, axes, dims_at = _host_ints(tuple(axis_dims))    # (dims: kept until the call is made)
+    try:
+        usual = positions.dtype is _I32 and positions.shape == (axes, T) and \
+            positions.get_device() == dev and positions.is_contiguous()
+    except _NOT_USUAL:
+        usual = False
+    if not usual:
+        _need(positions, "positions", _I32, 2)
         raise ValueError("positions must be [axes, T] on q's device")
     n_at = None
     if num_tokens is not None:
@@ -820,9 +839,9 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
         if num_tokens.numel() != 1 or num_tokens.get_device() != dev:
             raise ValueError("num_tokens must be one element on q's device")
         n_at = num_tokens.data_ptr()
-    args = (q.data_ptr(), kp, q_out.data_ptr(), ko_p, positions.data_ptr(), n_at, dims_at,
-            len(dims), T, qs, ks, qo, ko, Hq, Hkv, D, 1 if halves else 0, 1 if shared else 0,
-            float(base), _raw_stream(dev, stream))
+    args = (q.data_ptr(), kp, q_out.data_ptr(), ko_p, positions.data_ptr(), n_at, dims_at, axes, T,
+            qs, ks, qo, ko, Hq, Hkv, D, 1 if halves else 0, 1 if shared else 0, float(base),
+            _raw_stream(dev, stream))
     fn = lib.pa_rope_axes
     st = fn(*args) if _current_device() == dev else _call_on(dev, fn, args)
     if st != PA_OK:
@@ -832,6 +851,13 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
 
 def _matrix_stride(t: torch.Tensor, name: str, dev: int) -> int:
     """Elements from one row to the next of a bf16 matrix whose rows are contiguous."""
+    try:
+        M, N = t.shape
+        s0, s1 = t.stride()
+        if s1 == 1 and t.dtype is _BF16 and t.get_device() == dev:
+            return s0 if M > 1 else N
+    except _NOT_USUAL:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not _BF16:
@@ -847,10 +873,26 @@ def _matrix_stride(t: torch.Tensor, name: str, dev: int) -> int:
 
 
 def _weight(w: torch.Tensor, name: str, K: int, dev: int) -> int:
+    try:
+        N, k = w.shape
+        if k == K and w.dtype is _BF16 and w.get_device() == dev and w.is_contiguous():
+            return N
+    except _NOT_USUAL:
+        pass
     _need(w, name, _BF16, 2)
     if w.shape[1] != K or w.get_device() != dev:
         raise ValueError(f"{name} must be [N, {K}] on x's device, got {list(w.shape)}")
     return w.shape[0]
+
+
+def _need_vector(t: torch.Tensor, name: str, dtype, n: int, dev: int):
+    try:
+        if t.dtype is dtype and t.shape == (n,) and t.get_device() == dev and t.is_contiguous():
+            return
+    except _NOT_USUAL:
+        pass
+    _need(t, name, dtype, 1)
+    raise ValueError(f"{name} must be [{n}] on x's device")
 
 
 def _activation(act: str) -> int:
@@ -875,9 +917,7 @@ def linear_act_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
     b = r = None
     rs = 0
     if bias is not None:
-        _need(bias, "bias", _BF16, 1)
-        if bias.shape[0] != N or bias.get_device() != dev:
-            raise ValueError("bias must be [N] on x's device")
+        _need_vector(bias, "bias", _BF16, N, dev)
         b = bias.data_ptr()
     if residual is not None:
         rs = _matrix_stride(residual, "residual", dev)

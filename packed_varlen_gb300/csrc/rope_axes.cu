@@ -14,16 +14,19 @@
 // has an argument in [-1, 1).
 //
 // HBM bound: q and k are read and written once.  A warp's task is a token and
-// some of its heads.  A lane has a fixed place in its head, a vector of eight
-// elements (with halves, the two vectors of its pairs), so its fractions stay in
-// registers and its cos and sin, computed while the task's loads are in
-// flight, serve all of the task's heads.
+// its heads, or a share of them where the tokens are too few to fill the SMs.  A
+// lane has a fixed place in its head, a vector of eight elements (with halves,
+// the two vectors of its pairs), so its fractions stay in registers and its cos
+// and sin, computed while the task's first loads are in flight, serve all of
+// the task's heads.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "internal.h"
 #include "sched.cuh"
+#include "tc_ptx.cuh"
 
 namespace pa {
 namespace {
@@ -41,7 +44,8 @@ struct RopeParams {
   int total, Hq, Hkv, D;
   int width;                    // R
   int units;                    // lanes of a head
-  int heads_per_step, chunks;   // chunks: tasks of a token
+  int heads_per_step;
+  int chunks, steps;            // tasks of a token, and the steps of one
   uint64_t turn[kMaxPairs];     // theta_i / (2 pi), in 2^-64
   uint8_t axis[kMaxPairs];
 };
@@ -74,25 +78,30 @@ __device__ __forceinline__ float2 turned(int32_t position, uint64_t turn) {
   return cs;
 }
 
-// Heads a lane takes per task: 128 bytes of loads in flight.
-constexpr int steps_of(bool halves) { return halves ? 4 : 8; }
+// Heads of a lane at a time: 64 or 96 bytes in flight, with 24 warps an SM.  30269
+// tokens of 48 heads of 128: 115 us and 6.4 TB/s (four at a time 120); 9801 of 32
+// heads of 80, halves: 22.7 us and 4.4 TB/s (four at a time, 16 warps: 25.9).
+constexpr int batch_of(bool halves) { return halves ? 2 : 6; }
 
 // kHalves: pairs (i, i + R/2), else (2i, 2i + 1).  kElems: elements of a vector.
 template <bool kHalves, int kElems>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const __grid_constant__ RopeParams p) {
   using V = typename Vec<kElems>::type;
   constexpr int kPairs = kHalves ? kElems : kElems / 2;   // of a lane
-  constexpr int kSteps = steps_of(kHalves);
+  constexpr int kBatch = batch_of(kHalves);
   const int lane = threadIdx.x & 31;
   const int in_step = lane / p.units, u = lane - in_step * p.units;   // head of the step, place in it
   if (in_step >= p.heads_per_step) return;
   uint64_t turn[kPairs];
-  const int32_t *pos[kPairs];
+  uint32_t axes = 0;   // of the lane's pairs, four bits each
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
     turn[i] = p.turn[u * kPairs + i];
-    pos[i] = p.positions + static_cast<int64_t>(p.axis[u * kPairs + i]) * p.total;
+    axes |= static_cast<uint32_t>(p.axis[u * kPairs + i]) << (4 * i);
   }
+  // (as in linear_few.cu: what comes before ran beside the kernel before)
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
   const int total = p.num_tokens ? min(p.total, max(0, __ldg(p.num_tokens))) : p.total;
   const int heads = p.Hq + p.Hkv;
   const int a0 = u * kElems, b0 = a0 + p.width / 2;
@@ -100,54 +109,94 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_consta
   for (int task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); task < tasks;
        task += gridDim.x * (kThreads / 32)) {
     const int t = task / p.chunks, chunk = task - t * p.chunks;
-    const int h0 = chunk * kSteps * p.heads_per_step + in_step;
     const __nv_bfloat16 *q = p.q + t * p.q_stride, *k = p.k + t * p.k_stride;
     __nv_bfloat16 *q_out = p.q_out + t * p.q_out_stride, *k_out = p.k_out + t * p.k_out_stride;
-    V a[kSteps], b[kHalves ? kSteps : 1];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int h = h0 + s * p.heads_per_step;
-      if (h >= heads) break;
-      const __nv_bfloat16 *src = h < p.Hq ? q + static_cast<int64_t>(h) * p.D
-                                          : k + static_cast<int64_t>(h - p.Hq) * p.D;
-      a[s] = *reinterpret_cast<const V *>(src + a0);
-      if (kHalves) b[s] = *reinterpret_cast<const V *>(src + b0);
-    }
+    const int first = chunk * p.steps * p.heads_per_step + in_step;
+    const int end = min(heads, (chunk + 1) * p.steps * p.heads_per_step);
     float2 cs[kPairs];
+    for (int h0 = first; h0 < end; h0 += kBatch * p.heads_per_step) {
+      V a[kBatch], b[kHalves ? kBatch : 1];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) cs[i] = turned(__ldg(pos[i] + t), turn[i]);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int h = h0 + s * p.heads_per_step;
-      if (h >= heads) break;
-      uint32_t *aw = reinterpret_cast<uint32_t *>(&a[s]);
-      uint32_t *bw = reinterpret_cast<uint32_t *>(&b[kHalves ? s : 0]);
-#pragma unroll
-      for (int w = 0; w < kElems / 2; ++w) {
-        const float2 c0 = cs[kHalves ? 2 * w : w], c1 = cs[kHalves ? 2 * w + 1 : w];
-        const float x0 = lo_of(aw[w]), x1 = hi_of(aw[w]);
-        if (kHalves) {
-          const float y0 = lo_of(bw[w]), y1 = hi_of(bw[w]);
-          aw[w] = pack2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
-          bw[w] = pack2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
-        } else {
-          aw[w] = pack2(x0 * c0.x - x1 * c0.y, x0 * c0.y + x1 * c0.x);
-        }
-      }
-      __nv_bfloat16 *dst = h < p.Hq ? q_out + static_cast<int64_t>(h) * p.D
-                                    : k_out + static_cast<int64_t>(h - p.Hq) * p.D;
-      *reinterpret_cast<V *>(dst + a0) = a[s];
-      if (kHalves) *reinterpret_cast<V *>(dst + b0) = b[kHalves ? s : 0];
-      if (p.width < p.D) {   // elements past the rotated width
+      for (int s = 0; s < kBatch; ++s) {
+        const int h = h0 + s * p.heads_per_step;
+        if (h >= end) break;
         const __nv_bfloat16 *src = h < p.Hq ? q + static_cast<int64_t>(h) * p.D
                                             : k + static_cast<int64_t>(h - p.Hq) * p.D;
-        if (src != dst)
-          for (int at = p.width + a0; at < p.D; at += p.units * kElems)
-            *reinterpret_cast<V *>(dst + at) = *reinterpret_cast<const V *>(src + at);
+        a[s] = *reinterpret_cast<const V *>(src + a0);
+        if (kHalves) b[s] = *reinterpret_cast<const V *>(src + b0);
+      }
+      if (h0 == first) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const int64_t axis = (axes >> (4 * i)) & 15u;
+          cs[i] = turned(__ldg(p.positions + axis * p.total + t), turn[i]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const int h = h0 + s * p.heads_per_step;
+        if (h >= end) break;
+        uint32_t *aw = reinterpret_cast<uint32_t *>(&a[s]);
+        uint32_t *bw = reinterpret_cast<uint32_t *>(&b[kHalves ? s : 0]);
+#pragma unroll
+        for (int w = 0; w < kElems / 2; ++w) {
+          const float2 c0 = cs[kHalves ? 2 * w : w], c1 = cs[kHalves ? 2 * w + 1 : w];
+          const float x0 = lo_of(aw[w]), x1 = hi_of(aw[w]);
+          if (kHalves) {
+            const float y0 = lo_of(bw[w]), y1 = hi_of(bw[w]);
+            aw[w] = pack2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
+            bw[w] = pack2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
+          } else {
+            aw[w] = pack2(x0 * c0.x - x1 * c0.y, x0 * c0.y + x1 * c0.x);
+          }
+        }
+        __nv_bfloat16 *dst = h < p.Hq ? q_out + static_cast<int64_t>(h) * p.D
+                                      : k_out + static_cast<int64_t>(h - p.Hq) * p.D;
+        *reinterpret_cast<V *>(dst + a0) = a[s];
+        if (kHalves) *reinterpret_cast<V *>(dst + b0) = b[kHalves ? s : 0];
+        if (p.width < p.D) {   // elements past the rotated width
+          const __nv_bfloat16 *src = h < p.Hq ? q + static_cast<int64_t>(h) * p.D
+                                              : k + static_cast<int64_t>(h - p.Hq) * p.D;
+          if (src != dst)
+            for (int at = p.width + a0; at < p.D; at += p.units * kElems)
+              *reinterpret_cast<V *>(dst + at) = *reinterpret_cast<const V *>(src + at);
+        }
       }
     }
   }
 }
+
+// What a call's numbers say about every pair: theta / (2 pi) in 2^-64 of a turn, and
+// its axis.  64 powers take some 2 us, so each thread keeps the last call's.
+struct Spectrum {
+  int32_t axes = 0, shared = 0, dims[kMaxAxes] = {};
+  float base = 0.f;
+  uint64_t turn[kMaxPairs] = {};
+  uint8_t axis[kMaxPairs] = {};
+
+  bool of(const int32_t *d, int32_t n, int32_t s, float b) const {
+    if (n != axes || s != shared || b != base) return false;
+    for (int a = 0; a < n; ++a)
+      if (d[a] != dims[a]) return false;
+    return true;
+  }
+  void set(const int32_t *d, int32_t n, int32_t s, float b) {
+    axes = n;
+    shared = s;
+    base = b;
+    int width = 0, pair = 0;
+    for (int a = 0; a < n; ++a) width += dims[a] = d[a];
+    const double log2_base = log2(static_cast<double>(b));
+    for (int a = 0; a < n; ++a)
+      for (int j = 0; j < d[a] / 2; ++j, ++pair) {
+        const double power = s ? 2.0 * pair / width : 2.0 * j / d[a];
+        double turns = exp2(-power * log2_base) * 0.15915494309189533577;
+        turns -= floor(turns);   // (whole turns, with a base below 1)
+        turn[pair] = turns < 1.0 ? static_cast<uint64_t>(turns * 0x1p64) : 0;
+        axis[pair] = static_cast<uint8_t>(a);
+      }
+  }
+};
 
 }  // namespace
 }  // namespace pa
@@ -187,6 +236,7 @@ extern "C" pa_status pa_rope_axes(const void *q, const void *k, void *q_out, voi
       !aligned_to(k_out, 16) || !aligned_to(positions, 4) || !aligned_to(num_tokens, 4) ||
       ((q_stride | k_stride | q_out_stride | k_out_stride) & 7) != 0)
     return PA_ERR_MISALIGNED;
+  if (int64_t{total} * (Hq + Hkv) > (int64_t{1} << 30)) return PA_ERR_UNSUPPORTED;
   if (total == 0) return PA_OK;
   RopeParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -204,38 +254,41 @@ extern "C" pa_status pa_rope_axes(const void *q, const void *k, void *q_out, voi
   p.Hkv = Hkv;
   p.D = D;
   p.width = static_cast<int>(width);
-  const double log2_base = log2(static_cast<double>(base));
-  int pair = 0;
-  for (int a = 0; a < axes; ++a)
-    for (int j = 0; j < axis_dims[a] / 2; ++j, ++pair) {
-      const double power = shared ? 2.0 * pair / static_cast<double>(width)
-                                  : 2.0 * j / axis_dims[a];
-      // theta / (2 pi) of a turn; whole turns are dropped (a base below 1)
-      double turns = exp2(-power * log2_base) * 0.15915494309189533577;
-      turns -= floor(turns);
-      p.turn[pair] = turns < 1.0 ? static_cast<uint64_t>(turns * 0x1p64) : 0;
-      p.axis[pair] = static_cast<uint8_t>(a);
-    }
+  static thread_local Spectrum spectrum;
+  if (!spectrum.of(axis_dims, axes, shared != 0, base))
+    spectrum.set(axis_dims, axes, shared != 0, base);
+  memcpy(p.turn, spectrum.turn, sizeof(uint64_t) * (width / 2));
+  memcpy(p.axis, spectrum.axis, width / 2);
   // with halves a vector must not cross from one half into the other
   const int elems = halves && (width & 15) ? 4 : 8;
   p.units = static_cast<int>(width) / (halves ? 2 * elems : elems);   // (at most 32)
   p.heads_per_step = 32 / p.units;
-  const int heads_per_task = steps_of(halves != 0) * p.heads_per_step;
-  p.chunks = (Hq + Hkv + heads_per_task - 1) / heads_per_task;
-  const int64_t tasks = int64_t{total} * p.chunks;
-  if (tasks > (int64_t{1} << 30)) return PA_ERR_UNSUPPORTED;
   int32_t *status;
   int sms;
   const cudaError_t e = device_context(&status, &sms);
   if (e != cudaSuccess) return from_cuda(e);
+  // A token is shared out where whole ones leave the SMs short of 32 warps each,
+  // as far as a batch of loads a lane: cos and sin are then computed for each.
+  const int batch = batch_of(halves != 0);
+  const int all_steps = (Hq + Hkv - 1) / p.heads_per_step + 1;
+  const int most = (all_steps + batch - 1) / batch;
+  const int64_t want = (int64_t{sms} * 32 + total - 1) / total;
+  p.chunks = want < most ? static_cast<int>(want) : most;
+  p.steps = ((all_steps + p.chunks - 1) / p.chunks + batch - 1) / batch * batch;
+  p.chunks = (all_steps + p.steps - 1) / p.steps;
+  const int64_t tasks = int64_t{total} * p.chunks;
   const int64_t blocks = (tasks + kThreads / 32 - 1) / (kThreads / 32);
   const int grid = static_cast<int>(blocks < int64_t{sms} * 8 ? blocks : int64_t{sms} * 8);
-  auto s = reinterpret_cast<cudaStream_t>(stream);
-  if (halves && elems == 8)
-    rope_axes_kernel<true, 8><<<grid, kThreads, 0, s>>>(p);
-  else if (halves)
-    rope_axes_kernel<true, 4><<<grid, kThreads, 0, s>>>(p);
-  else
-    rope_axes_kernel<false, 8><<<grid, kThreads, 0, s>>>(p);
-  return from_cuda(cudaGetLastError());
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const auto kernel = !halves ? rope_axes_kernel<false, 8>
+                              : elems == 8 ? rope_axes_kernel<true, 8> : rope_axes_kernel<true, 4>;
+  return from_cuda(cudaLaunchKernelEx(&cfg, kernel, p));
 }
