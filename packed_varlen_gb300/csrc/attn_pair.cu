@@ -127,45 +127,52 @@ struct Walk {
   }
 };
 
-// Row maximum of 128 raw scores (TMEM words), over the first `valid` keys
-// (masked: some row of the warp has fewer than 128);
-// with a positive scale the maximum of the raw scores is scaled once,
-// otherwise every score is scaled first.  The unmasked positive-scale form
-// (every tile but a sequence's last) is three-input max chains only.
-__device__ __forceinline__ float tile_max(const uint32_t (&sr)[kTile], int valid, bool masked,
-                                          float sl2) {
+// Row maximum of 128 raw scores (TMEM words): three-input max chains.
+__device__ __forceinline__ float tile_max(const uint32_t (&sr)[kTile]) {
   float mx8[8];
-  if (sl2 > 0.f && !masked) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      mx8[e] = fmaxf(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+  for (int e = 0; e < 8; ++e)
+    mx8[e] = fmaxf(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
 #pragma unroll
-    for (int c = 8; c < kTile / 2; ++c)
-      mx8[c & 7] = fmax3(mx8[c & 7], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < kTile; ++c) {
-      float v = __uint_as_float(sr[c]);
-      if (!(sl2 > 0.f)) v *= sl2;
-      if (c >= valid) v = -INFINITY;
-      mx8[c & 7] = fmaxf(mx8[c & 7], v);
-    }
-  }
-  const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                         fmaxf(mx8[6], mx8[7]));
-  return sl2 > 0.f ? mx * sl2 : mx;
+  for (int c = 8; c < kTile / 2; ++c)
+    mx8[c & 7] = fmax3(mx8[c & 7], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
+  return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+               fmaxf(mx8[6], mx8[7]));
 }
 
-// P = 2^(s * scale_log2 - m) for the 128 keys of one TMEM lane's S row at
-// `taddr`, 64 at a time, written as bf16 pairs over the row's first 64
-// columns; adds P to the eight partial sums.  kMasked: keys from `valid` on
-// get P = 0 (a sequence's last key tile, tiles that causal order cuts).
-template <bool kMasked>
-__device__ __forceinline__ void tile_p(uint32_t taddr, int valid, float sl2, float m,
-                                       float2 (&sum8)[8]) {
-  const float2 sl22 = make_float2(sl2, sl2), negm2 = make_float2(-m, -m);
+// Rewrites one TMEM lane's S row where a score is hidden (key `valid` and those after it)
+// or the scale is not positive, and returns the maximum of the scaled scores:
+// hidden scores become the infinity that scales to -inf, and with a scale of 0
+// the others 0 (`mul` is 1 then).  A few tiles of an item take this way, and it is
+// a loop of 32 columns so that the code of the others stays small: with masked
+// forms of the whole tile beside the plain ones, instructions were fetched
+// anew for every item.
+__device__ __forceinline__ float hide(uint32_t taddr, int valid, float sl2, float mul) {
+  const float hidden = sl2 < 0.f ? INFINITY : -INFINITY;
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 32) {
+    uint32_t r[32];
+    tmem_ld32(taddr + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      float v = sl2 == 0.f ? 0.f : __uint_as_float(r[e]);
+      if (c + e >= valid) v = hidden;
+      mx = fmaxf(mx, v * mul);
+      r[e] = __float_as_uint(v);
+    }
+    tmem_st32(taddr + c, r);
+  }
+  tmem_wait_st();
+  return mx;
+}
+
+// P = 2^(s * mul - m) for the 128 keys of one TMEM lane's S row at `taddr`, 64 at
+// a time, written as bf16 pairs over the row's first 64 columns; adds P to the
+// eight partial sums.
+__device__ __forceinline__ void tile_p(uint32_t taddr, float mul, float m, float2 (&sum8)[8]) {
+  const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-m, -m);
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     uint32_t sr[64];
@@ -175,12 +182,8 @@ __device__ __forceinline__ void tile_p(uint32_t taddr, int valid, float sl2, flo
     uint32_t pk[32];
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-      float2 tt = __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])),
-                             sl22, negm2);
-      if (kMasked) {
-        if (hh * 64 + 2 * c >= valid) tt.x = -INFINITY;
-        if (hh * 64 + 2 * c + 1 >= valid) tt.y = -INFINITY;
-      }
+      const float2 tt = __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])),
+                                   mul2, negm2);
       const float2 pp = make_float2(ex2(tt.x), ex2(tt.y));
       sum8[c & 7] = __fadd2_rn(sum8[c & 7], pp);
       pk[c] = pack_bf16x2(pp.x, pp.y);
@@ -524,7 +527,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     float *xs = reinterpret_cast<float *>(gbase + C::kXSumOff);         // [item parity][quad][side][lane][2]
     int32_t *xs_ok = reinterpret_cast<int32_t *>(gbase + C::kXSumOkOff);  // [item parity][quad][side]
     const int to_me = quad * 2 + side, to_other = quad * 2 + (side ^ 1);
-    const float sl2 = p.scale_log2;
+    const float sl2 = p.scale_log2, mul = sl2 != 0.f ? sl2 : 1.f;
     const float head = p.causal ? kWeightHead : 0.f;
     const int row_token = row / p.G, row_head = row - row_token * p.G;   // of the tile, the group
     uint32_t g = 0, o_waits = 0;
@@ -568,13 +571,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         float mx = -INFINITY;
         if (okt) {
           fence_after_sync();
+          const bool special = masked || !(sl2 > 0.f);
+          float top = 0.f;
+          if (special) top = hide(lane_base + b * kTile, valid, sl2, mul);
           uint32_t sr[kTile];
 #pragma unroll
           for (int c = 0; c < kTile / 32; ++c)
             tmem_ld32(lane_base + b * kTile + c * 32,
                       *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           tmem_wait_ld();
-          mx = tile_max(sr, valid, masked, sl2);
+          mx = tile_max(sr) * mul;
+          if (special) mx = top;
         }
         // the running maximum after the previous tile (the other warp's)
         float m_prev = -INFINITY;
@@ -618,10 +625,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         float2 sum8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum8[e] = make_float2(0.f, 0.f);
-        if (!masked)
-          tile_p<false>(lane_base + b * kTile, valid, sl2, m, sum8);
-        else
-          tile_p<true>(lane_base + b * kTile, valid, sl2, m, sum8);
+        tile_p(lane_base + b * kTile, mul, m, sum8);
         const float2 s01 = __fadd2_rn(__fadd2_rn(sum8[0], sum8[1]), __fadd2_rn(sum8[2], sum8[3]));
         const float2 s45 = __fadd2_rn(__fadd2_rn(sum8[4], sum8[5]), __fadd2_rn(sum8[6], sum8[7]));
         const float2 s8 = __fadd2_rn(s01, s45);
