@@ -140,18 +140,21 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sr)[kTile]) {
                fmaxf(mx8[6], mx8[7]));
 }
 
-// Rewrites one TMEM lane's S row where a score is hidden (key `valid` and those after it)
-// or the scale is not positive, and returns the maximum of the scaled scores:
-// hidden scores become the infinity that scales to -inf, and with a scale of 0
-// the others 0 (`mul` is 1 then).  A few tiles of an item take this way, and it is
-// a loop of 32 columns so that the code of the others stays small: with masked
-// forms of the whole tile beside the plain ones, instructions were fetched
-// anew for every item.
+// Whole warp: rewrites each TMEM lane's S row (128 scores at `taddr`) where a score is
+// hidden (key `valid` and those after it) or the scale is not positive; then it
+// also returns the maximum of the scaled scores.  Hidden scores become the
+// infinity that scales to -inf; with a scale of 0 (`mul` is 1 then) the others
+// become 0.  A few tiles of an item take this way, in a loop of 32 columns, so that
+// the code of the others stays small: with masked forms of the whole tile beside
+// the plain ones, instructions were fetched anew for every item (64 prompts of 300
+// tokens, 32 heads on 8: 182 us, 137 this way).
 __device__ __forceinline__ float hide(uint32_t taddr, int valid, float sl2, float mul) {
   const float hidden = sl2 < 0.f ? INFINITY : -INFINITY;
   float mx = -INFINITY;
+  // with a positive scale only from the first hidden score of any lane
+  const int most = sl2 > 0.f ? __reduce_max_sync(0xffffffffu, kTile - valid) : kTile;
 #pragma unroll 1
-  for (int c = 0; c < kTile; c += 32) {
+  for (int c = max(0, kTile - most) & ~31; c < kTile; c += 32) {
     uint32_t r[32];
     tmem_ld32(taddr + c, r);
     tmem_wait_ld();
@@ -269,7 +272,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t loads = 0, q_loads = 0, tails = 0;
     bool ok = true, tail_pending = false;
     auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
-      const bool w = bounded_wait_cluster(b, parity, abort_flag, p.status, kWaitLimit);
+      const bool w = bounded_wait_cluster_small(b, parity, abort_flag, p.status, kWaitLimit);
       return __all_sync(0xffffffffu, w);
     };
     // next ring slot in load order, once the MMAs that read it are done
@@ -363,10 +366,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       kw.next(ring, abort_flag, p.status);
       return true;
     };
-    for (int t = 0; t < kSBufs && ok; ++t) ok = next_k();
-    while (ok && !vw.done()) {
-      ok = load_v(vw);
-      vw.next(ring, abort_flag, p.status);
+    for (int t = 0; ok && !vw.done(); ++t) {
+      if (t >= kSBufs) {
+        ok = load_v(vw);
+        vw.next(ring, abort_flag, p.status);
+      }
       if (ok) ok = next_k();
     }
     ok = ok && kw.ok && vw.ok;
@@ -458,43 +462,43 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         kw.next(ring, abort_flag, p.status);
         return true;
       };
-      if (!vw.done())
-        for (int t = 0; t < kSBufs && ok; ++t) ok = issue_s();
-      while (ok && !vw.done()) {
-        const uint32_t b = gv % kSBufs;
-        // P_gv written by the pair's 16 softmax warps
-        if (!wait_all(bar(C::kPReady + b), (gv / kSBufs) & 1u)) {
-          ok = false;
-          break;
-        }
-        // the first PV of an item writes over the O of the item before it
-        if (vw.j == 0 && outs > 0 && !wait_all(bar(C::kOFree), (outs - 1) & 1u)) {
-          ok = false;
-          break;
-        }
-        fence_after_sync();
-        uint32_t s;
-        if (!next_slot(s)) {
-          ok = false;
-          break;
-        }
-        // O += P V (P, bf16, over the first 64 columns of the S buffer)
-        const uint64_t b0 = vdesc0 + ((s * C::kSlotBytes) >> 4);
-        const uint32_t d_p = tmem + b * kTile;
+      for (int t = 0; ok && !vw.done(); ++t) {
+        if (t >= kSBufs) {
+          const uint32_t b = gv % kSBufs;
+          // P_gv written by the pair's 16 softmax warps
+          if (!wait_all(bar(C::kPReady + b), (gv / kSBufs) & 1u)) {
+            ok = false;
+            break;
+          }
+          // the first PV of an item writes over the O of the item before it
+          if (vw.j == 0 && outs > 0 && !wait_all(bar(C::kOFree), (outs - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          fence_after_sync();
+          uint32_t s;
+          if (!next_slot(s)) {
+            ok = false;
+            break;
+          }
+          // O += P V (P, bf16, over the first 64 columns of the S buffer)
+          const uint64_t b0 = vdesc0 + ((s * C::kSlotBytes) >> 4);
+          const uint32_t d_p = tmem + b * kTile;
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) {
-          if (lead)
-            mma_ts_pair(tmem + C::kColO, d_p + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescO,
-                        (vw.j == 0 && kk == 0) ? 0u : 1u);
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            if (lead)
+              mma_ts_pair(tmem + C::kColO, d_p + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescO,
+                          (vw.j == 0 && kk == 0) ? 0u : 1u);
+          }
+          issued = true;
+          if (vw.j == vw.it.nk - 1) {
+            commit_both(bar(C::kOFull));
+            ++outs;
+          }
+          commit_both(bar(C::kSlotEmpty + s));
+          ++gv;
+          vw.next(ring, abort_flag, p.status);
         }
-        issued = true;
-        if (vw.j == vw.it.nk - 1) {
-          commit_both(bar(C::kOFull));
-          ++outs;
-        }
-        commit_both(bar(C::kSlotEmpty + s));
-        ++gv;
-        vw.next(ring, abort_flag, p.status);
         ok = issue_s();
       }
       // every MMA issued so far has finished before TMEM is released
@@ -581,7 +585,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
                       *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           tmem_wait_ld();
           mx = tile_max(sr) * mul;
-          if (special) mx = top;
+          if (!(sl2 > 0.f)) mx = top;
         }
         // the running maximum after the previous tile (the other warp's)
         float m_prev = -INFINITY;
@@ -637,14 +641,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         // rescale O in place (PV_{g-1} is done, PV_g waits for this warp)
         if (any_rescale) {
           fence_after_sync();
-#pragma unroll
-          for (int c = 0; c < kD / 32; ++c) {
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 32) {
             uint32_t r[32];
-            tmem_ld32(lane_base + C::kColO + c * 32, r);
+            tmem_ld32(lane_base + C::kColO + c, r);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tmem_st32(lane_base + C::kColO + c * 32, r);
+            tmem_st32(lane_base + C::kColO + c, r);
           }
         }
         tmem_wait_st();

@@ -58,18 +58,18 @@ __device__ __forceinline__ SeqBounds seq_bounds(const int32_t *__restrict__ cu_q
 // memory the caller reuses afterwards).  All threads of the CTA call it; it
 // ends with __syncthreads().  Item count = prefix[batch].
 //
-// kLevels: the list of causal attention, where a query tile's work grows with
+// levels: the list of causal attention, where a query tile's work grows with
 // its place in the sequence.  Sequences are sorted by query length, and the
 // items go level by level, the last tiles first: level t holds tile t of every
 // sequence that has one, which are the first s + 1 of the order for t in
 // [T_{s+1}, T_s), T_s the tiles of sequence order[s].  prefix[s] counts the
 // items before that stretch of levels (sched_level_item decodes them).
-template <bool kLevels = false>
 __device__ inline void sched_build(int32_t *order, int32_t *prefix, int32_t *tmp_lq,
                                    int32_t *tmp_lk, const int32_t *__restrict__ cu_q,
                                    const int32_t *__restrict__ cu_k, int batch, int H,
                                    int tile_m, int total_q, int total_k, int max_q,
-                                   int max_k, int32_t *status, bool report) {
+                                   int max_k, int32_t *status, bool report,
+                                   bool levels = false) {
   const int tid = threadIdx.x, nt = blockDim.x;
   for (int b = tid; b < batch; b += nt) {
     int err;
@@ -80,7 +80,7 @@ __device__ inline void sched_build(int32_t *order, int32_t *prefix, int32_t *tmp
   }
   __syncthreads();
   // Rank sort by (key length descending, index ascending).
-  const int32_t *by = kLevels ? tmp_lq : tmp_lk;
+  const int32_t *by = levels ? tmp_lq : tmp_lk;
   for (int b = tid; b < batch; b += nt) {
     const int lb = by[b];
     int rank = 0;
@@ -98,7 +98,7 @@ __device__ inline void sched_build(int32_t *order, int32_t *prefix, int32_t *tmp
       const int idx = base + tid;
       int cnt = 0;
       if (idx < batch) cnt = H * ((tmp_lq[order[idx]] + tile_m - 1) / tile_m);
-      if (kLevels && idx < batch) {   // (the items of this stretch of levels)
+      if (levels && idx < batch) {   // (the items of this stretch of levels)
         const int below = idx + 1 < batch ? (tmp_lq[order[idx + 1]] + tile_m - 1) / tile_m : 0;
         cnt = (cnt - H * below) * (idx + 1);
       }
@@ -137,7 +137,7 @@ __device__ __forceinline__ WorkItem sched_item(const int32_t *order, const int32
   return w;
 }
 
-// Item i of a list built with kLevels.  Within a level the sequences in order,
+// Item i of a list built by levels.  Within a level the sequences in order,
 // heads innermost, so that heads which share a K/V head run side by side.
 __device__ __forceinline__ WorkItem sched_level_item(const int32_t *order, const int32_t *prefix,
                                                      const int32_t *__restrict__ cu_q, int batch,

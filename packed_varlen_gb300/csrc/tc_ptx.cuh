@@ -213,6 +213,32 @@ __device__ __forceinline__ bool bounded_wait_cluster(uint32_t bar, uint32_t pari
   }
 }
 
+// The same with the polling in a function of its own, for roles with many waits
+// and few registers: a wait in place is some forty instructions, and the warps of
+// a CTA that all stream through their code again and again share the
+// instruction cache.
+__device__ __noinline__ inline bool poll_cluster(uint32_t bar, uint32_t parity,
+                                                 volatile int32_t *abort_flag, int32_t *status,
+                                                 long long limit) {
+  return bounded_wait_cluster(bar, parity, abort_flag, status, limit);
+}
+__device__ __forceinline__ bool bounded_wait_cluster_small(uint32_t bar, uint32_t parity,
+                                                           volatile int32_t *abort_flag,
+                                                           int32_t *status, long long limit) {
+  return mbar_try_wait_cluster(bar, parity) || poll_cluster(bar, parity, abort_flag, status, limit);
+}
+
+__device__ __noinline__ inline bool poll_cta(uint32_t bar, uint32_t parity,
+                                             volatile int32_t *abort_flag, int32_t *status,
+                                             long long limit) {
+  return bounded_wait(bar, parity, abort_flag, status, limit);
+}
+__device__ __forceinline__ bool bounded_wait_small(uint32_t bar, uint32_t parity,
+                                                   volatile int32_t *abort_flag, int32_t *status,
+                                                   long long limit) {
+  return mbar_try_wait(bar, parity) || poll_cta(bar, parity, abort_flag, status, limit);
+}
+
 // Named CTA barrier `id` (1..15) over `count` threads (a multiple of 32):
 // wait for all of them, or (arrive) count this warp in and go on.  The
 // writes a thread made before either are visible to the threads that waited.

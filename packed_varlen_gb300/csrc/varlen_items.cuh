@@ -107,12 +107,8 @@ __device__ __forceinline__ ItemInfo item_info(const VarlenParams &p, const int32
 // The work list of a kernel, in shared memory (see sched_build).
 __device__ __forceinline__ void item_list(const VarlenParams &p, int32_t *order, int32_t *prefix,
                                           int32_t *tmp_lq, int32_t *tmp_lk, bool report) {
-  if (p.causal)
-    sched_build<true>(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H / p.G,
-                      2 * p.tokens, p.total_q, p.total_k, p.max_q, p.max_k, p.status, report);
-  else
-    sched_build(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H / p.G, 2 * p.tokens,
-                p.total_q, p.total_k, p.max_q, p.max_k, p.status, report);
+  sched_build(order, prefix, tmp_lq, tmp_lk, p.cu_q, p.cu_k, p.batch, p.H / p.G, 2 * p.tokens,
+              p.total_q, p.total_k, p.max_q, p.max_k, p.status, report, p.causal != 0);
 }
 
 // The worker's n-th item, of `workers`: round robin; in a causal list, whose
