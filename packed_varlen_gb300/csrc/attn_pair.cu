@@ -250,6 +250,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(base + C::kMiscOff, C::kTmemCols);
+  // (launch_beside: everything above ran beside the kernel before)
+  griddep_launch_dependents();
+  griddep_wait();
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
   item_list(p, order, prefix, tmp, tmp + PA_MAX_BATCH, blockIdx.x == 0);
@@ -738,8 +741,8 @@ cudaError_t launch_varlen_attn_pair(const VarlenArgs &a, cudaStream_t stream) {
                                 PairCfg::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   const int grid = a.num_sms / kCluster * kCluster;   // whole pairs, one CTA per SM
-  varlen_attn_pair_kernel<<<grid, kThreads, PairCfg::kSmemBytes, stream>>>(mq, mk, mv, p);
-  return cudaGetLastError();
+  return launch_beside(varlen_attn_pair_kernel, dim3(grid), kThreads, PairCfg::kSmemBytes, stream,
+                       mq, mk, mv, p);
 }
 
 }  // namespace pa

@@ -166,6 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(base + C::kMiscOff, C::kTmemCols);
+  // (launch_beside: everything above ran beside the kernel before)
+  griddep_launch_dependents();
+  griddep_wait();
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
   item_list(p, order, prefix, tmp, tmp + kMaxSeqs, blockIdx.x == 0);
@@ -593,8 +596,7 @@ cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
   static unsigned long long configured = 0;
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), smem, configured);
   if (e != cudaSuccess) return e;
-  kernel<<<a.num_sms, kThreads, smem, stream>>>(mq, mk, mv, p);
-  return cudaGetLastError();
+  return launch_beside(kernel, dim3(a.num_sms), kThreads, smem, stream, mq, mk, mv, p);
 }
 
 }  // namespace

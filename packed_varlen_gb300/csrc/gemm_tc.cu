@@ -169,6 +169,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();   // barriers of both CTAs initialised before any remote use
   fence_after_sync();
   const uint32_t tmem = *tmem_ptr;
+  // (launch_beside: everything above ran beside the kernel before)
+  griddep_launch_dependents();
+  griddep_wait();
   const int cl = blockIdx.x / kCluster, n_cl = gridDim.x / kCluster;
 
   if (warp == 0) {
@@ -416,9 +419,8 @@ pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
   // whole clusters, at most one CTA per SM
   const int max_ctas = sms / kCluster * kCluster;
   const int grid = kCluster * p.n_pairs < max_ctas ? kCluster * p.n_pairs : max_ctas;
-  linear_bf16_kernel<kMode><<<grid, kThreads, GemmCfg::kSmemBytes, stream>>>(mx, mw, mw2, mr, my,
-                                                                               p);
-  return from_cuda(cudaGetLastError());
+  return from_cuda(launch_beside(linear_bf16_kernel<kMode>, dim3(grid), kThreads,
+                                 GemmCfg::kSmemBytes, stream, mx, mw, mw2, mr, my, p));
 }
 
 // Largest row stride, in elements (TMA strides are below 2^40 bytes).

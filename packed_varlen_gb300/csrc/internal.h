@@ -64,6 +64,26 @@ inline cudaError_t set_smem_once(const void *kernel, int smem, unsigned long lon
   return e;
 }
 
+// Launches `kernel` so that it may set itself up (barriers, TMEM, descriptors)
+// while the kernel before it on the stream ends: it must execute griddep_wait()
+// before its first access to global memory, and griddep_launch_dependents() lets
+// the next one do the same.
+template <typename... P, typename... A>
+cudaError_t launch_beside(void (*kernel)(P...), dim3 grid, int threads, int smem,
+                          cudaStream_t stream, const A &...args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Device address of the per-device status word and the SM count of the
 // current device (api.cu).
 cudaError_t device_context(int32_t **status, int *num_sms);

@@ -108,9 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_ptr;
-  // The next kernel of the stream may set itself up on the SMs that this one
-  // leaves; everything above ran beside the kernel before, whose results (and
-  // reads of y) the rest waits for.
+  // (launch_beside: everything above ran beside the kernel before)
   griddep_launch_dependents();
   griddep_wait();
 
@@ -258,17 +256,8 @@ pa_status launch(const GemmArgs &a, FewParams &p, cudaStream_t stream) {
       set_smem_once(reinterpret_cast<const void *>(kernel), kRingOff + kRingBytes, configured);
   if (e != cudaSuccess) return from_cuda(e);
   const dim3 grid((a.N + p.features - 1) / p.features, (a.M + p.rows - 1) / p.rows);
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRingOff + kRingBytes;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return from_cuda(cudaLaunchKernelEx(&cfg, kernel, mx, mw, mw2, p));
+  return from_cuda(launch_beside(kernel, grid, kThreads, kRingOff + kRingBytes, stream, mx, mw,
+                                 mw2, p));
 }
 
 // How a call is cut: CTAs of F features x R rows, and its time in ns.

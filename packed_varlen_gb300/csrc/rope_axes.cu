@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const __grid_con
     turn[i] = p.turn[u * kPairs + i];
     axes |= static_cast<uint32_t>(p.axis[u * kPairs + i]) << (4 * i);
   }
-  // (as in linear_few.cu: what comes before ran beside the kernel before)
+  // (launch_beside: everything above ran beside the kernel before)
   tc::griddep_launch_dependents();
   tc::griddep_wait();
   const int total = p.num_tokens ? min(p.total, max(0, __ldg(p.num_tokens))) : p.total;
@@ -279,16 +279,8 @@ extern "C" pa_status pa_rope_axes(const void *q, const void *k, void *q_out, voi
   const int64_t tasks = int64_t{total} * p.chunks;
   const int64_t blocks = (tasks + kThreads / 32 - 1) / (kThreads / 32);
   const int grid = static_cast<int>(blocks < int64_t{sms} * 8 ? blocks : int64_t{sms} * 8);
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   const auto kernel = !halves ? rope_axes_kernel<false, 8>
                               : elems == 8 ? rope_axes_kernel<true, 8> : rope_axes_kernel<true, 4>;
-  return from_cuda(cudaLaunchKernelEx(&cfg, kernel, p));
+  return from_cuda(launch_beside(kernel, dim3(grid), kThreads, 0,
+                                 reinterpret_cast<cudaStream_t>(stream), p));
 }
