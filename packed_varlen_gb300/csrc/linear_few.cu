@@ -108,6 +108,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_ptr;
+  // w on its way from HBM to L2 for the first stages, before the kernel before
+  // has ended (the copies below come after it)
+  if (warp == 0 && blockIdx.y == 0 && elect_one()) {
+    const int ahead = min(p.k_blocks, p.stages * p.group);
+    for (int b = 0; b < ahead; ++b) {
+      tma_prefetch_2d(&tm_w, b * kLinearBK, n0);
+      if (kMode == kGated) tma_prefetch_2d(&tm_w2, b * kLinearBK, n0);
+    }
+  }
+  __syncwarp();
   // (launch_beside: everything above ran beside the kernel before)
   griddep_launch_dependents();
   griddep_wait();

@@ -118,6 +118,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// 2-D tile into L2 alone: nothing is read, so this may come before other kernels'
+// writes to it are done.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // 2-D tiled store from shared memory, part of this thread's current group of
 // copies (the part of the box past the tensor's ends is not written); closing
 // that group; and waiting until every group of this thread has been read out of
