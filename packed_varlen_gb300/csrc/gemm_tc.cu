@@ -370,6 +370,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!landed_ok) break;
     }
+    if (lead) bulk_wait();
     if (taken != loads) drain_wait(landed, taken & 1u, kDrainLimit);   // after an abort
   }
 
