@@ -137,7 +137,9 @@ pa_status pa_varlen_attn_fwd(const void *q, const void *k, const void *v, void *
  * (total_q = 0 or max_q = 0 does nothing; q and out, k and v may be NULL where
  * their total is 0); max_q / max_k bound every length; Hq a multiple of Hkv
  * and at most 65535, Hq / Hkv <= 128; (total_q * Hq / 128 + batch * Hkv at most
- * 2^30); D in {64, 128}; scale and scale * log2(e) finite.
+ * 2^30); D in {64, 128}; scale and scale * log2(e) finite, and scores of at most
+ * 2^29 in size once scaled by it (the rounding of a larger one can leave the
+ * exponent's range).
  * Rows outside a sequence never reach its result, whatever their bits.  A key
  * that causal order hides from a query has weight zero there; a NaN or infinity
  * in its V row can still reach that query as 0 * NaN (in its K row it cannot).
@@ -476,8 +478,8 @@ pa_status pa_linear_bf16(const void *x, const void *w, const void *bias, void *y
  * not overlap x, w, bias or the residual otherwise.  Accumulation, activation
  * and sums are fp32, rounded to bf16 once.  A row depends on its own x and
  * residual row, w and bias alone: packed, alone or at any row offset its bits
- * agree.  M >= 0 (0 does nothing; x and y may then be NULL), N >= 1, K >= 1; K
- * and N multiples of 8; every pointer 16-byte aligned.
+ * agree.  M >= 0 (0 does nothing; x and y may then be NULL), N >= 1, K in
+ * [1, 2^26]; K and N multiples of 8; every pointer 16-byte aligned.
  */
 pa_status pa_linear_act_bf16(const void *x, const void *w, const void *bias,
                              const void *residual, void *y, int32_t M, int32_t N, int32_t K,

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 from typing import Optional
 
@@ -785,7 +786,7 @@ def _host_ints(values):
     """The values as a host int32 array, how many they are, and its address."""
     known = _int_arrays.get(values)
     if known is None:
-        ints = [int(v) for v in values]
+        ints = [operator.index(v) for v in values]
         _fits_32_bits("pa_rope_axes", *[abs(v) for v in ints])
         arr = (ctypes.c_int32 * len(ints))(*ints)
         if len(_int_arrays) >= 256:

@@ -33,7 +33,11 @@
 //               warps, which share a scheduler, run half a tile apart.  P
 //               (bf16) is written over the first 64 columns of the S buffer.
 //               The same warps rescale O (when a row maximum grew by more
-//               than 2^8) and run the epilogue, 64 columns each.
+//               than 2^8, or 2^32 in causal calls: kWeightHead) and run the
+//               epilogue, 64 columns each, a row's part through shared memory
+//               (store_rows).  kOFree tells the issuer that both CTAs' warps
+//               have read O before the next item's first PV overwrites it.
+//   warp 10     finds the items ahead of the others (tell_items).
 // Every output row is computed by one CTA in a fixed key-tile order that
 // depends only on its own sequence, so results do not depend on the rest of
 // the batch.  Key columns past the sequence end are masked to -inf (P = 0)
@@ -63,6 +67,7 @@ constexpr int kThreads = 352;       // producer, MMA issuer, 8 softmax warps, it
 constexpr int kQBufs = 2;           // Q tile buffers
 constexpr int kSlots = 7;           // K/V ring slots (9 were no faster)
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
+constexpr long long kItemWaitLimit = 32 * kWaitLimit;   // of the item finder: whole items long
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 
@@ -514,7 +519,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kThreads / 32 - 1) {
     // ================= the items, ahead of everyone =================
     tell_items(p, order, prefix, blockIdx.x / kCluster, gridDim.x / kCluster, ring, kD,
-               static_cast<int>(rank), kCluster, abort_flag, kWaitLimit);
+               static_cast<int>(rank), kCluster, abort_flag, kItemWaitLimit);
   } else {
     // ================= softmax / rescale / epilogue =================
     // The two warps of a TMEM lane quadrant (warp % 4, a hardware rule) take

@@ -33,7 +33,9 @@
 //               online softmax in fp32 (exp2 with the scale folded in),
 //               writes P as bf16 over the first 64 columns of its S buffer,
 //               rescales O in TMEM only when the row maximum grew by more
-//               than 2^8, and finally normalises O and stores bf16 rows.
+//               than 2^8 (2^32 in causal calls: kWeightHead), and finally
+//               normalises O and stores bf16 rows (store_rows).
+//   warp 11     finds the items ahead of the others (tell_items).
 // P overwrites S in place: the MMA that next writes that S buffer is issued
 // after the PV that reads P by the same thread, and one thread's tcgen05
 // MMAs execute in order.
@@ -61,6 +63,7 @@ constexpr int kTile = kVarlenTile;          // rows of a Q tile, keys of a K/V t
 constexpr int kThreads = 384;       // producer, 2 MMA issuers, 2 x 4 softmax warps, item finder
 constexpr int kMmaWarp1 = 10;       // issuer of tile 1
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
+constexpr long long kItemWaitLimit = 32 * kWaitLimit;   // of the item finder: whole items long
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kThreads / 32 - 1) {
     // ================= the items, ahead of everyone =================
-    tell_items(p, order, prefix, blockIdx.x, gridDim.x, ring, D, 0, 1, abort_flag, kWaitLimit);
+    tell_items(p, order, prefix, blockIdx.x, gridDim.x, ring, D, 0, 1, abort_flag, kItemWaitLimit);
   } else {
     // ================= softmax / correction / epilogue =================
     // warps 2..5: tile 0, warps 6..9: tile 1; TMEM lane quadrant = warp % 4

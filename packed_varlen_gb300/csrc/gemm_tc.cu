@@ -427,6 +427,9 @@ pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
 // Largest row stride, in elements (TMA strides are below 2^40 bytes).
 constexpr int64_t kMostStride = int64_t{1} << 38;
 
+// Longest sum: a tile's, some 0.5 s of them, has to end within the waits for it.
+constexpr int32_t kMostK = 1 << 26;
+
 // The checks of the entry points with strides (bias, residual: may be null).
 pa_status check_gemm(const GemmArgs &a) {
   if (a.M < 0 || a.N < 1 || a.K < 1 || a.act < PA_ACT_NONE || a.act > PA_ACT_GELU_TANH)
@@ -435,7 +438,7 @@ pa_status check_gemm(const GemmArgs &a) {
   if (a.x_stride < a.K || a.y_stride < a.N || (a.residual && a.residual_stride < a.N) ||
       (a.residual && a.residual == a.y && a.residual_stride != a.y_stride))
     return PA_ERR_INVALID_ARG;
-  if (a.x_stride > kMostStride || a.y_stride > kMostStride || a.residual_stride > kMostStride)
+  if (a.K > kMostK || a.x_stride > kMostStride || a.y_stride > kMostStride || a.residual_stride > kMostStride)
     return PA_ERR_UNSUPPORTED;
   if (((a.K | a.N | a.x_stride | a.y_stride) & 7) != 0 ||
       (a.residual && (a.residual_stride & 7) != 0) || !aligned_to(a.x, 16) ||

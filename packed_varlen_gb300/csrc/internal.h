@@ -91,7 +91,7 @@ cudaError_t device_context(int32_t **status, int *num_sms);
 // Maps a CUDA error to a pa_status and remembers it for pa_last_cuda_error.
 pa_status from_cuda(cudaError_t e);
 
-// Launchers: return cudaSuccess or the launch error.
+// Launchers (launch_varlen_attn takes the kernel of the head dim): return cudaSuccess or the launch error.
 cudaError_t launch_varlen_attn(const VarlenArgs &a, cudaStream_t stream);
 cudaError_t launch_varlen_attn_pair(const VarlenArgs &a, cudaStream_t stream);   // D = 128
 cudaError_t launch_block_window_attn(const BlockWindowArgs &a, cudaStream_t stream);

@@ -208,6 +208,86 @@ def test_growing_and_falling_scores(pv, slope, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("reach", [12, 20, 29])
+def test_large_scores(pv, reach, causal, D):
+    """Exact scores up to 2^reach once scaled, each row's largest one at least 2^(reach - 8)
+    above the others, so that its weight is all there is (e^-16 times a few v beside it: below
+    2^-18): out is that key's v, but for the rounding of the weight and of the result."""
+    lq, lk, Hq, H = [300, 140], [300, 400], 4, 2
+    q = torch.zeros(sum(lq), Hq, D, dtype=BF16)
+    q[..., 0] = 1.0
+    v = _randn(sum(lk), H, D, seed=3)
+    rng, k0, q0 = np.random.default_rng(7), 0, 0
+    k = torch.zeros(sum(lk), H, D, dtype=BF16)
+    for n in lk:
+        # multiples of 2^(reach - 8), no two alike among 128 keys; those set apart below are each
+        # larger than all before
+        size = np.array([rng.permutation(200)[:128] for _ in range(-(-n // 128))]).ravel()[:n]
+        k[k0:k0 + n, :, 0] = torch.as_tensor(
+            (size[:, None] - 255.0) * 2.0 ** (reach - 8)).to(BF16)
+        k[k0 + 5, :, 0] = 2.0 ** (reach - 4)
+        k[k0 + n // 2, :, 0] = 2.0 ** (reach - 1)
+        k[k0 + n - 9, :, 0] = 2.0 ** reach
+        k0 += n
+    out = oracle.to_f64(_attend(pv, q.cuda(), k.cuda(), v.cuda(), lq, lk, causal, 1.0))
+    k0, seen = 0, 0
+    for nq, n in zip(lq, lk):
+        for i in range(nq):
+            end = n - nq + i + 1 if causal else n
+            size = oracle.to_f64(k[k0:k0 + end, 0, 0])
+            order = np.sort(size)
+            if end > 1 and order[-1] - order[-2] < 2.0 ** (reach - 8):
+                continue
+            want = oracle.to_f64(v[k0 + int(size.argmax())])[[0, 0, 1, 1]]
+            assert (np.abs(out[q0 + i] - want) <= 2.0 ** -7 * 1.01 * np.abs(want) + 2.0 ** -18).all(), \
+                (i, end)
+            seen += 1
+        k0, q0 = k0 + n, q0 + nq
+    assert seen > 300
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_bad_query_stays_its_own(pv, bad, D):
+    """NaN or an infinity in one row of q, beside other heads and tokens of its tile."""
+    lq, Hq, H = [70, 300], 6, 2
+    q = _randn(sum(lq), Hq, D, seed=1)
+    k, v = _randn(sum(lq), H, D, seed=2), _randn(sum(lq), H, D, seed=3)
+    rows = [(40, 1), (200, 3), (69, 5)]
+    for t, h in rows:
+        q[t, h, 7] = bad
+    out = oracle.to_f64(_attend(pv, q.cuda(), k.cuda(), v.cuda(), lq, lq))
+    for t, h in rows:
+        assert not np.isfinite(out[t, h]).any()
+        q[t, h] = 0
+        out[t, h] = 0
+    want, weight, reach = oracle.prompt_attention(q, k, v, lq, lq, True, D ** -0.5)
+    for t, h in rows:
+        want[t, h] = 0
+    _within(torch.as_tensor(out), want, _attention_tolerance(want, weight, reach, D))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [100, 127])
+def test_groups_that_leave_rows_of_a_tile(pv, G, D):
+    _attention_case(pv, [1, 5, 140], [1, 300, 140], 2 * G, 2, D, True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_first_boundary_is_zero(pv, D):
+    """Boundaries that start elsewhere: the first sequence is skipped, its rows untouched."""
+    lq, at = [40, 3], 29
+    q, k, v = (_randn(at + 43, h, D, seed=h + 1) for h in (4, 2, 2))
+    out = torch.full(q.shape, 5.0, dtype=BF16, device="cuda")
+    cu = _cu(lq) + at
+    pv.prompt_attn_fwd(q.cuda(), k.cuda(), v.cuda(), cu, cu, 40, 40, out=out)
+    assert pv.get_device_status() == 1 and (out[:69] == 5).all()
+    want, weight, reach = oracle.prompt_attention(q[69:], k[69:], v[69:], [3], [3], True, D ** -0.5)
+    _within(out[69:], want, _attention_tolerance(want, weight, reach, D))
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_slices_of_a_fused_projection(pv, D):
     lengths, Hq, H = [130, 300, 1], 8, 2
     T = sum(lengths)
@@ -483,6 +563,14 @@ def test_one_axis_is_the_rope_beside_it(pv):
         assert (x.float() - y.float()).abs().max() <= 2.0 ** -7 * y.float().abs().max()
 
 
+def test_rope_of_many_heads(pv):
+    q, k = _randn(3, 5000, 64, seed=1), _randn(3, 700, 64, seed=2)
+    pos = np.array([[5, -(1 << 31), 9], [(1 << 31) - 1, 0, -1]])
+    a, b = pv.rope_axes(q.cuda(), k.cuda(), _i32(pos.tolist()), [40, 24])
+    _check_rope(a, q, pos, [40, 24], 1e4, False, False)
+    _check_rope(b, k, pos, [40, 24], 1e4, False, False)
+
+
 def test_rope_many_rows(pv):
     """More rows and heads than the grid takes at once; offsets beyond 32 bits."""
     T, Hq, D = (1 << 32) // (64 * 256) + 37, 64, 256
@@ -675,6 +763,16 @@ def test_linear_rows_do_not_depend_on_the_batch(pv, N, K):
     assert pv.get_device_status() == 0
 
 
+def test_linear_of_many_features(pv):
+    M, N, K = 3, (1 << 20) + 8, 16
+    x, w, b, r = _linear_inputs(M, N, K, 1)
+    got = pv.linear_act_bf16(*_cuda(x, w, b), act="relu", residual=r.cuda())
+    _check_linear(got, x, w, b, "relu", r)
+    _check_gated(pv.linear_gated_bf16(x.cuda(), w.cuda(), w.flip(0).contiguous().cuda()), x, w,
+                 w.flip(0), "silu")
+    assert pv.get_device_status() == 0
+
+
 def test_linear_of_no_rows(pv):
     x = torch.zeros(0, 64, dtype=BF16, device="cuda")
     w = torch.ones(16, 64, dtype=BF16, device="cuda")
@@ -814,3 +912,53 @@ def test_a_layer(pv, D):
         for name in ("q", "k", "a", "h", "f", "y"):
             rows = slice(0, n) if name == "a" else slice(None)
             assert torch.equal(_bits(eager[name][rows]), _bits(held[name][rows])), name
+
+
+def test_layers_on_two_streams_and_in_two_graphs(pv):
+    """Two programs at once over the same weights: eager calls on two streams, then two
+    graphs replayed together, each with rows of its own."""
+    Hq, H, D, C, T = 8, 2, 128, 1024, 700
+    w_q, w_g, w_u, w_d = ((_randn(n, m, seed=40 + i).float() / math.sqrt(m)).to(BF16).cuda()
+                          for i, (n, m) in enumerate([((Hq + 2 * H) * D, C), (2048, C), (2048, C),
+                                                      (C, 2048)]))
+    cu, pos = _cu([500, 13, 187]), torch.arange(2 * T, dtype=torch.int32, device="cuda").view(2, T)
+
+    def layer(x, x1, stream=None):
+        kw = dict(stream=stream)
+        f = pv.linear_act_bf16(x, w_q, **kw).view(T, Hq + 2 * H, D)
+        q, k, v = f.split([Hq, H, H], dim=1)
+        pv.rope_axes(q, k, pos, [64, 64], **kw)
+        a = pv.prompt_attn_fwd(q, k, v, cu, cu, 500, 500, **kw).view(T, C)
+        y = pv.linear_act_bf16(pv.linear_gated_bf16(a, w_g, w_u, **kw), w_d, residual=x, **kw)
+        y1 = pv.linear_act_bf16(pv.linear_gated_bf16(x1, w_g, w_u, **kw), w_d, residual=x1, **kw)
+        return f, a, y, y1
+
+    xs = [[_randn(n, C, seed=50 + i).cuda() for n in (T, 5)] for i in range(2)]
+    want = [[t.clone() for t in layer(*x)] for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = layer(*xs[i])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(_bits(x), _bits(y)) for x, y in zip(a, b))
+    graphs = []
+    for i, s in enumerate(streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got[i] = layer(*xs[i])
+        graphs.append(g)
+    for t in [*got[0], *got[1]]:
+        t.fill_(5.0)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(_bits(x), _bits(y)) for x, y in zip(a, b))
+    assert pv.get_device_status() == 0

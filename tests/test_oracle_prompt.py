@@ -180,6 +180,14 @@ def test_rope_axes_host_checks(lib):
     assert list(keep) == [32, 48, 48]
 
 
+def test_axis_widths_are_whole_numbers():
+    import packed_varlen_gb300 as pv
+    with pytest.raises(TypeError):
+        pv._host_ints((31.5, 32.5))
+    with pytest.raises((ValueError, OverflowError, pv.PackedAttnError)):
+        pv._host_ints((1 << 40, 2))
+
+
 def test_linear_epilogue_host_checks(lib):
     ok = [A, A, A, A, A + 64, 300, 512, 4096, 4096, 512, 512, 3, None]
     big = 1 << 39
@@ -192,6 +200,9 @@ def test_linear_epilogue_host_checks(lib):
     args[3] = args[4]       # in place, but not the same rows
     args[9] = 520
     assert lib.pa_linear_act_bf16(*args) == 1
+    args = list(ok)         # sums too long to end within the waits for them
+    args[7], args[8] = (1 << 26) + 8, 1 << 27
+    assert lib.pa_linear_act_bf16(*args) == 2
     args = list(ok)
     args[0] = args[4] = None
     args[5] = 0
@@ -202,6 +213,9 @@ def test_linear_epilogue_host_checks(lib):
         (7, 4088, 1), (8, 504, 1), (9, -1, 1), (9, 5, 1), (7, big, 2), (8, big, 2), (5, 508, 3),
         (6, 4092, 3), (7, 4100, 3), (8, 516, 3), (0, MIS, 3), (1, MIS, 3), (2, MIS, 3),
         (3, MIS, 3)])
+    args = list(ok)
+    args[6], args[7] = (1 << 26) + 8, 1 << 27
+    assert lib.pa_linear_gated_bf16(*args) == 2
     args = list(ok)
     args[0] = args[3] = None
     args[4] = 0
