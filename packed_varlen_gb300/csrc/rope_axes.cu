@@ -18,7 +18,7 @@
 // lane has a fixed place in its head, a vector of eight elements (with halves,
 // the two vectors of its pairs), so its fractions stay in registers and its cos
 // and sin, computed while the task's first loads are in flight, serve all of
-// the task's heads.
+// the task's heads; lanes at one place of several heads compute a part each.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -78,26 +78,36 @@ __device__ __forceinline__ float2 turned(int32_t position, uint64_t turn) {
   return cs;
 }
 
-// Heads of a lane at a time: 64 or 96 bytes in flight, with 24 warps an SM.  30269
-// tokens of 48 heads of 128: 115 us and 6.4 TB/s (four at a time 120); 9801 of 32
-// heads of 80, halves: 22.7 us and 4.4 TB/s (four at a time, 16 warps: 25.9).
-constexpr int batch_of(bool halves) { return halves ? 2 : 6; }
+// A call of many tokens has tasks of whole tokens, or nearly, for all SMs; where there
+// are few it is the latency of a task that counts.  With 24 warps an SM:
+//   heads of a lane at a time: 6, or with halves 3 where tokens are many (9801 of 32
+//   heads of 80: 16.7 us, by two 18.2; 20000 of 40 heads of 128 65.3 and 67.8) and 2
+//   where they are few (48 of 40 heads of 128: 2.2 us, by three 3.2);
+//   cos and sin computed once for all heads of a step, but for many tokens without
+//   halves (48 tokens of 48 heads of 128: 2.5 us, each lane its own 2.8; 3000 14.3
+//   and 12.2).
+// (One call in a row of them in a graph, over rows in L2.)  30269 tokens of 48 heads
+// of 128: 115 us out of HBM, 6.4 TB/s.
+constexpr int batch_of(bool halves, bool many) { return !halves ? 6 : many ? 3 : 2; }
 
 // kHalves: pairs (i, i + R/2), else (2i, 2i + 1).  kElems: elements of a vector.
-template <bool kHalves, int kElems>
+// kOwn: pairs of a lane whose cos and sin it computes itself; the lanes at the same
+// place of the step's other heads have the rest.  kBatch: heads of a lane at a time.
+template <bool kHalves, int kElems, int kOwn, int kBatch>
 __global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const __grid_constant__ RopeParams p) {
   using V = typename Vec<kElems>::type;
   constexpr int kPairs = kHalves ? kElems : kElems / 2;   // of a lane
-  constexpr int kBatch = batch_of(kHalves);
   const int lane = threadIdx.x & 31;
   const int in_step = lane / p.units, u = lane - in_step * p.units;   // head of the step, place in it
   if (in_step >= p.heads_per_step) return;
-  uint64_t turn[kPairs];
-  uint32_t axes = 0;   // of the lane's pairs, four bits each
+  const uint32_t lanes = 0xffffffffu >> (32 - p.heads_per_step * p.units);
+  uint64_t turn[kOwn];
+  int64_t at[kOwn];   // of its axis' positions
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    turn[i] = p.turn[u * kPairs + i];
-    axes |= static_cast<uint32_t>(p.axis[u * kPairs + i]) << (4 * i);
+  for (int j = 0; j < kOwn; ++j) {
+    const int pair = u * kPairs + in_step % (kPairs / kOwn) * kOwn + j;
+    turn[j] = p.turn[pair];
+    at[j] = static_cast<int64_t>(p.axis[pair]) * p.total;
   }
   // (launch_beside: everything above ran beside the kernel before)
   tc::griddep_launch_dependents();
@@ -111,14 +121,14 @@ __global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const __grid_con
     const int t = task / p.chunks, chunk = task - t * p.chunks;
     const __nv_bfloat16 *q = p.q + t * p.q_stride, *k = p.k + t * p.k_stride;
     __nv_bfloat16 *q_out = p.q_out + t * p.q_out_stride, *k_out = p.k_out + t * p.k_out_stride;
-    const int first = chunk * p.steps * p.heads_per_step + in_step;
+    const int first = chunk * p.steps * p.heads_per_step;
     const int end = min(heads, (chunk + 1) * p.steps * p.heads_per_step);
     float2 cs[kPairs];
     for (int h0 = first; h0 < end; h0 += kBatch * p.heads_per_step) {
       V a[kBatch], b[kHalves ? kBatch : 1];
 #pragma unroll
       for (int s = 0; s < kBatch; ++s) {
-        const int h = h0 + s * p.heads_per_step;
+        const int h = h0 + in_step + s * p.heads_per_step;
         if (h >= end) break;
         const __nv_bfloat16 *src = h < p.Hq ? q + static_cast<int64_t>(h) * p.D
                                             : k + static_cast<int64_t>(h - p.Hq) * p.D;
@@ -126,15 +136,22 @@ __global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const __grid_con
         if (kHalves) b[s] = *reinterpret_cast<const V *>(src + b0);
       }
       if (h0 == first) {
+        float2 own[kOwn];
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) own[j] = turned(__ldg(p.positions + at[j] + t), turn[j]);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const int64_t axis = (axes >> (4 * i)) & 15u;
-          cs[i] = turned(__ldg(p.positions + axis * p.total + t), turn[i]);
+          const int from = i / kOwn * p.units + u;
+          cs[i] = own[i % kOwn];
+          if (kOwn < kPairs) {
+            cs[i].x = __shfl_sync(lanes, cs[i].x, from);
+            cs[i].y = __shfl_sync(lanes, cs[i].y, from);
+          }
         }
       }
 #pragma unroll
       for (int s = 0; s < kBatch; ++s) {
-        const int h = h0 + s * p.heads_per_step;
+        const int h = h0 + in_step + s * p.heads_per_step;
         if (h >= end) break;
         uint32_t *aw = reinterpret_cast<uint32_t *>(&a[s]);
         uint32_t *bw = reinterpret_cast<uint32_t *>(&b[kHalves ? s : 0]);
@@ -164,6 +181,14 @@ __global__ void __launch_bounds__(kThreads, 3) rope_axes_kernel(const __grid_con
       }
     }
   }
+}
+
+template <bool kHalves, int kElems, bool kMany>
+void (*pick(int own))(RopeParams) {
+  constexpr int kBatch = batch_of(kHalves, kMany);
+  return own == 1   ? rope_axes_kernel<kHalves, kElems, 1, kBatch>
+         : own == 2 ? rope_axes_kernel<kHalves, kElems, 2, kBatch>
+                    : rope_axes_kernel<kHalves, kElems, 4, kBatch>;
 }
 
 // What a call's numbers say about every pair: theta / (2 pi) in 2^-64 of a turn, and
@@ -269,18 +294,23 @@ extern "C" pa_status pa_rope_axes(const void *q, const void *k, void *q_out, voi
   if (e != cudaSuccess) return from_cuda(e);
   // A token is shared out where whole ones leave the SMs short of 32 warps each,
   // as far as a batch of loads a lane: cos and sin are then computed for each.
-  const int batch = batch_of(halves != 0);
+  const int64_t want = (int64_t{sms} * 32 + total - 1) / total;
+  const bool many = want <= 4;
+  const int batch = batch_of(halves != 0, many);
   const int all_steps = (Hq + Hkv - 1) / p.heads_per_step + 1;
   const int most = (all_steps + batch - 1) / batch;
-  const int64_t want = (int64_t{sms} * 32 + total - 1) / total;
   p.chunks = want < most ? static_cast<int>(want) : most;
   p.steps = ((all_steps + p.chunks - 1) / p.chunks + batch - 1) / batch * batch;
   p.chunks = (all_steps + p.steps - 1) / p.steps;
   const int64_t tasks = int64_t{total} * p.chunks;
   const int64_t blocks = (tasks + kThreads / 32 - 1) / (kThreads / 32);
   const int grid = static_cast<int>(blocks < int64_t{sms} * 8 ? blocks : int64_t{sms} * 8);
-  const auto kernel = !halves ? rope_axes_kernel<false, 8>
-                              : elems == 8 ? rope_axes_kernel<true, 8> : rope_axes_kernel<true, 4>;
+  // pairs of a lane's own: those it has, over the heads of a step (as a power of two)
+  int own = halves ? elems : elems / 2;
+  for (int others = 2; others <= p.heads_per_step && own > 1; others *= 2) own /= 2;
+  const auto kernel = !halves      ? pick<false, 8, false>(many ? 4 : own)
+                      : elems == 8 ? many ? pick<true, 8, true>(own) : pick<true, 8, false>(own)
+                      : many       ? pick<true, 4, true>(own) : pick<true, 4, false>(own);
   return from_cuda(launch_beside(kernel, dim3(grid), kThreads, 0,
                                  reinterpret_cast<cudaStream_t>(stream), p));
 }
