@@ -34,7 +34,7 @@
 //               writes P as bf16 over the first 64 columns of its S buffer,
 //               rescales O in TMEM only when the row maximum grew by more
 //               than 2^8 (2^32 in causal calls: kWeightHead), and finally
-//               normalises O and stores bf16 rows (store_rows).
+//               normalises O and stores bf16 rows (send_rows).
 //   warp 11     finds the items ahead of the others (tell_items).
 // P overwrites S in place: the MMA that next writes that S buffer is issued
 // after the PV that reads P by the same thread, and one thread's tcgen05
@@ -123,7 +123,8 @@ template <int D, int kSlots, int kMaxSeqs>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const VarlenParams p) {
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ CUtensorMap tm_o, const VarlenParams p) {
   using C = Cfg<D, kSlots, kMaxSeqs>;
   extern __shared__ uint8_t smem_raw[];
   // 128-byte swizzle atoms need a 1024-byte aligned base
@@ -433,9 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.rot = __shfl_sync(0xffffffffu, it.rot, 0);
       if (it.tokens <= t * p.tokens) continue;    // tile absent: nothing issued for it
       const int token = t * p.tokens + row_token;   // of the item
-      __nv_bfloat16 *dst =
-          p.out + (static_cast<int64_t>(it.q_row0 + token) * p.H + it.head * p.G + row_head) * D;
-      const bool store = token < it.tokens && row_token < p.tokens;
       const int row_keys = min(it.lk, it.seen + token + 1);   // that this row sees
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < it.nk; ++j) {
@@ -542,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++o_waits;
       fence_after_sync();
+      const int out_head = it.head * p.G + row_head;
+      const int out_token = token < it.tokens && row_token < p.tokens ? it.q_row0 + token : -1;
       const float inv = 1.f / l;
       const bool none = row_keys <= 0;   // the row sees no key (its sums are NaN)
 #pragma unroll
@@ -555,9 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           words[e] = none ? 0u
                           : pack_bf16x2(__uint_as_float(r[2 * e]) * inv,
                                         __uint_as_float(r[2 * e + 1]) * inv);
-        store_rows(gbase + C::kOutOff + (warp - 2) * 4096, words, store ? dst + c * 64 : nullptr);
+        send_rows(gbase + C::kOutOff + (warp - 2) * 4096, words, p, &tm_o, D, c * 64, out_head,
+                  out_token);
       }
     }
+    if (lane == 0) bulk_wait();
   }
 
   // ---- teardown -------------------------------------------------------------
@@ -588,18 +590,20 @@ bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t
 
 template <int D, int kSlots, int kMaxSeqs>
 cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   const VarlenParams p = varlen_params(a);
   if (!make_map(&mq, a.q, a.total_q, a.H, D, a.q_stride, p.G, p.tokens) ||
       !make_map(&mk, a.k, a.total_k, a.Hkv, D, a.k_stride, 1, kTile) ||
-      !make_map(&mv, a.v, a.total_k, a.Hkv, D, a.v_stride, 1, kTile))
+      !make_map(&mv, a.v, a.total_k, a.Hkv, D, a.v_stride, 1, kTile) ||
+      !make_map(&mo, a.out, a.total_q, a.H, D, int64_t{a.H} * D, p.G < 32 ? p.G : 32,
+                p.box_tokens > 0 ? p.box_tokens : 1))
     return cudaErrorInvalidValue;
   const int smem = Cfg<D, kSlots, kMaxSeqs>::kSmemBytes;
   const auto kernel = varlen_attn_tc_kernel<D, kSlots, kMaxSeqs>;
   static unsigned long long configured = 0;
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), smem, configured);
   if (e != cudaSuccess) return e;
-  return launch_beside(kernel, dim3(a.num_sms), kThreads, smem, stream, mq, mk, mv, p);
+  return launch_beside(kernel, dim3(a.num_sms), kThreads, smem, stream, mq, mk, mv, mo, p);
 }
 
 }  // namespace

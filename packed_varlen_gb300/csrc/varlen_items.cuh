@@ -12,6 +12,7 @@
 // causal: query i of a sequence sees key j iff j <= lk - lq + i.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -32,6 +33,7 @@ struct VarlenParams {
   float scale_log2;
   int32_t *status;
   int G, tokens, causal;   // query heads per K/V head, tokens of a tile, causal order
+  int box_tokens;          // of 32 rows of a tile, or 0 where they are no box of out
 };
 
 inline VarlenParams varlen_params(const VarlenArgs &a) {
@@ -50,6 +52,7 @@ inline VarlenParams varlen_params(const VarlenArgs &a) {
   p.G = a.H / a.Hkv;
   p.tokens = kVarlenTile / p.G;
   p.causal = a.causal;
+  p.box_tokens = 32 % p.G == 0 ? 32 / p.G : p.G % 32 == 0 ? 1 : 0;
   return p;
 }
 
@@ -130,10 +133,10 @@ constexpr float kWeightHead = 24.f;
 // A warp's 32 rows of 128 bytes (64 columns), a row to a lane in `words`, out to
 // where `dst` of the row's lane says (nullptr: not stored), through 4 KB of shared
 // memory: eight lanes write a row, four rows an instruction, where rows stored by
-// their own lanes are 32 separate pieces of 16 bytes (the end of an item of 64 KB
-// took 3300 cycles so, and 1560 this way; a bulk copy to a row 382 -> 400 us on 24
-// prompts of 90-2700 tokens, 32 heads on 8 of 128).  Pieces of a row are permuted against
-// bank conflicts.
+// their own lanes are 32 separate pieces of 16 bytes (head dim 128: the end of an item
+// of 64 KB took 3300 cycles so, and 1560 this way; a bulk copy to a row 382 -> 400 us
+// on 24 prompts of 90-2700 tokens, 32 heads on 8).  Pieces of a row are permuted
+// against bank conflicts, as the 128-byte swizzle has them.
 __device__ __forceinline__ void store_rows(uint8_t *buf, const uint32_t (&words)[32],
                                            __nv_bfloat16 *dst) {
   const int lane = threadIdx.x & 31, piece = lane & 7;
@@ -152,6 +155,38 @@ __device__ __forceinline__ void store_rows(uint8_t *buf, const uint32_t (&words)
     if (to) to[piece] = x;
   }
   __syncwarp();   // the buffer is free again
+}
+
+// The same for `token` and `head` of the row's lane (token < 0: not stored), columns
+// from `col`.  Where all 32 rows are stored and are a box of out (whole groups, or
+// part of one), one copy takes them, and nobody waits for it (before the kernel ends,
+// lane 0 waits for the copies to be written).  Head dim 64, the same 24 prompts: 280
+// -> 258 us, 64 of 300 tokens 83 -> 70, 16k 1015 -> 1010.  With head dim 128, whose
+// key loop has no register to spare, long sequences lost what short ones won (16k
+// 1113 -> 1129 us, the 24 prompts 397 -> 382).
+__device__ __forceinline__ void send_rows(uint8_t *buf, const uint32_t (&words)[32],
+                                          const VarlenParams &p, const CUtensorMap *map, int D,
+                                          int col, int head, int token) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) tc::bulk_wait_read();   // the copy before has read the buffer
+  __syncwarp();
+  if (p.box_tokens > 0 && __all_sync(0xffffffffu, token >= 0)) {
+    const int piece = lane & 7;
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      *reinterpret_cast<uint4 *>(buf + lane * 128 + ((v ^ piece) << 4)) =
+          make_uint4(words[4 * v], words[4 * v + 1], words[4 * v + 2], words[4 * v + 3]);
+    tc::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      tc::tma_store_3d(map, tc::smem_u32(buf), col, head, token);
+      tc::bulk_commit();
+    }
+  } else {
+    store_rows(buf, words,
+               token < 0 ? nullptr
+                         : p.out + (static_cast<int64_t>(token) * p.H + head) * D + col);
+  }
 }
 
 // The ring of items.  Finding an item takes a search and a chain of loads, some
