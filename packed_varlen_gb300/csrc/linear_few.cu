@@ -7,8 +7,9 @@
 // (a multiple of 16, at most 256; few_plan).  The product is turned around: w is the MMA's A operand, its rows
 // the accumulator's TMEM lanes, and x is B, its rows the columns, so
 // a call of 13 rows pays for 16 columns and not for a tile of 128 rows.  An MMA
-// has 64 or 128 rows; where F is less, the rows of shared memory past F hold
-// anything, and what they give in the lanes past F is never read.
+// has 64 or 128 rows; where F is less, those past F are whatever follows in shared
+// memory, and what they give in the lanes past F is never read.  (With room for all
+// rows in the ring less of w was on its way: gated 24 x 4096 x 11264 36.2 us, now 32.6.)
 //
 // An element's products are added in the same order as in the large kernel (K
 // in steps of 16, one accumulator, no split over K), and the epilogue is the
@@ -38,7 +39,7 @@ using namespace tc;
 
 constexpr int kThreads = 192;
 constexpr int kMaxStages = 16;
-constexpr int kRingBytes = 220 * 1024;          // stages, at most
+constexpr int kRingBytes = 212 * 1024;          // stages, at most
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr int kRowBytes = kLinearBK * 2;        // of a K-block: 128
@@ -49,7 +50,11 @@ constexpr int kChunk = 16;                      // columns the epilogue takes at
 constexpr int kBarBytes = (2 * kMaxStages + 1) * 8;
 constexpr int kMiscOff = kBarBytes;
 constexpr int kRingOff = 1024;
-static_assert(kMiscOff + 8 <= kRingOff && kRingOff + kRingBytes <= 232448, "shared memory plan");
+// An MMA reads the rows of kM features, of which a K-block has F: those past its
+// last one are the next one's bytes, and past the ring's end these.
+constexpr int kPadBytes = 56 * kRowBytes;
+constexpr int kSmemBytes = kRingOff + kRingBytes + kPadBytes;
+static_assert(kMiscOff + 8 <= kRingOff && kSmemBytes <= 232448, "shared memory plan");
 
 struct FewParams {
   const __nv_bfloat16 *bias;       // [N] or nullptr
@@ -60,7 +65,7 @@ struct FewParams {
   int M, N, K;
   int features, rows;              // of a CTA: F, and columns of its accumulator
   int k_blocks, group, stages;     // K-blocks, those of a stage
-  int stage_bytes;
+  int stage_bytes, block_bytes;    // of a stage, of a K-block
   uint32_t idesc, tmem_cols;
   int32_t *status;
 };
@@ -72,7 +77,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_w2, const FewParams p) {
   constexpr int kParts = kMode == kGated ? 2 : 1;   // weights, accumulators
-  constexpr int kABytes = kM * kRowBytes;           // a K-block of one weight
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = smem_u32(smem_raw);
   if (base & 1023u) {   // swizzle atoms need a 1024-byte aligned base
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem_raw + kMiscOff + 4);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int n0 = blockIdx.x * p.features, m0 = blockIdx.y * p.rows;
-  const int b_bytes = p.rows * kRowBytes;
+  const int a_bytes = p.features * kRowBytes, b_bytes = p.rows * kRowBytes;   // of a K-block
   const int n_stages = (p.k_blocks + p.group - 1) / p.group;   // filled in all
 
   if (tid == 0) {
@@ -134,13 +138,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kb0 = i * p.group, blocks = min(p.group, p.k_blocks - kb0);
       const uint32_t dst = base + kRingOff + s * p.stage_bytes;
       if (lead) {
-        mbar_arrive_expect_tx(full(s), blocks * (kParts * p.features * kRowBytes + b_bytes));
+        mbar_arrive_expect_tx(full(s), blocks * (kParts * a_bytes + b_bytes));
         for (int b = 0; b < blocks; ++b) {
-          const uint32_t a = dst + b * (kParts * kABytes + b_bytes);
+          const uint32_t a = dst + b * p.block_bytes;
           const int k = (kb0 + b) * kLinearBK;
           tma_load_2d(a, &tm_w, full(s), k, n0);
-          if (kMode == kGated) tma_load_2d(a + kABytes, &tm_w2, full(s), k, n0);
-          tma_load_2d(a + kParts * kABytes, &tm_x, full(s), k, m0);
+          if (kMode == kGated) tma_load_2d(a + a_bytes, &tm_w2, full(s), k, n0);
+          tma_load_2d(a + kParts * a_bytes, &tm_x, full(s), k, m0);
         }
       }
     }
@@ -151,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     const bool lead = elect_one();
     const uint64_t desc0 = sdesc_sw128(base + kRingOff, 16, 1024);
+    const uint64_t w2_off = a_bytes >> 4, x_off = kParts * a_bytes >> 4;
     bool ok = true;
     int i = 0;
     uint32_t s = 0, parity = 0, more = 0;
@@ -162,19 +167,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t a = desc0 + ((s * p.stage_bytes) >> 4);
 #pragma unroll 1
       for (int b = 0; b < blocks; ++b) {
-        const uint64_t x = a + ((kParts * kABytes) >> 4);
+        const uint64_t x = a + x_off;
         if (lead) {
           mma_ss(tmem, a, x, p.idesc, more);
-          if (kMode == kGated) mma_ss(tmem + p.rows, a + (kABytes >> 4), x, p.idesc, more);
+          if (kMode == kGated) mma_ss(tmem + p.rows, a + w2_off, x, p.idesc, more);
 #pragma unroll
           for (int kk = 1; kk < kLinearBK / 16; ++kk) {
             mma_ss(tmem, a + kk * 2, x + kk * 2, p.idesc, 1u);
             if (kMode == kGated)
-              mma_ss(tmem + p.rows, a + (kABytes >> 4) + kk * 2, x + kk * 2, p.idesc, 1u);
+              mma_ss(tmem + p.rows, a + w2_off + kk * 2, x + kk * 2, p.idesc, 1u);
           }
         }
         more = 1;
-        a += (kParts * kABytes + b_bytes) >> 4;
+        a += p.block_bytes >> 4;
       }
       if (lead) mma_commit(empty(s));
       if (++s == static_cast<uint32_t>(p.stages)) {
@@ -252,21 +257,24 @@ pa_status launch(const GemmArgs &a, FewParams &p, cudaStream_t stream) {
       !make_map_2d(&mw, a.w, a.N, a.K, a.K, p.features) ||
       !make_map_2d(&mw2, kMode == kGated ? a.w2 : a.w, a.N, a.K, a.K, p.features))
     return from_cuda(cudaErrorInvalidValue);
-  const int block = (kMode == kGated ? 2 : 1) * kM * kRowBytes + p.rows * kRowBytes;
+  p.block_bytes = ((kMode == kGated ? 2 : 1) * p.features + p.rows) * kRowBytes;
   p.idesc = idesc_bf16_f32(kM, p.rows, false);
-  // Stages of up to 64 KB: what a barrier costs the issuer is spread over some
-  // twenty MMAs (13 rows, 4096 x 4096: stages of 32 KB 11.9 us, 64 KB 9.8).
-  p.group = 65536 / block > 1 ? 65536 / block : 1;
+  // Stages of a quarter of the ring: large, as a barrier's cost to the issuer is
+  // spread over a stage's MMAs, and not larger, as a stage is waited for whole (13
+  // rows, K = 16384, 4096 features: a half 26.6 us, a third 24.9, a quarter 24.5).
+  // All of an SM's shared memory is on its way from HBM; rings of half of it, with
+  // the next call's CTAs beside this one's, took 9.9 us for 4096 x 4096 in place of 7.8.
+  p.group = kRingBytes / 4 / p.block_bytes > 1 ? kRingBytes / 4 / p.block_bytes : 1;
   if (p.group > p.k_blocks) p.group = p.k_blocks;
-  p.stage_bytes = p.group * block;
+  p.stage_bytes = p.group * p.block_bytes;
   p.stages = kRingBytes / p.stage_bytes < kMaxStages ? kRingBytes / p.stage_bytes : kMaxStages;
   static unsigned long long configured = 0;
   const auto kernel = linear_few_kernel<kMode, kM>;
   const cudaError_t e =
-      set_smem_once(reinterpret_cast<const void *>(kernel), kRingOff + kRingBytes, configured);
+      set_smem_once(reinterpret_cast<const void *>(kernel), kSmemBytes, configured);
   if (e != cudaSuccess) return from_cuda(e);
   const dim3 grid((a.N + p.features - 1) / p.features, (a.M + p.rows - 1) / p.rows);
-  return from_cuda(launch_beside(kernel, grid, kThreads, kRingOff + kRingBytes, stream, mx, mw,
+  return from_cuda(launch_beside(kernel, grid, kThreads, kSmemBytes, stream, mx, mw,
                                  mw2, p));
 }
 
