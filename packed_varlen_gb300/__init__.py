@@ -433,7 +433,7 @@ def _rows_stride(t: torch.Tensor, name: str, dev: int) -> int:
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the cache's device, not {t.device}")
+        raise ValueError(f"{name} must be on the device of the other tensors, not {t.device}")
     T, H, D = t.shape
     if not t.is_contiguous():
         sT, sH, sD = t.stride()
@@ -450,7 +450,7 @@ def _need_index(t: torch.Tensor, name: str, n: int, dev: int):
     except _NOT_USUAL:
         pass
     _need(t, name, _I32, 1)
-    raise ValueError(f"{name} must be [{n}] on the cache's device, got {list(t.shape)} on {t.device}")
+    raise ValueError(f"{name} must be [{n}] on the device of the other tensors, got {list(t.shape)} on {t.device}")
 
 
 def _need_out(t: torch.Tensor, name: str, shape, dev: int):
@@ -460,7 +460,7 @@ def _need_out(t: torch.Tensor, name: str, shape, dev: int):
     except _NOT_USUAL:
         pass
     _need(t, name, _BF16, len(shape))
-    raise ValueError(f"{name} must be {list(shape)} on the cache's device")
+    raise ValueError(f"{name} must be {list(shape)} on the device of the other tensors")
 
 
 def _batch_of(cu: torch.Tensor, name: str) -> int:
@@ -740,6 +740,19 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     return t.get_device()
 
 
+def _rows(t: torch.Tensor, name: str, dev: int):
+    """T, H, D of a packed bf16 tensor, and elements from one token to the next."""
+    try:
+        T, H, D = t.shape
+        sT, sH, sD = t.stride()
+        if sD == 1 and sH == D and t.dtype is _BF16 and t.get_device() == dev:
+            return T, H, D, sT if T > 1 else H * D
+    except _NOT_USUAL:
+        pass
+    stride = _rows_stride(t, name, dev)
+    return (*t.shape, stride)
+
+
 def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_q: int,
                     max_k: int, causal: bool = True, scale: Optional[float] = None,
@@ -754,21 +767,22 @@ def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if (max_q | max_k) >> 31:
         _fits_32_bits("pa_prompt_attn_fwd", max_q, max_k)
     dev = _device_of(q, "q")
-    qs, ks, vs = _rows_stride(q, "q", dev), _rows_stride(k, "k", dev), _rows_stride(v, "v", dev)
-    Tq, Hq, D = shape = q.shape
-    Tk, Hkv, Dk = k.shape
-    if Dk != D or v.shape != k.shape or Hkv < 1 or Hq < 1 or Hq % Hkv:
+    Tq, Hq, D, qs = _rows(q, "q", dev)
+    Tk, Hkv, Dk, ks = _rows(k, "k", dev)
+    Tv, Hv, Dv, vs = _rows(v, "v", dev)
+    if Dk != D or Dv != D or Tv != Tk or Hv != Hkv or Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError("k and v must be [Tk, Hkv, D] with q's D and Hq a multiple of Hkv")
     B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
     _need_index(cu_seqlens_q, "cu_seqlens_q", B + 1, dev)
-    _need_index(cu_seqlens_k, "cu_seqlens_k", B + 1, dev)
+    if cu_seqlens_k is not cu_seqlens_q:
+        _need_index(cu_seqlens_k, "cu_seqlens_k", B + 1, dev)
     if scale is None:
         scale = D ** -0.5
     raw = _raw_stream(dev, stream)
     if out is None:
-        out = _new(torch.zeros, shape, _BF16, dev, stream, raw)
+        out = _new(torch.zeros, (Tq, Hq, D), _BF16, dev, stream, raw)
     else:
-        _need_out(out, "out", shape, dev)
+        _need_out(out, "out", (Tq, Hq, D), dev)
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), cu_seqlens_q.data_ptr(),
             cu_seqlens_k.data_ptr(), B, Tq, Tk, max_q, max_k, qs, ks, vs, Hq, Hkv, D,
             1 if causal else 0, float(scale), raw)
@@ -809,20 +823,30 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
     Returns (q_out, k_out)."""
     lib = _lib or load_library()
     dev = _device_of(q, "q")
-    q_out = q if q_out is None else q_out
-    qs, qo = _rows_stride(q, "q", dev), _rows_stride(q_out, "q_out", dev)
-    T, Hq, D = q.shape
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
+    T, Hq, D, qs = _rows(q, "q", dev)
+    qp = qo_p = q.data_ptr()
+    qo = qs
+    if q_out is None:
+        q_out = q
+    elif q_out is not q:
+        To, Ho, Do, qo = _rows(q_out, "q_out", dev)
+        if To != T or Ho != Hq or Do != D:
+            raise ValueError("q_out must have q's shape")
+        qo_p = q_out.data_ptr()
     kp = ko_p = None
     ks = ko = Hkv = 0
     if k is not None:
-        k_out = k if k_out is None else k_out
-        ks, ko = _rows_stride(k, "k", dev), _rows_stride(k_out, "k_out", dev)
-        Hkv = k.shape[1]
-        if k.shape != (T, Hkv, D) or k_out.shape != k.shape:
+        Tk, Hkv, Dk, ks = _rows(k, "k", dev)
+        kp = ko_p = k.data_ptr()
+        ko = ks
+        To, Ho, Do = Tk, Hkv, Dk
+        if k_out is None:
+            k_out = k
+        elif k_out is not k:
+            To, Ho, Do, ko = _rows(k_out, "k_out", dev)
+            ko_p = k_out.data_ptr()
+        if Tk != T or Dk != D or To != T or Ho != Hkv or Do != D:
             raise ValueError("k and k_out must be [T, Hkv, D] with q's T and D")
-        kp, ko_p = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     dims, axes, dims_at = _host_ints(tuple(axis_dims))    # (dims: kept until the call is made)
@@ -840,7 +864,7 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
         if num_tokens.numel() != 1 or num_tokens.get_device() != dev:
             raise ValueError("num_tokens must be one element on q's device")
         n_at = num_tokens.data_ptr()
-    args = (q.data_ptr(), kp, q_out.data_ptr(), ko_p, positions.data_ptr(), n_at, dims_at, axes, T,
+    args = (qp, kp, qo_p, ko_p, positions.data_ptr(), n_at, dims_at, axes, T,
             qs, ks, qo, ko, Hq, Hkv, D, 1 if halves else 0, 1 if shared else 0, float(base),
             _raw_stream(dev, stream))
     fn = lib.pa_rope_axes
@@ -850,13 +874,14 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
     return q_out, k_out
 
 
-def _matrix_stride(t: torch.Tensor, name: str, dev: int) -> int:
-    """Elements from one row to the next of a bf16 matrix whose rows are contiguous."""
+def _matrix(t: torch.Tensor, name: str, dev: int):
+    """M, N of a bf16 matrix whose rows are contiguous, and elements from one row to the
+    next."""
     try:
         M, N = t.shape
         s0, s1 = t.stride()
         if s1 == 1 and t.dtype is _BF16 and t.get_device() == dev:
-            return s0 if M > 1 else N
+            return M, N, s0 if M > 1 else N
     except _NOT_USUAL:
         pass
     if not isinstance(t, torch.Tensor):
@@ -870,7 +895,7 @@ def _matrix_stride(t: torch.Tensor, name: str, dev: int) -> int:
     M, N = t.shape
     if N > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if M > 1 else N
+    return M, N, t.stride(0) if M > 1 else N
 
 
 def _weight(w: torch.Tensor, name: str, K: int, dev: int) -> int:
@@ -911,8 +936,7 @@ def linear_act_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
     may be slices of wider matrices; out may be residual itself."""
     lib = _lib or load_library()
     dev = _device_of(x, "x")
-    xs = _matrix_stride(x, "x", dev)
-    M, K = x.shape
+    M, K, xs = _matrix(x, "x", dev)
     N = _weight(w, "w", K, dev)
     code = _activation(act)
     b = r = None
@@ -921,15 +945,15 @@ def linear_act_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
         _need_vector(bias, "bias", _BF16, N, dev)
         b = bias.data_ptr()
     if residual is not None:
-        rs = _matrix_stride(residual, "residual", dev)
-        if residual.shape != (M, N):
+        Mr, Nr, rs = _matrix(residual, "residual", dev)
+        if Mr != M or Nr != N:
             raise ValueError("residual must be [M, N]")
         r = residual.data_ptr()
     raw = _raw_stream(dev, stream)
     if out is None:
         out = _new(torch.empty, (M, N), _BF16, dev, stream, raw)
-    ys = _matrix_stride(out, "out", dev)
-    if out.shape != (M, N):
+    Mo, No, ys = _matrix(out, "out", dev)
+    if Mo != M or No != N:
         raise ValueError("out must be [M, N]")
     args = (x.data_ptr(), w.data_ptr(), b, r, out.data_ptr(), M, N, K, xs, rs, ys, code, raw)
     fn = lib.pa_linear_act_bf16
@@ -947,8 +971,7 @@ def linear_gated_bf16(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     x and out may be slices of wider matrices."""
     lib = _lib or load_library()
     dev = _device_of(x, "x")
-    xs = _matrix_stride(x, "x", dev)
-    M, K = x.shape
+    M, K, xs = _matrix(x, "x", dev)
     N = _weight(w_gate, "w_gate", K, dev)
     if _weight(w_up, "w_up", K, dev) != N:
         raise ValueError("w_gate and w_up must have the same shape")
@@ -956,8 +979,8 @@ def linear_gated_bf16(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     raw = _raw_stream(dev, stream)
     if out is None:
         out = _new(torch.empty, (M, N), _BF16, dev, stream, raw)
-    ys = _matrix_stride(out, "out", dev)
-    if out.shape != (M, N):
+    Mo, No, ys = _matrix(out, "out", dev)
+    if Mo != M or No != N:
         raise ValueError("out must be [M, N]")
     args = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), M, N, K, xs, ys,
             code, raw)
