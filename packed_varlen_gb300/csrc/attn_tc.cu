@@ -17,28 +17,26 @@
 // twice the tensor-core work of a single-tile item.
 //   warp 0      TMA producer: Q0/Q1 once per item, then K0, V0, K1, V1, ...
 //               through a ring of shared-memory slots.
-//   warp 1      allocates TMEM (S0, S1, O0, O1: 128 columns each) and
-//               issues tile 0's tcgen05.mma in the order
-//                 S0_0 | PV0_0 S0_1 | PV0_1 S0_2 ...
+//   warp 1      allocates TMEM (S0, S1: 128 columns each; O0, O1, P0, P1: 64)
+//               and issues tile 0's tcgen05.mma in the order
+//                 S0_0 | S0_1 | PV0_0 | S0_2 | PV0_1 ...
 //   warp 10     issues tile 1's in the same order.
 //               S = Q K^T with both operands in shared memory, fp32 into TMEM;
 //               O += P V with P (bf16) read from TMEM, V from shared memory.
-//               While one tile's softmax runs, the tensor core computes the
-//               other tile's PV and next S.  Each issuer is a whole warp
+//               A tile's next S is computed while its softmax, which holds
+//               the one before in registers, runs.  Each issuer is a whole warp
 //               with one elected lane issuing (warp-uniform operands), and
 //               the two take turns group by group; with two issuers one
 //               thread's waits, fences and commits overlap the other's MMAs.
 //   warps 2..5  softmax of tile 0, one thread per query row (TMEM lane);
 //   warps 6..9  softmax of tile 1.  Each thread reads its row of S, runs the
 //               online softmax in fp32 (exp2 with the scale folded in),
-//               writes P as bf16 over the first 64 columns of its S buffer,
-//               rescales O in TMEM only when the row maximum grew by more
+//               writes P as bf16, rescales O in TMEM only when the row maximum grew by more
 //               than 2^8 (2^32 in causal calls: kWeightHead), and finally
 //               normalises O and stores bf16 rows (send_rows).
 //   warp 11     finds the items ahead of the others (tell_items).
-// P overwrites S in place: the MMA that next writes that S buffer is issued
-// after the PV that reads P by the same thread, and one thread's tcgen05
-// MMAs execute in order.
+// P has columns of its own (with P over S, a tile's next scores waited for its
+// product with V, and its warps 850 of 2400 cycles for them).
 // Every output row is computed by one CTA in a fixed key-tile order that
 // depends only on its own sequence, so results do not depend on the rest of
 // the batch.  Key columns past the sequence end are masked to -inf (P = 0);
@@ -80,19 +78,21 @@ struct Cfg {
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kOutOff = kRingOff + kSlots * kTileBytes;   // 4 KB a softmax warp
   static constexpr int kBarOff = kOutOff + 8 * 4096;
-  // barriers: per Q tile t an S-full, a P-ready and an O-full barrier
-  static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kPReady = 4, kOFull = 6,
-                       kFinal = 8, kTurn = 10, kSlotFull = 12, kSlotEmpty = 12 + kSlots;
-  static constexpr int kItemFull = 12 + 2 * kSlots, kItemEmpty = kItemFull + kItemSlots;
+  // barriers: per Q tile t an S-full, an S-free, a P-ready and a PV-done barrier
+  static constexpr int kQFull = 0, kQEmpty = 1, kSFull = 2, kSFree = 4, kPReady = 6, kPVDone = 8,
+                       kFinal = 10, kTurn = 12, kSlotFull = 14, kSlotEmpty = 14 + kSlots;
+  static constexpr int kItemFull = 14 + 2 * kSlots, kItemEmpty = kItemFull + kItemSlots;
   static constexpr int kNumBars = kItemEmpty + kItemSlots;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag
   static constexpr int kItemOff = (kMiscOff + 16 + 127) / 128 * 128;
   static constexpr int kSchedOff = kItemOff + kItemSlots * 32;
   static constexpr int kSmemBytes = kSchedOff + (2 * kMaxSeqs + 1) * 4;
   static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
-  // TMEM columns: S_t at 128 t (P_t over its first 64), O_t at 256 + D t
+  // TMEM columns: S_t at 128 t, O_t at 256 + D t, P_t at 384 + 64 t
   static constexpr uint32_t kColS = 0;
   static constexpr uint32_t kColO = 256;
+  static constexpr uint32_t kColP = 384;
+  static_assert(kColO + 2 * D <= kColP, "TMEM plan");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile, false);
   static constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D, true);
@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::kQEmpty), 2);   // one arrival per MMA issuer
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(C::kSFull + t), 1);
+      mbar_init(bar(C::kSFree + t), 4);    // a warp's lane each
       mbar_init(bar(C::kPReady + t), 128);
-      mbar_init(bar(C::kOFull + t), 1);
+      mbar_init(bar(C::kPVDone + t), 1);
     }
     mbar_init(bar(C::kFinal + 0), 1);
     mbar_init(bar(C::kFinal + 1), 1);
@@ -236,10 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ++q_loads;
-        for (int j = 0; j < it.nk && ok; ++j) {
-          const int row = it.k0 + key_tile(it, j) * kTile;
-          ok = load_kv(&tm_k, row, it.head);
-          if (ok) ok = load_kv(&tm_v, row, it.head);
+        for (int j = 0; j <= it.nk && ok; ++j) {   // K_0, K_1, V_0, K_2, V_1, ...
+          if (j < it.nk) ok = load_kv(&tm_k, it.k0 + key_tile(it, j) * kTile, it.head);
+          if (ok && j > 0) ok = load_kv(&tm_v, it.k0 + key_tile(it, j - 1) * kTile, it.head);
         }
       }
       if (!ok) {
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 || warp == kMmaWarp1) {
     // ================= MMA issuers: warp 1 for tile 0, the last warp for tile 1 ====
     // Each issuer walks the same items and the same ring slots; it issues its
-    // own tile's MMAs in the order S_0 | PV_0 S_1 | PV_1 S_2 ... and frees a
+    // own tile's MMAs in the order S_0 | S_1 | PV_0 | S_2 | PV_1 ... and frees a
     // slot (or the Q buffer) with one arrival on a two-arrival barrier: a
     // commit once its MMAs reading the slot are done, or a plain arrive when
     // its tile is absent from the item.
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp == 1 ? 0 : 1;
     {
       const bool lead = elect_one();
-      uint32_t q_uses = 0, slot_uses = 0, issued = 0, p_waits = 0;
+      uint32_t q_uses = 0, slot_uses = 0, issued = 0, p_waits = 0, free_waits = 0;
       bool ok = true;
       auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
         const bool w = bounded_wait(b, parity, abort_flag, p.status, kWaitLimit);
@@ -274,7 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // next ring slot in consumption order, once its load has landed
       auto wait_slot = [&](uint32_t &s) -> bool {
         s = slot_uses % C::kSlots;
-        return wait_all(bar(C::kSlotFull + s), (slot_uses / C::kSlots) & 1u);
+        const uint32_t parity = (slot_uses / C::kSlots) & 1u;
+        ++slot_uses;
+        return wait_all(bar(C::kSlotFull + s), parity);
       };
       // S_t = Q_t K^T into S buffer t (Q/K K-major, SBO = 8 rows x 128 B)
       // (descriptors advance by adding the byte offset >> 4 to the start
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
       const uint64_t vdesc0 = sdesc_sw128(sRing, C::kVLbo, 1024);
       const uint32_t d_s = tmem + C::kColS + t * kTile, d_o = tmem + C::kColO + t * D;
+      const uint32_t d_p = tmem + C::kColP + t * (kTile / 2);
       auto issue_s = [&](uint32_t slot) {
         const uint64_t b0 = kdesc0 + ((slot * C::kTileBytes) >> 4);
 #pragma unroll
@@ -291,20 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lead) mma_ss(d_s, qdesc0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
         }
       };
-      // O_t += P_t V (P_t is in the first 64 columns of the S buffer)
+      // O_t += P_t V
       auto issue_pv = [&](uint32_t slot, bool first) {
         const uint64_t b0 = vdesc0 + ((slot * C::kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk) {
           if (lead)
-            mma_ts(d_o, d_s + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescO,
+            mma_ts(d_o, d_p + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescO,
                    (first && kk == 0) ? 0u : 1u);
         }
       };
-      // The two issuers take turns group by group (S0_0, S1_0, [PV0_0 S0_1],
-      // [PV1_0 S1_1], ...), so the tensor pipe sees the single-thread order
-      // that staggers the two tiles; each thread finishes its waits before
-      // taking the turn and commits after passing it on.
+      // The two issuers take turns group by group (S0_0, S1_0, S0_1, S1_1, PV0_0,
+      // PV1_0, S0_2, ...), so the tensor pipe sees the order of a single thread;
+      // each thread commits after passing the turn on.
       uint32_t turns = 0;
       auto take_turn = [&]() -> bool {
         const uint32_t parity = t == 0 ? ((turns & 1u) ^ 1u) : (turns & 1u);
@@ -330,29 +332,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++q_uses;
-        // prologue: S_0 from K_0
-        uint32_t sk;
-        if (!wait_slot(sk) || !take_turn()) {
-          ok = false;
-          break;
-        }
-        if (mine) {
-          issue_s(sk);
-          issued = 1;
-        }
-        pass_turn();
-        if (mine && lead) mma_commit(bar(C::kSFull + t));
-        release(bar(C::kSlotEmpty + sk));
-        ++slot_uses;
-        if (it.nk == 1) release(bar(C::kQEmpty));
-        for (int j = 0; j < it.nk && ok; ++j) {
-          const bool more = j + 1 < it.nk;
-          uint32_t sv, sk2 = 0;
+        // S_j from K_j, once the softmax has S_{j-1} in registers (the one before an
+        // item's first was read before the last PV was issued)
+        auto do_s = [&](int j) -> bool {
+          uint32_t sk;
+          if (!wait_slot(sk) || !take_turn()) return false;
+          if (mine) {
+            if (j > 0) {
+              if (!wait_all(bar(C::kSFree + t), free_waits & 1u)) return false;
+              ++free_waits;
+              fence_after_sync();
+            }
+            issue_s(sk);
+            issued = 1;
+          }
+          pass_turn();
+          if (mine && lead) mma_commit(bar(C::kSFull + t));
+          release(bar(C::kSlotEmpty + sk));
+          if (j + 1 == it.nk) release(bar(C::kQEmpty));
+          return true;
+        };
+        for (int j = -1; j < it.nk && ok; ++j) {
+          if (j + 1 < it.nk) ok = do_s(j + 1);
+          if (!ok || j < 0) continue;
+          uint32_t sv;
           if (!wait_slot(sv)) {
             ok = false;
             break;
           }
-          ++slot_uses;
           // The last key tile of a sequence whose length is not a multiple
           // of 128 holds rows past the sequence end (the next sequence's, or
           // the buffer's trailing rows).  P is 0 there, but 0 * Inf and
@@ -363,10 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int valid = it.lk - (it.nk - 1) * kTile;
             if (valid < kTile)
               zero_v_tail<D>(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
-          }
-          if (more && !wait_slot(sk2)) {
-            ok = false;
-            break;
           }
           // the issue turn first (the order is fixed, so holding it early
           // blocks nobody), then P_j written by this tile's softmax
@@ -381,25 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++p_waits;
             fence_after_sync();
-          }
-          // PV_j, then S_{j+1} (after the PV that reads P from the S buffer)
-          if (mine) {
             issue_pv(sv, j == 0);
-            if (more) issue_s(sk2);
           }
           pass_turn();
-          if (mine && lead) {
-            if (more)
-              mma_commit(bar(C::kSFull + t));
-            else
-              mma_commit(bar(C::kOFull + t));
-          }
+          if (mine && lead) mma_commit(bar(C::kPVDone + t));
           release(bar(C::kSlotEmpty + sv));
-          if (more) {
-            release(bar(C::kSlotEmpty + sk2));
-            ++slot_uses;
-            if (j + 2 == it.nk) release(bar(C::kQEmpty));
-          }
         }
       }
       // every MMA this thread issued has finished before TMEM is released
@@ -420,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t colS = C::kColS + t * kTile;
-    const uint32_t colO = C::kColO + t * D;
+    const uint32_t colO = C::kColO + t * D, colP = C::kColP + t * (kTile / 2);
     const float sl2 = p.scale_log2;
     const float head = p.causal ? kWeightHead : 0.f;
     const bool pos_scale = sl2 > 0.f;
@@ -450,6 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kTile / 32; ++c)
           tmem_ld32(lane_base + colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
         tmem_wait_ld();
+        if (j + 1 < it.nk) {   // S may be overwritten
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kSFree + t));
+        }
         // x = raw scores as pairs; with a positive scale the scale is folded
         // into the exponent's FFMA, otherwise the scores are scaled first
         float2 x[kTile / 2];
@@ -504,8 +498,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 s45 = __fadd2_rn(__fadd2_rn(sum8[4], sum8[5]), __fadd2_rn(sum8[6], sum8[7]));
         const float2 s8 = __fadd2_rn(s01, s45);
         l = l * alpha + (s8.x + s8.y);
-        // S_j complete implies the PV issued before it is complete: O is
-        // current and can be rescaled in place
+        // the PV before this one is done: P may be overwritten, and O is current
+        // and can be rescaled in place
+        if (j > 0) {
+          ok = bounded_wait(bar(C::kPVDone + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ++o_waits;
+          fence_after_sync();
+        }
         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -517,15 +520,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(lane_base + colO + c, r);
           }
         }
-        // P over the first 64 columns of this tile's S buffer
         {
           uint32_t r[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = pk[e];
-          tmem_st32(lane_base + colS, r);
+          tmem_st32(lane_base + colP, r);
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = pk[32 + e];
-          tmem_st32(lane_base + colS + 32, r);
+          tmem_st32(lane_base + colP + 32, r);
         }
         tmem_wait_st();
         fence_before_sync();
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // epilogue: wait for this tile's last PV, normalise, store valid rows
-      ok = bounded_wait(bar(C::kOFull + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
+      ok = bounded_wait(bar(C::kPVDone + t), o_waits & 1u, abort_flag, p.status, kWaitLimit);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
