@@ -286,7 +286,7 @@ struct FewPlan {
 
 // A CTA's K-block takes 75 + 1.33 R ns with an MMA of 64 rows (F <= 64) and
 // 95 + 1.5 R with 128, 1.75 times that where there are two weights; all CTAs
-// together get 9.7 TB/s out of L2 and 5.6 of w out of HBM; and a call costs 3 us
+// together get 9.7 TB/s out of L2 and 6.7 of w out of HBM; and a call costs 3 us
 // besides.  This holds for what was measured within some 15 %: 4096 x 4096,
 // 64 / 128 / 256 / 512 rows 12.2 / 13.2 / 15.4 / 22.2 us where the large kernel
 // takes 25 to 26 (a tile's 64 K-blocks at 345 ns), and 1024 rows 34.5, where it
@@ -305,7 +305,7 @@ FewPlan few_plan(const GemmArgs &a, int mode, int sms) {
     if (parts == 2) block = block * 7 / 4;
     const int64_t tile = waves * blocks * block;
     const int64_t l2 = ctas * blocks * (parts * features + rows) * kRowBytes / 9700;
-    const int64_t hbm = parts * a.N * a.K * 2 / 5600;
+    const int64_t hbm = parts * a.N * a.K * 2 / 6700;
     int64_t ns = tile > l2 ? tile : l2;
     ns = 3000 + (ns > hbm ? ns : hbm);
     if (ns < best.ns)
@@ -315,11 +315,15 @@ FewPlan few_plan(const GemmArgs &a, int mode, int sms) {
 }
 
 // The large kernel's time of the same call: a round of tiles of 256 x 256 on pairs
-// of SMs (of 128 features, where there are two weights).
+// of SMs (of 128 features, where there are two weights), 345 ns a K-block, but 500
+// below 64 rows (two weights of 28672 x 1024: 40 rows 31.3 us, 64 rows 22.9; of 8192 x
+// 4096: 13 rows 39.5, 48 rows 27.3; by the kernel for few rows 24.9 of the former's 40,
+// and 22.7 and 24.4).
 int64_t large_ns(const GemmArgs &a, int mode, int sms) {
   const int64_t tile_n = mode == kGated ? 128 : 256;
   const int64_t tiles = ((a.N - 1) / tile_n + 1) * ((int64_t{a.M} - 1) / 256 + 1);
-  return 3000 + ((tiles - 1) / (sms / 2) + 1) * ((a.K - 1) / kLinearBK + 1) * 345;
+  return 3000 + ((tiles - 1) / (sms / 2) + 1) * ((a.K - 1) / kLinearBK + 1) *
+                    (a.M < 64 ? 500 : 345);
 }
 
 }  // namespace
