@@ -798,14 +798,16 @@ _int_arrays = {}    # host int32 arrays by their values: a program has a few
 
 def _host_ints(values):
     """The values as a host int32 array, how many they are, and its address."""
-    known = _int_arrays.get(values)
+    # (whole numbers before they are looked up: 16.0 and 16 are one key of a dict, and a
+    # tensor that stands for a number may have another value by the next call)
+    ints = tuple(map(operator.index, values))
+    known = _int_arrays.get(ints)
     if known is None:
-        ints = [operator.index(v) for v in values]
         _fits_32_bits("pa_rope_axes", *[abs(v) for v in ints])
         arr = (ctypes.c_int32 * len(ints))(*ints)
         if len(_int_arrays) >= 256:
             _int_arrays.clear()
-        known = _int_arrays[values] = (arr, len(ints), ctypes.addressof(arr))
+        known = _int_arrays[ints] = (arr, len(ints), ctypes.addressof(arr))
     return known
 
 
@@ -849,7 +851,7 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
             raise ValueError("k and k_out must be [T, Hkv, D] with q's T and D")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    dims, axes, dims_at = _host_ints(tuple(axis_dims))    # (dims: kept until the call is made)
+    dims, axes, dims_at = _host_ints(axis_dims)    # (dims: kept until the call is made)
     try:
         usual = positions.dtype is _I32 and positions.shape == (axes, T) and \
             positions.get_device() == dev and positions.is_contiguous()
