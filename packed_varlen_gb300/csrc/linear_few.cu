@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // accumulator rows: 32 a quadrant, or (an MMA of 64 rows) its first 16 lanes
     const int f = kM == 128 ? quad * 32 + lane : quad * 16 + lane;
     const int n = n0 + f;
-    const bool mine = (kM == 128 || lane < 16) && f < p.features && n < p.N;
+    const bool mine = (kM == 128 || lane < 16) && f < p.features && f < p.N - n0;
     const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int rows = min(p.rows, p.M - m0);
     float bias = 0.f;
@@ -273,7 +273,7 @@ pa_status launch(const GemmArgs &a, FewParams &p, cudaStream_t stream) {
   const cudaError_t e =
       set_smem_once(reinterpret_cast<const void *>(kernel), kSmemBytes, configured);
   if (e != cudaSuccess) return from_cuda(e);
-  const dim3 grid((a.N + p.features - 1) / p.features, (a.M + p.rows - 1) / p.rows);
+  const dim3 grid((a.N - 1) / p.features + 1, (a.M - 1) / p.rows + 1);   // (N up to 2^31 - 8)
   return from_cuda(launch_beside(kernel, grid, kThreads, kSmemBytes, stream, mx, mw,
                                  mw2, p));
 }

@@ -48,3 +48,20 @@ def test_far_tails_of_the_activations(pv, act, M):
     got = oracle.to_f64(pv.linear_gated_bf16(x.cuda(), w.cuda(), up.cuda(), act=act))
     assert (np.abs(got - 2 * want) <= 2 * loss).all()
     assert pv.get_device_status() == 0
+
+
+def test_most_features(pv):
+    """Out features up to the last multiple of 8 below 2^31."""
+    N, K = (1 << 31) - 8, 8
+    at = torch.tensor([0, 127, 1 << 30, N - 129, N - 128, N - 2, N - 1], device="cuda")
+    rows = torch.arange(1, len(at) + 1, device="cuda").to(BF16)
+    w = torch.zeros(N, K, dtype=BF16, device="cuda")
+    w[at, 3] = rows
+    x = torch.zeros(2, K, dtype=BF16, device="cuda")
+    x[0, 3], x[1, 3] = 1.0, 2.0
+    y = pv.linear_act_bf16(x[:1], w)
+    assert torch.equal(y[0, at], rows) and int(y.count_nonzero()) == len(at)
+    del y
+    y = pv.linear_gated_bf16(x[1:], w, w, act="none")
+    assert torch.equal(y[0, at], 4 * rows * rows) and int(y.count_nonzero()) == len(at)
+    assert pv.get_device_status() == 0
