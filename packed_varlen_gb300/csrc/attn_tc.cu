@@ -61,7 +61,9 @@ constexpr int kTile = kVarlenTile;          // rows of a Q tile, keys of a K/V t
 constexpr int kThreads = 384;       // producer, 2 MMA issuers, 2 x 4 softmax warps, item finder
 constexpr int kMmaWarp1 = 10;       // issuer of tile 1
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
-constexpr long long kItemWaitLimit = 32 * kWaitLimit;   // of the item finder: whole items long
+// Of waits that may last as long as an item: the item finder's, and those of the softmax of
+// tile 1, which an item of one tile leaves idle (one query of 8 10^8 keys: 4 s).
+constexpr long long kItemWaitLimit = 32 * kWaitLimit;
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the next item of a warp, or nk < 0 (ok: not because a wait ran out)
   ItemReader at{0};
   auto next_item = [&](ItemInfo &it, bool &ok) -> bool {
-    ok = at.next(ring, it, true, abort_flag, p.status, kWaitLimit);
+    ok = at.next(ring, it, true, abort_flag, p.status, kItemWaitLimit);
     return ok && it.nk >= 0;
   };
 
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row_keys = min(it.lk, it.seen + token + 1);   // that this row sees
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < it.nk; ++j) {
-        ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kWaitLimit);
+        ok = bounded_wait(bar(C::kSFull + t), s_waits & 1u, abort_flag, p.status, kItemWaitLimit);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;

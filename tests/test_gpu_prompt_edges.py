@@ -21,6 +21,10 @@ def pv():
     return pv
 
 
+def _cu(lengths):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+
+
 TAILS = {"silu": np.arange(-99.0, -79.9, 0.5),            # to e^-99
          "gelu_tanh": np.arange(-10.375, -9.0, 0.0625),   # to e^-97
          "gelu": np.arange(-13.75, -11.9, 0.0625)}        # to e^-97
@@ -65,3 +69,18 @@ def test_most_features(pv):
     y = pv.linear_gated_bf16(x[1:], w, w, act="none")
     assert torch.equal(y[0, at], 4 * rows * rows) and int(y.count_nonzero()) == len(at)
     assert pv.get_device_status() == 0
+
+
+def test_an_item_of_seconds(pv):
+    """One query over 3 2^28 keys, some 4 s of one SM, and behind it items of two tiles, of
+    which that one has the first: whoever works on the second tile has nothing to do
+    meanwhile.  The keys are alike but for one of the last tile, whose score is 64 above."""
+    D, n, more = 64, 3 << 28, 2 * 152 * 256
+    kv = torch.zeros(n + 1, 1, D, dtype=BF16, device="cuda")
+    kv[n - 3] = 1.0
+    kv[n:] = 3.0
+    q = torch.full((1 + more, 1, D), 8.0, dtype=BF16, device="cuda")
+    out = pv.prompt_attn_fwd(q, kv, kv, _cu([1, more]), _cu([n, 1]), more, n, causal=False)
+    assert pv.get_device_status() == 0
+    # (the others' weights: 2^30 e^-64 in all at most, of values of zero)
+    assert (out[:1] == 1.0).all() and (out[1:] == 3.0).all()
