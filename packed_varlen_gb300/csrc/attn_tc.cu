@@ -57,7 +57,9 @@ namespace {
 
 using namespace tc;
 
+constexpr int kD = 64;
 constexpr int kTile = kVarlenTile;          // rows of a Q tile, keys of a K/V tile
+constexpr int kSlots = 9;                   // K/V ring slots
 constexpr int kThreads = 384;       // producer, 2 MMA issuers, 2 x 4 softmax warps, item finder
 constexpr int kMmaWarp1 = 10;       // issuer of tile 1
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
@@ -67,15 +69,11 @@ constexpr long long kItemWaitLimit = 32 * kWaitLimit;
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 
-// Shared-memory plan for head dim D, kSlots K/V ring slots and a work list
-// of up to kMaxSeqs sequences.  The dynamic shared-memory window starts
+// Shared-memory plan: two Q tiles, the K/V ring and a work list of up to
+// PA_MAX_BATCH sequences.  The dynamic shared-memory window starts
 // 1024-byte aligned (checked at run time), so no alignment slack is added.
-template <int D, int kSlots_, int kMaxSeqs_>
 struct Cfg {
-  static constexpr int kSlots = kSlots_;
-  static constexpr int kMaxSeqs = kMaxSeqs_;
-  static constexpr int kHalfBytes = kTile * 64 * 2;         // 128 rows x 128 B
-  static constexpr int kTileBytes = kTile * D * 2;          // one Q/K/V tile
+  static constexpr int kTileBytes = kTile * kD * 2;         // one Q/K/V tile: 128 rows x 128 B
   static constexpr int kQOff = 0;                           // Q0, Q1
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kOutOff = kRingOff + kSlots * kTileBytes;   // 4 KB a softmax warp
@@ -88,46 +86,37 @@ struct Cfg {
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag
   static constexpr int kItemOff = (kMiscOff + 16 + 127) / 128 * 128;
   static constexpr int kSchedOff = kItemOff + kItemSlots * 32;
-  static constexpr int kSmemBytes = kSchedOff + (2 * kMaxSeqs + 1) * 4;
+  static constexpr int kSmemBytes = kSchedOff + (2 * PA_MAX_BATCH + 1) * 4;
   static_assert(kSmemBytes <= 232448, "shared memory plan exceeds the per-CTA limit");
-  // TMEM columns: S_t at 128 t, O_t at 256 + D t, P_t at 384 + 64 t
+  // TMEM columns: S_t at 128 t, O_t at 256 + 64 t, P_t at 384 + 64 t
   static constexpr uint32_t kColS = 0;
   static constexpr uint32_t kColO = 256;
   static constexpr uint32_t kColP = 384;
-  static_assert(kColO + 2 * D <= kColP, "TMEM plan");
+  static_assert(kColO + 2 * kD <= kColP, "TMEM plan");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile, false);
-  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D, true);
-  // V (MN-major): next 64-column half at LBO, next 8 keys at SBO = 1024.  With
-  // D = 64 the MMA spans a single half and LBO is never used.
-  static constexpr uint32_t kVLbo = D == 128 ? kHalfBytes : 1024;
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, kD, true);
 };
 
-// Whole warp: zero key rows [valid, 128) of a V tile in shared memory.  The
-// tile is D / 64 column halves of 128 rows x 128 bytes; the 128-byte swizzle
-// only permutes the 16-byte chunks inside a row, so a whole row is cleared
-// without unswizzling.  The fences order the stores after the TMA bytes that
+// Whole warp: zero key rows [valid, 128) of a V tile in shared memory, 128
+// bytes each.  The 128-byte swizzle only permutes the 16-byte chunks inside a
+// row, so a whole row is cleared without unswizzling.  The fences order the stores after the TMA bytes that
 // landed and before the tensor core's reads (both are async-proxy accesses).
-template <int D>
 __device__ __forceinline__ void zero_v_tail(uint8_t *tile, int valid, int lane) {
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-  const int per_half = (kTile - valid) * 8;   // 16-byte chunks per half
-  for (int c = lane; c < per_half * (D / 64); c += 32) {
-    const int hf = c / per_half, r = c - hf * per_half;
-    *reinterpret_cast<uint4 *>(tile + hf * (kTile * 128) + (valid + (r >> 3)) * 128 +
-                               (r & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int c = lane; c < (kTile - valid) * 8; c += 32)   // 16-byte chunks
+    *reinterpret_cast<uint4 *>(tile + (valid + (c >> 3)) * 128 + (c & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   __syncwarp();
 }
 
-template <int D, int kSlots, int kMaxSeqs>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v,
                           const __grid_constant__ CUtensorMap tm_o, const VarlenParams p) {
-  using C = Cfg<D, kSlots, kMaxSeqs>;
+  using C = Cfg;
   extern __shared__ uint8_t smem_raw[];
   // 128-byte swizzle atoms need a 1024-byte aligned base
   const uint32_t base = smem_u32(smem_raw);
@@ -142,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_base_ptr = reinterpret_cast<uint32_t *>(gbase + C::kMiscOff);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(gbase + C::kMiscOff + 4);
   int32_t *order = reinterpret_cast<int32_t *>(gbase + C::kSchedOff);
-  int32_t *prefix = order + kMaxSeqs;
+  int32_t *prefix = order + PA_MAX_BATCH;
 
   // (uniform, and the compiler knows, as in attn_pair.cu)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -161,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::kFinal + 1), 1);
     mbar_init(bar(C::kTurn + 0), 1);
     mbar_init(bar(C::kTurn + 1), 1);
-    for (int s = 0; s < C::kSlots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kSlotFull + s), 1);
       mbar_init(bar(C::kSlotEmpty + s), 2);   // one arrival per MMA issuer
     }
@@ -178,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   // the ring is free until the first load: use it for the build's temporaries
   int32_t *tmp = reinterpret_cast<int32_t *>(gbase + C::kRingOff);
-  item_list(p, order, prefix, tmp, tmp + kMaxSeqs, blockIdx.x == 0);
+  item_list(p, order, prefix, tmp, tmp + PA_MAX_BATCH, blockIdx.x == 0);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -209,15 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, w);
       };
       auto load_kv = [&](const CUtensorMap *tm, int row, int head) -> bool {
-        const uint32_t s = slot_loads % C::kSlots;
-        const uint32_t use = slot_loads / C::kSlots;
+        const uint32_t s = slot_loads % kSlots;
+        const uint32_t use = slot_loads / kSlots;
         if (!wait_all(bar(C::kSlotEmpty + s), (use & 1u) ^ 1u)) return false;
         const uint32_t dst = sRing + s * C::kTileBytes;
         if (lead) {
           mbar_arrive_expect_tx(bar(C::kSlotFull + s), C::kTileBytes);
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_3d(dst + hf * C::kHalfBytes, tm, bar(C::kSlotFull + s), hf * 64, head, row);
+          tma_load_3d(dst, tm, bar(C::kSlotFull + s), 0, head, row);
         }
         ++slot_loads;
         return true;
@@ -230,13 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lead) {
-          mbar_arrive_expect_tx(bar(C::kQFull), ntq * p.tokens * p.G * D * 2);
-          for (int t = 0; t < ntq; ++t) {
-#pragma unroll
-            for (int hf = 0; hf < D / 64; ++hf)
-              tma_load_3d(sQ + t * C::kTileBytes + hf * C::kHalfBytes, &tm_q, bar(C::kQFull),
-                          hf * 64, it.head * p.G, it.q_row0 + t * p.tokens);
-          }
+          mbar_arrive_expect_tx(bar(C::kQFull), ntq * p.tokens * p.G * kD * 2);
+          for (int t = 0; t < ntq; ++t)
+            tma_load_3d(sQ + t * C::kTileBytes, &tm_q, bar(C::kQFull), 0, it.head * p.G,
+                        it.q_row0 + t * p.tokens);
         }
         ++q_loads;
         for (int j = 0; j <= it.nk && ok; ++j) {   // K_0, K_1, V_0, K_2, V_1, ...
@@ -246,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         // give the copies already issued a bounded chance to land
-        for (uint32_t s = 0; s < C::kSlots && s < slot_loads; ++s) {
-          const uint32_t n = (slot_loads - s + C::kSlots - 1) / C::kSlots;  // loads into s
+        for (uint32_t s = 0; s < kSlots && s < slot_loads; ++s) {
+          const uint32_t n = (slot_loads - s + kSlots - 1) / kSlots;  // loads into s
           drain_wait(bar(C::kSlotFull + s), (n - 1) & 1u, kDrainLimit);
         }
         if (q_loads) drain_wait(bar(C::kQFull), (q_loads - 1) & 1u, kDrainLimit);
@@ -275,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // next ring slot in consumption order, once its load has landed
       auto wait_slot = [&](uint32_t &s) -> bool {
-        s = slot_uses % C::kSlots;
-        const uint32_t parity = (slot_uses / C::kSlots) & 1u;
+        s = slot_uses % kSlots;
+        const uint32_t parity = (slot_uses / kSlots) & 1u;
         ++slot_uses;
         return wait_all(bar(C::kSlotFull + s), parity);
       };
@@ -285,14 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // address field; every operand lies below 256 KB, so nothing carries)
       const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024) + ((t * C::kTileBytes) >> 4);
       const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
-      const uint64_t vdesc0 = sdesc_sw128(sRing, C::kVLbo, 1024);
-      const uint32_t d_s = tmem + C::kColS + t * kTile, d_o = tmem + C::kColO + t * D;
+      // V (MN-major): next 8 keys at SBO = 1024 (one MMA spans all 64 columns: no LBO)
+      const uint64_t vdesc0 = sdesc_sw128(sRing, 1024, 1024);
+      const uint32_t d_s = tmem + C::kColS + t * kTile, d_o = tmem + C::kColO + t * kD;
       const uint32_t d_p = tmem + C::kColP + t * (kTile / 2);
       auto issue_s = [&](uint32_t slot) {
         const uint64_t b0 = kdesc0 + ((slot * C::kTileBytes) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::kHalfBytes + (kk & 3) * 32) >> 4;
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off = (kk * 32) >> 4;
           if (lead) mma_ss(d_s, qdesc0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
         }
       };
@@ -371,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t == 0 && key_tile(it, j) == it.nk - 1) {
             const int valid = it.lk - (it.nk - 1) * kTile;
             if (valid < kTile)
-              zero_v_tail<D>(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
+              zero_v_tail(gbase + C::kRingOff + sv * C::kTileBytes, valid, lane);
           }
           // the issue turn first (the order is fixed, so holding it early
           // blocks nobody), then P_j written by this tile's softmax
@@ -402,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kThreads / 32 - 1) {
     // ================= the items, ahead of everyone =================
-    tell_items(p, order, prefix, blockIdx.x, gridDim.x, ring, D, 0, 1, abort_flag, kItemWaitLimit);
+    tell_items(p, order, prefix, blockIdx.x, gridDim.x, ring, kD, 0, 1, abort_flag, kItemWaitLimit);
   } else {
     // ================= softmax / correction / epilogue =================
     // warps 2..5: tile 0, warps 6..9: tile 1; TMEM lane quadrant = warp % 4
@@ -411,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t colS = C::kColS + t * kTile;
-    const uint32_t colO = C::kColO + t * D, colP = C::kColP + t * (kTile / 2);
+    const uint32_t colO = C::kColO + t * kD, colP = C::kColP + t * (kTile / 2);
     const float sl2 = p.scale_log2;
     const float head = p.causal ? kWeightHead : 0.f;
     const bool pos_scale = sl2 > 0.f;
@@ -513,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < kD; c += 32) {
             uint32_t r[32];
             tmem_ld32(lane_base + colO + c, r);
             tmem_wait_ld();
@@ -548,20 +533,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int out_token = token < it.tokens && row_token < p.tokens ? it.q_row0 + token : -1;
       const float inv = 1.f / l;
       const bool none = row_keys <= 0;   // the row sees no key (its sums are NaN)
+      uint32_t r[64], words[32];
+      tmem_ld32(lane_base + colO, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(lane_base + colO + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t r[64], words[32];
-        tmem_ld32(lane_base + colO + c * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-        tmem_ld32(lane_base + colO + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          words[e] = none ? 0u
-                          : pack_bf16x2(__uint_as_float(r[2 * e]) * inv,
-                                        __uint_as_float(r[2 * e + 1]) * inv);
-        send_rows(gbase + C::kOutOff + (warp - 2) * 4096, words, p, &tm_o, D, c * 64, out_head,
-                  out_token);
-      }
+      for (int e = 0; e < 32; ++e)
+        words[e] = none ? 0u
+                        : pack_bf16x2(__uint_as_float(r[2 * e]) * inv,
+                                      __uint_as_float(r[2 * e + 1]) * inv);
+      send_rows(gbase + C::kOutOff + (warp - 2) * 4096, words, p, &tm_o, out_head, out_token);
     }
     if (lane == 0) bulk_wait();
   }
@@ -573,17 +554,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// [rows, H, D] bf16 viewed as a 3-D tensor (D, H, rows), rows row_elems
-// elements apart; box 64 x box_heads x box_rows with 128-byte swizzle: one 128-row, 64-column half tile per load.
-bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t row_elems,
+// [rows, H, 64] bf16 viewed as a 3-D tensor (D, H, rows), rows row_elems
+// elements apart; box 64 x box_heads x box_rows with 128-byte swizzle.
+bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int64_t row_elems,
               int box_heads, int box_rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2,
                                  static_cast<cuuint64_t>(row_elems) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+  const cuuint32_t box[3] = {kD, static_cast<cuuint32_t>(box_heads),
                              static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides,
@@ -592,31 +573,28 @@ bool make_map(CUtensorMap *map, const void *ptr, int rows, int H, int D, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kSlots, int kMaxSeqs>
 cudaError_t launch_tc(const VarlenArgs &a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv, mo;
   const VarlenParams p = varlen_params(a);
-  if (!make_map(&mq, a.q, a.total_q, a.H, D, a.q_stride, p.G, p.tokens) ||
-      !make_map(&mk, a.k, a.total_k, a.Hkv, D, a.k_stride, 1, kTile) ||
-      !make_map(&mv, a.v, a.total_k, a.Hkv, D, a.v_stride, 1, kTile) ||
-      !make_map(&mo, a.out, a.total_q, a.H, D, int64_t{a.H} * D, p.G < 32 ? p.G : 32,
+  if (!make_map(&mq, a.q, a.total_q, a.H, a.q_stride, p.G, p.tokens) ||
+      !make_map(&mk, a.k, a.total_k, a.Hkv, a.k_stride, 1, kTile) ||
+      !make_map(&mv, a.v, a.total_k, a.Hkv, a.v_stride, 1, kTile) ||
+      !make_map(&mo, a.out, a.total_q, a.H, int64_t{a.H} * kD, p.G < 32 ? p.G : 32,
                 p.box_tokens > 0 ? p.box_tokens : 1))
     return cudaErrorInvalidValue;
-  const int smem = Cfg<D, kSlots, kMaxSeqs>::kSmemBytes;
-  const auto kernel = varlen_attn_tc_kernel<D, kSlots, kMaxSeqs>;
   static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), smem, configured);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(varlen_attn_tc_kernel),
+                                Cfg::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_beside(kernel, dim3(a.num_sms), kThreads, smem, stream, mq, mk, mv, mo, p);
+  return launch_beside(varlen_attn_tc_kernel, dim3(a.num_sms), kThreads, Cfg::kSmemBytes, stream,
+                       mq, mk, mv, mo, p);
 }
 
 }  // namespace
 
-// Head dim 128 runs on the CTA-pair kernel; head dim 64 here, with a
-// nine-slot K/V ring beside a work list of up to PA_MAX_BATCH sequences.
+// Head dim 128 runs on the CTA-pair kernel, head dim 64 here.
 cudaError_t launch_varlen_attn(const VarlenArgs &a, cudaStream_t stream) {
-  if (a.D == 128) return launch_varlen_attn_pair(a, stream);
-  return launch_tc<64, 9, PA_MAX_BATCH>(a, stream);
+  return a.D == 128 ? launch_varlen_attn_pair(a, stream) : launch_tc(a, stream);
 }
 
 }  // namespace pa

@@ -157,16 +157,16 @@ __device__ __forceinline__ void store_rows(uint8_t *buf, const uint32_t (&words)
   __syncwarp();   // the buffer is free again
 }
 
-// The same for `token` and `head` of the row's lane (token < 0: not stored), columns
-// from `col`.  Where all 32 rows are stored and are a box of out (whole groups, or
+// The same for `token` and `head` of the row's lane (token < 0: not stored), head dim 64.
+// Where all 32 rows are stored and are a box of out (whole groups, or
 // part of one), one copy takes them, and nobody waits for it (before the kernel ends,
-// lane 0 waits for the copies to be written).  Head dim 64, the same 24 prompts: 280
+// lane 0 waits for the copies to be written).  The same 24 prompts: 280
 // -> 258 us, 64 of 300 tokens 83 -> 70, 16k 1015 -> 1010.  With head dim 128, whose
 // key loop has no register to spare, long sequences lost what short ones won (16k
 // 1113 -> 1129 us, the 24 prompts 397 -> 382).
 __device__ __forceinline__ void send_rows(uint8_t *buf, const uint32_t (&words)[32],
-                                          const VarlenParams &p, const CUtensorMap *map, int D,
-                                          int col, int head, int token) {
+                                          const VarlenParams &p, const CUtensorMap *map, int head,
+                                          int token) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) tc::bulk_wait_read();   // the copy before has read the buffer
   __syncwarp();
@@ -179,13 +179,13 @@ __device__ __forceinline__ void send_rows(uint8_t *buf, const uint32_t (&words)[
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      tc::tma_store_3d(map, tc::smem_u32(buf), col, head, token);
+      tc::tma_store_3d(map, tc::smem_u32(buf), 0, head, token);
       tc::bulk_commit();
     }
   } else {
     store_rows(buf, words,
                token < 0 ? nullptr
-                         : p.out + (static_cast<int64_t>(token) * p.H + head) * D + col);
+                         : p.out + (static_cast<int64_t>(token) * p.H + head) * 64);
   }
 }
 
