@@ -390,6 +390,7 @@ def linear_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] =
     N = w.shape[0]
     if w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
+    _fits_32_bits("pa_linear_bf16", M, N, K)
     if bias is not None:
         _need(bias, "bias", torch.bfloat16, 1)
         if bias.shape[0] != N:
@@ -764,8 +765,6 @@ def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     ``out`` beyond cu_seqlens_q[B] are not written (a fresh ``out`` is zero-filled)."""
     lib = _lib or load_library()
     max_q, max_k = int(max_q), int(max_k)
-    if (max_q | max_k) >> 31:
-        _fits_32_bits("pa_prompt_attn_fwd", max_q, max_k)
     dev = _device_of(q, "q")
     Tq, Hq, D, qs = _rows(q, "q", dev)
     Tk, Hkv, Dk, ks = _rows(k, "k", dev)
@@ -773,6 +772,8 @@ def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if Dk != D or Dv != D or Tv != Tk or Hv != Hkv or Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError("k and v must be [Tk, Hkv, D] with q's D and Hq a multiple of Hkv")
     B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
+    if (max_q | max_k | B | Tq | Tk | Hq | D) >> 31:
+        _fits_32_bits("pa_prompt_attn_fwd", max_q, max_k, B, Tq, Tk, Hq, D)
     _need_index(cu_seqlens_q, "cu_seqlens_q", B + 1, dev)
     if cu_seqlens_k is not cu_seqlens_q:
         _need_index(cu_seqlens_k, "cu_seqlens_k", B + 1, dev)
@@ -851,6 +852,8 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
             raise ValueError("k and k_out must be [T, Hkv, D] with q's T and D")
     elif k_out is not None:
         raise ValueError("k_out without k")
+    if (T | Hq | Hkv | D) >> 31:
+        _fits_32_bits("pa_rope_axes", T, Hq, Hkv, D)
     dims, axes, dims_at = _host_ints(axis_dims)    # (dims: kept until the call is made)
     try:
         usual = positions.dtype is _I32 and positions.shape == (axes, T) and \
@@ -940,6 +943,8 @@ def linear_act_bf16(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
     dev = _device_of(x, "x")
     M, K, xs = _matrix(x, "x", dev)
     N = _weight(w, "w", K, dev)
+    if (M | N | K) >> 31:
+        _fits_32_bits("pa_linear_act_bf16", M, N, K)
     code = _activation(act)
     b = r = None
     rs = 0
@@ -977,6 +982,8 @@ def linear_gated_bf16(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     N = _weight(w_gate, "w_gate", K, dev)
     if _weight(w_up, "w_up", K, dev) != N:
         raise ValueError("w_gate and w_up must have the same shape")
+    if (M | N | K) >> 31:
+        _fits_32_bits("pa_linear_gated_bf16", M, N, K)
     code = _activation(act)
     raw = _raw_stream(dev, stream)
     if out is None:

@@ -84,3 +84,41 @@ def test_an_item_of_seconds(pv):
     assert pv.get_device_status() == 0
     # (the others' weights: 2^30 e^-64 in all at most, of values of zero)
     assert (out[:1] == 1.0).all() and (out[1:] == 3.0).all()
+
+
+def test_counts_beyond_32_bits_are_refused(pv):
+    """Sizes of 2^32 + 8 are not sizes of 8."""
+    n = (1 << 32) + 8
+    big = torch.zeros(n, 8, dtype=BF16, device="cuda")
+    few = torch.zeros(8, 8, dtype=BF16, device="cuda")
+    deep = big.view(8, n)
+    out = torch.zeros(8, 8, dtype=BF16, device="cuda")
+    out[:] = 5.0
+
+    def refused(call, *args, **kw):
+        with pytest.raises(pv.PackedAttnError) as e:
+            call(*args, **kw)
+        assert e.value.status == 2
+
+    refused(pv.linear_bf16, big, few)
+    refused(pv.linear_bf16, few, big)
+    refused(pv.linear_bf16, deep, deep, out=out)
+    refused(pv.linear_act_bf16, big, few)
+    refused(pv.linear_act_bf16, few, big)
+    refused(pv.linear_act_bf16, deep, deep, out=out)
+    refused(pv.linear_gated_bf16, big, few, few)
+    refused(pv.linear_gated_bf16, few, big, big)
+    refused(pv.linear_gated_bf16, deep, deep, deep, out=out)
+    assert (out == 5).all()
+    at = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    refused(pv.rope_axes, big.view(n, 1, 8), None, at, [8])
+    at = at[:, :1].contiguous()
+    refused(pv.rope_axes, big.view(1, n, 8), None, at, [8])
+    refused(pv.rope_axes, big.view(-1)[:n].view(1, 1, n), None, at, [8])
+    q = big.view(-1)[:(1 << 32) + 64].view(1, 1, -1)
+    refused(pv.prompt_attn_fwd, q, q, q, _cu([1]), _cu([1]), 1, 1)
+    del big, deep, q
+    one = torch.zeros(1, 1, 64, dtype=BF16, device="cuda")
+    cu = torch.zeros((1 << 32) + 2, dtype=torch.int32, device="cuda")
+    refused(pv.prompt_attn_fwd, one, one, one, cu, cu, 1, 1)
+    assert pv.get_device_status() == 0
