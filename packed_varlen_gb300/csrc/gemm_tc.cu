@@ -15,7 +15,7 @@
 // own x row, w and bias: packed or alone, at any row offset, the bits agree.
 //
 // Kernel: persistent, one CTA per SM, CTAs in clusters of two that work as a
-// cta_group::2 pair on 256 x 256 output tiles, six warps each.  One MMA
+// cta_group::2 pair on 256 x 256 output tiles, ten warps each.  One MMA
 // (M = 256, N = 256, K = 16) spans the pair: each CTA holds 128 rows of the
 // x tile and one 128-row half of the w tile in its own shared memory, loaded
 // by its own TMA from this GPU's memory (no CTA writes another's shared
@@ -73,6 +73,7 @@ constexpr int kThreads = 320;                   // TMA, MMA, 8 epilogue warps
 constexpr int kGroupM = 8;                      // row blocks (of a pair) of a group
 constexpr int kOutN = 64, kOutBytes = 32 * kOutN * 2;   // a warp's part of y in shared memory
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
+constexpr long long kTileWaitLimit = 32 * kWaitLimit;   // of the epilogue: for all of a tile's K
 constexpr long long kDrainLimit = 400000000LL;  // teardown after an abort (~0.2 s)
 
 struct GemmCfg {
@@ -307,7 +308,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     for (int tp = cl; tp < p.n_pairs; tp += n_cl, ++tiles_done) {
       const uint32_t buf = tiles_done & 1u, buse = tiles_done >> 1;
       const bool ok = bounded_wait_cluster(bar(C::kAccFull + buf), buse & 1u, abort_flag, p.status,
-                                           kWaitLimit);
+                                           kTileWaitLimit);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
       bool landed_ok = true;
@@ -427,7 +428,8 @@ pa_status launch_gemm(const GemmArgs &a, cudaStream_t stream) {
 // Largest row stride, in elements (TMA strides are below 2^40 bytes).
 constexpr int64_t kMostStride = int64_t{1} << 38;
 
-// Longest sum: a tile's, some 0.5 s of them, has to end within the waits for it.
+// Longest sum where the kernel for few rows may be taken: half a second or so at most,
+// which has to end within that kernel's waits for it.
 constexpr int32_t kMostK = 1 << 26;
 
 // The checks of the entry points with strides (bias, residual: may be null).

@@ -122,3 +122,16 @@ def test_counts_beyond_32_bits_are_refused(pv):
     cu = torch.zeros((1 << 32) + 2, dtype=torch.int32, device="cuda")
     refused(pv.prompt_attn_fwd, one, one, one, cu, cu, 1, 1)
     assert pv.get_device_status() == 0
+
+
+def test_a_sum_of_seconds(pv):
+    """linear_bf16 over K = 3 2^28: a tile of some 3 s."""
+    K = 3 << 28
+    x, w = (torch.zeros(n, K, dtype=BF16, device="cuda") for n in (2, 8))
+    at = torch.tensor([0, 63, 1 << 28, K - 65, K - 1], device="cuda")
+    w[:, at] = torch.arange(1, 9, device="cuda").to(BF16)[:, None]
+    x[0, at], x[1, at[:2]] = 1.0, 3.0
+    y = pv.linear_bf16(x, w)
+    assert pv.get_device_status() == 0
+    want = torch.arange(1, 9, device="cuda").to(BF16)
+    assert torch.equal(y[0], 5 * want) and torch.equal(y[1], 6 * want)
