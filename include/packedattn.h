@@ -126,7 +126,10 @@ pa_status pa_varlen_attn_fwd(const void *q, const void *k, const void *v, void *
  *   out[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], k[j,h',:]>) * v[j,h',:]
  * A query that sees no key gets zeros.  Scores, maxima, sums and the output's
  * accumulation are fp32; softmax weights are rounded to bf16 for the product
- * with V, and the output once to bf16.
+ * with V (the tensor cores take both factors of V's type), and the output once to
+ * bf16.  Weights of a causal call are held 2^-24 of their size until the end, so an
+ * output may be off by some 2^-124 in absolute terms (n 2^-124 at most, of n keys):
+ * values of V below 2^-112 in size lose digits there, others do not.
  *
  * q [total_q, Hq, D], k, v [total_k, Hkv, D] bf16, with q_stride, k_stride,
  * v_stride elements from one token to the next (>= heads * D, multiples of 8:

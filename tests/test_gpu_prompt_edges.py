@@ -135,3 +135,107 @@ def test_a_sum_of_seconds(pv):
     assert pv.get_device_status() == 0
     want = torch.arange(1, 9, device="cuda").to(BF16)
     assert torch.equal(y[0], 5 * want) and torch.equal(y[1], 6 * want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("power", [80, 104, 112, 120])
+def test_small_values(pv, power, causal, D):
+    """V near the end of fp32's range.  A product of weight and value, and each sum of them, is
+    cut at 2^-149 at the worst; the largest weight is 1 at least, or 2^-24 in causal order, by
+    which the sum is divided: 2 n 2^-149 (or 2^-125) beside the relative errors."""
+    n, Hq, H = 300, 4, 2
+    q, k, v = (torch.randn(n, h, D, generator=torch.Generator().manual_seed(h)).to(BF16)
+               for h in (Hq, H, H + 1))
+    v = (v[:, :H].float() * 2.0 ** -power).to(BF16)
+    out = pv.prompt_attn_fwd(q.cuda(), k.cuda(), v.cuda(), _cu([n]), _cu([n]), n, n, causal=causal)
+    want, weight, reach = oracle.prompt_attention(q, k, v, [n], [n], causal, D ** -0.5)
+    scores = (D + 4) * 2.0 ** -23 * reach + 2.0 ** -20
+    loss = (2.0 ** -8 + 2 * scores) * weight + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+    loss = loss + 2 * n * 2.0 ** (-125 if causal else -149) + 2.0 ** -134
+    assert (np.abs(oracle.to_f64(out) - want) <= loss).all()
+    assert pv.get_device_status() == 0
+
+
+def test_calls_that_follow_each_other(pv):
+    """Calls in a row, each set up beside the one before it, over buffers that the ones before
+    write or read (weights among them): the bits of the same calls with a wait after each,
+    eager and out of a graph."""
+    T, C, H, D = 600, 1024, 8, 128
+
+    def rn(*shape, seed):
+        return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(BF16).cuda()
+
+    first = [rn(T, C, seed=i) for i in range(3)] + [rn(C, C, seed=i) / 32 for i in (3, 4)]
+    cu, many = _cu([13, 287, 0, 300]), _cu([1, 599])
+    pos = torch.arange(2 * T, dtype=torch.int32, device="cuda").view(2, T)
+    lens, table = _cu([600])[1:], torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40)
+    work = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+    caches = [torch.zeros(40, 16, 2, D, dtype=BF16, device="cuda") for _ in range(2)]
+
+    def heads(x, n=H, at=0):
+        return x.view(T, C // D, D)[:, at:at + n]
+
+    def run(a, b, c, w, u, wait):
+        def narrow():                                    # heads of 64, over other boundaries
+            pv.prompt_attn_fwd(a.view(T, 16, 64), b.view(T, 16, 64)[:, :4],
+                               b.view(T, 16, 64)[:, 4:8], many, many, 599, 599,
+                               out=c.view(T, 16, 64))
+
+        calls = [
+            lambda: pv.linear_act_bf16(a, w, act="silu", residual=b, out=b),
+            lambda: pv.rope_axes(heads(b, 4), heads(b, 4, 4), pos, [64, 64]),
+            lambda: pv.kv_cache_write(heads(b, 2), heads(b, 2, 2), *caches, _cu600, table),
+            lambda: pv.prompt_attn_fwd(heads(b), heads(a, 2), heads(a, 2, 2), cu, cu, 300, 300,
+                                       out=heads(c)),
+            lambda: pv.linear_gated_bf16(c, w, u, out=a),
+            narrow,
+            lambda: pv.linear_act_bf16(c[:13], w, act="gelu", residual=a[:13], out=a[:13]),
+            lambda: pv.paged_attn_fwd(heads(a), *caches, _cu600, lens, table, 600, 600,
+                                      out=heads(b), workspace=work),
+            lambda: pv.linear_act_bf16(b[:20], u, out=w[40:60]),       # weights of the next
+            lambda: pv.linear_gated_bf16(a[:5], w, u, act="relu", out=c[7:12]),
+            lambda: pv.varlen_attn_fwd(heads(c), heads(b), heads(a), cu, cu, 300, 300,
+                                       out=spare),
+            lambda: pv.linear_bf16(spare.view(T, C), w, out=b),
+            lambda: pv.block_window_attn_fwd(*(x.view(1, T, H, D) for x in (b, c, a)), 24, 1, 0,
+                                             out=spare.view(1, T, H, D)),
+            lambda: pv.linear_act_bf16(spare.view(T, C)[300:330], u, residual=a[:30], out=a[:30]),
+            lambda: a.clamp_(-3, 3),
+        ]
+        for call in calls * 3:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+
+    _cu600, spare = _cu([600]), torch.zeros(T, H, D, dtype=BF16, device="cuda")
+
+    def fresh():
+        torch.cuda.synchronize()
+        for t in caches + [spare]:
+            t.zero_()
+        return [x.clone() for x in first]
+
+    def seen(buffers):
+        torch.cuda.synchronize()
+        return [t.clone().view(torch.int16) for t in [*buffers, *caches, spare]]
+
+    buffers = fresh()
+    run(*buffers, True)
+    want = seen(buffers)
+    for _ in range(5):
+        buffers = fresh()
+        torch.cuda.synchronize()
+        run(*buffers, False)
+        assert all(torch.equal(x, y) for x, y in zip(want, seen(buffers)))
+    buffers = fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(*buffers, False)
+    for _ in range(3):
+        for x, y in zip(buffers, fresh()):
+            x.copy_(y)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(want, seen(buffers)))
+    assert pv.get_device_status() == 0
