@@ -274,8 +274,9 @@ pa_status pa_rope_packed(void *q, void *k, const int32_t *cu_seqlens_q,
  * the angle positions[a, t] * theta_i: (x, y) -> (x cos - y sin, x sin + y cos).
  * theta_i = base^(-2 j / axis_dims[a]) with j the pair's place on its axis, or
  * (shared != 0: one spectrum over all axes) base^(-2 i / R).  Elements past R
- * are copied.  The fraction of a turn is exact to 2^-53 of theta times the
- * position, sin, cos and the rotation are fp32, the output is rounded once.
+ * are copied.  theta_i is off by 2^-52 at most (base >= 1), the angle by that times
+ * the position and not more; sin, cos and the rotation are fp32, the output is rounded
+ * once.
  *
  * q, q_out [total, Hq, D], k, k_out [total, Hkv, D] bf16 with their strides in
  * elements from one token to the next (>= heads * D, multiples of 8); q_out = q

@@ -177,8 +177,8 @@ __device__ __forceinline__ float hide(uint32_t taddr, int valid, float sl2, floa
 }
 
 // P = 2^(s * mul - m) for the 128 keys of one TMEM lane's S row at `taddr`, 64 at
-// a time, written as bf16 pairs over the row's first 64 columns; adds P to the
-// eight partial sums.
+// a time, written as bf16 pairs over the row's first 64 columns (an MMA takes both
+// factors in one type, V's); adds P, unrounded, to the eight partial sums.
 __device__ __forceinline__ void tile_p(uint32_t taddr, float mul, float m, float2 (&sum8)[8]) {
   const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-m, -m);
 #pragma unroll
@@ -473,7 +473,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t = 0; ok && !vw.done(); ++t) {
         if (t >= kSBufs) {
           const uint32_t b = gv % kSBufs;
-          // P_gv written by the pair's 16 softmax warps
+          // P_gv written by the 8 softmax warps of the pair that have the tile
           if (!wait_all(bar(C::kPReady + b), (gv / kSBufs) & 1u)) {
             ok = false;
             break;

@@ -31,7 +31,7 @@
 //   warps 2..5  softmax of tile 0, one thread per query row (TMEM lane);
 //   warps 6..9  softmax of tile 1.  Each thread reads its row of S, runs the
 //               online softmax in fp32 (exp2 with the scale folded in),
-//               writes P as bf16, rescales O in TMEM only when the row maximum grew by more
+//               writes P as bf16 (V's type, as the MMA wants both), rescales O in TMEM only when the row maximum grew by more
 //               than 2^8 (2^32 in causal calls: kWeightHead), and finally
 //               normalises O and stores bf16 rows (send_rows).
 //   warp 11     finds the items ahead of the others (tell_items).

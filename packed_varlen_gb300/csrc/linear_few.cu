@@ -287,10 +287,20 @@ struct FewPlan {
 // A CTA's K-block takes 75 + 1.33 R ns with an MMA of 64 rows (F <= 64) and
 // 95 + 1.5 R with 128, 1.75 times that where there are two weights; all CTAs
 // together get 9.7 TB/s out of L2 and 6.7 of w out of HBM; and a call costs 3 us
-// besides.  This holds for what was measured within some 15 %: 4096 x 4096,
-// 64 / 128 / 256 / 512 rows 12.2 / 13.2 / 15.4 / 22.2 us where the large kernel
-// takes 25 to 26 (a tile's 64 K-blocks at 345 ns), and 1024 rows 34.5, where it
-// takes 28; two weights of 11264 x 4096, 128 / 192 rows 38 / 53 against 48.
+// besides.  Up to 16 rows and for wide pairs of weights this is within some 20 % of
+// what was measured; from some 30 rows on the L2 term is far too slow and the model up
+// to 90 % high.  Measured here, modelled here, measured by the large kernel (us, w out of HBM):
+//   rows   4096 x 4096         4096 x 14336        two of 4096 x 4096   two of 11264 x 4096
+//     33   10.0  11.9  23.9    24.7  34.1  66.3    16.6  18.6  23.2     30.9  30.5  46.1
+//    128   12.4  18.0  24.6    32.3  55.5  67.0    18.3  25.0  22.5     37.0  37.3  47.4
+//    256   16.9  24.9  24.7    44.2  79.7  67.2    26.8  33.0  22.8     50.6  56.6  48.2
+//    300   18.2  26.8  24.9    45.8  86.4  67.5    30.4  37.0  23.6     73.7  79.2  58.7
+//    512   24.4  33.0  25.3    65.2   108  67.8    35.3  44.9  24.2     84.8   102  63.6
+//   1024   34.6  49.0  26.6    92.4   164  71.2    50.7  63.0  41.1      172   174   102
+// The choice by it is right or within 8 % of these, but for some 260 to 380 rows of one
+// weight, which go to the large kernel: 300 rows 24.9 in place of 18.2, 67 in place of 46.
+// What bounds 64 to 512 rows is what a K-block brings into an SM, F + R rows of 128
+// bytes, at 95 to 130 bytes a ns.
 FewPlan few_plan(const GemmArgs &a, int mode, int sms) {
   const int64_t parts = mode == kGated ? 2 : 1, blocks = (a.K - 1) / kLinearBK + 1;
   FewPlan best{0, 0, INT64_MAX};
@@ -316,7 +326,8 @@ FewPlan few_plan(const GemmArgs &a, int mode, int sms) {
 
 // The large kernel's time of the same call: a round of tiles of 256 x 256 on pairs
 // of SMs (of 128 features, where there are two weights), 345 ns a K-block, but 500
-// below 64 rows (two weights of 28672 x 1024: 40 rows 31.3 us, 64 rows 22.9; of 8192 x
+// below 64 rows (more than 4096 features take, 24 us at any of few rows, but there
+// the other kernel is far ahead; two weights of 28672 x 1024: 40 rows 31.3 us, 64 rows 22.9; of 8192 x
 // 4096: 13 rows 39.5, 48 rows 27.3; by the kernel for few rows 24.9 of the former's 40,
 // and 22.7 and 24.4).
 int64_t large_ns(const GemmArgs &a, int mode, int sms) {

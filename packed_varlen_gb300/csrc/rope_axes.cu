@@ -9,8 +9,8 @@
 //
 // Angles: theta_i / (2 pi) is kept as a 64-bit fraction of a turn (computed in
 // double on the host), so position * fraction modulo 2^64 is the fraction of a
-// turn that is left, with no error but the fraction's own (2^-53 of it, times
-// the position) and no double-precision arithmetic on the GPU.  sincospif then
+// turn that is left, with no error but the fraction's own (theta's 2^-52 at most,
+// times the position) and no double-precision arithmetic on the GPU.  sincospif then
 // has an argument in [-1, 1).
 //
 // HBM bound: q and k are read and written once.  A warp's task is a token and
@@ -87,7 +87,9 @@ __device__ __forceinline__ float2 turned(int32_t position, uint64_t turn) {
 //   halves (48 tokens of 48 heads of 128: 2.5 us, each lane its own 2.8; 3000 14.3
 //   and 12.2).
 // (One call in a row of them in a graph, over rows in L2.)  30269 tokens of 48 heads
-// of 128: 115 us out of HBM, 6.4 TB/s.
+// of 128: 115 us out of HBM, 6.4 TB/s.  9801 tokens of 32 heads of 80, halves: 20 us of 15
+// that the bytes take; 8 blocks an SM are launched, of which 3 are resident, so nearly
+// every warp has one task, and blocks turn over with nothing in flight between them.
 constexpr int batch_of(bool halves, bool many) { return !halves ? 6 : many ? 3 : 2; }
 
 // kHalves: pairs (i, i + R/2), else (2i, 2i + 1).  kElems: elements of a vector.

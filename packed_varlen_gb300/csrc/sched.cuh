@@ -59,7 +59,10 @@ __device__ __forceinline__ SeqBounds seq_bounds(const int32_t *__restrict__ cu_q
 // ends with __syncthreads().  Item count = prefix[batch].
 //
 // levels: the list of causal attention, where a query tile's work grows with
-// its place in the sequence.  Sequences are sorted by query length, and the
+// its place in the sequence.  (Keys before the queries are not looked at: a few
+// queries behind long keys come last, though theirs are the dearest items.  12 prompts
+// of 2000 tokens and 4 times 64 tokens behind 20,000 keys, 32 heads on 8 of 128: 403 us,
+// the prompts alone 326.)  Sequences are sorted by query length, and the
 // items go level by level, the last tiles first: level t holds tile t of every
 // sequence that has one, which are the first s + 1 of the order for t in
 // [T_{s+1}, T_s), T_s the tiles of sequence order[s].  prefix[s] counts the

@@ -115,7 +115,8 @@ __device__ __forceinline__ void item_list(const VarlenParams &p, int32_t *order,
 }
 
 // The worker's n-th item, of `workers`: round robin; in a causal list, whose
-// items grow cheaper, every second round backwards, which evens out what a
+// items grow cheaper (of sequences without keys before their queries), every second
+// round backwards, which evens out what a
 // round's first worker has more than its last.
 __device__ __forceinline__ int item_at(const VarlenParams &p, int n, int worker, int workers) {
   return n * workers + (p.causal && (n & 1) ? workers - 1 - worker : worker);
